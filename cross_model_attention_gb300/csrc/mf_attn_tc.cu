@@ -1,0 +1,832 @@
+// mf_attn_tc.cu — attention with a sliding window, sinks and shared prefixes
+// on the fifth-generation tensor cores, bf16, sm_103a.
+//
+// For a query row at position i of its sequence, over the keys j it sees
+// (j <= i, and i - j < window or j < sinks):
+//   o = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),  s_j = scale q.k_j,
+//   lse = m + log(sum_j exp(s_j - m)).
+// The softmax runs in one pass over the keys: m is a running reference, moved
+// (and o, the sum rescaled) only when a block's maximum exceeds it by 2^8, so
+// that exp2 arguments stay below 8 and the rescaling is rare.  Sums and o are
+// fp32; P is rounded to bf16 for the second product (relative 2^-9 for each
+// weight, the same size as the rounding of the output).
+//
+// Rows of a tile: (token, query head of one KV group), TQ = 128 / G tokens of
+// all G heads, so that the heads of a group share every key that is read.
+// A CTA (one per SM, persistent) runs two streams, each 128 rows with its own
+// softmax warpgroup and TMEM (S 128 columns, P over S's first 64, O d
+// columns).  Pair runs give the streams two neighbouring row tiles that share
+// each key block (K and V come through L2 at ~160 GB/s per SM, which one
+// 128-row tile would outrun); single-tile runs (few rows, many keys) give
+// them alternate key blocks of one tile and two partial results.  While one
+// stream's warps exponentiate, the other's products run.
+// Warps 0-3 and 4-7: softmax of stream 0 and 1 (thread = row).  Warp 8: MMA.
+// Warp 9: TMA loads, K and V blocks of 128 keys through one ring.
+//
+// Masked keys: a row's hidden scores are replaced by -inf before anything is
+// done with them, and V rows that no row may see (past a range's end, where
+// the box still reads) are zeroed in shared memory or left out of the
+// product, so what lies there, NaN included, reaches nothing.
+#include <cstdint>
+
+#include "mf_internal.cuh"
+#include "mf_ptx.cuh"
+
+namespace mf {
+namespace {
+
+constexpr int kRows = 128;
+constexpr int kKeys = 128;
+constexpr int kThreads = 320;
+
+template <int D>
+struct Lay {
+  static constexpr int kChunk = 128 * 128;           // 128 rows x 64 bf16
+  static constexpr int kTile = (D / 64) * kChunk;    // Q tile, K block or V block
+  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr int kQ = 0;
+  static constexpr int kRing = 2 * kTile;
+  static constexpr int kBar = kRing + kStages * kTile;
+  static constexpr int kMisc = kBar + 8 * (6 + 2 * kStages);
+  static constexpr int kMiscBytes = 128;
+  static constexpr int kBytes = kMisc + kMiscBytes + 1024;
+};
+static_assert(Lay<128>::kBytes <= 232448 && Lay<64>::kBytes <= 232448, "shared memory");
+
+// misc words: [0] TMEM address, [1] abort, [2..3] cache form: first request
+// and [4..5] its first block, [6..] reduction scratch
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0, kColO = 256;  // + 128 * stream each
+
+// ------------------------------------------------------------ PTX not in mf_ptx
+// D (+)= A[tmem] * B[smem]^T, kind::f16.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// Q tile: 64 columns of G heads of one group, of consecutive tokens.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
+                                            int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
+// Waits of a whole warp: one lane polls (and gives up where another role has),
+// every lane then has the phase's memory order from its own (passing) try.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* err, const volatile int* misc) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = !misc[1] && mbar_wait(bar, parity, err) ? 1 : 0;
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  if (ok) mbar_try(bar, parity);
+  __syncwarp();
+  return ok != 0;
+}
+
+// -------------------------------------------------------------------- runs --
+// What one run of key blocks is, for every role.
+struct Run {
+  int q_row, n_tok0, n_tok1;  // tokens of the tile(s); n_tok1 = 0: one tile
+  int alt;                    // one tile, key blocks alternate between the streams
+  int pos;                    // position of the first token
+  int k_row0, a1, b0, b1;
+  int blk0, blk1;
+  int head, prefix;           // prefix: K and V are the shared ones
+  int part;                   // first partial index, or -1
+};
+
+// Key block b of a run's ranges: start and how many of its keys count.
+__device__ __forceinline__ void block_at(const Run& r, int b, int& j0, int& valid) {
+  const int na = (r.a1 + kKeys - 1) / kKeys;
+  const bool in_a = b < na;
+  j0 = in_a ? b * kKeys : r.b0 + (b - na) * kKeys;
+  valid = min(kKeys, (in_a ? r.a1 : r.b1) - j0);
+}
+
+// The runs of this CTA in order, packed form: from the plan's table.
+struct PackedRuns {
+  const AttnParams& p;
+  int i, end;
+  AttnSeg nxt;
+  __device__ PackedRuns(const AttnParams& p_, const volatile int*) : p(p_) {
+    i = p.cta_segs[blockIdx.x];
+    end = p.cta_segs[blockIdx.x + 1];
+    if (i < end) nxt = p.segs[i];
+  }
+  __device__ bool next(Run& r) {
+    if (i >= end) return false;
+    const AttnSeg s = nxt;
+    if (++i < end) nxt = p.segs[i];  // in flight while this run is worked on
+    r.q_row = s.q_row;
+    r.n_tok0 = min(s.n_tok, p.TQ);
+    r.n_tok1 = s.n_tok - r.n_tok0;
+    r.alt = r.n_tok1 == 0 && s.part >= 0;
+    r.pos = s.pos;
+    r.k_row0 = s.k_row0;
+    r.a1 = s.a1;
+    r.b0 = s.b0;
+    r.b1 = s.b1;
+    r.blk0 = s.blk0;
+    r.blk1 = s.blk1;
+    r.head = s.head;
+    r.prefix = 0;
+    r.part = s.part;
+    return true;
+  }
+};
+
+// Cache form: every unit (prefix: tile pair and KV head; cache: request and
+// KV head) is a line of key blocks; the lines laid end to end are cut into
+// equal spans, one per CTA, so that uneven cache lengths balance and a unit is
+// cut only where a span ends.
+struct Unit {
+  int a1, b0, b1, nb;  // key ranges of a request's cache, in blocks
+};
+__device__ __forceinline__ Unit cache_unit(const AttnParams& p, int len) {
+  len = min(max(len, 0), p.cap);
+  Unit u;
+  u.b1 = len;
+  u.b0 = max(0, len - p.Lq - p.window + 1);
+  u.a1 = 0;
+  if (p.n_sink >= u.b0) u.b0 = 0;
+  else u.a1 = p.n_sink;
+  u.nb = (u.a1 + kKeys - 1) / kKeys + (u.b1 - u.b0 + kKeys - 1) / kKeys;
+  return u;
+}
+struct CacheSpan {
+  long long total, pre;  // blocks in all lines, and in the prefix's
+  long long per_cta;
+  int nbp, pairs;        // prefix: blocks per line, tile pairs
+};
+__device__ __forceinline__ CacheSpan cache_span(const AttnParams& p, long long suffix_blocks) {
+  CacheSpan c;
+  c.nbp = (p.P + kKeys - 1) / kKeys;
+  c.pairs = p.P > 0 ? (p.n_pre_tiles + 1) / 2 : 0;
+  c.pre = static_cast<long long>(c.pairs) * c.nbp * p.H_kv;
+  c.total = c.pre + suffix_blocks * p.H_kv;
+  c.per_cta = max(static_cast<long long>(p.min_blocks), (c.total + gridDim.x - 1) / gridDim.x);
+  return c;
+}
+
+struct CacheRuns {
+  const AttnParams& p;
+  CacheSpan c;
+  long long f, end;     // this CTA's span
+  int r;                // request of the walk
+  long long cum;        // blocks (per head) of the requests before it
+  Unit u;
+  // misc: [2] first request, [4..5] blocks before it, [6..7] all blocks
+  __device__ CacheRuns(const AttnParams& p_, const volatile int* misc) : p(p_) {
+    const volatile long long* m = reinterpret_cast<const volatile long long*>(misc);
+    c = cache_span(p, m[3]);
+    f = min(c.total, c.per_cta * blockIdx.x);
+    end = min(c.total, f + c.per_cta);
+    r = misc[2];
+    cum = m[2];
+    if (r < p.n) u = cache_unit(p, p.lens[r]);
+  }
+  __device__ bool next(Run& o) {
+    if (f >= end) return false;
+    long long unit, first;  // unit index and its line's first block
+    int nb;
+    if (f < c.pre) {
+      unit = f / c.nbp;
+      nb = c.nbp;
+      first = unit * nb;
+      const int pair = static_cast<int>(unit / p.H_kv);
+      o.head = static_cast<int>(unit % p.H_kv);
+      const int tok0 = pair * 2 * p.TQ, n_tok = p.n * p.Lq - tok0;
+      o.q_row = tok0;
+      o.n_tok0 = min(n_tok, p.TQ);
+      o.n_tok1 = min(n_tok - o.n_tok0, p.TQ);
+      o.pos = kAttnFar;
+      o.k_row0 = 0;
+      o.a1 = 0;
+      o.b0 = 0;
+      o.b1 = p.P;
+      o.prefix = 1;
+    } else {
+      const long long g = f - c.pre;
+      while (g >= (cum + u.nb) * p.H_kv && r + 1 < p.n) {  // ends at a request with blocks
+        cum += u.nb;
+        u = cache_unit(p, p.lens[++r]);
+      }
+      nb = u.nb;
+      if (nb == 0) return false;
+      const long long in = g - cum * p.H_kv;
+      o.head = static_cast<int>(in / nb);
+      unit = static_cast<long long>(c.pairs) * p.H_kv + static_cast<long long>(r) * p.H_kv + o.head;
+      first = c.pre + cum * p.H_kv + static_cast<long long>(o.head) * nb;
+      o.q_row = r * p.Lq;
+      o.n_tok0 = p.Lq;
+      o.n_tok1 = 0;
+      o.pos = min(max(p.lens[r], 0), p.cap) - p.Lq;
+      o.k_row0 = r * p.cap;
+      o.a1 = u.a1;
+      o.b0 = u.b0;
+      o.b1 = u.b1;
+      o.prefix = 0;
+    }
+    const long long last = min(end, first + nb);
+    o.blk0 = static_cast<int>(f - first);
+    o.blk1 = static_cast<int>(last - first);
+    o.alt = o.n_tok1 == 0;
+    const int piece = static_cast<int>(blockIdx.x - first / c.per_cta);
+    o.part = (o.prefix ? 0 : p.np_pre) + piece * (o.alt ? 2 : 1);
+    if (o.blk1 == nb && threadIdx.x == 0) p.n_part[unit] = piece + 1;
+    f = last;
+    return true;
+  }
+};
+
+// Cache form, all threads: the blocks of all requests, and the request in
+// which this CTA's span begins with the blocks before it.
+__device__ __forceinline__ void cache_find(const AttnParams& p, volatile int* misc) {
+  volatile long long* m = reinterpret_cast<volatile long long*>(misc);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) {
+    long long sum = 0;
+    for (int r = lane; r < p.n; r += 32) sum += cache_unit(p, p.lens[r]).nb;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const CacheSpan c = cache_span(p, sum);
+    const long long f = min(c.total, c.per_cta * blockIdx.x);
+    const long long g = f - c.pre;  // a place among the requests' lines, or before them
+    int first = 0;
+    long long before = 0, run = 0;
+    bool found = g < 0;
+    for (int r0 = 0; !found && r0 < p.n; r0 += 32) {
+      const int nb = r0 + lane < p.n ? cache_unit(p, p.lens[r0 + lane]).nb : 0;
+      long long inc = nb;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, r0 + lane < p.n && g < (run + inc) * p.H_kv);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        first = r0 + l;
+        before = run + __shfl_sync(0xffffffffu, inc - nb, l);
+        found = true;
+      }
+      run += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) {
+      misc[2] = first;
+      m[2] = before;
+      m[3] = sum;
+    }
+  }
+}
+
+// ----------------------------------------------------------------- softmax --
+// bits [lo, hi) of the 32 columns from c0 on
+__device__ __forceinline__ uint32_t span_bits(int lo, int hi, int c0) {
+  lo = min(max(lo - c0, 0), 32);
+  hi = min(max(hi - c0, 0), 32);
+  if (hi <= lo) return 0u;
+  const uint32_t upto = hi == 32 ? 0xffffffffu : (1u << hi) - 1u;
+  return upto & ~((1u << lo) - 1u);  // lo < 32 here
+}
+
+template <int D, typename Runs>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tkp,
+                const __grid_constant__ CUtensorMap tvp, const AttnParams p, const bool cached) {
+  using L = Lay<D>;
+  constexpr int NS = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* misc = reinterpret_cast<volatile int*>(smem + L::kMisc);
+
+  const uint32_t barQFull = sb + L::kBar, barQEmpty = sb + L::kBar + 8;
+  auto barS = [&](int s) { return sb + L::kBar + 16 + 8u * s; };
+  auto barP = [&](int s) { return sb + L::kBar + 32 + 8u * s; };
+  auto barFull = [&](int i) { return sb + L::kBar + 48 + 8u * i; };
+  auto barEmpty = [&](int i) { return sb + L::kBar + 48 + 8u * (NS + i); };
+
+  if (threadIdx.x == 0) {
+    mbar_init(barQFull, 1);
+    mbar_init(barQEmpty, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(barS(s), 1);
+      mbar_init(barP(s), 4);
+    }
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(barFull(i), 1);
+      mbar_init(barEmpty(i), 1);
+    }
+    fence_mbar_init();
+    misc[1] = 0;
+  }
+  if (warp == 8) tmem_alloc(sb + L::kMisc, kTmemCols);
+  // rows of the Q tiles that no load fills (G does not divide 128)
+  {
+    const int filled = p.G * p.TQ, spare = (kRows - filled) * 8;
+    for (int i = threadIdx.x; i < spare * 2 * (D / 64); i += kThreads)
+      *reinterpret_cast<uint4*>(smem + L::kQ + (i / spare) * L::kChunk + filled * 128 + (i % spare) * 16) =
+          make_uint4(0u, 0u, 0u, 0u);
+    fence_async_smem();
+  }
+  if (cached) cache_find(p, misc);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = static_cast<uint32_t>(misc[0]);
+  Runs runs(p, misc);
+  Run r;
+
+  if (warp == 9) {
+    // ------------------------------------------------------------- loader
+    if (lane == 0) {
+      int g = 0, nq = 0;  // ring uses, Q uses
+      bool ok = true;
+      auto load = [&](const CUtensorMap* map, int row) {
+        const int st = g % NS;
+        if (misc[1] || !mbar_wait(barEmpty(st), ((g / NS) & 1) ^ 1, p.err)) {
+          ok = false;
+          return;
+        }
+        mbar_arrive_tx(barFull(st), L::kTile);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_2d(sb + L::kRing + st * L::kTile + c * L::kChunk, map, r.head * D + c * 64, row, barFull(st));
+        ++g;
+      };
+      while (ok && runs.next(r)) {
+        const CUtensorMap* mk = r.prefix ? &tkp : &tk;
+        const CUtensorMap* mv = r.prefix ? &tvp : &tv;
+        const int nb = r.blk1 - r.blk0, ahead = r.alt ? 2 : 1;
+        auto row = [&](int i) {
+          int j0, valid;
+          block_at(r, r.blk0 + i, j0, valid);
+          return r.k_row0 + j0;
+        };
+        for (int i = 0; ok && i < min(ahead, nb); ++i) load(mk, row(i));
+        // Q replaces the previous run's once that run's S products are done
+        if (ok && !mbar_wait(barQEmpty, (nq & 1) ^ 1, p.err)) ok = false;
+        if (!ok) break;
+        const int tiles = r.n_tok1 > 0 ? 2 : 1;
+        mbar_arrive_tx(barQFull, tiles * (D / 64) * 128 * p.G * p.TQ);
+        for (int t = 0; t < tiles; ++t)
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(sb + L::kQ + t * L::kTile + c * L::kChunk, &tq, c * 64, 0, r.head,
+                        r.q_row + t * p.TQ, barQFull);
+        ++nq;
+        for (int i = 0; ok && i < nb; ++i) {
+          load(mv, row(i));
+          if (ok && i + ahead < nb) load(mk, row(i + ahead));
+        }
+      }
+      if (!ok) misc[1] = 1;
+      // drain what is in flight before the CTA may end
+      for (int u = max(0, g - NS); u < g; ++u) mbar_wait(barFull(u % NS), (u / NS) & 1, nullptr);
+      if (nq > 0) mbar_wait(barQFull, (nq - 1) & 1, nullptr);
+    }
+  } else if (warp == 8) {
+    // ---------------------------------------------------------------- MMA
+    constexpr uint32_t idS = idesc_bf16_f32(kRows, kKeys, false, false);
+    constexpr uint32_t idO = idesc_bf16_f32(kRows, D, false, true);
+    int g = 0, nq = 0;
+    uint32_t np[2] = {0, 0};  // P phases seen
+    bool ok = true;
+    auto take = [&]() {  // the ring's next block has landed; its stage
+      const int st = g % NS;
+      if (!warp_wait(barFull(st), (g / NS) & 1, p.err, misc)) ok = false;
+      ++g;
+      return st;
+    };
+    auto qk = [&](int s, int tile, int st) {
+      if (lane == 0) {
+        const uint32_t qa = sb + L::kQ + tile * L::kTile, ka = sb + L::kRing + st * L::kTile;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          tc_mma(tmem + kColS + 128 * s, sdesc_sw128(qa + (k >> 2) * L::kChunk + (k & 3) * 32, 16, 1024),
+                 sdesc_sw128(ka + (k >> 2) * L::kChunk + (k & 3) * 32, 16, 1024), idS, k > 0 ? 1u : 0u);
+      }
+    };
+    // O += P V over the block's first `steps` groups of 16 keys
+    auto pv = [&](int s, int st, int steps, bool fresh) {
+      if (!warp_wait(barP(s), np[s] & 1, p.err, misc)) {
+        ok = false;
+        return;
+      }
+      ++np[s];
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t va = sb + L::kRing + st * L::kTile;
+        for (int k = 0; k < steps; ++k)
+          tc_mma_ts(tmem + kColO + 128 * s, tmem + kColS + 128 * s + k * 8,
+                    sdesc_sw128(va + k * 2048, L::kChunk, 1024), idO, (fresh && k == 0) ? 0u : 1u);
+      }
+    };
+    // V rows past the block's last key, up to the next multiple of 16, become
+    // zero: their weights are zero, but what the box read there may be NaN
+    auto trim = [&](int st, int valid) {
+      const int upto = (valid + 15) & ~15;
+      if (valid == upto) return;
+      for (int i = lane; i < (upto - valid) * 8 * (D / 64); i += 32) {
+        const int c = i / ((upto - valid) * 8), x = i - c * (upto - valid) * 8;
+        *reinterpret_cast<uint4*>(smem + L::kRing + st * L::kTile + c * L::kChunk + valid * 128 + x * 16) =
+            make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_async_smem();
+      __syncwarp();
+    };
+    while (ok && runs.next(r)) {
+      if (!warp_wait(barQFull, nq & 1, p.err, misc)) {
+        ok = false;
+        break;
+      }
+      ++nq;
+      tc_fence_after();
+      const int nb = r.blk1 - r.blk0;
+      const int streams = r.alt ? min(2, nb) : (r.n_tok1 > 0 ? 2 : 1);
+      const int ahead = r.alt ? 2 : 1;
+      // the first S of each stream
+      int kst = 0;
+      for (int s = 0; ok && s < streams; ++s) {
+        if (s == 0 || r.alt) kst = take();
+        if (!ok) break;
+        tc_fence_after();
+        qk(s, r.alt ? 0 : s, kst);
+        if (lane == 0) {
+          tc_commit(barS(s));
+          if (r.alt || s == streams - 1) tc_commit(barEmpty(kst));
+          if (s == streams - 1 && nb <= ahead) tc_commit(barQEmpty);
+        }
+        __syncwarp();
+      }
+      for (int i = 0; ok && i < nb; ++i) {
+        const int vst = take();
+        if (!ok) break;
+        int j0, valid;
+        block_at(r, r.blk0 + i, j0, valid);
+        if (valid < kKeys) trim(vst, valid);
+        const int steps = (valid + 15) >> 4;
+        const bool more = i + ahead < nb;
+        const int s0 = r.alt ? (i & 1) : 0, s1 = r.alt ? s0 + 1 : streams;
+        for (int s = s0; ok && s < s1; ++s) {
+          pv(s, vst, steps, i < ahead);
+          if (!ok) break;
+          if (more) {
+            if (s == s0) kst = take();
+            if (!ok) break;
+            tc_fence_after();
+            qk(s, r.alt ? 0 : s, kst);
+          }
+          if (lane == 0) tc_commit(barS(s));  // O so far, and the next S
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          tc_commit(barEmpty(vst));
+          if (more) tc_commit(barEmpty(kst));
+          if (more && i + ahead == nb - 1) tc_commit(barQEmpty);  // the run's last S product
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok) misc[1] = 1;
+    // everything issued is done before TMEM is freed and the CTA ends
+    if (lane == 0) {
+      const uint32_t done = sb + L::kMisc + 64;
+      mbar_init(done, 1);
+      fence_mbar_init();
+      tc_commit(done);
+      mbar_wait(done, 0, nullptr);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int s = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t colS = lanes + kColS + 128 * s, colO = lanes + kColO + 128 * s;
+    const int tok = row / p.G, hg = row - tok * p.G;
+    const float sc = p.scale * 1.4426950408889634f;
+    const float slack = 8.f / sc;
+    uint32_t ph = 0;  // S phases seen
+    bool ok = true;
+    while (ok && runs.next(r)) {
+      const int tile = r.alt ? 0 : s;
+      if (!r.alt && s == 1 && r.n_tok1 == 0) continue;
+      const int n_tok = tile ? r.n_tok1 : r.n_tok0;
+      const int pos0 = r.pos + (r.prefix ? 0 : tile * p.TQ);
+      const int step = r.alt ? 2 : 1;
+      const int first = r.blk0 + (r.alt ? s : 0);
+      const int pos = r.prefix ? kAttnFar : pos0 + tok;
+      const int pos_last = r.prefix ? kAttnFar : pos0 + n_tok - 1;
+      // a warp none of whose rows is a query leaves its P as it finds it: rows
+      // of a product do not mix
+      const bool idle = (warp & 3) * 32 >= n_tok * p.G;
+      float m = -INFINITY, l = 0.f;  // reference (raw scores), sum
+      for (int b = first; b < r.blk1; b += step) {
+        if (!warp_wait(barS(s), ph & 1, p.err, misc)) {
+          ok = false;
+          break;
+        }
+        ++ph;
+        if (idle) {
+          if (lane == 0) mbar_arrive(barP(s));
+          continue;
+        }
+        tc_fence_after();
+        float x[kKeys];
+        {
+          uint32_t* w = reinterpret_cast<uint32_t*>(x);
+#pragma unroll
+          for (int c = 0; c < kKeys; c += 32) tmem_ld32(colS + c, w + c);
+        }
+        tc_wait_ld();
+        int j0, valid;
+        block_at(r, b, j0, valid);
+        // blocks that every row of the tile sees whole need no mask
+        const bool whole = valid == kKeys && j0 + kKeys - 1 <= pos0 &&
+                           (j0 > pos_last - p.window || j0 + kKeys <= p.n_sink);
+        if (!whole) {
+          const int hi = min(valid, pos + 1 - j0), lo = pos - p.window + 1 - j0;
+          const int sink = min(hi, p.n_sink - j0);
+#pragma unroll
+          for (int c = 0; c < kKeys; c += 32) {
+            const uint32_t seen = span_bits(lo, hi, c) | span_bits(0, sink, c);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[c + e] = (seen >> e) & 1u ? x[c + e] : -INFINITY;
+          }
+        }
+        float mx[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          mx[q] = fmaxf(x[q * 32], x[q * 32 + 1]);
+#pragma unroll
+          for (int e = 2; e < 32; e += 2) mx[q] = fmax3(mx[q], x[q * 32 + e], x[q * 32 + e + 1]);
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        // a row's first visible key sets its reference; later only a maximum
+        // 2^8 above it moves it
+        const bool move = m == -INFINITY ? top > -INFINITY : top > m + slack;
+        if (__any_sync(0xffffffffu, move)) {
+          float f = 1.f;
+          if (move) {
+            f = m == -INFINITY ? 0.f : ex2((m - top) * sc);
+            m = top;
+            l *= f;
+          }
+          if (b > first) {
+            // the barrier of this S also covers the products so far
+#pragma unroll
+            for (int c = 0; c < D; c += 16) {
+              uint32_t w[16];
+              tmem_ld16(colO + c, w);
+              tc_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
+              tmem_st16(colO + c, w);
+            }
+          }
+        }
+        const float ref = m == -INFINITY ? 0.f : m * sc;
+        const float2 sc2 = make_float2(sc, sc), nr = make_float2(-ref, -ref);
+        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < kKeys; c += 64) {
+          uint32_t w[32];
+#pragma unroll
+          for (int e = 0; e < 64; e += 2) {
+            float2 t = ffma2(make_float2(x[c + e], x[c + e + 1]), sc2, nr);
+            t.x = ex2(t.x);
+            t.y = ex2(t.y);
+            acc[(e >> 1) & 1] = fadd2(acc[(e >> 1) & 1], t);
+            w[e >> 1] = pack_bf16x2(t.x, t.y);
+          }
+          tmem_st32(colS + c / 2, w);
+        }
+        const float2 a = fadd2(acc[0], acc[1]);
+        l += a.x + a.y;
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(barP(s));
+      }
+      if (!ok) break;
+      // ----------------------------------------------------------- epilogue
+      const bool any = first < r.blk1;
+      if (any) {
+        if (!warp_wait(barS(s), ph & 1, p.err, misc)) {
+          ok = false;
+          break;
+        }
+        ++ph;
+        tc_fence_after();
+      }
+      const bool mine = tok < n_tok;
+      const long long q_tok = r.q_row + tile * p.TQ + tok;
+      const int head = r.head * p.G + hg;
+      if (r.part < 0) {
+        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + q_tok * p.ld_o + static_cast<long long>(head) * D;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t w[32];
+          tmem_ld32(colO + c, w);
+          tc_wait_ld();
+          if (mine) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              float f[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) f[i] = inv == 0.f ? 0.f : __uint_as_float(w[e + i]) * inv;
+              *reinterpret_cast<uint4*>(dst + c + e) =
+                  make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                             pack_bf16x2(f[6], f[7]));
+            }
+          }
+        }
+        if (mine && p.lse) p.lse[q_tok * p.H_q + head] = m == -INFINITY ? -INFINITY : m * p.scale + logf(l);
+      } else {
+        // packed: part + stream, rows of the tile; cache: one row per (token,
+        // head) of the batch, streams apart only where they share rows
+        const int part = r.part + ((r.alt || !cached) ? s : 0);
+        const long long prow = cached ? q_tok * p.H_q + head : row;
+        const long long at = static_cast<long long>(part) * p.part_rows + prow;
+        float* dst = p.part_o + at * D;
+        if (mine) p.part_ml[at] = make_float2(m == -INFINITY ? -INFINITY : m * sc, l);
+        if (any) {
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            uint32_t w[32];
+            tmem_ld32(colO + c, w);
+            tc_wait_ld();
+            if (mine) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+    }
+    if (!ok) misc[1] = 1;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// -------------------------------------------------------------------- join --
+// o = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p over a row's partial
+// results, in their order (the same result every time); a row without any
+// visible key gets 0 and lse = -inf.  A warp per row, lanes over d.
+template <int D, bool CACHED>
+__global__ void __launch_bounds__(256) join_kernel(const AttnParams p, const AttnJoin* joins, int n_joins) {
+  constexpr int V = D / 32;  // values per lane
+  const int lane = threadIdx.x & 31;
+  const long long w = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  long long prow, q_tok;
+  int head, n0, base0, step0, n1 = 0, base1 = 0;
+  if (CACHED) {
+    if (w >= p.part_rows) return;
+    prow = w;
+    q_tok = w / p.H_q;
+    head = static_cast<int>(w - q_tok * p.H_q);
+    const int kv = head / p.G, req = static_cast<int>(q_tok / p.Lq);
+    const int pairs = p.P > 0 ? (p.n_pre_tiles + 1) / 2 : 0;
+    n0 = 0;
+    base0 = 0;
+    step0 = 1;
+    // (counts are held to what the buffers have, whatever a failed run left)
+    if (p.P > 0) {
+      const int pair = static_cast<int>(q_tok / (2 * p.TQ));
+      n0 = p.n_part[static_cast<long long>(pair) * p.H_kv + kv];
+      // a lone last tile ran on both streams
+      if (2 * pair + 1 >= p.n_pre_tiles) n0 *= 2;
+      n0 = min(max(n0, 0), p.np_pre);
+    }
+    base1 = p.np_pre;
+    if (cache_unit(p, p.lens[req]).nb > 0)
+      n1 = min(max(2 * p.n_part[(static_cast<long long>(pairs) + req) * p.H_kv + kv], 0), p.np_suf);
+  } else {
+    const long long j = w / kRows;
+    if (j >= n_joins) return;
+    const AttnJoin jn = joins[j];
+    prow = w - j * kRows;
+    const int tok = static_cast<int>(prow) / p.G;
+    if (tok >= jn.n_tok) return;
+    q_tok = jn.q_row + tok;
+    head = jn.head * p.G + static_cast<int>(prow) - tok * p.G;
+    n0 = jn.n_part;
+    base0 = jn.part0;
+    step0 = jn.step;
+  }
+  auto at = [&](int i) {
+    const int part = i < n0 ? base0 + i * step0 : base1 + (i - n0);
+    return static_cast<long long>(part) * p.part_rows + prow;
+  };
+  float top = -INFINITY;
+  for (int i = lane; i < n0 + n1; i += 32) top = fmaxf(top, p.part_ml[at(i)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float acc[V] = {}, l = 0.f;
+  for (int i = 0; i < n0 + n1; ++i) {
+    const float2 ml = p.part_ml[at(i)];
+    if (ml.x == -INFINITY) continue;  // saw nothing; its o was perhaps not written
+    const float f = ex2(ml.x - top);
+    l += f * ml.y;
+    const float* src = p.part_o + at(i) * D + lane * V;
+    if (V == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(src);
+      acc[0] += f * v.x, acc[1] += f * v.y, acc[V - 2] += f * v.z, acc[V - 1] += f * v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(src);
+      acc[0] += f * v.x, acc[1] += f * v.y;
+    }
+  }
+  const float inv = top == -INFINITY ? 0.f : 1.f / l;
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + q_tok * p.ld_o + static_cast<long long>(head) * D + lane * V;
+  if (V == 4)
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[V - 2] * inv, acc[V - 1] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+  if (p.lse && lane == 0)
+    p.lse[q_tok * p.H_q + head] = top == -INFINITY ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+}
+
+template <int D, typename Runs>
+cudaError_t launch_main(const AttnParams& p, int grid, const CUtensorMap& tq, const CUtensorMap& tk,
+                        const CUtensorMap& tv, const CUtensorMap& tkp, const CUtensorMap& tvp, bool cached,
+                        cudaStream_t s) {
+  auto kern = attn_kernel<D, Runs>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kThreads, Lay<D>::kBytes, s>>>(tq, tk, tv, tkp, tvp, p, cached);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_packed(const AttnParams& p, int d, int grid, const CUtensorMap& tq,
+                               const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+  return d == 128 ? launch_main<128, PackedRuns>(p, grid, tq, tk, tv, tk, tv, false, s)
+                  : launch_main<64, PackedRuns>(p, grid, tq, tk, tv, tk, tv, false, s);
+}
+
+cudaError_t launch_attn_join(const AttnParams& p, int d, const AttnJoin* joins, int n_joins, cudaStream_t s) {
+  if (n_joins <= 0) return cudaSuccess;
+  const int grid = n_joins * (kRows / 8);
+  if (d == 128) join_kernel<128, false><<<grid, 256, 0, s>>>(p, joins, n_joins);
+  else join_kernel<64, false><<<grid, 256, 0, s>>>(p, joins, n_joins);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_attn_cache(const AttnParams& p, int d, int grid, const CUtensorMap& tq,
+                              const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tkp,
+                              const CUtensorMap& tvp, cudaStream_t s) {
+  cudaError_t e = d == 128 ? launch_main<128, CacheRuns>(p, grid, tq, tk, tv, tkp, tvp, true, s)
+                           : launch_main<64, CacheRuns>(p, grid, tq, tk, tv, tkp, tvp, true, s);
+  if (e != cudaSuccess) return e;
+  const long long blocks = (p.part_rows + 7) / 8;
+  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+  if (d == 128) join_kernel<128, true><<<static_cast<unsigned>(blocks), 256, 0, s>>>(p, nullptr, 0);
+  else join_kernel<64, true><<<static_cast<unsigned>(blocks), 256, 0, s>>>(p, nullptr, 0);
+  return cudaGetLastError();
+}
+
+}  // namespace mf

@@ -119,6 +119,11 @@ int make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, ui
              uint32_t box_inner, uint32_t box_rows,
              CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 
+// 4-D bf16 map (dims, then the three outer strides in bytes) with 128-byte
+// swizzle; out-of-range reads give 0.
+int make_map4(CUtensorMap* m, const void* base, const uint64_t dims[4], const uint64_t strides[3],
+              const uint32_t box[4]);
+
 // Device memory through the handle's allocator (stream-ordered).
 void* dev_alloc(mf_bsr_t h, size_t bytes, cudaStream_t s);
 void dev_free(mf_bsr_t h, void* p, cudaStream_t s);

@@ -162,6 +162,80 @@ cudaError_t launch_select_noalloc(const RowBlock* rbs_host, int R, int C, int H_
                                   int causal, float p, const float* mass, int* row_ptr,
                                   int* col_idx, long long* nnz, cudaStream_t s);
 
+// Per-head norm of queries and keys with the rotary embedding (mf_rope.cu).
+struct RopeParams {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  long long ld_q, ld_k, ld_qo, ld_ko;  // elements between tokens
+  const void* q_weight;                // [d] or null (ones)
+  const void* k_weight;
+  const int* positions;                // [T]
+  const unsigned long long* freq;      // [rot/2] turns per position, 64-bit fractions
+  int H_q, H_k, rot;
+  int layout;                          // 0: pairs (i, i + rot/2), 1: pairs (2i, 2i+1)
+  int norm;
+  float eps, gain;
+  long long n_rows;                    // T * (H_q + H_k)
+  int rows_per_cta;                    // set by the launcher
+};
+cudaError_t launch_rope(const RopeParams& p, int f32, int d, cudaStream_t s);
+
+// Attention over packed sequences or caches (mf_attn_tc.cu).
+constexpr int kAttnNoWindow = 1 << 30;  // a window that hides nothing
+constexpr int kAttnFar = 1 << 29;       // a row position past every key, and the most keys
+
+// One run of key blocks of one query tile pair (packed form): what a CTA does
+// between two loads of Q.  Keys are positions [0, a1) and [b0, b1) of a
+// sequence, cut into blocks of 128 from each range's start.
+struct alignas(16) AttnSeg {
+  int q_row;       // first token's row in q and o
+  int n_tok;       // tokens of the (one or two) tiles
+  int pos;         // position of the first token in its sequence
+  int k_row0;      // the sequence's first row in k and v
+  int a1, b0, b1;
+  int blk0, blk1;  // this run's blocks
+  int head;        // KV head
+  int part;        // partial result index, or -1: the run is whole and writes o
+  int pad;
+};
+// One tile whose runs wrote partial results (packed form).
+struct AttnJoin {
+  int q_row, n_tok, head;
+  int part0, n_part, step;
+};
+
+struct AttnParams {
+  int H_q, H_kv, G, TQ;      // heads, heads per group, tokens per 128-row tile
+  float scale;               // of the scores
+  int window, n_sink;
+  void* o;
+  long long ld_o;
+  float* lse;                // [rows of q][H_q] or null
+  // packed form
+  const AttnSeg* segs;
+  const int* cta_segs;       // [grid + 1]
+  // cache form
+  const int* lens;           // [n] device
+  int n, Lq, cap, P;
+  int n_pre_tiles;           // row tiles of all n * Lq tokens
+  int np_pre, np_suf;        // partial results a row can have from each
+  int min_blocks;            // least key blocks per CTA
+  int* n_part;               // [units] runs of each unit, written by its last run
+  // partial results
+  float* part_o;             // [partial][part_rows][d], not normalised
+  float2* part_ml;           // [partial][part_rows]: reference (log2 units), sum
+  long long part_rows;
+  int* err;
+};
+cudaError_t launch_attn_packed(const AttnParams& p, int d, int grid, const CUtensorMap& tq,
+                               const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s);
+cudaError_t launch_attn_join(const AttnParams& p, int d, const AttnJoin* joins, int n_joins, cudaStream_t s);
+cudaError_t launch_attn_cache(const AttnParams& p, int d, int grid, const CUtensorMap& tq,
+                              const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tkp,
+                              const CUtensorMap& tvp, cudaStream_t s);
+
 cudaError_t launch_selftest_wait(int* err, unsigned long long limit_ns, cudaStream_t s);
 
 }  // namespace mf

@@ -25,7 +25,9 @@ EXPORTED = ("mf_version", "mf_last_error", "mf_supported", "mf_bsr_create", "mf_
             "mf_device_status", "mf_selftest_wait", "mf_profile",
             "mf_profile_read", "mf_profile_kinds", "mf_select_noalloc", "mf_bsr_set_exact",
             "mf_bsr_create_chunked", "mf_prefix_hashes", "mf_bm_create", "mf_bm_destroy",
-            "mf_bm_insert", "mf_bm_match", "mf_bm_assemble", "mf_bm_stats")
+            "mf_bm_insert", "mf_bm_match", "mf_bm_assemble", "mf_bm_stats",
+            "mf_rope_frequencies", "mf_qk_norm_rope", "mf_attn_create_packed", "mf_attn_create_cache",
+            "mf_attn_destroy", "mf_attn_workspace", "mf_attn_packed", "mf_attn_cached", "mf_attn_status")
 KERNELS = ("stats", "select", "scan", "pack", "union", "retrieve")
 
 
@@ -90,6 +92,19 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mf_bm_match.argtypes = [vp, i32, u64p, i32, ctypes.POINTER(i32)]
     lib.mf_bm_assemble.argtypes = [vp, i32, u64p, vp, i32, vp]
     lib.mf_bm_stats.argtypes = [vp, i64p]
+    i64, f32, f64 = ctypes.c_int64, ctypes.c_float, ctypes.c_double
+    lib.mf_rope_frequencies.argtypes = [i32, f64, i32, f64, i32, f64, f64, u64p, ctypes.POINTER(f32)]
+    lib.mf_qk_norm_rope.argtypes = [vp, i64] * 4 + [vp, vp, i32, f32, vp, vp, i32, i32, f32, i32, i32, i32,
+                                                    i32, i32, vp]
+    lib.mf_attn_create_packed.argtypes = [ctypes.POINTER(vp), vp, vp, i32, i32, i32, i32, i32, i32, ALLOC_FN,
+                                          FREE_FN, vp]
+    lib.mf_attn_create_cache.argtypes = [ctypes.POINTER(vp)] + [i32] * 9 + [ALLOC_FN, FREE_FN, vp]
+    lib.mf_attn_destroy.argtypes = [vp]
+    lib.mf_attn_destroy.restype = None
+    lib.mf_attn_workspace.argtypes = [vp, i32, i64p]
+    lib.mf_attn_packed.argtypes = [vp] + [vp, i64] * 4 + [vp, i32, f32, vp, i64, vp]
+    lib.mf_attn_cached.argtypes = [vp, i32] + [vp, i64] * 3 + [vp] + [vp, i64] * 3 + [vp, i32, f32, vp, i64, vp]
+    lib.mf_attn_status.argtypes = [vp, vp]
     for name in EXPORTED:
         getattr(lib, name)
     _lib = lib
@@ -119,6 +134,47 @@ def _dtype_code(t) -> int:
     if t.dtype == torch.float32:
         return MF_DTYPE_F32
     raise TypeError(f"unsupported dtype {t.dtype}")
+
+
+def _on(device, stream):
+    """(device guard, stream, stream guard) for a call on `device`: memory made
+    under both guards belongs to the stream the call runs on."""
+    import torch
+    guard = torch.cuda.device(device)
+    with guard:
+        st = torch.cuda.current_stream() if stream is None else stream
+    if st.device != device:
+        raise MapFlowError(MF_ERR_ARG, f"the stream is on {st.device}, the tensors on {device}")
+    return torch.cuda.device(device), st, torch.cuda.stream(st)
+
+
+def _rows(name: str, t, heads: int, d: int, tokens: Optional[int], dtype, device):
+    """Checks a tensor of [..., heads, d] rows whose leading dimensions are
+    `tokens` equally spaced tokens; returns the values between two tokens."""
+    if t.device != device or t.device.type != "cuda":
+        raise MapFlowError(MF_ERR_ARG, f"{name} must be a CUDA tensor on {device}, is on {t.device}")
+    if t.dtype != dtype:
+        raise MapFlowError(MF_ERR_ARG, f"{name} must be {dtype}, is {t.dtype}")
+    if t.dim() < 3 or t.shape[-2] != heads or t.shape[-1] != d:
+        raise MapFlowError(MF_ERR_ARG, f"{name} must end in [{heads}, {d}], is {tuple(t.shape)}")
+    if t.stride(-1) != 1 or (heads > 1 and t.stride(-2) != d):
+        raise MapFlowError(MF_ERR_ARG, f"{name}: a token's heads must lie next to each other")
+    n, ld = 1, None
+    for i in range(t.dim() - 3, -1, -1):
+        if t.shape[i] != 1:
+            if ld is None:
+                ld = t.stride(i)
+            elif t.stride(i) != n * ld:
+                raise MapFlowError(MF_ERR_ARG, f"{name}: its tokens are not equally spaced")
+        n *= t.shape[i]
+    if tokens is not None and n != tokens:
+        raise MapFlowError(MF_ERR_ARG, f"{name} holds {n} tokens, {tokens} expected")
+    return heads * d if ld is None else ld
+
+
+def _vector(name: str, t, shape, dtype, device):
+    if t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise MapFlowError(MF_ERR_ARG, f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}")
 
 
 # ------------------------------------------------------ torch allocator ----
@@ -362,6 +418,216 @@ class BlockManager:
             self.close()
         except Exception:  # noqa: BLE001
             pass
+
+
+# ---------------------------------- rotary embedding and attention layers --
+_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def mf_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                        original_length: int = 0, beta_fast: float = 32.0,
+                        beta_slow: float = 1.0) -> Tuple[np.ndarray, float]:
+    """(turns uint64 [rot_dim/2], gain): the rotary table (see mapflow.h)."""
+    if scaling not in _SCALINGS:
+        raise MapFlowError(MF_ERR_ARG, f"unknown scaling {scaling!r} ({', '.join(_SCALINGS)})")
+    turns = np.zeros(max(int(rot_dim) // 2, 1), np.uint64)
+    gain = ctypes.c_float()
+    _check(load_library().mf_rope_frequencies(
+        int(rot_dim), float(base), _SCALINGS[scaling], float(factor), int(original_length), float(beta_fast),
+        float(beta_slow), turns.ctypes.data_as(ctypes.POINTER(ctypes.c_uint64)), ctypes.byref(gain)))
+    return turns, float(gain.value)
+
+
+class RotaryPlan:
+    """A rotary table on the device: per-head norm and rotary embedding of
+    queries and keys in one pass (see mf_qk_norm_rope in mapflow.h).
+
+    scaling: "none", "linear", "ntk" or "yarn"; layout: "half" (pairs i and
+    i + rot_dim/2) or "interleaved" (pairs 2i and 2i + 1)."""
+
+    def __init__(self, rot_dim: int, base: float = 10000.0, layout: str = "half", scaling: str = "none",
+                 factor: float = 1.0, original_length: int = 0, beta_fast: float = 32.0,
+                 beta_slow: float = 1.0, device=None):
+        import torch
+        if layout not in _LAYOUTS:
+            raise MapFlowError(MF_ERR_ARG, f"unknown layout {layout!r} ({', '.join(_LAYOUTS)})")
+        turns, self.gain = mf_rope_frequencies(rot_dim, base, scaling, factor, original_length, beta_fast,
+                                               beta_slow)
+        self.rot_dim, self.layout = int(rot_dim), layout
+        device = torch.device("cuda" if device is None else device)
+        self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
+
+    def apply(self, q, k, positions, q_weight=None, k_weight=None, eps: float = 1e-6, norm: Optional[bool] = None,
+              q_out=None, k_out=None, stream=None):
+        """q [T, H_q, d] and k [T, H_k, d] (or None) normed and rotated;
+        returns (q_out, k_out), new tensors unless given (q_out=q: in place).
+        The norm is taken when a weight is given or norm is True."""
+        import torch
+        if norm is None:
+            norm = q_weight is not None or k_weight is not None
+        dev, dt = q.device, q.dtype
+        code = _dtype_code(q)
+        if q.dim() != 3:
+            raise MapFlowError(MF_ERR_ARG, f"q must be [T, H_q, d], is {tuple(q.shape)}")
+        T, H_q, d = q.shape
+        ld_q = _rows("q", q, H_q, d, T, dt, dev)
+        H_k = 0 if k is None else k.shape[-2]
+        ld_k = 0 if k is None else _rows("k", k, H_k, d, T, dt, dev)
+        _vector("positions", positions, (T,), torch.int32, dev)
+        if self.turns.device != dev:
+            raise MapFlowError(MF_ERR_ARG, f"the plan is on {self.turns.device}, q on {dev}")
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is not None:
+                _vector(name, w, (d,), dt, dev)
+        dev_guard, st, st_guard = _on(dev, stream)
+        with dev_guard, st_guard:
+            if q_out is None:
+                q_out = torch.empty((T, H_q, d), dtype=dt, device=dev)
+            if k is not None and k_out is None:
+                k_out = torch.empty((T, H_k, d), dtype=dt, device=dev)
+            ld_qo = _rows("q_out", q_out, H_q, d, T, dt, dev)
+            ld_ko = 0 if k is None else _rows("k_out", k_out, H_k, d, T, dt, dev)
+            _check(load_library().mf_qk_norm_rope(
+                _ptr(q), ld_q, _ptr(q_out), ld_qo, _ptr(k), ld_k, _ptr(k_out) if k is not None else None, ld_ko,
+                _ptr(q_weight), _ptr(k_weight), int(norm), float(eps), _ptr(positions), _ptr(self.turns),
+                self.rot_dim, _LAYOUTS[self.layout], self.gain, code, T, H_q, H_k, d, int(st.cuda_stream)))
+        return q_out, (k_out if k is not None else None)
+
+
+class _AttentionPlan:
+    """Owner of one mf_attn_t."""
+
+    handle = None
+
+    def _workspace(self, n: int, dev):
+        import torch
+        need = ctypes.c_int64()
+        _check(load_library().mf_attn_workspace(self.handle, n, ctypes.byref(need)))
+        return torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
+
+    def _checked(self, q, k, v, o, lse, rows: int, q_shape, k_tokens: int):
+        import torch
+        dt, dev = torch.bfloat16, self.device
+        if tuple(q.shape) != tuple(q_shape):
+            raise MapFlowError(MF_ERR_ARG, f"q must be {tuple(q_shape)}, is {tuple(q.shape)}")
+        lds = [_rows("q", q, self.H_q, self.d, rows, dt, dev), _rows("k", k, self.H_kv, self.d, k_tokens, dt, dev),
+               _rows("v", v, self.H_kv, self.d, k_tokens, dt, dev)]
+        if o is None:
+            o = torch.empty(tuple(q_shape), dtype=dt, device=dev)
+        lds.append(_rows("o", o, self.H_q, self.d, rows, dt, dev))
+        if lse is not None:
+            _vector("lse", lse, tuple(q_shape)[:-1], torch.float32, dev)
+        return lds, o
+
+    def status(self, stream=None) -> None:
+        _, st, _ = _on(self.device, stream)
+        _check(load_library().mf_attn_status(self.handle, int(st.cuda_stream)))
+
+    def close(self) -> None:
+        if self.handle is not None:
+            load_library().mf_attn_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:  # noqa: BLE001
+            pass
+
+
+class WindowAttention(_AttentionPlan):
+    """Attention over packed sequences with an optional sliding window and
+    `sinks` first tokens that stay visible; with q_begin, over query chunks
+    (see mf_attn_create_packed in mapflow.h).  bf16."""
+
+    def __init__(self, cu_seqlens: Sequence[int], H_q: int, H_kv: int, d: int, window: Optional[int] = None,
+                 sinks: int = 0, q_begin: Optional[Sequence[int]] = None, use_torch_allocator: bool = True):
+        lib = load_library()
+        if window is not None and window < 1:
+            raise MapFlowError(MF_ERR_ARG, f"window = {window} must be >= 1 (None: no window)")
+        cu = np.ascontiguousarray(np.asarray(cu_seqlens, dtype=np.int32))
+        if cu.ndim != 1 or len(cu) < 2:
+            raise MapFlowError(MF_ERR_ARG, "cu_seqlens must hold at least two offsets")
+        qb = None if q_begin is None else np.ascontiguousarray(np.asarray(q_begin, dtype=np.int32))
+        if qb is not None and qb.shape != (len(cu) - 1,):
+            raise MapFlowError(MF_ERR_ARG, f"q_begin must hold {len(cu) - 1} rows")
+        self.H_q, self.H_kv, self.d, self.T = int(H_q), int(H_kv), int(d), int(cu[-1])
+        a, f = _torch_allocator() if use_torch_allocator else (ALLOC_FN(), FREE_FN())
+        self._keep = (a, f)
+        h = ctypes.c_void_p()
+        _check(lib.mf_attn_create_packed(
+            ctypes.byref(h), cu.ctypes.data_as(ctypes.c_void_p),
+            None if qb is None else qb.ctypes.data_as(ctypes.c_void_p), len(cu) - 1, self.H_q, self.H_kv, self.d,
+            0 if window is None else int(window), int(sinks), a, f, None))
+        self.handle = h
+        import torch
+        self.device = torch.device("cuda", torch.cuda.current_device())
+
+    def attend(self, q, k, v, scale: Optional[float] = None, o=None, lse=None, stream=None):
+        """q [T, H_q, d], k and v [T, H_kv, d] -> o [T, H_q, d] (rows before a
+        q_begin are left as they are); lse: fp32 [T, H_q] to fill, or None."""
+        dev_guard, st, st_guard = _on(self.device, stream)
+        with dev_guard, st_guard:
+            (lq, lk, lv, lo), o = self._checked(q, k, v, o, lse, self.T, (self.T, self.H_q, self.d), self.T)
+            ws = self._workspace(1, self.device)
+            _check(load_library().mf_attn_packed(
+                self.handle, _ptr(q), lq, _ptr(k), lk, _ptr(v), lv, _ptr(o), lo, _ptr(lse), MF_DTYPE_BF16,
+                self.d ** -0.5 if scale is None else float(scale), _ptr(ws), 0 if ws is None else ws.numel(),
+                int(st.cuda_stream)))
+        return o
+
+
+class CacheAttention(_AttentionPlan):
+    """Decoding attention of up to n requests with Lq new tokens each over
+    their caches of `capacity` rows, with an optional window and sinks, or over
+    a prefix of prefix_len tokens that all requests share (see
+    mf_attn_create_cache in mapflow.h).  bf16."""
+
+    def __init__(self, n: int, Lq: int, capacity: int, H_q: int, H_kv: int, d: int,
+                 window: Optional[int] = None, sinks: int = 0, prefix_len: int = 0,
+                 use_torch_allocator: bool = True):
+        lib = load_library()
+        if window is not None and window < 1:
+            raise MapFlowError(MF_ERR_ARG, f"window = {window} must be >= 1 (None: no window)")
+        self.n, self.Lq, self.capacity, self.prefix_len = int(n), int(Lq), int(capacity), int(prefix_len)
+        self.H_q, self.H_kv, self.d = int(H_q), int(H_kv), int(d)
+        a, f = _torch_allocator() if use_torch_allocator else (ALLOC_FN(), FREE_FN())
+        self._keep = (a, f)
+        h = ctypes.c_void_p()
+        _check(lib.mf_attn_create_cache(
+            ctypes.byref(h), self.n, self.Lq, self.capacity, self.prefix_len, self.H_q, self.H_kv, self.d,
+            0 if window is None else int(window), int(sinks), a, f, None))
+        self.handle = h
+        import torch
+        self.device = torch.device("cuda", torch.cuda.current_device())
+
+    def attend(self, q, k_cache, v_cache, lens, k_prefix=None, v_prefix=None, scale: Optional[float] = None,
+               o=None, lse=None, stream=None):
+        """q [m, Lq, H_q, d] of m <= n requests, k_cache and v_cache [m,
+        capacity, H_kv, d], lens int32 [m] on the device (keys in each cache,
+        the new tokens' among them), k_prefix and v_prefix [prefix_len, H_kv,
+        d] -> o [m, Lq, H_q, d]; lse: fp32 [m, Lq, H_q] to fill, or None."""
+        import torch
+        dt = torch.bfloat16
+        dev_guard, st, st_guard = _on(self.device, stream)
+        with dev_guard, st_guard:
+            m = q.shape[0]
+            (lq, lk, lv, lo), o = self._checked(q, k_cache, v_cache, o, lse, m * self.Lq,
+                                                (m, self.Lq, self.H_q, self.d), m * self.capacity)
+            _vector("lens", lens, (m,), torch.int32, self.device)
+            lkp = lvp = 0
+            if self.prefix_len:
+                if k_prefix is None or v_prefix is None:
+                    raise MapFlowError(MF_ERR_ARG, "the plan has a prefix: k_prefix and v_prefix are needed")
+                lkp = _rows("k_prefix", k_prefix, self.H_kv, self.d, self.prefix_len, dt, self.device)
+                lvp = _rows("v_prefix", v_prefix, self.H_kv, self.d, self.prefix_len, dt, self.device)
+            ws = self._workspace(m, self.device)
+            _check(load_library().mf_attn_cached(
+                self.handle, m, _ptr(q), lq, _ptr(k_cache), lk, _ptr(v_cache), lv, _ptr(lens), _ptr(k_prefix), lkp,
+                _ptr(v_prefix), lvp, _ptr(o), lo, _ptr(lse), MF_DTYPE_BF16,
+                self.d ** -0.5 if scale is None else float(scale), _ptr(ws), ws.numel(), int(st.cuda_stream)))
+        return o
 
 
 # ------------------------------------------------------ convenience class --

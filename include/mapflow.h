@@ -459,6 +459,142 @@ MF_API int mf_select_noalloc(const float* mass, const int32_t* cu_seqlens_host, 
                              int H_s, int B, int causal, float p, int32_t* row_ptr,
                              int32_t* col_idx, int64_t col_capacity, int64_t* nnz, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The layers around the reused maps: rotary embedding and attention
+ *
+ * [Summary] "MapFlow System Design" item 1 (partial recomputation): the
+ * receiver's first r layers run ordinarily; the sender's Q and K that
+ * mf_compress takes, and the receiver's, are normed and rotated first.  The
+ * pages print no formula for either; the definitions below are the usual ones.
+ *
+ * Tensors here are rows of heads with a stride between tokens: token t of a
+ * tensor with H heads has its values at t * ld .. t * ld + H * d, so that q, k
+ * and v may be parts of one fused projection.  Bases are 16-byte aligned and
+ * strides a multiple of 16 bytes (MF_ERR_ARG otherwise).  Products and softmax
+ * statistics are fp32; outputs are rounded once.
+ * ------------------------------------------------------------------------- */
+
+#define MF_ROPE_NONE   0  /* f_i = base^(-2i/rot_dim) radians per position        */
+#define MF_ROPE_LINEAR 1  /* f_i / factor                                         */
+#define MF_ROPE_NTK    2  /* base * factor^(rot_dim/(rot_dim-2)) for base         */
+#define MF_ROPE_YARN   3  /* by parts: f_i / factor where a pair turns less than
+                             beta_slow times in original_length, f_i where more
+                             than beta_fast times, a ramp over the pairs between;
+                             gain 0.1 ln(factor) + 1                              */
+#define MF_ROPE_HALF        0  /* pairs (i, i + rot_dim/2)                        */
+#define MF_ROPE_INTERLEAVED 1  /* pairs (2i, 2i + 1)                              */
+
+/*
+ * mf_rope_frequencies — the rotary table of rot_dim/2 pairs: each pair's
+ * angle per position as a 64-bit binary fraction of a turn (so that angles of
+ * far positions are exact: position times entry, modulo 2^64), and the gain
+ * by which cosine and sine are multiplied.  Host only.
+ *   factor           >= 1 (ignored by MF_ROPE_NONE)
+ *   original_length, beta_fast, beta_slow   MF_ROPE_YARN only
+ *   turns_out        HOST uint64 [rot_dim/2]     gain_out   HOST float
+ * Errors: MF_ERR_ARG.
+ */
+MF_API int mf_rope_frequencies(int rot_dim, double base, int scaling, double factor, int original_length,
+                               double beta_fast, double beta_slow, uint64_t* turns_out, float* gain_out);
+
+/*
+ * mf_qk_norm_rope — for every head of q and k: x * (mean(x^2) + eps)^(-1/2) *
+ * weight where norm is 1, then the rotation of its first rot_dim dimensions by
+ * positions[t] * the table's angles (times gain); the others keep the normed
+ * value.  fp32 throughout, rounded once.  One pass over the data.
+ *   q [T][H_q][d], k [T][H_k][d]   dtype, ld_q / ld_k values between tokens;
+ *                     H_k = 0: no keys (k, k_out NULL)
+ *   q_out, k_out      as q and k; the input itself (in place, same stride) or
+ *                     memory apart from every input and the other output
+ *   q_weight, k_weight  [d] (dtype) or NULL (ones); NULL when norm is 0
+ *   positions         int32 [T] (any value, in any order)
+ *   turns             DEVICE uint64 [rot_dim/2] as mf_rope_frequencies gives it
+ *   d                 64 or 128; rot_dim even, 2 .. d
+ * T = 0 is a no-op.  Errors: MF_ERR_ARG, MF_ERR_UNSUPPORTED, MF_ERR_CUDA.
+ */
+MF_API int mf_qk_norm_rope(const void* q, int64_t ld_q, void* q_out, int64_t ld_qo, const void* k, int64_t ld_k,
+                           void* k_out, int64_t ld_ko, const void* q_weight, const void* k_weight, int norm,
+                           float eps, const int32_t* positions, const uint64_t* turns, int rot_dim, int layout,
+                           float gain, int dtype, int T, int H_q, int H_k, int d, void* stream);
+
+typedef struct mf_attn_s* mf_attn_t; /* opaque; a plan for attention calls */
+
+/*
+ * mf_attn_create_packed — a plan for attention over packed sequences: the row
+ * at position i of a sequence sees the keys j <= i of it with i - j < window
+ * or j < n_sink.
+ *   cu_seqlens_host  HOST int32 [n_seqs + 1] as for mf_bsr_create
+ *   q_begin_host     HOST int32 [n_seqs] or NULL: first query row of each
+ *                    sequence, any value in [0, L_s]; its keys start at 0
+ *   H_q, H_kv        H_q % H_kv == 0, H_q / H_kv <= 128, H_q <= 1024; d 64 or 128
+ *   window           >= 1, or 0: no window       n_sink   >= 0
+ * The plan lays out the work on the host and copies its tables to the device
+ * (synchronous); it serves any number of calls with these lengths.  Errors:
+ * MF_ERR_ARG, MF_ERR_UNSUPPORTED, MF_ERR_OOM, MF_ERR_CUDA.
+ *
+ * mf_attn_create_cache — a plan for up to n_max requests with Lq new tokens
+ * each (their keys and values already in the caches), Lq * H_q / H_kv <= 128.
+ * Request r's cache is rows r * capacity .. of the cache tensors, of which
+ * lens[r] hold keys; new token t is at position p = lens[r] - Lq + t and sees
+ * keys j <= p of the cache with p - j < window or j < n_sink.  With
+ * prefix_len > 0 every row also sees all prefix_len keys of a prefix that the
+ * requests share, read once for all of them; window and n_sink are then 0
+ * (MF_ERR_UNSUPPORTED otherwise).  A row that sees no key gets o = 0 and
+ * lse = -inf.
+ *
+ * A value that is not finite in a key or value row spreads to the rows that
+ * see it, and a value row may reach others of its sequence within the same
+ * 128-key block; rows past a sequence's or a cache's end, and other requests'
+ * rows, reach nothing.
+ */
+MF_API int mf_attn_create_packed(mf_attn_t* out, const int32_t* cu_seqlens_host, const int32_t* q_begin_host,
+                                 int n_seqs, int H_q, int H_kv, int d, int window, int n_sink,
+                                 mf_alloc_fn alloc_fn, mf_free_fn free_fn, void* alloc_ctx);
+MF_API int mf_attn_create_cache(mf_attn_t* out, int n_max, int Lq, int capacity, int prefix_len, int H_q,
+                                int H_kv, int d, int window, int n_sink, mf_alloc_fn alloc_fn,
+                                mf_free_fn free_fn, void* alloc_ctx);
+/* Release a plan (waits for the device first). */
+MF_API void mf_attn_destroy(mf_attn_t h);
+
+/*
+ * mf_attn_workspace — bytes of device workspace one call needs (a packed plan
+ * may need none; n: the call's requests, cache plans only).  The workspace is
+ * the caller's, 256-byte aligned, needs no initialisation and holds nothing
+ * between calls; calls that may overlap on the GPU (other streams, graphs
+ * that replay at the same time) need one each.
+ */
+MF_API int mf_attn_workspace(mf_attn_t h, int n, int64_t* bytes);
+
+/*
+ * mf_attn_packed — o = softmax(scale * q k^T over the visible keys) v.
+ *   q, o [T][H_q][d], k, v [T][H_kv][d]   bf16, T = cu_seqlens[n_seqs]; rows
+ *                before a sequence's q_begin are neither read in q nor written
+ *                in o and lse; o shares no memory with an input
+ *   lse          fp32 [T][H_q] log of the softmax's denominator, or NULL
+ *   dtype        MF_DTYPE_BF16 (MF_ERR_UNSUPPORTED otherwise)
+ *   scale        > 0, e.g. 1/sqrt(d)
+ * Asynchronous, no host synchronisation, no state kept in the plan between
+ * calls (a failed device-side wait is recorded for mf_attn_status).
+ *
+ * mf_attn_cached — the cache form for n <= n_max requests.
+ *   q, o         [n * Lq][H_q][d];  lse fp32 [n * Lq][H_q] or NULL
+ *   k_cache, v_cache   [n * capacity][H_kv][d]
+ *   lens         DEVICE int32 [n], held to [0, capacity]; read on the device, so
+ *                that a captured graph follows it from replay to replay
+ *   k_prefix, v_prefix [prefix_len][H_kv][d], or NULL without a prefix
+ * Errors: MF_ERR_ARG, MF_ERR_UNSUPPORTED, MF_ERR_CUDA.
+ */
+MF_API int mf_attn_packed(mf_attn_t h, const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
+                          int64_t ld_v, void* o, int64_t ld_o, float* lse, int dtype, float scale,
+                          void* workspace, int64_t workspace_bytes, void* stream);
+MF_API int mf_attn_cached(mf_attn_t h, int n, const void* q, int64_t ld_q, const void* k_cache, int64_t ld_k,
+                          const void* v_cache, int64_t ld_v, const int32_t* lens, const void* k_prefix,
+                          int64_t ld_kp, const void* v_prefix, int64_t ld_vp, void* o, int64_t ld_o, float* lse,
+                          int dtype, float scale, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* mf_attn_status — as mf_device_status, for a plan's calls. */
+MF_API int mf_attn_status(mf_attn_t h, void* stream);
+
 /*
  * mf_selftest_wait — failure-detection self-test (no counterpart on the
  * pages).  Launches one thread that waits on a device barrier nothing will
