@@ -69,6 +69,7 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   volatile int* misc = reinterpret_cast<volatile int*>(smem + L::kMisc);
 
   const uint32_t barQFull = sb + L::kBar, barQEmpty = sb + L::kBar + 8;
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = static_cast<uint32_t>(misc[0]);
+  const uint32_t tmem = static_cast<uint32_t>(uniform(misc[0]));
   Runs runs(p, misc);
   Run r;
 
@@ -419,37 +420,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- MMA
     constexpr uint32_t idS = idesc_bf16_f32(kRows, kKeys, false, false);
     constexpr uint32_t idO = idesc_bf16_f32(kRows, D, false, true);
-    int g = 0, nq = 0;
-    uint32_t np[2] = {0, 0};  // P phases seen
+    const uint64_t q_desc = sdesc_sw128(sb + L::kQ, 16, 1024);             // K-major
+    const uint64_t k_desc = sdesc_sw128(sb + L::kRing, 16, 1024);
+    const uint64_t v_desc = sdesc_sw128(sb + L::kRing, L::kChunk, 1024);   // MN-major
+    int stage = 0;
+    uint32_t ring_ph = 0, q_ph = 0, p_ph0 = 0, p_ph1 = 0;
     bool ok = true;
     auto take = [&]() {  // the ring's next block has landed; its stage
-      const int st = g % NS;
-      if (!warp_wait(barFull(st), (g / NS) & 1, p.err, misc)) ok = false;
-      ++g;
+      const int st = stage;
+      if (!warp_wait(barFull(st), ring_ph, p.err, misc)) ok = false;
+      if (++stage == NS) {
+        stage = 0;
+        ring_ph ^= 1;
+      }
+      tc_fence_after();
       return st;
     };
     auto qk = [&](int s, int tile, int st) {
+      const uint64_t qd = q_desc + (uint32_t)(tile * (L::kTile >> 4)), kd = k_desc + (uint32_t)(st * (L::kTile >> 4));
+      constexpr uint32_t kC = L::kChunk >> 4;
+      const uint32_t dst = tmem + kColS + 128 * s;
       if (lane == 0) {
-        const uint32_t qa = sb + L::kQ + tile * L::kTile, ka = sb + L::kRing + st * L::kTile;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          tc_mma(tmem + kColS + 128 * s, sdesc_sw128(qa + (k >> 2) * L::kChunk + (k & 3) * 32, 16, 1024),
-                 sdesc_sw128(ka + (k >> 2) * L::kChunk + (k & 3) * 32, 16, 1024), idS, k > 0 ? 1u : 0u);
+          tc_mma(dst, qd + ((k >> 2) * kC + (k & 3) * 2), kd + ((k >> 2) * kC + (k & 3) * 2), idS, k > 0 ? 1u : 0u);
       }
     };
     // O += P V over the block's first `steps` groups of 16 keys
-    auto pv = [&](int s, int st, int steps, bool fresh) {
-      if (!warp_wait(barP(s), np[s] & 1, p.err, misc)) {
+    auto pv = [&](int s, int st, int steps, uint32_t fresh) {
+      uint32_t& ph = s ? p_ph1 : p_ph0;
+      if (!warp_wait(barP(s), ph, p.err, misc)) {
         ok = false;
         return;
       }
-      ++np[s];
+      ph ^= 1;
       tc_fence_after();
+      const uint64_t vd = v_desc + (uint32_t)(st * (L::kTile >> 4));
+      const uint32_t dst = tmem + kColO + 128 * s, src = tmem + kColS + 128 * s;
       if (lane == 0) {
-        const uint32_t va = sb + L::kRing + st * L::kTile;
-        for (int k = 0; k < steps; ++k)
-          tc_mma_ts(tmem + kColO + 128 * s, tmem + kColS + 128 * s + k * 8,
-                    sdesc_sw128(va + k * 2048, L::kChunk, 1024), idO, (fresh && k == 0) ? 0u : 1u);
+        if (steps == 8) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) tc_mma_ts(dst, src + k * 8, vd + k * 128, idO, k > 0 ? 1u : fresh ^ 1u);
+        } else {
+          for (int k = 0; k < steps; ++k) tc_mma_ts(dst, src + k * 8, vd + k * 128, idO, k > 0 ? 1u : fresh ^ 1u);
+        }
       }
     };
     // V rows past the block's last key, up to the next multiple of 16, become
@@ -465,26 +479,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_async_smem();
       __syncwarp();
     };
-    while (ok && runs.next(r)) {
-      if (!warp_wait(barQFull, nq & 1, p.err, misc)) {
+    while (ok && uniform(runs.next(r))) {
+      if (!warp_wait(barQFull, q_ph, p.err, misc)) {
         ok = false;
         break;
       }
-      ++nq;
+      q_ph ^= 1;
       tc_fence_after();
-      const int nb = r.blk1 - r.blk0;
-      const int streams = r.alt ? min(2, nb) : (r.n_tok1 > 0 ? 2 : 1);
-      const int ahead = r.alt ? 2 : 1;
+      const int nb = uniform(r.blk1 - r.blk0);
+      const int alt = uniform(r.alt), two = uniform(r.n_tok1 > 0);
+      const int streams = alt ? min(2, nb) : 1 + two;
+      const int ahead = alt ? 2 : 1;
       // the first S of each stream
       int kst = 0;
       for (int s = 0; ok && s < streams; ++s) {
-        if (s == 0 || r.alt) kst = take();
+        if (s == 0 || alt) kst = take();
         if (!ok) break;
-        tc_fence_after();
-        qk(s, r.alt ? 0 : s, kst);
+        qk(s, alt ? 0 : s, kst);
         if (lane == 0) {
           tc_commit(barS(s));
-          if (r.alt || s == streams - 1) tc_commit(barEmpty(kst));
+          if (alt || s == streams - 1) tc_commit(barEmpty(kst));
           if (s == streams - 1 && nb <= ahead) tc_commit(barQEmpty);
         }
         __syncwarp();
@@ -494,18 +508,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         int j0, valid;
         block_at(r, r.blk0 + i, j0, valid);
+        valid = uniform(valid);
         if (valid < kKeys) trim(vst, valid);
         const int steps = (valid + 15) >> 4;
         const bool more = i + ahead < nb;
-        const int s0 = r.alt ? (i & 1) : 0, s1 = r.alt ? s0 + 1 : streams;
+        const int s0 = alt ? (i & 1) : 0, s1 = alt ? s0 + 1 : streams;
         for (int s = s0; ok && s < s1; ++s) {
           pv(s, vst, steps, i < ahead);
           if (!ok) break;
           if (more) {
             if (s == s0) kst = take();
             if (!ok) break;
-            tc_fence_after();
-            qk(s, r.alt ? 0 : s, kst);
+            qk(s, alt ? 0 : s, kst);
           }
           if (lane == 0) tc_commit(barS(s));  // O so far, and the next S
           __syncwarp();
@@ -794,7 +808,8 @@ cudaError_t launch_main(const AttnParams& p, int grid, const CUtensorMap& tq, co
                         const CUtensorMap& tv, const CUtensorMap& tkp, const CUtensorMap& tvp, bool cached,
                         cudaStream_t s) {
   auto kern = attn_kernel<D, Runs>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kBytes);
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(kern, Lay<D>::kBytes, done);
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, Lay<D>::kBytes, s>>>(tq, tk, tv, tkp, tvp, p, cached);
   return cudaGetLastError();

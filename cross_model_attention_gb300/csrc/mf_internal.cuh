@@ -98,6 +98,20 @@ inline cudaError_t sm_count(int* out) {
   return cudaSuccess;
 }
 
+// Raises a kernel's dynamic shared-memory limit, once per device; `done` is a
+// static of the caller, one per kernel.
+template <typename K>
+cudaError_t allow_smem(K kern, int bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (done.load(std::memory_order_acquire) >> dev & 1ull) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(1ull << dev, std::memory_order_release);
+  return e;
+}
+
 // -------------------------------------------------------------- launchers --
 // All return cudaError_t of the launch (cudaSuccess when enqueued).
 // Head-map calibration: Gram matrix of the stacked head maps of two BSR

@@ -136,44 +136,60 @@ def _dtype_code(t) -> int:
     raise TypeError(f"unsupported dtype {t.dtype}")
 
 
+class _NoGuard:
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_NO_GUARD = _NoGuard()
+
+
 def _on(device, stream):
-    """(device guard, stream, stream guard) for a call on `device`: memory made
-    under both guards belongs to the stream the call runs on."""
+    """(guard, raw stream) for a call on `device`: inside the guard, device and
+    stream are the call's, so that memory made there belongs to the stream the
+    call runs on.  No guard where they are current already."""
     import torch
-    guard = torch.cuda.device(device)
-    with guard:
-        st = torch.cuda.current_stream() if stream is None else stream
-    if st.device != device:
-        raise MapFlowError(MF_ERR_ARG, f"the stream is on {st.device}, the tensors on {device}")
-    return torch.cuda.device(device), st, torch.cuda.stream(st)
+    if stream is None:
+        if torch.cuda.current_device() == device.index:
+            return _NO_GUARD, torch.cuda.current_stream().cuda_stream
+        with torch.cuda.device(device):
+            stream = torch.cuda.current_stream()
+    elif stream.device != device:
+        raise MapFlowError(MF_ERR_ARG, f"the stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(stream), stream.cuda_stream  # (the stream's device becomes current too)
 
 
-def _rows(name: str, t, heads: int, d: int, tokens: Optional[int], dtype, device):
-    """Checks a tensor of [..., heads, d] rows whose leading dimensions are
-    `tokens` equally spaced tokens; returns the values between two tokens."""
-    if t.device != device or t.device.type != "cuda":
-        raise MapFlowError(MF_ERR_ARG, f"{name} must be a CUDA tensor on {device}, is on {t.device}")
+def _rows(name: str, t, shape, dtype, device) -> int:
+    """Checks a tensor of `shape` [..., heads, d] whose leading dimensions are
+    equally spaced tokens; returns the values between two tokens."""
+    heads, d = shape[-2:]
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return heads * d
+    if t.device != device:
+        raise MapFlowError(MF_ERR_ARG, f"{name} must be on {device}, is on {t.device}")
     if t.dtype != dtype:
         raise MapFlowError(MF_ERR_ARG, f"{name} must be {dtype}, is {t.dtype}")
-    if t.dim() < 3 or t.shape[-2] != heads or t.shape[-1] != d:
-        raise MapFlowError(MF_ERR_ARG, f"{name} must end in [{heads}, {d}], is {tuple(t.shape)}")
-    if t.stride(-1) != 1 or (heads > 1 and t.stride(-2) != d):
+    if t.shape != shape:
+        raise MapFlowError(MF_ERR_ARG, f"{name} must be {tuple(shape)}, is {tuple(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1 or (heads > 1 and st[-2] != d):
         raise MapFlowError(MF_ERR_ARG, f"{name}: a token's heads must lie next to each other")
     n, ld = 1, None
-    for i in range(t.dim() - 3, -1, -1):
-        if t.shape[i] != 1:
+    for i in range(len(shape) - 3, -1, -1):
+        if shape[i] != 1:
             if ld is None:
-                ld = t.stride(i)
-            elif t.stride(i) != n * ld:
+                ld = st[i]
+            elif st[i] != n * ld:
                 raise MapFlowError(MF_ERR_ARG, f"{name}: its tokens are not equally spaced")
-        n *= t.shape[i]
-    if tokens is not None and n != tokens:
-        raise MapFlowError(MF_ERR_ARG, f"{name} holds {n} tokens, {tokens} expected")
+        n *= shape[i]
     return heads * d if ld is None else ld
 
 
 def _vector(name: str, t, shape, dtype, device):
-    if t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise MapFlowError(MF_ERR_ARG, f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}")
 
 
@@ -468,31 +484,40 @@ class RotaryPlan:
             norm = q_weight is not None or k_weight is not None
         dev, dt = q.device, q.dtype
         code = _dtype_code(q)
-        if q.dim() != 3:
-            raise MapFlowError(MF_ERR_ARG, f"q must be [T, H_q, d], is {tuple(q.shape)}")
-        T, H_q, d = q.shape
-        ld_q = _rows("q", q, H_q, d, T, dt, dev)
-        H_k = 0 if k is None else k.shape[-2]
-        ld_k = 0 if k is None else _rows("k", k, H_k, d, T, dt, dev)
+        if dev.type != "cuda" or self.turns.device != dev:
+            raise MapFlowError(MF_ERR_ARG, f"q is on {dev}, the plan on {self.turns.device}: both must be on one GPU")
+        if q.dim() != 3 or (k is not None and k.dim() != 3):
+            raise MapFlowError(MF_ERR_ARG, "q and k must be [T, heads, d]")
+        shape_q = T, H_q, d = q.shape
+        ld_q = _rows("q", q, shape_q, dt, dev)
+        H_k = ld_k = ld_ko = 0
+        if k is not None:
+            H_k = k.shape[1]
+            shape_k = (T, H_k, d)
+            ld_k = _rows("k", k, shape_k, dt, dev)
+        elif k_out is not None:
+            raise MapFlowError(MF_ERR_ARG, "k_out without k")
         _vector("positions", positions, (T,), torch.int32, dev)
-        if self.turns.device != dev:
-            raise MapFlowError(MF_ERR_ARG, f"the plan is on {self.turns.device}, q on {dev}")
-        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-            if w is not None:
-                _vector(name, w, (d,), dt, dev)
-        dev_guard, st, st_guard = _on(dev, stream)
-        with dev_guard, st_guard:
+        if q_weight is not None:
+            _vector("q_weight", q_weight, (d,), dt, dev)
+        if k_weight is not None:
+            _vector("k_weight", k_weight, (d,), dt, dev)
+        guard, raw = _on(dev, stream)
+        with guard:
             if q_out is None:
-                q_out = torch.empty((T, H_q, d), dtype=dt, device=dev)
-            if k is not None and k_out is None:
-                k_out = torch.empty((T, H_k, d), dtype=dt, device=dev)
-            ld_qo = _rows("q_out", q_out, H_q, d, T, dt, dev)
-            ld_ko = 0 if k is None else _rows("k_out", k_out, H_k, d, T, dt, dev)
+                q_out, ld_qo = torch.empty(shape_q, dtype=dt, device=dev), H_q * d
+            else:
+                ld_qo = _rows("q_out", q_out, shape_q, dt, dev)
+            if k is not None:
+                if k_out is None:
+                    k_out, ld_ko = torch.empty(shape_k, dtype=dt, device=dev), H_k * d
+                else:
+                    ld_ko = _rows("k_out", k_out, shape_k, dt, dev)
             _check(load_library().mf_qk_norm_rope(
-                _ptr(q), ld_q, _ptr(q_out), ld_qo, _ptr(k), ld_k, _ptr(k_out) if k is not None else None, ld_ko,
-                _ptr(q_weight), _ptr(k_weight), int(norm), float(eps), _ptr(positions), _ptr(self.turns),
-                self.rot_dim, _LAYOUTS[self.layout], self.gain, code, T, H_q, H_k, d, int(st.cuda_stream)))
-        return q_out, (k_out if k is not None else None)
+                q.data_ptr(), ld_q, q_out.data_ptr(), ld_qo, _ptr(k), ld_k, _ptr(k_out), ld_ko, _ptr(q_weight),
+                _ptr(k_weight), norm, eps, positions.data_ptr(), self.turns.data_ptr(), self.rot_dim,
+                _LAYOUTS[self.layout], self.gain, code, T, H_q, H_k, d, raw))
+        return q_out, k_out
 
 
 class _AttentionPlan:
@@ -500,29 +525,15 @@ class _AttentionPlan:
 
     handle = None
 
-    def _workspace(self, n: int, dev):
-        import torch
+    def _workspace_bytes(self, n: int) -> int:
         need = ctypes.c_int64()
         _check(load_library().mf_attn_workspace(self.handle, n, ctypes.byref(need)))
-        return torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
-
-    def _checked(self, q, k, v, o, lse, rows: int, q_shape, k_tokens: int):
-        import torch
-        dt, dev = torch.bfloat16, self.device
-        if tuple(q.shape) != tuple(q_shape):
-            raise MapFlowError(MF_ERR_ARG, f"q must be {tuple(q_shape)}, is {tuple(q.shape)}")
-        lds = [_rows("q", q, self.H_q, self.d, rows, dt, dev), _rows("k", k, self.H_kv, self.d, k_tokens, dt, dev),
-               _rows("v", v, self.H_kv, self.d, k_tokens, dt, dev)]
-        if o is None:
-            o = torch.empty(tuple(q_shape), dtype=dt, device=dev)
-        lds.append(_rows("o", o, self.H_q, self.d, rows, dt, dev))
-        if lse is not None:
-            _vector("lse", lse, tuple(q_shape)[:-1], torch.float32, dev)
-        return lds, o
+        return need.value
 
     def status(self, stream=None) -> None:
-        _, st, _ = _on(self.device, stream)
-        _check(load_library().mf_attn_status(self.handle, int(st.cuda_stream)))
+        """Waits for the stream; raises if a device-side wait of a call timed out."""
+        _, raw = _on(self.device, stream)
+        _check(load_library().mf_attn_status(self.handle, raw))
 
     def close(self) -> None:
         if self.handle is not None:
@@ -561,20 +572,31 @@ class WindowAttention(_AttentionPlan):
             None if qb is None else qb.ctypes.data_as(ctypes.c_void_p), len(cu) - 1, self.H_q, self.H_kv, self.d,
             0 if window is None else int(window), int(sinks), a, f, None))
         self.handle = h
+        self._ws_bytes = self._workspace_bytes(1)
         import torch
         self.device = torch.device("cuda", torch.cuda.current_device())
 
     def attend(self, q, k, v, scale: Optional[float] = None, o=None, lse=None, stream=None):
         """q [T, H_q, d], k and v [T, H_kv, d] -> o [T, H_q, d] (rows before a
         q_begin are left as they are); lse: fp32 [T, H_q] to fill, or None."""
-        dev_guard, st, st_guard = _on(self.device, stream)
-        with dev_guard, st_guard:
-            (lq, lk, lv, lo), o = self._checked(q, k, v, o, lse, self.T, (self.T, self.H_q, self.d), self.T)
-            ws = self._workspace(1, self.device)
+        import torch
+        dt, dev = torch.bfloat16, self.device
+        shape_q, shape_k = (self.T, self.H_q, self.d), (self.T, self.H_kv, self.d)
+        ld_q = _rows("q", q, shape_q, dt, dev)
+        ld_k = _rows("k", k, shape_k, dt, dev)
+        ld_v = _rows("v", v, shape_k, dt, dev)
+        if lse is not None:
+            _vector("lse", lse, shape_q[:2], torch.float32, dev)
+        guard, raw = _on(dev, stream)
+        with guard:
+            if o is None:
+                o = torch.empty(shape_q, dtype=dt, device=dev)
+            ld_o = _rows("o", o, shape_q, dt, dev)
+            # a workspace of its own for every call: calls may overlap
+            ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev) if self._ws_bytes else None
             _check(load_library().mf_attn_packed(
-                self.handle, _ptr(q), lq, _ptr(k), lk, _ptr(v), lv, _ptr(o), lo, _ptr(lse), MF_DTYPE_BF16,
-                self.d ** -0.5 if scale is None else float(scale), _ptr(ws), 0 if ws is None else ws.numel(),
-                int(st.cuda_stream)))
+                self.handle, q.data_ptr(), ld_q, k.data_ptr(), ld_k, v.data_ptr(), ld_v, o.data_ptr(), ld_o,
+                _ptr(lse), MF_DTYPE_BF16, self.d ** -0.5 if scale is None else scale, _ptr(ws), self._ws_bytes, raw))
         return o
 
 
@@ -599,6 +621,7 @@ class CacheAttention(_AttentionPlan):
             ctypes.byref(h), self.n, self.Lq, self.capacity, self.prefix_len, self.H_q, self.H_kv, self.d,
             0 if window is None else int(window), int(sinks), a, f, None))
         self.handle = h
+        self._ws_of: Dict[int, int] = {}  # workspace bytes by the number of requests
         import torch
         self.device = torch.device("cuda", torch.cuda.current_device())
 
@@ -609,24 +632,36 @@ class CacheAttention(_AttentionPlan):
         the new tokens' among them), k_prefix and v_prefix [prefix_len, H_kv,
         d] -> o [m, Lq, H_q, d]; lse: fp32 [m, Lq, H_q] to fill, or None."""
         import torch
-        dt = torch.bfloat16
-        dev_guard, st, st_guard = _on(self.device, stream)
-        with dev_guard, st_guard:
-            m = q.shape[0]
-            (lq, lk, lv, lo), o = self._checked(q, k_cache, v_cache, o, lse, m * self.Lq,
-                                                (m, self.Lq, self.H_q, self.d), m * self.capacity)
-            _vector("lens", lens, (m,), torch.int32, self.device)
-            lkp = lvp = 0
-            if self.prefix_len:
-                if k_prefix is None or v_prefix is None:
-                    raise MapFlowError(MF_ERR_ARG, "the plan has a prefix: k_prefix and v_prefix are needed")
-                lkp = _rows("k_prefix", k_prefix, self.H_kv, self.d, self.prefix_len, dt, self.device)
-                lvp = _rows("v_prefix", v_prefix, self.H_kv, self.d, self.prefix_len, dt, self.device)
-            ws = self._workspace(m, self.device)
+        dt, dev = torch.bfloat16, self.device
+        m = q.shape[0]
+        shape_q, shape_k = (m, self.Lq, self.H_q, self.d), (m, self.capacity, self.H_kv, self.d)
+        ld_q = _rows("q", q, shape_q, dt, dev)
+        ld_k = _rows("k_cache", k_cache, shape_k, dt, dev)
+        ld_v = _rows("v_cache", v_cache, shape_k, dt, dev)
+        _vector("lens", lens, (m,), torch.int32, dev)
+        if lse is not None:
+            _vector("lse", lse, shape_q[:3], torch.float32, dev)
+        ld_kp = ld_vp = 0
+        if self.prefix_len:
+            if k_prefix is None or v_prefix is None:
+                raise MapFlowError(MF_ERR_ARG, "the plan has a prefix: k_prefix and v_prefix are needed")
+            shape_p = (self.prefix_len, self.H_kv, self.d)
+            ld_kp = _rows("k_prefix", k_prefix, shape_p, dt, dev)
+            ld_vp = _rows("v_prefix", v_prefix, shape_p, dt, dev)
+        need = self._ws_of.get(m)
+        if need is None:
+            need = self._ws_of[m] = self._workspace_bytes(m)
+        guard, raw = _on(dev, stream)
+        with guard:
+            if o is None:
+                o = torch.empty(shape_q, dtype=dt, device=dev)
+            ld_o = _rows("o", o, shape_q, dt, dev)
+            # a workspace of its own for every call: calls may overlap
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
             _check(load_library().mf_attn_cached(
-                self.handle, m, _ptr(q), lq, _ptr(k_cache), lk, _ptr(v_cache), lv, _ptr(lens), _ptr(k_prefix), lkp,
-                _ptr(v_prefix), lvp, _ptr(o), lo, _ptr(lse), MF_DTYPE_BF16,
-                self.d ** -0.5 if scale is None else float(scale), _ptr(ws), ws.numel(), int(st.cuda_stream)))
+                self.handle, m, q.data_ptr(), ld_q, k_cache.data_ptr(), ld_k, v_cache.data_ptr(), ld_v,
+                lens.data_ptr(), _ptr(k_prefix), ld_kp, _ptr(v_prefix), ld_vp, o.data_ptr(), ld_o, _ptr(lse),
+                MF_DTYPE_BF16, self.d ** -0.5 if scale is None else scale, ws.data_ptr(), need, raw))
         return o
 
 
