@@ -14,8 +14,10 @@
 // Rows of a tile: (token, query head of one KV group), TQ = 128 / G tokens of
 // all G heads, so that the heads of a group share every key that is read.
 // A CTA (one per SM, persistent) runs two streams, each 128 rows with its own
-// softmax warpgroup and TMEM (S 128 columns, P over S's first 64, O d
-// columns).  Pair runs give the streams two neighbouring row tiles that share
+// softmax warpgroup and TMEM (S 128 columns in two halves of 64 keys, each
+// half's P over it, O d columns).  The halves decouple a stream's softmax from
+// its products: while one half is exponentiated, the other's P V and its next
+// Q K run.  Pair runs give the streams two neighbouring row tiles that share
 // each key block (K and V come through L2 at ~160 GB/s per SM, which one
 // 128-row tile would outrun); single-tile runs (few rows, many keys) give
 // them alternate key blocks of one tile and two partial results.  While one
@@ -36,7 +38,8 @@ namespace mf {
 namespace {
 
 constexpr int kRows = 128;
-constexpr int kKeys = 128;
+constexpr int kKeys = 128;   // keys per block
+constexpr int kHalf = 64;    // keys that the softmax takes at a time
 constexpr int kThreads = 320;
 
 template <int D>
@@ -47,7 +50,7 @@ struct Lay {
   static constexpr int kQ = 0;
   static constexpr int kRing = 2 * kTile;
   static constexpr int kBar = kRing + kStages * kTile;
-  static constexpr int kMisc = kBar + 8 * (6 + 2 * kStages);
+  static constexpr int kMisc = kBar + 8 * (10 + 2 * kStages);
   static constexpr int kMiscBytes = 128;
   static constexpr int kBytes = kMisc + kMiscBytes + 1024;
 };
@@ -99,15 +102,21 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// Waits of a whole warp: one lane polls (and gives up where another role has),
-// every lane then has the phase's memory order from its own (passing) try.
+// Waits of a whole, converged warp; false (in every lane) after the time limit
+// or where another role has given up.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* err, const volatile int* misc) {
-  int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = !misc[1] && mbar_wait(bar, parity, err) ? 1 : 0;
-  ok = __shfl_sync(0xffffffffu, ok, 0);
-  if (ok) mbar_try(bar, parity);
-  __syncwarp();
-  return ok != 0;
+  if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+  const unsigned long long t0 = globaltimer();
+  for (uint32_t it = 1;; ++it) {
+    if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+    if ((it & 63u) == 0) {
+      const bool late = globaltimer() - t0 > kWaitLimitNs;
+      if (__any_sync(0xffffffffu, late || misc[1] != 0)) {
+        if (late) set_error(err, kDevErrTimeout);
+        return false;
+      }
+    }
+  }
 }
 
 // -------------------------------------------------------------------- runs --
@@ -332,17 +341,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* misc = reinterpret_cast<volatile int*>(smem + L::kMisc);
 
   const uint32_t barQFull = sb + L::kBar, barQEmpty = sb + L::kBar + 8;
-  auto barS = [&](int s) { return sb + L::kBar + 16 + 8u * s; };
-  auto barP = [&](int s) { return sb + L::kBar + 32 + 8u * s; };
-  auto barFull = [&](int i) { return sb + L::kBar + 48 + 8u * i; };
-  auto barEmpty = [&](int i) { return sb + L::kBar + 48 + 8u * (NS + i); };
+  auto barS = [&](int s, int h) { return sb + L::kBar + 16 + 8u * (2 * s + h); };
+  auto barP = [&](int s, int h) { return sb + L::kBar + 48 + 8u * (2 * s + h); };
+  auto barFull = [&](int i) { return sb + L::kBar + 80 + 8u * i; };
+  auto barEmpty = [&](int i) { return sb + L::kBar + 80 + 8u * (NS + i); };
 
   if (threadIdx.x == 0) {
     mbar_init(barQFull, 1);
     mbar_init(barQEmpty, 1);
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(barS(s), 1);
-      mbar_init(barP(s), 4);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(barS(i >> 1, i & 1), 1);
+      mbar_init(barP(i >> 1, i & 1), 4);
     }
     for (int i = 0; i < NS; ++i) {
       mbar_init(barFull(i), 1);
@@ -418,13 +427,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 8) {
     // ---------------------------------------------------------------- MMA
-    constexpr uint32_t idS = idesc_bf16_f32(kRows, kKeys, false, false);
+    constexpr uint32_t idS = idesc_bf16_f32(kRows, kHalf, false, false);
     constexpr uint32_t idO = idesc_bf16_f32(kRows, D, false, true);
     const uint64_t q_desc = sdesc_sw128(sb + L::kQ, 16, 1024);             // K-major
     const uint64_t k_desc = sdesc_sw128(sb + L::kRing, 16, 1024);
     const uint64_t v_desc = sdesc_sw128(sb + L::kRing, L::kChunk, 1024);   // MN-major
     int stage = 0;
-    uint32_t ring_ph = 0, q_ph = 0, p_ph0 = 0, p_ph1 = 0;
+    uint32_t ring_ph = 0, q_ph = 0, p_ph[2] = {0, 0};  // p_ph: both halves of a stream's P
     bool ok = true;
     auto take = [&]() {  // the ring's next block has landed; its stage
       const int st = stage;
@@ -436,31 +445,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       return st;
     };
-    auto qk = [&](int s, int tile, int st) {
-      const uint64_t qd = q_desc + (uint32_t)(tile * (L::kTile >> 4)), kd = k_desc + (uint32_t)(st * (L::kTile >> 4));
+    // S of one half of a key block
+    auto qk = [&](int s, int h, int tile, int st) {
+      const uint64_t qd = q_desc + (uint32_t)(tile * (L::kTile >> 4));
+      const uint64_t kd = k_desc + (uint32_t)(st * (L::kTile >> 4) + h * (kHalf * 128 >> 4));
       constexpr uint32_t kC = L::kChunk >> 4;
-      const uint32_t dst = tmem + kColS + 128 * s;
+      const uint32_t dst = tmem + kColS + 128 * s + kHalf * h;
       if (lane == 0) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
           tc_mma(dst, qd + ((k >> 2) * kC + (k & 3) * 2), kd + ((k >> 2) * kC + (k & 3) * 2), idS, k > 0 ? 1u : 0u);
       }
     };
-    // O += P V over the block's first `steps` groups of 16 keys
-    auto pv = [&](int s, int st, int steps, uint32_t fresh) {
-      uint32_t& ph = s ? p_ph1 : p_ph0;
-      if (!warp_wait(barP(s), ph, p.err, misc)) {
+    // O += P V over the first `steps` groups of 16 keys of half h
+    auto pv = [&](int s, int h, int st, int steps, uint32_t fresh) {
+      if (!warp_wait(barP(s, h), p_ph[s], p.err, misc)) {
         ok = false;
         return;
       }
-      ph ^= 1;
       tc_fence_after();
-      const uint64_t vd = v_desc + (uint32_t)(st * (L::kTile >> 4));
-      const uint32_t dst = tmem + kColO + 128 * s, src = tmem + kColS + 128 * s;
+      const uint64_t vd = v_desc + (uint32_t)(st * (L::kTile >> 4) + h * (kHalf * 128 >> 4));
+      const uint32_t dst = tmem + kColO + 128 * s, src = tmem + kColS + 128 * s + kHalf * h;
       if (lane == 0) {
-        if (steps == 8) {
+        if (steps == 4) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) tc_mma_ts(dst, src + k * 8, vd + k * 128, idO, k > 0 ? 1u : fresh ^ 1u);
+          for (int k = 0; k < 4; ++k) tc_mma_ts(dst, src + k * 8, vd + k * 128, idO, k > 0 ? 1u : fresh ^ 1u);
         } else {
           for (int k = 0; k < steps; ++k) tc_mma_ts(dst, src + k * 8, vd + k * 128, idO, k > 0 ? 1u : fresh ^ 1u);
         }
@@ -495,36 +504,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int s = 0; ok && s < streams; ++s) {
         if (s == 0 || alt) kst = take();
         if (!ok) break;
-        qk(s, alt ? 0 : s, kst);
+        for (int h = 0; h < 2; ++h) {
+          qk(s, h, alt ? 0 : s, kst);
+          if (lane == 0) tc_commit(barS(s, h));
+        }
         if (lane == 0) {
-          tc_commit(barS(s));
           if (alt || s == streams - 1) tc_commit(barEmpty(kst));
           if (s == streams - 1 && nb <= ahead) tc_commit(barQEmpty);
         }
         __syncwarp();
       }
       for (int i = 0; ok && i < nb; ++i) {
+        // V of this block and K of the next are here before P is waited for
         const int vst = take();
+        const bool more = i + ahead < nb;
+        if (ok && more) kst = take();
         if (!ok) break;
         int j0, valid;
         block_at(r, r.blk0 + i, j0, valid);
         valid = uniform(valid);
         if (valid < kKeys) trim(vst, valid);
-        const int steps = (valid + 15) >> 4;
-        const bool more = i + ahead < nb;
         const int s0 = alt ? (i & 1) : 0, s1 = alt ? s0 + 1 : streams;
-        for (int s = s0; ok && s < s1; ++s) {
-          pv(s, vst, steps, i < ahead);
-          if (!ok) break;
-          if (more) {
-            if (s == s0) kst = take();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int steps = min(4, max(0, ((valid + 15) >> 4) - 4 * h));
+          for (int s = s0; ok && s < s1; ++s) {
+            pv(s, h, vst, steps, i < ahead && h == 0);
             if (!ok) break;
-            qk(s, alt ? 0 : s, kst);
+            if (more) qk(s, h, alt ? 0 : s, kst);
+            if (lane == 0) tc_commit(barS(s, h));  // O so far, and the next S
+            __syncwarp();
           }
-          if (lane == 0) tc_commit(barS(s));  // O so far, and the next S
-          __syncwarp();
         }
         if (!ok) break;
+        for (int s = s0; s < s1; ++s) p_ph[s] ^= 1;
         if (lane == 0) {
           tc_commit(barEmpty(vst));
           if (more) tc_commit(barEmpty(kst));
@@ -552,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tok = row / p.G, hg = row - tok * p.G;
     const float sc = p.scale * 1.4426950408889634f;
     const float slack = 8.f / sc;
-    uint32_t ph = 0;  // S phases seen
+    uint32_t ph = 0;  // phase of both halves' S
     bool ok = true;
     while (ok && runs.next(r)) {
       const int tile = r.alt ? 0 : s;
@@ -567,102 +580,110 @@ __global__ void __launch_bounds__(kThreads, 1)
       // of a product do not mix
       const bool idle = (warp & 3) * 32 >= n_tok * p.G;
       float m = -INFINITY, l = 0.f;  // reference (raw scores), sum
-      for (int b = first; b < r.blk1; b += step) {
-        if (!warp_wait(barS(s), ph & 1, p.err, misc)) {
-          ok = false;
-          break;
-        }
-        ++ph;
-        if (idle) {
-          if (lane == 0) mbar_arrive(barP(s));
-          continue;
-        }
-        tc_fence_after();
-        float x[kKeys];
-        {
-          uint32_t* w = reinterpret_cast<uint32_t*>(x);
-#pragma unroll
-          for (int c = 0; c < kKeys; c += 32) tmem_ld32(colS + c, w + c);
-        }
-        tc_wait_ld();
+      for (int b = first; ok && b < r.blk1; b += step) {
         int j0, valid;
         block_at(r, b, j0, valid);
         // blocks that every row of the tile sees whole need no mask
         const bool whole = valid == kKeys && j0 + kKeys - 1 <= pos0 &&
                            (j0 > pos_last - p.window || j0 + kKeys <= p.n_sink);
-        if (!whole) {
-          const int hi = min(valid, pos + 1 - j0), lo = pos - p.window + 1 - j0;
-          const int sink = min(hi, p.n_sink - j0);
-#pragma unroll
-          for (int c = 0; c < kKeys; c += 32) {
-            const uint32_t seen = span_bits(lo, hi, c) | span_bits(0, sink, c);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) x[c + e] = (seen >> e) & 1u ? x[c + e] : -INFINITY;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          if (!warp_wait(barS(s, h), ph, p.err, misc)) {
+            ok = false;
+            break;
           }
-        }
-        float mx[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          mx[q] = fmaxf(x[q * 32], x[q * 32 + 1]);
-#pragma unroll
-          for (int e = 2; e < 32; e += 2) mx[q] = fmax3(mx[q], x[q * 32 + e], x[q * 32 + e + 1]);
-        }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        // a row's first visible key sets its reference; later only a maximum
-        // 2^8 above it moves it
-        const bool move = m == -INFINITY ? top > -INFINITY : top > m + slack;
-        if (__any_sync(0xffffffffu, move)) {
-          float f = 1.f;
-          if (move) {
-            f = m == -INFINITY ? 0.f : ex2((m - top) * sc);
-            m = top;
-            l *= f;
+          if (idle) {
+            if (lane == 0) mbar_arrive(barP(s, h));
+            continue;
           }
-          if (b > first) {
-            // the barrier of this S also covers the products so far
+          tc_fence_after();
+          const uint32_t col = colS + kHalf * h;
+          float x[kHalf];
+          {
+            uint32_t* w = reinterpret_cast<uint32_t*>(x);
+            tmem_ld32(col, w);
+            tmem_ld32(col + 32, w + 32);
+          }
+          tc_wait_ld();
+          if (!whole) {
+            const int c0 = j0 + kHalf * h;  // position of the half's first key
+            const int hi = min(valid - kHalf * h, pos + 1 - c0), lo = pos - p.window + 1 - c0;
+            const int sink = min(hi, p.n_sink - c0);
 #pragma unroll
-            for (int c = 0; c < D; c += 16) {
-              uint32_t w[16];
-              tmem_ld16(colO + c, w);
-              tc_wait_ld();
+            for (int c = 0; c < kHalf; c += 32) {
+              const uint32_t seen = span_bits(lo, hi, c) | span_bits(0, sink, c);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
-              tmem_st16(colO + c, w);
+              for (int e = 0; e < 32; ++e) x[c + e] = (seen >> e) & 1u ? x[c + e] : -INFINITY;
             }
           }
-        }
-        const float ref = m == -INFINITY ? 0.f : m * sc;
-        const float2 sc2 = make_float2(sc, sc), nr = make_float2(-ref, -ref);
-        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          float mx[4];
 #pragma unroll
-        for (int c = 0; c < kKeys; c += 64) {
+          for (int q = 0; q < 4; ++q) {
+            mx[q] = fmaxf(x[q * 16], x[q * 16 + 1]);
+#pragma unroll
+            for (int e = 2; e < 16; e += 2) mx[q] = fmax3(mx[q], x[q * 16 + e], x[q * 16 + e + 1]);
+          }
+          const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
+          // a row's first visible key sets its reference; later only a maximum
+          // 2^8 above it moves it
+          const bool move = m == -INFINITY ? top > -INFINITY : top > m + slack;
+          if (__any_sync(0xffffffffu, move)) {
+            float f = 1.f;
+            if (move) {
+              f = m == -INFINITY ? 0.f : ex2((m - top) * sc);
+              m = top;
+              l *= f;
+            }
+            if (b > first || h > 0) {
+              // O must hold every product so far: those of the other half's last
+              // P are covered by that half's next S (or the run's end)
+              if (!warp_wait(barS(s, h ^ 1), h == 0 ? ph : ph ^ 1, p.err, misc)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+#pragma unroll
+              for (int c = 0; c < D; c += 16) {
+                uint32_t w[16];
+                tmem_ld16(colO + c, w);
+                tc_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
+                tmem_st16(colO + c, w);
+              }
+            }
+          }
+          const float ref = m == -INFINITY ? 0.f : m * sc;
+          const float2 sc2 = make_float2(sc, sc), nr = make_float2(-ref, -ref);
+          float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           uint32_t w[32];
 #pragma unroll
-          for (int e = 0; e < 64; e += 2) {
-            float2 t = ffma2(make_float2(x[c + e], x[c + e + 1]), sc2, nr);
+          for (int e = 0; e < kHalf; e += 2) {
+            float2 t = ffma2(make_float2(x[e], x[e + 1]), sc2, nr);
             t.x = ex2(t.x);
             t.y = ex2(t.y);
             acc[(e >> 1) & 1] = fadd2(acc[(e >> 1) & 1], t);
             w[e >> 1] = pack_bf16x2(t.x, t.y);
           }
-          tmem_st32(colS + c / 2, w);
+          tmem_st32(col, w);
+          const float2 a = fadd2(acc[0], acc[1]);
+          l += a.x + a.y;
+          tc_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(barP(s, h));
         }
-        const float2 a = fadd2(acc[0], acc[1]);
-        l += a.x + a.y;
-        tc_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(barP(s));
+        ph ^= 1;
       }
       if (!ok) break;
       // ----------------------------------------------------------- epilogue
       const bool any = first < r.blk1;
       if (any) {
-        if (!warp_wait(barS(s), ph & 1, p.err, misc)) {
+        if (!warp_wait(barS(s, 0), ph, p.err, misc) || !warp_wait(barS(s, 1), ph, p.err, misc)) {
           ok = false;
           break;
         }
-        ++ph;
+        ph ^= 1;
         tc_fence_after();
       }
       const bool mine = tok < n_tok;
