@@ -22,8 +22,10 @@
 // 128-row tile would outrun); single-tile runs (few rows, many keys) give
 // them alternate key blocks of one tile and two partial results.  While one
 // stream's warps exponentiate, the other's products run.
-// Warps 0-3 and 4-7: softmax of stream 0 and 1 (thread = row).  Warp 8: MMA.
-// Warp 9: TMA loads, K and V blocks of 128 keys through one ring.
+// Warps 0-3 and 4-7: softmax of stream 0 and 1 (thread = row).  Warps 8 and
+// 10: the streams' products (one issuing warp for both spent 2.7 us on a
+// block pair whose products take 1.3).  Warp 9: TMA loads, K and V blocks of
+// 128 keys through one ring.
 //
 // Masked keys: a row's hidden scores are replaced by -inf before anything is
 // done with them, and V rows that no row may see (past a range's end, where
@@ -40,7 +42,7 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kKeys = 128;   // keys per block
 constexpr int kHalf = 64;    // keys that the softmax takes at a time
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 
 template <int D>
 struct Lay {
@@ -348,14 +350,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(barQFull, 1);
-    mbar_init(barQEmpty, 1);
+    mbar_init(barQEmpty, 2);  // both streams' MMA warps
     for (int i = 0; i < 4; ++i) {
       mbar_init(barS(i >> 1, i & 1), 1);
       mbar_init(barP(i >> 1, i & 1), 4);
     }
     for (int i = 0; i < NS; ++i) {
       mbar_init(barFull(i), 1);
-      mbar_init(barEmpty(i), 1);
+      mbar_init(barEmpty(i), 2);
     }
     fence_mbar_init();
     misc[1] = 0;
@@ -425,15 +427,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = max(0, g - NS); u < g; ++u) mbar_wait(barFull(u % NS), (u / NS) & 1, nullptr);
       if (nq > 0) mbar_wait(barQFull, (nq - 1) & 1, nullptr);
     }
-  } else if (warp == 8) {
-    // ---------------------------------------------------------------- MMA
+  } else if (warp == 8 || warp == 10) {
+    // ------------------------------------------- MMA, one warp per stream
+    const int s = warp == 8 ? 0 : 1;
     constexpr uint32_t idS = idesc_bf16_f32(kRows, kHalf, false, false);
     constexpr uint32_t idO = idesc_bf16_f32(kRows, D, false, true);
     const uint64_t q_desc = sdesc_sw128(sb + L::kQ, 16, 1024);             // K-major
     const uint64_t k_desc = sdesc_sw128(sb + L::kRing, 16, 1024);
     const uint64_t v_desc = sdesc_sw128(sb + L::kRing, L::kChunk, 1024);   // MN-major
     int stage = 0;
-    uint32_t ring_ph = 0, q_ph = 0, p_ph[2] = {0, 0};  // p_ph: both halves of a stream's P
+    uint32_t ring_ph = 0, q_ph = 0, p_ph = 0;  // p_ph: both halves of P
     bool ok = true;
     auto take = [&]() {  // the ring's next block has landed; its stage
       const int st = stage;
@@ -446,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return st;
     };
     // S of one half of a key block
-    auto qk = [&](int s, int h, int tile, int st) {
+    auto qk = [&](int h, int tile, int st) {
       const uint64_t qd = q_desc + (uint32_t)(tile * (L::kTile >> 4));
       const uint64_t kd = k_desc + (uint32_t)(st * (L::kTile >> 4) + h * (kHalf * 128 >> 4));
       constexpr uint32_t kC = L::kChunk >> 4;
@@ -458,8 +461,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     // O += P V over the first `steps` groups of 16 keys of half h
-    auto pv = [&](int s, int h, int st, int steps, uint32_t fresh) {
-      if (!warp_wait(barP(s, h), p_ph[s], p.err, misc)) {
+    auto pv = [&](int h, int st, int steps, uint32_t fresh) {
+      if (!warp_wait(barP(s, h), p_ph, p.err, misc)) {
         ok = false;
         return;
       }
@@ -497,59 +500,67 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const int nb = uniform(r.blk1 - r.blk0);
       const int alt = uniform(r.alt), two = uniform(r.n_tok1 > 0);
-      const int streams = alt ? min(2, nb) : 1 + two;
-      const int ahead = alt ? 2 : 1;
-      // the first S of each stream
-      int kst = 0;
-      for (int s = 0; ok && s < streams; ++s) {
-        if (s == 0 || alt) kst = take();
-        if (!ok) break;
-        for (int h = 0; h < 2; ++h) {
-          qk(s, h, alt ? 0 : s, kst);
-          if (lane == 0) tc_commit(barS(s, h));
-        }
+      const int ahead = alt ? 2 : 1, tile = alt ? 0 : s;
+      const bool on = alt || s == 0 || two;  // whether this stream works in this run
+      auto mine = [&](int i) { return on && (!alt || (i & 1) == s); };
+      // the last block whose S this stream makes
+      const int last = !on ? -1 : alt ? nb - 1 - ((nb - 1 - s) & 1) : nb - 1;
+      // a stage this stream has issued its products of, or that it does not use
+      auto leave = [&](uint32_t bar, bool used) {
         if (lane == 0) {
-          if (alt || s == streams - 1) tc_commit(barEmpty(kst));
-          if (s == streams - 1 && nb <= ahead) tc_commit(barQEmpty);
+          if (used) tc_commit(bar);
+          else mbar_arrive(bar);
         }
+      };
+      if (last < 0) leave(barQEmpty, false);
+      // the stream's first S
+      for (int i = 0; ok && i < min(ahead, nb); ++i) {
+        const int kst = take();
+        if (!ok) break;
+        if (mine(i)) {
+          for (int h = 0; h < 2; ++h) {
+            qk(h, tile, kst);
+            if (lane == 0) tc_commit(barS(s, h));
+          }
+        }
+        leave(barEmpty(kst), mine(i));
+        if (i == last) leave(barQEmpty, true);
         __syncwarp();
       }
       for (int i = 0; ok && i < nb; ++i) {
         // V of this block and K of the next are here before P is waited for
         const int vst = take();
         const bool more = i + ahead < nb;
+        int kst = 0;
         if (ok && more) kst = take();
         if (!ok) break;
-        int j0, valid;
-        block_at(r, r.blk0 + i, j0, valid);
-        valid = uniform(valid);
-        if (valid < kKeys) trim(vst, valid);
-        const int s0 = alt ? (i & 1) : 0, s1 = alt ? s0 + 1 : streams;
+        if (mine(i)) {
+          int j0, valid;
+          block_at(r, r.blk0 + i, j0, valid);
+          valid = uniform(valid);
+          if (valid < kKeys) trim(vst, valid);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int steps = min(4, max(0, ((valid + 15) >> 4) - 4 * h));
-          for (int s = s0; ok && s < s1; ++s) {
-            pv(s, h, vst, steps, i < ahead && h == 0);
+          for (int h = 0; h < 2; ++h) {
+            const int steps = min(4, max(0, ((valid + 15) >> 4) - 4 * h));
+            pv(h, vst, steps, i < ahead && h == 0);
             if (!ok) break;
-            if (more) qk(s, h, alt ? 0 : s, kst);
+            if (more) qk(h, tile, kst);
             if (lane == 0) tc_commit(barS(s, h));  // O so far, and the next S
             __syncwarp();
           }
+          if (!ok) break;
+          p_ph ^= 1;
         }
-        if (!ok) break;
-        for (int s = s0; s < s1; ++s) p_ph[s] ^= 1;
-        if (lane == 0) {
-          tc_commit(barEmpty(vst));
-          if (more) tc_commit(barEmpty(kst));
-          if (more && i + ahead == nb - 1) tc_commit(barQEmpty);  // the run's last S product
-        }
+        leave(barEmpty(vst), mine(i));
+        if (more) leave(barEmpty(kst), mine(i));
+        if (more && i + ahead == last) leave(barQEmpty, true);
         __syncwarp();
       }
     }
     if (!ok) misc[1] = 1;
     // everything issued is done before TMEM is freed and the CTA ends
     if (lane == 0) {
-      const uint32_t done = sb + L::kMisc + 64;
+      const uint32_t done = sb + L::kMisc + 64 + 8 * s;
       mbar_init(done, 1);
       fence_mbar_init();
       tc_commit(done);
