@@ -42,7 +42,7 @@ struct mf_attn_s {
 namespace {
 
 constexpr int kBlock = 128;     // keys per block of the kernel
-constexpr int kMinBlocks = 2;   // cache form: least blocks per CTA
+constexpr int kMinSpan = 4;     // cache form: least work per CTA (a block of each stream)
 constexpr int kMaxTokens = kAttnFar;
 
 void* h_alloc(mf_attn_t h, size_t bytes) {
@@ -152,16 +152,18 @@ CacheLayout cache_layout(const mf_attn_s* h, int n) {
   if (h->window < kAttnNoWindow)
     nbs = std::min(nbs, (std::min((long long)h->n_sink, (long long)h->cap) + kBlock - 1) / kBlock +
                             ((long long)h->window + h->Lq - 1 + kBlock - 1) / kBlock) + 1;
-  // a line of nb blocks is cut every per_cta blocks: at most nb / per_cta + 2
-  // pieces; per_cta is at least the even share of what is certainly there
-  // (the prefix; for a request, its own blocks in every KV head too)
-  const double share_pre = std::max((double)kMinBlocks, (double)pairs * nbp * h->H_kv / h->grid);
-  const double share_suf = std::max((double)kMinBlocks, (double)(pairs * nbp + nbs) * h->H_kv / h->grid);
+  // a line whose blocks take w units is cut every per_cta units: at most
+  // w / per_cta + 2 pieces; per_cta is at least the even share of what is
+  // certainly there (the prefix; for a request, its own blocks in every KV
+  // head too)
+  const double pre = (double)pairs * nbp * kAttnCostPair * h->H_kv / h->grid;
+  const double share_pre = std::max((double)kMinSpan, pre);
+  const double share_suf = std::max((double)kMinSpan, pre + (double)nbs * kAttnCostOne * h->H_kv / h->grid);
   if (pairs > 0) {
-    c.np_pre = (int)(nbp / share_pre) + 3;
+    c.np_pre = (int)(nbp * kAttnCostPair / share_pre) + 3;
     if (c.pre_tiles & 1) c.np_pre *= 2;  // a lone tile's streams have results of their own
   }
-  c.np_suf = 2 * ((int)(nbs / share_suf) + 3);
+  c.np_suf = 2 * ((int)(nbs * kAttnCostOne / share_suf) + 3);
   const size_t rows = (size_t)toks * h->H_q;
   const size_t np = (size_t)c.np_pre + c.np_suf;
   c.n_part = 0;
@@ -446,6 +448,12 @@ int mf_attn_create_cache(mf_attn_t* out, int n_max, int Lq, int capacity, int pr
   if (capacity > kMaxTokens || prefix_len > kMaxTokens) return fail(MF_ERR_UNSUPPORTED, "more than 2^29 keys");
   if ((long long)n_max * capacity > 0x7fffffffll || (long long)n_max * Lq > 0x7fffffffll / 1024)
     return fail(MF_ERR_UNSUPPORTED, "n_max = %d is too large", n_max);
+  {  // the kernel lays all work end to end in 32 bits
+    const long long tiles = ((long long)n_max * Lq + kBlock / (H_q / H_kv) - 1) / (kBlock / (H_q / H_kv));
+    const long long lines = (tiles + 1) / 2 * (kAttnCostRun + kAttnCostPair * ((prefix_len + kBlock - 1ll) / kBlock)) +
+                            n_max * (kAttnCostRun + kAttnCostOne * ((capacity + kBlock - 1ll) / kBlock + 1));
+    if (lines * H_kv > (1ll << 30)) return fail(MF_ERR_UNSUPPORTED, "n_max = %d, capacity = %d and prefix_len = %d are too much work for one call", n_max, capacity, prefix_len);
+  }
   mf_attn_t h = new (std::nothrow) mf_attn_s();
   if (!h) return fail(MF_ERR_OOM, "host memory");
   h->cached = true;
@@ -604,7 +612,7 @@ int mf_attn_cached(mf_attn_t h, int n, const void* q, int64_t ld_q, const void* 
   p.n_pre_tiles = c.pre_tiles;
   p.np_pre = c.np_pre;
   p.np_suf = c.np_suf;
-  p.min_blocks = kMinBlocks;
+  p.min_span = kMinSpan;
   char* ws = static_cast<char*>(workspace);
   p.n_part = reinterpret_cast<int*>(ws + c.n_part);
   p.part_ml = reinterpret_cast<float2*>(ws + c.ml);

@@ -52,14 +52,14 @@ struct Lay {
   static constexpr int kQ = 0;
   static constexpr int kRing = 2 * kTile;
   static constexpr int kBar = kRing + kStages * kTile;
-  static constexpr int kMisc = kBar + 8 * (10 + 2 * kStages);
+  static constexpr int kMisc = kBar + 8 * (12 + 2 * kStages);
   static constexpr int kMiscBytes = 128;
   static constexpr int kBytes = kMisc + kMiscBytes + 1024;
 };
 static_assert(Lay<128>::kBytes <= 232448 && Lay<64>::kBytes <= 232448, "shared memory");
 
-// misc words: [0] TMEM address, [1] abort, [2..3] cache form: first request
-// and [4..5] its first block, [6..] reduction scratch
+// misc words: [0] TMEM address, [1] abort, cache form: [2] first request, [4]
+// the lines before it, [5] all lines; from byte 64 on two barriers
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 * stream each
 
@@ -191,130 +191,150 @@ __device__ __forceinline__ Unit cache_unit(const AttnParams& p, int len) {
   u.nb = (u.a1 + kKeys - 1) / kKeys + (u.b1 - u.b0 + kKeys - 1) / kKeys;
   return u;
 }
+// A line's length: what a run costs to start and end, then its blocks, in
+// units of ~0.4 us (a tile pair's block takes ~1.3 us, a single tile's ~0.8,
+// a run's start and end ~1.3).  A block belongs to the CTA in whose span it
+// begins.
+constexpr int kCostRun = kAttnCostRun, kCostPair = kAttnCostPair, kCostOne = kAttnCostOne;
 struct CacheSpan {
-  long long total, pre;  // blocks in all lines, and in the prefix's
-  long long per_cta;
-  int nbp, pairs;        // prefix: blocks per line, tile pairs
+  int total, pre;  // all lines, and the prefix's
+  int per_cta;
+  int nbp, pairs;  // prefix: blocks per line, tile pairs
 };
-__device__ __forceinline__ CacheSpan cache_span(const AttnParams& p, long long suffix_blocks) {
+__device__ __forceinline__ int line_of(int nb, int cost) { return nb > 0 ? kCostRun + nb * cost : 0; }
+__device__ __forceinline__ CacheSpan cache_span(const AttnParams& p, int suffix) {
   CacheSpan c;
   c.nbp = (p.P + kKeys - 1) / kKeys;
   c.pairs = p.P > 0 ? (p.n_pre_tiles + 1) / 2 : 0;
-  c.pre = static_cast<long long>(c.pairs) * c.nbp * p.H_kv;
-  c.total = c.pre + suffix_blocks * p.H_kv;
-  c.per_cta = max(static_cast<long long>(p.min_blocks), (c.total + gridDim.x - 1) / gridDim.x);
+  c.pre = c.pairs * line_of(c.nbp, kCostPair) * p.H_kv;
+  c.total = c.pre + suffix * p.H_kv;
+  c.per_cta = max(p.min_span, (c.total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
   return c;
 }
 
 struct CacheRuns {
   const AttnParams& p;
   CacheSpan c;
-  long long f, end;     // this CTA's span
-  int r;                // request of the walk
-  long long cum;        // blocks (per head) of the requests before it
-  Unit u;
-  // misc: [2] first request, [4..5] blocks before it, [6..7] all blocks
+  int f0, f1;      // this CTA's span
+  int at;          // start of the unit's line
+  int who, head;   // tile pair or request, KV head
+  bool prefix;
+  Unit u;          // of the request
+  // misc: [2] first request, [4] the lines (per head) before it, [5] all requests' lines
   __device__ CacheRuns(const AttnParams& p_, const volatile int* misc) : p(p_) {
-    const volatile long long* m = reinterpret_cast<const volatile long long*>(misc);
-    c = cache_span(p, m[3]);
-    f = min(c.total, c.per_cta * blockIdx.x);
-    end = min(c.total, f + c.per_cta);
-    r = misc[2];
-    cum = m[2];
-    if (r < p.n) u = cache_unit(p, p.lens[r]);
+    c = cache_span(p, misc[5]);
+    f0 = min(c.total, c.per_cta * static_cast<int>(blockIdx.x));
+    f1 = min(c.total, f0 + c.per_cta);
+    prefix = f0 < c.pre;
+    if (prefix) {
+      const int line = line_of(c.nbp, kCostPair), unit = f0 / line;
+      who = unit / p.H_kv;
+      head = unit - who * p.H_kv;
+      at = unit * line;
+    } else {
+      who = misc[2];
+      head = 0;
+      at = c.pre + misc[4] * p.H_kv;
+      u = cache_unit(p, who < p.n ? p.lens[who] : 0);
+      const int line = line_of(u.nb, kCostOne);
+      if (line > 0) {
+        head = (f0 - at) / line;
+        at += head * line;
+      }
+    }
   }
   __device__ bool next(Run& o) {
-    if (f >= end) return false;
-    long long unit, first;  // unit index and its line's first block
-    int nb;
-    if (f < c.pre) {
-      unit = f / c.nbp;
-      nb = c.nbp;
-      first = unit * nb;
-      const int pair = static_cast<int>(unit / p.H_kv);
-      o.head = static_cast<int>(unit % p.H_kv);
-      const int tok0 = pair * 2 * p.TQ, n_tok = p.n * p.Lq - tok0;
-      o.q_row = tok0;
-      o.n_tok0 = min(n_tok, p.TQ);
-      o.n_tok1 = min(n_tok - o.n_tok0, p.TQ);
-      o.pos = kAttnFar;
-      o.k_row0 = 0;
-      o.a1 = 0;
-      o.b0 = 0;
-      o.b1 = p.P;
-      o.prefix = 1;
-    } else {
-      const long long g = f - c.pre;
-      while (g >= (cum + u.nb) * p.H_kv && r + 1 < p.n) {  // ends at a request with blocks
-        cum += u.nb;
-        u = cache_unit(p, p.lens[++r]);
+    for (;;) {
+      if (at >= f1) return false;
+      // the unit at `at`
+      const int nb = prefix ? c.nbp : u.nb, cost = prefix ? kCostPair : kCostOne;
+      const int begin = at + kCostRun;  // where its first block begins
+      o.blk0 = max(0, (f0 - begin + cost - 1) / cost);
+      o.blk1 = min(nb, (f1 - begin + cost - 1) / cost);
+      const bool some = nb > 0 && f1 > begin && o.blk0 < o.blk1;
+      if (some) {
+        o.head = head;
+        o.prefix = prefix;
+        if (prefix) {
+          const int tok0 = who * 2 * p.TQ, n_tok = p.n * p.Lq - tok0;
+          o.q_row = tok0;
+          o.n_tok0 = min(n_tok, p.TQ);
+          o.n_tok1 = min(n_tok - o.n_tok0, p.TQ);
+          o.pos = kAttnFar;
+          o.k_row0 = 0;
+          o.a1 = 0;
+          o.b0 = 0;
+          o.b1 = p.P;
+        } else {
+          o.q_row = who * p.Lq;
+          o.n_tok0 = p.Lq;
+          o.n_tok1 = 0;
+          o.pos = u.b1 - p.Lq;
+          o.k_row0 = who * p.cap;
+          o.a1 = u.a1;
+          o.b0 = u.b0;
+          o.b1 = u.b1;
+        }
+        o.alt = o.n_tok1 == 0;
+        // (held to the buffers, whatever happens to lens meanwhile)
+        const int most = prefix ? p.np_pre : p.np_suf;
+        const int piece = min(max(static_cast<int>(blockIdx.x) - begin / c.per_cta, 0), most / (o.alt ? 2 : 1) - 1);
+        o.part = (prefix ? 0 : p.np_pre) + piece * (o.alt ? 2 : 1);
+        if (o.blk1 == nb && threadIdx.x == 0)
+          p.n_part[static_cast<long long>(prefix ? who : c.pairs + who) * p.H_kv + head] = piece + 1;
       }
-      nb = u.nb;
-      if (nb == 0) return false;
-      const long long in = g - cum * p.H_kv;
-      o.head = static_cast<int>(in / nb);
-      unit = static_cast<long long>(c.pairs) * p.H_kv + static_cast<long long>(r) * p.H_kv + o.head;
-      first = c.pre + cum * p.H_kv + static_cast<long long>(o.head) * nb;
-      o.q_row = r * p.Lq;
-      o.n_tok0 = p.Lq;
-      o.n_tok1 = 0;
-      o.pos = min(max(p.lens[r], 0), p.cap) - p.Lq;
-      o.k_row0 = r * p.cap;
-      o.a1 = u.a1;
-      o.b0 = u.b0;
-      o.b1 = u.b1;
-      o.prefix = 0;
+      // the next unit
+      at += line_of(nb, cost);
+      if (nb == 0) head = p.H_kv - 1;  // an empty cache: no head has work
+      if (++head == p.H_kv) {
+        head = 0;
+        ++who;
+        if (prefix && who == c.pairs) {
+          prefix = false;
+          who = 0;
+          u = cache_unit(p, p.lens[0]);
+        } else if (!prefix && who < p.n) {
+          u = cache_unit(p, p.lens[who]);
+        }
+        if (!prefix && who >= p.n) at = f1;  // (past the last request)
+      }
+      if (some) return true;
     }
-    const long long last = min(end, first + nb);
-    o.blk0 = static_cast<int>(f - first);
-    o.blk1 = static_cast<int>(last - first);
-    o.alt = o.n_tok1 == 0;
-    const int piece = static_cast<int>(blockIdx.x - first / c.per_cta);
-    o.part = (o.prefix ? 0 : p.np_pre) + piece * (o.alt ? 2 : 1);
-    if (o.blk1 == nb && threadIdx.x == 0) p.n_part[unit] = piece + 1;
-    f = last;
-    return true;
   }
 };
 
-// Cache form, all threads: the blocks of all requests, and the request in
-// which this CTA's span begins with the blocks before it.
+// Cache form, first warp: the length of all requests' lines, and the request
+// in which this CTA's span begins with the length before it.
 __device__ __forceinline__ void cache_find(const AttnParams& p, volatile int* misc) {
-  volatile long long* m = reinterpret_cast<volatile long long*>(misc);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0) {
-    long long sum = 0;
-    for (int r = lane; r < p.n; r += 32) sum += cache_unit(p, p.lens[r]).nb;
+  const int lane = threadIdx.x & 31;
+  int sum = 0;
+  for (int r = lane; r < p.n; r += 32) sum += line_of(cache_unit(p, p.lens[r]).nb, kCostOne);
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  const CacheSpan c = cache_span(p, sum);
+  const int g = min(c.total, c.per_cta * static_cast<int>(blockIdx.x)) - c.pre;
+  int first = 0, before = 0, run = 0;
+  bool found = g <= 0;
+  for (int r0 = 0; !found && r0 < p.n; r0 += 32) {
+    const int line = r0 + lane < p.n ? line_of(cache_unit(p, p.lens[r0 + lane]).nb, kCostOne) : 0;
+    int inc = line;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const CacheSpan c = cache_span(p, sum);
-    const long long f = min(c.total, c.per_cta * blockIdx.x);
-    const long long g = f - c.pre;  // a place among the requests' lines, or before them
-    int first = 0;
-    long long before = 0, run = 0;
-    bool found = g < 0;
-    for (int r0 = 0; !found && r0 < p.n; r0 += 32) {
-      const int nb = r0 + lane < p.n ? cache_unit(p, p.lens[r0 + lane]).nb : 0;
-      long long inc = nb;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, r0 + lane < p.n && g < (run + inc) * p.H_kv);
-      if (hit) {
-        const int l = __ffs(hit) - 1;
-        first = r0 + l;
-        before = run + __shfl_sync(0xffffffffu, inc - nb, l);
-        found = true;
-      }
-      run += __shfl_sync(0xffffffffu, inc, 31);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
     }
-    if (lane == 0) {
-      misc[2] = first;
-      m[2] = before;
-      m[3] = sum;
+    const unsigned hit = __ballot_sync(0xffffffffu, r0 + lane < p.n && g < (run + inc) * p.H_kv);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      first = r0 + l;
+      before = run + __shfl_sync(0xffffffffu, inc - line, l);
+      found = true;
     }
+    run += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  if (lane == 0) {
+    misc[2] = first;
+    misc[4] = before;
+    misc[5] = sum;
   }
 }
 
@@ -342,15 +362,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   volatile int* misc = reinterpret_cast<volatile int*>(smem + L::kMisc);
 
-  const uint32_t barQFull = sb + L::kBar, barQEmpty = sb + L::kBar + 8;
-  auto barS = [&](int s, int h) { return sb + L::kBar + 16 + 8u * (2 * s + h); };
-  auto barP = [&](int s, int h) { return sb + L::kBar + 48 + 8u * (2 * s + h); };
-  auto barFull = [&](int i) { return sb + L::kBar + 80 + 8u * i; };
-  auto barEmpty = [&](int i) { return sb + L::kBar + 80 + 8u * (NS + i); };
+  auto barQFull = [&](int t) { return sb + L::kBar + 8u * t; };
+  auto barQEmpty = [&](int t) { return sb + L::kBar + 16 + 8u * t; };
+  auto barS = [&](int s, int h) { return sb + L::kBar + 32 + 8u * (2 * s + h); };
+  auto barP = [&](int s, int h) { return sb + L::kBar + 64 + 8u * (2 * s + h); };
+  auto barFull = [&](int i) { return sb + L::kBar + 96 + 8u * i; };
+  auto barEmpty = [&](int i) { return sb + L::kBar + 96 + 8u * (NS + i); };
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up
   if (threadIdx.x == 0) {
-    mbar_init(barQFull, 1);
-    mbar_init(barQEmpty, 2);  // both streams' MMA warps
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(barQFull(t), 1);
+      mbar_init(barQEmpty(t), 2);  // both streams' MMA warps
+    }
     for (int i = 0; i < 4; ++i) {
       mbar_init(barS(i >> 1, i & 1), 1);
       mbar_init(barP(i >> 1, i & 1), 4);
@@ -371,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           make_uint4(0u, 0u, 0u, 0u);
     fence_async_smem();
   }
-  if (cached) cache_find(p, misc);
+  if (cached && warp == 0) cache_find(p, misc);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -382,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) {
     // ------------------------------------------------------------- loader
     if (lane == 0) {
-      int g = 0, nq = 0;  // ring uses, Q uses
+      int g = 0, nq0 = 0, nq1 = 0, slot = 0;  // ring uses, uses of the Q slots, next slot
       bool ok = true;
       auto load = [&](const CUtensorMap* map, int row) {
         const int st = g % NS;
@@ -405,18 +429,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           block_at(r, r.blk0 + i, j0, valid);
           return r.k_row0 + j0;
         };
-        for (int i = 0; ok && i < min(ahead, nb); ++i) load(mk, row(i));
-        // Q replaces the previous run's once that run's S products are done
-        if (ok && !mbar_wait(barQEmpty, (nq & 1) ^ 1, p.err)) ok = false;
-        if (!ok) break;
-        const int tiles = r.n_tok1 > 0 ? 2 : 1;
-        mbar_arrive_tx(barQFull, tiles * (D / 64) * 128 * p.G * p.TQ);
-        for (int t = 0; t < tiles; ++t)
+        // Q tile t into a slot, once the products of the slot's last run are done
+        auto load_q = [&](int to, int t) {
+          int& nq = to ? nq1 : nq0;
+          if (!ok || misc[1] || !mbar_wait(barQEmpty(to), (nq & 1) ^ 1, p.err)) {
+            ok = false;
+            return;
+          }
+          ++nq;
+          mbar_arrive_tx(barQFull(to), (D / 64) * 128 * p.G * p.TQ);
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(sb + L::kQ + t * L::kTile + c * L::kChunk, &tq, c * 64, 0, r.head,
-                        r.q_row + t * p.TQ, barQFull);
-        ++nq;
+            tma_load_4d(sb + L::kQ + to * L::kTile + c * L::kChunk, &tq, c * 64, 0, r.head, r.q_row + t * p.TQ,
+                        barQFull(to));
+        };
+        // one-tile runs alternate between the slots: the next run's Q comes
+        // while this one's is in use
+        if (r.alt) {
+          load_q(slot, 0);
+          slot ^= 1;
+        }
+        for (int i = 0; ok && i < min(ahead, nb); ++i) load(mk, row(i));
+        if (!r.alt) {
+          load_q(0, 0);
+          if (r.n_tok1 > 0) load_q(1, 1);
+        }
         for (int i = 0; ok && i < nb; ++i) {
           load(mv, row(i));
           if (ok && i + ahead < nb) load(mk, row(i + ahead));
@@ -425,7 +462,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) misc[1] = 1;
       // drain what is in flight before the CTA may end
       for (int u = max(0, g - NS); u < g; ++u) mbar_wait(barFull(u % NS), (u / NS) & 1, nullptr);
-      if (nq > 0) mbar_wait(barQFull, (nq - 1) & 1, nullptr);
+      if (nq0 > 0) mbar_wait(barQFull(0), (nq0 - 1) & 1, nullptr);
+      if (nq1 > 0) mbar_wait(barQFull(1), (nq1 - 1) & 1, nullptr);
     }
   } else if (warp == 8 || warp == 10) {
     // ------------------------------------------- MMA, one warp per stream
@@ -436,7 +474,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t k_desc = sdesc_sw128(sb + L::kRing, 16, 1024);
     const uint64_t v_desc = sdesc_sw128(sb + L::kRing, L::kChunk, 1024);   // MN-major
     int stage = 0;
-    uint32_t ring_ph = 0, q_ph = 0, p_ph = 0;  // p_ph: both halves of P
+    uint32_t ring_ph = 0, q_ph = 0, p_ph = 0;  // q_ph: bit per Q slot; p_ph: both halves of P
+    int slot = 0;
     bool ok = true;
     auto take = [&]() {  // the ring's next block has landed; its stage
       const int st = stage;
@@ -492,16 +531,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     };
     while (ok && uniform(runs.next(r))) {
-      if (!warp_wait(barQFull, q_ph, p.err, misc)) {
-        ok = false;
-        break;
-      }
-      q_ph ^= 1;
-      tc_fence_after();
       const int nb = uniform(r.blk1 - r.blk0);
       const int alt = uniform(r.alt), two = uniform(r.n_tok1 > 0);
-      const int ahead = alt ? 2 : 1, tile = alt ? 0 : s;
+      const int ahead = alt ? 2 : 1;
       const bool on = alt || s == 0 || two;  // whether this stream works in this run
+      const int tile = alt ? slot : s;       // the Q slot it reads
+      if (alt) slot ^= 1;
+      auto wait_q = [&](int t) {
+        if (!ok || !warp_wait(barQFull(t), (q_ph >> t) & 1u, p.err, misc)) ok = false;
+        q_ph ^= 1u << t;
+      };
+      if (on) wait_q(tile);
+      if (!ok) break;
+      tc_fence_after();
       auto mine = [&](int i) { return on && (!alt || (i & 1) == s); };
       // the last block whose S this stream makes
       const int last = !on ? -1 : alt ? nb - 1 - ((nb - 1 - s) & 1) : nb - 1;
@@ -512,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           else mbar_arrive(bar);
         }
       };
-      if (last < 0) leave(barQEmpty, false);
+      if (on && last < 0) leave(barQEmpty(tile), false);
       // the stream's first S
       for (int i = 0; ok && i < min(ahead, nb); ++i) {
         const int kst = take();
@@ -524,7 +566,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         leave(barEmpty(kst), mine(i));
-        if (i == last) leave(barQEmpty, true);
+        if (i == last) leave(barQEmpty(tile), true);
+        __syncwarp();
+      }
+      // the other stream's Q: this one only says that it does not read it
+      if (ok && !alt && (s == 1 || two)) {
+        wait_q(s ^ 1);
+        if (ok) leave(barQEmpty(s ^ 1), false);
         __syncwarp();
       }
       for (int i = 0; ok && i < nb; ++i) {
@@ -553,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         leave(barEmpty(vst), mine(i));
         if (more) leave(barEmpty(kst), mine(i));
-        if (more && i + ahead == last) leave(barQEmpty, true);
+        if (more && i + ahead == last) leave(barQEmpty(tile), true);
         __syncwarp();
       }
     }
@@ -764,6 +812,9 @@ template <int D, bool CACHED>
 __global__ void __launch_bounds__(256) join_kernel(const AttnParams p, const AttnJoin* joins, int n_joins) {
   constexpr int V = D / 32;  // values per lane
   const int lane = threadIdx.x & 31;
+  // launched while the attention kernel still runs; its results are there
+  // from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long w = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   long long prow, q_tok;
   int head, n0, base0, step0, n1 = 0, base1 = 0;
@@ -805,23 +856,37 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p, const Att
     const int part = i < n0 ? base0 + i * step0 : base1 + (i - n0);
     return static_cast<long long>(part) * p.part_rows + prow;
   };
-  float top = -INFINITY;
-  for (int i = lane; i < n0 + n1; i += 32) top = fmaxf(top, p.part_ml[at(i)].x);
+  const int n = n0 + n1;
+  float top = -INFINITY, l = 0.f, acc[V] = {};
+  for (int b = 0; b < n; b += 32) {  // 32 partial results at a time, one per lane
+    const float2 ml = b + lane < n ? p.part_ml[at(b + lane)] : make_float2(-INFINITY, 0.f);
+    float mx = ml.x;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  float acc[V] = {}, l = 0.f;
-  for (int i = 0; i < n0 + n1; ++i) {
-    const float2 ml = p.part_ml[at(i)];
-    if (ml.x == -INFINITY) continue;  // saw nothing; its o was perhaps not written
-    const float f = ex2(ml.x - top);
-    l += f * ml.y;
-    const float* src = p.part_o + at(i) * D + lane * V;
-    if (V == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(src);
-      acc[0] += f * v.x, acc[1] += f * v.y, acc[V - 2] += f * v.z, acc[V - 1] += f * v.w;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(src);
-      acc[0] += f * v.x, acc[1] += f * v.y;
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float was = top;
+    top = fmaxf(top, mx);
+    const float f = was == -INFINITY ? 0.f : ex2(was - top);
+    // (one that saw nothing has weight 0; its o was perhaps not written)
+    const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+    float add = w == 0.f ? 0.f : w * ml.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) add += __shfl_xor_sync(0xffffffffu, add, o);
+    l = l * f + add;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] *= f;
+    const int m = min(32, n - b);
+#pragma unroll 8
+    for (int i = 0; i < m; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      if (wi == 0.f) continue;
+      const float* src = p.part_o + at(b + i) * D + lane * V;
+      if (V == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        acc[0] += wi * v.x, acc[1] += wi * v.y, acc[V - 2] += wi * v.z, acc[V - 1] += wi * v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        acc[0] += wi * v.x, acc[1] += wi * v.y;
+      }
     }
   }
   const float inv = top == -INFINITY ? 0.f : 1.f / l;
@@ -833,6 +898,22 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p, const Att
     *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
   if (p.lse && lane == 0)
     p.lse[q_tok * p.H_q + head] = top == -INFINITY ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+}
+
+// The join kernel may be set up while the attention kernel before it in the
+// stream runs (it waits for its end on the device).
+cudaError_t launch_dependent(void (*kern)(const AttnParams, const AttnJoin*, int), int grid, cudaStream_t s,
+                             const AttnParams& p, const AttnJoin* joins, int n_joins) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p, joins, n_joins);
 }
 
 template <int D, typename Runs>
@@ -858,9 +939,8 @@ cudaError_t launch_attn_packed(const AttnParams& p, int d, int grid, const CUten
 cudaError_t launch_attn_join(const AttnParams& p, int d, const AttnJoin* joins, int n_joins, cudaStream_t s) {
   if (n_joins <= 0) return cudaSuccess;
   const int grid = n_joins * (kRows / 8);
-  if (d == 128) join_kernel<128, false><<<grid, 256, 0, s>>>(p, joins, n_joins);
-  else join_kernel<64, false><<<grid, 256, 0, s>>>(p, joins, n_joins);
-  return cudaGetLastError();
+  return d == 128 ? launch_dependent(join_kernel<128, false>, grid, s, p, joins, n_joins)
+                  : launch_dependent(join_kernel<64, false>, grid, s, p, joins, n_joins);
 }
 
 cudaError_t launch_attn_cache(const AttnParams& p, int d, int grid, const CUtensorMap& tq,
@@ -871,9 +951,8 @@ cudaError_t launch_attn_cache(const AttnParams& p, int d, int grid, const CUtens
   if (e != cudaSuccess) return e;
   const long long blocks = (p.part_rows + 7) / 8;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  if (d == 128) join_kernel<128, true><<<static_cast<unsigned>(blocks), 256, 0, s>>>(p, nullptr, 0);
-  else join_kernel<64, true><<<static_cast<unsigned>(blocks), 256, 0, s>>>(p, nullptr, 0);
-  return cudaGetLastError();
+  return d == 128 ? launch_dependent(join_kernel<128, true>, static_cast<int>(blocks), s, p, nullptr, 0)
+                  : launch_dependent(join_kernel<64, true>, static_cast<int>(blocks), s, p, nullptr, 0);
 }
 
 }  // namespace mf

@@ -198,6 +198,7 @@ cudaError_t launch_rope(const RopeParams& p, int f32, int d, cudaStream_t s);
 
 // Attention over packed sequences or caches (mf_attn_tc.cu).
 constexpr int kAttnNoWindow = 1 << 30;  // a window that hides nothing
+constexpr int kAttnCostRun = 3, kAttnCostPair = 3, kAttnCostOne = 2;
 constexpr int kAttnFar = 1 << 29;       // a row position past every key, and the most keys
 
 // One run of key blocks of one query tile pair (packed form): what a CTA does
@@ -235,7 +236,7 @@ struct AttnParams {
   int n, Lq, cap, P;
   int n_pre_tiles;           // row tiles of all n * Lq tokens
   int np_pre, np_suf;        // partial results a row can have from each
-  int min_blocks;            // least key blocks per CTA
+  int min_span;              // least work per CTA (kAttnCost units)
   int* n_part;               // [units] runs of each unit, written by its last run
   // partial results
   float* part_o;             // [partial][part_rows][d], not normalised
