@@ -31,7 +31,7 @@ struct mf_attn_s {
   int* cta_d = nullptr;
   AttnJoin* joins_d = nullptr;
   // cache form
-  int n_max = 0, Lq = 0, cap = 0, P = 0;
+  int n_max = 0, Lq = 0, cap = 0, P = 0, HG = 1, groups = 1;
   int* err_d = nullptr;
   int* host_err = nullptr;      // pinned
   mf_alloc_fn alloc = nullptr;
@@ -42,7 +42,7 @@ struct mf_attn_s {
 namespace {
 
 constexpr int kBlock = 128;     // keys per block of the kernel
-constexpr int kMinSpan = 4;     // cache form: least work per CTA (a block of each stream)
+constexpr int kMinSpan = 2;     // cache form: least key blocks per CTA (one for each stream)
 constexpr int kMaxTokens = kAttnFar;
 
 void* h_alloc(mf_attn_t h, size_t bytes) {
@@ -138,45 +138,43 @@ int finish_handle(mf_attn_t h, mf_attn_t* out, const std::vector<AttnSeg>& segs,
 
 // Cache form: partial results a row can have, and the workspace's parts.
 struct CacheLayout {
-  int np_pre, np_suf, pre_tiles;
+  int np_pre, np_suf, pairs, nbp;
   size_t n_part, ml, o, bytes;
 };
 CacheLayout cache_layout(const mf_attn_s* h, int n) {
   CacheLayout c{};
-  const long long toks = (long long)n * h->Lq;
-  c.pre_tiles = (int)((toks + h->TQ - 1) / h->TQ);
-  const long long pairs = h->P > 0 ? (c.pre_tiles + 1) / 2 : 0;
-  const long long nbp = (h->P + kBlock - 1) / kBlock;
+  const long long toks = (long long)n * h->Lq, tiles = (toks + h->TQ - 1) / h->TQ;
+  c.pairs = h->P > 0 ? (int)((tiles + 1) / 2) : 0;
+  c.nbp = (h->P + kBlock - 1) / kBlock;
   // most blocks of one request's cache: every key, or the window and sinks
   long long nbs = (h->cap + kBlock - 1) / kBlock;
   if (h->window < kAttnNoWindow)
     nbs = std::min(nbs, (std::min((long long)h->n_sink, (long long)h->cap) + kBlock - 1) / kBlock +
                             ((long long)h->window + h->Lq - 1 + kBlock - 1) / kBlock) + 1;
-  // a line whose blocks take w units is cut every per_cta units: at most
-  // w / per_cta + 2 pieces; per_cta is at least the even share of what is
-  // certainly there (the prefix; for a request, its own blocks in every KV
-  // head too)
-  const double pre = (double)pairs * nbp * kAttnCostPair * h->H_kv / h->grid;
-  const double share_pre = std::max((double)kMinSpan, pre);
-  const double share_suf = std::max((double)kMinSpan, pre + (double)nbs * kAttnCostOne * h->H_kv / h->grid);
-  if (pairs > 0) {
-    c.np_pre = (int)(nbp * kAttnCostPair / share_pre) + 3;
-    if (c.pre_tiles & 1) c.np_pre *= 2;  // a lone tile's streams have results of their own
+  // a line of nb blocks is cut every `span` blocks: at most nb / span + 2
+  // pieces; the span is at least the even share of what is certainly there
+  // (the prefix; for a request, its own blocks in every KV head)
+  const double span_pre = std::max((double)kMinSpan, (double)c.pairs * c.nbp * h->H_kv / h->grid);
+  const double span_suf = std::max((double)kMinSpan, (double)nbs * h->H_kv / h->grid);
+  if (c.pairs > 0) {
+    c.np_pre = (int)(c.nbp / span_pre) + 3;
+    if (tiles & 1) c.np_pre *= 2;  // a lone tile's streams have results of their own
   }
-  c.np_suf = 2 * ((int)(nbs * kAttnCostOne / share_suf) + 3);
+  c.np_suf = 2 * ((int)(nbs * h->HG / span_suf) + 3);
   const size_t rows = (size_t)toks * h->H_q;
   const size_t np = (size_t)c.np_pre + c.np_suf;
   c.n_part = 0;
-  c.ml = up256(((size_t)pairs + n) * h->H_kv * sizeof(int));
+  c.ml = up256(((size_t)c.pairs * h->H_kv + (size_t)n * h->groups) * sizeof(int));
   c.o = c.ml + up256(np * rows * sizeof(float2));
   c.bytes = c.o + up256(np * rows * h->d * sizeof(float));
   return c;
 }
 
-int make_q_map(const mf_attn_s* h, CUtensorMap* m, const void* q, int64_t ld, int64_t rows) {
+// Q tiles of `heads` KV heads' queries and `toks` tokens.
+int make_q_map(const mf_attn_s* h, CUtensorMap* m, const void* q, int64_t ld, int64_t rows, int heads, int toks) {
   const uint64_t dims[4] = {(uint64_t)h->d, (uint64_t)h->G, (uint64_t)h->H_kv, (uint64_t)rows};
   const uint64_t st[3] = {(uint64_t)h->d * 2, (uint64_t)h->G * h->d * 2, (uint64_t)ld * 2};
-  const uint32_t box[4] = {64, (uint32_t)h->G, 1, (uint32_t)h->TQ};
+  const uint32_t box[4] = {64, (uint32_t)h->G, (uint32_t)heads, (uint32_t)toks};
   return make_map4(m, q, dims, st, box);
 }
 
@@ -450,8 +448,8 @@ int mf_attn_create_cache(mf_attn_t* out, int n_max, int Lq, int capacity, int pr
     return fail(MF_ERR_UNSUPPORTED, "n_max = %d is too large", n_max);
   {  // the kernel lays all work end to end in 32 bits
     const long long tiles = ((long long)n_max * Lq + kBlock / (H_q / H_kv) - 1) / (kBlock / (H_q / H_kv));
-    const long long lines = (tiles + 1) / 2 * (kAttnCostRun + kAttnCostPair * ((prefix_len + kBlock - 1ll) / kBlock)) +
-                            n_max * (kAttnCostRun + kAttnCostOne * ((capacity + kBlock - 1ll) / kBlock + 1));
+    const long long lines = (tiles + 1) / 2 * (kAttnCostPre + (prefix_len + kBlock - 1ll) / kBlock) +
+                            n_max * (kAttnCostCache + (capacity + kBlock - 1ll) / kBlock + 1);
     if (lines * H_kv > (1ll << 30)) return fail(MF_ERR_UNSUPPORTED, "n_max = %d, capacity = %d and prefix_len = %d are too much work for one call", n_max, capacity, prefix_len);
   }
   mf_attn_t h = new (std::nothrow) mf_attn_s();
@@ -468,6 +466,8 @@ int mf_attn_create_cache(mf_attn_t* out, int n_max, int Lq, int capacity, int pr
   h->Lq = Lq;
   h->cap = capacity;
   h->P = prefix_len;
+  h->HG = std::min(H_kv, kBlock / (Lq * h->G));
+  h->groups = (H_kv + h->HG - 1) / h->HG;
   h->alloc = alloc_fn;
   h->dealloc = free_fn;
   h->ctx = alloc_ctx;
@@ -524,7 +524,7 @@ int mf_attn_packed(mf_attn_t h, const void* q, int64_t ld_q, const void* k, int6
     return fail(MF_ERR_ARG, "the workspace has %lld bytes, %lld are needed", (long long)workspace_bytes, (long long)need);
   if (reinterpret_cast<uintptr_t>(workspace) & 255) return fail(MF_ERR_ARG, "the workspace must be 256-byte aligned");
   CUtensorMap tq, tk, tv;
-  if ((rc = make_q_map(h, &tq, q, ld_q, T)) != MF_OK) return rc;
+  if ((rc = make_q_map(h, &tq, q, ld_q, T, 1, h->TQ)) != MF_OK) return rc;
   if ((rc = make_map(&tk, k, (uint64_t)wk, (uint64_t)T, (uint64_t)ld_k * 2, 64, kBlock)) != MF_OK) return rc;
   if ((rc = make_map(&tv, v, (uint64_t)wk, (uint64_t)T, (uint64_t)ld_v * 2, 64, kBlock)) != MF_OK) return rc;
   AttnParams p{};
@@ -538,6 +538,7 @@ int mf_attn_packed(mf_attn_t h, const void* q, int64_t ld_q, const void* k, int6
   p.o = o;
   p.ld_o = ld_o;
   p.lse = lse;
+  p.HG = 1;
   p.segs = h->segs_d;
   p.cta_segs = h->cta_d;
   p.part_rows = kBlock;
@@ -583,8 +584,9 @@ int mf_attn_cached(mf_attn_t h, int n, const void* q, int64_t ld_q, const void* 
   if (!workspace || workspace_bytes < (int64_t)c.bytes)
     return fail(MF_ERR_ARG, "the workspace has %lld bytes, %zu are needed", (long long)workspace_bytes, c.bytes);
   if (reinterpret_cast<uintptr_t>(workspace) & 255) return fail(MF_ERR_ARG, "the workspace must be 256-byte aligned");
-  CUtensorMap tq, tk, tv, tkp, tvp;
-  if ((rc = make_q_map(h, &tq, q, ld_q, rows)) != MF_OK) return rc;
+  CUtensorMap tq, tqc, tk, tv, tkp, tvp;
+  if ((rc = make_q_map(h, &tqc, q, ld_q, rows, h->HG, h->Lq)) != MF_OK) return rc;
+  if ((rc = make_q_map(h, &tq, q, ld_q, rows, 1, h->TQ)) != MF_OK) return rc;
   if ((rc = make_map(&tk, k_cache, (uint64_t)wk, (uint64_t)kr, (uint64_t)ld_k * 2, 64, kBlock)) != MF_OK) return rc;
   if ((rc = make_map(&tv, v_cache, (uint64_t)wk, (uint64_t)kr, (uint64_t)ld_v * 2, 64, kBlock)) != MF_OK) return rc;
   tkp = tk;
@@ -609,7 +611,10 @@ int mf_attn_cached(mf_attn_t h, int n, const void* q, int64_t ld_q, const void* 
   p.Lq = h->Lq;
   p.cap = h->cap;
   p.P = h->P;
-  p.n_pre_tiles = c.pre_tiles;
+  p.pre_pairs = c.pairs;
+  p.pre_blocks = c.nbp;
+  p.HG = h->HG;
+  p.groups = h->groups;
   p.np_pre = c.np_pre;
   p.np_suf = c.np_suf;
   p.min_span = kMinSpan;
@@ -619,7 +624,7 @@ int mf_attn_cached(mf_attn_t h, int n, const void* q, int64_t ld_q, const void* 
   p.part_o = reinterpret_cast<float*>(ws + c.o);
   p.part_rows = rows * h->H_q;
   p.err = h->err_d;
-  MF_CUDA(launch_attn_cache(p, h->d, h->grid, tq, tk, tv, tkp, tvp, static_cast<cudaStream_t>(stream)),
+  MF_CUDA(launch_attn_cache(p, h->d, h->grid, tq, tk, tv, tkp, tvp, tqc, static_cast<cudaStream_t>(stream)),
           "cache attention kernels");
   return MF_OK;
 }

@@ -128,16 +128,24 @@ struct Run {
   int alt;                    // one tile, key blocks alternate between the streams
   int pos;                    // position of the first token
   int k_row0, a1, b0, b1;
-  int blk0, blk1;
-  int head, prefix;           // prefix: K and V are the shared ones
+  int nb;                     // key blocks of a head
+  int blk0, blk1;             // this run's: block j is block j % nb of head j / nb
+  int head, heads;            // first KV head, KV heads of the tile
+  int kind;                   // kOwn, kPrefix (K and V are the shared ones), kCache
   int part;                   // first partial index, or -1
 };
+enum { kOwn = 0, kPrefix = 1, kCache = 2 };
 
-// Key block b of a run's ranges: start and how many of its keys count.
-__device__ __forceinline__ void block_at(const Run& r, int b, int& j0, int& valid) {
+// Block j of a run: its head (of the tile's), first key and how many count.
+__device__ __forceinline__ void block_at(const Run& r, int j, int& hh, int& j0, int& valid) {
+  hh = 0;
+  if (r.kind == kCache) {
+    hh = j / r.nb;
+    j -= hh * r.nb;
+  }
   const int na = (r.a1 + kKeys - 1) / kKeys;
-  const bool in_a = b < na;
-  j0 = in_a ? b * kKeys : r.b0 + (b - na) * kKeys;
+  const bool in_a = j < na;
+  j0 = in_a ? j * kKeys : r.b0 + (j - na) * kKeys;
   valid = min(kKeys, (in_a ? r.a1 : r.b1) - j0);
 }
 
@@ -166,17 +174,25 @@ struct PackedRuns {
     r.b1 = s.b1;
     r.blk0 = s.blk0;
     r.blk1 = s.blk1;
+    r.nb = 0;
     r.head = s.head;
-    r.prefix = 0;
+    r.heads = 1;
+    r.kind = kOwn;
     r.part = s.part;
     return true;
   }
 };
 
-// Cache form: every unit (prefix: tile pair and KV head; cache: request and
-// KV head) is a line of key blocks; the lines laid end to end are cut into
-// equal spans, one per CTA, so that uneven cache lengths balance and a unit is
-// cut only where a span ends.
+// Cache form.  The prefix's units are (tile pair, KV head); a cache's are
+// (request, group of as many KV heads as have their rows in one tile): all
+// heads' rows are one Q tile, and a block of head h gives weights to h's rows
+// only, so that a run takes a request's heads one after another without
+// starting anew.  Each unit is a line: what a run costs to start and end, then
+// its blocks.  The prefix's lines laid end to end are cut into equal spans,
+// one per CTA, and the caches' lines likewise, so that uneven lengths balance
+// and a unit is cut only where a span ends; a block belongs to the span in
+// which it begins.  Every second CTA takes its caches' span first: the
+// prefix's products and the caches' loads then overlap.
 struct Unit {
   int a1, b0, b1, nb;  // key ranges of a request's cache, in blocks
 };
@@ -191,112 +207,115 @@ __device__ __forceinline__ Unit cache_unit(const AttnParams& p, int len) {
   u.nb = (u.a1 + kKeys - 1) / kKeys + (u.b1 - u.b0 + kKeys - 1) / kKeys;
   return u;
 }
-// A line's length: what a run costs to start and end, then its blocks, in
-// units of ~0.4 us (a tile pair's block takes ~1.3 us, a single tile's ~0.8,
-// a run's start and end ~1.3).  A block belongs to the CTA in whose span it
-// begins.
-constexpr int kCostRun = kAttnCostRun, kCostPair = kAttnCostPair, kCostOne = kAttnCostOne;
-struct CacheSpan {
-  int total, pre;  // all lines, and the prefix's
-  int per_cta;
-  int nbp, pairs;  // prefix: blocks per line, tile pairs
-};
-__device__ __forceinline__ int line_of(int nb, int cost) { return nb > 0 ? kCostRun + nb * cost : 0; }
-__device__ __forceinline__ CacheSpan cache_span(const AttnParams& p, int suffix) {
-  CacheSpan c;
-  c.nbp = (p.P + kKeys - 1) / kKeys;
-  c.pairs = p.P > 0 ? (p.n_pre_tiles + 1) / 2 : 0;
-  c.pre = c.pairs * line_of(c.nbp, kCostPair) * p.H_kv;
-  c.total = c.pre + suffix * p.H_kv;
-  c.per_cta = max(p.min_span, (c.total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
-  return c;
+constexpr int kCostPre = kAttnCostPre, kCostCache = kAttnCostCache;  // a run's start and end, in blocks
+// the lines of a request's units
+__device__ __forceinline__ int cache_line(const AttnParams& p, int nb) {
+  return nb > 0 ? p.groups * kCostCache + nb * p.H_kv : 0;
+}
+__device__ __forceinline__ int span_of(const AttnParams& p, int total) {
+  return max(p.min_span, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
 }
 
 struct CacheRuns {
   const AttnParams& p;
-  CacheSpan c;
-  int f0, f1;      // this CTA's span
-  int at;          // start of the unit's line
-  int who, head;   // tile pair or request, KV head
-  bool prefix;
-  Unit u;          // of the request
-  // misc: [2] first request, [4] the lines (per head) before it, [5] all requests' lines
+  int todo;                  // parts left: 2, 1, 0
+  bool pre;                  // the part at hand is the prefix
+  int f0, f1, per;           // this CTA's span of it
+  int at;                    // start of the unit's line
+  int who, head;             // tile pair or request, (first) KV head
+  int suf_total, suf_first, suf_before;
+  Unit u;                    // of the request
+  // misc: [2] first request, [4] the lines before it, [5] all requests' lines
   __device__ CacheRuns(const AttnParams& p_, const volatile int* misc) : p(p_) {
-    c = cache_span(p, misc[5]);
-    f0 = min(c.total, c.per_cta * static_cast<int>(blockIdx.x));
-    f1 = min(c.total, f0 + c.per_cta);
-    prefix = f0 < c.pre;
-    if (prefix) {
-      const int line = line_of(c.nbp, kCostPair), unit = f0 / line;
+    suf_first = misc[2];
+    suf_before = misc[4];
+    suf_total = misc[5];
+    todo = 2;
+    pre = (blockIdx.x & 1) == 0;
+    begin();
+  }
+  __device__ int pre_line() const { return kCostPre + p.pre_blocks; }
+  __device__ void begin() {
+    const int total = pre ? p.pre_pairs * p.H_kv * pre_line() : suf_total;
+    per = span_of(p, total);
+    // (from the other end of the CTAs: two short lists meet late)
+    f0 = min(total, per * static_cast<int>(pre ? blockIdx.x : gridDim.x - 1 - blockIdx.x));
+    f1 = min(total, f0 + per);
+    if (pre) {
+      const int unit = f0 / pre_line();
       who = unit / p.H_kv;
       head = unit - who * p.H_kv;
-      at = unit * line;
+      at = unit * pre_line();
     } else {
-      who = misc[2];
+      who = suf_first;
       head = 0;
-      at = c.pre + misc[4] * p.H_kv;
+      at = suf_before;
       u = cache_unit(p, who < p.n ? p.lens[who] : 0);
-      const int line = line_of(u.nb, kCostOne);
-      if (line > 0) {
-        head = (f0 - at) / line;
-        at += head * line;
-      }
     }
   }
   __device__ bool next(Run& o) {
     for (;;) {
-      if (at >= f1) return false;
+      if (at >= f1) {
+        if (--todo <= 0) return false;
+        pre = !pre;
+        begin();
+        continue;
+      }
       // the unit at `at`
-      const int nb = prefix ? c.nbp : u.nb, cost = prefix ? kCostPair : kCostOne;
-      const int begin = at + kCostRun;  // where its first block begins
-      o.blk0 = max(0, (f0 - begin + cost - 1) / cost);
-      o.blk1 = min(nb, (f1 - begin + cost - 1) / cost);
-      const bool some = nb > 0 && f1 > begin && o.blk0 < o.blk1;
+      const int heads = pre ? 1 : min(p.HG, p.H_kv - head);
+      const int nb = pre ? p.pre_blocks : u.nb * heads;
+      const int begins = at + (pre ? kCostPre : kCostCache);
+      o.blk0 = max(0, f0 - begins);
+      o.blk1 = min(nb, f1 - begins);
+      const bool some = o.blk0 < o.blk1;
       if (some) {
         o.head = head;
-        o.prefix = prefix;
-        if (prefix) {
+        o.heads = heads;
+        int unit, most;
+        if (pre) {
           const int tok0 = who * 2 * p.TQ, n_tok = p.n * p.Lq - tok0;
+          o.kind = kPrefix;
           o.q_row = tok0;
           o.n_tok0 = min(n_tok, p.TQ);
           o.n_tok1 = min(n_tok - o.n_tok0, p.TQ);
+          o.alt = o.n_tok1 == 0;
           o.pos = kAttnFar;
           o.k_row0 = 0;
           o.a1 = 0;
           o.b0 = 0;
           o.b1 = p.P;
+          o.nb = nb;
+          unit = who * p.H_kv + head;
+          most = p.np_pre;
         } else {
+          o.kind = kCache;
           o.q_row = who * p.Lq;
           o.n_tok0 = p.Lq;
           o.n_tok1 = 0;
+          o.alt = 1;
           o.pos = u.b1 - p.Lq;
           o.k_row0 = who * p.cap;
           o.a1 = u.a1;
           o.b0 = u.b0;
           o.b1 = u.b1;
+          o.nb = u.nb;
+          unit = p.pre_pairs * p.H_kv + who * p.groups + head / p.HG;
+          most = p.np_suf;
         }
-        o.alt = o.n_tok1 == 0;
         // (held to the buffers, whatever happens to lens meanwhile)
-        const int most = prefix ? p.np_pre : p.np_suf;
-        const int piece = min(max(static_cast<int>(blockIdx.x) - begin / c.per_cta, 0), most / (o.alt ? 2 : 1) - 1);
-        o.part = (prefix ? 0 : p.np_pre) + piece * (o.alt ? 2 : 1);
-        if (o.blk1 == nb && threadIdx.x == 0)
-          p.n_part[static_cast<long long>(prefix ? who : c.pairs + who) * p.H_kv + head] = piece + 1;
+        const int step = o.alt ? 2 : 1;
+        const int piece = min(max(f0 / per - begins / per, 0), most / step - 1);
+        o.part = (pre ? 0 : p.np_pre) + piece * step;
+        if (o.blk1 == nb && threadIdx.x == 0) p.n_part[unit] = piece + 1;
       }
       // the next unit
-      at += line_of(nb, cost);
-      if (nb == 0) head = p.H_kv - 1;  // an empty cache: no head has work
-      if (++head == p.H_kv) {
+      if (nb > 0) at = begins + nb;
+      head += nb > 0 ? heads : p.H_kv;  // an empty cache has no units
+      if (head >= p.H_kv) {
         head = 0;
         ++who;
-        if (prefix && who == c.pairs) {
-          prefix = false;
-          who = 0;
-          u = cache_unit(p, p.lens[0]);
-        } else if (!prefix && who < p.n) {
-          u = cache_unit(p, p.lens[who]);
-        }
-        if (!prefix && who >= p.n) at = f1;  // (past the last request)
+        if (pre ? who >= p.pre_pairs : who >= p.n) at = f1;  // past the last
+        else if (!pre) u = cache_unit(p, p.lens[who]);
       }
       if (some) return true;
     }
@@ -308,26 +327,24 @@ struct CacheRuns {
 __device__ __forceinline__ void cache_find(const AttnParams& p, volatile int* misc) {
   const int lane = threadIdx.x & 31;
   int sum = 0;
-  for (int r = lane; r < p.n; r += 32) sum += line_of(cache_unit(p, p.lens[r]).nb, kCostOne);
+  for (int r = lane; r < p.n; r += 32) sum += cache_line(p, cache_unit(p, p.lens[r]).nb);
   sum = __reduce_add_sync(0xffffffffu, sum);
-  const CacheSpan c = cache_span(p, sum);
-  const int g = min(c.total, c.per_cta * static_cast<int>(blockIdx.x)) - c.pre;
-  int first = 0, before = 0, run = 0;
-  bool found = g <= 0;
-  for (int r0 = 0; !found && r0 < p.n; r0 += 32) {
-    const int line = r0 + lane < p.n ? line_of(cache_unit(p, p.lens[r0 + lane]).nb, kCostOne) : 0;
+  const int f0 = min(sum, span_of(p, sum) * static_cast<int>(gridDim.x - 1 - blockIdx.x));
+  int first = p.n, before = sum, run = 0;
+  for (int r0 = 0; r0 < p.n; r0 += 32) {
+    const int line = r0 + lane < p.n ? cache_line(p, cache_unit(p, p.lens[r0 + lane]).nb) : 0;
     int inc = line;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, r0 + lane < p.n && g < (run + inc) * p.H_kv);
+    const unsigned hit = __ballot_sync(0xffffffffu, f0 < run + inc);
     if (hit) {
       const int l = __ffs(hit) - 1;
       first = r0 + l;
       before = run + __shfl_sync(0xffffffffu, inc - line, l);
-      found = true;
+      break;
     }
     run += __shfl_sync(0xffffffffu, inc, 31);
   }
@@ -352,7 +369,8 @@ template <int D, typename Runs>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                 const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tkp,
-                const __grid_constant__ CUtensorMap tvp, const AttnParams p, const bool cached) {
+                const __grid_constant__ CUtensorMap tvp, const __grid_constant__ CUtensorMap tqc,
+                const AttnParams p, const bool cached) {
   using L = Lay<D>;
   constexpr int NS = L::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -401,15 +419,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(uniform(misc[0]));
   Runs runs(p, misc);
-  Run r;
+  Run r{};
 
   if (warp == 9) {
     // ------------------------------------------------------------- loader
     if (lane == 0) {
       int g = 0, nq0 = 0, nq1 = 0, slot = 0;  // ring uses, uses of the Q slots, next slot
       bool ok = true;
-      auto load = [&](const CUtensorMap* map, int row) {
+      auto load = [&](const CUtensorMap* map, int i) {
         const int st = g % NS;
+        int hh, j0, valid;
+        block_at(r, r.blk0 + i, hh, j0, valid);
         if (misc[1] || !mbar_wait(barEmpty(st), ((g / NS) & 1) ^ 1, p.err)) {
           ok = false;
           return;
@@ -417,18 +437,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_tx(barFull(st), L::kTile);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
-          tma_load_2d(sb + L::kRing + st * L::kTile + c * L::kChunk, map, r.head * D + c * 64, row, barFull(st));
+          tma_load_2d(sb + L::kRing + st * L::kTile + c * L::kChunk, map, (r.head + hh) * D + c * 64,
+                      r.k_row0 + j0, barFull(st));
         ++g;
       };
       while (ok && runs.next(r)) {
-        const CUtensorMap* mk = r.prefix ? &tkp : &tk;
-        const CUtensorMap* mv = r.prefix ? &tvp : &tv;
+        const CUtensorMap* mk = r.kind == kPrefix ? &tkp : &tk;
+        const CUtensorMap* mv = r.kind == kPrefix ? &tvp : &tv;
+        const CUtensorMap* mq = r.kind == kCache ? &tqc : &tq;
+        const int q_bytes = (D / 64) * 128 * p.G * (r.kind == kCache ? p.HG * p.Lq : p.TQ);
         const int nb = r.blk1 - r.blk0, ahead = r.alt ? 2 : 1;
-        auto row = [&](int i) {
-          int j0, valid;
-          block_at(r, r.blk0 + i, j0, valid);
-          return r.k_row0 + j0;
-        };
         // Q tile t into a slot, once the products of the slot's last run are done
         auto load_q = [&](int to, int t) {
           int& nq = to ? nq1 : nq0;
@@ -437,10 +455,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             return;
           }
           ++nq;
-          mbar_arrive_tx(barQFull(to), (D / 64) * 128 * p.G * p.TQ);
+          mbar_arrive_tx(barQFull(to), q_bytes);
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(sb + L::kQ + to * L::kTile + c * L::kChunk, &tq, c * 64, 0, r.head, r.q_row + t * p.TQ,
+            tma_load_4d(sb + L::kQ + to * L::kTile + c * L::kChunk, mq, c * 64, 0, r.head, r.q_row + t * p.TQ,
                         barQFull(to));
         };
         // one-tile runs alternate between the slots: the next run's Q comes
@@ -449,14 +467,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           load_q(slot, 0);
           slot ^= 1;
         }
-        for (int i = 0; ok && i < min(ahead, nb); ++i) load(mk, row(i));
+        for (int i = 0; ok && i < min(ahead, nb); ++i) load(mk, i);
         if (!r.alt) {
           load_q(0, 0);
           if (r.n_tok1 > 0) load_q(1, 1);
         }
         for (int i = 0; ok && i < nb; ++i) {
-          load(mv, row(i));
-          if (ok && i + ahead < nb) load(mk, row(i + ahead));
+          load(mv, i);
+          if (ok && i + ahead < nb) load(mk, i + ahead);
         }
       }
       if (!ok) misc[1] = 1;
@@ -583,8 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && more) kst = take();
         if (!ok) break;
         if (mine(i)) {
-          int j0, valid;
-          block_at(r, r.blk0 + i, j0, valid);
+          int hh, j0, valid;
+          block_at(r, r.blk0 + i, hh, j0, valid);
           valid = uniform(valid);
           if (valid < kKeys) trim(vst, valid);
 #pragma unroll
@@ -621,7 +639,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t colS = lanes + kColS + 128 * s, colO = lanes + kColO + 128 * s;
-    const int tok = row / p.G, hg = row - tok * p.G;
+    // the row's token, KV head of the tile and query head of the group, in a
+    // tile of one KV head and in a tile of a cache's HG
+    const int tok_1 = row / p.G, hg_1 = row - tok_1 * p.G;
+    const int tok_c = tok_1 / p.HG, hh_c = tok_1 - tok_c * p.HG;
     const float sc = p.scale * 1.4426950408889634f;
     const float slack = 8.f / sc;
     uint32_t ph = 0;  // phase of both halves' S
@@ -630,20 +651,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tile = r.alt ? 0 : s;
       if (!r.alt && s == 1 && r.n_tok1 == 0) continue;
       const int n_tok = tile ? r.n_tok1 : r.n_tok0;
-      const int pos0 = r.pos + (r.prefix ? 0 : tile * p.TQ);
+      const bool cache = r.kind == kCache, prefix = r.kind == kPrefix;
+      const int tok = cache ? tok_c : tok_1, my_hh = cache ? hh_c : 0;
+      const int pos0 = r.pos + (prefix ? 0 : tile * p.TQ);
       const int step = r.alt ? 2 : 1;
       const int first = r.blk0 + (r.alt ? s : 0);
-      const int pos = r.prefix ? kAttnFar : pos0 + tok;
-      const int pos_last = r.prefix ? kAttnFar : pos0 + n_tok - 1;
+      const int pos = prefix ? kAttnFar : pos0 + tok;
+      const int pos_last = prefix ? kAttnFar : pos0 + n_tok - 1;
       // a warp none of whose rows is a query leaves its P as it finds it: rows
       // of a product do not mix
-      const bool idle = (warp & 3) * 32 >= n_tok * p.G;
+      const bool idle = (warp & 3) * 32 >= n_tok * p.G * (cache ? p.HG : 1);
       float m = -INFINITY, l = 0.f;  // reference (raw scores), sum
       for (int b = first; ok && b < r.blk1; b += step) {
-        int j0, valid;
-        block_at(r, b, j0, valid);
+        int hh, j0, valid;
+        block_at(r, b, hh, j0, valid);
+        const bool mine = hh == my_hh && (!cache || tok < n_tok);  // whether the row takes part
+        const bool none = !__any_sync(0xffffffffu, mine);
         // blocks that every row of the tile sees whole need no mask
-        const bool whole = valid == kKeys && j0 + kKeys - 1 <= pos0 &&
+        const bool whole = !cache && valid == kKeys && j0 + kKeys - 1 <= pos0 &&
                            (j0 > pos_last - p.window || j0 + kKeys <= p.n_sink);
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
@@ -657,6 +682,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           const uint32_t col = colS + kHalf * h;
+          if (none) {  // another head's block: no weight for these rows
+            uint32_t w[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) w[e] = 0u;
+            tmem_st32(col, w);
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(barP(s, h));
+            continue;
+          }
           float x[kHalf];
           {
             uint32_t* w = reinterpret_cast<uint32_t*>(x);
@@ -666,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_wait_ld();
           if (!whole) {
             const int c0 = j0 + kHalf * h;  // position of the half's first key
-            const int hi = min(valid - kHalf * h, pos + 1 - c0), lo = pos - p.window + 1 - c0;
+            const int hi = mine ? min(valid - kHalf * h, pos + 1 - c0) : 0, lo = pos - p.window + 1 - c0;
             const int sink = min(hi, p.n_sink - c0);
 #pragma unroll
             for (int c = 0; c < kHalf; c += 32) {
@@ -686,30 +722,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           // a row's first visible key sets its reference; later only a maximum
           // 2^8 above it moves it
           const bool move = m == -INFINITY ? top > -INFINITY : top > m + slack;
-          if (__any_sync(0xffffffffu, move)) {
-            float f = 1.f;
-            if (move) {
-              f = m == -INFINITY ? 0.f : ex2((m - top) * sc);
-              m = top;
-              l *= f;
+          // (a row that starts has weight zero in O so far: nothing to rescale)
+          const bool rescale = move && m > -INFINITY;
+          float f = 1.f;
+          if (move) {
+            f = rescale ? ex2((m - top) * sc) : 0.f;
+            m = top;
+            l *= f;
+          }
+          if (__any_sync(0xffffffffu, rescale)) {
+            // O must hold every product so far: those of the other half's last
+            // P are covered by that half's next S (or the run's end)
+            if (!warp_wait(barS(s, h ^ 1), h == 0 ? ph : ph ^ 1, p.err, misc)) {
+              ok = false;
+              break;
             }
-            if (b > first || h > 0) {
-              // O must hold every product so far: those of the other half's last
-              // P are covered by that half's next S (or the run's end)
-              if (!warp_wait(barS(s, h ^ 1), h == 0 ? ph : ph ^ 1, p.err, misc)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
+            tc_fence_after();
+            if (!rescale) f = 1.f;
 #pragma unroll
-              for (int c = 0; c < D; c += 16) {
-                uint32_t w[16];
-                tmem_ld16(colO + c, w);
-                tc_wait_ld();
+            for (int c = 0; c < D; c += 16) {
+              uint32_t w[16];
+              tmem_ld16(colO + c, w);
+              tc_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
-                tmem_st16(colO + c, w);
-              }
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
+              tmem_st16(colO + c, w);
             }
           }
           const float ref = m == -INFINITY ? 0.f : m * sc;
@@ -745,9 +782,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ph ^= 1;
         tc_fence_after();
       }
-      const bool mine = tok < n_tok;
+      const bool mine = tok < n_tok && my_hh < r.heads;
       const long long q_tok = r.q_row + tile * p.TQ + tok;
-      const int head = r.head * p.G + hg;
+      const int head = (r.head + my_hh) * p.G + hg_1;
       if (r.part < 0) {
         const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + q_tok * p.ld_o + static_cast<long long>(head) * D;
@@ -824,21 +861,20 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p, const Att
     q_tok = w / p.H_q;
     head = static_cast<int>(w - q_tok * p.H_q);
     const int kv = head / p.G, req = static_cast<int>(q_tok / p.Lq);
-    const int pairs = p.P > 0 ? (p.n_pre_tiles + 1) / 2 : 0;
     n0 = 0;
     base0 = 0;
     step0 = 1;
     // (counts are held to what the buffers have, whatever a failed run left)
-    if (p.P > 0) {
+    if (p.pre_pairs > 0) {
       const int pair = static_cast<int>(q_tok / (2 * p.TQ));
-      n0 = p.n_part[static_cast<long long>(pair) * p.H_kv + kv];
+      n0 = p.n_part[pair * p.H_kv + kv];
       // a lone last tile ran on both streams
-      if (2 * pair + 1 >= p.n_pre_tiles) n0 *= 2;
+      if (2ll * pair * p.TQ + p.TQ >= static_cast<long long>(p.n) * p.Lq) n0 *= 2;
       n0 = min(max(n0, 0), p.np_pre);
     }
     base1 = p.np_pre;
     if (cache_unit(p, p.lens[req]).nb > 0)
-      n1 = min(max(2 * p.n_part[(static_cast<long long>(pairs) + req) * p.H_kv + kv], 0), p.np_suf);
+      n1 = min(max(2 * p.n_part[p.pre_pairs * p.H_kv + req * p.groups + kv / p.HG], 0), p.np_suf);
   } else {
     const long long j = w / kRows;
     if (j >= n_joins) return;
@@ -918,13 +954,13 @@ cudaError_t launch_dependent(void (*kern)(const AttnParams, const AttnJoin*, int
 
 template <int D, typename Runs>
 cudaError_t launch_main(const AttnParams& p, int grid, const CUtensorMap& tq, const CUtensorMap& tk,
-                        const CUtensorMap& tv, const CUtensorMap& tkp, const CUtensorMap& tvp, bool cached,
-                        cudaStream_t s) {
+                        const CUtensorMap& tv, const CUtensorMap& tkp, const CUtensorMap& tvp,
+                        const CUtensorMap& tqc, bool cached, cudaStream_t s) {
   auto kern = attn_kernel<D, Runs>;
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = allow_smem(kern, Lay<D>::kBytes, done);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kThreads, Lay<D>::kBytes, s>>>(tq, tk, tv, tkp, tvp, p, cached);
+  kern<<<grid, kThreads, Lay<D>::kBytes, s>>>(tq, tk, tv, tkp, tvp, tqc, p, cached);
   return cudaGetLastError();
 }
 
@@ -932,8 +968,8 @@ cudaError_t launch_main(const AttnParams& p, int grid, const CUtensorMap& tq, co
 
 cudaError_t launch_attn_packed(const AttnParams& p, int d, int grid, const CUtensorMap& tq,
                                const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
-  return d == 128 ? launch_main<128, PackedRuns>(p, grid, tq, tk, tv, tk, tv, false, s)
-                  : launch_main<64, PackedRuns>(p, grid, tq, tk, tv, tk, tv, false, s);
+  return d == 128 ? launch_main<128, PackedRuns>(p, grid, tq, tk, tv, tk, tv, tq, false, s)
+                  : launch_main<64, PackedRuns>(p, grid, tq, tk, tv, tk, tv, tq, false, s);
 }
 
 cudaError_t launch_attn_join(const AttnParams& p, int d, const AttnJoin* joins, int n_joins, cudaStream_t s) {
@@ -945,9 +981,9 @@ cudaError_t launch_attn_join(const AttnParams& p, int d, const AttnJoin* joins, 
 
 cudaError_t launch_attn_cache(const AttnParams& p, int d, int grid, const CUtensorMap& tq,
                               const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tkp,
-                              const CUtensorMap& tvp, cudaStream_t s) {
-  cudaError_t e = d == 128 ? launch_main<128, CacheRuns>(p, grid, tq, tk, tv, tkp, tvp, true, s)
-                           : launch_main<64, CacheRuns>(p, grid, tq, tk, tv, tkp, tvp, true, s);
+                              const CUtensorMap& tvp, const CUtensorMap& tqc, cudaStream_t s) {
+  cudaError_t e = d == 128 ? launch_main<128, CacheRuns>(p, grid, tq, tk, tv, tkp, tvp, tqc, true, s)
+                           : launch_main<64, CacheRuns>(p, grid, tq, tk, tv, tkp, tvp, tqc, true, s);
   if (e != cudaSuccess) return e;
   const long long blocks = (p.part_rows + 7) / 8;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;

@@ -198,7 +198,7 @@ cudaError_t launch_rope(const RopeParams& p, int f32, int d, cudaStream_t s);
 
 // Attention over packed sequences or caches (mf_attn_tc.cu).
 constexpr int kAttnNoWindow = 1 << 30;  // a window that hides nothing
-constexpr int kAttnCostRun = 3, kAttnCostPair = 3, kAttnCostOne = 2;
+constexpr int kAttnCostPre = 1, kAttnCostCache = 2;  // a run's start and end, in key blocks
 constexpr int kAttnFar = 1 << 29;       // a row position past every key, and the most keys
 
 // One run of key blocks of one query tile pair (packed form): what a CTA does
@@ -234,9 +234,10 @@ struct AttnParams {
   // cache form
   const int* lens;           // [n] device
   int n, Lq, cap, P;
-  int n_pre_tiles;           // row tiles of all n * Lq tokens
+  int pre_pairs, pre_blocks; // prefix: pairs of row tiles (0: no prefix), key blocks
+  int HG, groups;            // caches: KV heads per tile, tiles per request
   int np_pre, np_suf;        // partial results a row can have from each
-  int min_span;              // least work per CTA (kAttnCost units)
+  int min_span;              // least work per CTA, in blocks
   int* n_part;               // [units] runs of each unit, written by its last run
   // partial results
   float* part_o;             // [partial][part_rows][d], not normalised
@@ -249,7 +250,7 @@ cudaError_t launch_attn_packed(const AttnParams& p, int d, int grid, const CUten
 cudaError_t launch_attn_join(const AttnParams& p, int d, const AttnJoin* joins, int n_joins, cudaStream_t s);
 cudaError_t launch_attn_cache(const AttnParams& p, int d, int grid, const CUtensorMap& tq,
                               const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tkp,
-                              const CUtensorMap& tvp, cudaStream_t s);
+                              const CUtensorMap& tvp, const CUtensorMap& tqc, cudaStream_t s);
 
 cudaError_t launch_selftest_wait(int* err, unsigned long long limit_ns, cudaStream_t s);
 
