@@ -52,7 +52,7 @@ struct Lay {
   static constexpr int kQ = 0;
   static constexpr int kRing = 2 * kTile;
   static constexpr int kBar = kRing + kStages * kTile;
-  static constexpr int kMisc = kBar + 8 * (12 + 2 * kStages);
+  static constexpr int kMisc = kBar + 8 * (16 + 2 * kStages);
   static constexpr int kMiscBytes = 128;
   static constexpr int kBytes = kMisc + kMiscBytes + 1024;
 };
@@ -384,8 +384,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto barQEmpty = [&](int t) { return sb + L::kBar + 16 + 8u * t; };
   auto barS = [&](int s, int h) { return sb + L::kBar + 32 + 8u * (2 * s + h); };
   auto barP = [&](int s, int h) { return sb + L::kBar + 64 + 8u * (2 * s + h); };
-  auto barFull = [&](int i) { return sb + L::kBar + 96 + 8u * i; };
-  auto barEmpty = [&](int i) { return sb + L::kBar + 96 + 8u * (NS + i); };
+  // (a run's last products have barriers of their own: the next run's first S
+  // may be there before a softmax warp looks, and it must not miss a phase)
+  auto barO = [&](int s, int h) { return sb + L::kBar + 96 + 8u * (2 * s + h); };
+  auto barFull = [&](int i) { return sb + L::kBar + 128 + 8u * i; };
+  auto barEmpty = [&](int i) { return sb + L::kBar + 128 + 8u * (NS + i); };
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up
   if (threadIdx.x == 0) {
@@ -395,6 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(barS(i >> 1, i & 1), 1);
+      mbar_init(barO(i >> 1, i & 1), 1);
       mbar_init(barP(i >> 1, i & 1), 4);
     }
     for (int i = 0; i < NS; ++i) {
@@ -420,6 +424,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = static_cast<uint32_t>(uniform(misc[0]));
   Runs runs(p, misc);
   Run r{};
+  // Who waits for the ring.  A barrier's phase is told from the one before it
+  // only, so whoever waits for a stage's use must know the use before it to be
+  // done, and no use may pass unseen.  The streams' MMA warps see every use in
+  // turn, the other stream's too, and a stage is free when both have said so.
+  // In a pair run that is the products' critical path (every wait costs it
+  // ~0.1 us), so from block kLean on, when each stage's earlier use is one of
+  // this run's, a softmax warp waits instead and the block's P says that V and
+  // the next K have landed.
+  constexpr int kLean = NS / 2;
+  // V rows past the block's last key, up to the next multiple of 16, become
+  // zero: their weights are zero, but what the box read there may be NaN
+  // (both streams may do so to a shared block: they write the same)
+  auto trim = [&](int st, int valid) {
+    const int n = ((valid + 15) & ~15) - valid;
+    for (int i = lane; i < n * 8 * (D / 64); i += 32) {
+      const int c = i / (n * 8), x = i - c * n * 8;
+      *reinterpret_cast<uint4*>(smem + L::kRing + st * L::kTile + c * L::kChunk + valid * 128 + x * 16) =
+          make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_async_smem();
+    __syncwarp();
+  };
 
   if (warp == 9) {
     // ------------------------------------------------------------- loader
@@ -491,18 +517,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t q_desc = sdesc_sw128(sb + L::kQ, 16, 1024);             // K-major
     const uint64_t k_desc = sdesc_sw128(sb + L::kRing, 16, 1024);
     const uint64_t v_desc = sdesc_sw128(sb + L::kRing, L::kChunk, 1024);   // MN-major
-    int stage = 0;
+    int stage = 0;                    // of the ring's next block
     uint32_t ring_ph = 0, q_ph = 0, p_ph = 0;  // q_ph: bit per Q slot; p_ph: both halves of P
     int slot = 0;
     bool ok = true;
-    auto take = [&]() {  // the ring's next block has landed; its stage
+    auto pass = [&]() {  // the ring's next block's stage
       const int st = stage;
-      if (!warp_wait(barFull(st), ring_ph, p.err, misc)) ok = false;
       if (++stage == NS) {
         stage = 0;
         ring_ph ^= 1;
       }
-      tc_fence_after();
       return st;
     };
     // S of one half of a key block
@@ -535,19 +559,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     };
-    // V rows past the block's last key, up to the next multiple of 16, become
-    // zero: their weights are zero, but what the box read there may be NaN
-    auto trim = [&](int st, int valid) {
-      const int upto = (valid + 15) & ~15;
-      if (valid == upto) return;
-      for (int i = lane; i < (upto - valid) * 8 * (D / 64); i += 32) {
-        const int c = i / ((upto - valid) * 8), x = i - c * (upto - valid) * 8;
-        *reinterpret_cast<uint4*>(smem + L::kRing + st * L::kTile + c * L::kChunk + valid * 128 + x * 16) =
-            make_uint4(0u, 0u, 0u, 0u);
-      }
-      fence_async_smem();
-      __syncwarp();
-    };
     while (ok && uniform(runs.next(r))) {
       const int nb = uniform(r.blk1 - r.blk0);
       const int alt = uniform(r.alt), two = uniform(r.n_tok1 > 0);
@@ -565,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto mine = [&](int i) { return on && (!alt || (i & 1) == s); };
       // the last block whose S this stream makes
       const int last = !on ? -1 : alt ? nb - 1 - ((nb - 1 - s) & 1) : nb - 1;
-      // a stage this stream has issued its products of, or that it does not use
+      // a Q slot or stage this stream has issued its products of, or does not use
       auto leave = [&](uint32_t bar, bool used) {
         if (lane == 0) {
           if (used) tc_commit(bar);
@@ -575,8 +586,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (on && last < 0) leave(barQEmpty(tile), false);
       // the stream's first S
       for (int i = 0; ok && i < min(ahead, nb); ++i) {
-        const int kst = take();
-        if (!ok) break;
+        const uint32_t kph = ring_ph;
+        const int kst = pass();
+        if (!warp_wait(barFull(kst), kph, p.err, misc)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
         if (mine(i)) {
           for (int h = 0; h < 2; ++h) {
             qk(h, tile, kst);
@@ -594,33 +610,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       for (int i = 0; ok && i < nb; ++i) {
-        // V of this block and K of the next are here before P is waited for
-        const int vst = take();
+        const bool lean = on && !alt && i >= kLean;
+        const uint32_t vph = ring_ph;
+        const int vst = pass();
         const bool more = i + ahead < nb;
-        int kst = 0;
-        if (ok && more) kst = take();
-        if (!ok) break;
-        if (mine(i)) {
-          int hh, j0, valid;
-          block_at(r, r.blk0 + i, hh, j0, valid);
-          valid = uniform(valid);
-          if (valid < kKeys) trim(vst, valid);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int steps = min(4, max(0, ((valid + 15) >> 4) - 4 * h));
-            pv(h, vst, steps, i < ahead && h == 0);
-            if (!ok) break;
-            if (more) qk(h, tile, kst);
-            if (lane == 0) tc_commit(barS(s, h));  // O so far, and the next S
-            __syncwarp();
-          }
-          if (!ok) break;
-          p_ph ^= 1;
+        const uint32_t kph = ring_ph;
+        const int kst = more ? pass() : 0;
+        if (!lean && !warp_wait(barFull(vst), vph, p.err, misc)) {
+          ok = false;
+          break;
         }
-        leave(barEmpty(vst), mine(i));
-        if (more) leave(barEmpty(kst), mine(i));
-        if (more && i + ahead == last) leave(barQEmpty(tile), true);
+        if (!mine(i)) {
+          leave(barEmpty(vst), false);
+          if (more) {
+            if (!warp_wait(barFull(kst), kph, p.err, misc)) {
+              ok = false;
+              break;
+            }
+            leave(barEmpty(kst), false);
+          }
+          __syncwarp();
+          continue;
+        }
+        int hh, j0, valid;
+        block_at(r, r.blk0 + i, hh, j0, valid);
+        valid = uniform(valid);
+        if (!lean && (valid & 15)) trim(vst, valid);
+        const int steps = (valid + 15) >> 4;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          pv(h, vst, min(4, max(0, steps - 4 * h)), i < ahead && h == 0);
+          if (!ok) break;
+          if (more && !lean && h == 0 && !warp_wait(barFull(kst), kph, p.err, misc)) {
+            ok = false;
+            break;
+          }
+          if (more) qk(h, tile, kst);
+          if (lane == 0) {
+            tc_commit(more ? barS(s, h) : barO(s, h));  // O so far, and the next S
+            if (h == 1 && more && i + ahead == last) tc_commit(barQEmpty(tile));
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        leave(barEmpty(vst), true);
+        if (more) leave(barEmpty(kst), true);
         __syncwarp();
+        p_ph ^= 1;
       }
     }
     if (!ok) misc[1] = 1;
@@ -645,10 +681,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tok_c = tok_1 / p.HG, hh_c = tok_1 - tok_c * p.HG;
     const float sc = p.scale * 1.4426950408889634f;
     const float slack = 8.f / sc;
-    uint32_t ph = 0;  // phase of both halves' S
+    uint32_t ph = 0, o_ph = 0;  // phases of both halves' S, and of the runs' last products
+    int ring = 0;     // ring uses before this run
     bool ok = true;
+    const bool keeper = (warp & 3) == 0;  // the stream's warp that minds the ring
     while (ok && runs.next(r)) {
       const int tile = r.alt ? 0 : s;
+      // (a pair run uses the ring for K of its first block, then V of each block
+      // and K of the next)
+      const int ring0 = ring;
+      ring += 2 * (r.blk1 - r.blk0);
       if (!r.alt && s == 1 && r.n_tok1 == 0) continue;
       const int n_tok = tile ? r.n_tok1 : r.n_tok0;
       const bool cache = r.kind == kCache, prefix = r.kind == kPrefix;
@@ -675,6 +717,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!warp_wait(barS(s, h), ph, p.err, misc)) {
             ok = false;
             break;
+          }
+          if (keeper && h == 0 && !r.alt && b - r.blk0 >= kLean) {
+            // V of this block and K of the next are here before its P says so
+            const int vu = ring0 + 1 + 2 * (b - r.blk0), ku = b + 1 < r.blk1 ? vu + 1 : vu;
+            if (!warp_wait(barFull(vu % NS), (vu / NS) & 1, p.err, misc) ||
+                !warp_wait(barFull(ku % NS), (ku / NS) & 1, p.err, misc)) {
+              ok = false;
+              break;
+            }
+            if (valid & 15) trim(vu % NS, valid);
           }
           if (idle) {
             if (lane == 0) mbar_arrive(barP(s, h));
@@ -732,8 +784,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (__any_sync(0xffffffffu, rescale)) {
             // O must hold every product so far: those of the other half's last
-            // P are covered by that half's next S (or the run's end)
-            if (!warp_wait(barS(s, h ^ 1), h == 0 ? ph : ph ^ 1, p.err, misc)) {
+            // P are covered by that half's next S, or are the run's last
+            const bool end = h == 1 && b + step >= r.blk1;
+            if (!warp_wait(end ? barO(s, 0) : barS(s, h ^ 1), end ? o_ph : h == 0 ? ph : ph ^ 1, p.err, misc)) {
               ok = false;
               break;
             }
@@ -775,11 +828,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ----------------------------------------------------------- epilogue
       const bool any = first < r.blk1;
       if (any) {
-        if (!warp_wait(barS(s, 0), ph, p.err, misc) || !warp_wait(barS(s, 1), ph, p.err, misc)) {
+        if (!warp_wait(barO(s, 0), o_ph, p.err, misc) || !warp_wait(barO(s, 1), o_ph, p.err, misc)) {
           ok = false;
           break;
         }
-        ph ^= 1;
+        o_ph ^= 1;
         tc_fence_after();
       }
       const bool mine = tok < n_tok && my_hh < r.heads;
