@@ -280,8 +280,7 @@ int mf_qk_norm_rope(const void* q, int64_t ld_q, void* q_out, int64_t ld_qo, con
   p.norm = norm;
   p.eps = eps;
   p.gain = gain;
-  p.n_rows = (long long)T * (H_q + H_k);
-  MF_CUDA(launch_rope(p, dtype == MF_DTYPE_F32, d, static_cast<cudaStream_t>(stream)), "norm and rotary kernel");
+  MF_CUDA(launch_rope(p, T, dtype == MF_DTYPE_F32, d, static_cast<cudaStream_t>(stream)), "norm and rotary kernel");
   return MF_OK;
 }
 
@@ -586,12 +585,13 @@ int mf_attn_cached(mf_attn_t h, int n, const void* q, int64_t ld_q, const void* 
   if (reinterpret_cast<uintptr_t>(workspace) & 255) return fail(MF_ERR_ARG, "the workspace must be 256-byte aligned");
   CUtensorMap tq, tqc, tk, tv, tkp, tvp;
   if ((rc = make_q_map(h, &tqc, q, ld_q, rows, h->HG, h->Lq)) != MF_OK) return rc;
-  if ((rc = make_q_map(h, &tq, q, ld_q, rows, 1, h->TQ)) != MF_OK) return rc;
   if ((rc = make_map(&tk, k_cache, (uint64_t)wk, (uint64_t)kr, (uint64_t)ld_k * 2, 64, kBlock)) != MF_OK) return rc;
   if ((rc = make_map(&tv, v_cache, (uint64_t)wk, (uint64_t)kr, (uint64_t)ld_v * 2, 64, kBlock)) != MF_OK) return rc;
+  tq = tqc;
   tkp = tk;
   tvp = tv;
   if (h->P > 0) {
+    if ((rc = make_q_map(h, &tq, q, ld_q, rows, 1, h->TQ)) != MF_OK) return rc;
     if ((rc = make_map(&tkp, k_prefix, (uint64_t)wk, (uint64_t)h->P, (uint64_t)ld_kp * 2, 64, kBlock)) != MF_OK) return rc;
     if ((rc = make_map(&tvp, v_prefix, (uint64_t)wk, (uint64_t)h->P, (uint64_t)ld_vp * 2, 64, kBlock)) != MF_OK) return rc;
   }

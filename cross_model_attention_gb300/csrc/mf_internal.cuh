@@ -191,10 +191,11 @@ struct RopeParams {
   int layout;                          // 0: pairs (i, i + rot/2), 1: pairs (2i, 2i+1)
   int norm;
   float eps, gain;
-  long long n_rows;                    // T * (H_q + H_k)
-  int rows_per_cta;                    // set by the launcher
+  // set by the launcher: a token's heads in shares of heads_per_unit
+  long long n_units;
+  int heads_per_unit, q_chunks, k_chunks;
 };
-cudaError_t launch_rope(const RopeParams& p, int f32, int d, cudaStream_t s);
+cudaError_t launch_rope(const RopeParams& p, long long T, int f32, int d, cudaStream_t s);
 
 // Attention over packed sequences or caches (mf_attn_tc.cu).
 constexpr int kAttnNoWindow = 1 << 30;  // a window that hides nothing

@@ -14,11 +14,15 @@
 // the integer product with the position, taken modulo 2^64, IS the exact
 // fraction of a turn; its top 32 bits go to sincospif.
 //
-// Bound: HBM (each row read once, written once).  A lane takes two 16-byte
-// chunks of a row that hold both halves of its pairs, so the rotation needs
-// no exchange and the norm only log2(lanes per row) shuffles.  A CTA walks a
-// run of consecutive (token, head) rows and computes the sines and cosines of
-// its few tokens once, in shared memory, for all of their heads.
+// Bound: HBM (each row read once, written once).  A group of d * size / 32
+// lanes takes a token's heads one after another: a lane holds two 16-byte
+// chunks of the row that have both halves of its pairs, so that the rotation
+// needs no exchange and the norm only a few shuffles, and its pairs' sines and
+// cosines and its weights stay in registers for all of the group's heads.
+// (From shared memory for every row, their reads, at four-way bank conflicts,
+// bound the kernel: 143 us for 16384 tokens of 40 + 40 heads of 128 in bf16.)
+// A group's share of a token is as many heads as leave every SM about eight
+// rounds of groups; a single token's heads all go to groups of their own.
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -71,73 +75,95 @@ enum { kHalf = 0, kPairs = 1, kHalfOdd = 2 };
 template <typename T, int D, int LAYOUT>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
   constexpr int N = Vec<T>::N;
-  constexpr int LPR = D / (2 * N);       // lanes per row
-  constexpr int kRowsPerPass = kThreads / LPR;
-  extern __shared__ float smem[];        // [2][D] weights, then [span][rot/2] (cos, sin)
-  float* wsm = smem;
-  float2* cs = reinterpret_cast<float2*>(smem + 2 * D);
+  constexpr int LPR = D / (2 * N);       // lanes per group
+  constexpr int kGroups = kThreads / LPR;
   const int half = p.rot >> 1;
-  const int H = p.H_q + p.H_k;
-  const long long row0 = static_cast<long long>(blockIdx.x) * p.rows_per_cta;
-  const long long row_end = min(row0 + p.rows_per_cta, p.n_rows);
-  const int t0 = static_cast<int>(row0 / H);
-  const int h0 = static_cast<int>(row0 - static_cast<long long>(t0) * H);
-  const int n_here = static_cast<int>(row_end - row0);
-  const int span = (h0 + n_here - 1) / H + 1;
+  const int l = threadIdx.x % LPR;
+  const long long unit = static_cast<long long>(blockIdx.x) * kGroups + threadIdx.x / LPR;
+  // (a group past the end works on the last unit and stores nothing, so that
+  // every lane joins the shuffles)
+  const bool here = unit < p.n_units;
+  const long long u = here ? unit : p.n_units - 1;
+  const int chunks = p.q_chunks + p.k_chunks;
+  const long long tok = u / chunks;
+  int c = static_cast<int>(u - tok * chunks);
+  const bool is_q = c < p.q_chunks;
+  if (!is_q) c -= p.q_chunks;
+  const int h_begin = c * p.heads_per_unit;
+  const int n = here ? min(p.heads_per_unit, (is_q ? p.H_q : p.H_k) - h_begin) : 0;
+  const long long at = static_cast<long long>(h_begin) * D;
+  const T* src = is_q ? static_cast<const T*>(p.q) + tok * p.ld_q + at : static_cast<const T*>(p.k) + tok * p.ld_k + at;
+  T* dst = is_q ? static_cast<T*>(p.q_out) + tok * p.ld_qo + at : static_cast<T*>(p.k_out) + tok * p.ld_ko + at;
 
+  const int hc = half / N;  // kHalf: chunks of half the rotated part
+  const bool turned = LAYOUT != kHalf || l < hc;  // kHalf: whether this lane's chunks are rotated
+  const int c0 = LAYOUT == kHalf && turned ? l : 2 * l;  // (2 hc + 2 (l - hc) = 2 l)
+  const int c1 = LAYOUT == kHalf && turned ? l + hc : 2 * l + 1;
+  uint4 wa = make_uint4(0u, 0u, 0u, 0u), wb = wa;
+  if (n > 0) {
+    wa = *reinterpret_cast<const uint4*>(src + c0 * N);
+    wb = *reinterpret_cast<const uint4*>(src + c1 * N);
+  }
+
+  // sines and cosines of this lane's pairs
+  const long long pos = p.positions[tok];
+  auto turn_of = [&](int f, float& cn, float& sn) {
+    const unsigned long long turn = static_cast<unsigned long long>(pos) * p.freq[f];
+    // top 32 bits as a signed fraction of a turn; sincospif takes half turns
+    sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f, &sn, &cn);  // 2^-31
+    cn *= p.gain;
+    sn *= p.gain;
+  };
+  constexpr int kTurns = LAYOUT == kHalfOdd ? 2 * N : N;
+  float cs[kTurns], sn[kTurns];
+#pragma unroll
+  for (int e = 0; e < kTurns; ++e) {
+    int f;  // the pair
+    if (LAYOUT == kHalf) {
+      f = turned ? c0 * N + e : -1;
+    } else if (LAYOUT == kPairs) {
+      f = e < N / 2 ? c0 * (N / 2) + e : c1 * (N / 2) + e - N / 2;
+      if (f >= half) f = -1;
+    } else {
+      const int d = e < N ? c0 * N + e : c1 * N + e - N;
+      f = d < half ? d : d < p.rot ? d - half : -1;
+    }
+    cs[e] = 1.f;
+    sn[e] = 0.f;
+    if (f >= 0) turn_of(f, cs[e], sn[e]);
+  }
+  float ga[N], gb[N];  // weights
+#pragma unroll
+  for (int e = 0; e < N; ++e) ga[e] = gb[e] = 1.f;
   if (p.norm) {
-    for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
-      const T* w = static_cast<const T*>(i < D ? p.q_weight : p.k_weight);
-      wsm[i] = w ? Vec<T>::load(w + (i < D ? i : i - D)) : 1.f;
+    const T* w = static_cast<const T*>(is_q ? p.q_weight : p.k_weight);
+    if (w) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        ga[e] = Vec<T>::load(w + c0 * N + e);
+        gb[e] = Vec<T>::load(w + c1 * N + e);
+      }
     }
   }
-  for (int i = threadIdx.x; i < span * half; i += kThreads) {
-    const int t = i / half, f = i - t * half;
-    const unsigned long long turn =
-        static_cast<unsigned long long>(static_cast<long long>(p.positions[t0 + t])) * p.freq[f];
-    // top 32 bits as a signed fraction of a turn; sincospif takes half turns
-    const float x = static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f;  // 2^-31
-    float sn, cn;
-    sincospif(x, &sn, &cn);
-    cs[i] = make_float2(cn * p.gain, sn * p.gain);
-  }
-  __syncthreads();
 
-  const int lane_row = threadIdx.x / LPR, l = threadIdx.x % LPR;
-  const int hc = half / N;  // kHalf: chunks of half the rotated part
-  int c0, c1;
-  bool turned = true;       // kHalf: whether this lane's chunks are rotated
-  if (LAYOUT == kHalf) {
-    turned = l < hc;
-    c0 = turned ? l : 2 * l;              // 2 hc + 2 (l - hc) = 2 l
-    c1 = turned ? l + hc : 2 * l + 1;
-  } else {
-    c0 = 2 * l;
-    c1 = 2 * l + 1;
-  }
-  // Lanes of one row are in one warp; a row past the end is computed on the
-  // last row's data and not stored, so that every lane joins the shuffles.
-  for (int base = 0; base < n_here; base += kRowsPerPass) {
-    const int i = base + lane_row;
-    const bool live = i < n_here;
-    const int j = h0 + (live ? i : n_here - 1);
-    const int tt = j / H, h = j - tt * H;
-    const bool is_q = h < p.H_q;
-    const long long tok = t0 + tt;
-    const T* src = is_q ? static_cast<const T*>(p.q) + tok * p.ld_q + static_cast<long long>(h) * D
-                        : static_cast<const T*>(p.k) + tok * p.ld_k + static_cast<long long>(h - p.H_q) * D;
-    T* dst = is_q ? static_cast<T*>(p.q_out) + tok * p.ld_qo + static_cast<long long>(h) * D
-                  : static_cast<T*>(p.k_out) + tok * p.ld_ko + static_cast<long long>(h - p.H_q) * D;
+  for (int i = 0; i < p.heads_per_unit; ++i) {
     float a[N], b[N];
-    Vec<T>::unpack(*reinterpret_cast<const uint4*>(src + c0 * N), a);
-    Vec<T>::unpack(*reinterpret_cast<const uint4*>(src + c1 * N), b);
-    float oa[N], ob[N];  // kHalfOdd: each element's partner
+    Vec<T>::unpack(wa, a);
+    Vec<T>::unpack(wb, b);
+    const bool live = i < n;
+    if (i + 1 < n) {  // the next head is on its way while one is worked on
+      wa = *reinterpret_cast<const uint4*>(src + (i + 1) * D + c0 * N);
+      wb = *reinterpret_cast<const uint4*>(src + (i + 1) * D + c1 * N);
+    }
+    float oa[N], ob[N];  // kHalfOdd: each element's partner, normed
     if (LAYOUT == kHalfOdd) {
+      const T* row = src + i * D;
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         const int da = c0 * N + e, db = c1 * N + e;
-        oa[e] = da < p.rot ? Vec<T>::load(src + (da < half ? da + half : da - half)) : 0.f;
-        ob[e] = db < p.rot ? Vec<T>::load(src + (db < half ? db + half : db - half)) : 0.f;
+        const int pa = da < half ? da + half : da - half, pb = db < half ? db + half : db - half;
+        oa[e] = live && da < p.rot ? Vec<T>::load(row + pa) : 0.f;
+        ob[e] = live && db < p.rot ? Vec<T>::load(row + pb) : 0.f;
       }
     }
     if (p.norm) {
@@ -147,113 +173,96 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
 #pragma unroll
       for (int off = LPR / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
       const float r = rsqrtf(ss * (1.f / D) + p.eps);
-      const float* w = wsm + (is_q ? 0 : D);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        a[e] *= r * w[c0 * N + e];
-        b[e] *= r * w[c1 * N + e];
+        a[e] *= r * ga[e];
+        b[e] *= r * gb[e];
       }
       if (LAYOUT == kHalfOdd) {
+        const T* w = static_cast<const T*>(is_q ? p.q_weight : p.k_weight);
 #pragma unroll
         for (int e = 0; e < N; ++e) {
           const int da = c0 * N + e, db = c1 * N + e;
-          if (da < p.rot) oa[e] *= r * w[da < half ? da + half : da - half];
-          if (db < p.rot) ob[e] *= r * w[db < half ? db + half : db - half];
+          const int pa = da < half ? da + half : da - half, pb = db < half ? db + half : db - half;
+          oa[e] *= r * (w && da < p.rot ? Vec<T>::load(w + pa) : 1.f);
+          ob[e] *= r * (w && db < p.rot ? Vec<T>::load(w + pb) : 1.f);
         }
       }
     }
-    const float2* ct = cs + tt * half;
     if (LAYOUT == kHalf) {
-      if (turned) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const float2 c = ct[c0 * N + e];
-          const float x = a[e], y = b[e];
-          a[e] = x * c.x - y * c.y;
-          b[e] = y * c.x + x * c.y;
+      for (int e = 0; e < N; ++e) {
+        const float x = a[e], y = b[e];
+        if (turned) {
+          a[e] = x * cs[e] - y * sn[e];
+          b[e] = y * cs[e] + x * sn[e];
         }
       }
     } else if (LAYOUT == kPairs) {
 #pragma unroll
       for (int e = 0; e < N; e += 2) {
-        const int ia = (c0 * N + e) >> 1, ib = (c1 * N + e) >> 1;
-        if (ia < half) {
-          const float2 c = ct[ia];
-          const float x = a[e], y = a[e + 1];
-          a[e] = x * c.x - y * c.y;
-          a[e + 1] = y * c.x + x * c.y;
+        const float x = a[e], y = a[e + 1], z = b[e], w = b[e + 1];
+        const int i0 = e >> 1, i1 = (N + e) >> 1;
+        if (2 * (c0 * (N / 2) + i0) < p.rot) {
+          a[e] = x * cs[i0] - y * sn[i0];
+          a[e + 1] = y * cs[i0] + x * sn[i0];
         }
-        if (ib < half) {
-          const float2 c = ct[ib];
-          const float x = b[e], y = b[e + 1];
-          b[e] = x * c.x - y * c.y;
-          b[e + 1] = y * c.x + x * c.y;
+        if (2 * (c1 * (N / 2) + i0) < p.rot) {
+          b[e] = z * cs[i1] - w * sn[i1];
+          b[e + 1] = w * cs[i1] + z * sn[i1];
         }
       }
     } else {
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         const int da = c0 * N + e, db = c1 * N + e;
-        if (da < p.rot) {
-          const float2 c = ct[da < half ? da : da - half];
-          a[e] = a[e] * c.x + (da < half ? -oa[e] : oa[e]) * c.y;
-        }
-        if (db < p.rot) {
-          const float2 c = ct[db < half ? db : db - half];
-          b[e] = b[e] * c.x + (db < half ? -ob[e] : ob[e]) * c.y;
-        }
+        if (da < p.rot) a[e] = a[e] * cs[e] + (da < half ? -oa[e] : oa[e]) * sn[e];
+        if (db < p.rot) b[e] = b[e] * cs[N + e] + (db < half ? -ob[e] : ob[e]) * sn[N + e];
       }
+      // in place: every lane of the row has read it before any lane writes it
+      __syncwarp();
     }
-    // in place: every lane of the row has read it before any lane writes it
-    // (a dead lane re-reads a live row of the same warp or of an earlier one)
-    if (LAYOUT == kHalfOdd) __syncwarp();
     if (live) {
-      *reinterpret_cast<uint4*>(dst + c0 * N) = Vec<T>::pack(a);
-      *reinterpret_cast<uint4*>(dst + c1 * N) = Vec<T>::pack(b);
+      *reinterpret_cast<uint4*>(dst + i * D + c0 * N) = Vec<T>::pack(a);
+      *reinterpret_cast<uint4*>(dst + i * D + c1 * N) = Vec<T>::pack(b);
     }
   }
 }
 
 template <typename T, int D>
-cudaError_t launch_t(RopeParams p, cudaStream_t s) {
-  constexpr int kRowsPerPass = kThreads / (D / (2 * Vec<T>::N));
-  const int H = p.H_q + p.H_k;
+cudaError_t launch_t(RopeParams p, long long T_, cudaStream_t s) {
+  constexpr int kGroups = kThreads / (D / (2 * Vec<T>::N));
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  // passes per CTA: enough CTAs for eight per SM first, then more rows per
-  // CTA so that a token's angles serve more of its heads; several passes only
-  // while they span at most 34 tokens, and one pass spans at most 64 (the
-  // shared memory for their angles)
-  long long passes = p.n_rows / (static_cast<long long>(kRowsPerPass) * sms * 8);
-  if (passes > 8) passes = 8;
-  if (passes > 32ll * H / kRowsPerPass) passes = 32ll * H / kRowsPerPass;
-  if (passes < 1) passes = 1;
-  p.rows_per_cta = static_cast<int>(passes) * kRowsPerPass;
-  const int half = p.rot / 2;
-  const int span = (p.rows_per_cta + H - 2) / H + 1;  // most tokens that rows_per_cta rows touch
-  const size_t smem = (2 * D) * sizeof(float) + static_cast<size_t>(span) * half * sizeof(float2);
-  const long long grid = (p.n_rows + p.rows_per_cta - 1) / p.rows_per_cta;
+  // heads per group: one while that leaves less than eight rounds of three
+  // CTAs per SM, else what does; shares of a token as even as they go
+  const long long rounds = static_cast<long long>(sms) * 3 * kGroups * 8;
+  const int most = p.H_q > p.H_k ? p.H_q : p.H_k;
+  long long hpu = (T_ * (p.H_q + p.H_k) + rounds - 1) / rounds;
+  if (hpu > most) hpu = most;
+  const int shares = static_cast<int>((most + hpu - 1) / hpu);
+  p.heads_per_unit = (most + shares - 1) / shares;
+  p.q_chunks = (p.H_q + p.heads_per_unit - 1) / p.heads_per_unit;
+  p.k_chunks = (p.H_k + p.heads_per_unit - 1) / p.heads_per_unit;
+  p.n_units = T_ * (p.q_chunks + p.k_chunks);
+  const long long grid = (p.n_units + kGroups - 1) / kGroups;
   if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
   auto go = [&](auto kern) -> cudaError_t {
-    if (smem > 48 * 1024) {
-      cudaError_t a = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-      if (a != cudaSuccess) return a;
-    }
-    kern<<<static_cast<unsigned>(grid), kThreads, smem, s>>>(p);
+    kern<<<static_cast<unsigned>(grid), kThreads, 0, s>>>(p);
     return cudaGetLastError();
   };
   if (p.layout == 1) return go(rope_kernel<T, D, kPairs>);
-  if (half % Vec<T>::N == 0) return go(rope_kernel<T, D, kHalf>);
+  if (p.rot / 2 % Vec<T>::N == 0) return go(rope_kernel<T, D, kHalf>);
   return go(rope_kernel<T, D, kHalfOdd>);
 }
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeParams& p, int f32, int d, cudaStream_t s) {
-  if (p.n_rows <= 0) return cudaSuccess;
-  if (f32) return d == 128 ? launch_t<float, 128>(p, s) : launch_t<float, 64>(p, s);
-  return d == 128 ? launch_t<__nv_bfloat16, 128>(p, s) : launch_t<__nv_bfloat16, 64>(p, s);
+cudaError_t launch_rope(const RopeParams& p, long long T, int f32, int d, cudaStream_t s) {
+  if (T <= 0) return cudaSuccess;
+  if (f32) return d == 128 ? launch_t<float, 128>(p, T, s) : launch_t<float, 64>(p, T, s);
+  return d == 128 ? launch_t<__nv_bfloat16, 128>(p, T, s) : launch_t<__nv_bfloat16, 64>(p, T, s);
 }
 
 }  // namespace mf

@@ -136,30 +136,30 @@ def _dtype_code(t) -> int:
     raise TypeError(f"unsupported dtype {t.dtype}")
 
 
-class _NoGuard:
-    def __enter__(self):
-        pass
-
-    def __exit__(self, *exc):
-        pass
-
-
-_NO_GUARD = _NoGuard()
-
-
-def _on(device, stream):
-    """(guard, raw stream) for a call on `device`: inside the guard, device and
-    stream are the call's, so that memory made there belongs to the stream the
-    call runs on.  No guard where they are current already."""
+def _on(t, stream):
+    """(guard, raw stream) for a call on the GPU of tensor or device `t`:
+    inside the guard, device and stream are the call's, so that memory made
+    there belongs to the stream the call runs on."""
     import torch
+    device = getattr(t, "device", t)
+    if device.type != "cuda":
+        raise MapFlowError(MF_ERR_ARG, f"a CUDA tensor is needed, not one on {device}")
     if stream is None:
-        if torch.cuda.current_device() == device.index:
-            return _NO_GUARD, torch.cuda.current_stream().cuda_stream
         with torch.cuda.device(device):
             stream = torch.cuda.current_stream()
     elif stream.device != device:
         raise MapFlowError(MF_ERR_ARG, f"the stream is on {stream.device}, the tensors on {device}")
     return torch.cuda.stream(stream), stream.cuda_stream  # (the stream's device becomes current too)
+
+
+def _raw_current(index: int):
+    """The current stream of GPU `index` where that is the current device
+    (no guard is needed then), else None.  A decode step makes several such
+    calls a layer: this takes 0.4 us, a guard with its stream objects 7."""
+    import torch
+    if index >= 0 and torch.cuda.current_device() == index:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return None
 
 
 def _rows(name: str, t, shape, dtype, device) -> int:
@@ -470,7 +470,8 @@ class RotaryPlan:
             raise MapFlowError(MF_ERR_ARG, f"unknown layout {layout!r} ({', '.join(_LAYOUTS)})")
         turns, self.gain = mf_rope_frequencies(rot_dim, base, scaling, factor, original_length, beta_fast,
                                                beta_slow)
-        self.rot_dim, self.layout = int(rot_dim), layout
+        self.rot_dim, self.layout, self._layout = int(rot_dim), layout, _LAYOUTS[layout]
+        self._lib = load_library()
         device = torch.device("cuda" if device is None else device)
         self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
 
@@ -479,44 +480,55 @@ class RotaryPlan:
         """q [T, H_q, d] and k [T, H_k, d] (or None) normed and rotated;
         returns (q_out, k_out), new tensors unless given (q_out=q: in place).
         The norm is taken when a weight is given or norm is True."""
+        code = _dtype_code(q)
+        raw = None if stream is not None else _raw_current(q.get_device())
+        if raw is not None:
+            return self._apply(raw, code, q, k, positions, q_weight, k_weight, eps, norm, q_out, k_out)
+        guard, raw = _on(q, stream)
+        with guard:
+            return self._apply(raw, code, q, k, positions, q_weight, k_weight, eps, norm, q_out, k_out)
+
+    def _apply(self, raw, code, q, k, positions, q_weight, k_weight, eps, norm, q_out, k_out):
         import torch
         if norm is None:
             norm = q_weight is not None or k_weight is not None
         dev, dt = q.device, q.dtype
-        code = _dtype_code(q)
-        if dev.type != "cuda" or self.turns.device != dev:
-            raise MapFlowError(MF_ERR_ARG, f"q is on {dev}, the plan on {self.turns.device}: both must be on one GPU")
+        if self.turns.device != dev:
+            raise MapFlowError(MF_ERR_ARG, f"q is on {dev}, the plan on {self.turns.device}")
         if q.dim() != 3 or (k is not None and k.dim() != 3):
             raise MapFlowError(MF_ERR_ARG, "q and k must be [T, heads, d]")
         shape_q = T, H_q, d = q.shape
         ld_q = _rows("q", q, shape_q, dt, dev)
+        if q_out is None:
+            q_out, ld_qo = torch.empty(shape_q, dtype=dt, device=dev), H_q * d
+        else:
+            ld_qo = _rows("q_out", q_out, shape_q, dt, dev)
         H_k = ld_k = ld_ko = 0
+        pk = pko = pwq = pwk = None
         if k is not None:
             H_k = k.shape[1]
             shape_k = (T, H_k, d)
             ld_k = _rows("k", k, shape_k, dt, dev)
+            if k_out is None:
+                k_out, ld_ko = torch.empty(shape_k, dtype=dt, device=dev), H_k * d
+            else:
+                ld_ko = _rows("k_out", k_out, shape_k, dt, dev)
+            pk, pko = k.data_ptr(), k_out.data_ptr()
         elif k_out is not None:
             raise MapFlowError(MF_ERR_ARG, "k_out without k")
         _vector("positions", positions, (T,), torch.int32, dev)
         if q_weight is not None:
             _vector("q_weight", q_weight, (d,), dt, dev)
+            pwq = q_weight.data_ptr()
         if k_weight is not None:
             _vector("k_weight", k_weight, (d,), dt, dev)
-        guard, raw = _on(dev, stream)
-        with guard:
-            if q_out is None:
-                q_out, ld_qo = torch.empty(shape_q, dtype=dt, device=dev), H_q * d
-            else:
-                ld_qo = _rows("q_out", q_out, shape_q, dt, dev)
-            if k is not None:
-                if k_out is None:
-                    k_out, ld_ko = torch.empty(shape_k, dtype=dt, device=dev), H_k * d
-                else:
-                    ld_ko = _rows("k_out", k_out, shape_k, dt, dev)
-            _check(load_library().mf_qk_norm_rope(
-                q.data_ptr(), ld_q, q_out.data_ptr(), ld_qo, _ptr(k), ld_k, _ptr(k_out), ld_ko, _ptr(q_weight),
-                _ptr(k_weight), norm, eps, positions.data_ptr(), self.turns.data_ptr(), self.rot_dim,
-                _LAYOUTS[self.layout], self.gain, code, T, H_q, H_k, d, raw))
+            pwk = k_weight.data_ptr()
+        rc = self._lib.mf_qk_norm_rope(
+            q.data_ptr(), ld_q, q_out.data_ptr(), ld_qo, pk, ld_k, pko, ld_ko, pwq, pwk, norm, eps,
+            positions.data_ptr(), self.turns.data_ptr(), self.rot_dim, self._layout, self.gain, code, T, H_q, H_k, d,
+            raw)
+        if rc:
+            _check(rc)
         return q_out, k_out
 
 
@@ -532,8 +544,9 @@ class _AttentionPlan:
 
     def status(self, stream=None) -> None:
         """Waits for the stream; raises if a device-side wait of a call timed out."""
-        _, raw = _on(self.device, stream)
-        _check(load_library().mf_attn_status(self.handle, raw))
+        guard, raw = _on(self.device, stream)
+        with guard:
+            _check(load_library().mf_attn_status(self.handle, raw))
 
     def close(self) -> None:
         if self.handle is not None:
@@ -554,7 +567,7 @@ class WindowAttention(_AttentionPlan):
 
     def __init__(self, cu_seqlens: Sequence[int], H_q: int, H_kv: int, d: int, window: Optional[int] = None,
                  sinks: int = 0, q_begin: Optional[Sequence[int]] = None, use_torch_allocator: bool = True):
-        lib = load_library()
+        self._lib = lib = load_library()
         if window is not None and window < 1:
             raise MapFlowError(MF_ERR_ARG, f"window = {window} must be >= 1 (None: no window)")
         cu = np.ascontiguousarray(np.asarray(cu_seqlens, dtype=np.int32))
@@ -579,24 +592,35 @@ class WindowAttention(_AttentionPlan):
     def attend(self, q, k, v, scale: Optional[float] = None, o=None, lse=None, stream=None):
         """q [T, H_q, d], k and v [T, H_kv, d] -> o [T, H_q, d] (rows before a
         q_begin are left as they are); lse: fp32 [T, H_q] to fill, or None."""
+        raw = None if stream is not None else _raw_current(self.device.index)
+        if raw is not None:
+            return self._attend(raw, q, k, v, scale, o, lse)
+        guard, raw = _on(self.device, stream)
+        with guard:
+            return self._attend(raw, q, k, v, scale, o, lse)
+
+    def _attend(self, raw, q, k, v, scale, o, lse):
         import torch
         dt, dev = torch.bfloat16, self.device
         shape_q, shape_k = (self.T, self.H_q, self.d), (self.T, self.H_kv, self.d)
         ld_q = _rows("q", q, shape_q, dt, dev)
         ld_k = _rows("k", k, shape_k, dt, dev)
         ld_v = _rows("v", v, shape_k, dt, dev)
+        if o is None:
+            o = torch.empty(shape_q, dtype=dt, device=dev)
+        ld_o = _rows("o", o, shape_q, dt, dev)
+        p_lse = p_ws = None
         if lse is not None:
             _vector("lse", lse, shape_q[:2], torch.float32, dev)
-        guard, raw = _on(dev, stream)
-        with guard:
-            if o is None:
-                o = torch.empty(shape_q, dtype=dt, device=dev)
-            ld_o = _rows("o", o, shape_q, dt, dev)
-            # a workspace of its own for every call: calls may overlap
-            ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev) if self._ws_bytes else None
-            _check(load_library().mf_attn_packed(
-                self.handle, q.data_ptr(), ld_q, k.data_ptr(), ld_k, v.data_ptr(), ld_v, o.data_ptr(), ld_o,
-                _ptr(lse), MF_DTYPE_BF16, self.d ** -0.5 if scale is None else scale, _ptr(ws), self._ws_bytes, raw))
+            p_lse = lse.data_ptr()
+        if self._ws_bytes:  # a workspace of its own for every call: calls may overlap
+            ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev)
+            p_ws = ws.data_ptr()
+        rc = self._lib.mf_attn_packed(
+            self.handle, q.data_ptr(), ld_q, k.data_ptr(), ld_k, v.data_ptr(), ld_v, o.data_ptr(), ld_o, p_lse,
+            MF_DTYPE_BF16, self.d ** -0.5 if scale is None else scale, p_ws, self._ws_bytes, raw)
+        if rc:
+            _check(rc)
         return o
 
 
@@ -609,7 +633,7 @@ class CacheAttention(_AttentionPlan):
     def __init__(self, n: int, Lq: int, capacity: int, H_q: int, H_kv: int, d: int,
                  window: Optional[int] = None, sinks: int = 0, prefix_len: int = 0,
                  use_torch_allocator: bool = True):
-        lib = load_library()
+        self._lib = lib = load_library()
         if window is not None and window < 1:
             raise MapFlowError(MF_ERR_ARG, f"window = {window} must be >= 1 (None: no window)")
         self.n, self.Lq, self.capacity, self.prefix_len = int(n), int(Lq), int(capacity), int(prefix_len)
@@ -631,6 +655,14 @@ class CacheAttention(_AttentionPlan):
         capacity, H_kv, d], lens int32 [m] on the device (keys in each cache,
         the new tokens' among them), k_prefix and v_prefix [prefix_len, H_kv,
         d] -> o [m, Lq, H_q, d]; lse: fp32 [m, Lq, H_q] to fill, or None."""
+        raw = None if stream is not None else _raw_current(self.device.index)
+        if raw is not None:
+            return self._attend(raw, q, k_cache, v_cache, lens, k_prefix, v_prefix, scale, o, lse)
+        guard, raw = _on(self.device, stream)
+        with guard:
+            return self._attend(raw, q, k_cache, v_cache, lens, k_prefix, v_prefix, scale, o, lse)
+
+    def _attend(self, raw, q, k_cache, v_cache, lens, k_prefix, v_prefix, scale, o, lse):
         import torch
         dt, dev = torch.bfloat16, self.device
         m = q.shape[0]
@@ -639,8 +671,13 @@ class CacheAttention(_AttentionPlan):
         ld_k = _rows("k_cache", k_cache, shape_k, dt, dev)
         ld_v = _rows("v_cache", v_cache, shape_k, dt, dev)
         _vector("lens", lens, (m,), torch.int32, dev)
+        if o is None:
+            o = torch.empty(shape_q, dtype=dt, device=dev)
+        ld_o = _rows("o", o, shape_q, dt, dev)
+        p_lse = p_kp = p_vp = None
         if lse is not None:
             _vector("lse", lse, shape_q[:3], torch.float32, dev)
+            p_lse = lse.data_ptr()
         ld_kp = ld_vp = 0
         if self.prefix_len:
             if k_prefix is None or v_prefix is None:
@@ -648,20 +685,19 @@ class CacheAttention(_AttentionPlan):
             shape_p = (self.prefix_len, self.H_kv, self.d)
             ld_kp = _rows("k_prefix", k_prefix, shape_p, dt, dev)
             ld_vp = _rows("v_prefix", v_prefix, shape_p, dt, dev)
+            p_kp, p_vp = k_prefix.data_ptr(), v_prefix.data_ptr()
+        elif k_prefix is not None or v_prefix is not None:
+            raise MapFlowError(MF_ERR_ARG, "the plan has no prefix")
         need = self._ws_of.get(m)
         if need is None:
             need = self._ws_of[m] = self._workspace_bytes(m)
-        guard, raw = _on(dev, stream)
-        with guard:
-            if o is None:
-                o = torch.empty(shape_q, dtype=dt, device=dev)
-            ld_o = _rows("o", o, shape_q, dt, dev)
-            # a workspace of its own for every call: calls may overlap
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-            _check(load_library().mf_attn_cached(
-                self.handle, m, q.data_ptr(), ld_q, k_cache.data_ptr(), ld_k, v_cache.data_ptr(), ld_v,
-                lens.data_ptr(), _ptr(k_prefix), ld_kp, _ptr(v_prefix), ld_vp, o.data_ptr(), ld_o, _ptr(lse),
-                MF_DTYPE_BF16, self.d ** -0.5 if scale is None else scale, ws.data_ptr(), need, raw))
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)  # its own for every call: calls may overlap
+        rc = self._lib.mf_attn_cached(
+            self.handle, m, q.data_ptr(), ld_q, k_cache.data_ptr(), ld_k, v_cache.data_ptr(), ld_v, lens.data_ptr(),
+            p_kp, ld_kp, p_vp, ld_vp, o.data_ptr(), ld_o, p_lse, MF_DTYPE_BF16,
+            self.d ** -0.5 if scale is None else scale, ws.data_ptr(), need, raw)
+        if rc:
+            _check(rc)
         return o
 
 
