@@ -238,6 +238,8 @@ int mf_qk_norm_rope(const void* q, int64_t ld_q, void* q_out, int64_t ld_qo, con
   if (norm != 0 && norm != 1) return fail(MF_ERR_ARG, "norm must be 0 or 1");
   if (norm && !(eps > 0.f && std::isfinite(eps))) return fail(MF_ERR_ARG, "eps must be positive and finite");
   if (!norm && (q_weight || k_weight)) return fail(MF_ERR_ARG, "weights without a norm");
+  if ((reinterpret_cast<uintptr_t>(q_weight) & 15) || (reinterpret_cast<uintptr_t>(k_weight) & 15))
+    return fail(MF_ERR_ARG, "weights must be 16-byte aligned");
   if (!std::isfinite(gain)) return fail(MF_ERR_ARG, "gain must be finite");
   if (T == 0) return MF_OK;
   if (!positions || !turns) return fail(MF_ERR_ARG, "positions and turns must be non-NULL");

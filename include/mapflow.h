@@ -506,7 +506,8 @@ MF_API int mf_rope_frequencies(int rot_dim, double base, int scaling, double fac
  *                     H_k = 0: no keys (k, k_out NULL)
  *   q_out, k_out      as q and k; the input itself (in place, same stride) or
  *                     memory apart from every input and the other output
- *   q_weight, k_weight  [d] (dtype) or NULL (ones); NULL when norm is 0
+ *   q_weight, k_weight  [d] (dtype, 16-byte aligned) or NULL (ones); NULL when
+ *                     norm is 0
  *   positions         int32 [T] (any value, in any order)
  *   turns             DEVICE uint64 [rot_dim/2] as mf_rope_frequencies gives it
  *   d                 64 or 128; rot_dim even, 2 .. d

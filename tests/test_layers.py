@@ -62,7 +62,7 @@ def _rope(lib, **kw):
     (dict(ld_q=511), E.MF_ERR_ARG), (dict(ld_q=516), E.MF_ERR_ARG), (dict(ld_k=248), E.MF_ERR_ARG),
     (dict(rot=0), E.MF_ERR_ARG), (dict(rot=5), E.MF_ERR_ARG), (dict(rot=130), E.MF_ERR_ARG),
     (dict(layout=2), E.MF_ERR_ARG), (dict(norm=2), E.MF_ERR_ARG), (dict(norm=1, eps=0.0), E.MF_ERR_ARG),
-    (dict(norm=1, eps=float("nan")), E.MF_ERR_ARG), (dict(wq=7 * PTR), E.MF_ERR_ARG),
+    (dict(norm=1, eps=float("nan")), E.MF_ERR_ARG), (dict(wq=7 * PTR), E.MF_ERR_ARG), (dict(wq=7 * PTR + 2, norm=1), E.MF_ERR_ARG),
     (dict(gain=float("inf")), E.MF_ERR_ARG), (dict(dtype=3), E.MF_ERR_ARG), (dict(T=-1), E.MF_ERR_ARG),
     (dict(H_q=0), E.MF_ERR_ARG), (dict(H_k=-1), E.MF_ERR_ARG), (dict(d=96), E.MF_ERR_UNSUPPORTED),
     (dict(q_out=PTR + 1024), E.MF_ERR_ARG),            # shifted over q
