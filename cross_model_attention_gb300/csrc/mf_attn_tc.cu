@@ -32,6 +32,7 @@
 // the box still reads) are zeroed in shared memory or left out of the
 // product, so what lies there, NaN included, reaches nothing.
 #include <cstdint>
+#include <type_traits>
 
 #include "mf_internal.cuh"
 #include "mf_ptx.cuh"
@@ -326,13 +327,20 @@ struct CacheRuns {
 // in which this CTA's span begins with the length before it.
 __device__ __forceinline__ void cache_find(const AttnParams& p, volatile int* misc) {
   const int lane = threadIdx.x & 31;
-  int sum = 0;
-  for (int r = lane; r < p.n; r += 32) sum += cache_line(p, cache_unit(p, p.lens[r]).nb);
+  constexpr int kKept = 8;  // the first 256 requests' lines stay in registers
+  int kept[kKept], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) {
+    const int r = 32 * i + lane;
+    kept[i] = r < p.n ? cache_line(p, cache_unit(p, p.lens[r]).nb) : 0;
+    sum += kept[i];
+  }
+  for (int r = 32 * kKept + lane; r < p.n; r += 32) sum += cache_line(p, cache_unit(p, p.lens[r]).nb);
   sum = __reduce_add_sync(0xffffffffu, sum);
   const int f0 = min(sum, span_of(p, sum) * static_cast<int>(gridDim.x - 1 - blockIdx.x));
   int first = p.n, before = sum, run = 0;
-  for (int r0 = 0; r0 < p.n; r0 += 32) {
-    const int line = r0 + lane < p.n ? cache_line(p, cache_unit(p, p.lens[r0 + lane]).nb) : 0;
+  bool found = false;
+  auto look = [&](int r0, int line) {  // requests r0 .. r0 + 31
     int inc = line;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -344,10 +352,15 @@ __device__ __forceinline__ void cache_find(const AttnParams& p, volatile int* mi
       const int l = __ffs(hit) - 1;
       first = r0 + l;
       before = run + __shfl_sync(0xffffffffu, inc - line, l);
-      break;
+      found = true;
     }
     run += __shfl_sync(0xffffffffu, inc, 31);
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < kKept; ++i)
+    if (!found && 32 * i < p.n) look(32 * i, kept[i]);
+  for (int r0 = 32 * kKept; !found && r0 < p.n; r0 += 32)
+    look(r0, r0 + lane < p.n ? cache_line(p, cache_unit(p, p.lens[r0 + lane]).nb) : 0);
   if (lane == 0) {
     misc[2] = first;
     misc[4] = before;
@@ -391,6 +404,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto barEmpty = [&](int i) { return sb + L::kBar + 128 + 8u * (NS + i); };
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up
+  if (threadIdx.x == 9 * 32) {
+    prefetch_tmap(&tk);
+    prefetch_tmap(&tv);
+    prefetch_tmap(&tq);
+    if (cached) {
+      prefetch_tmap(&tqc);
+      if (p.P > 0) {
+        prefetch_tmap(&tkp);
+        prefetch_tmap(&tvp);
+      }
+    }
+  }
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(barQFull(t), 1);
@@ -947,34 +972,35 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p, const Att
   };
   const int n = n0 + n1;
   float top = -INFINITY, l = 0.f, acc[V] = {};
-  for (int b = 0; b < n; b += 32) {  // 32 partial results at a time, one per lane
-    const float2 ml = b + lane < n ? p.part_ml[at(b + lane)] : make_float2(-INFINITY, 0.f);
+  constexpr int kAtOnce = 16;  // results of o asked for together, before their weights are known
+  using Vec = typename std::conditional<V == 4, float4, float2>::type;
+  for (int b = 0; b < n; b += kAtOnce) {
+    const int m = min(kAtOnce, n - b);
+    const float2 ml = lane < m ? p.part_ml[at(b + lane)] : make_float2(-INFINITY, 0.f);
+    Vec v[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      if (i < m) v[i] = *reinterpret_cast<const Vec*>(p.part_o + at(b + i) * D + lane * V);
     float mx = ml.x;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    for (int o = kAtOnce / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o, kAtOnce));
+    mx = __shfl_sync(0xffffffffu, mx, 0);
     const float was = top;
     top = fmaxf(top, mx);
     const float f = was == -INFINITY ? 0.f : ex2(was - top);
-    // (one that saw nothing has weight 0; its o was perhaps not written)
     const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-    float add = w == 0.f ? 0.f : w * ml.y;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) add += __shfl_xor_sync(0xffffffffu, add, o);
-    l = l * f + add;
+    l *= f;
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[e] *= f;
-    const int m = min(32, n - b);
-#pragma unroll 8
-    for (int i = 0; i < m; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      if (wi == 0.f) continue;
-      const float* src = p.part_o + at(b + i) * D + lane * V;
-      if (V == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        acc[0] += wi * v.x, acc[1] += wi * v.y, acc[V - 2] += wi * v.z, acc[V - 1] += wi * v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        acc[0] += wi * v.x, acc[1] += wi * v.y;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i), li = __shfl_sync(0xffffffffu, ml.y, i);
+      // (one that saw nothing has weight 0; its o was perhaps not written)
+      if (i < m && wi != 0.f) {
+        l += wi * li;
+        const float* x = reinterpret_cast<const float*>(&v[i]);
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] += wi * x[e];
       }
     }
   }
