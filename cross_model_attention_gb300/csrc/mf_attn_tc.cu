@@ -75,6 +75,12 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// 32 bytes to a 32-byte aligned address: a lane's whole sector.
+__device__ __forceinline__ void st_global_v8(void* ptr, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(ptr), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -706,6 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tok_c = tok_1 / p.HG, hh_c = tok_1 - tok_c * p.HG;
     const float sc = p.scale * 1.4426950408889634f;
     const float slack = 8.f / sc;
+    const bool wide = ((reinterpret_cast<uintptr_t>(p.o) | static_cast<uintptr_t>(p.ld_o * 2)) & 31) == 0;
     uint32_t ph = 0, o_ph = 0;  // phases of both halves' S, and of the runs' last products
     int ring = 0;     // ring uses before this run
     bool ok = true;
@@ -871,15 +878,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t w[32];
           tmem_ld32(colO + c, w);
           tc_wait_ld();
+          uint32_t y[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            y[e / 2] = inv == 0.f ? 0u : pack_bf16x2(__uint_as_float(w[e]) * inv, __uint_as_float(w[e + 1]) * inv);
           if (mine) {
+            // (a lane writes its own row: whole sectors where the rows allow it)
+            if (wide) {
+              st_global_v8(dst + c, y);
+              st_global_v8(dst + c + 16, y + 8);
+            } else {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              float f[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) f[i] = inv == 0.f ? 0.f : __uint_as_float(w[e + i]) * inv;
-              *reinterpret_cast<uint4*>(dst + c + e) =
-                  make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                             pack_bf16x2(f[6], f[7]));
+              for (int e = 0; e < 16; e += 4)
+                *reinterpret_cast<uint4*>(dst + c + 2 * e) = make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
             }
           }
         }
@@ -900,8 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_wait_ld();
             if (mine) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+              for (int e = 0; e < 32; e += 8) st_global_v8(dst + c + e, w + e);
             }
           }
         }
