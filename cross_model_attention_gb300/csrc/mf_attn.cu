@@ -139,7 +139,7 @@ int finish_handle(mf_attn_t h, mf_attn_t* out, const std::vector<AttnSeg>& segs,
 // Cache form: partial results a row can have, and the workspace's parts.
 struct CacheLayout {
   int np_pre, np_suf, pairs, nbp;
-  size_t n_part, ml, o, bytes;
+  size_t cuts, ml, o, bytes;
 };
 CacheLayout cache_layout(const mf_attn_s* h, int n) {
   CacheLayout c{};
@@ -163,8 +163,8 @@ CacheLayout cache_layout(const mf_attn_s* h, int n) {
   c.np_suf = 2 * ((int)(nbs * h->HG / span_suf) + 3);
   const size_t rows = (size_t)toks * h->H_q;
   const size_t np = (size_t)c.np_pre + c.np_suf;
-  c.n_part = 0;
-  c.ml = up256(((size_t)c.pairs * h->H_kv + (size_t)n * h->groups) * sizeof(int));
+  c.cuts = 0;
+  c.ml = up256(((size_t)c.pairs * h->H_kv + (size_t)n * h->groups) * sizeof(int2));
   c.o = c.ml + up256(np * rows * sizeof(float2));
   c.bytes = c.o + up256(np * rows * h->d * sizeof(float));
   return c;
@@ -329,9 +329,10 @@ int mf_attn_create_packed(mf_attn_t* out, const int32_t* cu_seqlens_host, const 
     return cuda_fail(ce, "device query");
   }
   std::vector<AttnSeg> items, segs;
-  std::vector<int> cta(h->grid + 1, 0);
+  std::vector<int> cta;
   std::vector<AttnJoin> joins;
   try {
+    cta.assign(h->grid + 1, 0);
     for (int s = 0; s < n_seqs; ++s) {
       const int start = cu_seqlens_host[s], len = cu_seqlens_host[s + 1] - start;
       for (int head = 0; head < H_kv; ++head)
@@ -350,18 +351,20 @@ int mf_attn_create_packed(mf_attn_t* out, const int32_t* cu_seqlens_host, const 
         }
     }
     // Whole runs, the longest first, each to the CTA with the least work so
-    // far (a run costs its blocks and about two more for its start and end).
+    // far; a run costs its blocks and about two more for its start and end.
     // Where that leaves CTAs uneven (few query rows over many keys), the runs
-    // are laid end to end instead and cut into equal spans; a cut run's
-    // pieces write partial results that a second kernel joins.
+    // are laid end to end instead and cut into equal spans; a cut run's pieces
+    // write partial results that a second kernel joins, which costs about as
+    // much as five blocks.  (32q/8kv heads of 128, whole against cut: one row
+    // over 1000 keys 14.6 / 10.1 us, 64 rows over 700 16.6 / 21 us, 128 rows
+    // over 1500 26.8 / 17.3 us, a 1024-token prompt 20.4 / 34 us.)
     const int n = (int)items.size(), grid = h->grid;
+    constexpr int kRun = 2, kJoin = 5;
     std::vector<int> order(n);
     long long total = 0;
-    int longest = 0;
     for (int i = 0; i < n; ++i) {
       order[i] = i;
-      total += items[i].blk1;
-      longest = std::max(longest, items[i].blk1);
+      total += items[i].blk1 + kRun;
     }
     std::stable_sort(order.begin(), order.end(), [&](int a, int b) { return items[a].blk1 > items[b].blk1; });
     using Slot = std::pair<long long, int>;
@@ -373,30 +376,30 @@ int mf_attn_create_packed(mf_attn_t* out, const int32_t* cu_seqlens_host, const 
       Slot x = least.top();
       least.pop();
       mine[x.second].push_back(i);
-      x.first += items[i].blk1 + 2;
+      x.first += items[i].blk1 + kRun;
       makespan = std::max(makespan, x.first);
       least.push(x);
     }
-    const long long even = (total + 2ll * n + grid - 1) / grid;
-    if (longest <= 8 || makespan * 100 <= even * 115) {
+    const long long span = std::max<long long>(kRun + 2, (total + grid - 1) / grid);
+    if (makespan <= span + kJoin) {
       for (int c = 0; c < grid; ++c) {
         cta[c] = (int)segs.size();
         for (int i : mine[c]) segs.push_back(items[i]);
       }
       cta[grid] = (int)segs.size();
     } else {
-      const long long per = std::max<long long>(4, (total + grid - 1) / grid);
-      long long at = 0;  // blocks before item i
+      // block b of an item lies at place at + kRun + b, in CTA place / span
+      long long at = 0;
       int c = 0;
       for (int i = 0; i < n; ++i) {
         const int nb = items[i].blk1;
-        const long long first_cut = (at / per + 1) * per - at;  // blocks of this item in its first CTA
-        const bool cut = first_cut < nb;
+        const long long begin = at + kRun;
+        const bool cut = begin / span != (begin + nb - 1) / span;
         const int slot0 = h->n_slots;
         int pieces = 0;
         for (long long b = 0; b < nb;) {
-          const long long who = (at + b) / per;
-          const long long upto = std::min<long long>(nb, (who + 1) * per - at);
+          const long long who = (begin + b) / span;
+          const long long upto = std::min<long long>(nb, (who + 1) * span - begin);
           while (c < who) cta[++c] = (int)segs.size();
           AttnSeg a = items[i];
           a.blk0 = (int)b;
@@ -417,7 +420,7 @@ int mf_attn_create_packed(mf_attn_t* out, const int32_t* cu_seqlens_host, const 
             joins.push_back(AttnJoin{a.q_row, n0, a.head, 2 * slot0, 2 * pieces, 1});
           }
         }
-        at += nb;
+        at = begin + nb;
       }
       while (c < grid) cta[++c] = (int)segs.size();
     }
@@ -621,7 +624,7 @@ int mf_attn_cached(mf_attn_t h, int n, const void* q, int64_t ld_q, const void* 
   p.np_suf = c.np_suf;
   p.min_span = kMinSpan;
   char* ws = static_cast<char*>(workspace);
-  p.n_part = reinterpret_cast<int*>(ws + c.n_part);
+  p.cuts = reinterpret_cast<int2*>(ws + c.cuts);
   p.part_ml = reinterpret_cast<float2*>(ws + c.ml);
   p.part_o = reinterpret_cast<float*>(ws + c.o);
   p.part_rows = rows * h->H_q;

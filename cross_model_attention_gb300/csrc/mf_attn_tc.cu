@@ -313,7 +313,8 @@ struct CacheRuns {
         const int step = o.alt ? 2 : 1;
         const int piece = min(max(f0 / per - begins / per, 0), most / step - 1);
         o.part = (pre ? 0 : p.np_pre) + piece * step;
-        if (o.blk1 == nb && threadIdx.x == 0) p.n_part[unit] = piece + 1;
+        // where its blocks lie, for the join: block j is in piece (x + j) / y
+        if (o.blk1 == nb && threadIdx.x == 0) p.cuts[unit] = make_int2(begins % per, per);
       }
       // the next unit
       if (nb > 0) at = begins + nb;
@@ -949,20 +950,27 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p, const Att
     q_tok = w / p.H_q;
     head = static_cast<int>(w - q_tok * p.H_q);
     const int kv = head / p.G, req = static_cast<int>(q_tok / p.Lq);
-    n0 = 0;
     base0 = 0;
     step0 = 1;
+    n0 = 0;
     // (counts are held to what the buffers have, whatever a failed run left)
     if (p.pre_pairs > 0) {
       const int pair = static_cast<int>(q_tok / (2 * p.TQ));
-      n0 = p.n_part[pair * p.H_kv + kv];
+      const int2 cut = p.cuts[pair * p.H_kv + kv];
+      n0 = (cut.x + p.pre_blocks - 1) / cut.y + 1;
       // a lone last tile ran on both streams
       if (2ll * pair * p.TQ + p.TQ >= static_cast<long long>(p.n) * p.Lq) n0 *= 2;
       n0 = min(max(n0, 0), p.np_pre);
     }
+    const int nb = cache_unit(p, p.lens[req]).nb;
     base1 = p.np_pre;
-    if (cache_unit(p, p.lens[req]).nb > 0)
-      n1 = min(max(2 * p.n_part[p.pre_pairs * p.H_kv + req * p.groups + kv / p.HG], 0), p.np_suf);
+    if (nb > 0) {  // the pieces with blocks of the row's head
+      const int2 cut = p.cuts[p.pre_pairs * p.H_kv + req * p.groups + kv / p.HG];
+      const int at = cut.x + kv % p.HG * nb;
+      const int first = min(max(2 * (at / cut.y), 0), p.np_suf);
+      base1 += first;
+      n1 = min(max(2 * ((at + nb - 1) / cut.y) + 2 - first, 0), p.np_suf - first);
+    }
   } else {
     const long long j = w / kRows;
     if (j >= n_joins) return;

@@ -239,7 +239,7 @@ struct AttnParams {
   int HG, groups;            // caches: KV heads per tile, tiles per request
   int np_pre, np_suf;        // partial results a row can have from each
   int min_span;              // least work per CTA, in blocks
-  int* n_part;               // [units] runs of each unit, written by its last run
+  int2* cuts;                // [units] how a unit's blocks are cut, written by its last run
   // partial results
   float* part_o;             // [partial][part_rows][d], not normalised
   float2* part_ml;           // [partial][part_rows]: reference (log2 units), sum
