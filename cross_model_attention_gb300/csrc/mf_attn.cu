@@ -42,7 +42,10 @@ struct mf_attn_s {
 namespace {
 
 constexpr int kBlock = 128;     // keys per block of the kernel
-constexpr int kMinSpan = 2;     // cache form: least key blocks per CTA (one for each stream)
+// Cache form: least key blocks per CTA, one for each stream.  (One request of
+// 1024 keys 14.9 us, with four blocks 16.1; two requests over a prefix of 1000
+// 13.9 / 17.1 / with one block 15.6 us.)
+constexpr int kMinSpan = 2;
 constexpr int kMaxTokens = kAttnFar;
 
 void* h_alloc(mf_attn_t h, size_t bytes) {
@@ -356,8 +359,8 @@ int mf_attn_create_packed(mf_attn_t* out, const int32_t* cu_seqlens_host, const 
     // are laid end to end instead and cut into equal spans; a cut run's pieces
     // write partial results that a second kernel joins, which costs about as
     // much as five blocks.  (32q/8kv heads of 128, whole against cut: one row
-    // over 1000 keys 14.6 / 10.1 us, 64 rows over 700 16.6 / 21 us, 128 rows
-    // over 1500 26.8 / 17.3 us, a 1024-token prompt 20.4 / 34 us.)
+    // over 1000 keys 14.6 / 10.0 us, 64 rows over 700 16.4 / 17.5 us, 128 rows
+    // over 1500 26.8 / 19.8 us, a 1024-token prompt 20.2 / 33 us.)
     const int n = (int)items.size(), grid = h->grid;
     constexpr int kRun = 2, kJoin = 5;
     std::vector<int> order(n);

@@ -199,7 +199,13 @@ struct PackedRuns {
 // one per CTA, and the caches' lines likewise, so that uneven lengths balance
 // and a unit is cut only where a span ends; a block belongs to the span in
 // which it begins.  Every second CTA takes its caches' span first: the
-// prefix's products and the caches' loads then overlap.
+// prefix's products and the caches' loads then overlap.  Where a CTA's share
+// of both is at most kApart blocks, a second run's start and end costs more
+// than that brings: the spans are then as long as the shares together, and
+// prefix and caches meet from the two ends of the CTAs.  (32q/8kv heads of
+// 128, together against apart: 16 requests of 200 over 4096 26.2 / 20.9 us, 64
+// of 512 over 16384 58 / 53 us, 300 of 600 over 4096 134 / 140 us, 200 with two
+// new tokens each of 700 over 32768 272 / 278 us.)
 struct Unit {
   int a1, b0, b1, nb;  // key ranges of a request's cache, in blocks
 };
@@ -219,8 +225,16 @@ constexpr int kCostPre = kAttnCostPre, kCostCache = kAttnCostCache;  // a run's 
 __device__ __forceinline__ int cache_line(const AttnParams& p, int nb) {
   return nb > 0 ? p.groups * kCostCache + nb * p.H_kv : 0;
 }
-__device__ __forceinline__ int span_of(const AttnParams& p, int total) {
-  return max(p.min_span, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+constexpr int kApart = 32;
+__device__ __forceinline__ int pre_lines(const AttnParams& p) {
+  return p.pre_pairs * p.H_kv * (kCostPre + p.pre_blocks);
+}
+// length of the spans of the prefix's lines or of the caches' (`suffix` long)
+__device__ __forceinline__ int span_of(const AttnParams& p, bool pre, int suffix) {
+  const int grid = static_cast<int>(gridDim.x), first = pre_lines(p);
+  const int both = (first + suffix + grid - 1) / grid;
+  const int own = ((pre ? first : suffix) + grid - 1) / grid;
+  return max(p.min_span, both <= kApart ? both : own);
 }
 
 struct CacheRuns {
@@ -243,8 +257,8 @@ struct CacheRuns {
   }
   __device__ int pre_line() const { return kCostPre + p.pre_blocks; }
   __device__ void begin() {
-    const int total = pre ? p.pre_pairs * p.H_kv * pre_line() : suf_total;
-    per = span_of(p, total);
+    const int total = pre ? pre_lines(p) : suf_total;
+    per = span_of(p, pre, suf_total);
     // (from the other end of the CTAs: two short lists meet late)
     f0 = min(total, per * static_cast<int>(pre ? blockIdx.x : gridDim.x - 1 - blockIdx.x));
     f1 = min(total, f0 + per);
@@ -344,7 +358,7 @@ __device__ __forceinline__ void cache_find(const AttnParams& p, volatile int* mi
   }
   for (int r = 32 * kKept + lane; r < p.n; r += 32) sum += cache_line(p, cache_unit(p, p.lens[r]).nb);
   sum = __reduce_add_sync(0xffffffffu, sum);
-  const int f0 = min(sum, span_of(p, sum) * static_cast<int>(gridDim.x - 1 - blockIdx.x));
+  const int f0 = min(sum, span_of(p, false, sum) * static_cast<int>(gridDim.x - 1 - blockIdx.x));
   int first = p.n, before = sum, run = 0;
   bool found = false;
   auto look = [&](int r0, int line) {  // requests r0 .. r0 + 31

@@ -94,6 +94,20 @@ def test_rope_in_place_and_strided_out(rot, layout):
     assert torch.equal(q, qo) and torch.equal(k, ko)
 
 
+def test_rope_of_no_tokens_and_other_streams_tables():
+    plan = mapflow.RotaryPlan(128)
+    q = torch.empty(0, 4, 128, dtype=BF, device="cuda")
+    qo, ko = plan.apply(q, q[:, :2], torch.empty(0, dtype=torch.int32, device="cuda"), norm=True)
+    assert qo.shape == (0, 4, 128) and ko.shape == (0, 2, 128)
+
+
+def test_rope_many_tokens_uneven_heads():
+    # several heads to a group, shares of q and k that do not divide evenly
+    check_rope(9001, 40, 8, 64, 64, "half", BF, True, seed=2)
+    check_rope(9001, 7, 3, 128, 96, "interleaved", torch.float32, True, seed=3)
+    check_rope(3001, 13, 40, 128, 20, "half", BF, True, seed=4)
+
+
 def test_rope_refuses_overlap_and_wrong_tensors():
     plan = mapflow.RotaryPlan(64)
     buf = rnd(0, 20, 4, 64)
@@ -165,6 +179,26 @@ def test_packed_many_heads_and_long():
 def test_packed_chunks(lens, begin, H_q, H_kv, window, sinks):
     check_packed(lens, H_q, H_kv, 128, window, sinks, begin=begin)
     check_packed(lens, H_q, H_kv, 64, window, sinks, begin=begin, seed=9)
+
+
+def test_packed_rows_16_bytes_off_a_sector():
+    T, H_q, H_kv, d = 300, 4, 2, 64
+    q, k, v = rnd(0, T, H_q, d), rnd(1, T, H_kv, d), rnd(2, T, H_kv, d)
+    plan = mapflow.WindowAttention([0, T], H_q, H_kv, d)
+    want = plan.attend(q, k, v)
+    wide = torch.zeros(T, H_q * d + 8, dtype=BF, device="cuda")
+    o = wide[:, 8:].view(T, H_q, d)
+    plan.attend(q, k, v, o=o)
+    assert torch.equal(o, want) and (wide[:, :8] == 0).all()
+
+
+def test_packed_mixed_runs():
+    # pairs, lone tiles whole and cut, and a long chunk in one plan
+    lens = [3000, 20, 500, 1, 9000, 64, 0, 129]
+    begin = [0, 0, 490, 0, 8990, 0, 0, 1]
+    for d in (64, 128):
+        check_packed(lens, 8, 2, d, None, 0, begin=begin, seed=d)
+        check_packed(lens, 6, 2, d, 700, 9, begin=begin, seed=d + 1)
 
 
 def test_packed_large_scores_and_scale():
@@ -270,6 +304,28 @@ def test_cache(lens, Lq, cap, H_q, H_kv, d, window, sinks):
 ])
 def test_shared_prefix(lens, Lq, cap, H_q, H_kv, d, P):
     check_cache(lens, Lq, cap, H_q, H_kv, d, P=P)
+
+
+def test_cache_long_runs():
+    # tens of key blocks per CTA, the ring's stages used many times over
+    check_cache([9000, 20000, 1, 15000], 1, 20000, 32, 8, 128)
+    check_cache([20000, 3, 15000], 1, 20000, 16, 8, 64)
+    check_cache([12000] * 12, 2, 12000, 8, 8, 128, 5000, 130)
+
+
+def test_cache_many_requests_and_head_groups():
+    rng = np.random.default_rng(0)
+    check_cache([int(x) for x in rng.integers(0, 41, 600)], 1, 40, 4, 2, 64)
+    check_cache([int(x) for x in rng.integers(0, 300, 40)], 4, 300, 40, 40, 128)      # 3 heads to a tile, 14 tiles
+    check_cache([int(x) for x in rng.integers(0, 300, 30)], 3, 300, 44, 11, 64, 100, 7)  # last tile part full
+    check_cache([int(x) for x in rng.integers(0, 500, 300)], 1, 500, 24, 8, 128, P=2000)
+    check_cache([100, 0, 33], 1, 128, 1024, 1024, 64)
+
+
+@pytest.mark.parametrize("n,P", [(1, 20000), (3, 9000), (70, 9000)])
+def test_prefix_and_long_caches(n, P):
+    rng = np.random.default_rng(n)
+    check_cache([int(x) for x in rng.integers(1, 3000, n)], 1, 3000, 32, 8, 128, P=P)
 
 
 def test_cache_fewer_requests_than_planned_and_garbage():
