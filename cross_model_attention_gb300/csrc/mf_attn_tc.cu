@@ -839,7 +839,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             if (!rescale) f = 1.f;
-#pragma unroll
+// (rolled up: rare, and the loop it sits in has to stay small in the
+            // instruction cache: unrolled, a causal 8192-token prompt takes 393 us,
+            // so 378)
+#pragma unroll 1
             for (int c = 0; c < D; c += 16) {
               uint32_t w[16];
               tmem_ld16(colO + c, w);
@@ -1049,9 +1052,19 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p, const Att
 
 // The join kernel may be set up while the attention kernel before it in the
 // stream runs (it waits for its end on the device).
-cudaError_t launch_dependent(void (*kern)(const AttnParams, const AttnJoin*, int), int grid, cudaStream_t s,
+template <int D, bool CACHED>
+cudaError_t launch_dependent(int grid, cudaStream_t s,
                              const AttnParams& p, const AttnJoin* joins, int n_joins) {
   cudaLaunchAttribute at{};
+  // (the attention kernel takes nearly all of an SM's memory as shared memory;
+  // a kernel that wants another split beside it makes the SMs change over, twice
+  // per call)
+  auto kern = join_kernel<D, CACHED>;
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = once_per_device(done, [&] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  });
+  if (e != cudaSuccess) return e;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
@@ -1069,7 +1082,9 @@ cudaError_t launch_main(const AttnParams& p, int grid, const CUtensorMap& tq, co
                         const CUtensorMap& tqc, bool cached, cudaStream_t s) {
   auto kern = attn_kernel<D, Runs>;
   static std::atomic<unsigned long long> done{0};
-  cudaError_t e = allow_smem(kern, Lay<D>::kBytes, done);
+  cudaError_t e = once_per_device(done, [&] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kBytes);
+  });
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, Lay<D>::kBytes, s>>>(tq, tk, tv, tkp, tvp, tqc, p, cached);
   return cudaGetLastError();
@@ -1086,8 +1101,8 @@ cudaError_t launch_attn_packed(const AttnParams& p, int d, int grid, const CUten
 cudaError_t launch_attn_join(const AttnParams& p, int d, const AttnJoin* joins, int n_joins, cudaStream_t s) {
   if (n_joins <= 0) return cudaSuccess;
   const int grid = n_joins * (kRows / 8);
-  return d == 128 ? launch_dependent(join_kernel<128, false>, grid, s, p, joins, n_joins)
-                  : launch_dependent(join_kernel<64, false>, grid, s, p, joins, n_joins);
+  return d == 128 ? launch_dependent<128, false>(grid, s, p, joins, n_joins)
+                  : launch_dependent<64, false>(grid, s, p, joins, n_joins);
 }
 
 cudaError_t launch_attn_cache(const AttnParams& p, int d, int grid, const CUtensorMap& tq,
@@ -1098,8 +1113,8 @@ cudaError_t launch_attn_cache(const AttnParams& p, int d, int grid, const CUtens
   if (e != cudaSuccess) return e;
   const long long blocks = (p.part_rows + 7) / 8;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  return d == 128 ? launch_dependent(join_kernel<128, true>, static_cast<int>(blocks), s, p, nullptr, 0)
-                  : launch_dependent(join_kernel<64, true>, static_cast<int>(blocks), s, p, nullptr, 0);
+  return d == 128 ? launch_dependent<128, true>(static_cast<int>(blocks), s, p, nullptr, 0)
+                  : launch_dependent<64, true>(static_cast<int>(blocks), s, p, nullptr, 0);
 }
 
 }  // namespace mf

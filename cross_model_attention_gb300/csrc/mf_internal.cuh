@@ -98,16 +98,16 @@ inline cudaError_t sm_count(int* out) {
   return cudaSuccess;
 }
 
-// Raises a kernel's dynamic shared-memory limit, once per device; `done` is a
-// static of the caller, one per kernel.
-template <typename K>
-cudaError_t allow_smem(K kern, int bytes, std::atomic<unsigned long long>& done) {
+// Calls `set` (a kernel's attribute) once per device; `done` is a static of
+// the caller, one per kernel.
+template <typename F>
+cudaError_t once_per_device(std::atomic<unsigned long long>& done, F&& set) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (done.load(std::memory_order_acquire) >> dev & 1ull) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  e = set();
   if (e == cudaSuccess) done.fetch_or(1ull << dev, std::memory_order_release);
   return e;
 }
