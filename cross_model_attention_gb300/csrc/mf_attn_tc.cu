@@ -112,9 +112,9 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
 }
 
 // Waits of a whole, converged warp; false (in every lane) after the time limit
-// or where another role has given up.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* err, const volatile int* misc) {
-  if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+// or where another role has given up.  The roles' loops share the instruction
+// caches, so what is rare stays out of them.
+__device__ __noinline__ bool warp_wait_on(uint32_t bar, uint32_t parity, int* err, const volatile int* misc) {
   const unsigned long long t0 = globaltimer();
   for (uint32_t it = 1;; ++it) {
     if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
@@ -126,6 +126,24 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* er
       }
     }
   }
+}
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* err, const volatile int* misc) {
+  if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+  return warp_wait_on(bar, parity, err, misc);
+}
+// V rows past the block's last key, up to the next multiple of 16, become
+// zero: their weights are zero, but what the box read there may be NaN.  By a
+// warp; both streams' may do so to a shared block: they write the same.
+template <int D>
+__device__ __noinline__ void trim(uint8_t* stage, int valid) {
+  const int n = (((valid + 15) & ~15) - valid) * 8;
+  for (int i = threadIdx.x & 31; i < n * (D / 64); i += 32) {
+    const int c = i / n, x = i - c * n;
+    *reinterpret_cast<uint4*>(stage + c * Lay<D>::kChunk + valid * 128 + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_async_smem();
+  __syncwarp();
 }
 
 // -------------------------------------------------------------------- runs --
@@ -158,6 +176,7 @@ __device__ __forceinline__ void block_at(const Run& r, int j, int& hh, int& j0, 
 
 // The runs of this CTA in order, packed form: from the plan's table.
 struct PackedRuns {
+  static constexpr int kUnrollHalves = 1;
   const AttnParams& p;
   int i, end;
   AttnSeg nxt;
@@ -238,6 +257,7 @@ __device__ __forceinline__ int span_of(const AttnParams& p, bool pre, int suffix
 }
 
 struct CacheRuns {
+  static constexpr int kUnrollHalves = 2;
   const AttnParams& p;
   int todo;                  // parts left: 2, 1, 0
   bool pre;                  // the part at hand is the prefix
@@ -471,27 +491,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   Runs runs(p, misc);
   Run r{};
   // Who waits for the ring.  A barrier's phase is told from the one before it
-  // only, so whoever waits for a stage's use must know the use before it to be
-  // done, and no use may pass unseen.  The streams' MMA warps see every use in
-  // turn, the other stream's too, and a stage is free when both have said so.
-  // In a pair run that is the products' critical path (every wait costs it
-  // ~0.1 us), so from block kLean on, when each stage's earlier use is one of
-  // this run's, a softmax warp waits instead and the block's P says that V and
-  // the next K have landed.
-  constexpr int kLean = NS / 2;
-  // V rows past the block's last key, up to the next multiple of 16, become
-  // zero: their weights are zero, but what the box read there may be NaN
-  // (both streams may do so to a shared block: they write the same)
-  auto trim = [&](int st, int valid) {
-    const int n = ((valid + 15) & ~15) - valid;
-    for (int i = lane; i < n * 8 * (D / 64); i += 32) {
-      const int c = i / (n * 8), x = i - c * n * 8;
-      *reinterpret_cast<uint4*>(smem + L::kRing + st * L::kTile + c * L::kChunk + valid * 128 + x * 16) =
-          make_uint4(0u, 0u, 0u, 0u);
-    }
-    fence_async_smem();
-    __syncwarp();
-  };
+  // only, so no use of a stage may pass unseen: both streams' MMA warps see
+  // every use in turn, the other stream's too, and a stage is free when both
+  // have said so.
 
   if (warp == 9) {
     // ------------------------------------------------------------- loader
@@ -558,6 +560,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 8 || warp == 10) {
     // ------------------------------------------- MMA, one warp per stream
     const int s = warp == 8 ? 0 : 1;
+    // (code of the issuing loop, one half after the other or both laid out: a
+    // causal 8192-token prompt 370 / 399 us, 200 requests over a 32k prefix 223 /
+    // 208 us)
+    constexpr int kUnrollHalves = Runs::kUnrollHalves;
     constexpr uint32_t idS = idesc_bf16_f32(kRows, kHalf, false, false);
     constexpr uint32_t idO = idesc_bf16_f32(kRows, D, false, true);
     const uint64_t q_desc = sdesc_sw128(sb + L::kQ, 16, 1024);             // K-major
@@ -640,6 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         if (mine(i)) {
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             qk(h, tile, kst);
             if (lane == 0) tc_commit(barS(s, h));
@@ -656,13 +663,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       for (int i = 0; ok && i < nb; ++i) {
-        const bool lean = on && !alt && i >= kLean;
         const uint32_t vph = ring_ph;
         const int vst = pass();
         const bool more = i + ahead < nb;
         const uint32_t kph = ring_ph;
         const int kst = more ? pass() : 0;
-        if (!lean && !warp_wait(barFull(vst), vph, p.err, misc)) {
+        if (!warp_wait(barFull(vst), vph, p.err, misc)) {
           ok = false;
           break;
         }
@@ -681,13 +687,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         int hh, j0, valid;
         block_at(r, r.blk0 + i, hh, j0, valid);
         valid = uniform(valid);
-        if (!lean && (valid & 15)) trim(vst, valid);
+        if (valid & 15) trim<D>(smem + L::kRing + vst * L::kTile, valid);
         const int steps = (valid + 15) >> 4;
-#pragma unroll
+#pragma unroll kUnrollHalves
         for (int h = 0; h < 2; ++h) {
           pv(h, vst, min(4, max(0, steps - 4 * h)), i < ahead && h == 0);
           if (!ok) break;
-          if (more && !lean && h == 0 && !warp_wait(barFull(kst), kph, p.err, misc)) {
+          if (more && h == 0 && !warp_wait(barFull(kst), kph, p.err, misc)) {
             ok = false;
             break;
           }
@@ -729,15 +735,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float slack = 8.f / sc;
     const bool wide = ((reinterpret_cast<uintptr_t>(p.o) | static_cast<uintptr_t>(p.ld_o * 2)) & 31) == 0;
     uint32_t ph = 0, o_ph = 0;  // phases of both halves' S, and of the runs' last products
-    int ring = 0;     // ring uses before this run
     bool ok = true;
-    const bool keeper = (warp & 3) == 0;  // the stream's warp that minds the ring
     while (ok && runs.next(r)) {
       const int tile = r.alt ? 0 : s;
-      // (a pair run uses the ring for K of its first block, then V of each block
-      // and K of the next)
-      const int ring0 = ring;
-      ring += 2 * (r.blk1 - r.blk0);
       if (!r.alt && s == 1 && r.n_tok1 == 0) continue;
       const int n_tok = tile ? r.n_tok1 : r.n_tok0;
       const bool cache = r.kind == kCache, prefix = r.kind == kPrefix;
@@ -764,16 +764,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!warp_wait(barS(s, h), ph, p.err, misc)) {
             ok = false;
             break;
-          }
-          if (keeper && h == 0 && !r.alt && b - r.blk0 >= kLean) {
-            // V of this block and K of the next are here before its P says so
-            const int vu = ring0 + 1 + 2 * (b - r.blk0), ku = b + 1 < r.blk1 ? vu + 1 : vu;
-            if (!warp_wait(barFull(vu % NS), (vu / NS) & 1, p.err, misc) ||
-                !warp_wait(barFull(ku % NS), (ku / NS) & 1, p.err, misc)) {
-              ok = false;
-              break;
-            }
-            if (valid & 15) trim(vu % NS, valid);
           }
           if (idle) {
             if (lane == 0) mbar_arrive(barP(s, h));
@@ -839,9 +829,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             if (!rescale) f = 1.f;
-// (rolled up: rare, and the loop it sits in has to stay small in the
-            // instruction cache: unrolled, a causal 8192-token prompt takes 393 us,
-            // so 378)
+            // (rolled up: rare, and the loop it sits in has to stay small in the
+            // instruction cache; unrolled, a causal 8192-token prompt takes 15 us
+            // more)
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
               uint32_t w[16];
