@@ -543,10 +543,12 @@ typedef struct mf_attn_s* mf_attn_t; /* opaque; a plan for attention calls */
  * (MF_ERR_UNSUPPORTED otherwise).  A row that sees no key gets o = 0 and
  * lse = -inf.
  *
- * A value that is not finite in a key or value row spreads to the rows that
- * see it, and a value row may reach others of its sequence within the same
- * 128-key block; rows past a sequence's or a cache's end, and other requests'
- * rows, reach nothing.
+ * What is not finite in a key or value row reaches the rows that see it; in a
+ * value row it may also reach earlier rows of its sequence that share its
+ * 128-key block and, in the cache form, the other heads of its request (their
+ * weight for it is 0, and 0 times NaN is NaN).  Rows past a sequence's or a
+ * cache's end, keys that no row of a call sees, and other sequences' and
+ * requests' rows may hold anything.
  */
 MF_API int mf_attn_create_packed(mf_attn_t* out, const int32_t* cu_seqlens_host, const int32_t* q_begin_host,
                                  int n_seqs, int H_q, int H_kv, int d, int window, int n_sink,
