@@ -162,35 +162,35 @@ def _raw_current(index: int):
     return None
 
 
-def _rows(name: str, t, shape, dtype, device) -> int:
-    """Checks a tensor of `shape` [..., heads, d] whose leading dimensions are
-    equally spaced tokens; returns the values between two tokens."""
+def _rows(name: str, t, shape, dtype, gpu: int) -> int:
+    """Checks a tensor of `shape` [..., heads, d] on GPU `gpu` whose leading
+    dimensions are equally spaced tokens; returns the values between two
+    tokens."""
     heads, d = shape[-2:]
-    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
-        return heads * d
-    if t.device != device:
-        raise MapFlowError(MF_ERR_ARG, f"{name} must be on {device}, is on {t.device}")
-    if t.dtype != dtype:
-        raise MapFlowError(MF_ERR_ARG, f"{name} must be {dtype}, is {t.dtype}")
-    if t.shape != shape:
-        raise MapFlowError(MF_ERR_ARG, f"{name} must be {tuple(shape)}, is {tuple(t.shape)}")
-    st = t.stride()
-    if st[-1] != 1 or (heads > 1 and st[-2] != d):
+    if t.dtype is dtype and t.get_device() == gpu and t.shape == shape:
+        if t.is_contiguous():
+            return heads * d
+        st = t.stride()
+        if st[-1] == 1 and (st[-2] == d or heads == 1):
+            if len(st) == 3:
+                return st[0] if shape[0] != 1 else heads * d
+            n, ld = 1, None
+            for i in range(len(st) - 3, -1, -1):
+                if shape[i] != 1:
+                    if ld is None:
+                        ld = st[i]
+                    elif st[i] != n * ld:
+                        raise MapFlowError(MF_ERR_ARG, f"{name}: its tokens are not equally spaced")
+                n *= shape[i]
+            return heads * d if ld is None else ld
         raise MapFlowError(MF_ERR_ARG, f"{name}: a token's heads must lie next to each other")
-    n, ld = 1, None
-    for i in range(len(shape) - 3, -1, -1):
-        if shape[i] != 1:
-            if ld is None:
-                ld = st[i]
-            elif st[i] != n * ld:
-                raise MapFlowError(MF_ERR_ARG, f"{name}: its tokens are not equally spaced")
-        n *= shape[i]
-    return heads * d if ld is None else ld
+    raise MapFlowError(MF_ERR_ARG, f"{name} must be a {dtype} tensor {tuple(shape)} on cuda:{gpu}, is {t.dtype} "
+                                   f"{tuple(t.shape)} on {t.device}")
 
 
-def _vector(name: str, t, shape, dtype, device):
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise MapFlowError(MF_ERR_ARG, f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}")
+def _vector(name: str, t, shape, dtype, gpu: int):
+    if t.dtype is not dtype or t.get_device() != gpu or t.shape != shape or not t.is_contiguous():
+        raise MapFlowError(MF_ERR_ARG, f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on cuda:{gpu}")
 
 
 # ------------------------------------------------------ torch allocator ----
@@ -471,9 +471,10 @@ class RotaryPlan:
         turns, self.gain = mf_rope_frequencies(rot_dim, base, scaling, factor, original_length, beta_fast,
                                                beta_slow)
         self.rot_dim, self.layout, self._layout = int(rot_dim), layout, _LAYOUTS[layout]
-        self._lib = load_library()
+        self._call = load_library().mf_qk_norm_rope
         device = torch.device("cuda" if device is None else device)
         self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
+        self._turns, self._gpu = self.turns.data_ptr(), self.turns.get_device()
 
     def apply(self, q, k, positions, q_weight=None, k_weight=None, eps: float = 1e-6, norm: Optional[bool] = None,
               q_out=None, k_out=None, stream=None):
@@ -481,52 +482,52 @@ class RotaryPlan:
         returns (q_out, k_out), new tensors unless given (q_out=q: in place).
         The norm is taken when a weight is given or norm is True."""
         code = _dtype_code(q)
-        raw = None if stream is not None else _raw_current(q.get_device())
+        gpu = q.get_device()
+        raw = None if stream is not None else _raw_current(gpu)
         if raw is not None:
-            return self._apply(raw, code, q, k, positions, q_weight, k_weight, eps, norm, q_out, k_out)
+            return self._apply(raw, gpu, code, q, k, positions, q_weight, k_weight, eps, norm, q_out, k_out)
         guard, raw = _on(q, stream)
         with guard:
-            return self._apply(raw, code, q, k, positions, q_weight, k_weight, eps, norm, q_out, k_out)
+            return self._apply(raw, gpu, code, q, k, positions, q_weight, k_weight, eps, norm, q_out, k_out)
 
-    def _apply(self, raw, code, q, k, positions, q_weight, k_weight, eps, norm, q_out, k_out):
+    def _apply(self, raw, gpu, code, q, k, positions, q_weight, k_weight, eps, norm, q_out, k_out):
         import torch
-        if norm is None:
-            norm = q_weight is not None or k_weight is not None
-        dev, dt = q.device, q.dtype
-        if self.turns.device != dev:
-            raise MapFlowError(MF_ERR_ARG, f"q is on {dev}, the plan on {self.turns.device}")
+        dt = q.dtype
+        if self._gpu != gpu:
+            raise MapFlowError(MF_ERR_ARG, f"q is on cuda:{gpu}, the plan on {self.turns.device}")
         if q.dim() != 3 or (k is not None and k.dim() != 3):
             raise MapFlowError(MF_ERR_ARG, "q and k must be [T, heads, d]")
         shape_q = T, H_q, d = q.shape
-        ld_q = _rows("q", q, shape_q, dt, dev)
+        ld_q = _rows("q", q, shape_q, dt, gpu)
         if q_out is None:
-            q_out, ld_qo = torch.empty(shape_q, dtype=dt, device=dev), H_q * d
+            q_out, ld_qo = torch.empty(shape_q, dtype=dt, device=q.device), H_q * d
         else:
-            ld_qo = _rows("q_out", q_out, shape_q, dt, dev)
+            ld_qo = _rows("q_out", q_out, shape_q, dt, gpu)
         H_k = ld_k = ld_ko = 0
         pk = pko = pwq = pwk = None
         if k is not None:
             H_k = k.shape[1]
             shape_k = (T, H_k, d)
-            ld_k = _rows("k", k, shape_k, dt, dev)
+            ld_k = _rows("k", k, shape_k, dt, gpu)
             if k_out is None:
-                k_out, ld_ko = torch.empty(shape_k, dtype=dt, device=dev), H_k * d
+                k_out, ld_ko = torch.empty(shape_k, dtype=dt, device=q.device), H_k * d
             else:
-                ld_ko = _rows("k_out", k_out, shape_k, dt, dev)
+                ld_ko = _rows("k_out", k_out, shape_k, dt, gpu)
             pk, pko = k.data_ptr(), k_out.data_ptr()
         elif k_out is not None:
             raise MapFlowError(MF_ERR_ARG, "k_out without k")
-        _vector("positions", positions, (T,), torch.int32, dev)
+        _vector("positions", positions, (T,), torch.int32, gpu)
         if q_weight is not None:
-            _vector("q_weight", q_weight, (d,), dt, dev)
+            _vector("q_weight", q_weight, (d,), dt, gpu)
             pwq = q_weight.data_ptr()
         if k_weight is not None:
-            _vector("k_weight", k_weight, (d,), dt, dev)
+            _vector("k_weight", k_weight, (d,), dt, gpu)
             pwk = k_weight.data_ptr()
-        rc = self._lib.mf_qk_norm_rope(
+        if norm is None:
+            norm = pwq is not None or pwk is not None
+        rc = self._call(
             q.data_ptr(), ld_q, q_out.data_ptr(), ld_qo, pk, ld_k, pko, ld_ko, pwq, pwk, norm, eps,
-            positions.data_ptr(), self.turns.data_ptr(), self.rot_dim, self._layout, self.gain, code, T, H_q, H_k, d,
-            raw)
+            positions.data_ptr(), self._turns, self.rot_dim, self._layout, self.gain, code, T, H_q, H_k, d, raw)
         if rc:
             _check(rc)
         return q_out, k_out
@@ -567,7 +568,8 @@ class WindowAttention(_AttentionPlan):
 
     def __init__(self, cu_seqlens: Sequence[int], H_q: int, H_kv: int, d: int, window: Optional[int] = None,
                  sinks: int = 0, q_begin: Optional[Sequence[int]] = None, use_torch_allocator: bool = True):
-        self._lib = lib = load_library()
+        lib = load_library()
+        self._call = lib.mf_attn_packed
         if window is not None and window < 1:
             raise MapFlowError(MF_ERR_ARG, f"window = {window} must be >= 1 (None: no window)")
         cu = np.ascontiguousarray(np.asarray(cu_seqlens, dtype=np.int32))
@@ -587,12 +589,14 @@ class WindowAttention(_AttentionPlan):
         self.handle = h
         self._ws_bytes = self._workspace_bytes(1)
         import torch
-        self.device = torch.device("cuda", torch.cuda.current_device())
+        self._gpu = torch.cuda.current_device()
+        self.device = torch.device("cuda", self._gpu)
+        self._scale = self.d ** -0.5
 
     def attend(self, q, k, v, scale: Optional[float] = None, o=None, lse=None, stream=None):
         """q [T, H_q, d], k and v [T, H_kv, d] -> o [T, H_q, d] (rows before a
         q_begin are left as they are); lse: fp32 [T, H_q] to fill, or None."""
-        raw = None if stream is not None else _raw_current(self.device.index)
+        raw = None if stream is not None else _raw_current(self._gpu)
         if raw is not None:
             return self._attend(raw, q, k, v, scale, o, lse)
         guard, raw = _on(self.device, stream)
@@ -601,24 +605,24 @@ class WindowAttention(_AttentionPlan):
 
     def _attend(self, raw, q, k, v, scale, o, lse):
         import torch
-        dt, dev = torch.bfloat16, self.device
+        dt, gpu = torch.bfloat16, self._gpu
         shape_q, shape_k = (self.T, self.H_q, self.d), (self.T, self.H_kv, self.d)
-        ld_q = _rows("q", q, shape_q, dt, dev)
-        ld_k = _rows("k", k, shape_k, dt, dev)
-        ld_v = _rows("v", v, shape_k, dt, dev)
+        ld_q = _rows("q", q, shape_q, dt, gpu)
+        ld_k = _rows("k", k, shape_k, dt, gpu)
+        ld_v = _rows("v", v, shape_k, dt, gpu)
         if o is None:
-            o = torch.empty(shape_q, dtype=dt, device=dev)
-        ld_o = _rows("o", o, shape_q, dt, dev)
+            o = torch.empty(shape_q, dtype=dt, device=self.device)
+        ld_o = _rows("o", o, shape_q, dt, gpu)
         p_lse = p_ws = None
         if lse is not None:
-            _vector("lse", lse, shape_q[:2], torch.float32, dev)
+            _vector("lse", lse, shape_q[:2], torch.float32, gpu)
             p_lse = lse.data_ptr()
         if self._ws_bytes:  # a workspace of its own for every call: calls may overlap
-            ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev)
+            ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
             p_ws = ws.data_ptr()
-        rc = self._lib.mf_attn_packed(
+        rc = self._call(
             self.handle, q.data_ptr(), ld_q, k.data_ptr(), ld_k, v.data_ptr(), ld_v, o.data_ptr(), ld_o, p_lse,
-            MF_DTYPE_BF16, self.d ** -0.5 if scale is None else scale, p_ws, self._ws_bytes, raw)
+            MF_DTYPE_BF16, self._scale if scale is None else scale, p_ws, self._ws_bytes, raw)
         if rc:
             _check(rc)
         return o
@@ -633,7 +637,8 @@ class CacheAttention(_AttentionPlan):
     def __init__(self, n: int, Lq: int, capacity: int, H_q: int, H_kv: int, d: int,
                  window: Optional[int] = None, sinks: int = 0, prefix_len: int = 0,
                  use_torch_allocator: bool = True):
-        self._lib = lib = load_library()
+        lib = load_library()
+        self._call = lib.mf_attn_cached
         if window is not None and window < 1:
             raise MapFlowError(MF_ERR_ARG, f"window = {window} must be >= 1 (None: no window)")
         self.n, self.Lq, self.capacity, self.prefix_len = int(n), int(Lq), int(capacity), int(prefix_len)
@@ -647,7 +652,9 @@ class CacheAttention(_AttentionPlan):
         self.handle = h
         self._ws_of: Dict[int, int] = {}  # workspace bytes by the number of requests
         import torch
-        self.device = torch.device("cuda", torch.cuda.current_device())
+        self._gpu = torch.cuda.current_device()
+        self.device = torch.device("cuda", self._gpu)
+        self._scale = self.d ** -0.5
 
     def attend(self, q, k_cache, v_cache, lens, k_prefix=None, v_prefix=None, scale: Optional[float] = None,
                o=None, lse=None, stream=None):
@@ -655,7 +662,7 @@ class CacheAttention(_AttentionPlan):
         capacity, H_kv, d], lens int32 [m] on the device (keys in each cache,
         the new tokens' among them), k_prefix and v_prefix [prefix_len, H_kv,
         d] -> o [m, Lq, H_q, d]; lse: fp32 [m, Lq, H_q] to fill, or None."""
-        raw = None if stream is not None else _raw_current(self.device.index)
+        raw = None if stream is not None else _raw_current(self._gpu)
         if raw is not None:
             return self._attend(raw, q, k_cache, v_cache, lens, k_prefix, v_prefix, scale, o, lse)
         guard, raw = _on(self.device, stream)
@@ -664,38 +671,38 @@ class CacheAttention(_AttentionPlan):
 
     def _attend(self, raw, q, k_cache, v_cache, lens, k_prefix, v_prefix, scale, o, lse):
         import torch
-        dt, dev = torch.bfloat16, self.device
+        dt, gpu = torch.bfloat16, self._gpu
         m = q.shape[0]
         shape_q, shape_k = (m, self.Lq, self.H_q, self.d), (m, self.capacity, self.H_kv, self.d)
-        ld_q = _rows("q", q, shape_q, dt, dev)
-        ld_k = _rows("k_cache", k_cache, shape_k, dt, dev)
-        ld_v = _rows("v_cache", v_cache, shape_k, dt, dev)
-        _vector("lens", lens, (m,), torch.int32, dev)
+        ld_q = _rows("q", q, shape_q, dt, gpu)
+        ld_k = _rows("k_cache", k_cache, shape_k, dt, gpu)
+        ld_v = _rows("v_cache", v_cache, shape_k, dt, gpu)
+        _vector("lens", lens, (m,), torch.int32, gpu)
         if o is None:
-            o = torch.empty(shape_q, dtype=dt, device=dev)
-        ld_o = _rows("o", o, shape_q, dt, dev)
+            o = torch.empty(shape_q, dtype=dt, device=self.device)
+        ld_o = _rows("o", o, shape_q, dt, gpu)
         p_lse = p_kp = p_vp = None
         if lse is not None:
-            _vector("lse", lse, shape_q[:3], torch.float32, dev)
+            _vector("lse", lse, shape_q[:3], torch.float32, gpu)
             p_lse = lse.data_ptr()
         ld_kp = ld_vp = 0
         if self.prefix_len:
             if k_prefix is None or v_prefix is None:
                 raise MapFlowError(MF_ERR_ARG, "the plan has a prefix: k_prefix and v_prefix are needed")
             shape_p = (self.prefix_len, self.H_kv, self.d)
-            ld_kp = _rows("k_prefix", k_prefix, shape_p, dt, dev)
-            ld_vp = _rows("v_prefix", v_prefix, shape_p, dt, dev)
+            ld_kp = _rows("k_prefix", k_prefix, shape_p, dt, gpu)
+            ld_vp = _rows("v_prefix", v_prefix, shape_p, dt, gpu)
             p_kp, p_vp = k_prefix.data_ptr(), v_prefix.data_ptr()
         elif k_prefix is not None or v_prefix is not None:
             raise MapFlowError(MF_ERR_ARG, "the plan has no prefix")
         need = self._ws_of.get(m)
         if need is None:
             need = self._ws_of[m] = self._workspace_bytes(m)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)  # its own for every call: calls may overlap
-        rc = self._lib.mf_attn_cached(
+        ws = torch.empty(need, dtype=torch.uint8, device=self.device)  # its own for every call: calls may overlap
+        rc = self._call(
             self.handle, m, q.data_ptr(), ld_q, k_cache.data_ptr(), ld_k, v_cache.data_ptr(), ld_v, lens.data_ptr(),
             p_kp, ld_kp, p_vp, ld_vp, o.data_ptr(), ld_o, p_lse, MF_DTYPE_BF16,
-            self.d ** -0.5 if scale is None else scale, ws.data_ptr(), need, raw)
+            self._scale if scale is None else scale, ws.data_ptr(), need, raw)
         if rc:
             _check(rc)
         return o
