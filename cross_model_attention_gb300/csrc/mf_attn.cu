@@ -139,37 +139,25 @@ int finish_handle(mf_attn_t h, mf_attn_t* out, const std::vector<AttnSeg>& segs,
   return MF_OK;
 }
 
-// Cache form: partial results a row can have, and the workspace's parts.
+// Cache form: the workspace's parts.  A line of units cut into one span per
+// CTA has fewer than units + CTAs runs.
 struct CacheLayout {
-  int np_pre, np_suf, pairs, nbp;
-  size_t cuts, ml, o, bytes;
+  int pairs, nbp, suf_rows;
+  long long suf_base;
+  size_t ml, o, bytes;  // (the cuts of the units come first)
 };
 CacheLayout cache_layout(const mf_attn_s* h, int n) {
   CacheLayout c{};
   const long long toks = (long long)n * h->Lq, tiles = (toks + h->TQ - 1) / h->TQ;
   c.pairs = h->P > 0 ? (int)((tiles + 1) / 2) : 0;
   c.nbp = (h->P + kBlock - 1) / kBlock;
-  // most blocks of one request's cache: every key, or the window and sinks
-  long long nbs = (h->cap + kBlock - 1) / kBlock;
-  if (h->window < kAttnNoWindow)
-    nbs = std::min(nbs, (std::min((long long)h->n_sink, (long long)h->cap) + kBlock - 1) / kBlock +
-                            ((long long)h->window + h->Lq - 1 + kBlock - 1) / kBlock) + 1;
-  // a line of nb blocks is cut every `span` blocks: at most nb / span + 2
-  // pieces; the span is at least the even share of what is certainly there
-  // (the prefix; for a request, its own blocks in every KV head)
-  const double span_pre = std::max((double)kMinSpan, (double)c.pairs * c.nbp * h->H_kv / h->grid);
-  const double span_suf = std::max((double)kMinSpan, (double)nbs * h->H_kv / h->grid);
-  if (c.pairs > 0) {
-    c.np_pre = (int)(c.nbp / span_pre) + 3;
-    if (tiles & 1) c.np_pre *= 2;  // a lone tile's streams have results of their own
-  }
-  c.np_suf = 2 * ((int)(nbs * h->HG / span_suf) + 3);
-  const size_t rows = (size_t)toks * h->H_q;
-  const size_t np = (size_t)c.np_pre + c.np_suf;
-  c.cuts = 0;
-  c.ml = up256(((size_t)c.pairs * h->H_kv + (size_t)n * h->groups) * sizeof(int2));
-  c.o = c.ml + up256(np * rows * sizeof(float2));
-  c.bytes = c.o + up256(np * rows * h->d * sizeof(float));
+  c.suf_rows = h->Lq * h->HG * h->G;
+  const long long pre_units = (long long)c.pairs * h->H_kv, suf_units = (long long)n * h->groups;
+  c.suf_base = pre_units > 0 ? 2 * (pre_units + h->grid) * kBlock : 0;
+  const size_t rows = (size_t)(c.suf_base + 2 * (suf_units + h->grid) * c.suf_rows);
+  c.ml = up256((size_t)(pre_units + suf_units) * sizeof(int2));
+  c.o = c.ml + up256(rows * sizeof(float2));
+  c.bytes = c.o + up256(rows * h->d * sizeof(float));
   return c;
 }
 
@@ -548,7 +536,6 @@ int mf_attn_packed(mf_attn_t h, const void* q, int64_t ld_q, const void* k, int6
   p.HG = 1;
   p.segs = h->segs_d;
   p.cta_segs = h->cta_d;
-  p.part_rows = kBlock;
   const size_t rows = (size_t)h->n_slots * 2 * kBlock;
   p.part_ml = static_cast<float2*>(workspace);
   p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + up256(rows * sizeof(float2)));
@@ -623,14 +610,14 @@ int mf_attn_cached(mf_attn_t h, int n, const void* q, int64_t ld_q, const void* 
   p.pre_blocks = c.nbp;
   p.HG = h->HG;
   p.groups = h->groups;
-  p.np_pre = c.np_pre;
-  p.np_suf = c.np_suf;
+  p.grid = h->grid;
+  p.suf_base = c.suf_base;
+  p.suf_rows = c.suf_rows;
   p.min_span = kMinSpan;
   char* ws = static_cast<char*>(workspace);
-  p.cuts = reinterpret_cast<int2*>(ws + c.cuts);
+  p.cuts = reinterpret_cast<int2*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + c.ml);
   p.part_o = reinterpret_cast<float*>(ws + c.o);
-  p.part_rows = rows * h->H_q;
   p.err = h->err_d;
   MF_CUDA(launch_attn_cache(p, h->d, h->grid, tq, tk, tv, tkp, tvp, tqc, static_cast<cudaStream_t>(stream)),
           "cache attention kernels");

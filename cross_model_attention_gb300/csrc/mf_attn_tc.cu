@@ -312,7 +312,7 @@ struct CacheRuns {
       if (some) {
         o.head = head;
         o.heads = heads;
-        int unit, most;
+        int unit;
         if (pre) {
           const int tok0 = who * 2 * p.TQ, n_tok = p.n * p.Lq - tok0;
           o.kind = kPrefix;
@@ -327,7 +327,6 @@ struct CacheRuns {
           o.b1 = p.P;
           o.nb = nb;
           unit = who * p.H_kv + head;
-          most = p.np_pre;
         } else {
           o.kind = kCache;
           o.q_row = who * p.Lq;
@@ -340,15 +339,14 @@ struct CacheRuns {
           o.b0 = u.b0;
           o.b1 = u.b1;
           o.nb = u.nb;
-          unit = p.pre_pairs * p.H_kv + who * p.groups + head / p.HG;
-          most = p.np_suf;
+          unit = who * p.groups + head / p.HG;
         }
-        // (held to the buffers, whatever happens to lens meanwhile)
-        const int step = o.alt ? 2 : 1;
-        const int piece = min(max(f0 / per - begins / per, 0), most / step - 1);
-        o.part = (pre ? 0 : p.np_pre) + piece * step;
-        // where its blocks lie, for the join: block j is in piece (x + j) / y
-        if (o.blk1 == nb && threadIdx.x == 0) p.cuts[unit] = make_int2(begins % per, per);
+        // Along the lines neither unit nor span goes down and one of them goes
+        // up from run to run, so their sum tells the runs' results apart.
+        o.part = 2 * (unit + f0 / per);
+        // for the join: block j of the unit is in span (x + j) / y
+        if (o.blk1 == nb && threadIdx.x == 0)
+          p.cuts[pre ? unit : p.pre_pairs * p.H_kv + unit] = make_int2(begins, per);
       }
       // the next unit
       if (nb > 0) at = begins + nb;
@@ -904,11 +902,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (mine && p.lse) p.lse[q_tok * p.H_q + head] = m == -INFINITY ? -INFINITY : m * p.scale + logf(l);
       } else {
-        // packed: part + stream, rows of the tile; cache: one row per (token,
-        // head) of the batch, streams apart only where they share rows
-        const int part = r.part + ((r.alt || !cached) ? s : 0);
-        const long long prow = cached ? q_tok * p.H_q + head : row;
-        const long long at = static_cast<long long>(part) * p.part_rows + prow;
+        const long long part = r.part + s;
+        const long long at = cache ? p.suf_base + part * p.suf_rows + row : part * kRows + row;
         float* dst = p.part_o + at * D;
         if (mine) p.part_ml[at] = make_float2(m == -INFINITY ? -INFINITY : m * sc, l);
         if (any) {
@@ -949,52 +944,56 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p, const Att
   // from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long w = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  long long prow, q_tok;
-  int head, n0, base0, step0, n1 = 0, base1 = 0;
+  // A row's partial results: n0 of the prefix or of a packed tile, then n1 of
+  // its cache.  Result i: part first + i * step (in halves of a slot), rows
+  // apart by the tile's.
+  long long q_tok, at0 = 0, at1 = 0, step0 = 0;
+  int head, n0 = 0, n1 = 0;
   if (CACHED) {
-    if (w >= p.part_rows) return;
-    prow = w;
+    if (w >= static_cast<long long>(p.n) * p.Lq * p.H_q) return;
     q_tok = w / p.H_q;
     head = static_cast<int>(w - q_tok * p.H_q);
-    const int kv = head / p.G, req = static_cast<int>(q_tok / p.Lq);
-    base0 = 0;
-    step0 = 1;
-    n0 = 0;
-    // (counts are held to what the buffers have, whatever a failed run left)
+    const int kv = head / p.G, hg = head - kv * p.G, req = static_cast<int>(q_tok / p.Lq);
+    const int grid = p.grid;
+    // (slots are held to what the buffers have, whatever a failed run left)
+    auto slots = [&](int unit, int2 cut, int b0, int b1, int& slot) {
+      const int c0 = min(max((cut.x + b0) / cut.y, 0), grid - 1);
+      const int c1 = min(max((cut.x + b1) / cut.y, c0), grid - 1);
+      slot = unit + c0;
+      return c1 - c0 + 1;
+    };
     if (p.pre_pairs > 0) {
-      const int pair = static_cast<int>(q_tok / (2 * p.TQ));
-      const int2 cut = p.cuts[pair * p.H_kv + kv];
-      n0 = (cut.x + p.pre_blocks - 1) / cut.y + 1;
-      // a lone last tile ran on both streams
-      if (2ll * pair * p.TQ + p.TQ >= static_cast<long long>(p.n) * p.Lq) n0 *= 2;
-      n0 = min(max(n0, 0), p.np_pre);
+      const int tile = static_cast<int>(q_tok / p.TQ), pair = tile >> 1, unit = pair * p.H_kv + kv;
+      int slot;
+      n0 = slots(unit, p.cuts[unit], 0, p.pre_blocks - 1, slot);
+      // a pair's tiles have a stream each; a lone last tile ran on both
+      const bool lone = (2ll * pair + 1) * p.TQ >= static_cast<long long>(p.n) * p.Lq;
+      step0 = (lone ? 1 : 2) * kRows;
+      at0 = static_cast<long long>(2 * slot + (lone ? 0 : tile & 1)) * kRows +
+            (q_tok - static_cast<long long>(tile) * p.TQ) * p.G + hg;
+      if (lone) n0 *= 2;
     }
     const int nb = cache_unit(p, p.lens[req]).nb;
-    base1 = p.np_pre;
     if (nb > 0) {  // the pieces with blocks of the row's head
-      const int2 cut = p.cuts[p.pre_pairs * p.H_kv + req * p.groups + kv / p.HG];
-      const int at = cut.x + kv % p.HG * nb;
-      const int first = min(max(2 * (at / cut.y), 0), p.np_suf);
-      base1 += first;
-      n1 = min(max(2 * ((at + nb - 1) / cut.y) + 2 - first, 0), p.np_suf - first);
+      const int hh = kv % p.HG, unit = req * p.groups + kv / p.HG;
+      int slot;
+      n1 = 2 * slots(unit, p.cuts[p.pre_pairs * p.H_kv + unit], hh * nb, hh * nb + nb - 1, slot);
+      at1 = p.suf_base + 2ll * slot * p.suf_rows +
+            (static_cast<int>(q_tok - static_cast<long long>(req) * p.Lq) * p.HG + hh) * p.G + hg;
     }
   } else {
     const long long j = w / kRows;
     if (j >= n_joins) return;
     const AttnJoin jn = joins[j];
-    prow = w - j * kRows;
-    const int tok = static_cast<int>(prow) / p.G;
+    const int row = static_cast<int>(w - j * kRows), tok = row / p.G;
     if (tok >= jn.n_tok) return;
     q_tok = jn.q_row + tok;
-    head = jn.head * p.G + static_cast<int>(prow) - tok * p.G;
+    head = jn.head * p.G + row - tok * p.G;
     n0 = jn.n_part;
-    base0 = jn.part0;
-    step0 = jn.step;
+    at0 = static_cast<long long>(jn.part0) * kRows + row;
+    step0 = static_cast<long long>(jn.step) * kRows;
   }
-  auto at = [&](int i) {
-    const int part = i < n0 ? base0 + i * step0 : base1 + (i - n0);
-    return static_cast<long long>(part) * p.part_rows + prow;
-  };
+  auto at = [&](int i) { return i < n0 ? at0 + i * step0 : at1 + static_cast<long long>(i - n0) * p.suf_rows; };
   const int n = n0 + n1;
   float top = -INFINITY, l = 0.f, acc[V] = {};
   constexpr int kAtOnce = 16;  // results of o asked for together, before their weights are known
@@ -1101,7 +1100,7 @@ cudaError_t launch_attn_cache(const AttnParams& p, int d, int grid, const CUtens
   cudaError_t e = d == 128 ? launch_main<128, CacheRuns>(p, grid, tq, tk, tv, tkp, tvp, tqc, true, s)
                            : launch_main<64, CacheRuns>(p, grid, tq, tk, tv, tkp, tvp, tqc, true, s);
   if (e != cudaSuccess) return e;
-  const long long blocks = (p.part_rows + 7) / 8;
+  const long long blocks = (static_cast<long long>(p.n) * p.Lq * p.H_q + 7) / 8;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
   return d == 128 ? launch_dependent<128, true>(static_cast<int>(blocks), s, p, nullptr, 0)
                   : launch_dependent<64, true>(static_cast<int>(blocks), s, p, nullptr, 0);

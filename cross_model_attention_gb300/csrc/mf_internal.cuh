@@ -237,13 +237,16 @@ struct AttnParams {
   int n, Lq, cap, P;
   int pre_pairs, pre_blocks; // prefix: pairs of row tiles (0: no prefix), key blocks
   int HG, groups;            // caches: KV heads per tile, tiles per request
-  int np_pre, np_suf;        // partial results a row can have from each
+  int grid;                  // CTAs of the launch
   int min_span;              // least work per CTA, in blocks
   int2* cuts;                // [units] how a unit's blocks are cut, written by its last run
   // partial results
-  float* part_o;             // [partial][part_rows][d], not normalised
-  float2* part_ml;           // [partial][part_rows]: reference (log2 units), sum
-  long long part_rows;
+  float* part_o;             // [row][d], not normalised
+  float2* part_ml;           // [row]: reference (log2 units), sum
+  // a run's results: slot part/2, each of its two streams 128 rows; those of a
+  // cache's run from row suf_base on, suf_rows each
+  long long suf_base;
+  int suf_rows;
   int* err;
 };
 cudaError_t launch_attn_packed(const AttnParams& p, int d, int grid, const CUtensorMap& tq,

@@ -349,6 +349,15 @@ def test_cache_fewer_requests_than_planned_and_garbage():
     assert torch.equal(plan.attend(q, kw, v, dl, kp, vp), o)
 
 
+def test_workspace_grows_with_requests_not_with_their_keys():
+    # units + CTAs runs at most, two streams of a tile's 32 rows each
+    for n, cap, P in ((1, 8192, 0), (512, 8192, 0), (512, 8, 32768)):
+        plan = mapflow.CacheAttention(n, 1, cap, 32, 8, 128, prefix_len=P)
+        pairs = -(-n * 4 // 256) if P else 0
+        rows = 2 * (n + 160) * 32 + 2 * (pairs * 8 + 160) * 128 * (P > 0)
+        assert plan._workspace_bytes(n) <= rows * (128 * 4 + 8) + 8 * (n + 8 * pairs) + 1024
+
+
 def test_cache_refusals():
     plan = mapflow.CacheAttention(4, 1, 32, 4, 2, 64, prefix_len=16)
     q, k, v = rnd(0, 4, 1, 4, 64), rnd(1, 4, 32, 2, 64), rnd(2, 4, 32, 2, 64)
