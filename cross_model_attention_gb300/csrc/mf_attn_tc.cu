@@ -535,14 +535,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // one-tile runs alternate between the slots: the next run's Q comes
         // while this one's is in use
-        if (r.alt) {
+        const bool two = r.n_tok1 > 0;
+        if (!two) {
           load_q(slot, 0);
           slot ^= 1;
         }
         for (int i = 0; ok && i < min(ahead, nb); ++i) load(mk, i);
-        if (!r.alt) {
+        if (two) {
           load_q(0, 0);
-          if (r.n_tok1 > 0) load_q(1, 1);
+          load_q(1, 1);
         }
         for (int i = 0; ok && i < nb; ++i) {
           load(mv, i);
@@ -614,13 +615,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int alt = uniform(r.alt), two = uniform(r.n_tok1 > 0);
       const int ahead = alt ? 2 : 1;
       const bool on = alt || s == 0 || two;  // whether this stream works in this run
-      const int tile = alt ? slot : s;       // the Q slot it reads
-      if (alt) slot ^= 1;
+      const int tile = two ? s : slot;       // the Q slot it reads, or that is free without it
+      if (!two) slot ^= 1;
       auto wait_q = [&](int t) {
         if (!ok || !warp_wait(barQFull(t), (q_ph >> t) & 1u, p.err, misc)) ok = false;
         q_ph ^= 1u << t;
       };
-      if (on) wait_q(tile);
+      wait_q(tile);
       if (!ok) break;
       tc_fence_after();
       auto mine = [&](int i) { return on && (!alt || (i & 1) == s); };
@@ -633,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           else mbar_arrive(bar);
         }
       };
-      if (on && last < 0) leave(barQEmpty(tile), false);
+      if (last < 0) leave(barQEmpty(tile), false);
       // the stream's first S
       for (int i = 0; ok && i < min(ahead, nb); ++i) {
         const uint32_t kph = ring_ph;
@@ -655,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       // the other stream's Q: this one only says that it does not read it
-      if (ok && !alt && (s == 1 || two)) {
+      if (ok && two) {
         wait_q(s ^ 1);
         if (ok) leave(barQEmpty(s ^ 1), false);
         __syncwarp();
