@@ -264,21 +264,17 @@ struct CacheRuns {
   int f0, f1, per;           // this CTA's span of it
   int at;                    // start of the unit's line
   int who, head;             // tile pair or request, (first) KV head
-  int suf_total, suf_first, suf_before;
-  Unit u;                    // of the request
-  // misc: [2] first request, [4] the lines before it, [5] all requests' lines
-  __device__ CacheRuns(const AttnParams& p_, const volatile int* misc) : p(p_) {
-    suf_first = misc[2];
-    suf_before = misc[4];
-    suf_total = misc[5];
+  // (little is kept: these registers are live through the softmax)
+  const volatile int* misc;  // [2] first request, [4] the lines before it, [5] all requests' lines
+  __device__ CacheRuns(const AttnParams& p_, const volatile int* misc_) : p(p_), misc(misc_) {
     todo = 2;
     pre = (blockIdx.x & 1) == 0;
     begin();
   }
   __device__ int pre_line() const { return kCostPre + p.pre_blocks; }
   __device__ void begin() {
-    const int total = pre ? pre_lines(p) : suf_total;
-    per = span_of(p, pre, suf_total);
+    const int suffix = misc[5], total = pre ? pre_lines(p) : suffix;
+    per = span_of(p, pre, suffix);
     // (from the other end of the CTAs: two short lists meet late)
     f0 = min(total, per * static_cast<int>(pre ? blockIdx.x : gridDim.x - 1 - blockIdx.x));
     f1 = min(total, f0 + per);
@@ -288,10 +284,9 @@ struct CacheRuns {
       head = unit - who * p.H_kv;
       at = unit * pre_line();
     } else {
-      who = suf_first;
+      who = misc[2];
       head = 0;
-      at = suf_before;
-      u = cache_unit(p, who < p.n ? p.lens[who] : 0);
+      at = misc[4];
     }
   }
   __device__ bool next(Run& o) {
@@ -302,7 +297,9 @@ struct CacheRuns {
         begin();
         continue;
       }
-      // the unit at `at`
+      // the unit at `at` (at < f1: a request is there)
+      Unit u{};
+      if (!pre) u = cache_unit(p, p.lens[min(who, p.n - 1)]);
       const int heads = pre ? 1 : min(p.HG, p.H_kv - head);
       const int nb = pre ? p.pre_blocks : u.nb * heads;
       const int begins = at + (pre ? kCostPre : kCostCache);
@@ -355,7 +352,6 @@ struct CacheRuns {
         head = 0;
         ++who;
         if (pre ? who >= p.pre_pairs : who >= p.n) at = f1;  // past the last
-        else if (!pre) u = cache_unit(p, p.lens[who]);
       }
       if (some) return true;
     }
