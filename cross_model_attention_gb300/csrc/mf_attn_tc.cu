@@ -804,7 +804,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
           // a row's first visible key sets its reference; later only a maximum
-          // 2^8 above it moves it
+          // 2^8 above it moves it.  (The maximum passes over NaN; the sum does
+          // not, and tells a row that saw only such scores from one that saw
+          // none.)
           const bool move = m == -INFINITY ? top > -INFINITY : top > m + slack;
           // (a row that starts has weight zero in O so far: nothing to rescale)
           const bool rescale = move && m > -INFINITY;
@@ -897,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (mine && p.lse) p.lse[q_tok * p.H_q + head] = m == -INFINITY ? -INFINITY : m * p.scale + logf(l);
+        if (mine && p.lse) p.lse[q_tok * p.H_q + head] = l == 0.f ? -INFINITY : m * p.scale + logf(l);
       } else {
         const long long part = r.part + s;
         const long long at = cache ? p.suf_base + part * p.suf_rows + row : part * kRows + row;
@@ -1016,8 +1018,9 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p, const Att
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
       const float wi = __shfl_sync(0xffffffffu, w, i), li = __shfl_sync(0xffffffffu, ml.y, i);
-      // (one that saw nothing has weight 0; its o was perhaps not written)
-      if (i < m && wi != 0.f) {
+      // (one that saw nothing has sum 0, and its o was perhaps not written; a sum
+      // that is NaN comes through with weight 0 too)
+      if (i < m && li != 0.f) {
         l += wi * li;
         const float* x = reinterpret_cast<const float*>(&v[i]);
 #pragma unroll
@@ -1025,7 +1028,8 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p, const Att
       }
     }
   }
-  const float inv = top == -INFINITY ? 0.f : 1.f / l;
+  const bool none = l == 0.f;
+  const float inv = none ? 0.f : 1.f / l;
   __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + q_tok * p.ld_o + static_cast<long long>(head) * D + lane * V;
   if (V == 4)
     *reinterpret_cast<uint2*>(dst) =
@@ -1033,7 +1037,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p, const Att
   else
     *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
   if (p.lse && lane == 0)
-    p.lse[q_tok * p.H_q + head] = top == -INFINITY ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+    p.lse[q_tok * p.H_q + head] = none ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
 }
 
 // The join kernel may be set up while the attention kernel before it in the

@@ -349,6 +349,64 @@ def test_cache_fewer_requests_than_planned_and_garbage():
     assert torch.equal(plan.attend(q, kw, v, dl, kp, vp), o)
 
 
+def test_scores_that_are_not_numbers_stay_so():
+    """A query or a key that is NaN makes the rows that use it NaN, whole or
+    joined from partial results, and no other row."""
+    plan, q, k, v, o, lse = check_packed([700], 4, 2, 128)[:6]
+    chunk, cq, ck, cv, co, cl = check_packed([5000], 4, 2, 128, begin=[4990])
+    for p, x, y, z, at in ((plan, q, k, v, 650), (chunk, cq, ck, cv, 4995)):
+        want = p.attend(x, y, z)
+        x2, got, gl = x.clone(), torch.zeros_like(x), torch.zeros(x.shape[:2], device="cuda")
+        x2[at, 1] = float("nan")
+        p.attend(x2, y, z, o=got, lse=gl)
+        lo = 4990 if p is chunk else 0
+        hit = torch.zeros(x.shape[:2], dtype=torch.bool, device="cuda")
+        hit[at, 1] = True
+        assert torch.isnan(got[hit]).all() and torch.isnan(gl[hit]).all()
+        assert torch.equal(got[lo:][~hit[lo:]], want[lo:][~hit[lo:]]) and not torch.isnan(gl[lo:][~hit[lo:]]).any()
+    for P in (0, 1000):
+        plan, q, k, v, dl, kp, vp, o, lse = check_cache([300, 1, 0, 40], 2, 300, 8, 2, 128, P=P)
+        q2, gl = q.clone(), torch.empty_like(lse)
+        q2[0, 1, 3] = q2[1, 1, 0] = q2[3, 0, 7] = float("nan")
+        hit = torch.isnan(q2).any(-1)
+        got = plan.attend(q2, k, v, dl, kp, vp, lse=gl)
+        assert torch.isnan(got[hit]).all() and torch.isnan(gl[hit]).all()
+        assert torch.equal(got[~hit], o[~hit]) and torch.equal(gl[~hit], lse[~hit])
+
+
+def test_offsets_past_32_bits():
+    """Rows 2^26 and caches 2^31 values apart."""
+    T, H_q, H_kv, d, ld = 40, 4, 2, 128, 1 << 26
+    buf = torch.empty(T * ld, dtype=BF, device="cuda")
+    wide = buf.view(T, ld)
+    q, k, v, o = (wide[:, a:a + n * d].view(T, n, d) for a, n in ((0, H_q), (1024, H_kv), (2048, H_kv), (4096, H_q)))
+    q0, k0, v0 = rnd(0, T, H_q, d), rnd(1, T, H_kv, d), rnd(2, T, H_kv, d)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    rope = mapflow.RotaryPlan(d)
+    q.copy_(q0), k.copy_(k0), v.copy_(v0)
+    rope.apply(q, k, pos, norm=True, q_out=q, k_out=k)
+    q1, k1 = rope.apply(q0, k0, pos, norm=True)
+    assert torch.equal(q, q1) and torch.equal(k, k1)
+    plan = mapflow.WindowAttention([0, T], H_q, H_kv, d)
+    plan.attend(q, k, v, o=o)
+    plan.status()
+    assert torch.equal(o, plan.attend(q1, k1, v0))
+    # (the last request's cache begins 2^31 + 2^30 values in)
+    n, cap = 4, (1 << 30) // (H_kv * d)
+    kc, vc = (torch.empty(n, cap, H_kv, d, dtype=BF, device="cuda") for _ in range(2))
+    lens = torch.tensor([0, 0, 0, T], dtype=torch.int32, device="cuda")
+    kc[3, :T], vc[3, :T] = k0, v0
+    dec = mapflow.CacheAttention(n, 1, cap, H_q, H_kv, d)
+    qd = rnd(5, n, 1, H_q, d)
+    got = dec.attend(qd, kc, vc, lens)
+    dec.status()
+    small = mapflow.CacheAttention(n, 1, T, H_q, H_kv, d)
+    ks, vs = (x[:, :T].contiguous() for x in (kc, vc))
+    want, _, bo, _ = ref.attend(qd[3], ks[3], vs[3], torch.ones(1, T, dtype=torch.bool, device="cuda"), d ** -0.5)
+    close(got[3], want, bo, "far cache")
+    assert (got[:3] == 0).all() and (small.attend(qd, ks, vs, lens)[:3] == 0).all()
+
+
 def test_workspace_grows_with_requests_not_with_their_keys():
     # units + CTAs runs at most, two streams of a tile's 32 rows each
     for n, cap, P in ((1, 8192, 0), (512, 8192, 0), (512, 8, 32768)):
