@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdio>
 #include <cstring>
 #include <functional>
 #include <new>
@@ -47,6 +48,7 @@ constexpr int kBlock = 128;     // keys per block of the kernel
 // 13.9 / 17.1 / with one block 15.6 us.)
 constexpr int kMinSpan = 2;
 constexpr int kMaxTokens = kAttnFar;
+constexpr long long kMaxRuns = 1ll << 24;  // of a packed plan (its tables: 1 GB on the host)
 
 void* h_alloc(mf_attn_t h, size_t bytes) {
   if (h->alloc) return h->alloc(bytes, h->ctx, nullptr);
@@ -82,6 +84,12 @@ int check_rows(const char* name, const void* p, int64_t ld, int64_t heads, int d
   if (ld < heads * d) return fail(MF_ERR_ARG, "%s: %lld values between tokens, a token has %lld", name, (long long)ld, (long long)heads * d);
   if ((ld * esz) % 16 != 0) return fail(MF_ERR_ARG, "%s: tokens must be a multiple of 16 bytes apart", name);
   if (ld > (1ll << 32)) return fail(MF_ERR_UNSUPPORTED, "%s: tokens are too far apart", name);
+  return MF_OK;
+}
+
+// A vector of the caller's, of values of `size` bytes.
+int check_aligned(const char* name, const void* p, size_t size) {
+  if (reinterpret_cast<uintptr_t>(p) & (size - 1)) return fail(MF_ERR_ARG, "%s must be %zu-byte aligned", name, size);
   return MF_OK;
 }
 
@@ -131,9 +139,10 @@ int finish_handle(mf_attn_t h, mf_attn_t* out, const std::vector<AttnSeg>& segs,
     if (e != cudaSuccess) rc = cuda_fail(e, "attention plan setup");
   }
   if (rc != MF_OK) {
-    const std::string msg = mf_last_error();
+    char msg[512];
+    std::snprintf(msg, sizeof(msg), "%s", mf_last_error());
     mf_attn_destroy(h);
-    return fail(rc, "%s", msg.c_str());
+    return fail(rc, "%s", msg);
   }
   *out = h;
   return MF_OK;
@@ -236,6 +245,8 @@ int mf_qk_norm_rope(const void* q, int64_t ld_q, void* q_out, int64_t ld_qo, con
   if (!positions || !turns) return fail(MF_ERR_ARG, "positions and turns must be non-NULL");
   const int esz = dtype == MF_DTYPE_F32 ? 4 : 2;
   int rc;
+  if ((rc = check_aligned("positions", positions, 4)) != MF_OK) return rc;
+  if ((rc = check_aligned("turns", turns, 8)) != MF_OK) return rc;
   if ((rc = check_rows("q", q, ld_q, H_q, d, esz)) != MF_OK) return rc;
   if ((rc = check_rows("q_out", q_out, ld_qo, H_q, d, esz)) != MF_OK) return rc;
   if (H_k > 0) {
@@ -289,16 +300,19 @@ int mf_attn_create_packed(mf_attn_t* out, const int32_t* cu_seqlens_host, const 
   int rc = check_heads(H_q, H_kv, d, window, n_sink);
   if (rc != MF_OK) return rc;
   if (cu_seqlens_host[0] != 0) return fail(MF_ERR_ARG, "cu_seqlens[0] must be 0");
-  long long q_rows = 0;
+  long long q_rows = 0, runs = 0;
   for (int s = 0; s < n_seqs; ++s) {
     const long long len = (long long)cu_seqlens_host[s + 1] - cu_seqlens_host[s];
     if (len < 0) return fail(MF_ERR_ARG, "cu_seqlens must be non-decreasing (sequence %d)", s);
     const int qb = q_begin_host ? q_begin_host[s] : 0;
     if (qb < 0 || qb > len) return fail(MF_ERR_ARG, "q_begin[%d] = %d must be in [0, %lld]", s, qb, len);
     q_rows += len - qb;
+    const int pair = 2 * (kBlock / (H_q / H_kv));
+    runs += (len - qb + pair - 1) / pair;
   }
   if (cu_seqlens_host[n_seqs] > kMaxTokens) return fail(MF_ERR_UNSUPPORTED, "more than 2^29 tokens");
   if (q_rows == 0) return fail(MF_ERR_ARG, "the sequences hold no query rows");
+  if (runs * H_kv > kMaxRuns) return fail(MF_ERR_UNSUPPORTED, "%lld query tiles of %d heads are too many for one plan", 2 * runs, H_kv);
 
   mf_attn_t h = new (std::nothrow) mf_attn_s();
   if (!h) return fail(MF_ERR_OOM, "host memory");
@@ -508,6 +522,7 @@ int mf_attn_packed(mf_attn_t h, const void* q, int64_t ld_q, const void* k, int6
   if ((rc = check_rows("k", k, ld_k, h->H_kv, h->d, 2)) != MF_OK) return rc;
   if ((rc = check_rows("v", v, ld_v, h->H_kv, h->d, 2)) != MF_OK) return rc;
   if ((rc = check_rows("o", o, ld_o, h->H_q, h->d, 2)) != MF_OK) return rc;
+  if ((rc = check_aligned("lse", lse, 4)) != MF_OK) return rc;
   if ((rc = check_scale(scale)) != MF_OK) return rc;
   const int64_t wq = (int64_t)h->H_q * h->d, wk = (int64_t)h->H_kv * h->d, T = h->rows;
   if (overlap(q, ld_q, wq, T, o, ld_o, wq, T, 2) || overlap(k, ld_k, wk, T, o, ld_o, wq, T, 2) ||
@@ -556,6 +571,8 @@ int mf_attn_cached(mf_attn_t h, int n, const void* q, int64_t ld_q, const void* 
   if (dtype != MF_DTYPE_BF16) return fail(MF_ERR_UNSUPPORTED, "attention is built for bf16");
   if (!lens) return fail(MF_ERR_ARG, "lens is NULL");
   int rc;
+  if ((rc = check_aligned("lens", lens, 4)) != MF_OK) return rc;
+  if ((rc = check_aligned("lse", lse, 4)) != MF_OK) return rc;
   if ((rc = check_rows("q", q, ld_q, h->H_q, h->d, 2)) != MF_OK) return rc;
   if ((rc = check_rows("k_cache", k_cache, ld_k, h->H_kv, h->d, 2)) != MF_OK) return rc;
   if ((rc = check_rows("v_cache", v_cache, ld_v, h->H_kv, h->d, 2)) != MF_OK) return rc;

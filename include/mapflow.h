@@ -508,7 +508,7 @@ MF_API int mf_rope_frequencies(int rot_dim, double base, int scaling, double fac
  *                     memory apart from every input and the other output
  *   q_weight, k_weight  [d] (dtype, 16-byte aligned) or NULL (ones); NULL when
  *                     norm is 0
- *   positions         int32 [T] (any value, in any order)
+ *   positions         int32 [T] (any value, in any order), 4-byte aligned
  *   turns             DEVICE uint64 [rot_dim/2] as mf_rope_frequencies gives it
  *   d                 64 or 128; rot_dim even, 2 .. d
  * T = 0 is a no-op.  Errors: MF_ERR_ARG, MF_ERR_UNSUPPORTED, MF_ERR_CUDA.
@@ -530,7 +530,9 @@ typedef struct mf_attn_s* mf_attn_t; /* opaque; a plan for attention calls */
  *   H_q, H_kv        H_q % H_kv == 0, H_q / H_kv <= 128, H_q <= 1024; d 64 or 128
  *   window           >= 1, or 0: no window       n_sink   >= 0
  * The plan lays out the work on the host and copies its tables to the device
- * (synchronous); it serves any number of calls with these lengths.  Errors:
+ * (synchronous); it serves any number of calls with these lengths, up to 2^29
+ * tokens and 2^24 pairs of query tiles (of 128 / (H_q / H_kv) tokens each) over
+ * all KV heads (MF_ERR_UNSUPPORTED).  Errors:
  * MF_ERR_ARG, MF_ERR_UNSUPPORTED, MF_ERR_OOM, MF_ERR_CUDA.
  *
  * mf_attn_create_cache — a plan for up to n_max requests with Lq new tokens
@@ -571,9 +573,10 @@ MF_API int mf_attn_workspace(mf_attn_t h, int n, int64_t* bytes);
 /*
  * mf_attn_packed — o = softmax(scale * q k^T over the visible keys) v.
  *   q, o [T][H_q][d], k, v [T][H_kv][d]   bf16, T = cu_seqlens[n_seqs]; rows
- *                before a sequence's q_begin are neither read in q nor written
- *                in o and lse; o shares no memory with an input
- *   lse          fp32 [T][H_q] log of the softmax's denominator, or NULL
+ *                before a sequence's q_begin may hold anything in q and are
+ *                not written in o and lse; o shares no memory with an input
+ *   lse          fp32 [T][H_q] (4-byte aligned, as lens) log of the softmax's
+ *                denominator, or NULL
  *   dtype        MF_DTYPE_BF16 (MF_ERR_UNSUPPORTED otherwise)
  *   scale        > 0, e.g. 1/sqrt(d)
  * Asynchronous, no host synchronisation, no state kept in the plan between

@@ -58,7 +58,8 @@ def _rope(lib, **kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(q=None), E.MF_ERR_ARG), (dict(q_out=None), E.MF_ERR_ARG), (dict(k=None), E.MF_ERR_ARG),
-    (dict(pos=None), E.MF_ERR_ARG), (dict(turns=None), E.MF_ERR_ARG), (dict(q=PTR + 8), E.MF_ERR_ARG),
+    (dict(pos=None), E.MF_ERR_ARG), (dict(turns=None), E.MF_ERR_ARG),
+    (dict(pos=7 * PTR + 2), E.MF_ERR_ARG), (dict(turns=7 * PTR + 4), E.MF_ERR_ARG), (dict(q=PTR + 8), E.MF_ERR_ARG),
     (dict(ld_q=511), E.MF_ERR_ARG), (dict(ld_q=516), E.MF_ERR_ARG), (dict(ld_k=248), E.MF_ERR_ARG),
     (dict(rot=0), E.MF_ERR_ARG), (dict(rot=5), E.MF_ERR_ARG), (dict(rot=130), E.MF_ERR_ARG),
     (dict(layout=2), E.MF_ERR_ARG), (dict(norm=2), E.MF_ERR_ARG), (dict(norm=1, eps=0.0), E.MF_ERR_ARG),
@@ -96,6 +97,7 @@ def _packed(lib, cu=(0, 100), qb=None, H_q=4, H_kv=2, d=128, window=0, sinks=0, 
     (dict(H_q=2048, H_kv=2048), E.MF_ERR_UNSUPPORTED), (dict(window=-1), E.MF_ERR_ARG),
     (dict(sinks=-1), E.MF_ERR_ARG), (dict(qb=[101]), E.MF_ERR_ARG), (dict(qb=[-1]), E.MF_ERR_ARG),
     (dict(qb=[100]), E.MF_ERR_ARG), (dict(cu=[0, (1 << 29) + 1]), E.MF_ERR_UNSUPPORTED),
+    (dict(cu=[0, 1 << 29], H_q=64, H_kv=64), E.MF_ERR_UNSUPPORTED),    # tables of 2^27 runs
     (dict(alloc=mapflow.ALLOC_FN(lambda n, c, s: None)), E.MF_ERR_ARG)])
 def test_packed_plan_refuses(lib, kw, code):
     assert _packed(lib, **kw) == code
