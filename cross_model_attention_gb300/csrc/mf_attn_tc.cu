@@ -55,12 +55,15 @@ struct Lay {
   static constexpr int kBar = kRing + kStages * kTile;
   static constexpr int kMisc = kBar + 8 * (16 + 2 * kStages);
   static constexpr int kMiscBytes = 128;
-  static constexpr int kBytes = kMisc + kMiscBytes + 1024;
+  static constexpr int kFull = kMisc + kMiscBytes;  // cache form: bit per request
+  static constexpr int kBytes = kFull + 1024 + 1024;
 };
+constexpr int kFullBits = 8192;  // the requests that have one
 static_assert(Lay<128>::kBytes <= 232448 && Lay<64>::kBytes <= 232448, "shared memory");
 
 // misc words: [0] TMEM address, [1] abort, cache form: [2] first request, [4]
-// the lines before it, [5] all lines; from byte 64 on two barriers
+// the lines before it, [5] all lines; from byte 64 on two barriers; from byte
+// 128 on the first 8192 requests' bits, one where the cache holds a visible key
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 * stream each
 
@@ -289,6 +292,19 @@ struct CacheRuns {
       at = misc[4];
     }
   }
+  // to the next request with a key: a batch's unused slots cost nothing.  (One
+  // after another by their lengths, 246 of them between the first three and the last
+  // seven of 256 requests of 900 keys cost a call 72 us where it takes 22.)
+  __device__ void skip_empty() {
+    while (who < min(p.n, kFullBits)) {
+      const uint32_t w = static_cast<uint32_t>(misc[32 + (who >> 5)]) >> (who & 31);
+      if (w) {
+        who += __ffs(static_cast<int>(w)) - 1;
+        return;
+      }
+      who = (who | 31) + 1;
+    }
+  }
   __device__ bool next(Run& o) {
     for (;;) {
       if (at >= f1) {
@@ -351,6 +367,7 @@ struct CacheRuns {
       if (head >= p.H_kv) {
         head = 0;
         ++who;
+        if (!pre) skip_empty();
         if (pre ? who >= p.pre_pairs : who >= p.n) at = f1;  // past the last
       }
       if (some) return true;
@@ -362,40 +379,77 @@ struct CacheRuns {
 // in which this CTA's span begins with the length before it.
 __device__ __forceinline__ void cache_find(const AttnParams& p, volatile int* misc) {
   const int lane = threadIdx.x & 31;
-  constexpr int kKept = 8;  // the first 256 requests' lines stay in registers
-  int kept[kKept], sum = 0;
+  constexpr int kMany = 8, kChunk = 32 * kMany;  // requests whose lengths are asked for together
+  auto lines_of = [&](int r0, int (&line)[kMany]) {
 #pragma unroll
-  for (int i = 0; i < kKept; ++i) {
-    const int r = 32 * i + lane;
-    kept[i] = r < p.n ? cache_line(p, cache_unit(p, p.lens[r]).nb) : 0;
-    sum += kept[i];
+    for (int i = 0; i < kMany; ++i) {
+      const int r = r0 + 32 * i + lane;
+      line[i] = r < p.n ? cache_line(p, cache_unit(p, p.lens[r]).nb) : 0;
+    }
+  };
+  // Lane c keeps chunk c's length (of chunks past the 32nd only the sum is
+  // kept); the first chunk's lines stay in registers.
+  int kept[kMany], sum = 0, mine = 0;
+  auto take = [&](int r0, const int (&line)[kMany]) {
+    int part = 0;
+    unsigned word = 0;
+#pragma unroll
+    for (int i = 0; i < kMany; ++i) {
+      part += line[i];
+      const unsigned full = __ballot_sync(0xffffffffu, line[i] > 0);
+      if (lane == i) word = full;
+    }
+    if (lane < kMany && r0 < kFullBits) misc[32 + (r0 >> 5) + lane] = static_cast<int>(word);
+    part = __reduce_add_sync(0xffffffffu, part);
+    if (lane == r0 / kChunk) mine = part;
+    sum += part;
+  };
+  lines_of(0, kept);
+  take(0, kept);
+  for (int r0 = kChunk; r0 < p.n; r0 += kChunk) {
+    int line[kMany];
+    lines_of(r0, line);
+    take(r0, line);
   }
-  for (int r = 32 * kKept + lane; r < p.n; r += 32) sum += cache_line(p, cache_unit(p, p.lens[r]).nb);
-  sum = __reduce_add_sync(0xffffffffu, sum);
   const int f0 = min(sum, span_of(p, false, sum) * static_cast<int>(gridDim.x - 1 - blockIdx.x));
-  int first = p.n, before = sum, run = 0;
-  bool found = false;
-  auto look = [&](int r0, int line) {  // requests r0 .. r0 + 31
-    int inc = line;
+  int first = p.n, before = sum;
+  // the 32 values that begin at `run`: the lane whose value f0 falls in, or -1,
+  // and what lies before that lane's value
+  auto among = [&](int value, int run, int& at) {
+    int inc = value;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
     const unsigned hit = __ballot_sync(0xffffffffu, f0 < run + inc);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      first = r0 + l;
-      before = run + __shfl_sync(0xffffffffu, inc - line, l);
-      found = true;
+    if (hit == 0) {
+      at = run + __shfl_sync(0xffffffffu, inc, 31);
+      return -1;
     }
-    run += __shfl_sync(0xffffffffu, inc, 31);
+    const int l = __ffs(hit) - 1;
+    at = run + __shfl_sync(0xffffffffu, inc - value, l);
+    return l;
   };
+  if (f0 < sum) {
+    int run = 0, c = 0;
+    if (p.n > kChunk) c = among(mine, 0, run);
+    for (int r0 = (c < 0 ? 32 : c) * kChunk; first == p.n && r0 < p.n; r0 += kChunk) {
+      if (r0 > 0) lines_of(r0, kept);
 #pragma unroll
-  for (int i = 0; i < kKept; ++i)
-    if (!found && 32 * i < p.n) look(32 * i, kept[i]);
-  for (int r0 = 32 * kKept; !found && r0 < p.n; r0 += 32)
-    look(r0, r0 + lane < p.n ? cache_line(p, cache_unit(p, p.lens[r0 + lane]).nb) : 0);
+      for (int i = 0; i < kMany; ++i) {
+        if (first == p.n) {
+          int at;
+          const int l = among(kept[i], run, at);
+          if (l >= 0) {
+            first = r0 + 32 * i + l;
+            before = at;
+          }
+          run = at;
+        }
+      }
+    }
+  }
   if (lane == 0) {
     misc[2] = first;
     misc[4] = before;

@@ -407,6 +407,15 @@ def test_offsets_past_32_bits():
     assert (got[:3] == 0).all() and (small.attend(qd, ks, vs, lens)[:3] == 0).all()
 
 
+@pytest.mark.parametrize("P", [0, 300])
+def test_cache_mostly_unused_slots(P):
+    for n, used in ((256, (0, 31, 32, 200, 255)), (8300, (0, 8000, 8191, 8192, 8250, 8299)), (300, (299,))):
+        lens = [0] * n
+        for i, r in enumerate(used):
+            lens[r] = 40 - 3 * i
+        check_cache(lens, 1, 40, 2, 1, 64, P=P)
+
+
 def test_workspace_grows_with_requests_not_with_their_keys():
     # units + CTAs runs at most, two streams of a tile's 32 rows each
     for n, cap, P in ((1, 8192, 0), (512, 8192, 0), (512, 8, 32768)):
