@@ -48,6 +48,9 @@ constexpr int kBlock = 128;     // keys per block of the kernel
 // 13.9 / 17.1 / with one block 15.6 us.)
 constexpr int kMinSpan = 2;
 constexpr int kMaxTokens = kAttnFar;
+// One sequence's, cache's or prefix's keys: a run over them takes about a
+// second, and the kernel's waits give up after two.
+constexpr int kMaxKeys = 1 << 26;
 constexpr long long kMaxRuns = 1ll << 24;  // of a packed plan (its tables: 1 GB on the host)
 
 void* h_alloc(mf_attn_t h, size_t bytes) {
@@ -305,6 +308,7 @@ int mf_attn_create_packed(mf_attn_t* out, const int32_t* cu_seqlens_host, const 
     const long long len = (long long)cu_seqlens_host[s + 1] - cu_seqlens_host[s];
     if (len < 0) return fail(MF_ERR_ARG, "cu_seqlens must be non-decreasing (sequence %d)", s);
     const int qb = q_begin_host ? q_begin_host[s] : 0;
+    if (len > kMaxKeys) return fail(MF_ERR_UNSUPPORTED, "sequence %d has more than 2^26 tokens", s);
     if (qb < 0 || qb > len) return fail(MF_ERR_ARG, "q_begin[%d] = %d must be in [0, %lld]", s, qb, len);
     q_rows += len - qb;
     const int pair = 2 * (kBlock / (H_q / H_kv));
@@ -452,7 +456,7 @@ int mf_attn_create_cache(mf_attn_t* out, int n_max, int Lq, int capacity, int pr
     return fail(MF_ERR_UNSUPPORTED, "a shared prefix with a window");
   if ((long long)Lq * (H_q / H_kv) > kBlock)
     return fail(MF_ERR_UNSUPPORTED, "Lq * H_q / H_kv = %lld > 128 (use the packed form)", (long long)Lq * (H_q / H_kv));
-  if (capacity > kMaxTokens || prefix_len > kMaxTokens) return fail(MF_ERR_UNSUPPORTED, "more than 2^29 keys");
+  if (capacity > kMaxKeys || prefix_len > kMaxKeys) return fail(MF_ERR_UNSUPPORTED, "more than 2^26 keys");
   if ((long long)n_max * capacity > 0x7fffffffll || (long long)n_max * Lq > 0x7fffffffll / 1024)
     return fail(MF_ERR_UNSUPPORTED, "n_max = %d is too large", n_max);
   {  // the kernel lays all work end to end in 32 bits

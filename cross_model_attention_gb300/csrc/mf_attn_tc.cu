@@ -25,7 +25,8 @@
 // Warps 0-3 and 4-7: softmax of stream 0 and 1 (thread = row).  Warps 8 and
 // 10: the streams' products (one issuing warp for both spent 2.7 us on a
 // block pair whose products take 1.3).  Warp 9: TMA loads, K and V blocks of
-// 128 keys through one ring.
+// 128 keys through one ring.  Warp 11: the planner, which finds the CTA's runs
+// and lays them before the others.
 //
 // Masked keys: a row's hidden scores are replaced by -inf before anything is
 // done with them, and V rows that no row may see (past a range's end, where
@@ -43,7 +44,8 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kKeys = 128;   // keys per block
 constexpr int kHalf = 64;    // keys that the softmax takes at a time
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;
+constexpr int kRunSlots = 4;  // runs that the planner may be ahead
 
 template <int D>
 struct Lay {
@@ -53,17 +55,15 @@ struct Lay {
   static constexpr int kQ = 0;
   static constexpr int kRing = 2 * kTile;
   static constexpr int kBar = kRing + kStages * kTile;
-  static constexpr int kMisc = kBar + 8 * (16 + 2 * kStages);
-  static constexpr int kMiscBytes = 128;
-  static constexpr int kFull = kMisc + kMiscBytes;  // cache form: bit per request
+  static constexpr int kMisc = kBar + 8 * (16 + 2 * kStages + 2 * kRunSlots);
+  static constexpr int kRuns = kMisc + 32;            // the planner's runs
+  static constexpr int kFull = kRuns + 64 * kRunSlots;  // cache form: bit per request
   static constexpr int kBytes = kFull + 1024 + 1024;
 };
 constexpr int kFullBits = 8192;  // the requests that have one
 static_assert(Lay<128>::kBytes <= 232448 && Lay<64>::kBytes <= 232448, "shared memory");
 
-// misc words: [0] TMEM address, [1] abort, cache form: [2] first request, [4]
-// the lines before it, [5] all lines; from byte 64 on two barriers; from byte
-// 128 on the first 8192 requests' bits, one where the cache holds a visible key
+// misc words: [0] TMEM address, [1] abort; from byte 16 on two barriers
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 * stream each
 
@@ -151,7 +151,7 @@ __device__ __noinline__ void trim(uint8_t* stage, int valid) {
 
 // -------------------------------------------------------------------- runs --
 // What one run of key blocks is, for every role.
-struct Run {
+struct alignas(16) Run {
   int q_row, n_tok0, n_tok1;  // tokens of the tile(s); n_tok1 = 0: one tile
   int alt;                    // one tile, key blocks alternate between the streams
   int pos;                    // position of the first token
@@ -159,10 +159,11 @@ struct Run {
   int nb;                     // key blocks of a head
   int blk0, blk1;             // this run's: block j is block j % nb of head j / nb
   int head, heads;            // first KV head, KV heads of the tile
-  int kind;                   // kOwn, kPrefix (K and V are the shared ones), kCache
+  int kind;                   // kOwn, kPrefix (K and V are the shared ones), kCache, kEnd
   int part;                   // first partial index, or -1
 };
-enum { kOwn = 0, kPrefix = 1, kCache = 2 };
+enum { kOwn = 0, kPrefix = 1, kCache = 2, kEnd = 3 };
+static_assert(sizeof(Run) == 64, "a slot of the planner's");
 
 // Block j of a run: its head (of the tile's), first key and how many count.
 __device__ __forceinline__ void block_at(const Run& r, int j, int& hh, int& j0, int& valid) {
@@ -177,13 +178,19 @@ __device__ __forceinline__ void block_at(const Run& r, int j, int& hh, int& j0, 
   valid = min(kKeys, (in_a ? r.a1 : r.b1) - j0);
 }
 
+struct NoRuns {
+  __device__ NoRuns(const AttnParams&, volatile uint8_t*) {}
+  __device__ bool next(Run&) { return false; }
+};
+
 // The runs of this CTA in order, packed form: from the plan's table.
 struct PackedRuns {
   static constexpr int kUnrollHalves = 1;
+  static constexpr bool kPlanned = false;
   const AttnParams& p;
   int i, end;
   AttnSeg nxt;
-  __device__ PackedRuns(const AttnParams& p_, const volatile int*) : p(p_) {
+  __device__ PackedRuns(const AttnParams& p_, volatile uint8_t*) : p(p_) {
     i = p.cta_segs[blockIdx.x];
     end = p.cta_segs[blockIdx.x + 1];
     if (i < end) nxt = p.segs[i];
@@ -261,22 +268,28 @@ __device__ __forceinline__ int span_of(const AttnParams& p, bool pre, int suffix
 
 struct CacheRuns {
   static constexpr int kUnrollHalves = 2;
+  static constexpr bool kPlanned = true;
   const AttnParams& p;
-  int todo;                  // parts left: 2, 1, 0
-  bool pre;                  // the part at hand is the prefix
-  int f0, f1, per;           // this CTA's span of it
-  int at;                    // start of the unit's line
-  int who, head;             // tile pair or request, (first) KV head
-  // (little is kept: these registers are live through the softmax)
-  const volatile int* misc;  // [2] first request, [4] the lines before it, [5] all requests' lines
-  __device__ CacheRuns(const AttnParams& p_, const volatile int* misc_) : p(p_), misc(misc_) {
+  const volatile uint8_t* full;  // bit per request, one where its cache has a unit
+  int todo;                      // parts left: 2, 1, 0
+  bool pre;                      // the part at hand is the prefix
+  int f0, f1, per;               // this CTA's span of it
+  int at;                        // start of the unit's line
+  int who, head;                 // tile pair or request, (first) KV head
+  // all requests' lines, the request in which this CTA's span of them begins
+  // and the lines before it
+  int suffix, first, before;
+  // (by a whole warp)
+  __device__ CacheRuns(const AttnParams& p_, volatile uint8_t* full_) : p(p_), full(full_) {
+    find(full_);
     todo = 2;
     pre = (blockIdx.x & 1) == 0;
     begin();
   }
+  __device__ void find(volatile uint8_t* bits);
   __device__ int pre_line() const { return kCostPre + p.pre_blocks; }
   __device__ void begin() {
-    const int suffix = misc[5], total = pre ? pre_lines(p) : suffix;
+    const int total = pre ? pre_lines(p) : suffix;
     per = span_of(p, pre, suffix);
     // (from the other end of the CTAs: two short lists meet late)
     f0 = min(total, per * static_cast<int>(pre ? blockIdx.x : gridDim.x - 1 - blockIdx.x));
@@ -287,9 +300,9 @@ struct CacheRuns {
       head = unit - who * p.H_kv;
       at = unit * pre_line();
     } else {
-      who = misc[2];
+      who = first;
       head = 0;
-      at = misc[4];
+      at = before;
     }
   }
   // to the next request with a key: a batch's unused slots cost nothing.  (One
@@ -297,12 +310,12 @@ struct CacheRuns {
   // seven of 256 requests of 900 keys cost a call 72 us where it takes 22.)
   __device__ void skip_empty() {
     while (who < min(p.n, kFullBits)) {
-      const uint32_t w = static_cast<uint32_t>(misc[32 + (who >> 5)]) >> (who & 31);
+      const uint32_t w = static_cast<uint32_t>(full[who >> 3]) >> (who & 7);
       if (w) {
         who += __ffs(static_cast<int>(w)) - 1;
         return;
       }
-      who = (who | 31) + 1;
+      who = (who | 7) + 1;
     }
   }
   __device__ bool next(Run& o) {
@@ -358,7 +371,7 @@ struct CacheRuns {
         // up from run to run, so their sum tells the runs' results apart.
         o.part = 2 * (unit + f0 / per);
         // for the join: block j of the unit is in span (x + j) / y
-        if (o.blk1 == nb && threadIdx.x == 0)
+        if (o.blk1 == nb)
           p.cuts[pre ? unit : p.pre_pairs * p.H_kv + unit] = make_int2(begins, per);
       }
       // the next unit
@@ -375,85 +388,60 @@ struct CacheRuns {
   }
 };
 
-// Cache form, first warp: the length of all requests' lines, and the request
-// in which this CTA's span begins with the length before it.
-__device__ __forceinline__ void cache_find(const AttnParams& p, volatile int* misc) {
+// The length of all requests' lines, and the request in which this CTA's span
+// begins with the length before it.  A lane sums the lines of consecutive
+// requests, eight lengths asked for at a time, and the lanes' sums tell in whose
+// part the span begins.
+__device__ __forceinline__ void CacheRuns::find(volatile uint8_t* bits) {
   const int lane = threadIdx.x & 31;
-  constexpr int kMany = 8, kChunk = 32 * kMany;  // requests whose lengths are asked for together
-  auto lines_of = [&](int r0, int (&line)[kMany]) {
+  const int share = max(8, ((p.n + 31) / 32 + 7) & ~7), mine = lane * share;
+  int sum = 0;
+#pragma unroll 2
+  for (int r = mine; r < min(p.n, mine + share); r += 8) {
+    int len[8];
 #pragma unroll
-    for (int i = 0; i < kMany; ++i) {
-      const int r = r0 + 32 * i + lane;
-      line[i] = r < p.n ? cache_line(p, cache_unit(p, p.lens[r]).nb) : 0;
-    }
-  };
-  // Lane c keeps chunk c's length (of chunks past the 32nd only the sum is
-  // kept); the first chunk's lines stay in registers.
-  int kept[kMany], sum = 0, mine = 0;
-  auto take = [&](int r0, const int (&line)[kMany]) {
-    int part = 0;
-    unsigned word = 0;
+    for (int i = 0; i < 8; ++i) len[i] = r + i < p.n ? __ldg(p.lens + r + i) : 0;
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < kMany; ++i) {
-      part += line[i];
-      const unsigned full = __ballot_sync(0xffffffffu, line[i] > 0);
-      if (lane == i) word = full;
+    for (int i = 0; i < 8; ++i) {
+      const int line = cache_line(p, cache_unit(p, len[i]).nb);
+      sum += line;
+      m |= line > 0 ? 1u << i : 0u;
     }
-    if (lane < kMany && r0 < kFullBits) misc[32 + (r0 >> 5) + lane] = static_cast<int>(word);
-    part = __reduce_add_sync(0xffffffffu, part);
-    if (lane == r0 / kChunk) mine = part;
-    sum += part;
-  };
-  lines_of(0, kept);
-  take(0, kept);
-  for (int r0 = kChunk; r0 < p.n; r0 += kChunk) {
-    int line[kMany];
-    lines_of(r0, line);
-    take(r0, line);
+    if (r < kFullBits) bits[r >> 3] = static_cast<uint8_t>(m);
   }
-  const int f0 = min(sum, span_of(p, false, sum) * static_cast<int>(gridDim.x - 1 - blockIdx.x));
-  int first = p.n, before = sum;
-  // the 32 values that begin at `run`: the lane whose value f0 falls in, or -1,
-  // and what lies before that lane's value
-  auto among = [&](int value, int run, int& at) {
+  __syncwarp();
+  suffix = __reduce_add_sync(0xffffffffu, sum);
+  const int f = min(suffix, span_of(p, false, suffix) * static_cast<int>(gridDim.x - 1 - blockIdx.x));
+  first = p.n;
+  before = suffix;
+  if (f >= suffix) return;
+  // of 32 values that begin at `run`: the lane whose value f falls in, or -1
+  // where all lie before it; run moves to that lane's beginning, or past them
+  auto among = [&](int value, int& run) {
     int inc = value;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, f0 < run + inc);
-    if (hit == 0) {
-      at = run + __shfl_sync(0xffffffffu, inc, 31);
-      return -1;
-    }
-    const int l = __ffs(hit) - 1;
-    at = run + __shfl_sync(0xffffffffu, inc - value, l);
+    const unsigned hit = __ballot_sync(0xffffffffu, f < run + inc);
+    const int l = hit ? __ffs(static_cast<int>(hit)) - 1 : -1;
+    run += hit ? __shfl_sync(0xffffffffu, inc - value, l) : __shfl_sync(0xffffffffu, inc, 31);
     return l;
   };
-  if (f0 < sum) {
-    int run = 0, c = 0;
-    if (p.n > kChunk) c = among(mine, 0, run);
-    for (int r0 = (c < 0 ? 32 : c) * kChunk; first == p.n && r0 < p.n; r0 += kChunk) {
-      if (r0 > 0) lines_of(r0, kept);
-#pragma unroll
-      for (int i = 0; i < kMany; ++i) {
-        if (first == p.n) {
-          int at;
-          const int l = among(kept[i], run, at);
-          if (l >= 0) {
-            first = r0 + 32 * i + l;
-            before = at;
-          }
-          run = at;
-        }
-      }
+  int run = 0;
+  const int part = among(sum, run) * share;
+  for (int r = part; first == p.n; r += 32) {  // (f lies in this part)
+    const int at_r = r + lane;
+    const bool in = at_r < min(p.n, part + share);
+    const int l = among(in ? cache_line(p, cache_unit(p, __ldg(p.lens + at_r)).nb) : 0, run);
+    if (l >= 0) {
+      first = r + l;
+      before = run;
+    } else if (r - part >= share) {
+      break;  // not reached
     }
-  }
-  if (lane == 0) {
-    misc[2] = first;
-    misc[4] = before;
-    misc[5] = sum;
   }
 }
 
@@ -491,6 +479,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto barO = [&](int s, int h) { return sb + L::kBar + 96 + 8u * (2 * s + h); };
   auto barFull = [&](int i) { return sb + L::kBar + 128 + 8u * i; };
   auto barEmpty = [&](int i) { return sb + L::kBar + 128 + 8u * (NS + i); };
+  auto barRun = [&](int i) { return sb + L::kBar + 128 + 8u * (2 * NS + i); };
+  auto barRunFree = [&](int i) { return sb + L::kBar + 128 + 8u * (2 * NS + kRunSlots + i); };
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up
   if (threadIdx.x == 9 * 32) {
@@ -519,6 +509,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(barFull(i), 1);
       mbar_init(barEmpty(i), 2);
     }
+    for (int i = 0; i < kRunSlots; ++i) {
+      mbar_init(barRun(i), 1);
+      mbar_init(barRunFree(i), 11);  // all other warps
+    }
     fence_mbar_init();
     misc[1] = 0;
   }
@@ -531,13 +525,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           make_uint4(0u, 0u, 0u, 0u);
     fence_async_smem();
   }
-  if (cached && warp == 0) cache_find(p, misc);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(uniform(misc[0]));
-  Runs runs(p, misc);
+  // The CTA's runs.  The packed form's come from a table, each warp reads them
+  // for itself; the cache form's are worked out by the planner.
   Run r{};
+  using Own = typename std::conditional<Runs::kPlanned, NoRuns, Runs>::type;
+  Own own(p, nullptr);
+  int run_slot = 0;
+  uint32_t run_ph = 0;
+  // The next run, for a warp (LANE: for its first lane alone); false after the
+  // last or when something has given up.
+  auto next_run = [&](auto one) {
+    if (!Runs::kPlanned) return own.next(r);
+    if (one.value) {
+      if (misc[1] || !mbar_wait(barRun(run_slot), run_ph, p.err)) return false;
+    } else {
+      if (!warp_wait(barRun(run_slot), run_ph, p.err, misc)) return false;
+    }
+    r = *reinterpret_cast<const Run*>(smem + L::kRuns + 64 * run_slot);
+    if (!one.value) __syncwarp();
+    if (lane == 0) mbar_arrive(barRunFree(run_slot));
+    if (++run_slot == kRunSlots) {
+      run_slot = 0;
+      run_ph ^= 1;
+    }
+    return r.kind != kEnd;
+  };
   // Who waits for the ring.  A barrier's phase is told from the one before it
   // only, so no use of a stage may pass unseen: both streams' MMA warps see
   // every use in turn, the other stream's too, and a stage is free when both
@@ -563,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       r.k_row0 + j0, barFull(st));
         ++g;
       };
-      while (ok && runs.next(r)) {
+      while (ok && next_run(std::true_type())) {
         const CUtensorMap* mk = r.kind == kPrefix ? &tkp : &tk;
         const CUtensorMap* mv = r.kind == kPrefix ? &tvp : &tv;
         const CUtensorMap* mq = r.kind == kCache ? &tqc : &tq;
@@ -660,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     };
-    while (ok && uniform(runs.next(r))) {
+    while (ok && uniform(next_run(std::false_type()))) {
       const int nb = uniform(r.blk1 - r.blk0);
       const int alt = uniform(r.alt), two = uniform(r.n_tok1 > 0);
       const int ahead = alt ? 2 : 1;
@@ -763,13 +779,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok) misc[1] = 1;
     // everything issued is done before TMEM is freed and the CTA ends
     if (lane == 0) {
-      const uint32_t done = sb + L::kMisc + 64 + 8 * s;
+      const uint32_t done = sb + L::kMisc + 16 + 8 * s;
       mbar_init(done, 1);
       fence_mbar_init();
       tc_commit(done);
       mbar_wait(done, 0, nullptr);
     }
     __syncwarp();
+  } else if (warp == 11) {
+    // ------------------------------------------------------------ planner
+    if constexpr (Runs::kPlanned) {
+      Runs runs(p, smem + L::kFull);
+      if (lane == 0) {
+        for (bool more = true; more;) {
+          Run x{};
+          more = runs.next(x);
+          if (!more) x.kind = kEnd;
+          if (misc[1] || !mbar_wait(barRunFree(run_slot), run_ph ^ 1, p.err)) {
+            misc[1] = 1;
+            break;
+          }
+          *reinterpret_cast<Run*>(smem + L::kRuns + 64 * run_slot) = x;
+          mbar_arrive(barRun(run_slot));
+          if (++run_slot == kRunSlots) {
+            run_slot = 0;
+            run_ph ^= 1;
+          }
+        }
+      }
+      __syncwarp();
+    }
   } else {
     // ------------------------------------------------------------ softmax
     const int s = warp >> 2;
@@ -785,7 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool wide = ((reinterpret_cast<uintptr_t>(p.o) | static_cast<uintptr_t>(p.ld_o * 2)) & 31) == 0;
     uint32_t ph = 0, o_ph = 0;  // phases of both halves' S, and of the runs' last products
     bool ok = true;
-    while (ok && runs.next(r)) {
+    while (ok && next_run(std::false_type())) {
       const int tile = r.alt ? 0 : s;
       if (!r.alt && s == 1 && r.n_tok1 == 0) continue;
       const int n_tok = tile ? r.n_tok1 : r.n_tok0;

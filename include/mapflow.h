@@ -530,13 +530,14 @@ typedef struct mf_attn_s* mf_attn_t; /* opaque; a plan for attention calls */
  *   H_q, H_kv        H_q % H_kv == 0, H_q / H_kv <= 128, H_q <= 1024; d 64 or 128
  *   window           >= 1, or 0: no window       n_sink   >= 0
  * The plan lays out the work on the host and copies its tables to the device
- * (synchronous); it serves any number of calls with these lengths, up to 2^29
- * tokens and 2^24 pairs of query tiles (of 128 / (H_q / H_kv) tokens each) over
- * all KV heads (MF_ERR_UNSUPPORTED).  Errors:
+ * (synchronous); it serves any number of calls with these lengths, up to 2^26
+ * tokens a sequence, 2^29 in all and 2^24 pairs of query tiles (of 128 / (H_q /
+ * H_kv) tokens each) over all KV heads (MF_ERR_UNSUPPORTED).  Errors:
  * MF_ERR_ARG, MF_ERR_UNSUPPORTED, MF_ERR_OOM, MF_ERR_CUDA.
  *
  * mf_attn_create_cache — a plan for up to n_max requests with Lq new tokens
  * each (their keys and values already in the caches), Lq * H_q / H_kv <= 128.
+ * capacity and prefix_len are at most 2^26 (MF_ERR_UNSUPPORTED).
  * Request r's cache is rows r * capacity .. of the cache tensors, of which
  * lens[r] hold keys; new token t is at position p = lens[r] - Lq + t and sees
  * keys j <= p of the cache with p - j < window or j < n_sink.  With

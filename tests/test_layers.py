@@ -97,7 +97,8 @@ def _packed(lib, cu=(0, 100), qb=None, H_q=4, H_kv=2, d=128, window=0, sinks=0, 
     (dict(H_q=2048, H_kv=2048), E.MF_ERR_UNSUPPORTED), (dict(window=-1), E.MF_ERR_ARG),
     (dict(sinks=-1), E.MF_ERR_ARG), (dict(qb=[101]), E.MF_ERR_ARG), (dict(qb=[-1]), E.MF_ERR_ARG),
     (dict(qb=[100]), E.MF_ERR_ARG), (dict(cu=[0, (1 << 29) + 1]), E.MF_ERR_UNSUPPORTED),
-    (dict(cu=[0, 1 << 29], H_q=64, H_kv=64), E.MF_ERR_UNSUPPORTED),    # tables of 2^27 runs
+    (dict(cu=[0, (1 << 26) + 1]), E.MF_ERR_UNSUPPORTED),
+    (dict(cu=[i << 26 for i in range(8)] + [(7 << 26) + 5], H_q=64, H_kv=64), E.MF_ERR_UNSUPPORTED),  # 2^27 runs
     (dict(alloc=mapflow.ALLOC_FN(lambda n, c, s: None)), E.MF_ERR_ARG)])
 def test_packed_plan_refuses(lib, kw, code):
     assert _packed(lib, **kw) == code
@@ -108,7 +109,8 @@ def test_packed_plan_refuses(lib, kw, code):
     (dict(n=0), E.MF_ERR_ARG), (dict(Lq=0), E.MF_ERR_ARG), (dict(cap=0), E.MF_ERR_ARG), (dict(P=-1), E.MF_ERR_ARG),
     (dict(P=10, window=5), E.MF_ERR_UNSUPPORTED), (dict(P=10, sinks=5), E.MF_ERR_UNSUPPORTED),
     (dict(Lq=65), E.MF_ERR_UNSUPPORTED), (dict(n=70000, cap=70000), E.MF_ERR_UNSUPPORTED),
-    (dict(n=1 << 22), E.MF_ERR_UNSUPPORTED), (dict(cap=(1 << 29) + 1), E.MF_ERR_UNSUPPORTED),
+    (dict(n=1 << 22), E.MF_ERR_UNSUPPORTED), (dict(cap=(1 << 26) + 1), E.MF_ERR_UNSUPPORTED),
+    (dict(P=(1 << 26) + 1), E.MF_ERR_UNSUPPORTED),
     (dict(d=32), E.MF_ERR_UNSUPPORTED), (dict(H_q=5), E.MF_ERR_ARG)])
 def test_cache_plan_refuses(lib, kw, code):
     a = dict(n=2, Lq=1, cap=64, P=0, H_q=4, H_kv=2, d=128, window=0, sinks=0)
