@@ -1027,55 +1027,61 @@ __global__ void __launch_bounds__(kThreads, 1)
 // -------------------------------------------------------------------- join --
 // o = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p over a row's partial
 // results, in their order (the same result every time); a row without any
-// visible key gets 0 and lse = -inf.  A warp per row, lanes over d.
-template <int D, bool CACHED>
+// visible key gets 0 and lse = -inf.  A warp takes RW rows, 32 / RW lanes over d
+// each.
+template <int D, bool CACHED, int RW>
 __global__ void __launch_bounds__(256) join_kernel(const AttnParams p, const AttnJoin* joins, int n_joins) {
-  constexpr int V = D / 32;  // values per lane
-  const int lane = threadIdx.x & 31;
+  constexpr int LPR = 32 / RW;   // lanes of a row
+  constexpr int V = D / LPR;     // values per lane, in vectors LPR vectors apart
+  using Vec = typename std::conditional<V == 2, float2, float4>::type;
+  constexpr int NW = sizeof(Vec) / 4, NV = V / NW;
+  const int lane = threadIdx.x % LPR;
   // launched while the attention kernel still runs; its results are there
   // from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long w = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  // (at most 2^31 rows; 64-bit divisions would take as long as the rest)
+  const unsigned w = blockIdx.x * (blockDim.x / LPR) + threadIdx.x / LPR;
   // A row's partial results: n0 of the prefix or of a packed tile, then n1 of
   // its cache.  Result i: part first + i * step (in halves of a slot), rows
   // apart by the tile's.
-  long long q_tok, at0 = 0, at1 = 0, step0 = 0;
-  int head, n0 = 0, n1 = 0;
+  long long at0 = 0, at1 = 0, step0 = 0;
+  int q_tok = 0, head = 0, n0 = 0, n1 = 0;
+  bool live = true;  // (four rows to a warp: a last warp's rows may be past the end)
   if (CACHED) {
-    if (w >= static_cast<long long>(p.n) * p.Lq * p.H_q) return;
-    q_tok = w / p.H_q;
-    head = static_cast<int>(w - q_tok * p.H_q);
-    const int kv = head / p.G, hg = head - kv * p.G, req = static_cast<int>(q_tok / p.Lq);
-    const int grid = p.grid;
-    // (slots are held to what the buffers have, whatever a failed run left)
-    auto slots = [&](int unit, int2 cut, int b0, int b1, int& slot) {
-      const int c0 = min(max((cut.x + b0) / cut.y, 0), grid - 1);
-      const int c1 = min(max((cut.x + b1) / cut.y, c0), grid - 1);
-      slot = unit + c0;
-      return c1 - c0 + 1;
-    };
-    if (p.pre_pairs > 0) {
-      const int tile = static_cast<int>(q_tok / p.TQ), pair = tile >> 1, unit = pair * p.H_kv + kv;
-      int slot;
-      n0 = slots(unit, p.cuts[unit], 0, p.pre_blocks - 1, slot);
-      // a pair's tiles have a stream each; a lone last tile ran on both
-      const bool lone = (2ll * pair + 1) * p.TQ >= static_cast<long long>(p.n) * p.Lq;
-      step0 = (lone ? 1 : 2) * kRows;
-      at0 = static_cast<long long>(2 * slot + (lone ? 0 : tile & 1)) * kRows +
-            (q_tok - static_cast<long long>(tile) * p.TQ) * p.G + hg;
-      if (lone) n0 *= 2;
-    }
-    const int nb = cache_unit(p, p.lens[req]).nb;
-    if (nb > 0) {  // the pieces with blocks of the row's head
-      const int hh = kv % p.HG, unit = req * p.groups + kv / p.HG;
-      int slot;
-      n1 = 2 * slots(unit, p.cuts[p.pre_pairs * p.H_kv + unit], hh * nb, hh * nb + nb - 1, slot);
-      at1 = p.suf_base + 2ll * slot * p.suf_rows +
-            (static_cast<int>(q_tok - static_cast<long long>(req) * p.Lq) * p.HG + hh) * p.G + hg;
+    live = w < static_cast<unsigned>(p.n * p.Lq) * p.H_q;
+    if (live) {
+      q_tok = static_cast<int>(w / p.H_q);
+      head = static_cast<int>(w - static_cast<unsigned>(q_tok) * p.H_q);
+      const int kv = head / p.G, hg = head - kv * p.G, req = q_tok / p.Lq;
+      const int grid = p.grid;
+      // (slots are held to what the buffers have, whatever a failed run left)
+      auto slots = [&](int unit, int2 cut, int b0, int b1, int& slot) {
+        const int c0 = min(max((cut.x + b0) / cut.y, 0), grid - 1);
+        const int c1 = min(max((cut.x + b1) / cut.y, c0), grid - 1);
+        slot = unit + c0;
+        return c1 - c0 + 1;
+      };
+      if (p.pre_pairs > 0) {
+        const int tile = q_tok / p.TQ, pair = tile >> 1, unit = pair * p.H_kv + kv;
+        int slot;
+        n0 = slots(unit, p.cuts[unit], 0, p.pre_blocks - 1, slot);
+        // a pair's tiles have a stream each; a lone last tile ran on both
+        const bool lone = (2 * pair + 1) * p.TQ >= p.n * p.Lq;
+        step0 = (lone ? 1 : 2) * kRows;
+        at0 = static_cast<long long>(2 * slot + (lone ? 0 : tile & 1)) * kRows + (q_tok - tile * p.TQ) * p.G + hg;
+        if (lone) n0 *= 2;
+      }
+      const int nb = cache_unit(p, p.lens[req]).nb;
+      if (nb > 0) {  // the pieces with blocks of the row's head
+        const int hh = kv % p.HG, unit = req * p.groups + kv / p.HG;
+        int slot;
+        n1 = 2 * slots(unit, p.cuts[p.pre_pairs * p.H_kv + unit], hh * nb, hh * nb + nb - 1, slot);
+        at1 = p.suf_base + 2ll * slot * p.suf_rows + ((q_tok - req * p.Lq) * p.HG + hh) * p.G + hg;
+      }
     }
   } else {
-    const long long j = w / kRows;
-    if (j >= n_joins) return;
+    const unsigned j = w / kRows;
+    if (j >= static_cast<unsigned>(n_joins)) return;  // (a whole warp)
     const AttnJoin jn = joins[j];
     const int row = static_cast<int>(w - j * kRows), tok = row / p.G;
     if (tok >= jn.n_tok) return;
@@ -1086,21 +1092,25 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p, const Att
     step0 = static_cast<long long>(jn.step) * kRows;
   }
   auto at = [&](int i) { return i < n0 ? at0 + i * step0 : at1 + static_cast<long long>(i - n0) * p.suf_rows; };
-  const int n = n0 + n1;
+  const int n = n0 + n1, n_warp = RW == 1 ? n : __reduce_max_sync(0xffffffffu, n);
   float top = -INFINITY, l = 0.f, acc[V] = {};
-  constexpr int kAtOnce = 16;  // results of o asked for together, before their weights are known
-  using Vec = typename std::conditional<V == 4, float4, float2>::type;
-  for (int b = 0; b < n; b += kAtOnce) {
+  // results of o asked for together, before their weights are known
+  constexpr int kAtOnce = RW == 1 ? 16 : 64 / V < LPR ? 64 / V : LPR;
+  for (int b = 0; b < n_warp; b += kAtOnce) {
     const int m = min(kAtOnce, n - b);
     const float2 ml = lane < m ? p.part_ml[at(b + lane)] : make_float2(-INFINITY, 0.f);
-    Vec v[kAtOnce];
+    Vec v[kAtOnce][NV];
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i)
-      if (i < m) v[i] = *reinterpret_cast<const Vec*>(p.part_o + at(b + i) * D + lane * V);
+      if (i < m) {
+#pragma unroll
+        for (int c = 0; c < NV; ++c)
+          v[i][c] = *reinterpret_cast<const Vec*>(p.part_o + at(b + i) * D + (c * LPR + lane) * NW);
+      }
     float mx = ml.x;
 #pragma unroll
     for (int o = kAtOnce / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o, kAtOnce));
-    mx = __shfl_sync(0xffffffffu, mx, 0);
+    mx = __shfl_sync(0xffffffffu, mx, 0, LPR);
     const float was = top;
     top = fmaxf(top, mx);
     const float f = was == -INFINITY ? 0.f : ex2(was - top);
@@ -1110,12 +1120,12 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p, const Att
     for (int e = 0; e < V; ++e) acc[e] *= f;
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i), li = __shfl_sync(0xffffffffu, ml.y, i);
+      const float wi = __shfl_sync(0xffffffffu, w, i, LPR), li = __shfl_sync(0xffffffffu, ml.y, i, LPR);
       // (one that saw nothing has sum 0, and its o was perhaps not written; a sum
       // that is NaN comes through with weight 0 too)
       if (i < m && li != 0.f) {
         l += wi * li;
-        const float* x = reinterpret_cast<const float*>(&v[i]);
+        const float* x = reinterpret_cast<const float*>(v[i]);
 #pragma unroll
         for (int e = 0; e < V; ++e) acc[e] += wi * x[e];
       }
@@ -1123,26 +1133,31 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p, const Att
   }
   const bool none = l == 0.f;
   const float inv = none ? 0.f : 1.f / l;
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + q_tok * p.ld_o + static_cast<long long>(head) * D + lane * V;
-  if (V == 4)
-    *reinterpret_cast<uint2*>(dst) =
-        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[V - 2] * inv, acc[V - 1] * inv));
-  else
-    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+  if (!live) return;
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + q_tok * p.ld_o + head * D + lane * NW;
+#pragma unroll
+  for (int c = 0; c < NV; ++c) {
+    const float* x = acc + c * NW;
+    if (NW == 4)
+      *reinterpret_cast<uint2*>(dst + c * LPR * NW) =
+          make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[NW - 2] * inv, x[NW - 1] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(dst + c * LPR * NW) = pack_bf16x2(x[0] * inv, x[1] * inv);
+  }
   if (p.lse && lane == 0)
-    p.lse[q_tok * p.H_q + head] = none ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+    p.lse[static_cast<long long>(q_tok) * p.H_q + head] = none ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
 }
 
 // The join kernel may be set up while the attention kernel before it in the
 // stream runs (it waits for its end on the device).
-template <int D, bool CACHED>
+template <int D, bool CACHED, int RW>
 cudaError_t launch_dependent(int grid, cudaStream_t s,
                              const AttnParams& p, const AttnJoin* joins, int n_joins) {
   cudaLaunchAttribute at{};
   // (the attention kernel takes nearly all of an SM's memory as shared memory;
   // a kernel that wants another split beside it makes the SMs change over, twice
   // per call)
-  auto kern = join_kernel<D, CACHED>;
+  auto kern = join_kernel<D, CACHED, RW>;
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = once_per_device(done, [&] {
     return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
@@ -1184,8 +1199,8 @@ cudaError_t launch_attn_packed(const AttnParams& p, int d, int grid, const CUten
 cudaError_t launch_attn_join(const AttnParams& p, int d, const AttnJoin* joins, int n_joins, cudaStream_t s) {
   if (n_joins <= 0) return cudaSuccess;
   const int grid = n_joins * (kRows / 8);
-  return d == 128 ? launch_dependent<128, false>(grid, s, p, joins, n_joins)
-                  : launch_dependent<64, false>(grid, s, p, joins, n_joins);
+  return d == 128 ? launch_dependent<128, false, 1>(grid, s, p, joins, n_joins)
+                  : launch_dependent<64, false, 1>(grid, s, p, joins, n_joins);
 }
 
 cudaError_t launch_attn_cache(const AttnParams& p, int d, int grid, const CUtensorMap& tq,
@@ -1194,10 +1209,16 @@ cudaError_t launch_attn_cache(const AttnParams& p, int d, int grid, const CUtens
   cudaError_t e = d == 128 ? launch_main<128, CacheRuns>(p, grid, tq, tk, tv, tkp, tvp, tqc, true, s)
                            : launch_main<64, CacheRuns>(p, grid, tq, tk, tv, tkp, tvp, tqc, true, s);
   if (e != cudaSuccess) return e;
-  const long long blocks = (static_cast<long long>(p.n) * p.Lq * p.H_q + 7) / 8;
+  // More rows than the SMs take at once: four to a warp of the join.  (One /
+  // four: 64 requests of 512 over a 16384-token prefix 46.5 / 50.0 us, 256 of
+  // 500 104 / 97 us, 1024 of 200 215 / 191 us.)
+  const long long rows = static_cast<long long>(p.n) * p.Lq * p.H_q;
+  const bool many = rows > 32ll * grid;
+  const long long blocks = many ? (rows + 31) / 32 : (rows + 7) / 8;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  return d == 128 ? launch_dependent<128, true>(static_cast<int>(blocks), s, p, nullptr, 0)
-                  : launch_dependent<64, true>(static_cast<int>(blocks), s, p, nullptr, 0);
+  const int g = static_cast<int>(blocks);
+  if (many) return d == 128 ? launch_dependent<128, true, 4>(g, s, p, nullptr, 0) : launch_dependent<64, true, 4>(g, s, p, nullptr, 0);
+  return d == 128 ? launch_dependent<128, true, 1>(g, s, p, nullptr, 0) : launch_dependent<64, true, 1>(g, s, p, nullptr, 0);
 }
 
 }  // namespace mf
