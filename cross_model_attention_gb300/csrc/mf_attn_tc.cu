@@ -853,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          if (idle) {
+          if (idle || kHalf * h >= valid) {  // (or a half without keys: it has no product)
             if (lane == 0) mbar_arrive(barP(s, h));
             continue;
           }

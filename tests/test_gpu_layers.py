@@ -159,6 +159,9 @@ def check_packed(lens, H_q, H_kv, d, window=None, sinks=0, begin=None, seed=0, q
     ([1000, 0, 37], 3, 3, 128, 1, 1),        # each row sees itself and the first token
     ([900], 4, 4, 64, 2000, 5),              # window longer than the sequence
     ([260], 128, 1, 128, None, 0),           # one token per tile
+    ([500, 321], 8, 2, 128, 64, 64),         # sinks and windows that end with a half block, and one past it
+    ([700, 450], 4, 2, 64, 129, 65),
+    ([385, 64, 65, 63], 4, 4, 128, 190, 1),
     ([90], 100, 1, 64, 17, 2),               # tiles with spare rows
 ])
 def test_packed(lens, H_q, H_kv, d, window, sinks):
@@ -286,6 +289,9 @@ def check_cache(lens, Lq, cap, H_q, H_kv, d, window=None, sinks=0, P=0, n_max=No
     ([2000, 1, 777, 1500], 1, 2048, 32, 8, 128, 500, 4),
     ([2000, 900], 2, 2000, 24, 8, 128, 256, 300),      # more sinks than a block
     ([40, 41, 42], 32, 64, 4, 1, 128, None, 0),        # 128 rows of one request
+    ([63, 64, 65, 191, 192, 193, 320], 1, 320, 8, 2, 128, None, 0),
+    ([400, 193, 130, 129, 66], 1, 400, 8, 2, 64, 64, 1),
+    ([400, 350, 260, 129, 66], 2, 400, 4, 2, 128, 127, 64),
     ([-5, 99], 1, 64, 2, 1, 128, None, 0),             # lengths held to the capacity
     ([6000], 1, 6000, 2, 1, 128, None, 0),             # one request over every CTA
 ])
