@@ -44,8 +44,8 @@ namespace {
 
 constexpr int kBlock = 128;     // keys per block of the kernel
 // Cache form: least key blocks per CTA, one for each stream.  (One request of
-// 1024 keys 14.9 us, with four blocks 16.1; two requests over a prefix of 1000
-// 13.9 / 17.1 / with one block 15.6 us.)
+// 1024 keys with at least 1 / 2 / 4 blocks 12.6 / 12.4 / 13.5 us; two requests
+// over a prefix of 1000 13.8 / 12.6 / 14.5 us.)
 constexpr int kMinSpan = 2;
 constexpr int kMaxTokens = kAttnFar;
 // One sequence's, cache's or prefix's keys: a run over them takes about a
@@ -365,8 +365,8 @@ int mf_attn_create_packed(mf_attn_t* out, const int32_t* cu_seqlens_host, const 
     // are laid end to end instead and cut into equal spans; a cut run's pieces
     // write partial results that a second kernel joins, which costs about as
     // much as five blocks.  (32q/8kv heads of 128, whole against cut: one row
-    // over 1000 keys 14.6 / 10.0 us, 64 rows over 700 16.4 / 17.5 us, 128 rows
-    // over 1500 26.8 / 19.8 us, a 1024-token prompt 20.2 / 33 us.)
+    // over 1000 keys 14.6 / 10.0 us, 64 rows over 700 14.8 / 16.1, 128 rows over
+    // 1500 24.3 / 18.9, 256 over 4096 54 / 31, a 1024-token prompt 18.8 / 32.5.)
     const int n = (int)items.size(), grid = h->grid;
     constexpr int kRun = 2, kJoin = 5;
     std::vector<int> order(n);

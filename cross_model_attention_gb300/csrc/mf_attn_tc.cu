@@ -28,6 +28,16 @@
 // 128 keys through one ring.  Warp 11: the planner, which finds the CTA's runs
 // and lays them before the others.
 //
+// What bounds it.  A prompt: the tensor cores in principle; 8192 causal tokens
+// of 32q/8kv heads of 128 take 369 us back to back, 1.49 PFLOP/s of the 1.92
+// that a large matrix product reaches (the tensor pipes 66 % busy; what is left
+// is the chain S -> softmax -> P of the two streams at a time that the registers
+// hold, and a run's start and end).  Decoding: memory; 32 requests of up to 4100
+// visible keys read 0.47 GB in 86 us, 5.5 TB/s of 6.8 (the kernel alone 80 us;
+// four ring stages 90 us, three 107).  A prefix for many rows: both, 200
+// requests with two tokens each over 32767 keys and caches of up to 700 in 196
+// us, of them about 130 the prefix's products and 50 the caches' loads.
+//
 // Masked keys: a row's hidden scores are replaced by -inf before anything is
 // done with them, and V rows that no row may see (past a range's end, where
 // the box still reads) are zeroed in shared memory or left out of the
@@ -232,9 +242,10 @@ struct PackedRuns {
 // of both is at most kApart blocks, a second run's start and end costs more
 // than that brings: the spans are then as long as the shares together, and
 // prefix and caches meet from the two ends of the CTAs.  (32q/8kv heads of
-// 128, together against apart: 16 requests of 200 over 4096 26.2 / 20.9 us, 64
-// of 512 over 16384 58 / 53 us, 300 of 600 over 4096 134 / 140 us, 200 with two
-// new tokens each of 700 over 32768 272 / 278 us.)
+// 128, lengths from 1 to the one named, spans of both together against apart:
+// 16 requests of 200 over 4096 18.2 / 22.2 us, 64 of 512 over 16384 45.7 / 44.8,
+// 300 of 600 over 4096 121 / 104, 200 with two new tokens each of 700 over
+// 32768 257 / 240.)
 struct Unit {
   int a1, b0, b1, nb;  // key ranges of a request's cache, in blocks
 };
@@ -529,15 +540,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(uniform(misc[0]));
-  // The CTA's runs.  The packed form's come from a table, each warp reads them
-  // for itself; the cache form's are worked out by the planner.
+  // The CTA's runs.  The packed form's come from a table and each warp reads
+  // them for itself, from addresses that the compiler knows to be the same in
+  // all lanes (through the planner a causal 8192-token prompt takes 450 us, not
+  // 369); the cache form's are worked out by the planner, which is ahead of the
+  // others (each warp for itself: a 4096-key window for 32 requests 88 us, not
+  // 86, 1024 requests of 200 keys 5 us more).
   Run r{};
   using Own = typename std::conditional<Runs::kPlanned, NoRuns, Runs>::type;
   Own own(p, nullptr);
   int run_slot = 0;
   uint32_t run_ph = 0;
-  // The next run, for a warp (LANE: for its first lane alone); false after the
-  // last or when something has given up.
+  // The next run, for a warp or (one) its first lane alone; false after the last
+  // or when something has given up.
   auto next_run = [&](auto one) {
     if (!Runs::kPlanned) return own.next(r);
     if (one.value) {
@@ -626,8 +641,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------- MMA, one warp per stream
     const int s = warp == 8 ? 0 : 1;
     // (code of the issuing loop, one half after the other or both laid out: a
-    // causal 8192-token prompt 370 / 399 us, 200 requests over a 32k prefix 223 /
-    // 208 us)
+    // causal 8192-token prompt 370 / 399 us, 200 requests over a 32k prefix 207 /
+    // 196 us)
     constexpr int kUnrollHalves = Runs::kUnrollHalves;
     constexpr uint32_t idS = idesc_bf16_f32(kRows, kHalf, false, false);
     constexpr uint32_t idO = idesc_bf16_f32(kRows, D, false, true);
