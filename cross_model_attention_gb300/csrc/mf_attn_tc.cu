@@ -1051,9 +1051,6 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p, const Att
   using Vec = typename std::conditional<V == 2, float2, float4>::type;
   constexpr int NW = sizeof(Vec) / 4, NV = V / NW;
   const int lane = threadIdx.x % LPR;
-  // launched while the attention kernel still runs; its results are there
-  // from here on
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   // (at most 2^31 rows; 64-bit divisions would take as long as the rest)
   const unsigned w = blockIdx.x * (blockDim.x / LPR) + threadIdx.x / LPR;
   // A row's partial results: n0 of the prefix or of a packed tile, then n1 of
@@ -1062,8 +1059,14 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p, const Att
   long long at0 = 0, at1 = 0, step0 = 0;
   int q_tok = 0, head = 0, n0 = 0, n1 = 0;
   bool live = true;  // (four rows to a warp: a last warp's rows may be past the end)
+  // Launched while the attention kernel still runs; its results are there after
+  // this.  (What it does not write is looked at before: the lengths.)
+  auto wait = []() { asm volatile("griddepcontrol.wait;" ::: "memory"); };
   if (CACHED) {
     live = w < static_cast<unsigned>(p.n * p.Lq) * p.H_q;
+    const int len = live ? __ldg(p.lens + w / p.H_q / p.Lq) : 0;
+    const int nb = cache_unit(p, len).nb;
+    wait();
     if (live) {
       q_tok = static_cast<int>(w / p.H_q);
       head = static_cast<int>(w - static_cast<unsigned>(q_tok) * p.H_q);
@@ -1086,7 +1089,6 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p, const Att
         at0 = static_cast<long long>(2 * slot + (lone ? 0 : tile & 1)) * kRows + (q_tok - tile * p.TQ) * p.G + hg;
         if (lone) n0 *= 2;
       }
-      const int nb = cache_unit(p, p.lens[req]).nb;
       if (nb > 0) {  // the pieces with blocks of the row's head
         const int hh = kv % p.HG, unit = req * p.groups + kv / p.HG;
         int slot;
@@ -1095,6 +1097,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p, const Att
       }
     }
   } else {
+    wait();
     const unsigned j = w / kRows;
     if (j >= static_cast<unsigned>(n_joins)) return;  // (a whole warp)
     const AttnJoin jn = joins[j];

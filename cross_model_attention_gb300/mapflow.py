@@ -460,7 +460,8 @@ class RotaryPlan:
     queries and keys in one pass (see mf_qk_norm_rope in mapflow.h).
 
     scaling: "none", "linear", "ntk" or "yarn"; layout: "half" (pairs i and
-    i + rot_dim/2) or "interleaved" (pairs 2i and 2i + 1)."""
+    i + rot_dim/2) or "interleaved" (pairs 2i and 2i + 1).  No gradient is
+    recorded."""
 
     def __init__(self, rot_dim: int, base: float = 10000.0, layout: str = "half", scaling: str = "none",
                  factor: float = 1.0, original_length: int = 0, beta_fast: float = 32.0,
@@ -564,7 +565,7 @@ class _AttentionPlan:
 class WindowAttention(_AttentionPlan):
     """Attention over packed sequences with an optional sliding window and
     `sinks` first tokens that stay visible; with q_begin, over query chunks
-    (see mf_attn_create_packed in mapflow.h).  bf16."""
+    (see mf_attn_create_packed in mapflow.h).  bf16; no gradient is recorded."""
 
     def __init__(self, cu_seqlens: Sequence[int], H_q: int, H_kv: int, d: int, window: Optional[int] = None,
                  sinks: int = 0, q_begin: Optional[Sequence[int]] = None, use_torch_allocator: bool = True):
@@ -632,7 +633,7 @@ class CacheAttention(_AttentionPlan):
     """Decoding attention of up to n requests with Lq new tokens each over
     their caches of `capacity` rows, with an optional window and sinks, or over
     a prefix of prefix_len tokens that all requests share (see
-    mf_attn_create_cache in mapflow.h).  bf16."""
+    mf_attn_create_cache in mapflow.h).  bf16; no gradient is recorded."""
 
     def __init__(self, n: int, Lq: int, capacity: int, H_q: int, H_kv: int, d: int,
                  window: Optional[int] = None, sinks: int = 0, prefix_len: int = 0,

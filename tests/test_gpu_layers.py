@@ -1,6 +1,7 @@
 """GPU tests of the rotary embedding with head norms, window attention with
 sinks and shared-prefix attention, against fp64 definitions (layer_ref)."""
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -508,6 +509,30 @@ def test_streams():
     got, _ = rp.apply(q, None, pos, stream=streams[0])
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+def test_threads():
+    """Two threads use the same plans on streams of their own."""
+    plan, q, k, v, dl, kp, vp, o, lse = check_cache([30, 2, 64, 0], 1, 64, 8, 2, 128, P=300)
+    chunk, cq, ck, cv, co, _ = check_packed([5000], 4, 2, 128, begin=[4990])
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(30):
+                a, b = plan.attend(q, k, v, dl, kp, vp), chunk.attend(cq, ck, cv)
+                s.synchronize()
+                if not (torch.equal(a, o) and torch.equal(b[4990:], co[4990:])):
+                    wrong.append(1)
+
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
 
 
 def test_layers_together():
