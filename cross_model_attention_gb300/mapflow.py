@@ -8,8 +8,9 @@ missing, importing this module raises: there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
-from typing import Dict, Optional, Sequence, Tuple
+from typing import Dict, List, Optional, Sequence, Tuple
 
 import numpy as np
 
@@ -217,6 +218,53 @@ def _torch_allocator():
         if ptr:
             torch.cuda.caching_allocator_delete(ptr)
     return ALLOC_FN(_alloc), FREE_FN(_free)
+
+
+# ------------------------------------- memory that pending kernels read ----
+_parked: List = []  # releases put off while a stream was captured
+
+
+def _capturing(gpu: int) -> bool:
+    """Whether a stream is known to be captured: this thread's current one, on
+    its device or on `gpu`, or the one that torch.cuda.graph takes by itself."""
+    import torch
+    if not torch.cuda.is_initialized():
+        return False
+    if torch.cuda.is_current_stream_capturing():
+        return True
+    if gpu != torch.cuda.current_device():
+        with torch.cuda.device(gpu):
+            if torch.cuda.is_current_stream_capturing():
+                return True
+    s = getattr(torch.cuda.graph, "default_capture_stream", None)
+    if s is not None:
+        with torch.cuda.stream(s):
+            return torch.cuda.is_current_stream_capturing()
+    return False
+
+
+def _release(gpu: int, wait_and_free) -> None:
+    """Calls wait_and_free(), which waits for GPU `gpu` before it gives memory
+    back.  A device cannot be waited for while one of its streams is captured
+    (that ends the capture): then the release is put off to the next one."""
+    _parked.append((gpu, wait_and_free))
+    _release_parked()
+
+
+def _release_parked() -> None:
+    for _ in range(len(_parked)):
+        try:
+            gpu, wait_and_free = _parked.pop(0)
+        except IndexError:  # another thread has taken it
+            return
+        try:
+            if _capturing(gpu):
+                _parked.append((gpu, wait_and_free))
+            else:
+                wait_and_free()
+        except Exception:
+            _parked.append((gpu, wait_and_free))
+            raise
 
 
 # --------------------------------------------- same names as the C ABI -----
@@ -464,13 +512,27 @@ def mf_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "non
     return turns, float(gain.value)
 
 
+def _wait_for(gpu: int, table) -> None:
+    """Waits for GPU `gpu` while `table` is held."""
+    import torch
+    torch.cuda.synchronize(gpu)
+
+
 class RotaryPlan:
     """A rotary table on the device: per-head norm and rotary embedding of
     queries and keys in one pass (see mf_qk_norm_rope in mapflow.h).
 
     scaling: "none", "linear", "ntk" or "yarn"; layout: "half" (pairs i and
     i + rot_dim/2) or "interleaved" (pairs 2i and 2i + 1).  No gradient is
-    recorded."""
+    recorded.
+
+    The plan may be used on any stream and dropped right after a call: its
+    table goes back to the stream that was current when it was made, so where
+    a call ran on another one, dropping the plan waits for the device.  A
+    captured call reads the table at every replay: keep the plan as long as
+    the graph."""
+
+    _abroad = False  # a call ran on another stream than the table's
 
     def __init__(self, rot_dim: int, base: float = 10000.0, layout: str = "half", scaling: str = "none",
                  factor: float = 1.0, original_length: int = 0, beta_fast: float = 32.0,
@@ -485,6 +547,14 @@ class RotaryPlan:
         device = torch.device("cuda" if device is None else device)
         self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
         self._turns, self._gpu = self.turns.data_ptr(), self.turns.get_device()
+        self._home = torch._C._cuda_getCurrentRawStream(self._gpu) if self._gpu >= 0 else None
+
+    def __del__(self):
+        if self._abroad:
+            try:
+                _release(self._gpu, functools.partial(_wait_for, self._gpu, self.turns))
+            except Exception:  # noqa: BLE001
+                pass
 
     def apply(self, q, k, positions, q_weight=None, k_weight=None, eps: float = 1e-6, norm: Optional[bool] = None,
               q_out=None, k_out=None, stream=None):
@@ -535,6 +605,8 @@ class RotaryPlan:
             pwk = k_weight.data_ptr()
         if norm is None:
             norm = pwq is not None or pwk is not None
+        if raw != self._home:
+            self._abroad = True
         rc = self._call(
             q.data_ptr(), ld_q, q_out.data_ptr(), ld_qo, pk, ld_k, pko, ld_ko, pwq, pwk, norm, eps,
             positions.data_ptr(), self._turns, self.rot_dim, self._layout, self.gain, code, T, H_q, H_k, d, raw)
