@@ -21,6 +21,7 @@ using namespace mf;
 
 struct mf_attn_s {
   bool cached = false;
+  int device = 0;               // where the tables are and the calls run
   int H_q = 0, H_kv = 0, d = 0, G = 0, TQ = 0;
   int window = kAttnNoWindow, n_sink = 0;
   int grid = 0;
@@ -181,6 +182,13 @@ int make_q_map(const mf_attn_s* h, CUtensorMap* m, const void* q, int64_t ld, in
   return make_map4(m, q, dims, st, box);
 }
 
+int check_device(const mf_attn_s* h) {
+  int dev = -1;
+  MF_CUDA(cudaGetDevice(&dev), "device query");
+  if (dev != h->device) return fail(MF_ERR_ARG, "the plan is on device %d, the current device is %d", h->device, dev);
+  return MF_OK;
+}
+
 int check_scale(float scale) {
   if (!(scale > 1e-30f && scale < 1e30f)) return fail(MF_ERR_ARG, "scale must be positive and finite");
   return MF_OK;
@@ -332,7 +340,8 @@ int mf_attn_create_packed(mf_attn_t* out, const int32_t* cu_seqlens_host, const 
   h->alloc = alloc_fn;
   h->dealloc = free_fn;
   h->ctx = alloc_ctx;
-  cudaError_t ce = sm_count(&h->grid);
+  cudaError_t ce = cudaGetDevice(&h->device);
+  if (ce == cudaSuccess) ce = sm_count(&h->grid);
   if (ce != cudaSuccess) {
     delete h;
     return cuda_fail(ce, "device query");
@@ -484,7 +493,8 @@ int mf_attn_create_cache(mf_attn_t* out, int n_max, int Lq, int capacity, int pr
   h->alloc = alloc_fn;
   h->dealloc = free_fn;
   h->ctx = alloc_ctx;
-  cudaError_t ce = sm_count(&h->grid);
+  cudaError_t ce = cudaGetDevice(&h->device);
+  if (ce == cudaSuccess) ce = sm_count(&h->grid);
   if (ce != cudaSuccess) {
     delete h;
     return cuda_fail(ce, "device query");
@@ -494,6 +504,7 @@ int mf_attn_create_cache(mf_attn_t* out, int n_max, int Lq, int capacity, int pr
 
 void mf_attn_destroy(mf_attn_t h) {
   if (!h) return;
+  DeviceScope scope(h->device);
   cudaDeviceSynchronize();
   h_free(h, h->segs_d);
   h_free(h, h->cta_d);
@@ -521,7 +532,8 @@ int mf_attn_packed(mf_attn_t h, const void* q, int64_t ld_q, const void* k, int6
   if (!h) return fail(MF_ERR_ARG, "handle is NULL");
   if (h->cached) return fail(MF_ERR_ARG, "the plan is of the cache form");
   if (dtype != MF_DTYPE_BF16) return fail(MF_ERR_UNSUPPORTED, "attention is built for bf16");
-  int rc;
+  int rc = check_device(h);
+  if (rc != MF_OK) return rc;
   if ((rc = check_rows("q", q, ld_q, h->H_q, h->d, 2)) != MF_OK) return rc;
   if ((rc = check_rows("k", k, ld_k, h->H_kv, h->d, 2)) != MF_OK) return rc;
   if ((rc = check_rows("v", v, ld_v, h->H_kv, h->d, 2)) != MF_OK) return rc;
@@ -574,7 +586,8 @@ int mf_attn_cached(mf_attn_t h, int n, const void* q, int64_t ld_q, const void* 
   if (n < 1 || n > h->n_max) return fail(MF_ERR_ARG, "n = %d is not in [1, %d]", n, h->n_max);
   if (dtype != MF_DTYPE_BF16) return fail(MF_ERR_UNSUPPORTED, "attention is built for bf16");
   if (!lens) return fail(MF_ERR_ARG, "lens is NULL");
-  int rc;
+  int rc = check_device(h);
+  if (rc != MF_OK) return rc;
   if ((rc = check_aligned("lens", lens, 4)) != MF_OK) return rc;
   if ((rc = check_aligned("lse", lse, 4)) != MF_OK) return rc;
   if ((rc = check_rows("q", q, ld_q, h->H_q, h->d, 2)) != MF_OK) return rc;
@@ -647,6 +660,8 @@ int mf_attn_cached(mf_attn_t h, int n, const void* q, int64_t ld_q, const void* 
 
 int mf_attn_status(mf_attn_t h, void* stream) {
   if (!h) return fail(MF_ERR_ARG, "handle is NULL");
+  const int rc = check_device(h);
+  if (rc != MF_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   MF_CUDA(cudaMemcpyAsync(h->host_err, h->err_d, sizeof(int), cudaMemcpyDeviceToHost, s), "error word copy");
   MF_CUDA(cudaStreamSynchronize(s), "attention status");

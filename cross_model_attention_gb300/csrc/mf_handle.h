@@ -113,6 +113,22 @@ int cuda_fail(cudaError_t e, const char* what);
     if (e_ != cudaSuccess) return cuda_fail(e_, what); \
   } while (0)
 
+// Makes device `dev` current, and the caller's again at the end of the scope.
+class DeviceScope {
+ public:
+  explicit DeviceScope(int dev) {
+    if (cudaGetDevice(&was_) != cudaSuccess || was_ == dev || cudaSetDevice(dev) != cudaSuccess) was_ = -1;
+  }
+  ~DeviceScope() {
+    if (was_ >= 0) cudaSetDevice(was_);
+  }
+  DeviceScope(const DeviceScope&) = delete;
+  DeviceScope& operator=(const DeviceScope&) = delete;
+
+ private:
+  int was_ = -1;  // -1: nothing to put back
+};
+
 // 2-D bf16 map: `inner` elements per row, `rows` rows, `stride` bytes between
 // rows; box = box_inner x box_rows; out-of-range reads give 0.
 int make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t stride,

@@ -1,5 +1,8 @@
 """Plans of the rotary and attention layers that are dropped while their
 kernels may still run (host side, no GPU needed)."""
+import ctypes
+import os
+import subprocess
 import weakref
 
 import pytest
@@ -86,3 +89,77 @@ def test_a_failed_wait_keeps_the_table(gpu, monkeypatch):
     monkeypatch.setattr(torch.cuda, "synchronize", fails)
     del plan
     assert gpu.watch() is not None
+
+
+# ------------------------------- the library's host code on a fake runtime --
+@pytest.fixture(scope="module")
+def host(tmp_path_factory):
+    """mf_attn.cu's host code linked with stand-ins for the CUDA runtime."""
+    return fake_library(tmp_path_factory, "mf_attn.cu")
+
+
+def fake_library(tmp_path_factory, source, *flags):
+    here = os.path.dirname(os.path.abspath(__file__))
+    out = str(tmp_path_factory.mktemp("fake") / "libfake.so")
+    cuda = os.path.dirname(os.path.dirname(build_mod._nvcc()))
+    cmd = ["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-Wl,-Bsymbolic", *flags, "-I", os.path.join(cuda, "include"),
+           "-x", "c++", os.path.join(build_mod.CSRC, source), os.path.join(here, "fake_cuda.cpp"), "-o", out]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    lib = ctypes.CDLL(out)
+    lib.fake_log.restype = ctypes.c_char_p
+    return lib
+
+
+P = 1 << 30  # aligned addresses, far apart, that host checks never follow
+NO_ALLOC = (mapflow.ALLOC_FN(), mapflow.FREE_FN(), None)
+
+
+def plan_of(host, form, device=0):
+    host.fake_device(device)
+    h = ctypes.c_void_p()
+    if form == "packed":
+        cu = (ctypes.c_int32 * 2)(0, 5000)
+        rc = host.mf_attn_create_packed(ctypes.byref(h), cu, None, 1, 4, 2, 64, 0, 0, *NO_ALLOC)
+    else:
+        rc = host.mf_attn_create_cache(ctypes.byref(h), 2, 1, 64, 0, 4, 2, 64, 0, 0, *NO_ALLOC)
+    assert rc == mapflow.MF_OK
+    host.fake_log()
+    return h
+
+
+def attend(host, h, form):
+    i64, f32, vp = ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
+    if form == "packed":
+        a = [vp(P), i64(256), vp(2 * P), i64(128), vp(3 * P), i64(128), vp(4 * P), i64(256), None]
+        return host.mf_attn_packed(h, *a, mapflow.MF_DTYPE_BF16, f32(1), vp(5 * P), i64(1 << 30), None)
+    a = [vp(P), i64(256), vp(2 * P), i64(128), vp(3 * P), i64(128), vp(6 * P), None, i64(0), None, i64(0), vp(4 * P),
+         i64(256), None]
+    return host.mf_attn_cached(h, 2, *a, mapflow.MF_DTYPE_BF16, f32(1), vp(5 * P), i64(1 << 30), None)
+
+
+FORMS = ["packed", "cache"]
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_destroy_waits_for_the_plans_own_device(host, form):
+    h = plan_of(host, form, device=1)
+    host.fake_device(3)
+    host.mf_attn_destroy(h)
+    did = host.fake_log().decode().split()
+    assert did[0] == "sync1" and set(did[1:]) == {"free1", "unpin1"}
+    assert host.fake_current() == 3
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_calls_under_another_device_are_refused(host, form):
+    h = plan_of(host, form, device=1)
+    before = host.fake_launches()
+    host.fake_device(0)
+    assert attend(host, h, form) == mapflow.MF_ERR_ARG
+    assert host.mf_attn_status(h, None) == mapflow.MF_ERR_ARG
+    assert host.fake_launches() == before
+    host.fake_device(1)
+    assert attend(host, h, form) == mapflow.MF_OK and host.mf_attn_status(h, None) == mapflow.MF_OK
+    assert host.fake_launches() > before
+    host.mf_attn_destroy(h)
