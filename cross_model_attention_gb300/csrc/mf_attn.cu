@@ -505,12 +505,15 @@ int mf_attn_create_cache(mf_attn_t* out, int n_max, int Lq, int capacity, int pr
 void mf_attn_destroy(mf_attn_t h) {
   if (!h) return;
   DeviceScope scope(h->device);
-  cudaDeviceSynchronize();
-  h_free(h, h->segs_d);
-  h_free(h, h->cta_d);
-  h_free(h, h->joins_d);
-  h_free(h, h->err_d);
-  if (h->host_err) cudaFreeHost(h->host_err);
+  if (capture_refused(cudaDeviceSynchronize())) {
+    cudaGetLastError();  // kernels may still read the tables: they stay allocated
+  } else {
+    h_free(h, h->segs_d);
+    h_free(h, h->cta_d);
+    h_free(h, h->joins_d);
+    h_free(h, h->err_d);
+    if (h->host_err) cudaFreeHost(h->host_err);
+  }
   delete h;
 }
 

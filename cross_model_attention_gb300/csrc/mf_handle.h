@@ -129,6 +129,11 @@ class DeviceScope {
   int was_ = -1;  // -1: nothing to put back
 };
 
+// Whether a wait for the device was refused because a stream is captured.
+inline bool capture_refused(cudaError_t e) {
+  return e >= cudaErrorStreamCaptureUnsupported && e <= cudaErrorStreamCaptureWrongThread;
+}
+
 // 2-D bf16 map: `inner` elements per row, `rows` rows, `stride` bytes between
 // rows; box = box_inner x box_rows; out-of-range reads give 0.
 int make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t stride,

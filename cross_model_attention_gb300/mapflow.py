@@ -615,10 +615,18 @@ class RotaryPlan:
         return q_out, k_out
 
 
+def _destroy_plan(handle, keep) -> None:
+    """Waits for the plan's GPU and frees it; `keep` holds its allocator."""
+    load_library().mf_attn_destroy(handle)
+
+
 class _AttentionPlan:
-    """Owner of one mf_attn_t."""
+    """Owner of one mf_attn_t.  Dropping it waits for its GPU, or, during a
+    stream capture, puts the release off to the next one.  A captured call
+    reads the plan at every replay: keep it as long as the graph."""
 
     handle = None
+    _gpu = None
 
     def _workspace_bytes(self, n: int) -> int:
         need = ctypes.c_int64()
@@ -633,8 +641,8 @@ class _AttentionPlan:
 
     def close(self) -> None:
         if self.handle is not None:
-            load_library().mf_attn_destroy(self.handle)
-            self.handle = None
+            h, self.handle = self.handle, None
+            _release(0 if self._gpu is None else self._gpu, functools.partial(_destroy_plan, h, self._keep))
 
     def __del__(self):
         try:
@@ -651,6 +659,7 @@ class WindowAttention(_AttentionPlan):
     def __init__(self, cu_seqlens: Sequence[int], H_q: int, H_kv: int, d: int, window: Optional[int] = None,
                  sinks: int = 0, q_begin: Optional[Sequence[int]] = None, use_torch_allocator: bool = True):
         lib = load_library()
+        _release_parked()
         self._call = lib.mf_attn_packed
         if window is not None and window < 1:
             raise MapFlowError(MF_ERR_ARG, f"window = {window} must be >= 1 (None: no window)")
@@ -721,6 +730,7 @@ class CacheAttention(_AttentionPlan):
                  window: Optional[int] = None, sinks: int = 0, prefix_len: int = 0,
                  use_torch_allocator: bool = True):
         lib = load_library()
+        _release_parked()
         self._call = lib.mf_attn_cached
         if window is not None and window < 1:
             raise MapFlowError(MF_ERR_ARG, f"window = {window} must be >= 1 (None: no window)")

@@ -559,7 +559,11 @@ MF_API int mf_attn_create_packed(mf_attn_t* out, const int32_t* cu_seqlens_host,
 MF_API int mf_attn_create_cache(mf_attn_t* out, int n_max, int Lq, int capacity, int prefix_len, int H_q,
                                 int H_kv, int d, int window, int n_sink, mf_alloc_fn alloc_fn,
                                 mf_free_fn free_fn, void* alloc_ctx);
-/* Release a plan, from any current device (waits for the plan's device first). */
+/*
+ * Release a plan, from any current device.  Waits for the plan's device first,
+ * which is not permitted while one of its streams is captured and would end the
+ * capture; the plan's device memory is then not given back.
+ */
 MF_API void mf_attn_destroy(mf_attn_t h);
 
 /*

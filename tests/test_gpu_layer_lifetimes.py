@@ -58,3 +58,38 @@ def test_rotary_plan_dropped_during_a_capture():
     assert torch.equal(out, want)
     del kept
     assert not mapflow._parked
+
+
+def test_attention_plans_dropped_during_a_capture():
+    side = torch.cuda.Stream()
+    q, k, v = rnd(0, 5000, 4, 64), rnd(1, 5000, 2, 64), rnd(2, 5000, 2, 64)
+    lens = torch.tensor([4000], dtype=torch.int32, device="cuda")
+
+    def plans():
+        return (mapflow.WindowAttention([0, 5000], 4, 2, 64, q_begin=[4990]),
+                mapflow.CacheAttention(1, 1, 5000, 4, 2, 64))
+
+    def call(a, b, **kw):
+        return a.attend(q, k, v, **kw)[4990:], b.attend(q[None, :1], k[None], v[None], lens, **kw)
+    kept, old = plans(), plans()
+    want = call(*kept)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        got = call(*old)  # still to run when the plans go
+    g = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        g.capture_begin()  # (torch.cuda.graph would wait for the device)
+        out = call(*kept)
+        del old
+        assert len(mapflow._parked) == 2
+        g.capture_end()
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    for x, y, z in zip(got, want, out):
+        assert torch.equal(x, y) and torch.equal(z, y)
+    del kept
+    assert not mapflow._parked

@@ -22,7 +22,7 @@ def _built():
 def gpu(monkeypatch):
     """A stand-in for the GPU's state: the waits for it, and whether a stream is captured."""
     class State:
-        waits, capturing, watch = [], False, None
+        waits, capturing, watch, running = [], False, None, False
 
     state = State()
     state.waits = []
@@ -163,3 +163,48 @@ def test_calls_under_another_device_are_refused(host, form):
     assert attend(host, h, form) == mapflow.MF_OK and host.mf_attn_status(h, None) == mapflow.MF_OK
     assert host.fake_launches() > before
     host.mf_attn_destroy(h)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_destroy_without_a_wait_frees_nothing(host, form):
+    """A wait that a stream capture refuses leaves the tables to the kernels that may read them."""
+    h = plan_of(host, form)
+    host.fake_sync_returns(900)  # cudaErrorStreamCaptureUnsupported
+    host.mf_attn_destroy(h)
+    host.fake_sync_returns(0)
+    assert host.fake_log().decode().split() == ["sync0"]
+    h = plan_of(host, form)
+    host.fake_sync_returns(700)  # any other error: nothing runs any more
+    host.mf_attn_destroy(h)
+    host.fake_sync_returns(0)
+    assert "free0" in host.fake_log().decode().split()
+
+
+@pytest.mark.parametrize("cls", [mapflow.WindowAttention, mapflow.CacheAttention])
+def test_attention_plan_dropped_during_a_capture(gpu, monkeypatch, cls):
+    gone = []
+
+    class Lib:
+        mf_attn_destroy = staticmethod(gone.append)
+    monkeypatch.setattr(mapflow, "load_library", lambda: Lib)
+
+    class Plan(cls):
+        def __del__(self):
+            if gpu.running:  # (a failure leaves plans that are none)
+                super().__del__()
+
+    def plan(handle):
+        p = Plan.__new__(Plan)
+        p.handle, p._keep, p._gpu = handle, (), 0
+        return p
+    monkeypatch.setattr(gpu, "running", True)
+    a, b, c = plan(1), plan(2), plan(3)
+    a.close()
+    a.close()
+    assert gone == [1]
+    gpu.capturing = True
+    del b
+    assert gone == [1]
+    gpu.capturing = False
+    c.close()
+    assert sorted(gone) == [1, 2, 3]
