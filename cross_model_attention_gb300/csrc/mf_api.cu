@@ -258,6 +258,7 @@ int mf_bsr_create_chunked(mf_bsr_t* out, int n_layers, int T, int H_s, int B, in
   }
 
   mf_bsr_t h = new mf_bsr_s();
+  if (cudaGetDevice(&h->device) != cudaSuccess) h->device = -1;  // (the allocations below fail)
   h->n_layers = n_layers;
   h->T = T;
   h->H_s = H_s;
@@ -401,6 +402,7 @@ int mf_bsr_create_chunked(mf_bsr_t* out, int n_layers, int T, int H_s, int B, in
 
 void mf_bsr_destroy(mf_bsr_t h) {
   if (!h) return;
+  DeviceScope scope(h->device);
   cudaDeviceSynchronize();
   for (auto& r : h->prof) {
     cudaEventDestroy(r.a);

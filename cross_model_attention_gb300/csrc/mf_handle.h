@@ -68,6 +68,7 @@ struct mf_bsr_s {
   long long launches[MF_K_COUNT] = {0};
   std::vector<ProfRec> prof;
   std::vector<cudaEvent_t> event_pool;
+  int device = -1;  // where the buffers are
   int n_layers = 0, T = 0, H_s = 0, B = 0, causal = 1, n_seqs = 0;
   int R = 0, C = 0, max_cand = 0, n_tiles = 0, n_slabs = 0;
   std::vector<int> cu;

@@ -136,7 +136,8 @@ MF_API int mf_bsr_create_chunked(mf_bsr_t* out, int n_layers, int T, int H_s, in
                                  int n_seqs, mf_alloc_fn alloc_fn, mf_free_fn free_fn,
                                  void* alloc_ctx);
 
-/* Release every buffer of the handle (waits for the device first). */
+/* Release every buffer of the handle, from any current device (waits for the
+ * device on which it was created first). */
 MF_API void mf_bsr_destroy(mf_bsr_t h);
 
 /*

@@ -1,5 +1,5 @@
-"""Plans of the rotary and attention layers that are dropped while their
-kernels may still run (host side, no GPU needed)."""
+"""Plans of the rotary and attention layers, and compressed states, that are
+dropped while their kernels may still run (host side, no GPU needed)."""
 import ctypes
 import os
 import subprocess
@@ -208,3 +208,27 @@ def test_attention_plan_dropped_during_a_capture(gpu, monkeypatch, cls):
     gpu.capturing = False
     c.close()
     assert sorted(gone) == [1, 2, 3]
+
+
+@pytest.fixture(scope="module")
+def host_bsr(tmp_path_factory):
+    """mf_api.cu's host code linked with stand-ins for the CUDA runtime."""
+    return fake_library(tmp_path_factory, "mf_api.cu", "-DFAKE_RUNTIME_ONLY")
+
+
+def bsr_of(host, device=0):
+    host.fake_device(device)
+    h = ctypes.c_void_p()
+    cu = (ctypes.c_int32 * 2)(0, 300)
+    assert host.mf_bsr_create(ctypes.byref(h), 2, 300, 4, 64, 1, cu, 1, *NO_ALLOC) == mapflow.MF_OK
+    host.fake_log()
+    return h
+
+
+def test_bsr_destroy_waits_for_its_own_device(host_bsr):
+    h = bsr_of(host_bsr, device=1)
+    host_bsr.fake_device(3)
+    host_bsr.mf_bsr_destroy(h)
+    did = host_bsr.fake_log().decode().split()
+    assert did[0] == "sync1" and set(did[1:]) == {"free1", "sync1", "unpin1"}
+    assert host_bsr.fake_current() == 3
