@@ -102,11 +102,15 @@ def fake_library(tmp_path_factory, source, *flags):
     here = os.path.dirname(os.path.abspath(__file__))
     out = str(tmp_path_factory.mktemp("fake") / "libfake.so")
     cuda = os.path.dirname(os.path.dirname(build_mod._nvcc()))
-    cmd = ["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-Wl,-Bsymbolic", *flags, "-I", os.path.join(cuda, "include"),
+    cmd = ["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-Wl,-Bsymbolic,-z,lazy", *flags, "-I", os.path.join(cuda, "include"),
            "-x", "c++", os.path.join(build_mod.CSRC, source), os.path.join(here, "fake_cuda.cpp"), "-o", out]
     r = subprocess.run(cmd, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
-    lib = ctypes.CDLL(out)
+    dlopen = ctypes.CDLL(None).dlopen  # (ctypes itself would ask for every function, called or not)
+    dlopen.restype, dlopen.argtypes = ctypes.c_void_p, [ctypes.c_char_p, ctypes.c_int]
+    handle = dlopen(out.encode(), os.RTLD_LAZY)
+    assert handle
+    lib = ctypes.CDLL(out, handle=handle)
     lib.fake_log.restype = ctypes.c_char_p
     return lib
 
