@@ -403,7 +403,11 @@ int mf_bsr_create_chunked(mf_bsr_t* out, int n_layers, int T, int H_s, int B, in
 void mf_bsr_destroy(mf_bsr_t h) {
   if (!h) return;
   DeviceScope scope(h->device);
-  cudaDeviceSynchronize();
+  if (capture_refused(cudaDeviceSynchronize())) {
+    cudaGetLastError();  // kernels may still use the buffers: they stay allocated
+    delete h;
+    return;
+  }
   for (auto& r : h->prof) {
     cudaEventDestroy(r.a);
     cudaEventDestroy(r.b);

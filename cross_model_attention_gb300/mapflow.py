@@ -803,17 +803,27 @@ class CacheAttention(_AttentionPlan):
 
 
 # ------------------------------------------------------ convenience class --
+def _destroy_bsr(handle, keep) -> None:
+    """Waits for the state's GPU and frees it; `keep` holds its allocator."""
+    mf_bsr_destroy(handle)
+
+
 class BSR:
     """Owner of one mf_bsr_t (compressed sender state of several layers)."""
+
+    handle = None
 
     def __init__(self, n_layers: int, T: int, H_s: int, B: int, cu_seqlens: Sequence[int],
                  causal: bool = True, use_torch_allocator: bool = True,
                  q_begin: Optional[Sequence[int]] = None):
+        _release_parked()
         self.n_layers, self.T, self.H_s, self.B, self.causal = n_layers, T, H_s, B, causal
         self.cu_seqlens = [int(x) for x in cu_seqlens]
         self.q_begin = None if q_begin is None else [int(x) for x in q_begin]
         self.handle, self._keep = mf_bsr_create(n_layers, T, H_s, B, causal, self.cu_seqlens,
                                                 use_torch_allocator, self.q_begin)
+        import torch
+        self._gpu = torch.cuda.current_device()
         self.d: Optional[int] = None
 
     def compress(self, layer: int, q, k, p: float, stream=None) -> None:
@@ -889,9 +899,11 @@ class BSR:
         return {name: mf_profile_read(self.handle, i) for i, name in enumerate(KERNELS)}
 
     def close(self) -> None:
+        """Waits for the GPU and frees the state; during a stream capture the
+        release is put off to the next one."""
         if self.handle is not None:
-            mf_bsr_destroy(self.handle)
-            self.handle = None
+            h, self.handle = self.handle, None
+            _release(self._gpu, functools.partial(_destroy_bsr, h, self._keep))
 
     def __del__(self):
         try:

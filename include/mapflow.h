@@ -136,8 +136,10 @@ MF_API int mf_bsr_create_chunked(mf_bsr_t* out, int n_layers, int T, int H_s, in
                                  int n_seqs, mf_alloc_fn alloc_fn, mf_free_fn free_fn,
                                  void* alloc_ctx);
 
-/* Release every buffer of the handle, from any current device (waits for the
- * device on which it was created first). */
+/* Release every buffer of the handle, from any current device.  Waits for the
+ * device on which it was created first, which is not permitted while one of its
+ * streams is captured and would end the capture; the buffers (and the pins of
+ * views) are then not given back. */
 MF_API void mf_bsr_destroy(mf_bsr_t h);
 
 /*

@@ -93,3 +93,22 @@ def test_attention_plans_dropped_during_a_capture():
         assert torch.equal(x, y) and torch.equal(z, y)
     del kept
     assert not mapflow._parked
+
+
+def test_compressed_state_dropped_during_a_capture():
+    T, H, d = 256, 4, 128
+    q, k, v = rnd(1, T, H, d), rnd(2, T, H, d), rnd(3, 1, T, H, d)
+    bsr = mapflow.BSR(1, T, H, 64, [0, T])
+    bsr.compress(0, q, k, 0.95)
+    o, x = torch.empty_like(v), torch.zeros(8, device="cuda")
+    bsr.retrieve(torch.eye(H, device="cuda")[None], v, o, [0])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        x += 1
+        del bsr
+        assert len(mapflow._parked) == 1
+    g.replay()
+    assert (x == 1).all()
+    mapflow.BSR(1, T, H, 64, [0, T]).close()
+    assert not mapflow._parked

@@ -184,12 +184,12 @@ def test_destroy_without_a_wait_frees_nothing(host, form):
     assert "free0" in host.fake_log().decode().split()
 
 
-@pytest.mark.parametrize("cls", [mapflow.WindowAttention, mapflow.CacheAttention])
-def test_attention_plan_dropped_during_a_capture(gpu, monkeypatch, cls):
+@pytest.mark.parametrize("cls", [mapflow.WindowAttention, mapflow.CacheAttention, mapflow.BSR])
+def test_plans_and_states_dropped_during_a_capture(gpu, monkeypatch, cls):
     gone = []
 
     class Lib:
-        mf_attn_destroy = staticmethod(gone.append)
+        mf_attn_destroy = mf_bsr_destroy = staticmethod(gone.append)
     monkeypatch.setattr(mapflow, "load_library", lambda: Lib)
 
     class Plan(cls):
@@ -236,3 +236,11 @@ def test_bsr_destroy_waits_for_its_own_device(host_bsr):
     did = host_bsr.fake_log().decode().split()
     assert did[0] == "sync1" and set(did[1:]) == {"free1", "sync1", "unpin1"}
     assert host_bsr.fake_current() == 3
+
+
+def test_bsr_destroy_without_a_wait_frees_nothing(host_bsr):
+    h = bsr_of(host_bsr)
+    host_bsr.fake_sync_returns(900)  # cudaErrorStreamCaptureUnsupported
+    host_bsr.mf_bsr_destroy(h)
+    host_bsr.fake_sync_returns(0)
+    assert host_bsr.fake_log().decode().split() == ["sync0"]
