@@ -41,7 +41,9 @@
 // Masked keys: a row's hidden scores are replaced by -inf before anything is
 // done with them, and V rows that no row may see (past a range's end, where
 // the box still reads) are zeroed in shared memory or left out of the
-// product, so what lies there, NaN included, reaches nothing.
+// product, so what lies there, NaN included, reaches nothing.  A key that some
+// row of a tile pair sees is multiplied by all its rows, by weight 0 where it is
+// hidden: a value that is not finite makes those NaN too.
 #include <cstdint>
 #include <type_traits>
 

@@ -549,12 +549,19 @@ typedef struct mf_attn_s* mf_attn_t; /* opaque; a plan for attention calls */
  * (MF_ERR_UNSUPPORTED otherwise).  A row that sees no key gets o = 0 and
  * lse = -inf.
  *
- * What is not finite in a key or value row reaches the rows that see it; in a
- * value row it may also reach earlier rows of its sequence that share its
- * 128-key block and, in the cache form, the other heads of its request (their
- * weight for it is 0, and 0 times NaN is NaN).  Rows past a sequence's or a
- * cache's end, keys that no row of a call sees, and other sequences' and
- * requests' rows may hold anything.
+ * What is not finite in a key row reaches the rows that see it and no others.
+ * What is not finite in a value row reaches the rows that see it, and may reach
+ * rows for which it is hidden (their weight for it is 0, and 0 times NaN is NaN)
+ * where they are multiplied together with one that sees it, earlier or later:
+ *   packed form   tokens of a sequence from its first query row on go in pairs
+ *                 of tiles, 2 * floor(128 / (H_q / H_kv)) tokens; a value that
+ *                 any token of a pair sees may reach all of them (for the query
+ *                 heads of its KV head)
+ *   cache form    all new tokens of a request, and all heads of its KV head's
+ *                 group of floor(128 / (Lq * H_q / H_kv)) neighbouring KV heads
+ * A row that sees no key stays 0.  Rows past a sequence's or a cache's end, keys
+ * that no row of a call sees, and other sequences' and requests' rows may hold
+ * anything.
  */
 MF_API int mf_attn_create_packed(mf_attn_t* out, const int32_t* cu_seqlens_host, const int32_t* q_begin_host,
                                  int n_seqs, int H_q, int H_kv, int d, int window, int n_sink,
