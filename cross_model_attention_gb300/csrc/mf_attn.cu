@@ -651,6 +651,8 @@ int mf_attn_cached(mf_attn_t h, int n, const void* q, int64_t ld_q, const void* 
   p.suf_base = c.suf_base;
   p.suf_rows = c.suf_rows;
   p.min_span = kMinSpan;
+  if (n > kAttnSlotBits)  // (the kernel sums eight requests at a time: 0 or at least 3)
+    for (p.slot_shift = 3; n > kAttnSlotBits << p.slot_shift;) ++p.slot_shift;
   char* ws = static_cast<char*>(workspace);
   p.cuts = reinterpret_cast<int2*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + c.ml);

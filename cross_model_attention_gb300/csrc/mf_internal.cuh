@@ -200,6 +200,7 @@ cudaError_t launch_rope(const RopeParams& p, long long T, int f32, int d, cudaSt
 // Attention over packed sequences or caches (mf_attn_tc.cu).
 constexpr int kAttnNoWindow = 1 << 30;  // a window that hides nothing
 constexpr int kAttnCostPre = 1, kAttnCostCache = 2;  // a run's start and end, in key blocks
+constexpr int kAttnSlotBits = 8192;     // of the map of requests with keys
 constexpr int kAttnFar = 1 << 29;       // a row position past every key, and the most keys
 
 // One run of key blocks of one query tile pair (packed form): what a CTA does
@@ -239,6 +240,7 @@ struct AttnParams {
   int HG, groups;            // caches: KV heads per tile, tiles per request
   int grid;                  // CTAs of the launch
   int min_span;              // least work per CTA, in blocks
+  int slot_shift;            // a bit of the map of requests with keys stands for 2^this of them
   int2* cuts;                // [units] how a unit's blocks are cut, written by its last run
   // partial results
   float* part_o;             // [row][d], not normalised

@@ -92,3 +92,62 @@ def test_reach_of_a_value_cached(lens, Lq, H_q, H_kv, d, window, sinks, P, at, b
     k2 = k.clone()
     k2[0, at, head, 7] = bad
     assert torch.equal(plan.attend(q, k2, v, dl, **pre)[~sees], want[~sees])
+
+
+# --------------------------------------------------------------- empty slots --
+def slots_case(n, used, cap, H_q=2, H_kv=1, d=64, seed=0):
+    """A plan of n requests of which `used` (request -> keys) have any."""
+    q = rnd(seed, n, 1, H_q, d)
+    k, v = rnd(seed + 1, n, cap, H_kv, d), rnd(seed + 2, n, cap, H_kv, d)
+    lens = torch.zeros(n, dtype=torch.int32)
+    for r, x in used.items():
+        lens[r] = x
+    plan = mapflow.CacheAttention(n, 1, cap, H_q, H_kv, d)
+    return plan, q, k, v, lens.cuda()
+
+
+@pytest.mark.parametrize("n", [8191, 8192, 8193, 16384, 65537, 70001, 131073, 300001])
+def test_cache_slots_past_the_map(n):
+    """The map of used slots has a bit for one, or from 8193 requests on for 8, 16, 32 or 64 of them."""
+    rng = np.random.default_rng(n)
+    edges = [0, 7, 8, 63, 64, 127, 128, 2047, 2048, n // 2, n - 65, n - 64, n - 9, n - 8, n - 1]
+    used = {int(r): int(rng.integers(1, 9)) for r in list(rng.integers(0, n, 200)) + edges}
+    plan, q, k, v, lens = slots_case(n, used, 8, seed=1)
+    lse = torch.zeros(n, 1, 2, device="cuda")
+    o = plan.attend(q, k, v, lens, lse=lse)
+    plan.status()
+    some = torch.tensor(sorted(used), device="cuda")
+    none = torch.ones(n, dtype=torch.bool, device="cuda")
+    none[some] = False
+    assert (o[none] == 0).all() and torch.isneginf(lse[none]).all()
+    # the used ones at once: rows of one sequence each, other requests' keys hidden
+    mine = torch.arange(len(some), device="cuda")
+    seen = (mine[:, None] == mine.repeat_interleave(8)[None]) & \
+        (torch.arange(8, device="cuda").repeat(len(some))[None] < lens[some][:, None])
+    want, wl, bo, bl = ref.attend(q[some, 0], k[some].flatten(0, 1), v[some].flatten(0, 1), seen, 64 ** -0.5)
+    assert ((o[some, 0].double() - want).abs() <= bo).all()
+    assert ((lse[some, 0].double() - wl).abs() <= bl).all()
+
+
+def test_empty_slots_past_the_map_cost_little():
+    """100000 slots of which the first and last 300 are used: 0.3 ms, where a
+    walk over the others one by one would take more than 20 ms.  (3 ms: eight
+    times what the lengths and the launch take.)"""
+    n = 100000
+    used = {r: 600 for r in [*range(297), *range(n - 300, n)]}
+    plan, q, k, v, lens = slots_case(n, used, 600)
+    o = torch.empty_like(q)
+    times = []
+    for _ in range(6):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        plan.attend(q, k, v, lens, o=o)
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b))
+    plan.status()
+    assert min(times) < 3.0
+    for r in (0, 296, n - 300, n - 1):
+        want, _, bo, _ = ref.attend(q[r], k[r], v[r], torch.ones(1, 600, dtype=torch.bool, device="cuda"), 64 ** -0.5)
+        assert ((o[r].double() - want).abs() <= bo).all()
+    assert (o[297:n - 300] == 0).all()
