@@ -164,6 +164,32 @@ def _raw_current(index: int):
     return None
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _int(name: str, x) -> int:
+    """x as an int of the C ABI (ctypes would cut it to 32 bits)."""
+    x = int(x)
+    if not -_INT_MAX <= x <= _INT_MAX:
+        raise MapFlowError(MF_ERR_ARG, f"{name} = {x} is out of range")
+    return x
+
+
+def _ints(name: str, xs) -> np.ndarray:
+    """xs as an int32 array (a cast of a wider one would cut it to 32 bits)."""
+    wide = np.asarray(xs, dtype=np.int64)
+    if (np.abs(wide) > _INT_MAX).any():
+        raise MapFlowError(MF_ERR_ARG, f"{name}: a value is out of range")
+    return np.ascontiguousarray(wide.astype(np.int32))
+
+
+def _span(name: str, x, least: int) -> int:
+    """A number of keys, at least `least`; more than any sequence has is as many as the C ABI can say."""
+    if x < least:
+        raise MapFlowError(MF_ERR_ARG, f"{name} = {x} must be >= {least}" + (" (None: no window)" if least else ""))
+    return min(int(x), _INT_MAX)
+
+
 def _empty(t, shape):
     """A new contiguous tensor like t, of `shape` (t's, checked before)."""
     import torch
@@ -504,10 +530,11 @@ def mf_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "non
     """(turns uint64 [rot_dim/2], gain): the rotary table (see mapflow.h)."""
     if scaling not in _SCALINGS:
         raise MapFlowError(MF_ERR_ARG, f"unknown scaling {scaling!r} ({', '.join(_SCALINGS)})")
-    turns = np.zeros(max(int(rot_dim) // 2, 1), np.uint64)
+    rot_dim, original_length = _int("rot_dim", rot_dim), _int("original_length", original_length)
+    turns = np.zeros(max(rot_dim // 2, 1), np.uint64)
     gain = ctypes.c_float()
     _check(load_library().mf_rope_frequencies(
-        int(rot_dim), float(base), _SCALINGS[scaling], float(factor), int(original_length), float(beta_fast),
+        rot_dim, float(base), _SCALINGS[scaling], float(factor), original_length, float(beta_fast),
         float(beta_slow), turns.ctypes.data_as(ctypes.POINTER(ctypes.c_uint64)), ctypes.byref(gain)))
     return turns, float(gain.value)
 
@@ -661,22 +688,21 @@ class WindowAttention(_AttentionPlan):
         lib = load_library()
         _release_parked()
         self._call = lib.mf_attn_packed
-        if window is not None and window < 1:
-            raise MapFlowError(MF_ERR_ARG, f"window = {window} must be >= 1 (None: no window)")
-        cu = np.ascontiguousarray(np.asarray(cu_seqlens, dtype=np.int32))
+        window, sinks = 0 if window is None else _span("window", window, 1), _span("sinks", sinks, 0)
+        cu = _ints("cu_seqlens", cu_seqlens)
         if cu.ndim != 1 or len(cu) < 2:
             raise MapFlowError(MF_ERR_ARG, "cu_seqlens must hold at least two offsets")
-        qb = None if q_begin is None else np.ascontiguousarray(np.asarray(q_begin, dtype=np.int32))
+        qb = None if q_begin is None else _ints("q_begin", q_begin)
         if qb is not None and qb.shape != (len(cu) - 1,):
             raise MapFlowError(MF_ERR_ARG, f"q_begin must hold {len(cu) - 1} rows")
-        self.H_q, self.H_kv, self.d, self.T = int(H_q), int(H_kv), int(d), int(cu[-1])
+        self.H_q, self.H_kv, self.d, self.T = _int("H_q", H_q), _int("H_kv", H_kv), _int("d", d), int(cu[-1])
         a, f = _torch_allocator() if use_torch_allocator else (ALLOC_FN(), FREE_FN())
         self._keep = (a, f)
         h = ctypes.c_void_p()
         _check(lib.mf_attn_create_packed(
             ctypes.byref(h), cu.ctypes.data_as(ctypes.c_void_p),
             None if qb is None else qb.ctypes.data_as(ctypes.c_void_p), len(cu) - 1, self.H_q, self.H_kv, self.d,
-            0 if window is None else int(window), int(sinks), a, f, None))
+            window, sinks, a, f, None))
         self.handle = h
         self._ws_bytes = self._workspace_bytes(1)
         import torch
@@ -732,16 +758,16 @@ class CacheAttention(_AttentionPlan):
         lib = load_library()
         _release_parked()
         self._call = lib.mf_attn_cached
-        if window is not None and window < 1:
-            raise MapFlowError(MF_ERR_ARG, f"window = {window} must be >= 1 (None: no window)")
-        self.n, self.Lq, self.capacity, self.prefix_len = int(n), int(Lq), int(capacity), int(prefix_len)
-        self.H_q, self.H_kv, self.d = int(H_q), int(H_kv), int(d)
+        window, sinks = 0 if window is None else _span("window", window, 1), _span("sinks", sinks, 0)
+        self.n, self.Lq, self.capacity = _int("n", n), _int("Lq", Lq), _int("capacity", capacity)
+        self.prefix_len = _int("prefix_len", prefix_len)
+        self.H_q, self.H_kv, self.d = _int("H_q", H_q), _int("H_kv", H_kv), _int("d", d)
         a, f = _torch_allocator() if use_torch_allocator else (ALLOC_FN(), FREE_FN())
         self._keep = (a, f)
         h = ctypes.c_void_p()
         _check(lib.mf_attn_create_cache(
             ctypes.byref(h), self.n, self.Lq, self.capacity, self.prefix_len, self.H_q, self.H_kv, self.d,
-            0 if window is None else int(window), int(sinks), a, f, None))
+            window, sinks, a, f, None))
         self.handle = h
         self._ws_of: Dict[int, int] = {}  # workspace bytes by the number of requests
         import torch
