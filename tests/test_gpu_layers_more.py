@@ -151,3 +151,78 @@ def test_empty_slots_past_the_map_cost_little():
         want, _, bo, _ = ref.attend(q[r], k[r], v[r], torch.ones(1, 600, dtype=torch.bool, device="cuda"), 64 ** -0.5)
         assert ((o[r].double() - want).abs() <= bo).all()
     assert (o[297:n - 300] == 0).all()
+
+
+# --------------------------------------------------------------- lost blocks --
+def marks(m, H_kv, d):
+    """Values of m keys that are 1 in a column of 16 keys' own (d such groups
+    apart) and 0 elsewhere: a row's outputs are sums of its weights, so that 16
+    keys (one step of the second product) that are lost, or counted twice, show
+    however long the row is."""
+    v = torch.zeros(m, H_kv, d, dtype=BF, device="cuda")
+    j = torch.arange(m, device="cuda")
+    v[j, :, j // 16 % d] = 1
+    return v
+
+
+def check_marks(o, q, k, v, seen, what):
+    """o against fp64, within bounds that every whole group of 16 visible keys exceeds."""
+    n, H_q, d = q.shape
+    m, G = k.shape[0], H_q // k.shape[1]
+    want, _, bound, _ = ref.attend(q, k, v, seen, d ** -0.5)
+    over = (o.double() - want).abs() - bound
+    assert (over <= 0).all(), f"{what}: {over.max().item()} over the bound"
+    s = torch.einsum("nhd,mhd->nhm", q.double(), k.double().repeat_interleave(G, 1)) * d ** -0.5
+    p = torch.softmax(s.masked_fill(~seen[:, None], -math.inf), -1)
+    column = v[:, 0].argmax(-1)[::16]
+    groups = len(column)
+    pad = groups * 16 - m
+    weight = torch.nn.functional.pad(p, (0, pad)).view(n, H_q, groups, 16).sum(-1)
+    whole = torch.nn.functional.pad(seen, (0, pad)).view(n, groups, 16).all(-1)
+    seen_by = whole[:, None].expand_as(weight)
+    assert (weight > bound[..., column])[seen_by].all(), what
+
+
+@pytest.mark.parametrize("lens,Lq,cap,H_q,H_kv,d,window,sinks,P", [
+    ([9000, 20000, 1, 15000], 1, 20000, 32, 8, 128, None, 0, 0),
+    ([20000, 3, 15000], 1, 20000, 16, 8, 64, None, 0, 0),
+    ([12000] * 12, 2, 12000, 8, 8, 128, 5000, 130, 0),
+    ([6000], 1, 6000, 2, 1, 128, None, 0, 0),
+    ([900, 3000], 1, 3000, 32, 8, 128, None, 0, 20000),
+    ([(r * 997) % 3000 + 1 for r in range(70)], 1, 3000, 8, 2, 128, None, 0, 9000),
+    ([7] * 50, 3, 8, 6, 2, 64, None, 0, 3333),
+])
+def test_cache_loses_no_keys(lens, Lq, cap, H_q, H_kv, d, window, sinks, P):
+    n = len(lens)
+    q, k = rnd(0, n, Lq, H_q, d, std=0.5), rnd(1, n, cap, H_kv, d)
+    kp = rnd(2, P, H_kv, d) if P else None
+    every = marks(P + cap, H_kv, d)
+    v, vp = every[P:].repeat(n, 1, 1, 1), every[:P].contiguous() if P else None
+    plan = mapflow.CacheAttention(n, Lq, cap, H_q, H_kv, d, window=window, sinks=sinks, prefix_len=P)
+    o = plan.attend(q, k, v, torch.tensor(lens, dtype=torch.int32, device="cuda"), kp, vp)
+    plan.status()
+    for r, L in enumerate(lens):
+        seen = ref.seen_packed(torch.arange(L - Lq, L, device="cuda"), torch.arange(L, device="cuda"), window, sinks)
+        kk = k[r, :L]
+        if P:
+            kk = torch.cat([kp, kk])
+            seen = torch.cat([torch.ones(Lq, P, dtype=torch.bool, device="cuda"), seen], 1)
+        check_marks(o[r], q[r], kk, every[:P + L], seen, f"request {r}")
+
+
+@pytest.mark.parametrize("L,begin,H_q,H_kv,d,window,sinks", [
+    (6000, 5999, 32, 8, 128, None, 0),
+    (6000, 5900, 8, 2, 64, None, 0),
+    (9000, 8950, 4, 2, 128, 4500, 7),
+    (4100, 0, 4, 1, 128, 1024, 4),
+    (5000, 0, 2, 2, 64, None, 0),
+])
+def test_packed_loses_no_keys(L, begin, H_q, H_kv, d, window, sinks):
+    q, k, v = rnd(0, L, H_q, d, std=0.5), rnd(1, L, H_kv, d), marks(L, H_kv, d)
+    plan = mapflow.WindowAttention([0, L], H_q, H_kv, d, window=window, sinks=sinks, q_begin=[begin])
+    o = plan.attend(q, k, v)
+    plan.status()
+    for r0 in range(begin, L, 500):
+        r1 = min(L, r0 + 500)
+        seen = ref.seen_packed(torch.arange(r0, r1, device="cuda"), torch.arange(r1, device="cuda"), window, sinks)
+        check_marks(o[r0:r1], q[r0:r1], k[:r1], v[:r1], seen, f"rows {r0} to {r1}")
