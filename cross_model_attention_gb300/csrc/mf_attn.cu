@@ -27,7 +27,6 @@ struct mf_attn_s {
   int grid = 0;
   // packed form
   int rows = 0;                 // rows of q, k, v and o that the sequences cover
-  int q_rows = 0;               // query rows
   int n_segs = 0, n_joins = 0, n_slots = 0;
   AttnSeg* segs_d = nullptr;
   int* cta_d = nullptr;
@@ -52,7 +51,9 @@ constexpr int kMaxTokens = kAttnFar;
 // One sequence's, cache's or prefix's keys: a run over them takes about a
 // second, and the kernel's waits give up after two.
 constexpr int kMaxKeys = 1 << 26;
-constexpr long long kMaxRuns = 1ll << 24;  // of a packed plan (its tables: 1 GB on the host)
+// Of a packed plan: its table takes up to 0.8 GB on the device, and twice that
+// and some 0.3 GB of lists on the host while the plan is made.
+constexpr long long kMaxRuns = 1ll << 24;
 
 void* h_alloc(mf_attn_t h, size_t bytes) {
   if (h->alloc) return h->alloc(bytes, h->ctx, nullptr);
@@ -336,7 +337,6 @@ int mf_attn_create_packed(mf_attn_t* out, const int32_t* cu_seqlens_host, const 
   h->window = window == 0 || window > kAttnFar ? kAttnNoWindow : window;
   h->n_sink = std::min(n_sink, kAttnFar);
   h->rows = cu_seqlens_host[n_seqs];
-  h->q_rows = (int)q_rows;
   h->alloc = alloc_fn;
   h->dealloc = free_fn;
   h->ctx = alloc_ctx;
@@ -351,6 +351,8 @@ int mf_attn_create_packed(mf_attn_t* out, const int32_t* cu_seqlens_host, const 
   std::vector<AttnJoin> joins;
   try {
     cta.assign(h->grid + 1, 0);
+    items.reserve(runs * H_kv);
+    segs.reserve(runs * H_kv + h->grid);  // (cut, the runs are at most that many)
     for (int s = 0; s < n_seqs; ++s) {
       const int start = cu_seqlens_host[s], len = cu_seqlens_host[s + 1] - start;
       for (int head = 0; head < H_kv; ++head)
