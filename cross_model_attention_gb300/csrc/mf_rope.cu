@@ -10,9 +10,11 @@
 //
 // Angles: position * f_i is far larger than a turn for far positions, and its
 // fp32 product would lose the angle (2^-24 of 10^6 radians is 0.06).  The
-// table therefore holds f_i / 2 pi as a 64-bit binary fraction of a turn, so
-// the integer product with the position, taken modulo 2^64, IS the exact
-// fraction of a turn; its top 32 bits go to sincospif.
+// table therefore holds f_i / 2 pi as a 64-bit binary fraction of a turn, whose
+// integer product with the position, taken modulo 2^64, is the fraction of a turn
+// without a further rounding (the entry has that of its fp64 computation: at
+// positions up to 2^27 less than fp32's own, 2^-24); its top 32 bits go to
+// sincospif.
 //
 // Bound: HBM (each row read once, written once).  A group of d * size / 32
 // lanes takes a token's heads one after another: a lane holds two 16-byte

@@ -482,16 +482,19 @@ MF_API int mf_select_noalloc(const float* mass, const int32_t* cu_seqlens_host, 
 #define MF_ROPE_NTK    2  /* base * factor^(rot_dim/(rot_dim-2)) for base         */
 #define MF_ROPE_YARN   3  /* by parts: f_i / factor where a pair turns less than
                              beta_slow times in original_length, f_i where more
-                             than beta_fast times, a ramp over the pairs between;
+                             than beta_fast times, a ramp over the pairs between
+                             (from pair 0 on at the earliest: f_0 is never scaled);
                              gain 0.1 ln(factor) + 1                              */
 #define MF_ROPE_HALF        0  /* pairs (i, i + rot_dim/2)                        */
 #define MF_ROPE_INTERLEAVED 1  /* pairs (2i, 2i + 1)                              */
 
 /*
  * mf_rope_frequencies — the rotary table of rot_dim/2 pairs: each pair's
- * angle per position as a 64-bit binary fraction of a turn (so that angles of
- * far positions are exact: position times entry, modulo 2^64), and the gain
- * by which cosine and sine are multiplied.  Host only.
+ * angle per position as a 64-bit binary fraction of a turn (position times
+ * entry, modulo 2^64, loses nothing however far the position is; the entry itself
+ * is computed in fp64 and off by a few 2^-53 of its value, 5e-7 to 1e-6 radians
+ * at position 2^31), and the gain by which cosine and sine are multiplied.  Host
+ * only.
  *   factor           >= 1 (ignored by MF_ROPE_NONE)
  *   original_length, beta_fast, beta_slow   MF_ROPE_YARN only
  *   turns_out        HOST uint64 [rot_dim/2]     gain_out   HOST float

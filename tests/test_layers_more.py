@@ -72,3 +72,32 @@ def test_offsets_past_32_bits_are_refused():
     refused(lambda: mapflow.WindowAttention([0, 9], 4, 2, 64, sinks=-1))
     refused(lambda: mapflow.mf_rope_frequencies(2 ** 32 + 64))
     refused(lambda: mapflow.mf_rope_frequencies(64, scaling="yarn", factor=2.0, original_length=2 ** 32 + 4096))
+
+
+@pytest.mark.parametrize("rot,base", [(128, 10000.0), (128, 1e6), (96, 500000.0), (20, 10000.0), (2, 10000.0)])
+def test_table_entries_are_off_by_their_fp64_rounding_alone(rot, base):
+    """Against 50 digits.  The exponent x = 2 i / rot is rounded (ln(base) x 2^-53
+    of the power), the power is off by at most one step (2^-52), 2 pi and the
+    division by half a step each (2^-53), and the entry is rounded to a whole."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 50
+    two_pi = 2 * Decimal("3.14159265358979323846264338327950288419716939937510")
+    turns, _ = mapflow.mf_rope_frequencies(rot, base)
+    ln = Decimal(base).ln()
+    for i, t in enumerate(turns):
+        x = Decimal(2 * i) / rot
+        want = (-x * ln).exp() / two_pi * 2 ** 64
+        bound = want * (4 + ln * x) / 2 ** 53 + Decimal("0.5")
+        assert abs(int(t) - want) <= bound, i
+        # as an angle at the farthest position: what the header says
+        assert abs(int(t) - want) / 2 ** 64 * two_pi * 2 ** 31 < Decimal("1e-6") + two_pi / 2 ** 34, i
+
+
+def test_by_parts_scaling_leaves_pair_0():
+    """Also where every pair turns less than beta_slow times in the original length."""
+    plain, _ = mapflow.mf_rope_frequencies(64)
+    for length in (1, 4, 100, 4096):
+        t, _ = mapflow.mf_rope_frequencies(64, scaling="yarn", factor=4.0, original_length=length)
+        assert t[0] == plain[0] and (t <= plain).all()
+    t, _ = mapflow.mf_rope_frequencies(64, scaling="yarn", factor=4.0, original_length=4)
+    np.testing.assert_allclose(t[1:].astype(np.float64), plain[1:] / 4.0, rtol=1e-14)
