@@ -8,8 +8,9 @@
 // The softmax runs in one pass over the keys: m is a running reference, moved
 // (and o, the sum rescaled) only when a block's maximum exceeds it by 2^8, so
 // that exp2 arguments stay below 8 and the rescaling is rare.  Sums and o are
-// fp32; P is rounded to bf16 for the second product (relative 2^-9 for each
-// weight, the same size as the rounding of the output).
+// fp32; P is rounded to bf16 for the second product (at most 2^-8 of each
+// weight, the same size as the rounding of the output): the tensor cores take
+// both its operands in one type, and V is bf16.
 //
 // Rows of a tile: (token, query head of one KV group), TQ = 128 / G tokens of
 // all G heads, so that the heads of a group share every key that is read.

@@ -473,8 +473,10 @@ MF_API int mf_select_noalloc(const float* mass, const int32_t* cu_seqlens_host, 
  * Tensors here are rows of heads with a stride between tokens: token t of a
  * tensor with H heads has its values at t * ld .. t * ld + H * d, so that q, k
  * and v may be parts of one fused projection.  Bases are 16-byte aligned and
- * strides a multiple of 16 bytes (MF_ERR_ARG otherwise).  Products and softmax
- * statistics are fp32; outputs are rounded once.
+ * strides a multiple of 16 bytes (MF_ERR_ARG otherwise).  Scores, softmax
+ * statistics, sums and partial results are fp32 and outputs are rounded once;
+ * attention also rounds each softmax weight to bf16 (by at most 2^-8 of it) for
+ * its product with v, not for the sum that it is divided by.
  * ------------------------------------------------------------------------- */
 
 #define MF_ROPE_NONE   0  /* f_i = base^(-2i/rot_dim) radians per position        */
