@@ -34,9 +34,9 @@
 // that a large matrix product reaches (the tensor pipes 66 % busy; what is left
 // is the chain S -> softmax -> P of the two streams at a time that the registers
 // hold, and a run's start and end).  Decoding: memory; 32 requests of up to 4100
-// visible keys read 0.47 GB in 86 us, 5.5 TB/s of 6.8 (the kernel alone 80 us;
+// visible keys read 0.47 GB in 85 us, 5.5 TB/s of 6.8 (the kernel alone 80 us;
 // four ring stages 90 us, three 107).  A prefix for many rows: both, 200
-// requests with two tokens each over 32767 keys and caches of up to 700 in 196
+// requests with two tokens each over 32767 keys and caches of up to 700 in 194
 // us, of them about 130 the prefix's products and 50 the caches' loads.
 //
 // Masked keys: a row's hidden scores are replaced by -inf before anything is
@@ -241,13 +241,24 @@ struct PackedRuns {
 // and a unit is cut only where a span ends; a block belongs to the span in
 // which it begins.  Every second CTA takes its caches' span first: the
 // prefix's products and the caches' loads then overlap.  Where a CTA's share
-// of both is at most kApart blocks, a second run's start and end costs more
+// of both is at most kApart blocks, a second run's start and end can cost more
 // than that brings: the spans are then as long as the shares together, and
-// prefix and caches meet from the two ends of the CTAs.  (32q/8kv heads of
-// 128, lengths from 1 to the one named, spans of both together against apart:
-// 16 requests of 200 over 4096 18.2 / 22.2 us, 64 of 512 over 16384 45.7 / 44.8,
-// 300 of 600 over 4096 121 / 104, 200 with two new tokens each of 700 over
-// 32768 257 / 240.)
+// prefix and caches meet from the two ends of the CTAs.  32q/8kv heads of 128,
+// lengths from 1 to the one named, spans of both together against apart, us:
+//   share 3   16 requests of 200 over 4096    17.6 / 21.9
+//        11   64 of 512 over 4096             31.8 / 35.2
+//        16   64 of 512 over 16384            45.1 / 44.1
+//        17   16 of 3000 over 16384           37.2 / 44.2
+//        25   128 of 512 over 8192            63.5 / 60.4
+//        26   300 of 100 over 4096            67.5 / 60.0
+//        34   16 of 6000 over 32768           58.4 / 65.8
+//        36   64 of 1500 over 32768           78.3 / 73.1
+//        56   300 of 600 over 4096            121 / 104
+//       130   200 with two new tokens of 700 over 32768  257 / 239
+// Together wins up to about 15 blocks, and where requests are few (16) past 34;
+// where they are many, apart wins from about 16 blocks on.  32 lies between: the
+// rule takes the slower side of some shares from 16 to 34, by at most 13 % in
+// these.
 struct Unit {
   int a1, b0, b1, nb;  // key ranges of a request's cache, in blocks
 };
