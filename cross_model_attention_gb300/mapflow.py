@@ -288,9 +288,8 @@ def _release_parked() -> None:
                 _parked.append((gpu, wait_and_free))
             else:
                 wait_and_free()
-        except Exception:
+        except Exception:  # noqa: BLE001 - the wait failed: keep the memory, see to the others
             _parked.append((gpu, wait_and_free))
-            raise
 
 
 # --------------------------------------------- same names as the C ABI -----

@@ -89,6 +89,13 @@ def test_a_failed_wait_keeps_the_table(gpu, monkeypatch):
     monkeypatch.setattr(torch.cuda, "synchronize", fails)
     del plan
     assert gpu.watch() is not None
+    # and does not keep what is released after it
+    done = []
+    mapflow._release(0, lambda: done.append(1))
+    assert done == [1] and gpu.watch() is not None
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda dev=None: None)
+    mapflow._release_parked()
+    assert gpu.watch() is None
 
 
 # ------------------------------- the library's host code on a fake runtime --
