@@ -178,9 +178,10 @@ def _int(name: str, x) -> int:
 def _ints(name: str, xs) -> np.ndarray:
     """xs as an int32 array (a cast of a wider one would cut it to 32 bits)."""
     wide = np.asarray(xs, dtype=np.int64)
-    if (np.abs(wide) > _INT_MAX).any():
+    cut = np.ascontiguousarray(wide.astype(np.int32))
+    if (cut != wide).any():
         raise MapFlowError(MF_ERR_ARG, f"{name}: a value is out of range")
-    return np.ascontiguousarray(wide.astype(np.int32))
+    return cut
 
 
 def _span(name: str, x, least: int) -> int:

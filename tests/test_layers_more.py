@@ -66,7 +66,7 @@ def test_sizes_past_32_bits_are_refused(name, extra):
 
 
 def test_offsets_past_32_bits_are_refused():
-    for cu in ([0, 2 ** 32 + 5], np.array([0, 2 ** 32 + 5]), np.array([0, 2 ** 31])):
+    for cu in ([0, 2 ** 32 + 5], np.array([0, 2 ** 32 + 5]), np.array([0, 2 ** 31]), np.array([-2 ** 63, 9])):
         refused(lambda: mapflow.WindowAttention(cu, 4, 2, 64))
     refused(lambda: mapflow.WindowAttention([0, 9], 4, 2, 64, q_begin=np.array([2 ** 32])))
     refused(lambda: mapflow.WindowAttention([0, 9], 4, 2, 64, sinks=-1))
