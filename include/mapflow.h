@@ -600,7 +600,9 @@ MF_API int mf_attn_workspace(mf_attn_t h, int n, int64_t* bytes);
  *   dtype        MF_DTYPE_BF16 (MF_ERR_UNSUPPORTED otherwise)
  *   scale        > 0, e.g. 1/sqrt(d)
  * Asynchronous, no host synchronisation, no state kept in the plan between
- * calls (a failed device-side wait is recorded for mf_attn_status).
+ * calls (a failed device-side wait is recorded for mf_attn_status).  A captured
+ * call reads the plan's tables at every replay: the plan has to outlive its
+ * graphs, and the graph's inputs and workspace as for any captured kernel.
  *
  * mf_attn_cached — the cache form for n <= n_max requests.
  *   q, o         [n * Lq][H_q][d];  lse fp32 [n * Lq][H_q] or NULL
