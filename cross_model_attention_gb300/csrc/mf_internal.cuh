@@ -258,6 +258,69 @@ cudaError_t launch_attn_cache(const AttnParams& p, int d, int grid, const CUtens
                               const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tkp,
                               const CUtensorMap& tvp, const CUtensorMap& tqc, cudaStream_t s);
 
+// A paged cache and the tokens that go in or come out (mf_cache.cu).
+struct CacheParams {
+  // the cache: 4-bit pages, or (pages null) bf16 rows of heads
+  uint8_t* pages;
+  void* k;
+  void* v;
+  long long ld_k, ld_v;        // elements between tokens
+  const float* k_scale;        // [H] or null (ones)
+  const float* v_scale;
+  long long n_pages;
+  int ps, H;                   // tokens of a page, heads
+  // where the tokens are
+  const int* seq;              // [T]
+  const int* at;               // [T]
+  const int* table;            // [n_seqs][max_pages], ld_table apart
+  long long ld_table;
+  int n_seqs, max_pages;
+  // append
+  const void* k_in;
+  const void* v_in;
+  long long ld_kin, ld_vin;    // (read: of k_out and v_out)
+  const int* positions;        // [T]
+  const unsigned long long* freq;
+  int rot, layout, norm;
+  float eps, gain;
+  const void* weight;          // [d] or null (ones)
+  // read
+  void* k_out;
+  void* v_out;
+  // set by the launcher
+  long long n_units;
+  int heads_per_unit, shares;
+};
+cudaError_t launch_cache_append(const CacheParams& p, long long T, int d, cudaStream_t s);
+cudaError_t launch_cache_read(const CacheParams& p, long long T, int d, cudaStream_t s);
+
+// Decoding attention over a paged cache in 4 bits (mf_paged.cu).
+struct PagedParams {
+  const uint8_t* pages;
+  const float* k_scale;        // [H_kv] or null
+  const float* v_scale;
+  long long n_pages;
+  int ps, H_kv, G;
+  const int* table;            // [n][max_pages], ld_table apart
+  long long ld_table;
+  int max_pages;
+  const int* lens;             // [n]
+  const float* slopes;         // [H_q] or null
+  const void* q;               // [n * Lq][H_q][d] bf16
+  void* o;
+  long long ld_q, ld_o;
+  float* lse;                  // [n * Lq][H_q] or null
+  int n, Lq, window, n_sink;
+  float scale, cap;            // cap 0: none
+  // workspace: a CTA's two partial results and a warp's one
+  float* part_o;               // [2 grid + warps][rows][d]
+  float2* part_ml;             // [2 grid + warps][rows]
+  int4* cuts;                  // [2 grid]
+  int rows;                    // of a partial result
+};
+// What a launch takes: CTAs, partial results and rows of one.
+void paged_shape(int Lq, int G, int sms, int* grid, int* parts, int* rows);
+cudaError_t launch_paged(const PagedParams& p, int d, cudaStream_t s);
 cudaError_t launch_selftest_wait(int* err, unsigned long long limit_ns, cudaStream_t s);
 
 }  // namespace mf

@@ -1,0 +1,839 @@
+// mf_paged.cu — decoding attention over a paged cache held in 4 bits
+// (mf_attn_paged), sm_103a.
+//
+// For new token t of a request with len keys, at position i = len - Lq + t, over
+// the keys j <= i with i - j < window or j < sinks:
+//   s_j = scale q.k_j,  cap tanh(s_j / cap) where scores are capped,
+//   less slope (i - j) where there is a bias by distance,
+//   o = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),  lse = m + log(sum_j exp(s_j - m)).
+//
+// What bounds it: a key and a value of one head are 9 d / 8 bytes (144 at d =
+// 128), which an SM's share of memory brings every 6 cycles, but 2 d numbers that
+// have to become operands of a matrix product.  They do so in registers: a warp
+// takes 16 keys at a time as the A operand of 16 x 8 x 16 products, K against q
+// and V (transposed) against the weights, whose rows are few in decoding (8 to a
+// product, the query heads of a KV head and its new tokens).  Through shared
+// memory, as tcgen05 takes its operands, the 512 bytes of a key and value
+// unpacked to fp16 would be written once and read once: 8 cycles at 128 bytes a
+// cycle, more than memory needs to bring them.
+//
+// An e2m1 code times its e4m3 scale is exact in fp16, so K and V meet the
+// products as they are held; q goes there scaled by a power of two per row (its
+// bf16 values then are exact in fp16 within 2^-32 of the row's largest), weights
+// scaled by 2^7 (off by 2^-11, or 2^-32 of the row's largest).  Sums, the
+// softmax's statistics and o are fp32.
+//
+// One pass over the keys: a row's reference m moves (and o and the sum are
+// rescaled) only where a score exceeds it by 2^8.
+//
+// Work: tiles of 32 or 64 keys of all (request, head) pairs laid end to end, cut
+// into equal spans, one per warp; a warp has a ring of tiles of its own in shared
+// memory, filled by cp.async, and waits for no other warp until the end.  Pieces
+// of a pair that warps of a CTA share are joined in shared memory, those that
+// CTAs share through the workspace, by a second kernel; both in a fixed order.
+#include <cstdint>
+
+#include <cuda_bf16.h>
+
+#include "mf_fp4.cuh"
+#include "mf_internal.cuh"
+#include "mf_ptx.cuh"
+
+namespace mf {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kRingBytes = 221184;   // of a CTA
+constexpr int kCost = 1;             // a pair's start and end, in tiles
+constexpr int kMinSpan = 2;          // least work of a CTA, in tiles
+constexpr float kLift = 7.f;         // weights are held times 2^7
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// D dimensions, NT times 8 rows to a unit of work.
+template <int D, int NT>
+struct Cfg {
+  static constexpr int W = NT == 1 ? 16 : 8;            // warps
+  static constexpr int NB = D == 128 && NT == 1 ? 2 : 4;  // 16-key blocks of a tile
+  static constexpr int TK = NB * 16;
+  static constexpr int kPiece = fp4_piece(D);
+  static constexpr int kStage = NB * kPiece;
+  static constexpr int kRing = kRingBytes / W;
+  static constexpr int S = kRing / kStage;
+  static constexpr int R = 8 * NT;
+  static constexpr int kThreads = 32 * W;
+  static constexpr int kPrefix = kRingBytes;             // [threads + 1] long long
+  static constexpr int kDesc = kPrefix + 8 * (kThreads + 2);
+  static constexpr int kPieces = kDesc + 32 * W * S;
+  static constexpr int kBytes = kPieces + 16 * 2 * W;
+  static_assert(kBytes <= 232448, "shared memory");
+  static_assert(R * D * 4 + R * 8 <= kRing, "a partial result in a warp's ring");
+  static_assert(S >= 2 && 32 % NB == 0, "ring");
+};
+
+// A tile in the ring: what the consumer has to know of it.
+struct alignas(16) Desc {
+  int key0, flags, r, u;
+  int len, end, pad0, pad1;
+};
+enum { kFirst = 1, kLast = 2, kBegins = 4, kEnds = 8, kMore = 16, kBadShift = 8 };
+// A partial result of a warp.
+struct alignas(16) Piece {
+  int r, u, flags, end;  // end: the last CTA with tiles of the unit
+};
+enum { kHere = 1 };
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), fp16.
+__device__ __forceinline__ void mma(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Bits of x where m has ones, of y elsewhere.
+__device__ __forceinline__ uint32_t select(uint32_t m, uint32_t x, uint32_t y) { return (m & x) | (~m & y); }
+
+// The tiles of a request: [0, ta) and [tb, tb + nt - ta) of its keys.
+struct Tiles {
+  int len, ta, tb, nt;
+};
+template <int TK>
+__device__ __forceinline__ Tiles tiles_of(const PagedParams& p, int len) {
+  Tiles t;
+  t.len = min(max(len, 0), p.max_pages * p.ps);
+  const int b0 = max(0, t.len - p.Lq - p.window + 1);
+  t.tb = b0 / TK;
+  t.ta = min(t.tb, (min(p.n_sink, t.len) + TK - 1) / TK);
+  t.nt = t.ta + (t.len + TK - 1) / TK - t.tb;
+  return t;
+}
+__device__ __forceinline__ long long line_of(const Tiles& t, int units) {
+  return t.nt > 0 ? static_cast<long long>(units) * (kCost + t.nt) : 0;
+}
+
+// Where row `row` of unit u of request r is in q and o, its head; false past the last row.
+struct Row {
+  long long tok;
+  int head, t;
+};
+__device__ __forceinline__ bool row_of(const PagedParams& p, int r, int u, int row, int R, Row& x) {
+  const int rg = u / p.H_kv, h = u - rg * p.H_kv, rr = rg * R + row;
+  if (rr >= p.Lq * p.G) return false;
+  x.t = rr / p.G;
+  x.head = h * p.G + rr - x.t * p.G;
+  x.tok = static_cast<long long>(r) * p.Lq + x.t;
+  return true;
+}
+__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : (m - kLift + log2f(l)) * kLn2; }
+__device__ __forceinline__ float inv_of(const PagedParams& p, int h, float l) {
+  return l == 0.f ? 0.f : (p.v_scale ? p.v_scale[h] : 1.f) / l;
+}
+// A piece's weight beside others under the common reference M.
+__device__ __forceinline__ float weight_of(float m, float l, float M) {
+  return m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2(m - M);  // (a sum without a reference is NaN)
+}
+
+// A warp's D / 32 values of a joined row.
+template <int D>
+__device__ __forceinline__ void store_row(const PagedParams& p, int r, int u, int row, int R, float M, float L, const float* acc) {
+  Row x;
+  if (!row_of(p, r, u, row, R, x)) return;
+  const int lane = threadIdx.x & 31;
+  const float inv = inv_of(p, x.head / p.G, L);
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + x.tok * p.ld_o + x.head * D + lane * (D / 32);
+  uint32_t w[D / 64];
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) w[i] = L == 0.f ? 0u : pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+  if (D == 128) *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[D / 64 - 1]);
+  else *reinterpret_cast<uint32_t*>(o) = w[0];
+  if (p.lse && lane == 0) p.lse[x.tok * (p.H_kv * p.G) + x.head] = lse_of(M, L);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const PagedParams p) {
+  using C = Cfg<D, NT>;
+  constexpr int W = C::W, NB = C::NB, TK = C::TK, S = C::S;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int units = p.H_kv * ((p.Lq * p.G + C::R - 1) / C::R);
+  long long* prefix = reinterpret_cast<long long*>(smem + C::kPrefix);
+  Desc* desc = reinterpret_cast<Desc*>(smem + C::kDesc) + warp * S;
+  Piece* pieces = reinterpret_cast<Piece*>(smem + C::kPieces);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up
+
+  // ---- the lines: a thread sums those of consecutive requests
+  const int share = (p.n + C::kThreads - 1) / C::kThreads;
+  long long sum = 0;
+  for (int r = threadIdx.x * share; r < min(p.n, (static_cast<int>(threadIdx.x) + 1) * share); ++r)
+    sum += line_of(tiles_of<TK>(p, p.lens[r]), units);
+  {
+    long long inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(kFull, inc, o);
+      if (lane >= o) inc += y;
+    }
+    // (the warps' sums first, in the rows' place)
+    if (lane == 31) prefix[warp] = inc;
+    __syncthreads();
+    long long before = 0;
+    for (int w = 0; w < warp; ++w) before += prefix[w];
+    __syncthreads();
+    prefix[threadIdx.x + 1] = before + inc;
+    if (threadIdx.x == 0) prefix[0] = 0;
+  }
+  if (lane < 2) pieces[2 * warp + lane].flags = 0;
+  __syncthreads();
+  const long long total = prefix[C::kThreads];
+  const long long per = max(static_cast<long long>(kMinSpan), (total + gridDim.x - 1) / gridDim.x);
+  const long long cta0 = min(total, per * blockIdx.x), cta1 = min(total, cta0 + per);
+  const long long f0 = cta0 + (cta1 - cta0) * warp / W, f1 = cta0 + (cta1 - cta0) * (warp + 1) / W;
+
+  // ---- requests without keys
+  for (int r = blockIdx.x + gridDim.x * warp; r < p.n; r += gridDim.x * W) {
+    if (tiles_of<TK>(p, p.lens[r]).nt > 0) continue;
+    const int H = p.H_kv * p.G;
+    for (int i = lane; i < p.Lq * H * (D / 8); i += 32) {
+      const int tt = i / (H * (D / 8)), x = i - tt * (H * (D / 8));
+      reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + (static_cast<long long>(r) * p.Lq + tt) * p.ld_o)[x] =
+          make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (p.lse)
+      for (int i = lane; i < p.Lq * H; i += 32) p.lse[static_cast<long long>(r) * p.Lq * H + i] = -INFINITY;
+  }
+
+  // ---- the walk over this warp's span
+  int wr = p.n, wu = 0;       // request and unit of the line at `at`
+  long long at = total;
+  Tiles wt{0, 0, 0, 0};
+  if (f0 < f1) {
+    // the thread whose requests' lines f0 lies in, then the request
+    int j = 0;
+    {
+      constexpr int kStep = C::kThreads / 32;
+      const unsigned c = __ballot_sync(kFull, prefix[lane * kStep] <= f0);
+      const int hi = 31 - __clz(c);
+      const unsigned f = __ballot_sync(kFull, lane < kStep && prefix[hi * kStep + (lane & (kStep - 1))] <= f0);
+      j = hi * kStep + 31 - __clz(f);
+    }
+    at = prefix[j];
+    for (int r0 = j * share; r0 < p.n; r0 += 32) {
+      const int r = r0 + lane;
+      const Tiles x = tiles_of<TK>(p, r < p.n ? p.lens[r] : 0);
+      const long long mine = line_of(x, units);
+      long long inc = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(kFull, inc, o);
+        if (lane >= o) inc += y;
+      }
+      const unsigned hit = __ballot_sync(kFull, at + inc > f0);
+      if (hit) {
+        const int k = __ffs(hit) - 1;
+        wr = r0 + k;
+        at += __shfl_sync(kFull, inc - mine, k);
+        break;
+      }
+      at += __shfl_sync(kFull, inc, 31);
+    }
+    if (wr < p.n) {
+      wt = tiles_of<TK>(p, p.lens[wr]);
+      wu = static_cast<int>((f0 - at) / (kCost + wt.nt));
+      at += static_cast<long long>(wu) * (kCost + wt.nt);
+    }
+  }
+  // the piece at hand: tiles i .. i1 of unit pu of request pr
+  int pr = 0, pu = 0, i = 0, i1 = 0, pstart = 0;
+  bool pbegins = false, pends = false;
+  Tiles pt{0, 0, 0, 0};
+  auto next_piece = [&]() {
+    while (at < f1 && wr < p.n) {
+      if (wu == units) {  // to the next request with keys
+        wu = 0;
+        int r0 = wr + 1;
+        wr = p.n;
+        for (; r0 < p.n; r0 += 32) {
+          const int r = r0 + lane;
+          const unsigned some = __ballot_sync(kFull, r < p.n && tiles_of<TK>(p, p.lens[min(r, p.n - 1)]).nt > 0);
+          if (some) {
+            wr = r0 + __ffs(some) - 1;
+            break;
+          }
+        }
+        if (wr >= p.n) return false;
+        wt = tiles_of<TK>(p, p.lens[wr]);
+      }
+      const long long b = at + kCost;
+      const int lo = static_cast<int>(max(0ll, f0 - b)), hi = static_cast<int>(min(static_cast<long long>(wt.nt), f1 - b));
+      pr = wr;
+      pu = wu;
+      at += kCost + wt.nt;
+      ++wu;
+      if (lo < hi) {
+        i = pstart = lo;
+        i1 = hi;
+        pbegins = lo == 0;
+        pends = hi == wt.nt;
+        pt = wt;
+        return true;
+      }
+    }
+    return false;
+  };
+  bool have = next_piece();
+  int fill = 0;            // the ring's next slot
+  long long offs = 0;      // lane's block of the next 32: its bytes' place, or -1
+  const long long hstride = static_cast<long long>(p.ps / kFp4Block) * C::kPiece;
+  const uint32_t ring = sb + warp * C::kRing;
+  auto issue = [&]() {
+    if (have) {
+      const int k = (i - pstart) * NB;
+      if ((k & 31) == 0) {
+        const int ii = i + lane / NB, b = lane % NB;
+        const int tile = ii < pt.ta ? ii : pt.tb + ii - pt.ta;
+        const int key = (tile * NB + b) * kFp4Block;
+        offs = -1;
+        if (ii < i1 && key < pt.len) {
+          const int page = key / p.ps;
+          const int id = p.table[pr * p.ld_table + page];
+          if (id >= 0 && id < p.n_pages)
+            offs = (static_cast<long long>(id) * p.H_kv + pu % p.H_kv) * hstride + (key - page * p.ps) / kFp4Block * C::kPiece;
+        }
+      }
+      const uint32_t dst = ring + fill * C::kStage;
+      int bad = 0;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const long long off = __shfl_sync(kFull, offs, (k + b) & 31);
+        if (off < 0) {
+          bad |= 1 << b;
+        } else {
+#pragma unroll
+          for (int c = 0; c < C::kPiece / 16; c += 32)
+            if (c + lane < C::kPiece / 16) cp16(dst + b * C::kPiece + (c + lane) * 16, p.pages + off + (c + lane) * 16);
+        }
+      }
+      Desc d;
+      d.key0 = (i < pt.ta ? i : pt.tb + i - pt.ta) * TK;
+      d.r = pr;
+      d.u = pu;
+      d.len = pt.len;
+      d.flags = (i == pstart ? kFirst : 0) | (pbegins ? kBegins : 0) | (pends ? kEnds : 0) | bad << kBadShift;
+      d.end = 0;
+      if (++i == i1) {
+        d.flags |= kLast;
+        d.end = static_cast<int>((at - 1) / per);
+        have = next_piece();
+        if (have) d.flags |= kMore;
+      }
+      if (lane == 0) desc[fill] = d;
+      if (++fill == S) fill = 0;
+    }
+    cp_commit();
+  };
+
+  // ---- tiles
+  uint32_t qf[NT][D / 16][2];
+  float acc[D / 16][NT][4], m[NT][2], l[NT][2], coef[NT][2], slope[NT][2];
+  int prow[NT][2];
+#pragma unroll 1
+  for (int s = 0; s < S - 1; ++s) issue();
+  int slot = 0;
+  bool any = f0 < f1;
+  for (; any;) {
+    // (a warp without tiles has an empty ring: its first descriptor says so)
+    cp_wait<S - 2>();
+    __syncwarp();
+    const bool left = fill != slot;
+    if (!left) break;
+    const Desc d = desc[slot];
+    const uint32_t st = ring + slot * C::kStage;
+    issue();
+    if (d.flags & kFirst) {
+      const int h = d.u % p.H_kv;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        Row x;
+        const bool ok = row_of(p, d.r, d.u, nt * 8 + g, C::R, x);
+        uint4 w[D / 32];
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          w[c] = make_uint4(0u, 0u, 0u, 0u);
+          if (ok) w[c] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + x.tok * p.ld_q + x.head * D + t * (D / 4) + c * 8);
+          const uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, max(v[e] & 0x7fffu, (v[e] >> 16) & 0x7fffu));
+        }
+        top = max(top, __shfl_xor_sync(kFull, top, 1));
+        top = max(top, __shfl_xor_sync(kFull, top, 2));
+        // 2^e brings the row's largest to [2^14, 2^15)
+        const int ex = static_cast<int>(top >> 7);
+        const bool fine = ex < 255;
+        const int e = top == 0 || !fine ? 0 : min(120, 141 - ex);
+        const float up = __int_as_float((e + 127) << 23);
+        float c = p.scale * (p.k_scale ? p.k_scale[h] : 1.f) * __int_as_float((127 - e) << 23);
+        c *= p.cap > 0.f ? 1.f / p.cap : kLog2e;
+        if (!fine) c = NAN;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          const uint32_t v[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) qf[nt][2 * k + (j >> 1)][j & 1] = pack_f16x2(bf16lo(v[j]) * up, bf16hi(v[j]) * up);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          coef[nt][j] = __shfl_sync(kFull, c, (2 * t + j) * 4);
+          Row y;
+          const bool is = row_of(p, d.r, d.u, nt * 8 + 2 * t + j, C::R, y);
+          prow[nt][j] = is ? d.len - p.Lq + y.t : -1;
+          slope[nt][j] = is && p.slopes ? p.slopes[y.head] * kLog2e : 0.f;
+          m[nt][j] = -INFINITY;
+          l[nt][j] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int a = 0; a < D / 16; ++a)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[a][nt][e] = 0.f;
+    }
+
+    // S = K q^T: rows are keys, columns the unit's rows
+    float x[NB][NT][4];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[b][nt][e] = 0.f;
+      const uint32_t base = st + b * C::kPiece;
+      uint32_t k0[D / 32], k1[D / 32];  // a lane's codes of keys g and g + 8
+      uint32_t s0, s1;                  // their scales, one or two
+      if (D == 128) {
+        const uint4 a = lds128(base + g * 64 + t * 16), c = lds128(base + (g + 8) * 64 + t * 16);
+        k0[0] = a.x, k0[1] = a.y, k0[D / 32 - 2] = a.z, k0[D / 32 - 1] = a.w;
+        k1[0] = c.x, k1[1] = c.y, k1[D / 32 - 2] = c.z, k1[D / 32 - 1] = c.w;
+        s0 = e4m3x2_f16x2(lds16(base + 16 * D + g * 8 + t * 2));
+        s1 = e4m3x2_f16x2(lds16(base + 16 * D + (g + 8) * 8 + t * 2));
+      } else {
+        const uint2 a = lds64(base + g * 32 + t * 8), c = lds64(base + (g + 8) * 32 + t * 8);
+        k0[0] = a.x, k0[1] = a.y;
+        k1[0] = c.x, k1[1] = c.y;
+        s0 = e4m3x2_f16x2(lds8(base + 16 * D + g * 4 + t));
+        s1 = e4m3x2_f16x2(lds8(base + 16 * D + (g + 8) * 4 + t));
+      }
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w) {
+        const bool second = D == 128 && w >= 2;  // of the lane's two blocks of 16
+        const uint32_t f0_ = __byte_perm(s0, 0, second ? 0x3232 : 0x1010);
+        const uint32_t f1_ = __byte_perm(s1, 0, second ? 0x3232 : 0x1010);
+        const uint32_t a0 = mul_f16x2(e2m1x2_f16x2<0>(k0[w]), f0_), a1 = mul_f16x2(e2m1x2_f16x2<0>(k1[w]), f1_);
+        const uint32_t a2 = mul_f16x2(e2m1x2_f16x2<1>(k0[w]), f0_), a3 = mul_f16x2(e2m1x2_f16x2<1>(k1[w]), f1_);
+        const uint32_t c0 = mul_f16x2(e2m1x2_f16x2<2>(k0[w]), f0_), c1 = mul_f16x2(e2m1x2_f16x2<2>(k1[w]), f1_);
+        const uint32_t c2 = mul_f16x2(e2m1x2_f16x2<3>(k0[w]), f0_), c3 = mul_f16x2(e2m1x2_f16x2<3>(k1[w]), f1_);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma(x[b][nt], a0, a1, a2, a3, qf[nt][2 * w][0], qf[nt][2 * w][1]);
+          mma(x[b][nt], c0, c1, c2, c3, qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
+        }
+      }
+    }
+
+    // scores, in base 2
+    const bool whole = d.key0 + TK - 1 <= d.len - p.Lq && (d.flags >> kBadShift) == 0 &&
+                       (d.len - 1 - d.key0 < p.window || d.key0 + TK <= p.n_sink);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[b][nt][e] *= coef[nt][e & 1];
+    if (p.cap > 0.f) {
+      const float c2 = p.cap * kLog2e;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[b][nt][e] = c2 * tanhf(x[b][nt][e]);
+    }
+    if (p.slopes) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[b][nt][e] += slope[nt][e & 1] * static_cast<float>(d.key0 + 16 * b + g + (e & 2) * 4 - prow[nt][e & 1]);
+    }
+    if (!whole) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = d.key0 + 16 * b + g + (e & 2) * 4, far = prow[nt][e & 1] - j;
+            const bool seen = far >= 0 && (far < p.window || j < p.n_sink) && !(d.flags >> (kBadShift + b) & 1);
+            if (!seen) x[b][nt][e] = -INFINITY;
+          }
+    }
+
+    // the rows' references
+    {
+      float mx[NT][2];
+      bool up = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          mx[nt][j] = -INFINITY;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) mx[nt][j] = fmaxf(mx[nt][j], fmaxf(x[b][nt][j], x[b][nt][2 + j]));
+          up |= mx[nt][j] > m[nt][j] + 8.f;
+        }
+      if (__any_sync(kFull, up)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float y = mx[nt][j];
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(kFull, y, o));
+            const float old = m[nt][j];
+            const bool move = y > old + 8.f;
+            const float f = !move ? 1.f : old == -INFINITY ? 0.f : ex2(old - y);
+            if (move) m[nt][j] = y;
+            l[nt][j] *= f;
+#pragma unroll
+            for (int a = 0; a < D / 16; ++a) {
+              acc[a][nt][j] *= f;
+              acc[a][nt][2 + j] *= f;
+            }
+          }
+      }
+    }
+    // weights, and as the B operand: keys by rows
+    uint32_t pf[NB][NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float lift[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) lift[j] = kLift - (m[nt][j] == -INFINITY ? 0.f : m[nt][j]);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = ex2(x[b][nt][e] + lift[e & 1]);
+        l[nt][0] += w[0] + w[2];
+        l[nt][1] += w[1] + w[3];
+        pf[b][nt][0] = transpose8x8(pack_f16x2(w[0], w[1]));
+        pf[b][nt][1] = transpose8x8(pack_f16x2(w[2], w[3]));
+      }
+    }
+
+    // O^T += V^T P^T: rows are dimensions
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const uint32_t base = st + b * C::kPiece;
+      constexpr int NW = D / 64;  // words (8 dimensions) of a lane
+      uint32_t va[2][NW], vb[2][NW], sc[2];  // keys 2t and 2t + 1 of each half
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        if (D == 128) {
+          const uint4 v = lds128(base + 8 * D + hf * 512 + g * 64 + t * 16);
+          va[hf][0] = v.x, va[hf][NW - 1] = v.y;
+          vb[hf][0] = v.z, vb[hf][NW - 1] = v.w;
+          sc[hf] = e4m3x2_f16x2(lds16(base + 17 * D + g * 16 + hf * 8 + t * 2));
+        } else {
+          const uint32_t at_ = base + 8 * D + hf * 256 + (g >> 1) * 64 + t * 16 + (g & 1) * 4;
+          va[hf][0] = lds32(at_);
+          vb[hf][0] = lds32(at_ + 8);
+          sc[hf] = e4m3x2_f16x2(lds16(base + 17 * D + (g >> 1) * 16 + hf * 8 + t * 2));
+        }
+        if (!whole) {  // what no row sees may be anything
+          const int b0 = d.len - p.Lq - p.window + 1;
+          uint32_t keep = 0;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int key = d.key0 + 16 * b + 8 * hf + 2 * t + j;
+            const bool dead = key >= d.len || (key < b0 && key >= p.n_sink) || (d.flags >> (kBadShift + b) & 1);
+            keep |= dead ? 0u : 0xffffu << (16 * j);
+          }
+          sc[hf] &= keep;
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        // codes of both keys to each dimension: even ones and odd ones
+        uint32_t ev[2], od[2];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          ev[hf] = select(0x0f0f0f0fu, va[hf][w], vb[hf][w] << 4);
+          od[hf] = select(0x0f0f0f0fu, va[hf][w] >> 4, vb[hf][w]);
+        }
+        auto four = [&](auto I) {
+          constexpr int kI = decltype(I)::value;
+          const uint32_t a0 = mul_f16x2(e2m1x2_f16x2<kI>(ev[0]), sc[0]), a1 = mul_f16x2(e2m1x2_f16x2<kI>(od[0]), sc[0]);
+          const uint32_t a2 = mul_f16x2(e2m1x2_f16x2<kI>(ev[1]), sc[1]), a3 = mul_f16x2(e2m1x2_f16x2<kI>(od[1]), sc[1]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma(acc[4 * w + kI][nt], a0, a1, a2, a3, pf[b][nt][0], pf[b][nt][1]);
+        };
+        four(std::integral_constant<int, 0>());
+        four(std::integral_constant<int, 1>());
+        four(std::integral_constant<int, 2>());
+        four(std::integral_constant<int, 3>());
+      }
+    }
+
+    if (d.flags & kLast) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) l[nt][j] += __shfl_xor_sync(kFull, l[nt][j], o);
+      const bool done = (d.flags & (kBegins | kEnds)) == (kBegins | kEnds);
+      const bool more = d.flags & kMore;
+      // a whole unit's rows, or a partial result: in the ring, which is empty
+      // then, or in the workspace where the warp goes on
+      const long long spot = 2ll * gridDim.x + static_cast<long long>(blockIdx.x) * W + warp;
+      float* po = more ? p.part_o + spot * p.rows * D : reinterpret_cast<float*>(smem + warp * C::kRing);
+      float2* pm = more ? p.part_ml + spot * p.rows : reinterpret_cast<float2*>(smem + warp * C::kRing + C::R * D * 4);
+      __syncwarp();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int row = nt * 8 + 2 * t + j;
+          Row y;
+          if (!row_of(p, d.r, d.u, row, C::R, y)) continue;
+          const float L = l[nt][j];
+          if (done) {
+            const float inv = inv_of(p, y.head / p.G, L);
+            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + y.tok * p.ld_o + y.head * D + g * (D / 8);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = L == 0.f ? 0u : pack_bf16x2(acc[4 * c + e][nt][j] * inv, acc[4 * c + e][nt][2 + j] * inv);
+              reinterpret_cast<uint4*>(o)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            if (p.lse && g == 0) p.lse[y.tok * (p.H_kv * p.G) + y.head] = lse_of(m[nt][j], L);
+          } else {
+            float* to = po + row * D + g * (D / 8);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c)
+              reinterpret_cast<float4*>(to)[c] = make_float4(acc[2 * c][nt][j], acc[2 * c][nt][2 + j],
+                                                             acc[2 * c + 1][nt][j], acc[2 * c + 1][nt][2 + j]);
+            if (g == 0) pm[row] = make_float2(m[nt][j], L);
+          }
+        }
+      if (!done && lane == 0) pieces[2 * warp + (more ? 0 : 1)] = Piece{d.r, d.u, kHere | (d.flags & (kBegins | kEnds)), d.end};
+    }
+    if (++slot == S) slot = 0;
+  }
+
+  // ---- the CTA's pieces: those of one unit follow each other
+  __syncthreads();
+  Piece mine{0, 0, 0, 0};
+  if (lane < 2 * W) mine = pieces[lane];
+  const unsigned present = __ballot_sync(kFull, (mine.flags & kHere) != 0);
+  const unsigned lower = present & ((1u << lane) - 1u);
+  const int prev = lower ? 31 - __clz(lower) : lane;
+  const int prev_r = __shfl_sync(kFull, mine.r, prev), prev_u = __shfl_sync(kFull, mine.u, prev);
+  const bool leads = (mine.flags & kHere) && (!lower || prev_r != mine.r || prev_u != mine.u);
+  const unsigned leaders = __ballot_sync(kFull, leads);
+  int item = 0;
+  int4 tail = make_int4(-1, 0, 0, 0);
+  for (unsigned rest = leaders; rest; rest &= rest - 1) {
+    const int first = __ffs(rest) - 1;
+    const unsigned after = rest & (rest - 1);
+    const unsigned group = present & ~((1u << first) - 1u) & (after ? (1u << (__ffs(after) - 1)) - 1u : kFull);
+    const int last = 31 - __clz(group);
+    const int r = __shfl_sync(kFull, mine.r, first), u = __shfl_sync(kFull, mine.u, first);
+    const bool begins = __shfl_sync(kFull, mine.flags, first) & kBegins, ends = __shfl_sync(kFull, mine.flags, last) & kEnds;
+    const int end = __shfl_sync(kFull, mine.end, last);
+    if (begins && !ends) tail = make_int4(r, u, end, 0);
+    const int rows = min(C::R, p.Lq * p.G - u / p.H_kv * C::R);
+    for (int row = 0; row < rows; ++row, ++item) {
+      if (item % W != warp) continue;
+      const float* src = nullptr;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (group >> lane & 1) {
+        const int w = lane >> 1;
+        if (lane & 1) {
+          src = reinterpret_cast<const float*>(smem + w * C::kRing) + row * D;
+          ml = reinterpret_cast<const float2*>(smem + w * C::kRing + C::R * D * 4)[row];
+        } else {
+          const long long spot = 2ll * gridDim.x + static_cast<long long>(blockIdx.x) * W + w;
+          src = p.part_o + (spot * p.rows + row) * D;
+          ml = p.part_ml[spot * p.rows + row];
+        }
+      }
+      float M = ml.x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+      const float wt_ = weight_of(ml.x, ml.y, M);
+      float L = wt_ * ml.y;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) L += __shfl_xor_sync(kFull, L, o);
+      float out[D / 32];
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) out[e] = 0.f;
+      for (unsigned x = group; x; x &= x - 1) {
+        const int k = __ffs(x) - 1;
+        const float f = __shfl_sync(kFull, wt_, k);
+        const float* s = reinterpret_cast<const float*>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(src), k)) + lane * (D / 32);
+        if (D == 128) {
+          const float4 v = *reinterpret_cast<const float4*>(s);
+          out[0] = fmaf(f, v.x, out[0]), out[1] = fmaf(f, v.y, out[1]);
+          out[D / 32 - 2] = fmaf(f, v.z, out[D / 32 - 2]), out[D / 32 - 1] = fmaf(f, v.w, out[D / 32 - 1]);
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(s);
+          out[0] = fmaf(f, v.x, out[0]), out[1] = fmaf(f, v.y, out[1]);
+        }
+      }
+      if (begins && ends) {
+        store_row<D>(p, r, u, row, C::R, M, L, out);
+      } else {
+        const long long spot = 2ll * blockIdx.x + (begins ? 1 : 0);
+        float* to = p.part_o + (spot * p.rows + row) * D + lane * (D / 32);
+        if (D == 128) *reinterpret_cast<float4*>(to) = make_float4(out[0], out[1], out[D / 32 - 2], out[D / 32 - 1]);
+        else *reinterpret_cast<float2*>(to) = make_float2(out[0], out[1]);
+        if (lane == 0) p.part_ml[spot * p.rows + row] = make_float2(M, L);
+      }
+    }
+  }
+  if (threadIdx.x == 0) p.cuts[blockIdx.x] = tail;
+}
+
+// The units that several CTAs share: a warp to a row, the results of CTA c's
+// last unit and of the following CTAs' first.
+template <int D, int NT>
+__global__ void __launch_bounds__(32) join_kernel(const PagedParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x, row = blockIdx.y, lane = threadIdx.x;
+  const int4 cut = p.cuts[c];
+  if (cut.x < 0) return;
+  Row x;
+  if (!row_of(p, cut.x, cut.y, row, 8 * NT, x)) return;
+  const int n = cut.z - c + 1;
+  auto spot = [&](int k) { return k == 0 ? 2ll * c + 1 : 2ll * (c + k); };
+  float M = -INFINITY, L = 0.f;
+  for (int k = lane; k < n; k += 32) M = fmaxf(M, p.part_ml[spot(k) * p.rows + row].x);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+  float out[D / 32];
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) out[e] = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < n; ++k) {
+    const float2 ml = p.part_ml[spot(k) * p.rows + row];
+    const float f = weight_of(ml.x, ml.y, M);
+    L += f * ml.y;
+    const float* s = p.part_o + (spot(k) * p.rows + row) * D + lane * (D / 32);
+    if (D == 128) {
+      const float4 v = *reinterpret_cast<const float4*>(s);
+      out[0] = fmaf(f, v.x, out[0]), out[1] = fmaf(f, v.y, out[1]);
+      out[D / 32 - 2] = fmaf(f, v.z, out[D / 32 - 2]), out[D / 32 - 1] = fmaf(f, v.w, out[D / 32 - 1]);
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(s);
+      out[0] = fmaf(f, v.x, out[0]), out[1] = fmaf(f, v.y, out[1]);
+    }
+  }
+  store_row<D>(p, cut.x, cut.y, row, 8 * NT, M, L, out);
+}
+
+template <int D, int NT>
+cudaError_t launch_t(const PagedParams& p, cudaStream_t s) {
+  using C = Cfg<D, NT>;
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = once_per_device(done, [] {
+    return cudaFuncSetAttribute(paged_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+  });
+  if (e != cudaSuccess) return e;
+  int sms = 0;
+  if ((e = sm_count(&sms)) != cudaSuccess) return e;
+  paged_kernel<D, NT><<<sms, C::kThreads, C::kBytes, s>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(sms, p.rows);
+  cfg.blockDim = dim3(32);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<D, NT>, p);
+}
+
+}  // namespace
+
+void paged_shape(int Lq, int G, int sms, int* grid, int* parts, int* rows) {
+  const int nt = Lq * G > 8 ? 2 : 1;
+  *grid = sms;
+  *parts = sms * (2 + (nt == 1 ? 16 : 8));
+  *rows = Lq * G < 8 * nt ? Lq * G : 8 * nt;
+}
+
+cudaError_t launch_paged(const PagedParams& p, int d, cudaStream_t s) {
+  if (p.n <= 0) return cudaSuccess;
+  if (p.Lq * p.G > 8) return d == 128 ? launch_t<128, 2>(p, s) : launch_t<64, 2>(p, s);
+  return d == 128 ? launch_t<128, 1>(p, s) : launch_t<64, 1>(p, s);
+}
+
+}  // namespace mf

@@ -28,7 +28,8 @@ EXPORTED = ("mf_version", "mf_last_error", "mf_supported", "mf_bsr_create", "mf_
             "mf_bsr_create_chunked", "mf_prefix_hashes", "mf_bm_create", "mf_bm_destroy",
             "mf_bm_insert", "mf_bm_match", "mf_bm_assemble", "mf_bm_stats",
             "mf_rope_frequencies", "mf_qk_norm_rope", "mf_attn_create_packed", "mf_attn_create_cache",
-            "mf_attn_destroy", "mf_attn_workspace", "mf_attn_packed", "mf_attn_cached", "mf_attn_status")
+            "mf_attn_destroy", "mf_attn_workspace", "mf_attn_packed", "mf_attn_cached", "mf_attn_status",
+            "mf_cache_append", "mf_cache_read", "mf_attn_paged_workspace", "mf_attn_paged")
 KERNELS = ("stats", "select", "scan", "pack", "union", "retrieve")
 
 
@@ -40,6 +41,14 @@ class MapFlowError(RuntimeError):
 
 ALLOC_FN = ctypes.CFUNCTYPE(ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p)
 FREE_FN = ctypes.CFUNCTYPE(None, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p)
+
+class CacheStruct(ctypes.Structure):
+    """mf_cache_t of mapflow.h."""
+    _fields_ = [("format", ctypes.c_int), ("page_size", ctypes.c_int), ("H", ctypes.c_int), ("d", ctypes.c_int),
+                ("n_pages", ctypes.c_int64), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("ld_k", ctypes.c_int64), ("ld_v", ctypes.c_int64), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
 
 _lib = None
 
@@ -106,6 +115,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mf_attn_packed.argtypes = [vp] + [vp, i64] * 4 + [vp, i32, f32, vp, i64, vp]
     lib.mf_attn_cached.argtypes = [vp, i32] + [vp, i64] * 3 + [vp] + [vp, i64] * 3 + [vp, i32, f32, vp, i64, vp]
     lib.mf_attn_status.argtypes = [vp, vp]
+    lib.mf_cache_append.argtypes = [vp] + [vp, i64] * 2 + [i32, vp, vp, vp, i64, i32, i32, vp, vp, i32, i32, f32, vp,
+                                                           i32, f32, vp]
+    lib.mf_cache_read.argtypes = [vp, i32, vp, vp, vp, i64, i32, i32, vp, i64, vp, i64, vp]
+    lib.mf_attn_paged_workspace.argtypes = [i32, i32, i32, i32, i64p]
+    lib.mf_attn_paged.argtypes = [vp, i32, i32, i32, vp, i64, vp, i64, i32, vp, vp, i64, vp, vp, f32, i32, i32, f32,
+                                  vp, i64, vp]
     for name in EXPORTED:
         getattr(lib, name)
     _lib = lib
@@ -823,6 +838,207 @@ class CacheAttention(_AttentionPlan):
             self.handle, m, q.data_ptr(), ld_q, k_cache.data_ptr(), ld_k, v_cache.data_ptr(), ld_v, lens.data_ptr(),
             p_kp, ld_kp, p_vp, ld_vp, o.data_ptr(), ld_o, p_lse, MF_DTYPE_BF16,
             self._scale if scale is None else scale, ws.data_ptr(), need, raw)
+        if rc:
+            _check(rc)
+        return o
+
+
+# ------------------------------------------------------------ paged cache --
+MF_CACHE_BF16, MF_CACHE_FP4 = 0, 1
+
+
+class PagedCache:
+    """A paged cache of one layer's keys and values over tensors of the caller
+    (see mf_cache_t in mapflow.h): PagedCache.fp4 for pages of 4 bits,
+    PagedCache.bf16 for bf16 rows.  Calls leave nothing behind but what they
+    write to these tensors; no gradient is recorded.
+
+    Tokens are named by `seq` and `at`, int32 [T] on the device: a token's row of
+    `table` (int32 [n_seqs, max_pages], page numbers) and its place in that
+    sequence; tokens with seq = -1 are left out."""
+
+    def __init__(self, fmt: int, page_size: int, H: int, d: int, n_pages: int, tensors, ld_k: int = 0, ld_v: int = 0):
+        lib = load_library()
+        self._append_call, self._read_call, self._attend_call = lib.mf_cache_append, lib.mf_cache_read, lib.mf_attn_paged
+        self.format, self.page_size, self.H, self.d, self.n_pages = fmt, page_size, H, d, n_pages
+        self._tensors = tensors  # kept: the calls read their memory
+        k, v, ks, vs = tensors
+        self.device, self._gpu = k.device, k.get_device()
+        self._struct = CacheStruct(fmt, _int("page_size", page_size), _int("H", H), _int("d", d), n_pages,
+                                   k.data_ptr(), _ptr(v), ld_k, ld_v, _ptr(ks), _ptr(vs))
+        self._c = ctypes.addressof(self._struct)
+        self._scale = d ** -0.5
+        self._ws_of: Dict[Tuple[int, int], int] = {}  # workspace bytes by Lq and H_q
+
+    @classmethod
+    def fp4(cls, pages, page_size: int, d: int, k_scale=None, v_scale=None) -> "PagedCache":
+        """pages: uint8 [n_pages, H, page_size / 16 * 18 * d] on a GPU, contiguous
+        (any contents until a token is appended); k_scale and v_scale: fp32 [H],
+        positive, a scale for each head's keys and values, or None (1)."""
+        import torch
+        page_size, d = _int("page_size", page_size), _int("d", d)
+        if d not in (64, 128) or page_size < 16 or page_size % 16:
+            raise MapFlowError(MF_ERR_ARG, f"page_size = {page_size} must be a multiple of 16, d = {d} 64 or 128")
+        if pages.dim() != 3:
+            raise MapFlowError(MF_ERR_ARG, "pages must be [n_pages, H, page_size / 16 * 18 * d]")
+        gpu = pages.get_device()
+        if gpu < 0:
+            raise MapFlowError(MF_ERR_ARG, f"a CUDA tensor is needed, not one on {pages.device}")
+        n, H = pages.shape[:2]
+        _vector("pages", pages, (n, H, page_size // 16 * 18 * d), torch.uint8, gpu)
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is not None:
+                _vector(name, t, (H,), torch.float32, gpu)
+        return cls(MF_CACHE_FP4, page_size, H, d, n, (pages, None, k_scale, v_scale))
+
+    @classmethod
+    def bf16(cls, k, v) -> "PagedCache":
+        """k and v: bf16 [n_pages, page_size, H, d] on a GPU, tokens equally
+        spaced.  With a page to a request these are CacheAttention's caches."""
+        import torch
+        if k.dim() != 4:
+            raise MapFlowError(MF_ERR_ARG, "k and v must be [n_pages, page_size, H, d]")
+        gpu = k.get_device()
+        if gpu < 0:
+            raise MapFlowError(MF_ERR_ARG, f"a CUDA tensor is needed, not one on {k.device}")
+        n, page_size, H, d = shape = k.shape
+        ld_k, ld_v = _rows("k", k, shape, torch.bfloat16, gpu), _rows("v", v, shape, torch.bfloat16, gpu)
+        return cls(MF_CACHE_BF16, page_size, H, d, n, (k, v, None, None), ld_k, ld_v)
+
+    def _table(self, table, rows=None) -> int:
+        """Checks a table; returns the numbers between two of its rows."""
+        import torch
+        if table.dtype is torch.int32 and table.get_device() == self._gpu and table.dim() == 2 and \
+                (rows is None or table.shape[0] == rows) and (table.shape[1] == 1 or table.stride(1) == 1):
+            return table.stride(0) if table.shape[0] > 1 else table.shape[1]
+        raise MapFlowError(MF_ERR_ARG, f"table must be an int32 tensor [{'n_seqs' if rows is None else rows}, max_pages] "
+                                       f"on cuda:{self._gpu} with a row's numbers next to each other")
+
+    def append(self, k, v, seq, at, table, rope: Optional["RotaryPlan"] = None, positions=None, k_weight=None,
+               eps: float = 1e-6, norm: Optional[bool] = None, stream=None) -> None:
+        """Puts k and v (bf16 [T, H, d]) of T tokens in their places, the keys
+        normed (when a weight is given or norm is True) and rotated by `rope` at
+        `positions` (int32 [T]; None: `at`) on the way (see mf_cache_append)."""
+        raw = None if stream is not None else _raw_current(self._gpu)
+        if raw is not None:
+            return self._append(raw, k, v, seq, at, table, rope, positions, k_weight, eps, norm)
+        guard, raw = _on(self.device, stream)
+        with guard:
+            return self._append(raw, k, v, seq, at, table, rope, positions, k_weight, eps, norm)
+
+    def _append(self, raw, k, v, seq, at, table, rope, positions, k_weight, eps, norm):
+        import torch
+        dt, gpu, i32 = torch.bfloat16, self._gpu, torch.int32
+        T = k.shape[0]
+        shape = (T, self.H, self.d)
+        ld_k = _rows("k", k, shape, dt, gpu)
+        ld_v = _rows("v", v, shape, dt, gpu)
+        _vector("seq", seq, (T,), i32, gpu)
+        _vector("at", at, (T,), i32, gpu)
+        ld_t = self._table(table)
+        p_pos = p_w = turns = None
+        rot, layout, gain = 0, 0, 1.0
+        if positions is not None:
+            _vector("positions", positions, (T,), i32, gpu)
+            p_pos = positions.data_ptr()
+        if rope is not None:
+            if rope._gpu != gpu:
+                raise MapFlowError(MF_ERR_ARG, f"the cache is on cuda:{gpu}, the rotary plan on {rope.turns.device}")
+            if raw != rope._home:
+                rope._abroad = True
+            turns, rot, layout, gain = rope._turns, rope.rot_dim, rope._layout, rope.gain
+        elif positions is not None:
+            raise MapFlowError(MF_ERR_ARG, "positions without a rotary plan")
+        if k_weight is not None:
+            _vector("k_weight", k_weight, (self.d,), dt, gpu)
+            p_w = k_weight.data_ptr()
+        if norm is None:
+            norm = p_w is not None
+        rc = self._append_call(
+            self._c, k.data_ptr(), ld_k, v.data_ptr(), ld_v, T, seq.data_ptr(), at.data_ptr(), table.data_ptr(), ld_t,
+            table.shape[0], table.shape[1], p_pos, turns, rot, layout, gain, p_w, norm, eps, raw)
+        if rc:
+            _check(rc)
+
+    def read(self, seq, at, table, k=None, v=None, stream=None):
+        """(k, v): bf16 [T, H, d] of T tokens, new tensors unless given; rows of
+        tokens that are left out keep what was there (see mf_cache_read)."""
+        raw = None if stream is not None else _raw_current(self._gpu)
+        if raw is not None:
+            return self._read(raw, seq, at, table, k, v)
+        guard, raw = _on(self.device, stream)
+        with guard:
+            return self._read(raw, seq, at, table, k, v)
+
+    def _read(self, raw, seq, at, table, k, v):
+        import torch
+        gpu = self._gpu
+        T = seq.shape[0]
+        _vector("seq", seq, (T,), torch.int32, gpu)
+        _vector("at", at, (T,), torch.int32, gpu)
+        ld_t = self._table(table)
+        shape, ld = (T, self.H, self.d), []
+        for name, t in (("k", k), ("v", v)):
+            ld.append(self.H * self.d if t is None else _rows(name, t, shape, torch.bfloat16, gpu))
+        if k is None:
+            k = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
+        if v is None:
+            v = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
+        rc = self._read_call(self._c, T, seq.data_ptr(), at.data_ptr(), table.data_ptr(), ld_t, table.shape[0],
+                             table.shape[1], k.data_ptr(), ld[0], v.data_ptr(), ld[1], raw)
+        if rc:
+            _check(rc)
+        return k, v
+
+    def attend(self, q, table, lens, window: Optional[int] = None, sinks: int = 0, softcap: Optional[float] = None,
+               slopes=None, scale: Optional[float] = None, o=None, lse=None, stream=None):
+        """Decoding attention over a 4-bit cache: q [n, Lq, H_q, d] of n requests,
+        table int32 [n, max_pages], lens int32 [n] on the device (keys of each
+        request, the new tokens' among them) -> o [n, Lq, H_q, d].  softcap: scores
+        are capped by a tanh; slopes: fp32 [H_q], a bias by distance; lse: fp32 [n,
+        Lq, H_q] to fill, or None (see mf_attn_paged)."""
+        raw = None if stream is not None else _raw_current(self._gpu)
+        if raw is not None:
+            return self._attend(raw, q, table, lens, window, sinks, softcap, slopes, scale, o, lse)
+        guard, raw = _on(self.device, stream)
+        with guard:
+            return self._attend(raw, q, table, lens, window, sinks, softcap, slopes, scale, o, lse)
+
+    def _attend(self, raw, q, table, lens, window, sinks, softcap, slopes, scale, o, lse):
+        import torch
+        dt, gpu = torch.bfloat16, self._gpu
+        if q.dim() != 4:
+            raise MapFlowError(MF_ERR_ARG, "q must be [n, Lq, H_q, d]")
+        shape = n, Lq, H_q, _ = (*q.shape[:3], self.d)
+        ld_q = _rows("q", q, shape, dt, gpu)
+        _vector("lens", lens, (n,), torch.int32, gpu)
+        ld_t = self._table(table, n)
+        window, sinks = 0 if window is None else _span("window", window, 1), _span("sinks", sinks, 0)
+        if softcap is None:
+            softcap = 0.0
+        elif not softcap > 0:
+            raise MapFlowError(MF_ERR_ARG, f"softcap = {softcap} must be positive (None: none)")
+        if o is None:
+            o, ld_o = _empty(q, shape), H_q * self.d
+        else:
+            ld_o = _rows("o", o, shape, dt, gpu)
+        p_lse = p_slopes = None
+        if lse is not None:
+            _vector("lse", lse, shape[:3], torch.float32, gpu)
+            p_lse = lse.data_ptr()
+        if slopes is not None:
+            _vector("slopes", slopes, (H_q,), torch.float32, gpu)
+            p_slopes = slopes.data_ptr()
+        need = self._ws_of.get((Lq, H_q))
+        if need is None:
+            bytes_ = ctypes.c_int64()
+            _check(load_library().mf_attn_paged_workspace(Lq, H_q, self.H, self.d, ctypes.byref(bytes_)))
+            need = self._ws_of[Lq, H_q] = bytes_.value
+        ws = torch.empty(need, dtype=torch.uint8, device=self.device)  # its own for every call: calls may overlap
+        rc = self._attend_call(
+            self._c, n, Lq, H_q, q.data_ptr(), ld_q, table.data_ptr(), ld_t, table.shape[1], lens.data_ptr(),
+            o.data_ptr(), ld_o, p_lse, p_slopes, softcap, window, sinks, self._scale if scale is None else scale,
+            ws.data_ptr(), need, raw)
         if rc:
             _check(rc)
         return o

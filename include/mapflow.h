@@ -623,6 +623,118 @@ MF_API int mf_attn_cached(mf_attn_t h, int n, const void* q, int64_t ld_q, const
 /* mf_attn_status — as mf_device_status, for a plan's calls. */
 MF_API int mf_attn_status(mf_attn_t h, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * A paged cache of keys and values
+ *
+ * [Article], the paragraph after "其三": the system runs with paged attention.
+ * Pages of page_size tokens of all heads of one layer lie in one piece of
+ * memory, n_pages of them; a sequence's tokens are on the pages that its row of
+ * `table` names (token `at` on page table[seq][at / page_size], at place
+ * at % page_size), in any order and shared between sequences where a caller
+ * wishes.  The caller owns the memory, the table and the lengths; nothing is
+ * kept between calls.  A number of the table is read only for tokens that a call
+ * names; a token with seq outside [0, n_seqs), `at` outside [0, max_pages *
+ * page_size) or a page outside [0, n_pages) is left out (unused places of a
+ * batch: seq = -1), and nothing is read or written for it.
+ *
+ * MF_CACHE_BF16: rows of heads, keys and values apart: token i of page p is row
+ *   p * page_size + i.  With page_size = capacity and table[r] = {r} these are
+ *   the caches of mf_attn_cached.
+ * MF_CACHE_FP4: 4 bits and a scale for 16 dimensions, 9/32 of the bytes.  Of 16
+ *   neighbouring dimensions of a token's head, with a scale g of the head,
+ *     s = e4m3(max |x| / (6 g))   to the nearest, ties to even, at most 448,
+ *     a value is held as the e2m1 number (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ *     negatives) nearest to x / (s g), ties to even, at most 6,
+ *   and stands for that number times s g.  Which number that is goes by the exact
+ *   value of x (fp64 decides where fp32 cannot).  A block with a value that is not
+ *   finite is held as NaN.  16 tokens of a head are 18 d bytes,
+ *     keys' codes    [16 tokens][d/2]             (even dimension in the low bits)
+ *     values' codes  [2][d/16][8 tokens][8]
+ *     keys' scales   [16 tokens][d/16]   values' scales [d/16][16 tokens]   (e4m3)
+ *   and a page is [H][page_size / 16] of these.
+ * ------------------------------------------------------------------------- */
+#define MF_CACHE_BF16 0
+#define MF_CACHE_FP4  1
+
+typedef struct {
+  int format;            /* MF_CACHE_BF16 or MF_CACHE_FP4                        */
+  int page_size;         /* tokens, >= 1; MF_CACHE_FP4: a multiple of 16         */
+  int H, d;              /* KV heads (1 .. 1024), dimensions (64 or 128)         */
+  int64_t n_pages;       /* 1 .. 2^31 - 1                                        */
+  void* k;               /* keys, or the 4-bit pages; 16-byte aligned            */
+  void* v;               /* values; NULL for MF_CACHE_FP4                        */
+  int64_t ld_k, ld_v;    /* MF_CACHE_BF16: values between tokens (16-byte multiples) */
+  const float* k_scale;  /* DEVICE fp32 [H], positive normal numbers, the heads' g;
+                            NULL: 1 (MF_CACHE_BF16: NULL)                        */
+  const float* v_scale;
+} mf_cache_t;
+
+/*
+ * mf_cache_append — T tokens' keys and values into the cache, on the way to which
+ * the keys get their norm and rotary embedding as by mf_qk_norm_rope (fp32, for
+ * 4 bits as said above; rounded once).
+ *   k, v         bf16 [T][H][d], ld_k_in / ld_v_in values between tokens
+ *   seq, at      int32 [T]: a token's sequence (row of table) and place there
+ *   table        int32 [n_seqs][max_pages], rows ld_table apart
+ *   positions    int32 [T] of the rotary embedding; NULL: `at`
+ *   turns, rot_dim, layout, gain   as for mf_qk_norm_rope; rot_dim 0: no rotary
+ *   k_weight, norm, eps            as for mf_qk_norm_rope
+ * Two tokens of one call at one place leave either's values there, or parts of
+ * both.  Shares no memory between cache and inputs.  max_pages * page_size is at
+ * most 2^26 (MF_ERR_UNSUPPORTED).  T = 0 is a no-op.
+ *
+ * mf_cache_read — T tokens' keys and values as bf16 rows (each rounded once: a
+ * code times its scale times the head's), e.g. for mf_attn_packed over a chunk and
+ * its cached prefix.  Rows of tokens that are left out are not written.
+ * Errors of both: MF_ERR_ARG, MF_ERR_UNSUPPORTED, MF_ERR_CUDA.
+ */
+MF_API int mf_cache_append(const mf_cache_t* cache, const void* k, int64_t ld_k_in, const void* v, int64_t ld_v_in,
+                           int T, const int32_t* seq, const int32_t* at, const int32_t* table, int64_t ld_table,
+                           int n_seqs, int max_pages, const int32_t* positions, const uint64_t* turns, int rot_dim,
+                           int layout, float gain, const void* k_weight, int norm, float eps, void* stream);
+MF_API int mf_cache_read(const mf_cache_t* cache, int T, const int32_t* seq, const int32_t* at,
+                         const int32_t* table, int64_t ld_table, int n_seqs, int max_pages, void* k_out,
+                         int64_t ld_k_out, void* v_out, int64_t ld_v_out, void* stream);
+
+/*
+ * mf_attn_paged — decoding attention of n requests with Lq new tokens each (their
+ * keys and values already in the cache) over a MF_CACHE_FP4 cache (others:
+ * MF_ERR_UNSUPPORTED).  New token t of request r is at position i = lens[r] - Lq +
+ * t and sees keys j <= i with i - j < window or j < n_sink, those on pages outside
+ * [0, n_pages) excepted.  Its scores are
+ *     s = scale * q.k;   softcap > 0: softcap * tanh(s / softcap);
+ *     slopes: less slopes[head] * (i - j)
+ * and o = softmax(s) v, lse the log of the softmax's denominator.  A row that sees
+ * no key gets o = 0 and lse = -inf.
+ *   q, o         bf16 [n * Lq][H_q][d], Lq * H_q / H <= 128, H_q <= 1024; o shares no
+ *                memory with an input
+ *   table        int32 [n][max_pages], ld_table apart; numbers past a request's
+ *                keys, or before its window, are not used
+ *   lens         DEVICE int32 [n], held to [0, max_pages * page_size <= 2^26]; read on
+ *                the device, so that a captured graph follows it (and the table)
+ *                from replay to replay
+ *   slopes       DEVICE fp32 [H_q] or NULL      softcap  0: none
+ *   window       >= 1, or 0: no window          n_sink   >= 0
+ *   lse          fp32 [n * Lq][H_q] or NULL
+ *   workspace    the caller's, 256-byte aligned, mf_attn_paged_workspace bytes; needs
+ *                no initialisation and holds nothing between calls; calls that may
+ *                overlap on the GPU need one each
+ * Scores, softmax statistics, sums and partial results are fp32; a key's and
+ * value's code times scale is exact; softmax weights are rounded to 11 bits for
+ * their product with v (2^-32 of the row's largest at most where they are small),
+ * not for the sum that it is divided by.  What is not finite in a key reaches the
+ * rows that see it; in a value the rows that see it, and may reach the other new
+ * tokens of that request (weight 0 times NaN is NaN).  Keys that no row of a
+ * request sees may hold anything.  A row of q that is not finite gives NaN.
+ * Asynchronous, without waits on the device and without state: results repeat bit
+ * for bit.  Errors: MF_ERR_ARG, MF_ERR_UNSUPPORTED, MF_ERR_CUDA.
+ */
+MF_API int mf_attn_paged_workspace(int Lq, int H_q, int H_kv, int d, int64_t* bytes);
+MF_API int mf_attn_paged(const mf_cache_t* cache, int n, int Lq, int H_q, const void* q, int64_t ld_q,
+                         const int32_t* table, int64_t ld_table, int max_pages, const int32_t* lens, void* o,
+                         int64_t ld_o, float* lse, const float* slopes, float softcap, int window, int n_sink,
+                         float scale, void* workspace, int64_t workspace_bytes, void* stream);
+
 /*
  * mf_selftest_wait — failure-detection self-test (no counterpart on the
  * pages).  Launches one thread that waits on a device barrier nothing will
