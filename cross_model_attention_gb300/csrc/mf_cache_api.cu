@@ -259,6 +259,7 @@ int mf_attn_paged(const mf_cache_t* cache, int n, int Lq, int H_q, const void* q
   p.ps = cache->page_size;
   p.H_kv = H;
   p.G = H_q / H;
+  p.inv_G = (65536 + p.G - 1) / p.G;
   p.table = table;
   p.ld_table = ld_table;
   p.max_pages = max_pages;

@@ -311,6 +311,7 @@ struct PagedParams {
   long long ld_q, ld_o;
   float* lse;                  // [n * Lq][H_q] or null
   int n, Lq, window, n_sink;
+  unsigned inv_G;              // rr * inv_G >> 16 = rr / G for rr < 128
   float scale, cap;            // cap 0: none
   // workspace: a CTA's two partial results and a warp's one
   float* part_o;               // [2 grid + warps][rows][d]

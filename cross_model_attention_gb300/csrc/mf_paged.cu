@@ -32,6 +32,7 @@
 // of a pair that warps of a CTA share are joined in shared memory, those that
 // CTAs share through the workspace, by a second kernel; both in a fixed order.
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 
@@ -61,26 +62,31 @@ struct Cfg {
   static constexpr int S = kRing / kStage;
   static constexpr int R = 8 * NT;
   static constexpr int kThreads = 32 * W;
-  static constexpr int kPrefix = kRingBytes;             // [threads + 1] long long
-  static constexpr int kDesc = kPrefix + 8 * (kThreads + 2);
-  static constexpr int kPieces = kDesc + 32 * W * S;
-  static constexpr int kBytes = kPieces + 16 * 2 * W;
+  static constexpr int kQueue = S < 4 ? 4 : 8;           // parts of a warp that the ring can hold, and one
+  static constexpr int kPrefix = kRingBytes;             // [threads + 2] long long
+  static constexpr int kLens = kPrefix + 8 * (kThreads + 2);  // [threads]
+  static constexpr int kParts = kLens + 4 * kThreads;
+  static constexpr int kPieces = kParts + 48 * W * kQueue;
+  static constexpr int kWalk = kPieces + 16 * 2 * W;
+  static constexpr int kBytes = kWalk + 48 * W;
   static_assert(kBytes <= 232448, "shared memory");
   static_assert(R * D * 4 + R * 8 <= kRing, "a partial result in a warp's ring");
-  static_assert(S >= 2 && 32 % NB == 0, "ring");
+  static_assert(S >= 2 && S < kQueue && 32 % NB == 0 && S * NB <= 32, "ring");
 };
 
-// A tile in the ring: what the consumer has to know of it.
-struct alignas(16) Desc {
-  int key0, flags, r, u;
-  int len, end, pad0, pad1;
+// A part of a warp's span: tiles i0 .. i1 of a unit.
+struct alignas(16) Part {
+  int r, u, len, i0, i1, flags, end, ta, tb, pad[3];
 };
-enum { kFirst = 1, kLast = 2, kBegins = 4, kEnds = 8, kMore = 16, kBadShift = 8 };
+enum { kBegins = 1, kEnds = 2, kHere = 4 };
+// Where a warp's walk over its span is: the unit whose line begins at `at`.
+struct alignas(16) Walk {
+  int r, u, at, f0, f1, len, ta, tb, nt, pad[3];
+};
 // A partial result of a warp.
 struct alignas(16) Piece {
   int r, u, flags, end;  // end: the last CTA with tiles of the unit
 };
-enum { kHere = 1 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -90,36 +96,10 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
 // D (16 x 8, fp32) += A (16 x 16) B (16 x 8), fp16.
 __device__ __forceinline__ void mma(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -200,493 +180,545 @@ __device__ __forceinline__ void store_row(const PagedParams& p, int r, int u, in
 template <int D, int NT>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const PagedParams p) {
   using C = Cfg<D, NT>;
-  constexpr int W = C::W, NB = C::NB, TK = C::TK, S = C::S;
+  constexpr int W = C::W, NB = C::NB, TK = C::TK, S = C::S, T = C::kThreads;
   extern __shared__ __align__(16) uint8_t smem[];
-  const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int units = p.H_kv * ((p.Lq * p.G + C::R - 1) / C::R);
   long long* prefix = reinterpret_cast<long long*>(smem + C::kPrefix);
-  Desc* desc = reinterpret_cast<Desc*>(smem + C::kDesc) + warp * S;
+  int* lens_s = reinterpret_cast<int*>(smem + C::kLens);
+  Part* parts = reinterpret_cast<Part*>(smem + C::kParts) + warp * C::kQueue;
   Piece* pieces = reinterpret_cast<Piece*>(smem + C::kPieces);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up
 
   // ---- the lines: a thread sums those of consecutive requests
-  const int share = (p.n + C::kThreads - 1) / C::kThreads;
-  long long sum = 0;
-  for (int r = threadIdx.x * share; r < min(p.n, (static_cast<int>(threadIdx.x) + 1) * share); ++r)
-    sum += line_of(tiles_of<TK>(p, p.lens[r]), units);
+  const int share = (p.n + T - 1) / T;
+  const int groups = (p.Lq * p.G + C::R - 1) / C::R, units = p.H_kv * groups;
   {
+    long long sum = 0;
+    for (int j = 0; j < share; ++j) {
+      const int r = threadIdx.x * share + j;
+      if (r >= p.n) break;
+      const int len = p.lens[r];
+      if (share == 1) lens_s[r] = len;
+      sum += line_of(tiles_of<TK>(p, len), units);
+    }
     long long inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(kFull, inc, o);
       if (lane >= o) inc += y;
     }
-    // (the warps' sums first, in the rows' place)
+    // (the warps' sums first, in the threads' place)
     if (lane == 31) prefix[warp] = inc;
     __syncthreads();
-    long long before = 0;
-    for (int w = 0; w < warp; ++w) before += prefix[w];
+    long long before = lane < warp ? prefix[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) before += __shfl_xor_sync(kFull, before, o);
     __syncthreads();
     prefix[threadIdx.x + 1] = before + inc;
     if (threadIdx.x == 0) prefix[0] = 0;
+    if (lane < 2) pieces[2 * warp + lane].flags = 0;
+    __syncthreads();
   }
-  if (lane < 2) pieces[2 * warp + lane].flags = 0;
-  __syncthreads();
-  const long long total = prefix[C::kThreads];
-  const long long per = max(static_cast<long long>(kMinSpan), (total + gridDim.x - 1) / gridDim.x);
-  const long long cta0 = min(total, per * blockIdx.x), cta1 = min(total, cta0 + per);
-  const long long f0 = cta0 + (cta1 - cta0) * warp / W, f1 = cta0 + (cta1 - cta0) * (warp + 1) / W;
-
-  // ---- requests without keys
-  for (int r = blockIdx.x + gridDim.x * warp; r < p.n; r += gridDim.x * W) {
-    if (tiles_of<TK>(p, p.lens[r]).nt > 0) continue;
-    const int H = p.H_kv * p.G;
-    for (int i = lane; i < p.Lq * H * (D / 8); i += 32) {
-      const int tt = i / (H * (D / 8)), x = i - tt * (H * (D / 8));
-      reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + (static_cast<long long>(r) * p.Lq + tt) * p.ld_o)[x] =
-          make_uint4(0u, 0u, 0u, 0u);
-    }
-    if (p.lse)
-      for (int i = lane; i < p.Lq * H; i += 32) p.lse[static_cast<long long>(r) * p.Lq * H + i] = -INFINITY;
-  }
+  auto len_of = [&](int r) { return share == 1 ? lens_s[r] : p.lens[r]; };
+  const long long total = prefix[T];
+  const int per = static_cast<int>(max(static_cast<long long>(kMinSpan), (total + gridDim.x - 1) / gridDim.x));
+  // this CTA's span, from here on in places from its start, and this warp's
+  const long long cta0 = min(total, static_cast<long long>(per) * blockIdx.x);
+  const int cta1 = static_cast<int>(min(total - cta0, static_cast<long long>(per)));
+  const int f0 = static_cast<int>(static_cast<long long>(cta1) * warp / W);
+  const int f1 = static_cast<int>(static_cast<long long>(cta1) * (warp + 1) / W);
 
   // ---- the walk over this warp's span
-  int wr = p.n, wu = 0;       // request and unit of the line at `at`
-  long long at = total;
+  int wr = p.n, wu = 0, at = 0;  // request and unit of the line that begins at `at`
   Tiles wt{0, 0, 0, 0};
   if (f0 < f1) {
     // the thread whose requests' lines f0 lies in, then the request
-    int j = 0;
-    {
-      constexpr int kStep = C::kThreads / 32;
-      const unsigned c = __ballot_sync(kFull, prefix[lane * kStep] <= f0);
-      const int hi = 31 - __clz(c);
-      const unsigned f = __ballot_sync(kFull, lane < kStep && prefix[hi * kStep + (lane & (kStep - 1))] <= f0);
-      j = hi * kStep + 31 - __clz(f);
-    }
-    at = prefix[j];
-    for (int r0 = j * share; r0 < p.n; r0 += 32) {
-      const int r = r0 + lane;
-      const Tiles x = tiles_of<TK>(p, r < p.n ? p.lens[r] : 0);
-      const long long mine = line_of(x, units);
-      long long inc = mine;
+    constexpr int kStep = T / 32;
+    const long long f = cta0 + f0;
+    const int hi = 31 - __clz(__ballot_sync(kFull, prefix[lane * kStep] <= f));
+    const int j = hi * kStep + 31 - __clz(__ballot_sync(kFull, lane < kStep && prefix[hi * kStep + (lane & (kStep - 1))] <= f));
+    long long line = prefix[j];
+    wr = j;
+    if (share > 1) {
+      wr = p.n;
+      for (int r0 = j * share; r0 < p.n; r0 += 32) {
+        const int r = r0 + lane;
+        const long long mine = line_of(tiles_of<TK>(p, r < p.n ? p.lens[r] : 0), units);
+        long long inc = mine;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(kFull, inc, o);
-        if (lane >= o) inc += y;
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(kFull, inc, o);
+          if (lane >= o) inc += y;
+        }
+        const unsigned hit = __ballot_sync(kFull, line + inc > f);
+        if (hit) {
+          const int k = __ffs(hit) - 1;
+          wr = r0 + k;
+          line += __shfl_sync(kFull, inc - mine, k);
+          break;
+        }
+        line += __shfl_sync(kFull, inc, 31);
       }
-      const unsigned hit = __ballot_sync(kFull, at + inc > f0);
-      if (hit) {
-        const int k = __ffs(hit) - 1;
-        wr = r0 + k;
-        at += __shfl_sync(kFull, inc - mine, k);
-        break;
-      }
-      at += __shfl_sync(kFull, inc, 31);
     }
     if (wr < p.n) {
-      wt = tiles_of<TK>(p, p.lens[wr]);
-      wu = static_cast<int>((f0 - at) / (kCost + wt.nt));
-      at += static_cast<long long>(wu) * (kCost + wt.nt);
+      wt = tiles_of<TK>(p, len_of(wr));
+      // (a request's lines may be 2^31 and more long, a unit's are not)
+      const long long in = f - line;
+      wu = in < 0x7fffffff ? static_cast<int>(in) / (kCost + wt.nt) : static_cast<int>(in / (kCost + wt.nt));
+      at = static_cast<int>(line + static_cast<long long>(wu) * (kCost + wt.nt) - cta0);
     }
   }
-  // the piece at hand: tiles i .. i1 of unit pu of request pr
-  int pr = 0, pu = 0, i = 0, i1 = 0, pstart = 0;
-  bool pbegins = false, pends = false;
-  Tiles pt{0, 0, 0, 0};
-  auto next_piece = [&]() {
-    while (at < f1 && wr < p.n) {
-      if (wu == units) {  // to the next request with keys
-        wu = 0;
-        int r0 = wr + 1;
-        wr = p.n;
+  Walk* walk = reinterpret_cast<Walk*>(smem + C::kWalk) + warp;
+  if (lane == 0) *walk = Walk{wr, wu, at, f0, f1, wt.len, wt.ta, wt.tb, wt.nt, {0, 0, 0}};
+  __syncwarp();
+  // The producer's part: tiles i .. i1 of it are to be asked for.  The next one,
+  // onto the queue; false after the last.
+  int i = 0, i1 = 0, pushed = 0, popped = 0;
+  auto next_part = [&]() {
+    Walk x = *walk;
+    bool some = false;
+    while (!some && x.at < x.f1 && x.r < p.n) {
+      if (x.u == units) {  // to the next request with keys
+        x.u = 0;
+        int r0 = x.r + 1;
+        x.r = p.n;
         for (; r0 < p.n; r0 += 32) {
           const int r = r0 + lane;
-          const unsigned some = __ballot_sync(kFull, r < p.n && tiles_of<TK>(p, p.lens[min(r, p.n - 1)]).nt > 0);
-          if (some) {
-            wr = r0 + __ffs(some) - 1;
+          const unsigned full = __ballot_sync(kFull, r < p.n && tiles_of<TK>(p, len_of(min(r, p.n - 1))).nt > 0);
+          if (full) {
+            x.r = r0 + __ffs(full) - 1;
             break;
           }
         }
-        if (wr >= p.n) return false;
-        wt = tiles_of<TK>(p, p.lens[wr]);
+        if (x.r >= p.n) break;
+        const Tiles y = tiles_of<TK>(p, len_of(x.r));
+        x.len = y.len, x.ta = y.ta, x.tb = y.tb, x.nt = y.nt;
       }
-      const long long b = at + kCost;
-      const int lo = static_cast<int>(max(0ll, f0 - b)), hi = static_cast<int>(min(static_cast<long long>(wt.nt), f1 - b));
-      pr = wr;
-      pu = wu;
-      at += kCost + wt.nt;
-      ++wu;
+      const int b = x.at + kCost;
+      const int lo = max(0, x.f0 - b), hi = min(x.nt, x.f1 - b);
+      x.at = b + x.nt;
+      const int u = x.u++;
       if (lo < hi) {
-        i = pstart = lo;
+        some = true;
+        i = lo;
         i1 = hi;
-        pbegins = lo == 0;
-        pends = hi == wt.nt;
-        pt = wt;
-        return true;
+        // (its tiles past this CTA's span are the next CTAs')
+        const int end = hi == x.nt ? 0 : static_cast<int>(blockIdx.x + (static_cast<unsigned>(x.at - cta1) + per - 1) / static_cast<unsigned>(per));
+        if (lane == 0)
+          parts[pushed & (C::kQueue - 1)] = Part{x.r, u, x.len, lo, hi, (lo == 0 ? kBegins : 0) | (hi == x.nt ? kEnds : 0), end, x.ta, x.tb, {0, 0, 0}};
+        ++pushed;
       }
     }
-    return false;
+    __syncwarp();
+    if (lane == 0) *walk = x;
+    __syncwarp();
+    return some;
   };
-  bool have = next_piece();
+
+  // Row rr of a unit's head: its token and its head within the group.
+  auto split = [&](int rr, int& tt, int& gg) {
+    tt = static_cast<int>(static_cast<unsigned>(rr) * p.inv_G >> 16);
+    gg = rr - tt * p.G;
+    return rr < p.Lq * p.G;
+  };
+  auto head_of = [&](int u, int& rg) {  // (and its group of rows)
+    rg = groups == 1 ? 0 : u / p.H_kv;
+    return u - rg * p.H_kv;
+  };
+
+  // ---- q of a part: loads, then fp16
+  uint4 qw[NT][D / 32];
+  float kscale = 1.f;
+  auto load_q = [&](int r, int u) {
+    int rg;
+    const int h = head_of(u, rg);
+    if (p.k_scale) kscale = p.k_scale[h];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      int tt, gg;
+      const bool ok = split(rg * C::R + nt * 8 + g, tt, gg);
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (static_cast<long long>(r) * p.Lq + tt) * p.ld_q +
+                                 (h * p.G + gg) * D + t * (D / 4);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        qw[nt][c] = make_uint4(0u, 0u, 0u, 0u);
+        if (ok) qw[nt][c] = reinterpret_cast<const uint4*>(src)[c];
+      }
+    }
+  };
+
+  bool have = next_part();
+  if (have) load_q(parts[0].r, parts[0].u);  // (before the first tiles: what is asked for first comes first)
+
   int fill = 0;            // the ring's next slot
-  long long offs = 0;      // lane's block of the next 32: its bytes' place, or -1
+  unsigned bad = 0;        // of the ring's blocks: those on no page, NB bits to a slot
+  long long offs = 0;      // of the lane's block of 32: its bytes' place, or -1
+  int at_block = 32;       // the next of them
   const long long hstride = static_cast<long long>(p.ps / kFp4Block) * C::kPiece;
-  const uint32_t ring = sb + warp * C::kRing;
+  const uint32_t ring = smem_u32(smem) + warp * C::kRing;
   auto issue = [&]() {
     if (have) {
-      const int k = (i - pstart) * NB;
-      if ((k & 31) == 0) {
+      if (at_block == 32) {
+        at_block = 0;
+        const Part& x = parts[(pushed - 1) & (C::kQueue - 1)];
         const int ii = i + lane / NB, b = lane % NB;
-        const int tile = ii < pt.ta ? ii : pt.tb + ii - pt.ta;
+        const int tile = ii < x.ta ? ii : x.tb + ii - x.ta;
         const int key = (tile * NB + b) * kFp4Block;
         offs = -1;
-        if (ii < i1 && key < pt.len) {
+        if (ii < i1 && key < x.len) {
           const int page = key / p.ps;
-          const int id = p.table[pr * p.ld_table + page];
+          const int id = p.table[x.r * p.ld_table + page];
+          int rg;
+          const int h = head_of(x.u, rg);
           if (id >= 0 && id < p.n_pages)
-            offs = (static_cast<long long>(id) * p.H_kv + pu % p.H_kv) * hstride + (key - page * p.ps) / kFp4Block * C::kPiece;
+            offs = (static_cast<long long>(id) * p.H_kv + h) * hstride + (key - page * p.ps) / kFp4Block * C::kPiece;
         }
       }
-      const uint32_t dst = ring + fill * C::kStage;
-      int bad = 0;
+      const uint32_t dst = ring + fill * C::kStage + lane * 16;
+      unsigned miss = 0;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const long long off = __shfl_sync(kFull, offs, (k + b) & 31);
+        const long long off = __shfl_sync(kFull, offs, at_block + b);
         if (off < 0) {
-          bad |= 1 << b;
+          miss |= 1u << b;
         } else {
+          const uint8_t* src = p.pages + off + lane * 16;
 #pragma unroll
           for (int c = 0; c < C::kPiece / 16; c += 32)
-            if (c + lane < C::kPiece / 16) cp16(dst + b * C::kPiece + (c + lane) * 16, p.pages + off + (c + lane) * 16);
+            if (c + 32 <= C::kPiece / 16 || lane < C::kPiece / 16 - c) cp16(dst + b * C::kPiece + c * 16, src + c * 16);
         }
       }
-      Desc d;
-      d.key0 = (i < pt.ta ? i : pt.tb + i - pt.ta) * TK;
-      d.r = pr;
-      d.u = pu;
-      d.len = pt.len;
-      d.flags = (i == pstart ? kFirst : 0) | (pbegins ? kBegins : 0) | (pends ? kEnds : 0) | bad << kBadShift;
-      d.end = 0;
+      bad = (bad & ~(((1u << NB) - 1u) << (fill * NB))) | miss << (fill * NB);
+      at_block += NB;
       if (++i == i1) {
-        d.flags |= kLast;
-        d.end = static_cast<int>((at - 1) / per);
-        have = next_piece();
-        if (have) d.flags |= kMore;
+        have = next_part();
+        at_block = 32;
       }
-      if (lane == 0) desc[fill] = d;
       if (++fill == S) fill = 0;
     }
     cp_commit();
   };
-
-  // ---- tiles
-  uint32_t qf[NT][D / 16][2];
-  float acc[D / 16][NT][4], m[NT][2], l[NT][2], coef[NT][2], slope[NT][2];
-  int prow[NT][2];
 #pragma unroll 1
   for (int s = 0; s < S - 1; ++s) issue();
-  int slot = 0;
-  bool any = f0 < f1;
-  for (; any;) {
-    // (a warp without tiles has an empty ring: its first descriptor says so)
-    cp_wait<S - 2>();
-    __syncwarp();
-    const bool left = fill != slot;
-    if (!left) break;
-    const Desc d = desc[slot];
-    const uint32_t st = ring + slot * C::kStage;
-    issue();
-    if (d.flags & kFirst) {
-      const int h = d.u % p.H_kv;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        Row x;
-        const bool ok = row_of(p, d.r, d.u, nt * 8 + g, C::R, x);
-        uint4 w[D / 32];
-        uint32_t top = 0;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          w[c] = make_uint4(0u, 0u, 0u, 0u);
-          if (ok) w[c] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + x.tok * p.ld_q + x.head * D + t * (D / 4) + c * 8);
-          const uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = max(top, max(v[e] & 0x7fffu, (v[e] >> 16) & 0x7fffu));
-        }
-        top = max(top, __shfl_xor_sync(kFull, top, 1));
-        top = max(top, __shfl_xor_sync(kFull, top, 2));
-        // 2^e brings the row's largest to [2^14, 2^15)
-        const int ex = static_cast<int>(top >> 7);
-        const bool fine = ex < 255;
-        const int e = top == 0 || !fine ? 0 : min(120, 141 - ex);
-        const float up = __int_as_float((e + 127) << 23);
-        float c = p.scale * (p.k_scale ? p.k_scale[h] : 1.f) * __int_as_float((127 - e) << 23);
-        c *= p.cap > 0.f ? 1.f / p.cap : kLog2e;
-        if (!fine) c = NAN;
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          const uint32_t v[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) qf[nt][2 * k + (j >> 1)][j & 1] = pack_f16x2(bf16lo(v[j]) * up, bf16hi(v[j]) * up);
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          coef[nt][j] = __shfl_sync(kFull, c, (2 * t + j) * 4);
-          Row y;
-          const bool is = row_of(p, d.r, d.u, nt * 8 + 2 * t + j, C::R, y);
-          prow[nt][j] = is ? d.len - p.Lq + y.t : -1;
-          slope[nt][j] = is && p.slopes ? p.slopes[y.head] * kLog2e : 0.f;
-          m[nt][j] = -INFINITY;
-          l[nt][j] = 0.f;
-        }
-      }
-#pragma unroll
-      for (int a = 0; a < D / 16; ++a)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[a][nt][e] = 0.f;
-    }
 
-    // S = K q^T: rows are keys, columns the unit's rows
-    float x[NB][NT][4];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[b][nt][e] = 0.f;
-      const uint32_t base = st + b * C::kPiece;
-      uint32_t k0[D / 32], k1[D / 32];  // a lane's codes of keys g and g + 8
-      uint32_t s0, s1;                  // their scales, one or two
-      if (D == 128) {
-        const uint4 a = lds128(base + g * 64 + t * 16), c = lds128(base + (g + 8) * 64 + t * 16);
-        k0[0] = a.x, k0[1] = a.y, k0[D / 32 - 2] = a.z, k0[D / 32 - 1] = a.w;
-        k1[0] = c.x, k1[1] = c.y, k1[D / 32 - 2] = c.z, k1[D / 32 - 1] = c.w;
-        s0 = e4m3x2_f16x2(lds16(base + 16 * D + g * 8 + t * 2));
-        s1 = e4m3x2_f16x2(lds16(base + 16 * D + (g + 8) * 8 + t * 2));
-      } else {
-        const uint2 a = lds64(base + g * 32 + t * 8), c = lds64(base + (g + 8) * 32 + t * 8);
-        k0[0] = a.x, k0[1] = a.y;
-        k1[0] = c.x, k1[1] = c.y;
-        s0 = e4m3x2_f16x2(lds8(base + 16 * D + g * 4 + t));
-        s1 = e4m3x2_f16x2(lds8(base + 16 * D + (g + 8) * 4 + t));
-      }
-#pragma unroll
-      for (int w = 0; w < D / 32; ++w) {
-        const bool second = D == 128 && w >= 2;  // of the lane's two blocks of 16
-        const uint32_t f0_ = __byte_perm(s0, 0, second ? 0x3232 : 0x1010);
-        const uint32_t f1_ = __byte_perm(s1, 0, second ? 0x3232 : 0x1010);
-        const uint32_t a0 = mul_f16x2(e2m1x2_f16x2<0>(k0[w]), f0_), a1 = mul_f16x2(e2m1x2_f16x2<0>(k1[w]), f1_);
-        const uint32_t a2 = mul_f16x2(e2m1x2_f16x2<1>(k0[w]), f0_), a3 = mul_f16x2(e2m1x2_f16x2<1>(k1[w]), f1_);
-        const uint32_t c0 = mul_f16x2(e2m1x2_f16x2<2>(k0[w]), f0_), c1 = mul_f16x2(e2m1x2_f16x2<2>(k1[w]), f1_);
-        const uint32_t c2 = mul_f16x2(e2m1x2_f16x2<3>(k0[w]), f0_), c3 = mul_f16x2(e2m1x2_f16x2<3>(k1[w]), f1_);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma(x[b][nt], a0, a1, a2, a3, qf[nt][2 * w][0], qf[nt][2 * w][1]);
-          mma(x[b][nt], c0, c1, c2, c3, qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
-        }
-      }
+  // ---- requests without keys
+  for (int r = blockIdx.x + gridDim.x * warp; r < p.n; r += gridDim.x * W) {
+    if (tiles_of<TK>(p, len_of(r)).nt > 0) continue;
+    const int H = p.H_kv * p.G;
+#pragma unroll 1
+    for (int x = lane; x < p.Lq * H * (D / 8); x += 32) {
+      const int tt = x / (H * (D / 8)), y = x - tt * (H * (D / 8));
+      reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + (static_cast<long long>(r) * p.Lq + tt) * p.ld_o)[y] =
+          make_uint4(0u, 0u, 0u, 0u);
     }
-
-    // scores, in base 2
-    const bool whole = d.key0 + TK - 1 <= d.len - p.Lq && (d.flags >> kBadShift) == 0 &&
-                       (d.len - 1 - d.key0 < p.window || d.key0 + TK <= p.n_sink);
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[b][nt][e] *= coef[nt][e & 1];
-    if (p.cap > 0.f) {
-      const float c2 = p.cap * kLog2e;
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[b][nt][e] = c2 * tanhf(x[b][nt][e]);
-    }
-    if (p.slopes) {
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            x[b][nt][e] += slope[nt][e & 1] * static_cast<float>(d.key0 + 16 * b + g + (e & 2) * 4 - prow[nt][e & 1]);
-    }
-    if (!whole) {
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = d.key0 + 16 * b + g + (e & 2) * 4, far = prow[nt][e & 1] - j;
-            const bool seen = far >= 0 && (far < p.window || j < p.n_sink) && !(d.flags >> (kBadShift + b) & 1);
-            if (!seen) x[b][nt][e] = -INFINITY;
-          }
-    }
-
-    // the rows' references
-    {
-      float mx[NT][2];
-      bool up = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          mx[nt][j] = -INFINITY;
-#pragma unroll
-          for (int b = 0; b < NB; ++b) mx[nt][j] = fmaxf(mx[nt][j], fmaxf(x[b][nt][j], x[b][nt][2 + j]));
-          up |= mx[nt][j] > m[nt][j] + 8.f;
-        }
-      if (__any_sync(kFull, up)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float y = mx[nt][j];
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(kFull, y, o));
-            const float old = m[nt][j];
-            const bool move = y > old + 8.f;
-            const float f = !move ? 1.f : old == -INFINITY ? 0.f : ex2(old - y);
-            if (move) m[nt][j] = y;
-            l[nt][j] *= f;
-#pragma unroll
-            for (int a = 0; a < D / 16; ++a) {
-              acc[a][nt][j] *= f;
-              acc[a][nt][2 + j] *= f;
-            }
-          }
-      }
-    }
-    // weights, and as the B operand: keys by rows
-    uint32_t pf[NB][NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float lift[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) lift[j] = kLift - (m[nt][j] == -INFINITY ? 0.f : m[nt][j]);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        float w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = ex2(x[b][nt][e] + lift[e & 1]);
-        l[nt][0] += w[0] + w[2];
-        l[nt][1] += w[1] + w[3];
-        pf[b][nt][0] = transpose8x8(pack_f16x2(w[0], w[1]));
-        pf[b][nt][1] = transpose8x8(pack_f16x2(w[2], w[3]));
-      }
-    }
-
-    // O^T += V^T P^T: rows are dimensions
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const uint32_t base = st + b * C::kPiece;
-      constexpr int NW = D / 64;  // words (8 dimensions) of a lane
-      uint32_t va[2][NW], vb[2][NW], sc[2];  // keys 2t and 2t + 1 of each half
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        if (D == 128) {
-          const uint4 v = lds128(base + 8 * D + hf * 512 + g * 64 + t * 16);
-          va[hf][0] = v.x, va[hf][NW - 1] = v.y;
-          vb[hf][0] = v.z, vb[hf][NW - 1] = v.w;
-          sc[hf] = e4m3x2_f16x2(lds16(base + 17 * D + g * 16 + hf * 8 + t * 2));
-        } else {
-          const uint32_t at_ = base + 8 * D + hf * 256 + (g >> 1) * 64 + t * 16 + (g & 1) * 4;
-          va[hf][0] = lds32(at_);
-          vb[hf][0] = lds32(at_ + 8);
-          sc[hf] = e4m3x2_f16x2(lds16(base + 17 * D + (g >> 1) * 16 + hf * 8 + t * 2));
-        }
-        if (!whole) {  // what no row sees may be anything
-          const int b0 = d.len - p.Lq - p.window + 1;
-          uint32_t keep = 0;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int key = d.key0 + 16 * b + 8 * hf + 2 * t + j;
-            const bool dead = key >= d.len || (key < b0 && key >= p.n_sink) || (d.flags >> (kBadShift + b) & 1);
-            keep |= dead ? 0u : 0xffffu << (16 * j);
-          }
-          sc[hf] &= keep;
-        }
-      }
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        // codes of both keys to each dimension: even ones and odd ones
-        uint32_t ev[2], od[2];
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          ev[hf] = select(0x0f0f0f0fu, va[hf][w], vb[hf][w] << 4);
-          od[hf] = select(0x0f0f0f0fu, va[hf][w] >> 4, vb[hf][w]);
-        }
-        auto four = [&](auto I) {
-          constexpr int kI = decltype(I)::value;
-          const uint32_t a0 = mul_f16x2(e2m1x2_f16x2<kI>(ev[0]), sc[0]), a1 = mul_f16x2(e2m1x2_f16x2<kI>(od[0]), sc[0]);
-          const uint32_t a2 = mul_f16x2(e2m1x2_f16x2<kI>(ev[1]), sc[1]), a3 = mul_f16x2(e2m1x2_f16x2<kI>(od[1]), sc[1]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma(acc[4 * w + kI][nt], a0, a1, a2, a3, pf[b][nt][0], pf[b][nt][1]);
-        };
-        four(std::integral_constant<int, 0>());
-        four(std::integral_constant<int, 1>());
-        four(std::integral_constant<int, 2>());
-        four(std::integral_constant<int, 3>());
-      }
-    }
-
-    if (d.flags & kLast) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) l[nt][j] += __shfl_xor_sync(kFull, l[nt][j], o);
-      const bool done = (d.flags & (kBegins | kEnds)) == (kBegins | kEnds);
-      const bool more = d.flags & kMore;
-      // a whole unit's rows, or a partial result: in the ring, which is empty
-      // then, or in the workspace where the warp goes on
-      const long long spot = 2ll * gridDim.x + static_cast<long long>(blockIdx.x) * W + warp;
-      float* po = more ? p.part_o + spot * p.rows * D : reinterpret_cast<float*>(smem + warp * C::kRing);
-      float2* pm = more ? p.part_ml + spot * p.rows : reinterpret_cast<float2*>(smem + warp * C::kRing + C::R * D * 4);
-      __syncwarp();
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int row = nt * 8 + 2 * t + j;
-          Row y;
-          if (!row_of(p, d.r, d.u, row, C::R, y)) continue;
-          const float L = l[nt][j];
-          if (done) {
-            const float inv = inv_of(p, y.head / p.G, L);
-            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + y.tok * p.ld_o + y.head * D + g * (D / 8);
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = L == 0.f ? 0u : pack_bf16x2(acc[4 * c + e][nt][j] * inv, acc[4 * c + e][nt][2 + j] * inv);
-              reinterpret_cast<uint4*>(o)[c] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            if (p.lse && g == 0) p.lse[y.tok * (p.H_kv * p.G) + y.head] = lse_of(m[nt][j], L);
-          } else {
-            float* to = po + row * D + g * (D / 8);
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c)
-              reinterpret_cast<float4*>(to)[c] = make_float4(acc[2 * c][nt][j], acc[2 * c][nt][2 + j],
-                                                             acc[2 * c + 1][nt][j], acc[2 * c + 1][nt][2 + j]);
-            if (g == 0) pm[row] = make_float2(m[nt][j], L);
-          }
-        }
-      if (!done && lane == 0) pieces[2 * warp + (more ? 0 : 1)] = Piece{d.r, d.u, kHere | (d.flags & (kBegins | kEnds)), d.end};
-    }
-    if (++slot == S) slot = 0;
+    if (p.lse)
+#pragma unroll 1
+      for (int x = lane; x < p.Lq * H; x += 32) p.lse[static_cast<long long>(r) * p.Lq * H + x] = -INFINITY;
   }
 
-  // ---- the CTA's pieces: those of one unit follow each other
+  // ---- parts and their tiles
+  int slot = 0;
+  bool q_here = true;
+  __syncwarp();
+#pragma unroll 1
+  while (popped != pushed) {
+    // (its place in the queue is not used again before it is done)
+    const Part& d = parts[popped & (C::kQueue - 1)];
+    ++popped;
+    if (!q_here) load_q(d.r, d.u);
+    q_here = false;
+    uint32_t qf[NT][D / 16][2];
+    float acc[D / 16][NT][4], m[NT][2], l[NT][2], coef[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        const uint32_t v[4] = {qw[nt][c].x, qw[nt][c].y, qw[nt][c].z, qw[nt][c].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, max(v[e] & 0x7fffu, v[e] >> 16 & 0x7fffu));
+      }
+      top = max(top, __shfl_xor_sync(kFull, top, 1));
+      top = max(top, __shfl_xor_sync(kFull, top, 2));
+      // 2^e brings the row's largest to [2^14, 2^15)
+      const int ex = static_cast<int>(top >> 7);
+      const bool fine = ex < 255;
+      const int e = top == 0 || !fine ? 0 : min(120, 141 - ex);
+      const float up = __int_as_float((e + 127) << 23);
+      float c = p.scale * kscale * __int_as_float((127 - e) << 23);
+      c *= p.cap > 0.f ? 1.f / p.cap : kLog2e;
+      if (!fine) c = NAN;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        const uint32_t v[4] = {qw[nt][k].x, qw[nt][k].y, qw[nt][k].z, qw[nt][k].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) qf[nt][2 * k + (j >> 1)][j & 1] = pack_f16x2(bf16lo(v[j]) * up, bf16hi(v[j]) * up);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        coef[nt][j] = __shfl_sync(kFull, c, (2 * t + j) * 4);
+        m[nt][j] = -INFINITY;
+        l[nt][j] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < D / 16; ++a)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[a][nt][e] = 0.f;
+
+    const int len = d.len, last_tile = d.i1, ta = d.ta, skip = d.tb - d.ta;
+#pragma unroll 1
+    for (int ci = d.i0; ci < last_tile; ++ci) {
+      cp_wait<S - 2>();
+      __syncwarp();
+      issue();
+      const uint8_t* st = smem + warp * C::kRing + slot * C::kStage;
+      const unsigned gone = bad >> (slot * NB) & ((1u << NB) - 1u);
+      if (++slot == S) slot = 0;
+      const int key0 = (ci < ta ? ci : ci + skip) * TK;
+
+      // S = K q^T: rows are keys, columns the unit's rows
+      float x[NB][NT][4];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[b][nt][e] = 0.f;
+        const uint8_t* base = st + b * C::kPiece;
+        uint32_t k0[D / 32], k1[D / 32];  // a lane's codes of keys g and g + 8
+        uint32_t s0, s1;                  // their scales, one or two
+        if (D == 128) {
+          const uint4 a = *reinterpret_cast<const uint4*>(base + g * 64 + t * 16);
+          const uint4 c = *reinterpret_cast<const uint4*>(base + (g + 8) * 64 + t * 16);
+          k0[0] = a.x, k0[1] = a.y, k0[D / 32 - 2] = a.z, k0[D / 32 - 1] = a.w;
+          k1[0] = c.x, k1[1] = c.y, k1[D / 32 - 2] = c.z, k1[D / 32 - 1] = c.w;
+          s0 = e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(base + 16 * D + g * 8 + t * 2));
+          s1 = e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(base + 16 * D + (g + 8) * 8 + t * 2));
+        } else {
+          const uint2 a = *reinterpret_cast<const uint2*>(base + g * 32 + t * 8);
+          const uint2 c = *reinterpret_cast<const uint2*>(base + (g + 8) * 32 + t * 8);
+          k0[0] = a.x, k0[1] = a.y;
+          k1[0] = c.x, k1[1] = c.y;
+          s0 = e4m3x2_f16x2(base[16 * D + g * 4 + t]);
+          s1 = e4m3x2_f16x2(base[16 * D + (g + 8) * 4 + t]);
+        }
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          const bool second = D == 128 && w >= 2;  // of the lane's two blocks of 16
+          const uint32_t fa = __byte_perm(s0, 0, second ? 0x3232 : 0x1010);
+          const uint32_t fb = __byte_perm(s1, 0, second ? 0x3232 : 0x1010);
+          const uint32_t a0 = mul_f16x2(e2m1x2_f16x2<0>(k0[w]), fa), a1 = mul_f16x2(e2m1x2_f16x2<0>(k1[w]), fb);
+          const uint32_t a2 = mul_f16x2(e2m1x2_f16x2<1>(k0[w]), fa), a3 = mul_f16x2(e2m1x2_f16x2<1>(k1[w]), fb);
+          const uint32_t c0 = mul_f16x2(e2m1x2_f16x2<2>(k0[w]), fa), c1 = mul_f16x2(e2m1x2_f16x2<2>(k1[w]), fb);
+          const uint32_t c2 = mul_f16x2(e2m1x2_f16x2<3>(k0[w]), fa), c3 = mul_f16x2(e2m1x2_f16x2<3>(k1[w]), fb);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma(x[b][nt], a0, a1, a2, a3, qf[nt][2 * w][0], qf[nt][2 * w][1]);
+            mma(x[b][nt], c0, c1, c2, c3, qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
+          }
+        }
+      }
+
+      // scores in base 2: x times its factor
+      const bool whole = key0 + TK - 1 <= len - p.Lq && gone == 0 && (len - 1 - key0 < p.window || key0 + TK <= p.n_sink);
+      float by[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) by[nt][j] = coef[nt][j];
+      if (p.cap > 0.f || p.slopes || !whole) {
+        const float c2 = p.cap * kLog2e;
+        int rg;
+        const int h = head_of(d.u, rg);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            int tt, gg;
+            const bool is = split(rg * C::R + nt * 8 + 2 * t + k, tt, gg);
+            const int row = is ? len - p.Lq + tt : -1;
+            const float slope = is && p.slopes ? p.slopes[h * p.G + gg] * kLog2e : 0.f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int e = k; e < 4; e += 2) {
+                float y = x[b][nt][e] * coef[nt][k];
+                if (p.cap > 0.f) y = c2 * tanhf(y);
+                const int j = key0 + 16 * b + g + (e & 2) * 4, far = row - j;
+                y = fmaf(slope, -static_cast<float>(far), y);
+                const bool seen = far >= 0 && (far < p.window || j < p.n_sink) && !(gone >> b & 1);
+                x[b][nt][e] = seen ? y : -INFINITY;
+              }
+            by[nt][k] = 1.f;
+          }
+      }
+
+      // the rows' references
+      {
+        float mx[NT][2];
+        bool up = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            mx[nt][j] = fmaxf(x[0][nt][j], x[0][nt][2 + j]);
+#pragma unroll
+            for (int b = 1; b < NB; ++b) mx[nt][j] = fmaxf(mx[nt][j], fmaxf(x[b][nt][j], x[b][nt][2 + j]));
+            mx[nt][j] *= by[nt][j];
+            up |= mx[nt][j] > m[nt][j] + 8.f;
+          }
+        if (__any_sync(kFull, up)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float y = mx[nt][j];
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(kFull, y, o));
+              const float old = m[nt][j];
+              const bool move = y > old + 8.f;
+              const float f = !move ? 1.f : old == -INFINITY ? 0.f : ex2(old - y);
+              if (move) m[nt][j] = y;
+              l[nt][j] *= f;
+#pragma unroll
+              for (int a = 0; a < D / 16; ++a) {
+                acc[a][nt][j] *= f;
+                acc[a][nt][2 + j] *= f;
+              }
+            }
+        }
+      }
+      // weights, and as the B operand: keys by rows
+      uint32_t pf[NB][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float lift[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) lift[j] = kLift - (m[nt][j] == -INFINITY ? 0.f : m[nt][j]);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = ex2(fmaf(x[b][nt][e], by[nt][e & 1], lift[e & 1]));
+          l[nt][0] += w[0] + w[2];
+          l[nt][1] += w[1] + w[3];
+          pf[b][nt][0] = transpose8x8(pack_f16x2(w[0], w[1]));
+          pf[b][nt][1] = transpose8x8(pack_f16x2(w[2], w[3]));
+        }
+      }
+
+      // O^T += V^T P^T: rows are dimensions
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const uint8_t* base = st + b * C::kPiece;
+        constexpr int NW = D / 64;  // words (8 dimensions) of a lane
+        uint32_t va[2][NW], vb[2][NW], sc[2];  // keys 2t and 2t + 1 of each half
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          if (D == 128) {
+            const uint4 v = *reinterpret_cast<const uint4*>(base + 8 * D + hf * 512 + g * 64 + t * 16);
+            va[hf][0] = v.x, va[hf][NW - 1] = v.y;
+            vb[hf][0] = v.z, vb[hf][NW - 1] = v.w;
+            sc[hf] = e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(base + 17 * D + g * 16 + hf * 8 + t * 2));
+          } else {
+            const uint8_t* from = base + 8 * D + hf * 256 + (g >> 1) * 64 + t * 16 + (g & 1) * 4;
+            va[hf][0] = *reinterpret_cast<const uint32_t*>(from);
+            vb[hf][0] = *reinterpret_cast<const uint32_t*>(from + 8);
+            sc[hf] = e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(base + 17 * D + (g >> 1) * 16 + hf * 8 + t * 2));
+          }
+          if (!whole) {  // what no row sees may be anything
+            const int b0 = len - p.Lq - p.window + 1;
+            uint32_t keep = 0;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int key = key0 + 16 * b + 8 * hf + 2 * t + j;
+              const bool dead = key >= len || (key < b0 && key >= p.n_sink) || (gone >> b & 1);
+              keep |= dead ? 0u : 0xffffu << (16 * j);
+            }
+            sc[hf] &= keep;
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          // codes of both keys to each dimension: even ones and odd ones
+          uint32_t ev[2], od[2];
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            ev[hf] = select(0x0f0f0f0fu, va[hf][w], vb[hf][w] << 4);
+            od[hf] = select(0x0f0f0f0fu, va[hf][w] >> 4, vb[hf][w]);
+          }
+          auto four = [&](auto I) {
+            constexpr int kI = decltype(I)::value;
+            const uint32_t a0 = mul_f16x2(e2m1x2_f16x2<kI>(ev[0]), sc[0]), a1 = mul_f16x2(e2m1x2_f16x2<kI>(od[0]), sc[0]);
+            const uint32_t a2 = mul_f16x2(e2m1x2_f16x2<kI>(ev[1]), sc[1]), a3 = mul_f16x2(e2m1x2_f16x2<kI>(od[1]), sc[1]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma(acc[4 * w + kI][nt], a0, a1, a2, a3, pf[b][nt][0], pf[b][nt][1]);
+          };
+          four(std::integral_constant<int, 0>());
+          four(std::integral_constant<int, 1>());
+          four(std::integral_constant<int, 2>());
+          four(std::integral_constant<int, 3>());
+        }
+      }
+    }
+
+    // ---- the part's end
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[nt][j] += __shfl_xor_sync(kFull, l[nt][j], o);
+    const bool done = (d.flags & (kBegins | kEnds)) == (kBegins | kEnds);
+    const bool more = popped != pushed;
+    // a whole unit's rows, or a partial result: in the ring, which is empty
+    // then, or in the workspace where the warp goes on
+    const long long spot = 2ll * gridDim.x + static_cast<long long>(blockIdx.x) * W + warp;
+    float* po = more ? p.part_o + spot * p.rows * D : reinterpret_cast<float*>(smem + warp * C::kRing);
+    float2* pm = more ? p.part_ml + spot * p.rows : reinterpret_cast<float2*>(smem + warp * C::kRing + C::R * D * 4);
+    int rg;
+    const int h = head_of(d.u, rg);
+    const float vscale = p.v_scale ? p.v_scale[h] : 1.f;
+    __syncwarp();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int row = nt * 8 + 2 * t + j;
+        int tt, gg;
+        if (!split(rg * C::R + row, tt, gg)) continue;
+        const float L = l[nt][j];
+        if (done) {
+          const float inv = L == 0.f ? 0.f : vscale / L;
+          const long long tok = static_cast<long long>(d.r) * p.Lq + tt;
+          const int head = h * p.G + gg;
+          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + tok * p.ld_o + head * D + g * (D / 8);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = L == 0.f ? 0u : pack_bf16x2(acc[4 * c + e][nt][j] * inv, acc[4 * c + e][nt][2 + j] * inv);
+            reinterpret_cast<uint4*>(o)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          if (p.lse && g == 0) p.lse[tok * (p.H_kv * p.G) + head] = lse_of(m[nt][j], L);
+        } else {
+          float* to = po + row * D + g * (D / 8);
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c)
+            reinterpret_cast<float4*>(to)[c] = make_float4(acc[2 * c][nt][j], acc[2 * c][nt][2 + j],
+                                                           acc[2 * c + 1][nt][j], acc[2 * c + 1][nt][2 + j]);
+          if (g == 0) pm[row] = make_float2(m[nt][j], L);
+        }
+      }
+    if (!done && lane == 0) pieces[2 * warp + (more ? 0 : 1)] = Piece{d.r, d.u, kHere | d.flags, d.end};
+  }
+
+  // ---- the CTA's pieces: those of one unit follow each other, all but perhaps
+  // the last of them in shared memory
   __syncthreads();
   Piece mine{0, 0, 0, 0};
   if (lane < 2 * W) mine = pieces[lane];
@@ -698,6 +730,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
   const unsigned leaders = __ballot_sync(kFull, leads);
   int item = 0;
   int4 tail = make_int4(-1, 0, 0, 0);
+#pragma unroll 1
   for (unsigned rest = leaders; rest; rest &= rest - 1) {
     const int first = __ffs(rest) - 1;
     const unsigned after = rest & (rest - 1);
@@ -707,22 +740,30 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
     const bool begins = __shfl_sync(kFull, mine.flags, first) & kBegins, ends = __shfl_sync(kFull, mine.flags, last) & kEnds;
     const int end = __shfl_sync(kFull, mine.end, last);
     if (begins && !ends) tail = make_int4(r, u, end, 0);
-    const int rows = min(C::R, p.Lq * p.G - u / p.H_kv * C::R);
+    const int rows = min(C::R, p.Lq * p.G - (groups == 1 ? 0 : u / p.H_kv * C::R));
+#pragma unroll 1
     for (int row = 0; row < rows; ++row, ++item) {
       if (item % W != warp) continue;
-      const float* src = nullptr;
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (group >> lane & 1) {
-        const int w = lane >> 1;
-        if (lane & 1) {
-          src = reinterpret_cast<const float*>(smem + w * C::kRing) + row * D;
-          ml = reinterpret_cast<const float2*>(smem + w * C::kRing + C::R * D * 4)[row];
+      const bool far = !(last & 1);  // the last piece is in the workspace
+      const int w0 = first >> 1, w1 = (last >> 1) + (far ? 0 : 1);  // warps with a piece in shared memory
+      const long long spot = 2ll * gridDim.x + static_cast<long long>(blockIdx.x) * W + (last >> 1);
+      constexpr int E = D / 32;
+      float out[E], add[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) out[e] = add[e] = 0.f;
+      auto take = [&](const float* from, float* v) {
+        if (D == 128) {
+          const float4 x = *reinterpret_cast<const float4*>(from);
+          v[0] = x.x, v[1] = x.y, v[E - 2] = x.z, v[E - 1] = x.w;
         } else {
-          const long long spot = 2ll * gridDim.x + static_cast<long long>(blockIdx.x) * W + w;
-          src = p.part_o + (spot * p.rows + row) * D;
-          ml = p.part_ml[spot * p.rows + row];
+          const float2 x = *reinterpret_cast<const float2*>(from);
+          v[0] = x.x, v[1] = x.y;
         }
-      }
+      };
+      if (far) take(p.part_o + (spot * p.rows + row) * D + lane * E, add);
+      float2 ml = make_float2(-INFINITY, 0.f);  // of the lane's warp's piece; lane W: the last one's
+      if (lane < W && group >> (2 * lane + 1) & 1) ml = reinterpret_cast<const float2*>(smem + lane * C::kRing + C::R * D * 4)[row];
+      if (far && lane == W) ml = p.part_ml[spot * p.rows + row];
       float M = ml.x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
@@ -730,30 +771,28 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
       float L = wt_ * ml.y;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) L += __shfl_xor_sync(kFull, L, o);
-      float out[D / 32];
+#pragma unroll 4
+      for (int w = w0; w < w1; ++w) {
+        if (!(group >> (2 * w + 1) & 1)) continue;  // (short spans leave warps without tiles)
+        float v[E];
+        take(reinterpret_cast<const float*>(smem + w * C::kRing) + row * D + lane * E, v);
+        const float f = __shfl_sync(kFull, wt_, w);
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) out[e] = 0.f;
-      for (unsigned x = group; x; x &= x - 1) {
-        const int k = __ffs(x) - 1;
-        const float f = __shfl_sync(kFull, wt_, k);
-        const float* s = reinterpret_cast<const float*>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(src), k)) + lane * (D / 32);
-        if (D == 128) {
-          const float4 v = *reinterpret_cast<const float4*>(s);
-          out[0] = fmaf(f, v.x, out[0]), out[1] = fmaf(f, v.y, out[1]);
-          out[D / 32 - 2] = fmaf(f, v.z, out[D / 32 - 2]), out[D / 32 - 1] = fmaf(f, v.w, out[D / 32 - 1]);
-        } else {
-          const float2 v = *reinterpret_cast<const float2*>(s);
-          out[0] = fmaf(f, v.x, out[0]), out[1] = fmaf(f, v.y, out[1]);
-        }
+        for (int e = 0; e < E; ++e) out[e] = fmaf(f, v[e], out[e]);
+      }
+      if (far) {
+        const float f = __shfl_sync(kFull, wt_, W);
+#pragma unroll
+        for (int e = 0; e < E; ++e) out[e] = fmaf(f, add[e], out[e]);
       }
       if (begins && ends) {
         store_row<D>(p, r, u, row, C::R, M, L, out);
       } else {
-        const long long spot = 2ll * blockIdx.x + (begins ? 1 : 0);
-        float* to = p.part_o + (spot * p.rows + row) * D + lane * (D / 32);
-        if (D == 128) *reinterpret_cast<float4*>(to) = make_float4(out[0], out[1], out[D / 32 - 2], out[D / 32 - 1]);
+        const long long to_spot = 2ll * blockIdx.x + (begins ? 1 : 0);
+        float* to = p.part_o + (to_spot * p.rows + row) * D + lane * E;
+        if (D == 128) *reinterpret_cast<float4*>(to) = make_float4(out[0], out[1], out[E - 2], out[E - 1]);
         else *reinterpret_cast<float2*>(to) = make_float2(out[0], out[1]);
-        if (lane == 0) p.part_ml[spot * p.rows + row] = make_float2(M, L);
+        if (lane == 0) p.part_ml[to_spot * p.rows + row] = make_float2(M, L);
       }
     }
   }
