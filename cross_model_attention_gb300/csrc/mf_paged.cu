@@ -47,6 +47,7 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kRingBytes = 221184;   // of a CTA
 constexpr int kCost = 1;             // a pair's start and end, in tiles
 constexpr int kMinSpan = 2;          // least work of a CTA, in tiles
+constexpr int kLensHere = 900;       // requests whose lengths are kept in shared memory
 constexpr float kLift = 7.f;         // weights are held times 2^7
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -58,25 +59,26 @@ struct Cfg {
   static constexpr int TK = NB * 16;
   static constexpr int kPiece = fp4_piece(D);
   static constexpr int kStage = NB * kPiece;
-  static constexpr int kRing = kRingBytes / W;
+  static constexpr int kRing = kRingBytes / W & ~15;
   static constexpr int S = kRing / kStage;
   static constexpr int R = 8 * NT;
   static constexpr int kThreads = 32 * W;
-  static constexpr int kQueue = S < 4 ? 4 : 8;           // parts of a warp that the ring can hold, and one
+  static constexpr int kQueue = S < 4 ? 4 : 8;           // parts of a warp: one in work, those in the ring, the next
   static constexpr int kPrefix = kRingBytes;             // [threads + 2] long long
-  static constexpr int kLens = kPrefix + 8 * (kThreads + 2);  // [threads]
-  static constexpr int kParts = kLens + 4 * kThreads;
-  static constexpr int kPieces = kParts + 48 * W * kQueue;
+  static constexpr int kSums = kPrefix + 8 * (kThreads + 2);  // [W] long long
+  static constexpr int kLens = kSums + 8 * W;            // [kLensHere]
+  static constexpr int kParts = kLens + 4 * kLensHere;
+  static constexpr int kPieces = kParts + 32 * W * kQueue;
   static constexpr int kWalk = kPieces + 16 * 2 * W;
   static constexpr int kBytes = kWalk + 48 * W;
   static_assert(kBytes <= 232448, "shared memory");
   static_assert(R * D * 4 + R * 8 <= kRing, "a partial result in a warp's ring");
-  static_assert(S >= 2 && S < kQueue && 32 % NB == 0 && S * NB <= 32, "ring");
+  static_assert(S >= 2 && S + 1 <= kQueue && 32 % NB == 0 && S * NB <= 32, "ring");
 };
 
 // A part of a warp's span: tiles i0 .. i1 of a unit.
 struct alignas(16) Part {
-  int r, u, len, i0, i1, flags, end, ta, tb, pad[3];
+  int r, u, len, i0, i1, flags, ta, tb;  // flags: and from bit 8 on the last CTA with tiles of the unit
 };
 enum { kBegins = 1, kEnds = 2, kHere = 4 };
 // Where a warp's walk over its span is: the unit whose line begins at `at`.
@@ -118,6 +120,17 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// tanh: by its series below 0.3, above by the exponential, 1 - 2 / (1 + e^2a); off
+// by 2^-20 of it.  (With tanhf 32 requests of 16384 keys with capped
+// scores take 158 us, with this 138.)
+__device__ __forceinline__ float tanh_of(float x) {
+  const float a = fabsf(x), q = x * x;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(2.f * kLog2e * a)));
+  const float far = copysignf(fmaf(-2.f, r, 1.f), x);
+  const float near = x * fmaf(q, fmaf(q, fmaf(q, fmaf(q, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), 1.f);
+  return a < 0.3f ? near : far;
+}
 // Bits of x where m has ones, of y elsewhere.
 __device__ __forceinline__ uint32_t select(uint32_t m, uint32_t x, uint32_t y) { return (m & x) | (~m & y); }
 
@@ -142,20 +155,16 @@ __device__ __forceinline__ long long line_of(const Tiles& t, int units) {
 // Where row `row` of unit u of request r is in q and o, its head; false past the last row.
 struct Row {
   long long tok;
-  int head, t;
+  int head;
 };
 __device__ __forceinline__ bool row_of(const PagedParams& p, int r, int u, int row, int R, Row& x) {
-  const int rg = u / p.H_kv, h = u - rg * p.H_kv, rr = rg * R + row;
-  if (rr >= p.Lq * p.G) return false;
-  x.t = rr / p.G;
-  x.head = h * p.G + rr - x.t * p.G;
-  x.tok = static_cast<long long>(r) * p.Lq + x.t;
-  return true;
+  const int rg = p.Lq * p.G <= R ? 0 : u / p.H_kv, h = u - rg * p.H_kv, rr = rg * R + row;
+  const int t = static_cast<int>(static_cast<unsigned>(rr) * p.inv_G >> 16);
+  x.head = h * p.G + rr - t * p.G;
+  x.tok = static_cast<long long>(r) * p.Lq + t;
+  return rr < p.Lq * p.G;
 }
 __device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : (m - kLift + log2f(l)) * kLn2; }
-__device__ __forceinline__ float inv_of(const PagedParams& p, int h, float l) {
-  return l == 0.f ? 0.f : (p.v_scale ? p.v_scale[h] : 1.f) / l;
-}
 // A piece's weight beside others under the common reference M.
 __device__ __forceinline__ float weight_of(float m, float l, float M) {
   return m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2(m - M);  // (a sum without a reference is NaN)
@@ -167,7 +176,7 @@ __device__ __forceinline__ void store_row(const PagedParams& p, int r, int u, in
   Row x;
   if (!row_of(p, r, u, row, R, x)) return;
   const int lane = threadIdx.x & 31;
-  const float inv = inv_of(p, x.head / p.G, L);
+  const float inv = L == 0.f ? 0.f : 1.f / L;
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + x.tok * p.ld_o + x.head * D + lane * (D / 32);
   uint32_t w[D / 64];
 #pragma unroll
@@ -193,12 +202,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
   const int share = (p.n + T - 1) / T;
   const int groups = (p.Lq * p.G + C::R - 1) / C::R, units = p.H_kv * groups;
   {
+    long long* sums = reinterpret_cast<long long*>(smem + C::kSums);
     long long sum = 0;
     for (int j = 0; j < share; ++j) {
       const int r = threadIdx.x * share + j;
       if (r >= p.n) break;
       const int len = p.lens[r];
-      if (share == 1) lens_s[r] = len;
+      if (p.n <= kLensHere) lens_s[r] = len;
       sum += line_of(tiles_of<TK>(p, len), units);
     }
     long long inc = sum;
@@ -207,19 +217,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
       const long long y = __shfl_up_sync(kFull, inc, o);
       if (lane >= o) inc += y;
     }
-    // (the warps' sums first, in the threads' place)
-    if (lane == 31) prefix[warp] = inc;
-    __syncthreads();
-    long long before = lane < warp ? prefix[lane] : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) before += __shfl_xor_sync(kFull, before, o);
-    __syncthreads();
-    prefix[threadIdx.x + 1] = before + inc;
-    if (threadIdx.x == 0) prefix[0] = 0;
+    if (lane == 31) sums[warp] = inc;
     if (lane < 2) pieces[2 * warp + lane].flags = 0;
     __syncthreads();
+#pragma unroll
+    for (int w = 0; w < W; ++w) inc += w < warp ? sums[w] : 0;
+    prefix[threadIdx.x + 1] = inc;
+    if (threadIdx.x == 0) prefix[0] = 0;
+    __syncthreads();
   }
-  auto len_of = [&](int r) { return share == 1 ? lens_s[r] : p.lens[r]; };
+  auto len_of = [&](int r) { return p.n <= kLensHere ? lens_s[r] : p.lens[r]; };
   const long long total = prefix[T];
   const int per = static_cast<int>(max(static_cast<long long>(kMinSpan), (total + gridDim.x - 1) / gridDim.x));
   // this CTA's span, from here on in places from its start, and this warp's
@@ -236,14 +243,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
     constexpr int kStep = T / 32;
     const long long f = cta0 + f0;
     const int hi = 31 - __clz(__ballot_sync(kFull, prefix[lane * kStep] <= f));
-    const int j = hi * kStep + 31 - __clz(__ballot_sync(kFull, lane < kStep && prefix[hi * kStep + (lane & (kStep - 1))] <= f));
+    const int j = hi * kStep + 31 - __clz(__ballot_sync(kFull, lane < kStep && prefix[hi * kStep + min(lane, kStep - 1)] <= f));
     long long line = prefix[j];
     wr = j;
     if (share > 1) {
       wr = p.n;
       for (int r0 = j * share; r0 < p.n; r0 += 32) {
         const int r = r0 + lane;
-        const long long mine = line_of(tiles_of<TK>(p, r < p.n ? p.lens[r] : 0), units);
+        const long long mine = line_of(tiles_of<TK>(p, r < p.n ? len_of(r) : 0), units);
         long long inc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -305,7 +312,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
         // (its tiles past this CTA's span are the next CTAs')
         const int end = hi == x.nt ? 0 : static_cast<int>(blockIdx.x + (static_cast<unsigned>(x.at - cta1) + per - 1) / static_cast<unsigned>(per));
         if (lane == 0)
-          parts[pushed & (C::kQueue - 1)] = Part{x.r, u, x.len, lo, hi, (lo == 0 ? kBegins : 0) | (hi == x.nt ? kEnds : 0), end, x.ta, x.tb, {0, 0, 0}};
+          parts[pushed & (C::kQueue - 1)] = Part{x.r, u, x.len, lo, hi, (lo == 0 ? kBegins : 0) | (hi == x.nt ? kEnds : 0) | end << 8, x.ta, x.tb};
         ++pushed;
       }
     }
@@ -328,11 +335,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
 
   // ---- q of a part: loads, then fp16
   uint4 qw[NT][D / 32];
-  float kscale = 1.f;
+  float kscale = 1.f, vscale = 1.f;
   auto load_q = [&](int r, int u) {
     int rg;
     const int h = head_of(u, rg);
     if (p.k_scale) kscale = p.k_scale[h];
+    if (p.v_scale) vscale = p.v_scale[h];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       int tt, gg;
@@ -417,8 +425,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
   }
 
   // ---- parts and their tiles
+  const bool special = p.cap > 0.f || p.slopes;
   int slot = 0;
-  bool q_here = true;
+  bool q_here = have || pushed > 0;
   __syncwarp();
 #pragma unroll 1
   while (popped != pushed) {
@@ -427,6 +436,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
     ++popped;
     if (!q_here) load_q(d.r, d.u);
     q_here = false;
+    const float vs = vscale;
     uint32_t qf[NT][D / 16][2];
     float acc[D / 16][NT][4], m[NT][2], l[NT][2], coef[NT][2];
 #pragma unroll
@@ -529,8 +539,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) by[nt][j] = coef[nt][j];
-      if (p.cap > 0.f || p.slopes || !whole) {
-        const float c2 = p.cap * kLog2e;
+      if (special || !whole) {
         int rg;
         const int h = head_of(d.u, rg);
 #pragma unroll
@@ -540,19 +549,30 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
             int tt, gg;
             const bool is = split(rg * C::R + nt * 8 + 2 * t + k, tt, gg);
             const int row = is ? len - p.Lq + tt : -1;
-            const float slope = is && p.slopes ? p.slopes[h * p.G + gg] * kLog2e : 0.f;
+            if (special) {
+              const float slope = is && p.slopes ? p.slopes[h * p.G + gg] * kLog2e : 0.f;
+              const float near = static_cast<float>(key0 + g - row);  // less what the row is away, in keys
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
+              for (int b = 0; b < NB; ++b)
 #pragma unroll
-              for (int e = k; e < 4; e += 2) {
-                float y = x[b][nt][e] * coef[nt][k];
-                if (p.cap > 0.f) y = c2 * tanhf(y);
-                const int j = key0 + 16 * b + g + (e & 2) * 4, far = row - j;
-                y = fmaf(slope, -static_cast<float>(far), y);
-                const bool seen = far >= 0 && (far < p.window || j < p.n_sink) && !(gone >> b & 1);
-                x[b][nt][e] = seen ? y : -INFINITY;
-              }
-            by[nt][k] = 1.f;
+                for (int e = k; e < 4; e += 2) {
+                  float y = x[b][nt][e] * coef[nt][k];
+                  if (p.cap > 0.f) y = p.cap * kLog2e * tanh_of(y);
+                  x[b][nt][e] = fmaf(slope, near + static_cast<float>(16 * b + (e & 2) * 4), y);
+                }
+              by[nt][k] = 1.f;
+            }
+            if (!whole) {
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int e = k; e < 4; e += 2) {
+                  const int j = key0 + 16 * b + g + (e & 2) * 4, far = row - j;
+                  const bool seen = far >= 0 && (far < p.window || j < p.n_sink) && !(gone >> b & 1);
+                  x[b][nt][e] = seen ? x[b][nt][e] * by[nt][k] : -INFINITY;
+                }
+              by[nt][k] = 1.f;
+            }
           }
       }
 
@@ -681,7 +701,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
     float2* pm = more ? p.part_ml + spot * p.rows : reinterpret_cast<float2*>(smem + warp * C::kRing + C::R * D * 4);
     int rg;
     const int h = head_of(d.u, rg);
-    const float vscale = p.v_scale ? p.v_scale[h] : 1.f;
     __syncwarp();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -692,7 +711,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
         if (!split(rg * C::R + row, tt, gg)) continue;
         const float L = l[nt][j];
         if (done) {
-          const float inv = L == 0.f ? 0.f : vscale / L;
+          const float inv = L == 0.f ? 0.f : vs / L;
           const long long tok = static_cast<long long>(d.r) * p.Lq + tt;
           const int head = h * p.G + gg;
           __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + tok * p.ld_o + head * D + g * (D / 8);
@@ -709,12 +728,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
           float* to = po + row * D + g * (D / 8);
 #pragma unroll
           for (int c = 0; c < D / 32; ++c)
-            reinterpret_cast<float4*>(to)[c] = make_float4(acc[2 * c][nt][j], acc[2 * c][nt][2 + j],
-                                                           acc[2 * c + 1][nt][j], acc[2 * c + 1][nt][2 + j]);
+            reinterpret_cast<float4*>(to)[c] = make_float4(acc[2 * c][nt][j] * vs, acc[2 * c][nt][2 + j] * vs,
+                                                           acc[2 * c + 1][nt][j] * vs, acc[2 * c + 1][nt][2 + j] * vs);
           if (g == 0) pm[row] = make_float2(m[nt][j], L);
         }
       }
-    if (!done && lane == 0) pieces[2 * warp + (more ? 0 : 1)] = Piece{d.r, d.u, kHere | d.flags, d.end};
+    if (!done && lane == 0) pieces[2 * warp + (more ? 0 : 1)] = Piece{d.r, d.u, kHere | (d.flags & 0xff), d.flags >> 8};
   }
 
   // ---- the CTA's pieces: those of one unit follow each other, all but perhaps
@@ -728,75 +747,78 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
   const int prev_r = __shfl_sync(kFull, mine.r, prev), prev_u = __shfl_sync(kFull, mine.u, prev);
   const bool leads = (mine.flags & kHere) && (!lower || prev_r != mine.r || prev_u != mine.u);
   const unsigned leaders = __ballot_sync(kFull, leads);
-  int item = 0;
-  int4 tail = make_int4(-1, 0, 0, 0);
-#pragma unroll 1
-  for (unsigned rest = leaders; rest; rest &= rest - 1) {
-    const int first = __ffs(rest) - 1;
-    const unsigned after = rest & (rest - 1);
+  // (group, row) by warp; a group's last piece has the CTA's tail
+  const int n_groups = __popc(leaders), rank = __popc(leaders & ((1u << lane) - 1u));
+  constexpr int E = D / 32;
+  auto take = [&](const float* from, float* v) {
+    if (D == 128) {
+      const float4 x = *reinterpret_cast<const float4*>(from);
+      v[0] = x.x, v[1] = x.y, v[E - 2] = x.z, v[E - 1] = x.w;
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(from);
+      v[0] = x.x, v[1] = x.y;
+    }
+  };
+  for (int item = warp; item < n_groups * p.rows; item += W) {
+    const int at_group = item / p.rows, row = item - at_group * p.rows;
+    const int first = __ffs(__ballot_sync(kFull, leads && rank == at_group)) - 1;
+    const unsigned after = leaders & ~((2u << first) - 1u);
     const unsigned group = present & ~((1u << first) - 1u) & (after ? (1u << (__ffs(after) - 1)) - 1u : kFull);
     const int last = 31 - __clz(group);
-    const int r = __shfl_sync(kFull, mine.r, first), u = __shfl_sync(kFull, mine.u, first);
-    const bool begins = __shfl_sync(kFull, mine.flags, first) & kBegins, ends = __shfl_sync(kFull, mine.flags, last) & kEnds;
-    const int end = __shfl_sync(kFull, mine.end, last);
-    if (begins && !ends) tail = make_int4(r, u, end, 0);
-    const int rows = min(C::R, p.Lq * p.G - (groups == 1 ? 0 : u / p.H_kv * C::R));
-#pragma unroll 1
-    for (int row = 0; row < rows; ++row, ++item) {
-      if (item % W != warp) continue;
-      const bool far = !(last & 1);  // the last piece is in the workspace
-      const int w0 = first >> 1, w1 = (last >> 1) + (far ? 0 : 1);  // warps with a piece in shared memory
+    const Piece a = pieces[first], z = pieces[last];
+    const bool begins = a.flags & kBegins, ends = z.flags & kEnds;
+    const bool far = !(last & 1);  // the last piece is in the workspace
+    const int w0 = first >> 1, w1 = (last >> 1) + (far ? 0 : 1);  // warps with a piece in shared memory
+    float out[E], add[E], M = -INFINITY, L = 0.f;
+    float2 ml_far = make_float2(-INFINITY, 0.f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) out[e] = add[e] = 0.f;
+    if (far) {
       const long long spot = 2ll * gridDim.x + static_cast<long long>(blockIdx.x) * W + (last >> 1);
-      constexpr int E = D / 32;
-      float out[E], add[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) out[e] = add[e] = 0.f;
-      auto take = [&](const float* from, float* v) {
-        if (D == 128) {
-          const float4 x = *reinterpret_cast<const float4*>(from);
-          v[0] = x.x, v[1] = x.y, v[E - 2] = x.z, v[E - 1] = x.w;
-        } else {
-          const float2 x = *reinterpret_cast<const float2*>(from);
-          v[0] = x.x, v[1] = x.y;
-        }
-      };
-      if (far) take(p.part_o + (spot * p.rows + row) * D + lane * E, add);
-      float2 ml = make_float2(-INFINITY, 0.f);  // of the lane's warp's piece; lane W: the last one's
-      if (lane < W && group >> (2 * lane + 1) & 1) ml = reinterpret_cast<const float2*>(smem + lane * C::kRing + C::R * D * 4)[row];
-      if (far && lane == W) ml = p.part_ml[spot * p.rows + row];
-      float M = ml.x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-      const float wt_ = weight_of(ml.x, ml.y, M);
-      float L = wt_ * ml.y;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) L += __shfl_xor_sync(kFull, L, o);
+      take(p.part_o + (spot * p.rows + row) * D + lane * E, add);
+      ml_far = p.part_ml[spot * p.rows + row];
+    }
+    // (short spans leave warps without tiles)
+    auto ml_of = [&](int w) {
+      return group >> (2 * w + 1) & 1 ? reinterpret_cast<const float2*>(smem + w * C::kRing + C::R * D * 4)[row] : make_float2(-INFINITY, 0.f);
+    };
 #pragma unroll 4
-      for (int w = w0; w < w1; ++w) {
-        if (!(group >> (2 * w + 1) & 1)) continue;  // (short spans leave warps without tiles)
-        float v[E];
-        take(reinterpret_cast<const float*>(smem + w * C::kRing) + row * D + lane * E, v);
-        const float f = __shfl_sync(kFull, wt_, w);
+    for (int w = w0; w < w1; ++w) M = fmaxf(M, ml_of(w).x);
+    M = fmaxf(M, ml_far.x);
+#pragma unroll 4
+    for (int w = w0; w < w1; ++w) {
+      const float2 ml = ml_of(w);
+      const float f = weight_of(ml.x, ml.y, M);
+      float v[E];
+      if (!(group >> (2 * w + 1) & 1)) continue;
+      take(reinterpret_cast<const float*>(smem + w * C::kRing) + row * D + lane * E, v);
+      L = fmaf(f, ml.y, L);
 #pragma unroll
-        for (int e = 0; e < E; ++e) out[e] = fmaf(f, v[e], out[e]);
-      }
-      if (far) {
-        const float f = __shfl_sync(kFull, wt_, W);
+      for (int e = 0; e < E; ++e) out[e] = fmaf(f, v[e], out[e]);
+    }
+    if (far) {
+      const float f = weight_of(ml_far.x, ml_far.y, M);
+      L = fmaf(f, ml_far.y, L);
 #pragma unroll
-        for (int e = 0; e < E; ++e) out[e] = fmaf(f, add[e], out[e]);
-      }
-      if (begins && ends) {
-        store_row<D>(p, r, u, row, C::R, M, L, out);
-      } else {
-        const long long to_spot = 2ll * blockIdx.x + (begins ? 1 : 0);
-        float* to = p.part_o + (to_spot * p.rows + row) * D + lane * E;
-        if (D == 128) *reinterpret_cast<float4*>(to) = make_float4(out[0], out[1], out[E - 2], out[E - 1]);
-        else *reinterpret_cast<float2*>(to) = make_float2(out[0], out[1]);
-        if (lane == 0) p.part_ml[to_spot * p.rows + row] = make_float2(M, L);
-      }
+      for (int e = 0; e < E; ++e) out[e] = fmaf(f, add[e], out[e]);
+    }
+    if (begins && ends) {
+      store_row<D>(p, a.r, a.u, row, C::R, M, L, out);
+    } else {
+      const long long spot = 2ll * blockIdx.x + (begins ? 1 : 0);
+      float* to = p.part_o + (spot * p.rows + row) * D + lane * E;
+      if (D == 128) *reinterpret_cast<float4*>(to) = make_float4(out[0], out[1], out[E - 2], out[E - 1]);
+      else *reinterpret_cast<float2*>(to) = make_float2(out[0], out[1]);
+      if (lane == 0) p.part_ml[spot * p.rows + row] = make_float2(M, L);
     }
   }
-  if (threadIdx.x == 0) p.cuts[blockIdx.x] = tail;
+  if (warp == 0) {  // for the join: a unit that begins here and ends in another CTA
+    const int last = present ? 31 - __clz(present) : 0, head = leaders ? 31 - __clz(leaders) : 0;
+    if (lane == 0) {
+      const Piece a = pieces[head], z = pieces[last];
+      p.cuts[blockIdx.x] = present && (a.flags & kBegins) && !(z.flags & kEnds) ? make_int4(z.r, z.u, z.end, 0) : make_int4(-1, 0, 0, 0);
+    }
+  }
 }
 
 // The units that several CTAs share: a warp to a row, the results of CTA c's
@@ -805,32 +827,45 @@ template <int D, int NT>
 __global__ void __launch_bounds__(32) join_kernel(const PagedParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x, row = blockIdx.y, lane = threadIdx.x;
+  auto spot = [&](int k) { return (k == 0 ? 2ll * c + 1 : 2ll * (c + k)) * p.rows + row; };
+  // (the first results are asked for before it is known which there are)
+  constexpr int kAhead = 4, E = D / 32;
   const int4 cut = p.cuts[c];
+  float v[kAhead][E];
+  float2 ml[kAhead];
+  auto take = [&](int j, int k) {
+    ml[j] = p.part_ml[spot(k)];
+    const float* s = p.part_o + spot(k) * D + lane * E;
+    if (D == 128) {
+      const float4 y = *reinterpret_cast<const float4*>(s);
+      v[j][0] = y.x, v[j][1] = y.y, v[j][E - 2] = y.z, v[j][E - 1] = y.w;
+    } else {
+      const float2 y = *reinterpret_cast<const float2*>(s);
+      v[j][0] = y.x, v[j][1] = y.y;
+    }
+  };
+  const int most = gridDim.x - c;
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) take(j, min(j, most - 1));
   if (cut.x < 0) return;
-  Row x;
-  if (!row_of(p, cut.x, cut.y, row, 8 * NT, x)) return;
   const int n = cut.z - c + 1;
-  auto spot = [&](int k) { return k == 0 ? 2ll * c + 1 : 2ll * (c + k); };
   float M = -INFINITY, L = 0.f;
-  for (int k = lane; k < n; k += 32) M = fmaxf(M, p.part_ml[spot(k) * p.rows + row].x);
+  for (int k = lane; k < n; k += 32) M = fmaxf(M, p.part_ml[spot(k)].x);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-  float out[D / 32];
+  float out[E];
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e) out[e] = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < n; ++k) {
-    const float2 ml = p.part_ml[spot(k) * p.rows + row];
-    const float f = weight_of(ml.x, ml.y, M);
-    L += f * ml.y;
-    const float* s = p.part_o + (spot(k) * p.rows + row) * D + lane * (D / 32);
-    if (D == 128) {
-      const float4 v = *reinterpret_cast<const float4*>(s);
-      out[0] = fmaf(f, v.x, out[0]), out[1] = fmaf(f, v.y, out[1]);
-      out[D / 32 - 2] = fmaf(f, v.z, out[D / 32 - 2]), out[D / 32 - 1] = fmaf(f, v.w, out[D / 32 - 1]);
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(s);
-      out[0] = fmaf(f, v.x, out[0]), out[1] = fmaf(f, v.y, out[1]);
+  for (int e = 0; e < E; ++e) out[e] = 0.f;
+  for (int k0 = 0; k0 < n; k0 += kAhead) {
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (k0 + j < n) {
+        const float f = weight_of(ml[j].x, ml[j].y, M);
+        L = fmaf(f, ml[j].y, L);
+#pragma unroll
+        for (int e = 0; e < E; ++e) out[e] = fmaf(f, v[j][e], out[e]);
+      }
+      if (k0 + kAhead + j < n) take(j, k0 + kAhead + j);
     }
   }
   store_row<D>(p, cut.x, cut.y, row, 8 * NT, M, L, out);
