@@ -13,9 +13,10 @@
 // of it is an error of a whole code.  Codes are therefore those of the exact
 // values, whatever the order of sums: fp32 is good to 2^-19 (with the norm; 2^-21
 // without: angle, sine and cosine 2^-22 together, products and sum 2^-24 each,
-// the norm's sum and root 2^-20) of a pair's |a| + |b|, a row with a value that
-// near to a step (one in some hundred) is done again in fp64, by the warp that
-// finds it.  What is exact in fp32 (values, keys that are neither normed nor
+// the norm's sum and root 2^-20) of a pair's |a| + |b|, and a row with a value that
+// near to a step (one in some hundred) is done again in twice that precision, by
+// the warp that finds it, once its other rows are done (mf_ff.cuh: 2^-43, which
+// leaves one value in 10^11 undecided).  What is exact in fp32 (values, keys that are neither normed nor
 // rotated) often lies on a step itself: its quotient is corrected by its residue,
 // which finds those exactly.
 //
@@ -28,6 +29,7 @@
 
 #include <cuda_bf16.h>
 
+#include "mf_ff.cuh"
 #include "mf_fp4.cuh"
 #include "mf_internal.cuh"
 #include "mf_ptx.cuh"
@@ -97,46 +99,62 @@ __device__ __forceinline__ Scale scale_of(uint32_t top, float off, float g, bool
 // quotient of few bits comes out exactly.
 __device__ __forceinline__ float quotient(float y, const Scale& s) {
   const float t = y * s.r;
-  const float rest = fmaf(-t, s.lo, fmaf(-t, s.sg, y));
-  return fabsf(t) < 8.f ? fmaf(rest, s.r, t) : t;
+  return fmaf(fmaf(-t, s.lo, fmaf(-t, s.sg, y)), s.r, t);
 }
-// Codes of 8 values that are off by at most off[e] or `off`; near: whether
-// one of them has another code as likely (a zero's sign says nothing).
-__device__ __forceinline__ uint32_t codes_of(const float* y, const Scale& s, float off, unsigned loose, bool& near) {
+// Codes of 8 values, each exact in fp32.
+__device__ __forceinline__ uint32_t codes_exactly(const float* y, const Scale& s) {
+  float t[8];
+  if (s.byte == 0x7e) {  // the largest scale: quotients may be of any size
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = fabsf(y[i] * s.r) < 8.f ? quotient(y[i], s) : y[i] * s.r;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = quotient(y[i], s);
+  }
+  return f32x8_e2m1(t);
+}
+// Codes of 8 values that are off by at most `off` (which counts the quotient's
+// own rounding); near: whether one of them has another code as likely (a zero's
+// sign says nothing).
+__device__ __forceinline__ uint32_t codes_of(const float* y, const Scale& s, float off, bool& near) {
   float lo[8], hi[8];
   const float e = off * s.r;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float t = quotient(y[i], s), ei = (loose >> i) & 1 ? e : 0.f;
-    lo[i] = t - ei;
-    hi[i] = t + ei;
+    lo[i] = fmaf(y[i], s.r, -e);
+    hi[i] = fmaf(y[i], s.r, e);
   }
   const uint32_t a = f32x8_e2m1(lo), b = f32x8_e2m1(hi);
   near |= ((a ^ b) & 0x77777777u) != 0;
   return b;
 }
-__device__ __forceinline__ uint32_t codes_exactly(const float* y, const Scale& s) {
-  float t[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) t[i] = quotient(y[i], s);
-  return f32x8_e2m1(t);
-}
 
-// The same in fp64.
-__device__ __forceinline__ uint32_t scale64(double top, double g) {
-  if (!(top < 1e300)) return kNanScale;
-  return f32x2_e4m3(static_cast<float>(fmin(top / (6.0 * g), 448.0)), 0.f) & 0xffu;
+// The same in two fp32 numbers, of a value and a scale g.
+__device__ __forceinline__ uint32_t scale_ff(ff top, float g) {
+  if (!(top.h < INFINITY)) return kNanScale;
+  const float g6 = mul_rn(6.f, g), q = top.h / g6;
+  const uint32_t two = f32x2_e4m3(q * (1.f - 4.76837158203125e-07f), q * (1.f + 4.76837158203125e-07f));
+  const uint32_t a = two & 0xffu, b = two >> 8;
+  if (a == b) return a;
+  const float border = 0.5f * (e4m3_f32(a) + e4m3_f32(b));  // between neighbours: exact
+  const float d = add_rn(fmaf(-border, g6, top.h), fmaf(-border, fmaf(6.f, g, -g6), top.l));
+  return d > 0.f || (d == 0.f && (a & 1)) ? b : a;
 }
-__device__ __forceinline__ uint32_t codes64(const double* y, uint32_t byte, double g) {
-  const double sg = byte == kNanScale ? 0.0 : static_cast<double>(e4m3_f32(byte)) * g;
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const double t = sg > 0.0 ? fabs(y[i]) / sg : 0.0;
-    const uint32_t c = (t > 0.25) + (t >= 0.75) + (t > 1.25) + (t >= 1.75) + (t > 2.5) + (t >= 3.5) + (t > 5.0);
-    w |= (c | (y[i] < 0.0 ? 8u : 0u)) << (4 * i);
-  }
-  return w;
+__device__ __forceinline__ uint32_t code_ff(ff y, float sg, float lo) {
+  const bool minus = y.h < 0.f;
+  if (minus) y = ff_neg(y);
+  // past the border x (a half between codes goes to the even one)
+  auto past = [&](float x, bool even) {
+    const float d = add_rn(fmaf(-x, sg, y.h), fmaf(-x, lo, y.l));
+    return d > 0.f || (even && d == 0.f) ? 1u : 0u;
+  };
+  const uint32_t c = past(0.25f, false) + past(0.75f, true) + past(1.25f, false) + past(1.75f, true) + past(2.5f, false) +
+                     past(3.5f, true) + past(5.f, false);
+  return sg > 0.f ? c | (minus ? 8u : 0u) : 0u;
+}
+__device__ __forceinline__ ff larger(ff a, ff b) { return a.h > b.h || (a.h == b.h && a.l >= b.l) ? a : b; }
+__device__ __forceinline__ ff from_lane(ff a, int mask) {
+  return {__shfl_xor_sync(kFull, a.h, mask), __shfl_xor_sync(kFull, a.l, mask)};
 }
 
 struct Held {
@@ -144,93 +162,118 @@ struct Held {
   uint32_t s0, s1;  // the scales of their blocks
 };
 
-// One row in fp64, by the lanes that have it (the whole warp comes here; rows
-// without keys bring `row` = nullptr).
+// One row in twice fp32's precision, by the lanes that have it (the whole warp
+// comes here; rows that are not asked for bring nullptr).
 template <int D, int LAYOUT>
 __device__ __noinline__ Held exact_row(const CacheParams& p, const __nv_bfloat16* row, long long pos, int c0, int c1,
                                        bool turned, float g) {
   constexpr int LPR = D / 16;
   const int half = p.rot >> 1;
   const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(p.weight);
-  auto x_of = [&](int d) { return row ? static_cast<double>(__bfloat162float(row[d])) : 0.0; };
-  double y[16];
-  double ss = 0.0;
+  auto x_of = [&](int d) { return row ? __bfloat162float(row[d]) : 0.f; };
+  auto dim = [&](int e) { return (e < 8 ? c0 * 8 : c1 * 8 - 8) + e; };
+  ff y[16];
+  uint32_t top = 0;
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
-    y[e] = x_of((e < 8 ? c0 * 8 : c1 * 8 - 8) + e);
-    ss += y[e] * y[e];
+    y[e] = {x_of(dim(e)), 0.f};
+    top = max(top, mag(y[e].h));
   }
 #pragma unroll
-  for (int off = LPR / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(kFull, ss, off);
-  const double r = p.norm ? 1.0 / sqrt(ss / D + static_cast<double>(p.eps)) : 1.0;
-  auto normed = [&](double x, int d) { return x * r * (w ? static_cast<double>(__bfloat162float(w[d])) : 1.0); };
-  auto turn = [&](int f, double& cn, double& sn) {
-    const unsigned long long t = static_cast<unsigned long long>(pos) * p.freq[f];
-    sincospi(static_cast<double>(static_cast<long long>(t)) * 1.0842021724855044e-19, &sn, &cn);  // 2^-63
-    cn *= static_cast<double>(p.gain);
-    sn *= static_cast<double>(p.gain);
+  for (int off = LPR / 2; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(kFull, top, off));
+  // rows of huge values are brought into range (what the norm gives is in it), with
+  // what they are compared with
+  const int ex = static_cast<int>(top >> 23) - 127;
+  const float down = ex > 30 ? __int_as_float((127 - min(ex, 127) + 30) << 23) : 1.f;
+  if (!p.norm) g *= down;
+  ff r = {1.f, 0.f};
+  ff ss = {0.f, 0.f};
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    y[e].h *= down;
+    const ff t = ff_sum(ss.h, mul_rn(y[e].h, y[e].h));  // (a square of 8 bits is exact)
+    ss = {t.h, add_rn(ss.l, t.l)};
+  }
+  if (p.norm) {
+#pragma unroll
+    for (int off = LPR / 2; off > 0; off >>= 1) ss = ff_add(ss, from_lane(ss, off));
+    const ff m = ff_add(ff{ss.h * (1.f / D), ss.l * (1.f / D)}, ff{p.eps * down * down, 0.f});
+    const float r0 = rsqrtf(m.h);
+    const ff q = ff_mul(m, ff_mul(ff{r0, 0.f}, r0));
+    r = ff_fast_sum(r0, mul_rn(0.5f * r0, add_rn(add_rn(1.f, -q.h), -q.l)));  // one step of Newton's
+    if (top >= kInf) r = {top > kInf ? NAN : 0.f, 0.f};  // (an infinity's row: 0 but for it)
+  }
+  auto normed = [&](float x, int d) {
+    const float v = w ? mul_rn(x, __bfloat162float(w[d])) : x;  // (16 bits)
+    return p.norm ? ff_mul(r, v) : ff{v, 0.f};
+  };
+  auto turn = [&](int f, ff& cn, ff& sn) {
+    ff_sincos(static_cast<uint64_t>(pos) * p.freq[f], &sn, &cn);
+    cn = ff_mul(cn, p.gain);
+    sn = ff_mul(sn, p.gain);
   };
 #pragma unroll
-  for (int e = 0; e < 16; ++e) y[e] = normed(y[e], (e < 8 ? c0 * 8 : c1 * 8 - 8) + e);
-  double cn, sn;
+  for (int e = 0; e < 16; ++e) y[e] = normed(y[e].h, dim(e));
+  ff cn, sn;
   if (LAYOUT == kHalf) {
     if (turned) {
-#pragma unroll 1
+#pragma unroll
       for (int e = 0; e < 8; ++e) {
         turn(c0 * 8 + e, cn, sn);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)  // (registers, not an array in memory)
-          if (i == e) {
-            const double a = y[i], b = y[8 + i];
-            y[i] = a * cn - b * sn;
-            y[8 + i] = b * cn + a * sn;
-          }
+        const ff a = y[e], b = y[8 + e];
+        y[e] = ff_add(ff_mul(a, cn), ff_neg(ff_mul(b, sn)));
+        y[8 + e] = ff_add(ff_mul(b, cn), ff_mul(a, sn));
       }
+    }
+  } else if (LAYOUT == kPairs) {
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      if (c0 * 8 + e >= p.rot) continue;
+      turn(c0 * 4 + (e >> 1), cn, sn);
+      const ff a = y[e], b = y[e + 1];
+      y[e] = ff_add(ff_mul(a, cn), ff_neg(ff_mul(b, sn)));
+      y[e + 1] = ff_add(ff_mul(b, cn), ff_mul(a, sn));
     }
   } else {
-#pragma unroll 1
-    for (int e = 0; e < 16; e += LAYOUT == kPairs ? 2 : 1) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
       const int d = c0 * 8 + e;
-      if (d >= p.rot) break;
-      if (LAYOUT == kPairs) {
-        turn(d >> 1, cn, sn);
-#pragma unroll
-        for (int i = 0; i < 16; i += 2)
-          if (i == e) {
-            const double a = y[i], b = y[i + 1];
-            y[i] = a * cn - b * sn;
-            y[i + 1] = b * cn + a * sn;
-          }
-      } else {
-        const int other = d < half ? d + half : d - half;
-        const double z = normed(x_of(other), other);
-        turn(d < half ? d : other, cn, sn);
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (i == e) y[i] = d < half ? y[i] * cn - z * sn : y[i] * cn + z * sn;
-      }
+      if (d >= p.rot) continue;
+      const int other = d < half ? d + half : d - half;
+      const ff z = normed(x_of(other) * down, other);
+      turn(d < half ? d : other, cn, sn);
+      const ff t = ff_mul(z, sn);
+      y[e] = ff_add(ff_mul(y[e], cn), d < half ? ff_neg(t) : t);
     }
   }
-  constexpr double kBad = 1e308;  // above everything that a row of bf16 can come to
-  auto size = [](double v) { return fabs(v) < kBad ? fabs(v) : kBad; };
-  double t0 = 0.0, t1 = 0.0;
+  ff t0 = {0.f, 0.f}, t1 = {0.f, 0.f};
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    t0 = fmax(t0, size(y[e]));
-    t1 = fmax(t1, size(y[8 + e]));
+    auto size = [](ff v) {
+      if (!(fabsf(v.h) < INFINITY)) return ff{INFINITY, 0.f};
+      return v.h < 0.f ? ff_neg(v) : v;
+    };
+    t0 = larger(t0, size(y[e]));
+    t1 = larger(t1, size(y[8 + e]));
   }
   if (LAYOUT == kHalf) {
-    const double o0 = __shfl_xor_sync(kFull, t0, 1), o1 = __shfl_xor_sync(kFull, t1, 1);
-    t0 = turned ? fmax(t0, o0) : fmax(t0, t1);
-    t1 = turned ? fmax(t1, o1) : t0;
+    const ff o0 = from_lane(t0, 1), o1 = from_lane(t1, 1);
+    t0 = larger(t0, turned ? o0 : t1);
+    t1 = turned ? larger(t1, o1) : t0;
   } else {
-    t0 = t1 = fmax(t0, t1);
+    t0 = t1 = larger(t0, t1);
   }
   Held h;
-  h.s0 = scale64(t0, g);
-  h.s1 = scale64(t1, g);
-  h.c0 = codes64(y, h.s0, g);
-  h.c1 = codes64(y + 8, h.s1, g);
+  h.s0 = scale_ff(t0, g);
+  h.s1 = scale_ff(t1, g);
+  h.c0 = h.c1 = 0;
+  const float f0 = h.s0 == kNanScale ? 0.f : e4m3_f32(h.s0), f1 = h.s1 == kNanScale ? 0.f : e4m3_f32(h.s1);
+  const float g0 = mul_rn(f0, g), g1 = mul_rn(f1, g);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    h.c0 |= code_ff(y[e], g0, fmaf(f0, g, -g0)) << (4 * e);
+    h.c1 |= code_ff(y[8 + e], g1, fmaf(f1, g, -g1)) << (4 * e);
+  }
   return h;
 }
 
@@ -301,11 +344,10 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const CacheParams p) {
     unpack8(*reinterpret_cast<const uint4*>(w + c0 * 8), ga);
     unpack8(*reinterpret_cast<const uint4*>(w + c1 * 8), gb);
   }
-  // which of the lane's dimensions are not exact in fp32, and by how much of
-  // |a| + |b| they are off
-  unsigned loose = p.norm || turned ? 0xffffu : 0u;
-  if (LAYOUT != kHalf && !p.norm && c0 * 8 < p.rot) loose = p.rot - c0 * 8 >= 16 ? 0xffffu : (1u << (p.rot - c0 * 8)) - 1u;
-  const float err = (p.norm ? 1.9073486328125e-06f : 4.76837158203125e-07f) * fmaxf(1.f, p.gain);
+  // How far a key's values may be off, of |a| + |b|: all of the lane's or (kAny,
+  // kPairs) some, where the rest is taken to be off as much.
+  const bool loose = p.norm || (LAYOUT == kHalf ? turned : c0 * 8 < p.rot);
+  const float err = (p.norm ? 1.9073486328125e-06f : 4.76837158203125e-07f) * fmaxf(1.f, p.gain);  // 2^-19, 2^-21
 
   // where the rows go
   uint8_t *kdst = nullptr, *ksdst = nullptr, *vdst = nullptr, *vsdst = nullptr;
@@ -329,6 +371,24 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const CacheParams p) {
     vout = static_cast<__nv_bfloat16*>(p.v) + row * p.ld_v + at;
   }
 
+  auto put = [&](int i, bool live, const Held& kh) {
+    if (!live) return;
+    uint8_t* dst = kdst + i * hstride;
+    uint8_t* sdst = ksdst + i * hstride;
+    if (turned) {
+      *reinterpret_cast<uint32_t*>(dst + c0 * 4) = kh.c0;
+      *reinterpret_cast<uint32_t*>(dst + c1 * 4) = kh.c1;
+      if ((l & 1) == 0) {
+        sdst[c0 >> 1] = static_cast<uint8_t>(kh.s0);
+        sdst[c1 >> 1] = static_cast<uint8_t>(kh.s1);
+      }
+    } else {
+      *reinterpret_cast<uint2*>(dst + l * 8) = make_uint2(kh.c0, kh.c1);
+      sdst[l] = static_cast<uint8_t>(kh.s0);
+    }
+  };
+  unsigned again = 0;  // of 32 heads: those to be done more exactly
+#pragma unroll 1
   for (int i = 0; i < p.heads_per_unit; ++i) {
     float a[8], b[8], x[8], z[8];
     unpack8(ka, a);
@@ -427,28 +487,19 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const CacheParams p) {
     Held kh;
     {
       const Scale s0 = scale_of(t0, off, gk, near);
-      kh.s0 = s0.byte;
-      kh.c0 = codes_of(x, s0, off, loose & 0xffu, near);
       const Scale s1 = LAYOUT == kHalf ? scale_of(t1, off, gk, near) : s0;
+      kh.s0 = s0.byte;
       kh.s1 = s1.byte;
-      kh.c1 = codes_of(z, s1, off, loose >> 8, near);
-    }
-    if (__any_sync(kFull, near && live)) kh = exact_row<D, LAYOUT>(p, live ? row : nullptr, pos, c0, c1, turned, gk);
-    if (live) {
-      uint8_t* dst = kdst + i * hstride;
-      uint8_t* sdst = ksdst + i * hstride;
-      if (turned) {
-        *reinterpret_cast<uint32_t*>(dst + c0 * 4) = kh.c0;
-        *reinterpret_cast<uint32_t*>(dst + c1 * 4) = kh.c1;
-        if ((l & 1) == 0) {
-          sdst[c0 >> 1] = static_cast<uint8_t>(kh.s0);
-          sdst[c1 >> 1] = static_cast<uint8_t>(kh.s1);
-        }
+      if (loose) {
+        kh.c0 = codes_of(x, s0, off, near);
+        kh.c1 = codes_of(z, s1, off, near);
       } else {
-        *reinterpret_cast<uint2*>(dst + l * 8) = make_uint2(kh.c0, kh.c1);
-        sdst[l] = static_cast<uint8_t>(kh.s0);
+        kh.c0 = codes_exactly(x, s0);
+        kh.c1 = codes_exactly(z, s1);
       }
     }
+    if (__any_sync(kFull, near && live)) again |= 1u << (i & 31);
+    put(i, live, kh);
     // the value's block
     unpack8(v0, x);
     unpack8(v1, z);
@@ -463,6 +514,15 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const CacheParams p) {
     if (i < vn) {
       *reinterpret_cast<uint2*>(vdst + i * hstride) = make_uint2(d0, d1);
       vsdst[i * hstride] = static_cast<uint8_t>(ds);
+    }
+    if ((i & 31) == 31 || i + 1 == p.heads_per_unit) {
+#pragma unroll 1
+      for (; again; again &= again - 1) {
+        const int j = (i & ~31) + __ffs(again) - 1;
+        const bool on = j < n;
+        put(j, on, exact_row<D, LAYOUT>(p, on ? ksrc + j * D : nullptr, pos, c0, c1, turned,
+                                        on && p.k_scale ? p.k_scale[h_begin + j] : 1.f));
+      }
     }
   }
 }
