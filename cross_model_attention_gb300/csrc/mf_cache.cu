@@ -11,14 +11,14 @@
 //
 // Which code a value gets is a step, and a rounding of fp32 on the wrong side
 // of it is an error of a whole code.  Codes are therefore those of the exact
-// values, whatever the order of sums: fp32 is good to 2^-19 (with the norm; 2^-21
-// without: angle, sine and cosine 2^-22 together, products and sum 2^-24 each,
-// the norm's sum and root 2^-20) of a pair's |a| + |b|, and a row with a value that
-// near to a step (one in some hundred) is done again in twice that precision, by
-// the warp that finds it, once its other rows are done (mf_ff.cuh: 2^-43, which
-// leaves one value in 10^11 undecided).  What is exact in fp32 (values, keys that are neither normed nor
-// rotated) often lies on a step itself: its quotient is corrected by its residue,
-// which finds those exactly.
+// values, whatever the order of sums.  In units of 2^-24 of a pair's |a| + |b|, fp32
+// is good to 8 for angle, sine, cosine and the products with them, 5 for the
+// quotient and 14 for the norm's sum and root: 2^-19 with the norm and 2^-20
+// without are counted, and a row with a value that near to a step (one in a hundred)
+// is done again in twice that precision, by the warp that finds it, once its other
+// rows are done (mf_ff.cuh: 2^-43, which leaves one value in 10^11 undecided).  What
+// is exact in fp32 (values, keys that are neither normed nor rotated) often lies on
+// a step itself: its quotient is corrected by its residue, which finds those exactly.
 //
 // Bound: HBM.  Lanes as in the rotary kernel: d / 16 lanes to a head's row, each
 // with two chunks of 8 dimensions that hold both halves of its pairs, sines and
@@ -77,23 +77,44 @@ __device__ __forceinline__ uint32_t mag(float x) { return __float_as_uint(x) & 0
 constexpr uint32_t kInf = 0x7f800000u;
 constexpr uint32_t kNanScale = 0x7f;
 
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// The larger magnitude, NaN where one is.
+__device__ __forceinline__ float most(float m, float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+
 struct Scale {
   uint32_t byte;
   float sg, lo, r;  // s g in two parts and the reciprocal of it, 0 where s is 0
 };
-// Of a block with the largest magnitude `top` (its bits), off by at most `off`;
-// near: whether another scale is as likely.
-__device__ __forceinline__ Scale scale_of(uint32_t top, float off, float g, bool& near) {
+__device__ __forceinline__ Scale scale_of(uint32_t byte, float g) {
   Scale s;
-  const float g6 = 6.f * g, q = __uint_as_float(top) / g6, e = off / g6;
-  const uint32_t two = f32x2_e4m3(q - e, q + e);
-  near |= (two & 0xffu) != (two >> 8);
-  s.byte = top >= kInf ? kNanScale : two >> 8;
-  const float f = top >= kInf ? 0.f : e4m3_f32(s.byte);
+  const float f = byte == kNanScale ? 0.f : e4m3_f32(byte);
+  s.byte = byte;
   s.sg = f * g;
   s.lo = fmaf(f, g, -s.sg);
-  s.r = s.sg > 0.f ? 1.f / s.sg : 0.f;
+  s.r = s.sg > 0.f ? rcp(s.sg) : 0.f;
   return s;
+}
+// Of a block with the largest magnitude `top`, off by at most `off`; near: whether
+// another scale is as likely.  (inv_g6 = 1 / (6 g) to a unit in the last place,
+// which `off` counts.)
+__device__ __forceinline__ uint32_t scale_about(float top, float off, float inv_g6, bool& near) {
+  const uint32_t two = f32x2_e4m3(fmaf(top, inv_g6, -off * inv_g6), fmaf(top, inv_g6, off * inv_g6));
+  near |= (two & 0xffu) != (two >> 8);
+  return top < INFINITY ? two >> 8 : kNanScale;
+}
+// Where it is exact: the quotient corrected by its residue (see below).
+__device__ __forceinline__ uint32_t scale_exactly(float top, float g6, float inv_g6) {
+  const float q = top * inv_g6;
+  const uint32_t s = f32x2_e4m3(q < 1e4f ? fmaf(fmaf(-q, g6, top), inv_g6, q) : 448.f, 0.f) & 0xffu;
+  return top < INFINITY ? s : kNanScale;
 }
 // y / (s g): a product with the reciprocal, corrected by its residue, so that a
 // quotient of few bits comes out exactly.
@@ -113,16 +134,15 @@ __device__ __forceinline__ uint32_t codes_exactly(const float* y, const Scale& s
   }
   return f32x8_e2m1(t);
 }
-// Codes of 8 values that are off by at most `off` (which counts the quotient's
+// Codes of 8 values times r that are off by at most e (which counts the product's
 // own rounding); near: whether one of them has another code as likely (a zero's
 // sign says nothing).
-__device__ __forceinline__ uint32_t codes_of(const float* y, const Scale& s, float off, bool& near) {
+__device__ __forceinline__ uint32_t codes_about(const float* y, float r, float e, bool& near) {
   float lo[8], hi[8];
-  const float e = off * s.r;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    lo[i] = fmaf(y[i], s.r, -e);
-    hi[i] = fmaf(y[i], s.r, e);
+    lo[i] = fmaf(y[i], r, -e);
+    hi[i] = fmaf(y[i], r, e);
   }
   const uint32_t a = f32x8_e2m1(lo), b = f32x8_e2m1(hi);
   near |= ((a ^ b) & 0x77777777u) != 0;
@@ -157,129 +177,78 @@ __device__ __forceinline__ ff from_lane(ff a, int mask) {
   return {__shfl_xor_sync(kFull, a.h, mask), __shfl_xor_sync(kFull, a.l, mask)};
 }
 
-struct Held {
-  uint32_t c0, c1;  // codes of the two chunks
-  uint32_t s0, s1;  // the scales of their blocks
-};
-
-// One row in twice fp32's precision, by the lanes that have it (the whole warp
-// comes here; rows that are not asked for bring nullptr).
-template <int D, int LAYOUT>
-__device__ __noinline__ Held exact_row(const CacheParams& p, const __nv_bfloat16* row, long long pos, int c0, int c1,
-                                       bool turned, float g) {
-  constexpr int LPR = D / 16;
-  const int half = p.rot >> 1;
+// One row in twice fp32's precision, by a whole warp: a lane has d / 32
+// neighbouring dimensions, and the other halves of their pairs besides.
+template <int D>
+__device__ __noinline__ void exact_row(const CacheParams& p, const __nv_bfloat16* row, long long pos, float g,
+                                       uint8_t* codes, uint8_t* scales) {
+  constexpr int N = D / 32;
+  const int lane = threadIdx.x & 31, half = p.rot >> 1;
   const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(p.weight);
-  auto x_of = [&](int d) { return row ? __bfloat162float(row[d]) : 0.f; };
-  auto dim = [&](int e) { return (e < 8 ? c0 * 8 : c1 * 8 - 8) + e; };
-  ff y[16];
+  float x[N];
   uint32_t top = 0;
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    y[e] = {x_of(dim(e)), 0.f};
-    top = max(top, mag(y[e].h));
+  for (int e = 0; e < N; ++e) {
+    x[e] = __bfloat162float(row[lane * N + e]);
+    top = max(top, mag(x[e]));
   }
-#pragma unroll
-  for (int off = LPR / 2; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(kFull, top, off));
+  top = __reduce_max_sync(kFull, top);
   // rows of huge values are brought into range (what the norm gives is in it), with
   // what they are compared with
   const int ex = static_cast<int>(top >> 23) - 127;
   const float down = ex > 30 ? __int_as_float((127 - min(ex, 127) + 30) << 23) : 1.f;
   if (!p.norm) g *= down;
   ff r = {1.f, 0.f};
-  ff ss = {0.f, 0.f};
-#pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    y[e].h *= down;
-    const ff t = ff_sum(ss.h, mul_rn(y[e].h, y[e].h));  // (a square of 8 bits is exact)
-    ss = {t.h, add_rn(ss.l, t.l)};
-  }
   if (p.norm) {
+    ff ss = {0.f, 0.f};
 #pragma unroll
-    for (int off = LPR / 2; off > 0; off >>= 1) ss = ff_add(ss, from_lane(ss, off));
+    for (int e = 0; e < N; ++e) {
+      const ff t = ff_sum(ss.h, mul_rn(x[e] * down, x[e] * down));  // (a square of 8 bits is exact)
+      ss = {t.h, add_rn(ss.l, t.l)};
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) ss = ff_add(ss, from_lane(ss, off));
     const ff m = ff_add(ff{ss.h * (1.f / D), ss.l * (1.f / D)}, ff{p.eps * down * down, 0.f});
     const float r0 = rsqrtf(m.h);
     const ff q = ff_mul(m, ff_mul(ff{r0, 0.f}, r0));
     r = ff_fast_sum(r0, mul_rn(0.5f * r0, add_rn(add_rn(1.f, -q.h), -q.l)));  // one step of Newton's
     if (top >= kInf) r = {top > kInf ? NAN : 0.f, 0.f};  // (an infinity's row: 0 but for it)
   }
-  auto normed = [&](float x, int d) {
-    const float v = w ? mul_rn(x, __bfloat162float(w[d])) : x;  // (16 bits)
+  auto normed = [&](float v, int d) {
+    v *= down;
+    if (w) v = mul_rn(v, __bfloat162float(w[d]));  // (16 bits)
     return p.norm ? ff_mul(r, v) : ff{v, 0.f};
   };
-  auto turn = [&](int f, ff& cn, ff& sn) {
-    ff_sincos(static_cast<uint64_t>(pos) * p.freq[f], &sn, &cn);
-    cn = ff_mul(cn, p.gain);
-    sn = ff_mul(sn, p.gain);
-  };
+  ff y[N], most = {0.f, 0.f};
 #pragma unroll
-  for (int e = 0; e < 16; ++e) y[e] = normed(y[e].h, dim(e));
-  ff cn, sn;
-  if (LAYOUT == kHalf) {
-    if (turned) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        turn(c0 * 8 + e, cn, sn);
-        const ff a = y[e], b = y[8 + e];
-        y[e] = ff_add(ff_mul(a, cn), ff_neg(ff_mul(b, sn)));
-        y[8 + e] = ff_add(ff_mul(b, cn), ff_mul(a, sn));
-      }
+  for (int e = 0; e < N; ++e) {
+    const int d = lane * N + e;
+    y[e] = normed(x[e], d);
+    if (d < p.rot) {
+      const bool first = p.layout == 1 ? (d & 1) == 0 : d < half;
+      const int other = p.layout == 1 ? d ^ 1 : first ? d + half : d - half;
+      ff cn, sn;
+      ff_sincos(static_cast<uint64_t>(pos) * p.freq[p.layout == 1 ? d >> 1 : first ? d : other], &sn, &cn);
+      const ff t = ff_mul(normed(__bfloat162float(row[other]), other), ff_mul(sn, p.gain));
+      y[e] = ff_add(ff_mul(y[e], ff_mul(cn, p.gain)), first ? ff_neg(t) : t);
     }
-  } else if (LAYOUT == kPairs) {
-#pragma unroll
-    for (int e = 0; e < 16; e += 2) {
-      if (c0 * 8 + e >= p.rot) continue;
-      turn(c0 * 4 + (e >> 1), cn, sn);
-      const ff a = y[e], b = y[e + 1];
-      y[e] = ff_add(ff_mul(a, cn), ff_neg(ff_mul(b, sn)));
-      y[e + 1] = ff_add(ff_mul(b, cn), ff_mul(a, sn));
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const int d = c0 * 8 + e;
-      if (d >= p.rot) continue;
-      const int other = d < half ? d + half : d - half;
-      const ff z = normed(x_of(other) * down, other);
-      turn(d < half ? d : other, cn, sn);
-      const ff t = ff_mul(z, sn);
-      y[e] = ff_add(ff_mul(y[e], cn), d < half ? ff_neg(t) : t);
-    }
+    most = larger(most, !(fabsf(y[e].h) < INFINITY) ? ff{INFINITY, 0.f} : y[e].h < 0.f ? ff_neg(y[e]) : y[e]);
   }
-  ff t0 = {0.f, 0.f}, t1 = {0.f, 0.f};
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    auto size = [](ff v) {
-      if (!(fabsf(v.h) < INFINITY)) return ff{INFINITY, 0.f};
-      return v.h < 0.f ? ff_neg(v) : v;
-    };
-    t0 = larger(t0, size(y[e]));
-    t1 = larger(t1, size(y[8 + e]));
-  }
-  if (LAYOUT == kHalf) {
-    const ff o0 = from_lane(t0, 1), o1 = from_lane(t1, 1);
-    t0 = larger(t0, turned ? o0 : t1);
-    t1 = turned ? larger(t1, o1) : t0;
-  } else {
-    t0 = t1 = larger(t0, t1);
-  }
-  Held h;
-  h.s0 = scale_ff(t0, g);
-  h.s1 = scale_ff(t1, g);
-  h.c0 = h.c1 = 0;
-  const float f0 = h.s0 == kNanScale ? 0.f : e4m3_f32(h.s0), f1 = h.s1 == kNanScale ? 0.f : e4m3_f32(h.s1);
-  const float g0 = mul_rn(f0, g), g1 = mul_rn(f1, g);
+  for (int off = 1; off < 16 / N; off <<= 1) most = larger(most, from_lane(most, off));
+  const uint32_t s = scale_ff(most, g);
+  const float f = s == kNanScale ? 0.f : e4m3_f32(s), sg = mul_rn(f, g), lo = fmaf(f, g, -sg);
+  uint32_t c = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    h.c0 |= code_ff(y[e], g0, fmaf(f0, g, -g0)) << (4 * e);
-    h.c1 |= code_ff(y[8 + e], g1, fmaf(f1, g, -g1)) << (4 * e);
-  }
-  return h;
+  for (int e = 0; e < N; ++e) c |= code_ff(y[e], sg, lo) << (4 * e);
+  if (N == 4) reinterpret_cast<uint16_t*>(codes)[lane] = static_cast<uint16_t>(c);
+  else codes[lane] = static_cast<uint8_t>(c);
+  if (lane % (16 / N) == 0) scales[lane / (16 / N)] = static_cast<uint8_t>(s);
 }
 
 // ------------------------------------------------------------------ append --
 template <int D, int LAYOUT, bool FP4>
-__global__ void __launch_bounds__(kThreads) append_kernel(const CacheParams p) {
+__global__ void __launch_bounds__(kThreads, FP4 ? 4 : 5) append_kernel(const CacheParams p) {
   constexpr int LPR = D / 16;            // lanes to a row
   constexpr int kGroups = kThreads / LPR;
   constexpr int kPerWarp = 32 / LPR;     // rows to a warp
@@ -312,42 +281,70 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const CacheParams p) {
   };
   load(0);
 
+  // A lane's 16 outputs are its inputs times `own` and their partners (the pair's
+  // other half) times `other`: cosines and sines with the weights in them.
   const long long pos = p.rot ? p.positions[tok] : 0;
-  constexpr int kTurns = LAYOUT == kAny ? 16 : 8;
-  float cs[kTurns], sn[kTurns];
+  const __nv_bfloat16* weight = static_cast<const __nv_bfloat16*>(p.weight);
+  auto weight_of = [&](int d) { return weight ? __bfloat162float(weight[d]) : 1.f; };
+  auto dim = [&](int e) { return (e < 8 ? c0 * 8 : c1 * 8 - 8) + e; };
+  float own[16], other[16], heaviest = 0.f;
+  auto turn_of = [&](int f, float& sn, float& cs) {
+    const unsigned long long turn = static_cast<unsigned long long>(pos) * p.freq[f];
+    sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f, &sn, &cs);  // 2^-31
+    cs *= p.gain;
+    sn *= p.gain;
+  };
 #pragma unroll
-  for (int e = 0; e < kTurns; ++e) {
-    int f;  // the pair
-    if (LAYOUT == kHalf) {
-      f = turned ? c0 * 8 + e : -1;
-    } else if (LAYOUT == kPairs) {
-      f = c0 * 4 + e;
-      if (f >= half) f = -1;
-    } else {
+  for (int e = 0; e < 16; ++e) {
+    own[e] = weight_of(dim(e));
+    other[e] = 0.f;
+    heaviest = fmaxf(heaviest, fabsf(own[e]));
+  }
+  if (LAYOUT == kHalf) {
+    if (turned) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float sn, cs;
+        turn_of(c0 * 8 + e, sn, cs);
+        const float a = own[e], b = own[8 + e];
+        own[e] = a * cs;
+        own[8 + e] = b * cs;
+        other[e] = -b * sn;
+        other[8 + e] = a * sn;
+      }
+    }
+  } else if (LAYOUT == kPairs) {
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      if (c0 * 8 + e < p.rot) {
+        float sn, cs;
+        turn_of(c0 * 4 + (e >> 1), sn, cs);
+        const float a = own[e], b = own[e + 1];
+        own[e] = a * cs;
+        own[e + 1] = b * cs;
+        other[e] = -b * sn;
+        other[e + 1] = a * sn;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
       const int d = c0 * 8 + e;
-      f = d < half ? d : d < p.rot ? d - half : -1;
-    }
-    cs[e] = 1.f;
-    sn[e] = 0.f;
-    if (f >= 0) {
-      const unsigned long long turn = static_cast<unsigned long long>(pos) * p.freq[f];
-      sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f, &sn[e], &cs[e]);  // 2^-31
-      cs[e] *= p.gain;
-      sn[e] *= p.gain;
+      if (d < p.rot) {
+        float sn, cs;
+        const int q = d < half ? d + half : d - half;
+        turn_of(d < half ? d : q, sn, cs);
+        const float b = weight_of(q);
+        own[e] *= cs;
+        other[e] = d < half ? -b * sn : b * sn;
+        heaviest = fmaxf(heaviest, fabsf(b));
+      }
     }
   }
-  float ga[8], gb[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) ga[e] = gb[e] = 1.f;
-  if (p.weight) {
-    const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(p.weight);
-    unpack8(*reinterpret_cast<const uint4*>(w + c0 * 8), ga);
-    unpack8(*reinterpret_cast<const uint4*>(w + c1 * 8), gb);
-  }
-  // How far a key's values may be off, of |a| + |b|: all of the lane's or (kAny,
-  // kPairs) some, where the rest is taken to be off as much.
+  // Whether the lane's values are not exact in fp32, and how far they may be off,
+  // of |a| + |b| (kAny and kPairs: where only some are, the rest is taken to be so too).
   const bool loose = p.norm || (LAYOUT == kHalf ? turned : c0 * 8 < p.rot);
-  const float err = (p.norm ? 1.9073486328125e-06f : 4.76837158203125e-07f) * fmaxf(1.f, p.gain);  // 2^-19, 2^-21
+  const float err = (p.norm ? 1.9073486328125e-06f : 9.5367431640625e-07f) * fmaxf(1.f, p.gain);  // 2^-19, 2^-20
 
   // where the rows go
   uint8_t *kdst = nullptr, *ksdst = nullptr, *vdst = nullptr, *vsdst = nullptr;
@@ -371,158 +368,140 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const CacheParams p) {
     vout = static_cast<__nv_bfloat16*>(p.v) + row * p.ld_v + at;
   }
 
-  auto put = [&](int i, bool live, const Held& kh) {
-    if (!live) return;
-    uint8_t* dst = kdst + i * hstride;
-    uint8_t* sdst = ksdst + i * hstride;
-    if (turned) {
-      *reinterpret_cast<uint32_t*>(dst + c0 * 4) = kh.c0;
-      *reinterpret_cast<uint32_t*>(dst + c1 * 4) = kh.c1;
-      if ((l & 1) == 0) {
-        sdst[c0 >> 1] = static_cast<uint8_t>(kh.s0);
-        sdst[c1 >> 1] = static_cast<uint8_t>(kh.s1);
-      }
-    } else {
-      *reinterpret_cast<uint2*>(dst + l * 8) = make_uint2(kh.c0, kh.c1);
-      sdst[l] = static_cast<uint8_t>(kh.s0);
-    }
-  };
   unsigned again = 0;  // of 32 heads: those to be done more exactly
 #pragma unroll 1
   for (int i = 0; i < p.heads_per_unit; ++i) {
-    float a[8], b[8], x[8], z[8];
+    float a[16], y[16];
     unpack8(ka, a);
-    unpack8(kb, b);
+    unpack8(kb, a + 8);
     const bool live = i < n;
+    bool near = false;  // whether the row is to be done more exactly
     const uint4 v0 = va, v1 = vb;
     load(i + 1);
-    const __nv_bfloat16* row = ksrc + i * D;
-    bool near = false;  // whether the row is to be done in fp64
-    float oa[8], ob[8];  // kAny: each element's partner, normed
-    if (LAYOUT == kAny) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int da = c0 * 8 + e, db = c1 * 8 + e;
-        oa[e] = live && da < p.rot ? __bfloat162float(row[da < half ? da + half : da - half]) : 0.f;
-        ob[e] = live && db < p.rot ? __bfloat162float(row[db < half ? db + half : db - half]) : 0.f;
-      }
-    }
+    float r = 1.f;  // the norm's factor
     if (p.norm) {
       float ss = 0.f;  // (in the rotary kernel's order)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
+      for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], fmaf(a[8 + e], a[8 + e], ss));
 #pragma unroll
       for (int off = LPR / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(kFull, ss, off);
       near = !(ss < 1e36f);  // (bf16 squares pass fp32's range)
-      const float r = rsqrtf(ss * (1.f / D) + p.eps);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        a[e] *= r * ga[e];
-        b[e] *= r * gb[e];
-      }
-      if (LAYOUT == kAny) {
-        const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(p.weight);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int da = c0 * 8 + e, db = c1 * 8 + e;
-          oa[e] *= r * (w && da < p.rot ? __bfloat162float(w[da < half ? da + half : da - half]) : 1.f);
-          ob[e] *= r * (w && db < p.rot ? __bfloat162float(w[db < half ? db + half : db - half]) : 1.f);
-        }
-      }
+      r = rsqrtf(ss * (1.f / D) + p.eps);
     }
-    float off = 0.f;  // the largest |a| + |b|
-    if (LAYOUT == kHalf) {
+    float sum = 0.f;  // kAny: a bound of |a| + |b|
+    if (LAYOUT == kAny) {
+      float ma = 0.f, mb = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[e] = turned ? a[e] * cs[e] - b[e] * sn[e] : a[e];
-        z[e] = turned ? b[e] * cs[e] + a[e] * sn[e] : b[e];
-        off = fmaxf(off, fabsf(a[e]) + fabsf(b[e]));
+      for (int e = 0; e < 16; ++e) {
+        const int d = c0 * 8 + e;
+        const float b = live && d < p.rot ? __bfloat162float(ksrc[i * D + (d < half ? d + half : d - half)]) : 0.f;
+        y[e] = fmaf(b, other[e], a[e] * own[e]);
+        ma = fmaxf(ma, fabsf(a[e]));
+        mb = fmaxf(mb, fabsf(b));
       }
-    } else if (LAYOUT == kPairs) {
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        x[e] = a[e] * cs[e >> 1] - a[e + 1] * sn[e >> 1];
-        x[e + 1] = a[e + 1] * cs[e >> 1] + a[e] * sn[e >> 1];
-        z[e] = b[e] * cs[4 + (e >> 1)] - b[e + 1] * sn[4 + (e >> 1)];
-        z[e + 1] = b[e + 1] * cs[4 + (e >> 1)] + b[e] * sn[4 + (e >> 1)];
-        off = fmaxf(off, fmaxf(fabsf(a[e]) + fabsf(a[e + 1]), fabsf(b[e]) + fabsf(b[e + 1])));
-      }
+      sum = (ma + mb) * heaviest;
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int da = c0 * 8 + e, db = c1 * 8 + e;
-        x[e] = da < p.rot ? a[e] * cs[e] + (da < half ? -oa[e] : oa[e]) * sn[e] : a[e];
-        z[e] = db < p.rot ? b[e] * cs[8 + e] + (db < half ? -ob[e] : ob[e]) * sn[8 + e] : b[e];
-        off = fmaxf(off, fmaxf(fabsf(a[e]) + fabsf(oa[e]), fabsf(b[e]) + fabsf(ob[e])));
-      }
+      for (int e = 0; e < 16; ++e) y[e] = fmaf(a[LAYOUT == kHalf ? e ^ 8 : e ^ 1], other[e], a[e] * own[e]);
     }
     if (!FP4) {
       if (live) {
-        *reinterpret_cast<uint4*>(kout + i * D + c0 * 8) = pack8(x);
-        *reinterpret_cast<uint4*>(kout + i * D + c1 * 8) = pack8(z);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e] *= r;
+        *reinterpret_cast<uint4*>(kout + i * D + c0 * 8) = pack8(y);
+        *reinterpret_cast<uint4*>(kout + i * D + c1 * 8) = pack8(y + 8);
         *reinterpret_cast<uint4*>(vout + i * D + l * 16) = v0;
         *reinterpret_cast<uint4*>(vout + i * D + l * 16 + 8) = v1;
       }
       continue;
     }
     // the key's blocks: a lane's two chunks, or one chunk of each of two lanes
-    off = loose ? off * err : 0.f;
-    uint32_t t0 = 0, t1 = 0;
+    float t0 = 0.f, t1 = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      t0 = max(t0, mag(x[e]));
-      t1 = max(t1, mag(z[e]));
+    for (int e = 0; e < 8; e += 2) {
+      t0 = most(t0, y[e], y[e + 1]);
+      t1 = most(t1, y[8 + e], y[9 + e]);
     }
     if (LAYOUT == kHalf) {
-      const uint32_t o0 = __shfl_xor_sync(kFull, t0, 1), o1 = __shfl_xor_sync(kFull, t1, 1);
-      const float oo = __shfl_xor_sync(kFull, off, 1);
-      if (turned) off = fmaxf(off, oo);
-      t0 = turned ? max(t0, o0) : max(t0, t1);
-      t1 = turned ? max(t1, o1) : t0;
+      const float o0 = __shfl_xor_sync(kFull, t0, 1), o1 = __shfl_xor_sync(kFull, t1, 1);
+      t0 = most(t0, turned ? o0 : t1, 0.f);
+      t1 = turned ? most(t1, o1, 0.f) : t0;
     } else {
-      t0 = t1 = max(t0, t1);
+      t0 = t1 = most(t0, t1, 0.f);
     }
     const int h = live ? h_begin + i : 0;
-    const float gk = p.k_scale ? p.k_scale[h] : 1.f;
-    Held kh;
+    const float gk = p.k_scale ? p.k_scale[h] : 1.f, gv = p.v_scale ? p.v_scale[h] : 1.f;
     {
-      const Scale s0 = scale_of(t0, off, gk, near);
-      const Scale s1 = LAYOUT == kHalf ? scale_of(t1, off, gk, near) : s0;
-      kh.s0 = s0.byte;
-      kh.s1 = s1.byte;
+      uint32_t w0, w1, b0, b1;
+      const float g6 = 6.f * gk, inv = rcp(g6);
       if (loose) {
-        kh.c0 = codes_of(x, s0, off, near);
-        kh.c1 = codes_of(z, s1, off, near);
-      } else {
-        kh.c0 = codes_exactly(x, s0);
-        kh.c1 = codes_exactly(z, s1);
+        // (|a| + |b| is at most 2 max(|y_a|, |y_b|) of the rotated pair, both of
+        // which are in these blocks)
+        const float off = (LAYOUT == kAny ? sum : 2.f * fmaxf(t0, t1)) * r * err;
+        b0 = scale_about(t0 * r, off, inv, near);
+        const Scale s0 = scale_of(b0, gk);
+        w0 = codes_about(y, r * s0.r, off * s0.r, near);
+        b1 = b0;
+        float r1 = s0.r;
+        if (LAYOUT == kHalf) {
+          b1 = scale_about(t1 * r, off, inv, near);
+          r1 = scale_of(b1, gk).r;
+        }
+        w1 = codes_about(y + 8, r * r1, off * r1, near);
+      } else {  // (one block)
+        b0 = b1 = scale_exactly(t0, g6, inv);
+        const Scale s0 = scale_of(b0, gk);
+        w0 = codes_exactly(y, s0);
+        w1 = codes_exactly(y + 8, s0);
       }
+      if (live) {
+        uint8_t* dst = kdst + i * hstride;
+        uint8_t* sdst = ksdst + i * hstride;
+        if (turned) {
+          *reinterpret_cast<uint32_t*>(dst + c0 * 4) = w0;
+          *reinterpret_cast<uint32_t*>(dst + c1 * 4) = w1;
+          if ((l & 1) == 0) {
+            sdst[c0 >> 1] = static_cast<uint8_t>(b0);
+            sdst[c1 >> 1] = static_cast<uint8_t>(b1);
+          }
+        } else {
+          *reinterpret_cast<uint2*>(dst + l * 8) = make_uint2(w0, w1);
+          sdst[l] = static_cast<uint8_t>(b0);
+        }
+      }
+      if (near && live) again |= 1u << (i & 31);
     }
-    if (__any_sync(kFull, near && live)) again |= 1u << (i & 31);
-    put(i, live, kh);
     // the value's block
-    unpack8(v0, x);
-    unpack8(v1, z);
-    uint32_t tv = 0;
+    unpack8(v0, y);
+    unpack8(v1, y + 8);
+    float tv = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) tv = max(tv, max(mag(x[e]), mag(z[e])));
-    bool none = false;
-    const Scale sv = scale_of(tv, 0.f, p.v_scale ? p.v_scale[h] : 1.f, none);
-    const uint32_t d0 = __shfl_sync(kFull, codes_exactly(x, sv), vsrc_lane);
-    const uint32_t d1 = __shfl_sync(kFull, codes_exactly(z, sv), vsrc_lane);
+    for (int e = 0; e < 16; e += 2) tv = most(tv, y[e], y[e + 1]);
+    const float g6 = 6.f * gv;
+    const Scale sv = scale_of(scale_exactly(tv, g6, rcp(g6)), gv);
+    const uint32_t d0 = __shfl_sync(kFull, codes_exactly(y, sv), vsrc_lane);
+    const uint32_t d1 = __shfl_sync(kFull, codes_exactly(y + 8, sv), vsrc_lane);
     const uint32_t ds = __shfl_sync(kFull, sv.byte, vsrc_lane);
     if (i < vn) {
       *reinterpret_cast<uint2*>(vdst + i * hstride) = make_uint2(d0, d1);
       vsdst[i * hstride] = static_cast<uint8_t>(ds);
     }
     if ((i & 31) == 31 || i + 1 == p.heads_per_unit) {
-#pragma unroll 1
-      for (; again; again &= again - 1) {
-        const int j = (i & ~31) + __ffs(again) - 1;
-        const bool on = j < n;
-        put(j, on, exact_row<D, LAYOUT>(p, on ? ksrc + j * D : nullptr, pos, c0, c1, turned,
-                                        on && p.k_scale ? p.k_scale[h_begin + j] : 1.f));
+      __syncwarp();  // (what is written again was written by other lanes)
+      for (unsigned rest = __reduce_or_sync(kFull, again); rest; rest &= rest - 1) {
+        const int b = __ffs(rest) - 1, j = (i & ~31) + b;
+        for (unsigned rows = __ballot_sync(kFull, again >> b & 1); rows;) {
+          const int from = (__ffs(rows) - 1) / LPR * LPR;  // the row's first lane
+          rows &= ~(((1u << LPR) - 1u) << from);
+          auto of = [&](auto* x) {
+            return reinterpret_cast<decltype(x)>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(x), from));
+          };
+          const int hj = __shfl_sync(kFull, h_begin, from) + j;
+          exact_row<D>(p, of(ksrc) + j * D, __shfl_sync(kFull, pos, from), p.k_scale ? p.k_scale[hj] : 1.f,
+                       of(kdst) + j * hstride, of(ksdst) + j * hstride);
+        }
       }
+      again = 0;
     }
   }
 }
