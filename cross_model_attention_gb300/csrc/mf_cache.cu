@@ -246,9 +246,37 @@ __device__ __noinline__ void exact_row(const CacheParams& p, const __nv_bfloat16
   if (lane % (16 / N) == 0) scales[lane / (16 / N)] = static_cast<uint8_t>(s);
 }
 
+// 16 values of one block, rounded once.
+__device__ __forceinline__ Sector block_values(uint2 codes, uint32_t scale, float g) {
+  const uint32_t s = e4m3x2_f16x2(scale | scale << 8);
+  auto two = [&](uint32_t f16x2) {
+    const __half2 x = *reinterpret_cast<const __half2*>(&f16x2);
+    return pack_bf16x2(__low2float(x) * g, __high2float(x) * g);
+  };
+  return {two(mul_f16x2(e2m1x2_f16x2<0>(codes.x), s)), two(mul_f16x2(e2m1x2_f16x2<1>(codes.x), s)),
+          two(mul_f16x2(e2m1x2_f16x2<2>(codes.x), s)), two(mul_f16x2(e2m1x2_f16x2<3>(codes.x), s)),
+          two(mul_f16x2(e2m1x2_f16x2<0>(codes.y), s)), two(mul_f16x2(e2m1x2_f16x2<1>(codes.y), s)),
+          two(mul_f16x2(e2m1x2_f16x2<2>(codes.y), s)), two(mul_f16x2(e2m1x2_f16x2<3>(codes.y), s))};
+}
+// A lane's 16 values to or from memory that is 16-byte aligned: whole sectors
+// where `even` says that all the rows' lie so.
+__device__ __forceinline__ void put16(__nv_bfloat16* to, const Sector& x, bool even) {
+  if (even) {
+    st_sector(to, x);
+  } else {
+    reinterpret_cast<uint4*>(to)[0] = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
+    reinterpret_cast<uint4*>(to)[1] = make_uint4(x.w[4], x.w[5], x.w[6], x.w[7]);
+  }
+}
+__device__ __forceinline__ Sector get16(const __nv_bfloat16* from, bool even) {
+  if (even) return ld_sector(from);
+  const uint4 a = reinterpret_cast<const uint4*>(from)[0], b = reinterpret_cast<const uint4*>(from)[1];
+  return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+}
+
 // ------------------------------------------------------------------ append --
 template <int D, int LAYOUT, bool FP4>
-__global__ void __launch_bounds__(kThreads, FP4 ? 4 : 5) append_kernel(const CacheParams p) {
+__global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p) {
   constexpr int LPR = D / 16;            // lanes to a row
   constexpr int kGroups = kThreads / LPR;
   constexpr int kPerWarp = 32 / LPR;     // rows to a warp
@@ -270,16 +298,23 @@ __global__ void __launch_bounds__(kThreads, FP4 ? 4 : 5) append_kernel(const Cac
   const bool turned = LAYOUT == kHalf && l < hc;
   const int c0 = turned ? l : 2 * l, c1 = turned ? l + hc : 2 * l + 1;
 
-  uint4 ka = make_uint4(0u, 0u, 0u, 0u), kb = ka, va = ka, vb = ka;
-  auto load = [&](int i) {
+  // heads on their way ahead of the one worked on
+  constexpr int kAhead = FP4 ? 1 : 2;
+  uint4 ka[kAhead], kb[kAhead];
+  Sector vw[kAhead];
+  auto load = [&](int i, int j) {
     if (i < n) {
-      ka = *reinterpret_cast<const uint4*>(ksrc + i * D + c0 * 8);
-      kb = *reinterpret_cast<const uint4*>(ksrc + i * D + c1 * 8);
-      va = *reinterpret_cast<const uint4*>(vsrc + i * D + l * 16);
-      vb = *reinterpret_cast<const uint4*>(vsrc + i * D + l * 16 + 8);
+      ka[j] = *reinterpret_cast<const uint4*>(ksrc + i * D + c0 * 8);
+      kb[j] = *reinterpret_cast<const uint4*>(ksrc + i * D + c1 * 8);
+      vw[j] = get16(vsrc + i * D + l * 16, p.even);
     }
   };
-  load(0);
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) {
+    ka[j] = kb[j] = make_uint4(0u, 0u, 0u, 0u);
+    vw[j] = Sector{{0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u}};
+    load(j, j);
+  }
 
   // A lane's 16 outputs are its inputs times `own` and their partners (the pair's
   // other half) times `other`: cosines and sines with the weights in them.
@@ -370,14 +405,17 @@ __global__ void __launch_bounds__(kThreads, FP4 ? 4 : 5) append_kernel(const Cac
 
   unsigned again = 0;  // of 32 heads: those to be done more exactly
 #pragma unroll 1
-  for (int i = 0; i < p.heads_per_unit; ++i) {
+  for (int ib = 0; ib < p.heads_per_unit; ib += kAhead)
+#pragma unroll
+  for (int ja = 0; ja < kAhead; ++ja) {
+    const int i = ib + ja;  // (past the last: a row that is not live)
     float a[16], y[16];
-    unpack8(ka, a);
-    unpack8(kb, a + 8);
+    unpack8(ka[ja], a);
+    unpack8(kb[ja], a + 8);
     const bool live = i < n;
     bool near = false;  // whether the row is to be done more exactly
-    const uint4 v0 = va, v1 = vb;
-    load(i + 1);
+    const Sector v = vw[ja];
+    load(i + kAhead, ja);
     float r = 1.f;  // the norm's factor
     if (p.norm) {
       float ss = 0.f;  // (in the rotary kernel's order)
@@ -410,8 +448,7 @@ __global__ void __launch_bounds__(kThreads, FP4 ? 4 : 5) append_kernel(const Cac
         for (int e = 0; e < 16; ++e) y[e] *= r;
         *reinterpret_cast<uint4*>(kout + i * D + c0 * 8) = pack8(y);
         *reinterpret_cast<uint4*>(kout + i * D + c1 * 8) = pack8(y + 8);
-        *reinterpret_cast<uint4*>(vout + i * D + l * 16) = v0;
-        *reinterpret_cast<uint4*>(vout + i * D + l * 16 + 8) = v1;
+        put16(vout + i * D + l * 16, v, p.even);
       }
       continue;
     }
@@ -472,8 +509,8 @@ __global__ void __launch_bounds__(kThreads, FP4 ? 4 : 5) append_kernel(const Cac
       if (near && live) again |= 1u << (i & 31);
     }
     // the value's block
-    unpack8(v0, y);
-    unpack8(v1, y + 8);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[2 * e] = bf16lo(v.w[e]), y[2 * e + 1] = bf16hi(v.w[e]);
     float tv = 0.f;
 #pragma unroll
     for (int e = 0; e < 16; e += 2) tv = most(tv, y[e], y[e + 1]);
@@ -507,19 +544,6 @@ __global__ void __launch_bounds__(kThreads, FP4 ? 4 : 5) append_kernel(const Cac
 }
 
 // -------------------------------------------------------------------- read --
-// 16 values of one block, rounded once.
-__device__ __forceinline__ void block_values(uint2 codes, uint32_t scale, float g, uint4* out) {
-  const uint32_t s = e4m3x2_f16x2(scale | scale << 8);
-  auto two = [&](uint32_t f16x2) {
-    const __half2 x = *reinterpret_cast<const __half2*>(&f16x2);
-    return pack_bf16x2(__low2float(x) * g, __high2float(x) * g);
-  };
-  out[0] = make_uint4(two(mul_f16x2(e2m1x2_f16x2<0>(codes.x), s)), two(mul_f16x2(e2m1x2_f16x2<1>(codes.x), s)),
-                      two(mul_f16x2(e2m1x2_f16x2<2>(codes.x), s)), two(mul_f16x2(e2m1x2_f16x2<3>(codes.x), s)));
-  out[1] = make_uint4(two(mul_f16x2(e2m1x2_f16x2<0>(codes.y), s)), two(mul_f16x2(e2m1x2_f16x2<1>(codes.y), s)),
-                      two(mul_f16x2(e2m1x2_f16x2<2>(codes.y), s)), two(mul_f16x2(e2m1x2_f16x2<3>(codes.y), s)));
-}
-
 template <int D, bool FP4>
 __global__ void __launch_bounds__(kThreads) read_kernel(const CacheParams p) {
   constexpr int LPR = D / 16;
@@ -540,15 +564,21 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const CacheParams p) {
     const __nv_bfloat16* ks = static_cast<const __nv_bfloat16*>(p.k) + row * p.ld_k + at + l * 16;
     const __nv_bfloat16* vs = static_cast<const __nv_bfloat16*>(p.v) + row * p.ld_v + at + l * 16;
     __nv_bfloat16* vout = static_cast<__nv_bfloat16*>(p.v_out) + tok * p.ld_vin + at + l * 16;
-#pragma unroll 2
-    for (int i = 0; i < n; ++i) {
-      const uint4* k4 = reinterpret_cast<const uint4*>(ks + i * D);
-      const uint4* v4 = reinterpret_cast<const uint4*>(vs + i * D);
-      const uint4 a = k4[0], b = k4[1], c = v4[0], d = v4[1];
-      uint4* ko = reinterpret_cast<uint4*>(kout + i * D);
-      uint4* vo = reinterpret_cast<uint4*>(vout + i * D);
-      ko[0] = a, ko[1] = b;
-      vo[0] = c, vo[1] = d;
+    constexpr int kAhead = 4;
+    for (int i0 = 0; i0 < n; i0 += kAhead) {
+      Sector a[kAhead], b[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (i0 + j < n) {
+          a[j] = get16(ks + (i0 + j) * D, p.even);
+          b[j] = get16(vs + (i0 + j) * D, p.even);
+        }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (i0 + j < n) {
+          put16(kout + (i0 + j) * D, a[j], p.even);
+          put16(vout + (i0 + j) * D, b[j], p.even);
+        }
     }
     return;
   }
@@ -591,17 +621,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const CacheParams p) {
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const int i = i0 + j;
-      uint4 w[2];
-      if (i < n) {
-        block_values(kw[j], kq[j], gk[j], w);
-        uint4* to = reinterpret_cast<uint4*>(kout + i * D);
-        to[0] = w[0], to[1] = w[1];
-      }
-      if (i < vn) {
-        block_values(vw[j], vq[j], gv[j], w);
-        uint4* to = reinterpret_cast<uint4*>(vout + i * D);
-        to[0] = w[0], to[1] = w[1];
-      }
+      if (i < n) put16(kout + i * D, block_values(kw[j], kq[j], gk[j]), p.even);
+      if (i < vn) put16(vout + i * D, block_values(vw[j], vq[j], gv[j]), p.even);
     }
   }
 }
@@ -627,6 +648,8 @@ cudaError_t spread(CacheParams p, long long T, int D, F&& go) {
   return cudaGetLastError();
 }
 
+bool even32(const void* a, long long ld) { return !a || ((reinterpret_cast<uintptr_t>(a) & 31) == 0 && ld % 16 == 0); }
+
 template <int D, bool FP4>
 cudaError_t append_t(const CacheParams& p, long long T, cudaStream_t s) {
   return spread(p, T, D, [&](const CacheParams& q, unsigned grid) {
@@ -642,13 +665,17 @@ cudaError_t read_t(const CacheParams& p, long long T, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_cache_append(const CacheParams& p, long long T, int d, cudaStream_t s) {
+cudaError_t launch_cache_append(const CacheParams& c, long long T, int d, cudaStream_t s) {
   if (T <= 0) return cudaSuccess;
+  CacheParams p = c;
+  p.even = even32(p.v_in, p.ld_vin) && even32(p.v, p.ld_v);
   if (p.pages) return d == 128 ? append_t<128, true>(p, T, s) : append_t<64, true>(p, T, s);
   return d == 128 ? append_t<128, false>(p, T, s) : append_t<64, false>(p, T, s);
 }
-cudaError_t launch_cache_read(const CacheParams& p, long long T, int d, cudaStream_t s) {
+cudaError_t launch_cache_read(const CacheParams& c, long long T, int d, cudaStream_t s) {
   if (T <= 0) return cudaSuccess;
+  CacheParams p = c;
+  p.even = even32(p.k_out, p.ld_kin) && even32(p.v_out, p.ld_vin) && even32(p.k, p.ld_k) && even32(p.v, p.ld_v);
   if (p.pages) return d == 128 ? read_t<128, true>(p, T, s) : read_t<64, true>(p, T, s);
   return d == 128 ? read_t<128, false>(p, T, s) : read_t<64, false>(p, T, s);
 }

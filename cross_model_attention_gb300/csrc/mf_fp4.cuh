@@ -70,4 +70,21 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// 32 bytes at a 32-byte aligned address: a lane's whole sector.
+struct Sector {
+  uint32_t w[8];
+};
+__device__ __forceinline__ void st_sector(void* p, const Sector& s) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(s.w[0]), "r"(s.w[1]), "r"(s.w[2]),
+               "r"(s.w[3]), "r"(s.w[4]), "r"(s.w[5]), "r"(s.w[6]), "r"(s.w[7])
+               : "memory");
+}
+__device__ __forceinline__ Sector ld_sector(const void* p) {
+  Sector s;
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(s.w[0]), "=r"(s.w[1]), "=r"(s.w[2]), "=r"(s.w[3]), "=r"(s.w[4]), "=r"(s.w[5]), "=r"(s.w[6]), "=r"(s.w[7])
+               : "l"(p));
+  return s;
+}
+
 }  // namespace mf

@@ -290,6 +290,7 @@ struct CacheParams {
   // set by the launcher
   long long n_units;
   int heads_per_unit, shares;
+  int even;                    // whether rows lie at multiples of 32 bytes
 };
 cudaError_t launch_cache_append(const CacheParams& p, long long T, int d, cudaStream_t s);
 cudaError_t launch_cache_read(const CacheParams& p, long long T, int d, cudaStream_t s);
@@ -318,6 +319,7 @@ struct PagedParams {
   float2* part_ml;             // [2 grid + warps][rows]
   int4* cuts;                  // [2 grid]
   int rows;                    // of a partial result
+  float inv_grid;              // set by the launcher: 1 / CTAs, rounded up
 };
 // What a launch takes: CTAs, partial results and rows of one.
 void paged_shape(int Lq, int G, int sms, int* grid, int* parts, int* rows);

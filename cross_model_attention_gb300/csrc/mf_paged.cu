@@ -31,6 +31,7 @@
 // memory, filled by cp.async, and waits for no other warp until the end.  Pieces
 // of a pair that warps of a CTA share are joined in shared memory, those that
 // CTAs share through the workspace, by a second kernel; both in a fixed order.
+#include <cmath>
 #include <cstdint>
 #include <type_traits>
 
@@ -54,19 +55,22 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // D dimensions, NT times 8 rows to a unit of work.
 template <int D, int NT>
 struct Cfg {
-  static constexpr int W = NT == 1 ? 16 : 8;            // warps
-  static constexpr int NB = D == 128 && NT == 1 ? 2 : 4;  // 16-key blocks of a tile
+  static constexpr int W = NT == 1 ? 16 : NT == 2 ? 12 : 8;  // warps
+  static constexpr int NB = D == 128 ? 2 : 4;            // 16-key blocks of a tile
   static constexpr int TK = NB * 16;
   static constexpr int kPiece = fp4_piece(D);
   static constexpr int kStage = NB * kPiece;
-  static constexpr int kRing = kRingBytes / W & ~15;
+  static constexpr bool kQShared = NT > 1;               // q's operands in shared memory, not in registers
+  static constexpr int kQBytes = kQShared ? D / 16 * NT * 256 : 0;  // of a warp
+  static constexpr int kRing = (kRingBytes / W - kQBytes) & ~15;
   static constexpr int S = kRing / kStage;
   static constexpr int R = 8 * NT;
   static constexpr int kThreads = 32 * W;
   static constexpr int kQueue = S < 4 ? 4 : 8;           // parts of a warp: one in work, those in the ring, the next
-  static constexpr int kPrefix = kRingBytes;             // [threads + 2] long long
-  static constexpr int kSums = kPrefix + 8 * (kThreads + 2);  // [W] long long
-  static constexpr int kLens = kSums + 8 * W;            // [kLensHere]
+  static constexpr int kQ = W * kRing;
+  static constexpr int kPrefix = kQ + W * kQBytes;       // [threads + 4] int
+  static constexpr int kSums = kPrefix + 4 * (kThreads + 4);  // [16] int
+  static constexpr int kLens = kSums + 64;               // [kLensHere]
   static constexpr int kParts = kLens + 4 * kLensHere;
   static constexpr int kPieces = kParts + 32 * W * kQueue;
   static constexpr int kWalk = kPieces + 16 * 2 * W;
@@ -148,9 +152,8 @@ __device__ __forceinline__ Tiles tiles_of(const PagedParams& p, int len) {
   t.nt = t.ta + (t.len + TK - 1) / TK - t.tb;
   return t;
 }
-__device__ __forceinline__ long long line_of(const Tiles& t, int units) {
-  return t.nt > 0 ? static_cast<long long>(units) * (kCost + t.nt) : 0;
-}
+// The line of one of a request's units.
+__device__ __forceinline__ int line_of(const Tiles& t) { return t.nt > 0 ? kCost + t.nt : 0; }
 
 // Where row `row` of unit u of request r is in q and o, its head; false past the last row.
 struct Row {
@@ -192,7 +195,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
   constexpr int W = C::W, NB = C::NB, TK = C::TK, S = C::S, T = C::kThreads;
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  long long* prefix = reinterpret_cast<long long*>(smem + C::kPrefix);
+  int* prefix = reinterpret_cast<int*>(smem + C::kPrefix);
   int* lens_s = reinterpret_cast<int*>(smem + C::kLens);
   Part* parts = reinterpret_cast<Part*>(smem + C::kParts) + warp * C::kQueue;
   Piece* pieces = reinterpret_cast<Piece*>(smem + C::kPieces);
@@ -201,39 +204,43 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
   // ---- the lines: a thread sums those of consecutive requests
   const int share = (p.n + T - 1) / T;
   const int groups = (p.Lq * p.G + C::R - 1) / C::R, units = p.H_kv * groups;
+  int all;  // the lines of one unit of every request
   {
-    long long* sums = reinterpret_cast<long long*>(smem + C::kSums);
-    long long sum = 0;
-    for (int j = 0; j < share; ++j) {
-      const int r = threadIdx.x * share + j;
-      if (r >= p.n) break;
-      const int len = p.lens[r];
-      if (p.n <= kLensHere) lens_s[r] = len;
-      sum += line_of(tiles_of<TK>(p, len), units);
-    }
-    long long inc = sum;
+    int* sums = reinterpret_cast<int*>(smem + C::kSums);
+    const int busy = (p.n + 32 * share - 1) / (32 * share);  // warps with a request
+    int inc = 0;
+    if (warp < busy) {
+      for (int j = 0; j < share; ++j) {
+        const int r = threadIdx.x * share + j;
+        if (r >= p.n) break;
+        const int len = p.lens[r];
+        if (p.n <= kLensHere) lens_s[r] = len;
+        inc += line_of(tiles_of<TK>(p, len));
+      }
+      __syncwarp();
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(kFull, inc, o);
-      if (lane >= o) inc += y;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, inc, o);
+        if (lane >= o) inc += y;
+      }
+      if (lane == 31) sums[warp] = inc;
     }
-    if (lane == 31) sums[warp] = inc;
     if (lane < 2) pieces[2 * warp + lane].flags = 0;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < W; ++w) inc += w < warp ? sums[w] : 0;
-    prefix[threadIdx.x + 1] = inc;
+    const int of_warp = lane < busy ? sums[lane] : 0;
+    all = __reduce_add_sync(kFull, of_warp);
+    prefix[threadIdx.x + 1] = inc + __reduce_add_sync(kFull, lane < warp ? of_warp : 0);
     if (threadIdx.x == 0) prefix[0] = 0;
     __syncthreads();
   }
   auto len_of = [&](int r) { return p.n <= kLensHere ? lens_s[r] : p.lens[r]; };
-  const long long total = prefix[T];
-  const int per = static_cast<int>(max(static_cast<long long>(kMinSpan), (total + gridDim.x - 1) / gridDim.x));
+  const long long total = static_cast<long long>(all) * units;
+  // (rounded up: all spans together are never short)
+  const int per = max(kMinSpan, __float2int_ru(__fmul_ru(__ll2float_ru(total), p.inv_grid)));
   // this CTA's span, from here on in places from its start, and this warp's
   const long long cta0 = min(total, static_cast<long long>(per) * blockIdx.x);
   const int cta1 = static_cast<int>(min(total - cta0, static_cast<long long>(per)));
-  const int f0 = static_cast<int>(static_cast<long long>(cta1) * warp / W);
-  const int f1 = static_cast<int>(static_cast<long long>(cta1) * (warp + 1) / W);
+  const int f0 = cta1 / W * warp + cta1 % W * warp / W, f1 = cta1 / W * (warp + 1) + cta1 % W * (warp + 1) / W;
 
   // ---- the walk over this warp's span
   int wr = p.n, wu = 0, at = 0;  // request and unit of the line that begins at `at`
@@ -242,22 +249,23 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
     // the thread whose requests' lines f0 lies in, then the request
     constexpr int kStep = T / 32;
     const long long f = cta0 + f0;
-    const int hi = 31 - __clz(__ballot_sync(kFull, prefix[lane * kStep] <= f));
-    const int j = hi * kStep + 31 - __clz(__ballot_sync(kFull, lane < kStep && prefix[hi * kStep + min(lane, kStep - 1)] <= f));
-    long long line = prefix[j];
+    auto begins = [&](int line) { return static_cast<long long>(line) * units; };
+    const int hi = 31 - __clz(__ballot_sync(kFull, begins(prefix[lane * kStep]) <= f));
+    const int j = hi * kStep + 31 - __clz(__ballot_sync(kFull, lane < kStep && begins(prefix[hi * kStep + min(lane, kStep - 1)]) <= f));
+    int line = prefix[j];
     wr = j;
     if (share > 1) {
       wr = p.n;
       for (int r0 = j * share; r0 < p.n; r0 += 32) {
         const int r = r0 + lane;
-        const long long mine = line_of(tiles_of<TK>(p, r < p.n ? len_of(r) : 0), units);
-        long long inc = mine;
+        const int mine = line_of(tiles_of<TK>(p, r < p.n ? len_of(r) : 0));
+        int inc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const long long y = __shfl_up_sync(kFull, inc, o);
+          const int y = __shfl_up_sync(kFull, inc, o);
           if (lane >= o) inc += y;
         }
-        const unsigned hit = __ballot_sync(kFull, line + inc > f);
+        const unsigned hit = __ballot_sync(kFull, begins(line + inc) > f);
         if (hit) {
           const int k = __ffs(hit) - 1;
           wr = r0 + k;
@@ -270,9 +278,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
     if (wr < p.n) {
       wt = tiles_of<TK>(p, len_of(wr));
       // (a request's lines may be 2^31 and more long, a unit's are not)
-      const long long in = f - line;
+      const long long in = f - begins(line);
       wu = in < 0x7fffffff ? static_cast<int>(in) / (kCost + wt.nt) : static_cast<int>(in / (kCost + wt.nt));
-      at = static_cast<int>(line + static_cast<long long>(wu) * (kCost + wt.nt) - cta0);
+      at = static_cast<int>(begins(line) + static_cast<long long>(wu) * (kCost + wt.nt) - cta0);
     }
   }
   Walk* walk = reinterpret_cast<Walk*>(smem + C::kWalk) + warp;
@@ -334,24 +342,28 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
   };
 
   // ---- q of a part: loads, then fp16
-  uint4 qw[NT][D / 32];
+  constexpr int NQ = C::kQShared ? 1 : NT;
+  uint4 qw[NQ][D / 32];
   float kscale = 1.f, vscale = 1.f;
+  auto load_rows = [&](int r, int h, int rg, int nt, uint4* w) {
+    int tt, gg;
+    const bool ok = split(rg * C::R + nt * 8 + g, tt, gg);
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (static_cast<long long>(r) * p.Lq + tt) * p.ld_q +
+                               (h * p.G + gg) * D + t * (D / 4);
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      w[c] = make_uint4(0u, 0u, 0u, 0u);
+      if (ok) w[c] = reinterpret_cast<const uint4*>(src)[c];
+    }
+  };
   auto load_q = [&](int r, int u) {
     int rg;
     const int h = head_of(u, rg);
     if (p.k_scale) kscale = p.k_scale[h];
     if (p.v_scale) vscale = p.v_scale[h];
+    if (!C::kQShared) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      int tt, gg;
-      const bool ok = split(rg * C::R + nt * 8 + g, tt, gg);
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (static_cast<long long>(r) * p.Lq + tt) * p.ld_q +
-                                 (h * p.G + gg) * D + t * (D / 4);
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        qw[nt][c] = make_uint4(0u, 0u, 0u, 0u);
-        if (ok) qw[nt][c] = reinterpret_cast<const uint4*>(src)[c];
-      }
+      for (int nt = 0; nt < NQ; ++nt) load_rows(r, h, rg, nt, qw[nt]);
     }
   };
 
@@ -437,17 +449,23 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
     if (!q_here) load_q(d.r, d.u);
     q_here = false;
     const float vs = vscale;
-    uint32_t qf[NT][D / 16][2];
+    uint32_t qf[NQ][D / 16][2];
+    uint2* qs = reinterpret_cast<uint2*>(smem + C::kQ + warp * C::kQBytes) + lane;  // [D / 16][NT][32], where they are shared
     float acc[D / 16][NT][4], m[NT][2], l[NT][2], coef[NT][2];
+    int rg0;
+    const int h0 = head_of(d.u, rg0);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      uint4* w = qw[C::kQShared ? 0 : nt];
+      if (C::kQShared) load_rows(d.r, h0, rg0, nt, w);
       uint32_t top = 0;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
-        const uint32_t v[4] = {qw[nt][c].x, qw[nt][c].y, qw[nt][c].z, qw[nt][c].w};
+        const uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top = max(top, max(v[e] & 0x7fffu, v[e] >> 16 & 0x7fffu));
+        for (int e = 0; e < 4; ++e) top = __vmaxu2(top, v[e] & 0x7fff7fffu);
       }
+      top = max(top & 0xffffu, top >> 16);
       top = max(top, __shfl_xor_sync(kFull, top, 1));
       top = max(top, __shfl_xor_sync(kFull, top, 2));
       // 2^e brings the row's largest to [2^14, 2^15)
@@ -460,9 +478,17 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
       if (!fine) c = NAN;
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) {
-        const uint32_t v[4] = {qw[nt][k].x, qw[nt][k].y, qw[nt][k].z, qw[nt][k].w};
+        const uint32_t v[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+        uint32_t f[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) qf[nt][2 * k + (j >> 1)][j & 1] = pack_f16x2(bf16lo(v[j]) * up, bf16hi(v[j]) * up);
+        for (int j = 0; j < 4; ++j) f[j] = pack_f16x2(bf16lo(v[j]) * up, bf16hi(v[j]) * up);
+        if (C::kQShared) {
+          qs[(2 * k * NT + nt) * 32] = make_uint2(f[0], f[1]);
+          qs[((2 * k + 1) * NT + nt) * 32] = make_uint2(f[2], f[3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) qf[C::kQShared ? 0 : nt][2 * k + (j >> 1)][j & 1] = f[j];
+        }
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -491,6 +517,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
 
       // S = K q^T: rows are keys, columns the unit's rows
       float x[NB][NT][4];
+      uint32_t k0[NB][D / 32], k1[NB][D / 32];  // a lane's codes of keys g and g + 8
+      uint32_t s0[NB], s1[NB];                  // their scales, one or two
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
 #pragma unroll
@@ -498,36 +526,51 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[b][nt][e] = 0.f;
         const uint8_t* base = st + b * C::kPiece;
-        uint32_t k0[D / 32], k1[D / 32];  // a lane's codes of keys g and g + 8
-        uint32_t s0, s1;                  // their scales, one or two
         if (D == 128) {
           const uint4 a = *reinterpret_cast<const uint4*>(base + g * 64 + t * 16);
           const uint4 c = *reinterpret_cast<const uint4*>(base + (g + 8) * 64 + t * 16);
-          k0[0] = a.x, k0[1] = a.y, k0[D / 32 - 2] = a.z, k0[D / 32 - 1] = a.w;
-          k1[0] = c.x, k1[1] = c.y, k1[D / 32 - 2] = c.z, k1[D / 32 - 1] = c.w;
-          s0 = e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(base + 16 * D + g * 8 + t * 2));
-          s1 = e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(base + 16 * D + (g + 8) * 8 + t * 2));
+          k0[b][0] = a.x, k0[b][1] = a.y, k0[b][D / 32 - 2] = a.z, k0[b][D / 32 - 1] = a.w;
+          k1[b][0] = c.x, k1[b][1] = c.y, k1[b][D / 32 - 2] = c.z, k1[b][D / 32 - 1] = c.w;
+          s0[b] = e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(base + 16 * D + g * 8 + t * 2));
+          s1[b] = e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(base + 16 * D + (g + 8) * 8 + t * 2));
         } else {
           const uint2 a = *reinterpret_cast<const uint2*>(base + g * 32 + t * 8);
           const uint2 c = *reinterpret_cast<const uint2*>(base + (g + 8) * 32 + t * 8);
-          k0[0] = a.x, k0[1] = a.y;
-          k1[0] = c.x, k1[1] = c.y;
-          s0 = e4m3x2_f16x2(base[16 * D + g * 4 + t]);
-          s1 = e4m3x2_f16x2(base[16 * D + (g + 8) * 4 + t]);
+          k0[b][0] = a.x, k0[b][1] = a.y;
+          k1[b][0] = c.x, k1[b][1] = c.y;
+          s0[b] = e4m3x2_f16x2(base[16 * D + g * 4 + t]);
+          s1[b] = e4m3x2_f16x2(base[16 * D + (g + 8) * 4 + t]);
         }
+      }
+      // (blocks inside words where q comes from shared memory, which is then read once
+      // a tile; words inside blocks where it does not, for fewer registers)
+      constexpr int kOuter = C::kQShared ? D / 32 : NB, kInner = C::kQShared ? NB : D / 32;
 #pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
-          const bool second = D == 128 && w >= 2;  // of the lane's two blocks of 16
-          const uint32_t fa = __byte_perm(s0, 0, second ? 0x3232 : 0x1010);
-          const uint32_t fb = __byte_perm(s1, 0, second ? 0x3232 : 0x1010);
-          const uint32_t a0 = mul_f16x2(e2m1x2_f16x2<0>(k0[w]), fa), a1 = mul_f16x2(e2m1x2_f16x2<0>(k1[w]), fb);
-          const uint32_t a2 = mul_f16x2(e2m1x2_f16x2<1>(k0[w]), fa), a3 = mul_f16x2(e2m1x2_f16x2<1>(k1[w]), fb);
-          const uint32_t c0 = mul_f16x2(e2m1x2_f16x2<2>(k0[w]), fa), c1 = mul_f16x2(e2m1x2_f16x2<2>(k1[w]), fb);
-          const uint32_t c2 = mul_f16x2(e2m1x2_f16x2<3>(k0[w]), fa), c3 = mul_f16x2(e2m1x2_f16x2<3>(k1[w]), fb);
+      for (int io = 0; io < kOuter; ++io) {
+        uint2 qa[C::kQShared ? NT : 1], qb[C::kQShared ? NT : 1];
+        if (C::kQShared) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma(x[b][nt], a0, a1, a2, a3, qf[nt][2 * w][0], qf[nt][2 * w][1]);
-            mma(x[b][nt], c0, c1, c2, c3, qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
+            qa[C::kQShared ? nt : 0] = qs[(2 * io * NT + nt) * 32];
+            qb[C::kQShared ? nt : 0] = qs[((2 * io + 1) * NT + nt) * 32];
+          }
+        }
+#pragma unroll
+        for (int ii = 0; ii < kInner; ++ii) {
+          const int w = C::kQShared ? io : ii, b = C::kQShared ? ii : io;
+          const bool second = D == 128 && w >= 2;  // of the lane's two blocks of 16
+          const uint32_t fa = __byte_perm(s0[b], 0, second ? 0x3232 : 0x1010);
+          const uint32_t fb = __byte_perm(s1[b], 0, second ? 0x3232 : 0x1010);
+          const uint32_t a0 = mul_f16x2(e2m1x2_f16x2<0>(k0[b][w]), fa), a1 = mul_f16x2(e2m1x2_f16x2<0>(k1[b][w]), fb);
+          const uint32_t a2 = mul_f16x2(e2m1x2_f16x2<1>(k0[b][w]), fa), a3 = mul_f16x2(e2m1x2_f16x2<1>(k1[b][w]), fb);
+          const uint32_t c0 = mul_f16x2(e2m1x2_f16x2<2>(k0[b][w]), fa), c1 = mul_f16x2(e2m1x2_f16x2<2>(k1[b][w]), fb);
+          const uint32_t c2 = mul_f16x2(e2m1x2_f16x2<3>(k0[b][w]), fa), c3 = mul_f16x2(e2m1x2_f16x2<3>(k1[b][w]), fb);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint2 q0 = C::kQShared ? qa[C::kQShared ? nt : 0] : make_uint2(qf[C::kQShared ? 0 : nt][2 * w][0], qf[C::kQShared ? 0 : nt][2 * w][1]);
+            const uint2 q1 = C::kQShared ? qb[C::kQShared ? nt : 0] : make_uint2(qf[C::kQShared ? 0 : nt][2 * w + 1][0], qf[C::kQShared ? 0 : nt][2 * w + 1][1]);
+            mma(x[b][nt], a0, a1, a2, a3, q0.x, q0.y);
+            mma(x[b][nt], c0, c1, c2, c3, q1.x, q1.y);
           }
         }
       }
@@ -872,7 +915,7 @@ __global__ void __launch_bounds__(32) join_kernel(const PagedParams p) {
 }
 
 template <int D, int NT>
-cudaError_t launch_t(const PagedParams& p, cudaStream_t s) {
+cudaError_t launch_t(PagedParams p, cudaStream_t s) {
   using C = Cfg<D, NT>;
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = once_per_device(done, [] {
@@ -881,6 +924,7 @@ cudaError_t launch_t(const PagedParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   int sms = 0;
   if ((e = sm_count(&sms)) != cudaSuccess) return e;
+  p.inv_grid = std::nextafterf(1.f / sms, 1.f);
   paged_kernel<D, NT><<<sms, C::kThreads, C::kBytes, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -897,17 +941,26 @@ cudaError_t launch_t(const PagedParams& p, cudaStream_t s) {
 
 }  // namespace
 
+// Rows to a unit: 8 where there are no more, 16 where there are no more than
+// that, else 32 and as many units to a head as it takes.
+namespace {
+int row_tiles(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+}  // namespace
+
 void paged_shape(int Lq, int G, int sms, int* grid, int* parts, int* rows) {
-  const int nt = Lq * G > 8 ? 2 : 1;
+  const int nt = row_tiles(Lq * G);
   *grid = sms;
-  *parts = sms * (2 + (nt == 1 ? 16 : 8));
+  *parts = sms * (2 + (nt == 1 ? Cfg<128, 1>::W : nt == 2 ? Cfg<128, 2>::W : Cfg<128, 4>::W));
   *rows = Lq * G < 8 * nt ? Lq * G : 8 * nt;
 }
 
 cudaError_t launch_paged(const PagedParams& p, int d, cudaStream_t s) {
   if (p.n <= 0) return cudaSuccess;
-  if (p.Lq * p.G > 8) return d == 128 ? launch_t<128, 2>(p, s) : launch_t<64, 2>(p, s);
-  return d == 128 ? launch_t<128, 1>(p, s) : launch_t<64, 1>(p, s);
+  switch (row_tiles(p.Lq * p.G)) {
+    case 1: return d == 128 ? launch_t<128, 1>(p, s) : launch_t<64, 1>(p, s);
+    case 2: return d == 128 ? launch_t<128, 2>(p, s) : launch_t<64, 2>(p, s);
+    default: return d == 128 ? launch_t<128, 4>(p, s) : launch_t<64, 4>(p, s);
+  }
 }
 
 }  // namespace mf
