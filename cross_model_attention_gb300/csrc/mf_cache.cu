@@ -12,8 +12,8 @@
 // Which code a value gets is a step, and a rounding of fp32 on the wrong side
 // of it is an error of a whole code.  Codes are therefore those of the exact
 // values, whatever the order of sums.  In units of 2^-24 of a pair's |a| + |b|, fp32
-// is good to 8 for angle, sine, cosine and the products with them, 5 for the
-// quotient and 14 for the norm's sum and root: 2^-19 with the norm and 2^-20
+// is good to 7 for angle, sine, cosine and the products with them, 5 for the
+// quotient and 7.1 for the norm's sum and root: 20 with the norm and 16
 // without are counted, and a row with a value that near to a step (one in a hundred)
 // is done again in twice that precision, by the warp that finds it, once its other
 // rows are done (mf_ff.cuh: 2^-43, which leaves one value in 10^11 undecided).  What
@@ -66,6 +66,11 @@ __device__ __forceinline__ bool place_of(const CacheParams& p, long long t, long
   page = p.table[s * p.ld_table + i];
   return page >= 0 && page < p.n_pages;
 }
+// The token of a unit (of shares of a token's heads).
+__device__ __forceinline__ long long token_of(const CacheParams& p, long long unit) {
+  if (p.shares == 1) return unit;
+  return p.n_units <= 0x7fffffff ? static_cast<int>(unit) / p.shares : unit / p.shares;
+}
 template <int D>
 __device__ __forceinline__ uint8_t* piece_of(const CacheParams& p, long long page, int o, int h) {
   return p.pages + ((page * p.H + h) * (p.ps / kFp4Block) + o / kFp4Block) * fp4_piece(D);
@@ -79,7 +84,7 @@ constexpr uint32_t kNanScale = 0x7f;
 
 __device__ __forceinline__ float rcp(float x) {
   float r;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 // The larger magnitude, NaN where one is.
@@ -129,8 +134,14 @@ __device__ __forceinline__ uint32_t codes_exactly(const float* y, const Scale& s
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[i] = fabsf(y[i] * s.r) < 8.f ? quotient(y[i], s) : y[i] * s.r;
   } else {
+    const float2 r = make_float2(s.r, s.r), sg = make_float2(-s.sg, -s.sg), lo = make_float2(-s.lo, -s.lo);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = quotient(y[i], s);
+    for (int i = 0; i < 8; i += 2) {
+      const float2 v = make_float2(y[i], y[i + 1]), q = fmul2(v, r);
+      const float2 c = ffma2(ffma2(q, lo, ffma2(q, sg, v)), r, q);
+      t[i] = c.x;
+      t[i + 1] = c.y;
+    }
   }
   return f32x8_e2m1(t);
 }
@@ -140,9 +151,11 @@ __device__ __forceinline__ uint32_t codes_exactly(const float* y, const Scale& s
 __device__ __forceinline__ uint32_t codes_about(const float* y, float r, float e, bool& near) {
   float lo[8], hi[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo[i] = fmaf(y[i], r, -e);
-    hi[i] = fmaf(y[i], r, e);
+  for (int i = 0; i < 8; i += 2) {
+    const float2 v = make_float2(y[i], y[i + 1]), f = make_float2(r, r);
+    const float2 a = ffma2(v, f, make_float2(-e, -e)), b = ffma2(v, f, make_float2(e, e));
+    lo[i] = a.x, lo[i + 1] = a.y;
+    hi[i] = b.x, hi[i + 1] = b.y;
   }
   const uint32_t a = f32x8_e2m1(lo), b = f32x8_e2m1(hi);
   near |= ((a ^ b) & 0x77777777u) != 0;
@@ -284,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
   const int l = threadIdx.x % LPR;
   const long long unit = static_cast<long long>(blockIdx.x) * kGroups + threadIdx.x / LPR;
   // (a group without a token stores nothing, but joins the shuffles)
-  const long long tok = unit < p.n_units ? unit / p.shares : 0;
+  const long long tok = unit < p.n_units ? token_of(p, unit) : 0;
   const int h_begin = static_cast<int>(unit - tok * p.shares) * p.heads_per_unit;
   long long page = 0;
   int o = 0;
@@ -321,7 +334,6 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
   const long long pos = p.rot ? p.positions[tok] : 0;
   const __nv_bfloat16* weight = static_cast<const __nv_bfloat16*>(p.weight);
   auto weight_of = [&](int d) { return weight ? __bfloat162float(weight[d]) : 1.f; };
-  auto dim = [&](int e) { return (e < 8 ? c0 * 8 : c1 * 8 - 8) + e; };
   float own[16], other[16], heaviest = 0.f;
   auto turn_of = [&](int f, float& sn, float& cs) {
     const unsigned long long turn = static_cast<unsigned long long>(pos) * p.freq[f];
@@ -330,11 +342,13 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
     sn *= p.gain;
   };
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    own[e] = weight_of(dim(e));
-    other[e] = 0.f;
-    heaviest = fmaxf(heaviest, fabsf(own[e]));
+  for (int e = 0; e < 16; ++e) own[e] = 1.f, other[e] = 0.f;
+  if (weight) {
+    unpack8(*reinterpret_cast<const uint4*>(weight + c0 * 8), own);
+    unpack8(*reinterpret_cast<const uint4*>(weight + c1 * 8), own + 8);
   }
+#pragma unroll
+  for (int e = 0; e < 16; ++e) heaviest = fmaxf(heaviest, fabsf(own[e]));
   if (LAYOUT == kHalf) {
     if (turned) {
 #pragma unroll
@@ -379,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
   // Whether the lane's values are not exact in fp32, and how far they may be off,
   // of |a| + |b| (kAny and kPairs: where only some are, the rest is taken to be so too).
   const bool loose = p.norm || (LAYOUT == kHalf ? turned : c0 * 8 < p.rot);
-  const float err = (p.norm ? 1.9073486328125e-06f : 9.5367431640625e-07f) * fmaxf(1.f, p.gain);  // 2^-19, 2^-20
+  const float err = (p.norm ? 20.f : 16.f) * 5.9604644775390625e-08f * fmaxf(1.f, p.gain);  // 2^-24
 
   // where the rows go
   uint8_t *kdst = nullptr, *ksdst = nullptr, *vdst = nullptr, *vsdst = nullptr;
@@ -403,6 +417,8 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
     vout = static_cast<__nv_bfloat16*>(p.v) + row * p.ld_v + at;
   }
 
+  float gk_next = FP4 && here && p.k_scale ? p.k_scale[h_begin] : 1.f;
+  float gv_next = FP4 && here && p.v_scale ? p.v_scale[h_begin] : 1.f;
   unsigned again = 0;  // of 32 heads: those to be done more exactly
 #pragma unroll 1
   for (int ib = 0; ib < p.heads_per_unit; ib += kAhead)
@@ -418,13 +434,18 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
     load(i + kAhead, ja);
     float r = 1.f;  // the norm's factor
     if (p.norm) {
-      float ss = 0.f;  // (in the rotary kernel's order)
+      float2 s0 = make_float2(0.f, 0.f), s1 = s0;  // (four short sums: a small error)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], fmaf(a[8 + e], a[8 + e], ss));
+      for (int e = 0; e < 8; e += 2) {
+        const float2 x = make_float2(a[e], a[e + 1]), z = make_float2(a[8 + e], a[9 + e]);
+        s0 = ffma2(x, x, s0);
+        s1 = ffma2(z, z, s1);
+      }
+      float ss = (s0.x + s0.y) + (s1.x + s1.y);
 #pragma unroll
       for (int off = LPR / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(kFull, ss, off);
       near = !(ss < 1e36f);  // (bf16 squares pass fp32's range)
-      r = rsqrtf(ss * (1.f / D) + p.eps);
+      asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(ss, 1.f / D, p.eps)));
     }
     float sum = 0.f;  // kAny: a bound of |a| + |b|
     if (LAYOUT == kAny) {
@@ -440,7 +461,13 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
       sum = (ma + mb) * heaviest;
     } else {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) y[e] = fmaf(a[LAYOUT == kHalf ? e ^ 8 : e ^ 1], other[e], a[e] * own[e]);
+      for (int e = 0; e < 16; e += 2) {
+        const float2 x = make_float2(a[e], a[e + 1]);
+        const float2 z = LAYOUT == kHalf ? make_float2(a[e ^ 8], a[(e ^ 8) + 1]) : make_float2(x.y, x.x);
+        const float2 v = ffma2(z, make_float2(other[e], other[e + 1]), fmul2(x, make_float2(own[e], own[e + 1])));
+        y[e] = v.x;
+        y[e + 1] = v.y;
+      }
     }
     if (!FP4) {
       if (live) {
@@ -466,8 +493,11 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
     } else {
       t0 = t1 = most(t0, t1, 0.f);
     }
-    const int h = live ? h_begin + i : 0;
-    const float gk = p.k_scale ? p.k_scale[h] : 1.f, gv = p.v_scale ? p.v_scale[h] : 1.f;
+    const float gk = gk_next, gv = gv_next;
+    if (i + 1 < n) {
+      if (p.k_scale) gk_next = p.k_scale[h_begin + i + 1];
+      if (p.v_scale) gv_next = p.v_scale[h_begin + i + 1];
+    }
     {
       uint32_t w0, w1, b0, b1;
       const float g6 = 6.f * gk, inv = rcp(g6);
@@ -551,7 +581,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const CacheParams p) {
   constexpr int kPerWarp = 32 / LPR;
   const int lane = threadIdx.x & 31, l = threadIdx.x % LPR;
   const long long unit = static_cast<long long>(blockIdx.x) * kGroups + threadIdx.x / LPR;
-  const long long tok = unit < p.n_units ? unit / p.shares : 0;
+  const long long tok = unit < p.n_units ? token_of(p, unit) : 0;
   const int h_begin = static_cast<int>(unit - tok * p.shares) * p.heads_per_unit;
   long long page = 0;
   int o = 0;
@@ -628,15 +658,17 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const CacheParams p) {
 }
 
 // A token's heads in shares: all of them to one group of lanes where that
-// leaves every SM about eight rounds, else spread.
+// leaves every SM about `rounds` rounds, else spread.  (Appending, whose groups
+// begin with sines and cosines, two: 16384 tokens of 8 heads 43.0 us, with eight
+// 45.3; reading eight: the same 16.4 us, with two 17.0.)
 template <typename F>
-cudaError_t spread(CacheParams p, long long T, int D, F&& go) {
+cudaError_t spread(CacheParams p, long long T, int D, int rounds, F&& go) {
   const int groups = kThreads / (D / 16);
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  const long long rounds = static_cast<long long>(sms) * groups * 8;
-  long long hpu = (T * p.H + rounds - 1) / rounds;
+  const long long all = static_cast<long long>(sms) * groups * rounds;
+  long long hpu = (T * p.H + all - 1) / all;
   if (hpu > p.H) hpu = p.H;
   p.shares = static_cast<int>((p.H + hpu - 1) / hpu);
   p.heads_per_unit = (p.H + p.shares - 1) / p.shares;
@@ -652,7 +684,7 @@ bool even32(const void* a, long long ld) { return !a || ((reinterpret_cast<uintp
 
 template <int D, bool FP4>
 cudaError_t append_t(const CacheParams& p, long long T, cudaStream_t s) {
-  return spread(p, T, D, [&](const CacheParams& q, unsigned grid) {
+  return spread(p, T, D, 2, [&](const CacheParams& q, unsigned grid) {
     if (q.rot == 0 || q.layout == 1) append_kernel<D, kPairs, FP4><<<grid, kThreads, 0, s>>>(q);
     else if (q.rot % 32 == 0) append_kernel<D, kHalf, FP4><<<grid, kThreads, 0, s>>>(q);
     else append_kernel<D, kAny, FP4><<<grid, kThreads, 0, s>>>(q);
@@ -660,7 +692,7 @@ cudaError_t append_t(const CacheParams& p, long long T, cudaStream_t s) {
 }
 template <int D, bool FP4>
 cudaError_t read_t(const CacheParams& p, long long T, cudaStream_t s) {
-  return spread(p, T, D, [&](const CacheParams& q, unsigned grid) { read_kernel<D, FP4><<<grid, kThreads, 0, s>>>(q); });
+  return spread(p, T, D, 8, [&](const CacheParams& q, unsigned grid) { read_kernel<D, FP4><<<grid, kThreads, 0, s>>>(q); });
 }
 
 }  // namespace
