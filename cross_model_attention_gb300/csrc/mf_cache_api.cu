@@ -241,7 +241,7 @@ int mf_attn_paged(const mf_cache_t* cache, int n, int Lq, int H_q, const void* q
   if ((rc = check_table(cache, table, ld_table, n, max_pages)) != MF_OK) return rc;
   // (the kernel counts tiles of 32 keys, of one head in 32 bits)
   const long long lines = (long long)n * ((long long)max_pages * cache->page_size / 32 + 2);
-  if (lines >= 1ll << 31 || lines * H * ((Lq * (H_q / H) + 31) / 32) >= 1ll << 37)
+  if (lines >= 1ll << 31 || lines * H * ((Lq * (H_q / H) + 15) / 16) >= 1ll << 37)
     return fail(MF_ERR_UNSUPPORTED, "%d requests of up to %lld keys: too many keys for one call", n, (long long)max_pages * cache->page_size);
   if ((rc = check_aligned("lens", lens, 4)) != MF_OK) return rc;
   if (lse && (rc = check_aligned("lse", lse, 4)) != MF_OK) return rc;

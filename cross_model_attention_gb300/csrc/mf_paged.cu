@@ -50,12 +50,13 @@ constexpr int kCost = 1;             // a pair's start and end, in tiles
 constexpr int kMinSpan = 2;          // least work of a CTA, in tiles
 constexpr int kLensHere = 900;       // requests whose lengths are kept in shared memory
 constexpr float kLift = 7.f;         // weights are held times 2^7
+constexpr float kNoRef = 1e30f;      // kLift less the reference of a row that has seen no key
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // D dimensions, NT times 8 rows to a unit of work.
 template <int D, int NT>
 struct Cfg {
-  static constexpr int W = NT == 1 ? 16 : NT == 2 ? 12 : 8;  // warps
+  static constexpr int W = NT == 1 ? 16 : 12;                // warps
   static constexpr int NB = D == 128 ? 2 : 4;            // 16-key blocks of a tile
   static constexpr int TK = NB * 16;
   static constexpr int kPiece = fp4_piece(D);
@@ -167,7 +168,8 @@ __device__ __forceinline__ bool row_of(const PagedParams& p, int r, int u, int r
   x.tok = static_cast<long long>(r) * p.Lq + t;
   return rr < p.Lq * p.G;
 }
-__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : (m - kLift + log2f(l)) * kLn2; }
+// Of a reference (in base 2, less kLift) and a sum of weights beside it.
+__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2; }
 // A piece's weight beside others under the common reference M.
 __device__ __forceinline__ float weight_of(float m, float l, float M) {
   return m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2(m - M);  // (a sum without a reference is NaN)
@@ -451,7 +453,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
     const float vs = vscale;
     uint32_t qf[NQ][D / 16][2];
     uint2* qs = reinterpret_cast<uint2*>(smem + C::kQ + warp * C::kQBytes) + lane;  // [D / 16][NT][32], where they are shared
-    float acc[D / 16][NT][4], m[NT][2], l[NT][2], coef[NT][2];
+    float acc[D / 16][NT][4], lift[NT][2], l[NT][2], coef[NT][2];  // lift: kLift less the reference
     int rg0;
     const int h0 = head_of(d.u, rg0);
 #pragma unroll
@@ -493,7 +495,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         coef[nt][j] = __shfl_sync(kFull, c, (2 * t + j) * 4);
-        m[nt][j] = -INFINITY;
+        lift[nt][j] = kNoRef;
         l[nt][j] = 0.f;
       }
     }
@@ -521,10 +523,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
       uint32_t s0[NB], s1[NB];                  // their scales, one or two
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[b][nt][e] = 0.f;
         const uint8_t* base = st + b * C::kPiece;
         if (D == 128) {
           const uint4 a = *reinterpret_cast<const uint4*>(base + g * 64 + t * 16);
@@ -569,6 +567,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
           for (int nt = 0; nt < NT; ++nt) {
             const uint2 q0 = C::kQShared ? qa[C::kQShared ? nt : 0] : make_uint2(qf[C::kQShared ? 0 : nt][2 * w][0], qf[C::kQShared ? 0 : nt][2 * w][1]);
             const uint2 q1 = C::kQShared ? qb[C::kQShared ? nt : 0] : make_uint2(qf[C::kQShared ? 0 : nt][2 * w + 1][0], qf[C::kQShared ? 0 : nt][2 * w + 1][1]);
+            if (w == 0) x[b][nt][0] = x[b][nt][1] = x[b][nt][2] = x[b][nt][3] = 0.f;
             mma(x[b][nt], a0, a1, a2, a3, q0.x, q0.y);
             mma(x[b][nt], c0, c1, c2, c3, q1.x, q1.y);
           }
@@ -606,12 +605,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
               by[nt][k] = 1.f;
             }
             if (!whole) {
+              const int far0 = row - key0 - g;  // to the lane's first key
 #pragma unroll
               for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int e = k; e < 4; e += 2) {
-                  const int j = key0 + 16 * b + g + (e & 2) * 4, far = row - j;
-                  const bool seen = far >= 0 && (far < p.window || j < p.n_sink) && !(gone >> b & 1);
+                  const int far = far0 - (16 * b + (e & 2) * 4);
+                  const bool seen = far >= 0 && (far < p.window || row - far < p.n_sink) && !(gone >> b & 1);
                   x[b][nt][e] = seen ? x[b][nt][e] * by[nt][k] : -INFINITY;
                 }
               by[nt][k] = 1.f;
@@ -619,32 +619,44 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
           }
       }
 
-      // the rows' references
+      // exponents, and the rows' references
+      float y[NB][NT][4];
+      auto exponents = [&]() {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[b][nt][e] = fmaf(x[b][nt][e], by[nt][e & 1], lift[nt][e & 1]);
+      };
+      exponents();
       {
-        float mx[NT][2];
+        float top[NT][2];
         bool up = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            mx[nt][j] = fmaxf(x[0][nt][j], x[0][nt][2 + j]);
+            top[nt][j] = fmaxf(y[0][nt][j], y[0][nt][2 + j]);
 #pragma unroll
-            for (int b = 1; b < NB; ++b) mx[nt][j] = fmaxf(mx[nt][j], fmaxf(x[b][nt][j], x[b][nt][2 + j]));
-            mx[nt][j] *= by[nt][j];
-            up |= mx[nt][j] > m[nt][j] + 8.f;
+            for (int b = 1; b < NB; ++b) top[nt][j] = fmaxf(top[nt][j], fmaxf(y[b][nt][j], y[b][nt][2 + j]));
+            up |= top[nt][j] > kLift + 8.f;
           }
         if (__any_sync(kFull, up)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              float y = mx[nt][j];
+              // (without a reference, kNoRef hides the scores: theirs is to be taken)
+              float s = -INFINITY;
 #pragma unroll
-              for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(kFull, y, o));
-              const float old = m[nt][j];
-              const bool move = y > old + 8.f;
-              const float f = !move ? 1.f : old == -INFINITY ? 0.f : ex2(old - y);
-              if (move) m[nt][j] = y;
+              for (int b = 0; b < NB; ++b) s = fmaxf(s, fmaxf(x[b][nt][j], x[b][nt][2 + j]) * by[nt][j]);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) s = fmaxf(s, __shfl_xor_sync(kFull, s, o));
+              const float old = lift[nt][j];
+              const bool move = s + old > kLift + 8.f;
+              if (move) lift[nt][j] = kLift - s;
+              const float f = !move ? 1.f : old == kNoRef ? 0.f : ex2(lift[nt][j] - old);
               l[nt][j] *= f;
 #pragma unroll
               for (int a = 0; a < D / 16; ++a) {
@@ -652,20 +664,18 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
                 acc[a][nt][2 + j] *= f;
               }
             }
+          exponents();
         }
       }
       // weights, and as the B operand: keys by rows
       uint32_t pf[NB][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float lift[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) lift[j] = kLift - (m[nt][j] == -INFINITY ? 0.f : m[nt][j]);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           float w[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = ex2(fmaf(x[b][nt][e], by[nt][e & 1], lift[e & 1]));
+          for (int e = 0; e < 4; ++e) w[e] = ex2(y[b][nt][e]);
           l[nt][0] += w[0] + w[2];
           l[nt][1] += w[1] + w[3];
           pf[b][nt][0] = transpose8x8(pack_f16x2(w[0], w[1]));
@@ -766,14 +776,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
               w[e] = L == 0.f ? 0u : pack_bf16x2(acc[4 * c + e][nt][j] * inv, acc[4 * c + e][nt][2 + j] * inv);
             reinterpret_cast<uint4*>(o)[c] = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          if (p.lse && g == 0) p.lse[tok * (p.H_kv * p.G) + head] = lse_of(m[nt][j], L);
+          if (p.lse && g == 0) p.lse[tok * (p.H_kv * p.G) + head] = lse_of(-lift[nt][j], L);
         } else {
           float* to = po + row * D + g * (D / 8);
 #pragma unroll
           for (int c = 0; c < D / 32; ++c)
             reinterpret_cast<float4*>(to)[c] = make_float4(acc[2 * c][nt][j] * vs, acc[2 * c][nt][2 + j] * vs,
                                                            acc[2 * c + 1][nt][j] * vs, acc[2 * c + 1][nt][2 + j] * vs);
-          if (g == 0) pm[row] = make_float2(m[nt][j], L);
+          if (g == 0) pm[row] = make_float2(lift[nt][j] == kNoRef ? -INFINITY : -lift[nt][j], L);
         }
       }
     if (!done && lane == 0) pieces[2 * warp + (more ? 0 : 1)] = Piece{d.r, d.u, kHere | (d.flags & 0xff), d.flags >> 8};
@@ -802,8 +812,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
       v[0] = x.x, v[1] = x.y;
     }
   };
-  for (int item = warp; item < n_groups * p.rows; item += W) {
-    const int at_group = item / p.rows, row = item - at_group * p.rows;
+  constexpr int RI = NT;  // rows at a time
+  const int row_items = (p.rows + RI - 1) / RI;
+  for (int item = warp; item < n_groups * row_items; item += W) {
+    const int at_group = item / row_items, row0 = (item - at_group * row_items) * RI;
     const int first = __ffs(__ballot_sync(kFull, leads && rank == at_group)) - 1;
     const unsigned after = leaders & ~((2u << first) - 1u);
     const unsigned group = present & ~((1u << first) - 1u) & (after ? (1u << (__ffs(after) - 1)) - 1u : kFull);
@@ -812,47 +824,66 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
     const bool begins = a.flags & kBegins, ends = z.flags & kEnds;
     const bool far = !(last & 1);  // the last piece is in the workspace
     const int w0 = first >> 1, w1 = (last >> 1) + (far ? 0 : 1);  // warps with a piece in shared memory
-    float out[E], add[E], M = -INFINITY, L = 0.f;
-    float2 ml_far = make_float2(-INFINITY, 0.f);
+    // (rows past the last are the last again, and not stored)
+    int row[RI];
+    float out[RI][E], add[RI][E], M[RI], L[RI];
+    float2 ml_far[RI];
+    const long long spot_far = 2ll * gridDim.x + static_cast<long long>(blockIdx.x) * W + (last >> 1);
 #pragma unroll
-    for (int e = 0; e < E; ++e) out[e] = add[e] = 0.f;
-    if (far) {
-      const long long spot = 2ll * gridDim.x + static_cast<long long>(blockIdx.x) * W + (last >> 1);
-      take(p.part_o + (spot * p.rows + row) * D + lane * E, add);
-      ml_far = p.part_ml[spot * p.rows + row];
+    for (int x = 0; x < RI; ++x) {
+      row[x] = min(row0 + x, p.rows - 1);
+      M[x] = -INFINITY;
+      L[x] = 0.f;
+      ml_far[x] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) out[x][e] = add[x][e] = 0.f;
+      if (far) {
+        take(p.part_o + (spot_far * p.rows + row[x]) * D + lane * E, add[x]);
+        ml_far[x] = p.part_ml[spot_far * p.rows + row[x]];
+      }
     }
     // (short spans leave warps without tiles)
-    auto ml_of = [&](int w) {
-      return group >> (2 * w + 1) & 1 ? reinterpret_cast<const float2*>(smem + w * C::kRing + C::R * D * 4)[row] : make_float2(-INFINITY, 0.f);
+    auto ml_of = [&](int w, int x) {
+      return group >> (2 * w + 1) & 1 ? reinterpret_cast<const float2*>(smem + w * C::kRing + C::R * D * 4)[row[x]] : make_float2(-INFINITY, 0.f);
     };
 #pragma unroll 4
-    for (int w = w0; w < w1; ++w) M = fmaxf(M, ml_of(w).x);
-    M = fmaxf(M, ml_far.x);
+    for (int w = w0; w < w1; ++w)
+#pragma unroll
+      for (int x = 0; x < RI; ++x) M[x] = fmaxf(M[x], ml_of(w, x).x);
+#pragma unroll
+    for (int x = 0; x < RI; ++x) M[x] = fmaxf(M[x], ml_far[x].x);
 #pragma unroll 4
     for (int w = w0; w < w1; ++w) {
-      const float2 ml = ml_of(w);
-      const float f = weight_of(ml.x, ml.y, M);
-      float v[E];
       if (!(group >> (2 * w + 1) & 1)) continue;
-      take(reinterpret_cast<const float*>(smem + w * C::kRing) + row * D + lane * E, v);
-      L = fmaf(f, ml.y, L);
 #pragma unroll
-      for (int e = 0; e < E; ++e) out[e] = fmaf(f, v[e], out[e]);
-    }
-    if (far) {
-      const float f = weight_of(ml_far.x, ml_far.y, M);
-      L = fmaf(f, ml_far.y, L);
+      for (int x = 0; x < RI; ++x) {
+        const float2 ml = ml_of(w, x);
+        const float f = weight_of(ml.x, ml.y, M[x]);
+        float v[E];
+        take(reinterpret_cast<const float*>(smem + w * C::kRing) + row[x] * D + lane * E, v);
+        L[x] = fmaf(f, ml.y, L[x]);
 #pragma unroll
-      for (int e = 0; e < E; ++e) out[e] = fmaf(f, add[e], out[e]);
+        for (int e = 0; e < E; ++e) out[x][e] = fmaf(f, v[e], out[x][e]);
+      }
     }
-    if (begins && ends) {
-      store_row<D>(p, a.r, a.u, row, C::R, M, L, out);
-    } else {
-      const long long spot = 2ll * blockIdx.x + (begins ? 1 : 0);
-      float* to = p.part_o + (spot * p.rows + row) * D + lane * E;
-      if (D == 128) *reinterpret_cast<float4*>(to) = make_float4(out[0], out[1], out[E - 2], out[E - 1]);
-      else *reinterpret_cast<float2*>(to) = make_float2(out[0], out[1]);
-      if (lane == 0) p.part_ml[spot * p.rows + row] = make_float2(M, L);
+#pragma unroll
+    for (int x = 0; x < RI; ++x) {
+      if (row0 + x >= p.rows) continue;
+      if (far) {
+        const float f = weight_of(ml_far[x].x, ml_far[x].y, M[x]);
+        L[x] = fmaf(f, ml_far[x].y, L[x]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) out[x][e] = fmaf(f, add[x][e], out[x][e]);
+      }
+      if (begins && ends) {
+        store_row<D>(p, a.r, a.u, row[x], C::R, M[x], L[x], out[x]);
+      } else {
+        const long long spot = 2ll * blockIdx.x + (begins ? 1 : 0);
+        float* to = p.part_o + (spot * p.rows + row[x]) * D + lane * E;
+        if (D == 128) *reinterpret_cast<float4*>(to) = make_float4(out[x][0], out[x][1], out[x][E - 2], out[x][E - 1]);
+        else *reinterpret_cast<float2*>(to) = make_float2(out[x][0], out[x][1]);
+        if (lane == 0) p.part_ml[spot * p.rows + row[x]] = make_float2(M[x], L[x]);
+      }
     }
   }
   if (warp == 0) {  // for the join: a unit that begins here and ends in another CTA
@@ -941,26 +972,25 @@ cudaError_t launch_t(PagedParams p, cudaStream_t s) {
 
 }  // namespace
 
-// Rows to a unit: 8 where there are no more, 16 where there are no more than
-// that, else 32 and as many units to a head as it takes.
+// Rows to a unit: 8 where there are no more, else 16 and as many units to a head as
+// it takes.  (Units of 32 rows, whose products alone fill 255 registers of 8 warps: 64
+// rows over 32 requests of 16384 keys 488 us, not 548; of 4096 152, not 159; over 8
+// requests of 4000 keys on average 65, not 60.)
 namespace {
-int row_tiles(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+int row_tiles(int rows) { return rows <= 8 ? 1 : 2; }
 }  // namespace
 
 void paged_shape(int Lq, int G, int sms, int* grid, int* parts, int* rows) {
   const int nt = row_tiles(Lq * G);
   *grid = sms;
-  *parts = sms * (2 + (nt == 1 ? Cfg<128, 1>::W : nt == 2 ? Cfg<128, 2>::W : Cfg<128, 4>::W));
+  *parts = sms * (2 + (nt == 1 ? Cfg<128, 1>::W : Cfg<128, 2>::W));
   *rows = Lq * G < 8 * nt ? Lq * G : 8 * nt;
 }
 
 cudaError_t launch_paged(const PagedParams& p, int d, cudaStream_t s) {
   if (p.n <= 0) return cudaSuccess;
-  switch (row_tiles(p.Lq * p.G)) {
-    case 1: return d == 128 ? launch_t<128, 1>(p, s) : launch_t<64, 1>(p, s);
-    case 2: return d == 128 ? launch_t<128, 2>(p, s) : launch_t<64, 2>(p, s);
-    default: return d == 128 ? launch_t<128, 4>(p, s) : launch_t<64, 4>(p, s);
-  }
+  if (row_tiles(p.Lq * p.G) == 1) return d == 128 ? launch_t<128, 1>(p, s) : launch_t<64, 1>(p, s);
+  return d == 128 ? launch_t<128, 2>(p, s) : launch_t<64, 2>(p, s);
 }
 
 }  // namespace mf

@@ -716,7 +716,7 @@ MF_API int mf_cache_read(const mf_cache_t* cache, int T, const int32_t* seq, con
  *   slopes       DEVICE fp32 [H_q] or NULL      softcap  0: none
  *   window       >= 1, or 0: no window          n_sink   >= 0
  *   n            at most 2^20; n * (max_pages * page_size / 32 + 2) below 2^31, and
- *                that times H and a 32nd of the rows of a head, Lq * H_q / H, rounded
+ *                that times H and a 16th of the rows of a head, Lq * H_q / H, rounded
  *                up, below 2^37 (MF_ERR_UNSUPPORTED)
  *   lse          fp32 [n * Lq][H_q] or NULL
  *   workspace    the caller's, 256-byte aligned, mf_attn_paged_workspace bytes; needs
