@@ -293,6 +293,8 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
   constexpr int LPR = D / 16;            // lanes to a row
   constexpr int kGroups = kThreads / LPR;
   constexpr int kPerWarp = 32 / LPR;     // rows to a warp
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // what comes after may be set up
+  asm volatile("griddepcontrol.wait;" ::: "memory");               // what came before may still run
   const int half = p.rot >> 1, lane = threadIdx.x & 31;
   const int l = threadIdx.x % LPR;
   const long long unit = static_cast<long long>(blockIdx.x) * kGroups + threadIdx.x / LPR;
@@ -579,6 +581,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const CacheParams p) {
   constexpr int LPR = D / 16;
   constexpr int kGroups = kThreads / LPR;
   constexpr int kPerWarp = 32 / LPR;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, l = threadIdx.x % LPR;
   const long long unit = static_cast<long long>(blockIdx.x) * kGroups + threadIdx.x / LPR;
   const long long tok = unit < p.n_units ? token_of(p, unit) : 0;
@@ -676,23 +680,22 @@ cudaError_t spread(CacheParams p, long long T, int D, int rounds, F&& go) {
   p.n_units = T * p.shares;
   const long long grid = (p.n_units + groups - 1) / groups;
   if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
-  go(p, static_cast<unsigned>(grid));
-  return cudaGetLastError();
+  return go(p, dim3(static_cast<unsigned>(grid)));
 }
 
 bool even32(const void* a, long long ld) { return !a || ((reinterpret_cast<uintptr_t>(a) & 31) == 0 && ld % 16 == 0); }
 
 template <int D, bool FP4>
 cudaError_t append_t(const CacheParams& p, long long T, cudaStream_t s) {
-  return spread(p, T, D, 2, [&](const CacheParams& q, unsigned grid) {
-    if (q.rot == 0 || q.layout == 1) append_kernel<D, kPairs, FP4><<<grid, kThreads, 0, s>>>(q);
-    else if (q.rot % 32 == 0) append_kernel<D, kHalf, FP4><<<grid, kThreads, 0, s>>>(q);
-    else append_kernel<D, kAny, FP4><<<grid, kThreads, 0, s>>>(q);
+  return spread(p, T, D, 2, [&](const CacheParams& q, dim3 grid) {
+    const bool pairs = q.rot == 0 || q.layout == 1;
+    auto* kernel = pairs ? append_kernel<D, kPairs, FP4> : q.rot % 32 == 0 ? append_kernel<D, kHalf, FP4> : append_kernel<D, kAny, FP4>;
+    return launch_early(kernel, grid, kThreads, 0, s, q);
   });
 }
 template <int D, bool FP4>
 cudaError_t read_t(const CacheParams& p, long long T, cudaStream_t s) {
-  return spread(p, T, D, 8, [&](const CacheParams& q, unsigned grid) { read_kernel<D, FP4><<<grid, kThreads, 0, s>>>(q); });
+  return spread(p, T, D, 8, [&](const CacheParams& q, dim3 grid) { return launch_early(read_kernel<D, FP4>, grid, kThreads, 0, s, q); });
 }
 
 }  // namespace

@@ -112,6 +112,23 @@ cudaError_t once_per_device(std::atomic<unsigned long long>& done, F&& set) {
   return e;
 }
 
+// Launches a kernel that may be set up while the one before it still runs: its
+// first instruction that touches memory comes after griddepcontrol.wait.
+template <typename P>
+cudaError_t launch_early(void (*kernel)(P), dim3 grid, int threads, size_t smem, cudaStream_t s, const P& p) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 // -------------------------------------------------------------- launchers --
 // All return cudaError_t of the launch (cudaSuccess when enqueued).
 // Head-map calibration: Gram matrix of the stacked head maps of two BSR

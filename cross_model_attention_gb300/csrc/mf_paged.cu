@@ -201,7 +201,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
   int* lens_s = reinterpret_cast<int*>(smem + C::kLens);
   Part* parts = reinterpret_cast<Part*>(smem + C::kParts) + warp * C::kQueue;
   Piece* pieces = reinterpret_cast<Piece*>(smem + C::kPieces);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // what comes after may be set up
+  asm volatile("griddepcontrol.wait;" ::: "memory");               // what came before may still run
 
   // ---- the lines: a thread sums those of consecutive requests
   const int share = (p.n + T - 1) / T;
@@ -899,6 +900,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
 // last unit and of the following CTAs' first.
 template <int D, int NT>
 __global__ void __launch_bounds__(32) join_kernel(const PagedParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x, row = blockIdx.y, lane = threadIdx.x;
   auto spot = [&](int k) { return (k == 0 ? 2ll * c + 1 : 2ll * (c + k)) * p.rows + row; };
@@ -956,18 +958,8 @@ cudaError_t launch_t(PagedParams p, cudaStream_t s) {
   int sms = 0;
   if ((e = sm_count(&sms)) != cudaSuccess) return e;
   p.inv_grid = std::nextafterf(1.f / sms, 1.f);
-  paged_kernel<D, NT><<<sms, C::kThreads, C::kBytes, s>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(sms, p.rows);
-  cfg.blockDim = dim3(32);
-  cfg.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D, NT>, p);
+  if ((e = launch_early(paged_kernel<D, NT>, dim3(sms), C::kThreads, C::kBytes, s, p)) != cudaSuccess) return e;
+  return launch_early(join_kernel<D, NT>, dim3(sms, p.rows), 32, 0, s, p);
 }
 
 }  // namespace
