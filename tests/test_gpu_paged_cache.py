@@ -642,3 +642,131 @@ def test_bindings_refuse(dev):
             call()
             pytest.fail(f"call {i} was taken")
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_that_begin_between_32_bytes(dev, d):
+    """Rows at odd multiples of 16 bytes give what rows at even ones give."""
+    g, H, ps, T = _gen(dev, 25 + d), 3, 16, 75
+    width = H * d + 8
+
+    def odd(T, heads):
+        return torch.zeros(T, heads * d + 8, dtype=BF, device=dev)[:, 8:].view(T, heads, d)
+
+    assert odd(2, H).data_ptr() % 32 == 16 and odd(2, H).stride(0) == width
+    k, v, q = _rnd(g, dev, T, H, d), _rnd(g, dev, T, H, d), _rnd(g, dev, 5, 1, 2 * H, d)
+    ko, vo, qo = odd(T, H), odd(T, H), odd(5, 2 * H)
+    ko.copy_(k), vo.copy_(v), qo.copy_(q[:, 0])
+    seq, at = _tokens([20, 1, 16, 30, 8], dev)
+    table = torch.randperm(10, generator=g, device=dev).to(torch.int32).view(5, 2)
+    lens = torch.tensor([20, 1, 16, 30, 8], dtype=torch.int32, device=dev)
+    for layout, rot in (("half", d), ("interleaved", 32), ("half", 20)):
+        plan = mapflow.RotaryPlan(rot, layout=layout)
+        held = []
+        for kk, vv in ((k, v), (ko, vo), (k, vo)):
+            pages = torch.zeros(10, H, 18 * d, dtype=torch.uint8, device=dev)
+            mapflow.PagedCache.fp4(pages, ps, d).append(kk, vv, seq, at, table, rope=plan, norm=True)
+            held.append(pages)
+        assert torch.equal(held[0], held[1]) and torch.equal(held[0], held[2])
+        cache = mapflow.PagedCache.fp4(held[0], ps, d)
+        want, got = cache.read(seq, at, table), cache.read(seq, at, table, k=odd(T, H), v=odd(T, H))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        o = odd(5, 2 * H)[:, None]
+        assert torch.equal(cache.attend(qo[:, None], table, lens, o=o), cache.attend(q, table, lens))
+        rows = []
+        for kk, vv, make in ((k, v, None), (ko, vo, None), (k, v, odd)):
+            if make is None:
+                ck, cv = (torch.zeros(10, ps, H, d, dtype=BF, device=dev) for _ in range(2))
+            else:
+                ck, cv = (make(10 * ps, H).unflatten(0, (10, ps)) for _ in range(2))
+            c = mapflow.PagedCache.bf16(ck, cv)
+            c.append(kk, vv, seq, at, table, rope=plan, norm=True)
+            rows.append((ck, cv, *c.read(seq, at, table), *c.read(seq, at, table, k=odd(T, H), v=odd(T, H))))
+        for other in rows[1:]:
+            assert all(torch.equal(a, b) for a, b in zip(rows[0], other))
+        assert torch.equal(rows[0][2], rows[0][4]) and torch.equal(rows[0][3], v) and torch.equal(rows[0][5], v)
+
+
+def test_pages_that_requests_share(dev):
+    lens = [900, 900, 900]
+    g, pages, table, lens_t, gk, gv, keys = _world(dev, 30, 3, 2, 128, 64, lens)
+    cache = mapflow.PagedCache.fp4(pages, 64, 128, k_scale=gk, v_scale=gv)
+    q = _rnd(g, dev, 3, 1, 8, 128)
+    table[1:, :9] = table[0, :9]  # one prompt's pages in all three
+    table[2, 11] = table[2, 10]   # and one page twice in a request
+    copies = pages[table.long().flatten()].contiguous()
+    own = torch.arange(table.numel(), dtype=torch.int32, device=dev).view_as(table)
+    o = cache.attend(q, table, lens_t)
+    assert torch.equal(o, mapflow.PagedCache.fp4(copies, 64, 128, k_scale=gk, v_scale=gv).attend(q, own, lens_t))
+    assert torch.equal(o[:, 0, 0].isfinite(), torch.ones_like(o[:, 0, 0], dtype=torch.bool))
+
+
+def test_two_graphs_replayed_at_once(dev):
+    lens = [5000, 20, 3000]
+    g, pages, table, lens_t, gk, gv, keys = _world(dev, 31, 3, 2, 128, 64, lens)
+    cache = mapflow.PagedCache.fp4(pages, 64, 128, k_scale=gk, v_scale=gv)
+    qs = [_rnd(g, dev, 3, 1, 8, 128) for _ in range(2)]
+    want = [cache.attend(q, table, lens_t) for q in qs]
+    got = [torch.zeros_like(q) for q in qs]
+    torch.cuda.synchronize()
+    graphs = []
+    for q, o in zip(qs, got):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(4):
+                cache.attend(q, table, lens_t, o=o)
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(5):
+        for o in got:
+            o.zero_()
+        torch.cuda.synchronize()
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_steps_in_a_row_follow_each_other(dev, captured):
+    """A step's attention sees what the append before it wrote, and no step's
+    append overtakes the attention or the reading before it."""
+    g, H, d, n, steps = _gen(dev, 32), 8, 128, 40, 24
+    k, v = _rnd(g, dev, steps, n, H, d), _rnd(g, dev, steps, n, H, d)
+    q = _rnd(g, dev, n, 1, 4 * H, d)
+    table = torch.arange(2 * n, dtype=torch.int32, device=dev).view(n, 2)
+    seq = torch.arange(n, dtype=torch.int32, device=dev)
+    at = [torch.full((n,), x % 18, dtype=torch.int32, device=dev) for x in range(steps)]  # the last ones over the first
+    lens = [torch.full((n,), min(x + 1, 18), dtype=torch.int32, device=dev) for x in range(steps)]
+    pages = torch.zeros(2 * n, H, 18 * d, dtype=torch.uint8, device=dev)
+    cache = mapflow.PagedCache.fp4(pages, 16, d)
+    plan = mapflow.RotaryPlan(d)
+    o = [torch.zeros_like(q) for _ in range(steps)]
+    rows = [(torch.zeros_like(k[0]), torch.zeros_like(k[0])) for _ in range(steps)]
+
+    def run(wait):
+        for x in range(steps):
+            cache.append(k[x], v[x], seq, at[x], table, rope=plan, norm=True)
+            wait()
+            cache.attend(q, table, lens[x], o=o[x])
+            wait()
+            cache.read(seq, at[x], table, *rows[x])
+            wait()
+
+    run(torch.cuda.synchronize)
+    want = [t.clone() for t in o + [a for r in rows for a in r] + [pages]]
+    graph = None
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run(lambda: None)
+    for _ in range(5):
+        for t in o + [a for r in rows for a in r] + [pages]:
+            t.zero_()
+        torch.cuda.synchronize()
+        graph.replay() if captured else run(lambda: None)
+        torch.cuda.synchronize()
+        for a, b in zip(o + [a for r in rows for a in r] + [pages], want):
+            assert torch.equal(a, b)

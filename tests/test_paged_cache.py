@@ -200,3 +200,15 @@ def test_packing_and_unpacking():
         assert int(piece[17 * d + 2 * 16 + 9]) == int(vs[2, 9, 1, 2])
         assert (int(piece[9 * (d // 2) + 17]) >> 4) == int(kc[2, 9, 1, 35])
         assert int(piece[16 * d + 9 * (d // 16) + 2]) == int(ks[2, 9, 1, 2])
+
+
+@pytest.mark.parametrize("kw", [
+    dict(n=1 << 20, max_pages=1 << 10, ld_table=1 << 10),                        # 2^20 requests of 2^16 keys
+    dict(n=1 << 10, max_pages=1 << 20, ld_table=1 << 20),                        # 2^10 of 2^26
+    dict(n=1 << 14, max_pages=1 << 15, ld_table=1 << 15, Lq=32, H_q=1024, ld_q=1 << 17, ld_o=1 << 17,  # 2^30 tiles of
+         cache=dict(H=256))])                                                    # 256 heads of 8 groups of 16 rows
+def test_more_keys_than_a_call_counts_are_refused(lib, kw):
+    kw = dict(kw)
+    c = _cache(**kw.pop("cache", {}))
+    assert _attend(lib, c, **dict(kw, q=1 << 44, o=1 << 45)) == E.MF_ERR_UNSUPPORTED
+    assert "too many keys" in lib.mf_last_error().decode()
