@@ -33,6 +33,7 @@
 // CTAs share through the workspace, by a second kernel; both in a fixed order.
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -904,27 +905,38 @@ __global__ void __launch_bounds__(32) join_kernel(const PagedParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x, row = blockIdx.y, lane = threadIdx.x;
   auto spot = [&](int k) { return (k == 0 ? 2ll * c + 1 : 2ll * (c + k)) * p.rows + row; };
-  // (the first results are asked for before it is known which there are)
-  constexpr int kAhead = 4, E = D / 32;
+  // Two results are asked for before it is known which there are, then 16 at a
+  // time.  (Four, each replaced as it is added: one request of 16000 keys, in 19
+  // CTAs to a head, 16.5 us for 13.2; 1000 keys 12.2 for 9.3.)
+  constexpr int kAhead = 2, E = D / 32;
   const int4 cut = p.cuts[c];
   float v[kAhead][E];
   float2 ml[kAhead];
-  auto take = [&](int j, int k) {
-    ml[j] = p.part_ml[spot(k)];
+  auto take = [&](int k, float* x, float2& m) {
+    m = p.part_ml[spot(k)];
     const float* s = p.part_o + spot(k) * D + lane * E;
     if (D == 128) {
       const float4 y = *reinterpret_cast<const float4*>(s);
-      v[j][0] = y.x, v[j][1] = y.y, v[j][E - 2] = y.z, v[j][E - 1] = y.w;
+      x[0] = y.x, x[1] = y.y, x[E - 2] = y.z, x[E - 1] = y.w;
     } else {
       const float2 y = *reinterpret_cast<const float2*>(s);
-      v[j][0] = y.x, v[j][1] = y.y;
+      x[0] = y.x, x[1] = y.y;
     }
   };
   const int most = gridDim.x - c;
 #pragma unroll
-  for (int j = 0; j < kAhead; ++j) take(j, min(j, most - 1));
+  for (int j = 0; j < kAhead; ++j) take(min(j, most - 1), v[j], ml[j]);
   if (cut.x < 0) return;
   const int n = cut.z - c + 1;
+  constexpr int kMore = 16;
+  float w[kMore][E];
+  float2 wl[kMore];
+  auto ask = [&](int k0) {
+#pragma unroll
+    for (int j = 0; j < kMore; ++j)
+      if (k0 + j < n) take(k0 + j, w[j], wl[j]);
+  };
+  ask(kAhead);
   float M = -INFINITY, L = 0.f;
   for (int k = lane; k < n; k += 32) M = fmaxf(M, p.part_ml[spot(k)].x);
 #pragma unroll
@@ -932,17 +944,20 @@ __global__ void __launch_bounds__(32) join_kernel(const PagedParams p) {
   float out[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) out[e] = 0.f;
-  for (int k0 = 0; k0 < n; k0 += kAhead) {
+  auto add = [&](const float2 m, const float* x) {
+    const float f = weight_of(m.x, m.y, M);
+    L = fmaf(f, m.y, L);
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      if (k0 + j < n) {
-        const float f = weight_of(ml[j].x, ml[j].y, M);
-        L = fmaf(f, ml[j].y, L);
+    for (int e = 0; e < E; ++e) out[e] = fmaf(f, x[e], out[e]);
+  };
 #pragma unroll
-        for (int e = 0; e < E; ++e) out[e] = fmaf(f, v[j][e], out[e]);
-      }
-      if (k0 + kAhead + j < n) take(j, k0 + kAhead + j);
-    }
+  for (int j = 0; j < kAhead; ++j)
+    if (j < n) add(ml[j], v[j]);
+  for (int k0 = kAhead; k0 < n; k0 += kMore) {
+    if (k0 > kAhead) ask(k0);
+#pragma unroll
+    for (int j = 0; j < kMore; ++j)
+      if (k0 + j < n) add(wl[j], w[j]);
   }
   store_row<D>(p, cut.x, cut.y, row, 8 * NT, M, L, out);
 }
@@ -981,6 +996,9 @@ void paged_shape(int Lq, int G, int sms, int* grid, int* parts, int* rows) {
 
 cudaError_t launch_paged(const PagedParams& p, int d, cudaStream_t s) {
   if (p.n <= 0) return cudaSuccess;
+  // a call's two launches follow each other, so that calls of several threads on one stream may share a workspace
+  static std::mutex mutex;
+  const std::lock_guard<std::mutex> lock(mutex);
   if (row_tiles(p.Lq * p.G) == 1) return d == 128 ? launch_t<128, 1>(p, s) : launch_t<64, 1>(p, s);
   return d == 128 ? launch_t<128, 2>(p, s) : launch_t<64, 2>(p, s);
 }

@@ -847,6 +847,9 @@ class CacheAttention(_AttentionPlan):
 MF_CACHE_BF16, MF_CACHE_FP4 = 0, 1
 
 
+_default_ws: Dict[int, "object"] = {}  # PagedCache.attend's workspace of each GPU's default stream
+
+
 class PagedCache:
     """A paged cache of one layer's keys and values over tensors of the caller
     (see mf_cache_t in mapflow.h): PagedCache.fp4 for pages of 4 bits,
@@ -905,12 +908,17 @@ class PagedCache:
         ld_k, ld_v = _rows("k", k, shape, torch.bfloat16, gpu), _rows("v", v, shape, torch.bfloat16, gpu)
         return cls(MF_CACHE_BF16, page_size, H, d, n, (k, v, None, None), ld_k, ld_v)
 
-    def _table(self, table, rows=None) -> int:
-        """Checks a table; returns the numbers between two of its rows."""
+    def _table(self, table, rows=None) -> Tuple[int, int, int]:
+        """Checks a table; returns the numbers between two of its rows, its rows and
+        its columns."""
         import torch
-        if table.dtype is torch.int32 and table.get_device() == self._gpu and table.dim() == 2 and \
-                (rows is None or table.shape[0] == rows) and (table.shape[1] == 1 or table.stride(1) == 1):
-            return table.stride(0) if table.shape[0] > 1 else table.shape[1]
+        if table.dtype is torch.int32 and table.get_device() == self._gpu and table.dim() == 2:
+            n, m = table.shape
+            if rows is None or n == rows:
+                if table.is_contiguous():
+                    return m, n, m
+                if m == 1 or table.stride(1) == 1:
+                    return table.stride(0) if n > 1 else m, n, m
         raise MapFlowError(MF_ERR_ARG, f"table must be an int32 tensor [{'n_seqs' if rows is None else rows}, max_pages] "
                                        f"on cuda:{self._gpu} with a row's numbers next to each other")
 
@@ -935,7 +943,7 @@ class PagedCache:
         ld_v = _rows("v", v, shape, dt, gpu)
         _vector("seq", seq, (T,), i32, gpu)
         _vector("at", at, (T,), i32, gpu)
-        ld_t = self._table(table)
+        table_shape = self._table(table)
         p_pos = p_w = turns = None
         rot, layout, gain = 0, 0, 1.0
         if positions is not None:
@@ -955,8 +963,8 @@ class PagedCache:
         if norm is None:
             norm = p_w is not None
         rc = self._append_call(
-            self._c, k.data_ptr(), ld_k, v.data_ptr(), ld_v, T, seq.data_ptr(), at.data_ptr(), table.data_ptr(), ld_t,
-            table.shape[0], table.shape[1], p_pos, turns, rot, layout, gain, p_w, norm, eps, raw)
+            self._c, k.data_ptr(), ld_k, v.data_ptr(), ld_v, T, seq.data_ptr(), at.data_ptr(), table.data_ptr(),
+            *table_shape, p_pos, turns, rot, layout, gain, p_w, norm, eps, raw)
         if rc:
             _check(rc)
 
@@ -976,16 +984,15 @@ class PagedCache:
         T = seq.shape[0]
         _vector("seq", seq, (T,), torch.int32, gpu)
         _vector("at", at, (T,), torch.int32, gpu)
-        ld_t = self._table(table)
+        table_shape = self._table(table)
         shape, ld = (T, self.H, self.d), []
         for name, t in (("k", k), ("v", v)):
             ld.append(self.H * self.d if t is None else _rows(name, t, shape, torch.bfloat16, gpu))
-        if k is None:
-            k = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
-        if v is None:
-            v = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
-        rc = self._read_call(self._c, T, seq.data_ptr(), at.data_ptr(), table.data_ptr(), ld_t, table.shape[0],
-                             table.shape[1], k.data_ptr(), ld[0], v.data_ptr(), ld[1], raw)
+        if k is None or v is None:
+            new = torch.zeros((1 + (k is v), *shape), dtype=torch.bfloat16, device=self.device)
+            k, v = new[0] if k is None else k, new[-1] if v is None else v
+        rc = self._read_call(self._c, T, seq.data_ptr(), at.data_ptr(), table.data_ptr(), *table_shape,
+                             k.data_ptr(), ld[0], v.data_ptr(), ld[1], raw)
         if rc:
             _check(rc)
         return k, v
@@ -1012,7 +1019,7 @@ class PagedCache:
         shape = n, Lq, H_q, _ = (*q.shape[:3], self.d)
         ld_q = _rows("q", q, shape, dt, gpu)
         _vector("lens", lens, (n,), torch.int32, gpu)
-        ld_t = self._table(table, n)
+        ld_t, _, max_pages = self._table(table, n)
         window, sinks = 0 if window is None else _span("window", window, 1), _span("sinks", sinks, 0)
         if softcap is None:
             softcap = 0.0
@@ -1034,9 +1041,16 @@ class PagedCache:
             bytes_ = ctypes.c_int64()
             _check(load_library().mf_attn_paged_workspace(Lq, H_q, self.H, self.d, ctypes.byref(bytes_)))
             need = self._ws_of[Lq, H_q] = bytes_.value
-        ws = torch.empty(need, dtype=torch.uint8, device=self.device)  # its own for every call: calls may overlap
+        # The default stream's calls follow each other and are never captured: they
+        # share a workspace (beside launches an allocation takes 6 us).  Others may
+        # overlap and have their own.
+        ws = _default_ws.get(gpu) if raw == 0 else None
+        if ws is None or ws.shape[0] < need:
+            ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+            if raw == 0:
+                _default_ws[gpu] = ws
         rc = self._attend_call(
-            self._c, n, Lq, H_q, q.data_ptr(), ld_q, table.data_ptr(), ld_t, table.shape[1], lens.data_ptr(),
+            self._c, n, Lq, H_q, q.data_ptr(), ld_q, table.data_ptr(), ld_t, max_pages, lens.data_ptr(),
             o.data_ptr(), ld_o, p_lse, p_slopes, softcap, window, sinks, self._scale if scale is None else scale,
             ws.data_ptr(), need, raw)
         if rc:

@@ -646,8 +646,9 @@ MF_API int mf_attn_status(mf_attn_t h, void* stream);
  *     a value is held as the e2m1 number (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
  *     negatives) nearest to x / (s g), ties to even, at most 6,
  *   and stands for that number times s g.  Which number that is goes by the exact
- *   value of x (fp64 decides where fp32 cannot).  A block with a value that is not
- *   finite is held as NaN.  16 tokens of a head are 18 d bytes,
+ *   value of x (two fp32 numbers, good to 2^-43, decide where one cannot).  A block
+ *   with a value that is not finite is held as NaN.  16 tokens of a head are 18 d
+ *   bytes,
  *     keys' codes    [16 tokens][d/2]             (even dimension in the low bits)
  *     values' codes  [2][d/16][8 tokens][8]
  *     keys' scales   [16 tokens][d/16]   values' scales [d/16][16 tokens]   (e4m3)
@@ -721,7 +722,7 @@ MF_API int mf_cache_read(const mf_cache_t* cache, int T, const int32_t* seq, con
  *   lse          fp32 [n * Lq][H_q] or NULL
  *   workspace    the caller's, 256-byte aligned, mf_attn_paged_workspace bytes; needs
  *                no initialisation and holds nothing between calls; calls that may
- *                overlap on the GPU need one each
+ *                overlap on the GPU need one each (calls on one stream do not)
  * Scores, softmax statistics, sums and partial results are fp32; a key's and
  * value's code times scale is exact; softmax weights are rounded to 11 bits for
  * their product with v (2^-32 of the row's largest at most where they are small),

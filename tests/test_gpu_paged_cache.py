@@ -1,6 +1,7 @@
 """A paged cache, appended to, read back and attended over, against the fp64
 definitions of tests/paged_ref.py."""
 import math
+import threading
 
 import pytest
 import torch
@@ -770,3 +771,45 @@ def test_steps_in_a_row_follow_each_other(dev, captured):
         torch.cuda.synchronize()
         for a, b in zip(o + [a for r in rows for a in r] + [pages], want):
             assert torch.equal(a, b)
+
+
+def test_threads_on_one_stream(dev):
+    """Calls of several threads on the default stream, which share its workspace."""
+    lens = [5000, 20, 3000]
+    g, pages, table, lens_t, gk, gv, keys = _world(dev, 33, 3, 2, 128, 64, lens)
+    cache = mapflow.PagedCache.fp4(pages, 64, 128, k_scale=gk, v_scale=gv)
+    qs = [_rnd(g, dev, 3, lq, 8, 128) for lq in (1, 1, 2, 8)]
+    want = [cache.attend(q, table, lens_t) for q in qs]
+    got = [[torch.zeros_like(q) for _ in range(100)] for q in qs]
+    torch.cuda.synchronize()
+
+    def work(q, out):
+        for o in out:
+            cache.attend(q, table, lens_t, o=o)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(qs, got)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(o, b) for o in a)
+
+
+def test_reading_into_given_and_new_tensors(dev):
+    g, pages, table, lens_t, gk, gv, keys = _world(dev, 34, 2, 3, 64, 16, [20, 33])
+    cache = mapflow.PagedCache.fp4(pages, 16, 64, k_scale=gk, v_scale=gv)
+    seq, at = _tokens([20, 33], dev)
+    seq[4] = -1
+    k, v = cache.read(seq, at, table)
+    assert k.is_contiguous() and v.is_contiguous() and (k[4] == 0).all() and (v[4] == 0).all() and k[5].any()
+    for given in ({"k"}, {"v"}, {"k", "v"}):
+        own = {name: torch.full_like(k, 7.0) for name in given}
+        got = cache.read(seq, at, table, **own)
+        for name, a, b in zip("kv", got, (k, v)):
+            assert name not in own or a is own[name]
+            assert (a[4] == (7 if name in own else 0)).all()
+            assert torch.equal(a[:4], b[:4]) and torch.equal(a[5:], b[5:])
+    empty = cache.read(seq[:0], at[:0], table)
+    assert empty[0].shape == empty[1].shape == (0, 3, 64)
