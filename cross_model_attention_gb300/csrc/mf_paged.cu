@@ -203,7 +203,21 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
   Part* parts = reinterpret_cast<Part*>(smem + C::kParts) + warp * C::kQueue;
   Piece* pieces = reinterpret_cast<Piece*>(smem + C::kPieces);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // what comes after may be set up
-  asm volatile("griddepcontrol.wait;" ::: "memory");               // what came before may still run
+  // What came before may still run.  Meanwhile q, the lengths and the table come
+  // as far as L2, which has the newest of what is still being written: a line to a
+  // thread.  (A window of 4096 keys of 32 requests 34.1 us for 33.6.)
+  {
+    const long long x = static_cast<long long>(threadIdx.x) * gridDim.x + blockIdx.x;
+    auto ask = [&](const void* base, long long rows, long long ld, unsigned lines) {
+      if (x >= rows * lines) return;
+      const unsigned y = static_cast<unsigned>(x) / lines;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(base) + y * ld + (static_cast<unsigned>(x) - y * lines) * 128u));
+    };
+    ask(p.q, static_cast<long long>(p.n) * p.Lq, p.ld_q * 2, p.H_kv * p.G * D / 64);
+    ask(p.lens, 1, 0, (p.n + 31) / 32);
+    ask(p.table, p.n, p.ld_table * 4, (p.max_pages + 31) / 32);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---- the lines: a thread sums those of consecutive requests
   const int share = (p.n + T - 1) / T;
@@ -458,10 +472,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
     float acc[D / 16][NT][4], lift[NT][2], l[NT][2], coef[NT][2];  // lift: kLift less the reference
     int rg0;
     const int h0 = head_of(d.u, rg0);
+    uint4 qn[C::kQShared ? NT : 1][D / 32];
+    if (C::kQShared) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) load_rows(d.r, h0, rg0, nt, qn[C::kQShared ? nt : 0]);
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      uint4* w = qw[C::kQShared ? 0 : nt];
-      if (C::kQShared) load_rows(d.r, h0, rg0, nt, w);
+      const uint4* w = C::kQShared ? qn[C::kQShared ? nt : 0] : qw[C::kQShared ? 0 : nt];
       uint32_t top = 0;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
@@ -814,7 +832,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
       v[0] = x.x, v[1] = x.y;
     }
   };
-  constexpr int RI = NT;  // rows at a time
+  // (16 rows four at a time, so that a CTA with many short units has enough loads in
+  // flight: 64 rows of 8 requests of 500 to 7500 keys 57.1 us with two, 54.2 with four)
+  constexpr int RI = NT == 1 ? 1 : 4;
   const int row_items = (p.rows + RI - 1) / RI;
   for (int item = warp; item < n_groups * row_items; item += W) {
     const int at_group = item / row_items, row0 = (item - at_group * row_items) * RI;
@@ -848,25 +868,38 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
     auto ml_of = [&](int w, int x) {
       return group >> (2 * w + 1) & 1 ? reinterpret_cast<const float2*>(smem + w * C::kRing + C::R * D * 4)[row[x]] : make_float2(-INFINITY, 0.f);
     };
-#pragma unroll 4
-    for (int w = w0; w < w1; ++w)
+    constexpr int kAtOnce = 4 / RI;
+    for (int w = w0; w < w1; w += kAtOnce)
 #pragma unroll
-      for (int x = 0; x < RI; ++x) M[x] = fmaxf(M[x], ml_of(w, x).x);
+      for (int j = 0; j < kAtOnce; ++j)
+#pragma unroll
+        for (int x = 0; x < RI; ++x) M[x] = fmaxf(M[x], w + j < w1 ? ml_of(w + j, x).x : -INFINITY);
 #pragma unroll
     for (int x = 0; x < RI; ++x) M[x] = fmaxf(M[x], ml_far[x].x);
-#pragma unroll 4
-    for (int w = w0; w < w1; ++w) {
-      if (!(group >> (2 * w + 1) & 1)) continue;
+    for (int w = w0; w < w1; w += kAtOnce) {
+      float2 ml[kAtOnce][RI];
+      float v[kAtOnce][RI][E];
 #pragma unroll
-      for (int x = 0; x < RI; ++x) {
-        const float2 ml = ml_of(w, x);
-        const float f = weight_of(ml.x, ml.y, M[x]);
-        float v[E];
-        take(reinterpret_cast<const float*>(smem + w * C::kRing) + row[x] * D + lane * E, v);
-        L[x] = fmaf(f, ml.y, L[x]);
+      for (int j = 0; j < kAtOnce; ++j)
 #pragma unroll
-        for (int e = 0; e < E; ++e) out[x][e] = fmaf(f, v[e], out[x][e]);
-      }
+        for (int x = 0; x < RI; ++x) {
+          ml[j][x] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[j][x][e] = 0.f;
+          if (w + j < w1 && (group >> (2 * (w + j) + 1) & 1)) {
+            ml[j][x] = ml_of(w + j, x);
+            take(reinterpret_cast<const float*>(smem + (w + j) * C::kRing) + row[x] * D + lane * E, v[j][x]);
+          }
+        }
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+#pragma unroll
+        for (int x = 0; x < RI; ++x) {
+          const float f = weight_of(ml[j][x].x, ml[j][x].y, M[x]);
+          L[x] = fmaf(f, ml[j][x].y, L[x]);
+#pragma unroll
+          for (int e = 0; e < E; ++e) out[x][e] = fmaf(f, v[j][x][e], out[x][e]);
+        }
     }
 #pragma unroll
     for (int x = 0; x < RI; ++x) {
@@ -905,7 +938,7 @@ __global__ void __launch_bounds__(32) join_kernel(const PagedParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x, row = blockIdx.y, lane = threadIdx.x;
   auto spot = [&](int k) { return (k == 0 ? 2ll * c + 1 : 2ll * (c + k)) * p.rows + row; };
-  // Two results are asked for before it is known which there are, then 16 at a
+  // Two results are asked for before it is known which there are, then 16 or 8 at a
   // time.  (Four, each replaced as it is added: one request of 16000 keys, in 19
   // CTAs to a head, 16.5 us for 13.2; 1000 keys 12.2 for 9.3.)
   constexpr int kAhead = 2, E = D / 32;
@@ -928,7 +961,7 @@ __global__ void __launch_bounds__(32) join_kernel(const PagedParams p) {
   for (int j = 0; j < kAhead; ++j) take(min(j, most - 1), v[j], ml[j]);
   if (cut.x < 0) return;
   const int n = cut.z - c + 1;
-  constexpr int kMore = 16;
+  constexpr int kMore = 16 / NT;
   float w[kMore][E];
   float2 wl[kMore];
   auto ask = [&](int k0) {
