@@ -14,20 +14,20 @@
 // values, whatever the order of sums.  In units of 2^-24 of a pair's |a| + |b|, fp32
 // is good to 7 for angle, sine, cosine and the products with them, 5 for the
 // quotient and 7.1 for the norm's sum and root: 20 with the norm and 16
-// without are counted, and a row with a value that near to a step (one in a hundred)
-// is done again in twice that precision, by the warp that finds it, once its other
+// without are counted, and blocks with a value that near to a step (in one row of
+// 150) are done again in twice that precision, by the warp that finds them, once its
 // rows are done (mf_ff.cuh: 2^-43, which leaves one value in 10^11 undecided).  What
 // is exact in fp32 (values, keys that are neither normed nor rotated) often lies on
 // a step itself: its quotient is corrected by its residue, which finds those exactly.
 //
 // Bound: HBM for bf16 rows (4099 tokens of 40 heads of 128 put in their places in
 // 30 us, 5.6 TB/s, 82 % of the copy rate) and reading (32000 tokens of 8 heads 29 us,
-// 5.8 TB/s); instructions for 4 bits (16384 tokens of 8 heads 40 us, 2.2 TB/s: 560
-// to a warp's keys and values of a head, half of the issue slots).
+// 5.8 TB/s); instructions for 4 bits (16384 tokens of 8 heads 31 us, 2.8 TB/s; 26
+// where no block has to be done again).
 //
-// Lanes as in the rotary kernel: d / 16 lanes to a head's row, each
-// with two chunks of 8 dimensions that hold both halves of its pairs, sines and
-// cosines kept over a token's heads.  A value's 4-bit codes lie by block, then
+// Lanes as in the rotary kernel: d / 16 lanes to a head's row, each with two chunks
+// of 8 dimensions that hold both halves of its pairs, sines and cosines kept over a
+// token's heads.  A value's 4-bit codes lie by block, then
 // token: the lanes of a warp, which hold neighbouring tokens, exchange them so
 // that neighbouring lanes write neighbouring bytes.
 #include <cstdint>
@@ -291,6 +291,8 @@ __device__ __forceinline__ Sector get16(const __nv_bfloat16* from, bool even) {
 }
 
 // ------------------------------------------------------------------ append --
+// (Four CTAs to an SM: 16384 tokens of 8 heads 31.3 us; three 33.8, five, which
+// spill, 34.9.)
 template <int D, int LAYOUT, bool FP4>
 __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p) {
   constexpr int LPR = D / 16;            // lanes to a row
@@ -424,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
 
   float gk_next = FP4 && here && p.k_scale ? p.k_scale[h_begin] : 1.f;
   float gv_next = FP4 && here && p.v_scale ? p.v_scale[h_begin] : 1.f;
-  unsigned again = 0;  // of 32 heads: those to be done more exactly
+  unsigned again = 0;  // of 32 heads: those with blocks to be done more exactly
 #pragma unroll 1
   for (int ib = 0; ib < p.heads_per_unit; ib += kAhead)
 #pragma unroll
@@ -434,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
     unpack8(ka[ja], a);
     unpack8(kb[ja], a + 8);
     const bool live = i < n;
-    bool near = false;  // whether the row is to be done more exactly
+    bool near = false;  // whether the lane's blocks are to be done more exactly
     const Sector v = vw[ja];
     load(i + kAhead, ja);
     float r = 1.f;  // the norm's factor
@@ -668,8 +670,9 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const CacheParams p) {
 
 // A token's heads in shares: all of them to one group of lanes where that
 // leaves every SM about `rounds` rounds, else spread.  (Appending, whose groups
-// begin with sines and cosines, two: 16384 tokens of 8 heads 43.0 us, with eight
-// 45.3; reading eight: the same 16.4 us, with two 17.0.)
+// begin with sines and cosines, two: 16384 tokens of 8 heads 31.3 us, with eight
+// 33.2; 4099 of 40 heads in bf16 30.0, with one 34.3 and with four 32.0.  Reading
+// eight: the same 16384 16.4 us, with two 17.0.)
 template <typename F>
 cudaError_t spread(CacheParams p, long long T, int D, int rounds, F&& go) {
   const int groups = kThreads / (D / 16);
