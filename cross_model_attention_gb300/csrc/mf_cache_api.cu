@@ -289,4 +289,24 @@ int mf_attn_paged(const mf_cache_t* cache, int n, int Lq, int H_q, const void* q
   return MF_OK;
 }
 
+int mf_cache_append_args(const mf_cache_append_args_t* a) {
+  if (!a) return fail(MF_ERR_ARG, "args is NULL");
+  return mf_cache_append(a->cache, a->k, a->ld_k_in, a->v, a->ld_v_in, a->T, a->seq, a->at, a->table, a->ld_table, a->n_seqs,
+                         a->max_pages, a->positions, a->turns, a->rot_dim, a->layout, static_cast<float>(a->gain),
+                         a->k_weight, a->norm, static_cast<float>(a->eps), a->stream);
+}
+
+int mf_cache_read_args(const mf_cache_read_args_t* a) {
+  if (!a) return fail(MF_ERR_ARG, "args is NULL");
+  return mf_cache_read(a->cache, a->T, a->seq, a->at, a->table, a->ld_table, a->n_seqs, a->max_pages, a->k_out, a->ld_k_out,
+                       a->v_out, a->ld_v_out, a->stream);
+}
+
+int mf_attn_paged_args(const mf_attn_paged_args_t* a) {
+  if (!a) return fail(MF_ERR_ARG, "args is NULL");
+  return mf_attn_paged(a->cache, a->n, a->Lq, a->H_q, a->q, a->ld_q, a->table, a->ld_table, a->max_pages, a->lens, a->o,
+                       a->ld_o, a->lse, a->slopes, static_cast<float>(a->softcap), a->window, a->n_sink,
+                       static_cast<float>(a->scale), a->workspace, a->workspace_bytes, a->stream);
+}
+
 }  // extern "C"

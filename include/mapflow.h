@@ -740,6 +740,59 @@ MF_API int mf_attn_paged(const mf_cache_t* cache, int n, int Lq, int H_q, const 
                          float scale, void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
+ * The three calls with their arguments in one piece of memory, for callers to whom
+ * an argument costs something (a step of a small batch makes several of these calls
+ * a layer).  Fields as the parameters above, checks and errors the same; NULL
+ * arguments: MF_ERR_ARG.  Nothing is kept of `args` after the call.
+ */
+typedef struct {
+  const mf_cache_t* cache;
+  const void* k;
+  int64_t ld_k_in;
+  const void* v;
+  int64_t ld_v_in;
+  const int32_t *seq, *at, *table;
+  int64_t ld_table;
+  const int32_t* positions;
+  const uint64_t* turns;
+  const void* k_weight;
+  void* stream;
+  double gain, eps;      /* (rounded to fp32) */
+  int T, n_seqs, max_pages, rot_dim, layout, norm;
+} mf_cache_append_args_t;
+typedef struct {
+  const mf_cache_t* cache;
+  const int32_t *seq, *at, *table;
+  int64_t ld_table;
+  void* k_out;
+  int64_t ld_k_out;
+  void* v_out;
+  int64_t ld_v_out;
+  void* stream;
+  int T, n_seqs, max_pages, unused;
+} mf_cache_read_args_t;
+typedef struct {
+  const mf_cache_t* cache;
+  const void* q;
+  int64_t ld_q;
+  const int32_t* table;
+  int64_t ld_table;
+  const int32_t* lens;
+  void* o;
+  int64_t ld_o;
+  float* lse;
+  const float* slopes;
+  void* workspace;
+  int64_t workspace_bytes;
+  void* stream;
+  double softcap, scale; /* (rounded to fp32) */
+  int n, Lq, H_q, max_pages, window, n_sink;
+} mf_attn_paged_args_t;
+MF_API int mf_cache_append_args(const mf_cache_append_args_t* args);
+MF_API int mf_cache_read_args(const mf_cache_read_args_t* args);
+MF_API int mf_attn_paged_args(const mf_attn_paged_args_t* args);
+
+/*
  * mf_selftest_wait — failure-detection self-test (no counterpart on the
  * pages).  Launches one thread that waits on a device barrier nothing will
  * complete, bounded by `limit_ms` milliseconds (1..10000); the wait gives up,

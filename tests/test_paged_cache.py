@@ -212,3 +212,54 @@ def test_more_keys_than_a_call_counts_are_refused(lib, kw):
     c = _cache(**kw.pop("cache", {}))
     assert _attend(lib, c, **dict(kw, q=1 << 44, o=1 << 45)) == E.MF_ERR_UNSUPPORTED
     assert "too many keys" in lib.mf_last_error().decode()
+
+
+def test_calls_with_their_arguments_in_one_piece(lib):
+    """The struct forms check and refuse as the plain calls do, field by field."""
+    good, bad = _cache(), _cache(d=96)
+
+    def append(cache=good, k=3 * PTR, ld_k=1024, v=4 * PTR, ld_v=1024, seq=5 * PTR, at=6 * PTR, table=7 * PTR, ld_table=4,
+               positions=0, turns=8 * PTR, w=0, gain=1.0, eps=1e-6, T=5, n_seqs=2, max_pages=4, rot=128, layout=0, norm=0):
+        return lib.mf_cache_append_args(mapflow._append_args(
+            ctypes.addressof(cache), k, ld_k, v, ld_v, seq, at, table, ld_table, positions, turns, w, 0, gain, eps, T, n_seqs,
+            max_pages, rot, layout, norm))
+
+    def read(cache=good, seq=5 * PTR, at=6 * PTR, table=7 * PTR, ld_table=4, k=3 * PTR, ld_k=1024, v=4 * PTR, ld_v=1024, T=5,
+             n_seqs=2, max_pages=4):
+        return lib.mf_cache_read_args(mapflow._read_args(ctypes.addressof(cache), seq, at, table, ld_table, k, ld_k, v, ld_v,
+                                                         0, T, n_seqs, max_pages, 0))
+
+    def attend(cache=good, q=3 * PTR, ld_q=4096, table=7 * PTR, ld_table=4, lens=5 * PTR, o=4 * PTR, ld_o=4096, lse=0, slopes=0,
+               ws=9 * PTR, ws_bytes=1 << 40, softcap=0.0, scale=0.1, n=3, Lq=1, H_q=32, max_pages=4, window=0, n_sink=0):
+        return lib.mf_attn_paged_args(mapflow._paged_args(
+            ctypes.addressof(cache), q, ld_q, table, ld_table, lens, o, ld_o, lse, slopes, ws, ws_bytes, 0, softcap, scale, n,
+            Lq, H_q, max_pages, window, n_sink))
+
+    def fails(call, word, code=E.MF_ERR_ARG, **kw):
+        assert call(**kw) == code, (word, kw)
+        assert word in lib.mf_last_error().decode(), (word, lib.mf_last_error())
+
+    assert append(T=0) == read(T=0) == attend(n=0) == E.MF_OK
+    for call in (append, read, attend):
+        fails(call, "d = 96", E.MF_ERR_UNSUPPORTED, cache=bad)
+        fails(call, "max_pages", max_pages=0)
+        fails(call, "table", table=0)
+        fails(call, "table", ld_table=3)
+    for call in (append, read):
+        for name in ("seq", "at"):
+            fails(call, name, **{name: 0})
+            fails(call, name, **{name: PTR + 1})
+        fails(call, "k", k=0), fails(call, "v", v=0), fails(call, "k", ld_k=1016), fails(call, "v", ld_v=1028)
+        fails(call, "T must", T=-1)
+        fails(call, "no rows", n_seqs=0)
+    fails(append, "positions", positions=PTR + 2), fails(append, "turns", turns=0), fails(append, "k_weight", w=PTR + 2, norm=1)
+    fails(append, "weight without", w=PTR), fails(append, "gain", gain=float("inf")), fails(append, "gain", gain=1e300)
+    fails(append, "eps", norm=1, eps=0.0), fails(append, "eps", norm=1, eps=1e300), fails(append, "rot_dim", rot=7)
+    fails(append, "layout", layout=2), fails(append, "norm", norm=2)
+    fails(attend, "q", q=0), fails(attend, "q", ld_q=4088), fails(attend, "lens", lens=0), fails(attend, "o", o=0)
+    fails(attend, "o", ld_o=4100), fails(attend, "lse", lse=PTR + 2), fails(attend, "slopes", slopes=PTR + 1)
+    fails(attend, "workspace", ws=0), fails(attend, "softcap", softcap=-1.0), fails(attend, "softcap", softcap=1e300)
+    fails(attend, "scale", scale=0.0), fails(attend, "scale", scale=1e300), fails(attend, "n must", n=-1)
+    fails(attend, "Lq", Lq=0), fails(attend, "H_q", H_q=12), fails(attend, "window", window=-1), fails(attend, "n_sink", n_sink=-1)
+    for call in (lib.mf_cache_append_args, lib.mf_cache_read_args, lib.mf_attn_paged_args):
+        assert call(None) == E.MF_ERR_ARG
