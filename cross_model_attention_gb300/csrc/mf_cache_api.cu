@@ -13,7 +13,8 @@ using namespace mf;
 
 namespace {
 
-// A sequence's tokens: positions stay exact in fp32 (as distances) and in int.
+// A sequence's tokens: tiles and distances stay in int (as fp32, for a bias by
+// distance, they are off by 2^-24 of themselves at most).
 constexpr long long kMaxKeys = 1ll << 26;
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -235,6 +236,7 @@ int mf_attn_paged(const mf_cache_t* cache, int n, int Lq, int H_q, const void* q
   if (n_sink < 0) return fail(MF_ERR_ARG, "n_sink must be >= 0");
   if (!(scale > 1e-30f && scale < 1e30f)) return fail(MF_ERR_ARG, "scale must be positive and finite");
   if (!(softcap >= 0.f && softcap < 1e30f) || (softcap > 0.f && softcap < 1e-30f)) return fail(MF_ERR_ARG, "softcap must be positive and finite (0: none)");
+  if (softcap > 0.f && !(scale / softcap > 1e-30f && scale / softcap < 1e30f)) return fail(MF_ERR_ARG, "scale / softcap is out of range");
   const int H = cache->H, d = cache->d;
   if ((rc = check_shape(Lq, H_q, H, d)) != MF_OK) return rc;
   if (n == 0) return MF_OK;

@@ -714,7 +714,8 @@ MF_API int mf_cache_read(const mf_cache_t* cache, int T, const int32_t* seq, con
  *   lens         DEVICE int32 [n], held to [0, max_pages * page_size <= 2^26]; read on
  *                the device, so that a captured graph follows it (and the table)
  *                from replay to replay
- *   slopes       DEVICE fp32 [H_q] or NULL      softcap  0: none
+ *   slopes       DEVICE fp32 [H_q] or NULL
+ *   softcap      0: none; scale and scale / softcap lie in (1e-30, 1e30)
  *   window       >= 1, or 0: no window          n_sink   >= 0
  *   n            at most 2^20; n * (max_pages * page_size / 32 + 2) below 2^31, and
  *                that times H and a 16th of the rows of a head, Lq * H_q / H, rounded
@@ -723,7 +724,8 @@ MF_API int mf_cache_read(const mf_cache_t* cache, int T, const int32_t* seq, con
  *   workspace    the caller's, 256-byte aligned, mf_attn_paged_workspace bytes; needs
  *                no initialisation and holds nothing between calls; calls that may
  *                overlap on the GPU need one each (calls on one stream do not)
- * Scores, softmax statistics, sums and partial results are fp32; a key's and
+ * Scores, softmax statistics, sums and partial results are fp32 (scores below
+ * -1e30 count as keys that are not seen); a key's and
  * value's code times scale is exact; softmax weights are rounded to 11 bits for
  * their product with v (2^-32 of the row's largest at most where they are small),
  * not for the sum that it is divided by.  What is not finite in a key reaches the

@@ -813,3 +813,18 @@ def test_reading_into_given_and_new_tensors(dev):
             assert torch.equal(a[:4], b[:4]) and torch.equal(a[5:], b[5:])
     empty = cache.read(seq[:0], at[:0], table)
     assert empty[0].shape == empty[1].shape == (0, 3, 64)
+
+
+@pytest.mark.parametrize("layout,rot", [("half", 64), ("interleaved", 64), ("half", 20)])
+def test_append_of_more_heads_than_32_at_once(dev, layout, rot):
+    """A prompt long enough for a group of lanes to take all 40 heads of a token."""
+    g, H, d, ps, T = _gen(dev, 35 + rot), 40, 64, 64, 5000
+    k, v = _rnd(g, dev, T, H, d), _rnd(g, dev, T, H, d)
+    seq, at = _tokens([T], dev)
+    table = torch.randperm((T + ps - 1) // ps, generator=g, device=dev).to(torch.int32)[None]
+    gk, gv = _scales(g, dev, H), _scales(g, dev, H)
+    pages = _pages(dev, table.shape[1], H, ps, d)
+    cache = mapflow.PagedCache.fp4(pages, ps, d, k_scale=gk, v_scale=gv)
+    cache.append(k, v, seq, at, table, rope=mapflow.RotaryPlan(rot, layout=layout), norm=True)
+    y, _ = _rotated(k, None, True, at, True, layout, rot)
+    _check_held(pages, ps, d, *_slots(seq, at, table, ps), y, v, gk, gv)

@@ -122,6 +122,7 @@ def test_a_bf16_cache_apart_from_what_goes_in(lib):
     (dict(o=3 * PTR), E.MF_ERR_ARG), (dict(window=-1), E.MF_ERR_ARG), (dict(n_sink=-1), E.MF_ERR_ARG),
     (dict(scale=0.0), E.MF_ERR_ARG), (dict(scale=float("nan")), E.MF_ERR_ARG), (dict(softcap=-1.0), E.MF_ERR_ARG),
     (dict(softcap=float("inf")), E.MF_ERR_ARG), (dict(softcap=float("nan")), E.MF_ERR_ARG), (dict(ws=None), E.MF_ERR_ARG),
+    (dict(softcap=1e-20, scale=1e15), E.MF_ERR_ARG), (dict(softcap=1e20, scale=1e-15), E.MF_ERR_ARG),
     (dict(ws=9 * PTR + 128), E.MF_ERR_ARG)])
 def test_attend_refuses(lib, kw, code):
     assert _attend(lib, _cache(), **kw) == code
