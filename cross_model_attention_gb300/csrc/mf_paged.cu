@@ -39,7 +39,7 @@
 // on the instructions of 12 warps are the bound: 144 us over 16384 keys with 9 to 16
 // rows, as much again for every further 16.  So they are with heads of 64, whose keys
 // have half the bytes but the same softmax (68 us over 16384 keys, 4.4 TB/s), and
-// with capped scores (135 us).
+// with capped scores (122 us).
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -85,7 +85,8 @@ struct Cfg {
   static constexpr int kParts = kLens + 4 * kLensHere;
   static constexpr int kPieces = kParts + 32 * W * kQueue;
   static constexpr int kWalk = kPieces + 16 * 2 * W;
-  static constexpr int kBytes = kWalk + 48 * W;
+  static constexpr int kRows = kWalk + 48 * W;           // [R] slope and position of each row
+  static constexpr int kBytes = kRows + 8 * R * W;
   static_assert(kBytes <= 232448, "shared memory");
   static_assert(R * D * 4 + R * 8 <= kRing, "a partial result in a warp's ring");
   static_assert(S >= 2 && S + 1 <= kQueue && 32 % NB == 0 && S * NB <= 32, "ring");
@@ -136,8 +137,9 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 // tanh: by its series below 0.3, above by the exponential, 1 - 2 / (1 + e^2a); off
-// by 2^-20 of it.  (With tanhf 32 requests of 16384 keys with capped
-// scores take 158 us, with this 138.)
+// by 2^-20 of it.  (With tanhf 32 requests of 16384 keys with capped scores took 158
+// us, with this 138, and 122 since a tile's are taken together; two by two in packed
+// arithmetic 2 more.)
 __device__ __forceinline__ float tanh_of(float x) {
   const float a = fabsf(x), q = x * x;
   float r;
@@ -201,7 +203,9 @@ __device__ __forceinline__ void store_row(const PagedParams& p, int r, int u, in
   if (p.lse && lane == 0) p.lse[x.tok * (p.H_kv * p.G) + x.head] = lse_of(M, L);
 }
 
-template <int D, int NT>
+// SPECIAL: scores are capped or there is a bias by distance.  (In one kernel with the
+// rest 9 to 16 rows over 16384 keys took 148 us, not 143, and one to 8 rows 108.6.)
+template <int D, int NT, bool SPECIAL>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const PagedParams p) {
   using C = Cfg<D, NT>;
   constexpr int W = C::W, NB = C::NB, TK = C::TK, S = C::S, T = C::kThreads;
@@ -464,7 +468,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
   }
 
   // ---- parts and their tiles
-  const bool special = p.cap > 0.f || p.slopes;
   int slot = 0;
   bool q_here = have || pushed > 0;
   __syncwarp();
@@ -505,7 +508,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
       const int e = top == 0 || !fine ? 0 : min(120, 141 - ex);
       const float up = __int_as_float((e + 127) << 23);
       float c = p.scale * kscale * __int_as_float((127 - e) << 23);
-      c *= p.cap > 0.f ? 1.f / p.cap : kLog2e;
+      c *= SPECIAL && p.cap > 0.f ? 1.f / p.cap : kLog2e;
       if (!fine) c = NAN;
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) {
@@ -536,6 +539,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
         for (int e = 0; e < 4; ++e) acc[a][nt][e] = 0.f;
 
     const int len = d.len, last_tile = d.i1, ta = d.ta, skip = d.tb - d.ta;
+    float2* rows_s = reinterpret_cast<float2*>(smem + C::kRows) + warp * C::R;
+    if (SPECIAL) {
+      __syncwarp();
+      if (lane < C::R) {
+        int tt, gg;
+        const bool is = split(rg0 * C::R + lane, tt, gg);
+        rows_s[lane] = make_float2(is && p.slopes ? p.slopes[h0 * p.G + gg] * kLog2e : 0.f, __int_as_float(is ? len - p.Lq + tt : -1));
+      }
+      __syncwarp();
+    }
 #pragma unroll 1
     for (int ci = d.i0; ci < last_tile; ++ci) {
       cp_wait<S - 2>();
@@ -610,42 +623,59 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) by[nt][j] = coef[nt][j];
-      if (special || !whole) {
-        int rg;
-        const int h = head_of(d.u, rg);
+      if (SPECIAL && p.cap > 0.f) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[b][nt][e] = p.cap * kLog2e * tanh_of(x[b][nt][e] * coef[nt][e & 1]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) by[nt][0] = by[nt][1] = 1.f;
+      }
+      if (SPECIAL && p.slopes) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float4 two = *reinterpret_cast<const float4*>(rows_s + nt * 8 + 2 * t);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            int tt, gg;
-            const bool is = split(rg * C::R + nt * 8 + 2 * t + k, tt, gg);
-            const int row = is ? len - p.Lq + tt : -1;
-            if (special) {
-              const float slope = is && p.slopes ? p.slopes[h * p.G + gg] * kLog2e : 0.f;
-              const float near = static_cast<float>(key0 + g - row);  // less what the row is away, in keys
+            const float slope = k ? two.z : two.x;
+            const float near = static_cast<float>(key0 + g - __float_as_int(k ? two.w : two.y));  // less what the row is away, in keys
 #pragma unroll
-              for (int b = 0; b < NB; ++b)
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int e = k; e < 4; e += 2) {
-                  float y = x[b][nt][e] * coef[nt][k];
-                  if (p.cap > 0.f) y = p.cap * kLog2e * tanh_of(y);
-                  x[b][nt][e] = fmaf(slope, near + static_cast<float>(16 * b + (e & 2) * 4), y);
-                }
-              by[nt][k] = 1.f;
-            }
-            if (!whole) {
-              const int far0 = row - key0 - g;  // to the lane's first key
-#pragma unroll
-              for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int e = k; e < 4; e += 2) {
-                  const int far = far0 - (16 * b + (e & 2) * 4);
-                  const bool seen = far >= 0 && (far < p.window || row - far < p.n_sink) && !(gone >> b & 1);
-                  x[b][nt][e] = seen ? x[b][nt][e] * by[nt][k] : -INFINITY;
-                }
-              by[nt][k] = 1.f;
-            }
+              for (int e = k; e < 4; e += 2)
+                x[b][nt][e] = fmaf(slope, near + static_cast<float>(16 * b + (e & 2) * 4), x[b][nt][e] * by[nt][k]);
+            by[nt][k] = 1.f;
           }
+        }
+      }
+      if (!whole) {
+        int rg;
+        if (!SPECIAL) head_of(d.u, rg);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            int row;
+            if (SPECIAL) {
+              row = __float_as_int(rows_s[nt * 8 + 2 * t + k].y);
+            } else {
+              int tt, gg;
+              row = split(rg * C::R + nt * 8 + 2 * t + k, tt, gg) ? len - p.Lq + tt : -1;
+            }
+            const int far0 = row - key0 - g;  // to the lane's first key
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int e = k; e < 4; e += 2) {
+                const int far = far0 - (16 * b + (e & 2) * 4);
+                const bool seen = far >= 0 && (far < p.window || row - far < p.n_sink) && !(gone >> b & 1);
+                x[b][nt][e] = seen ? x[b][nt][e] * by[nt][k] : -INFINITY;
+              }
+            by[nt][k] = 1.f;
+          }
+        }
       }
 
       // exponents, and the rows' references
@@ -1004,18 +1034,18 @@ __global__ void __launch_bounds__(32) join_kernel(const PagedParams p) {
   store_row<D>(p, cut.x, cut.y, row, 8 * NT, M, L, out);
 }
 
-template <int D, int NT>
+template <int D, int NT, bool SPECIAL>
 cudaError_t launch_t(PagedParams p, cudaStream_t s) {
   using C = Cfg<D, NT>;
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = once_per_device(done, [] {
-    return cudaFuncSetAttribute(paged_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+    return cudaFuncSetAttribute(paged_kernel<D, NT, SPECIAL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
   });
   if (e != cudaSuccess) return e;
   int sms = 0;
   if ((e = sm_count(&sms)) != cudaSuccess) return e;
   p.inv_grid = std::nextafterf(1.f / sms, 1.f);
-  if ((e = launch_early(paged_kernel<D, NT>, dim3(sms), C::kThreads, C::kBytes, s, p)) != cudaSuccess) return e;
+  if ((e = launch_early(paged_kernel<D, NT, SPECIAL>, dim3(sms), C::kThreads, C::kBytes, s, p)) != cudaSuccess) return e;
   return launch_early(join_kernel<D, NT>, dim3(sms, p.rows), 32, 0, s, p);
 }
 
@@ -1041,8 +1071,12 @@ cudaError_t launch_paged(const PagedParams& p, int d, cudaStream_t s) {
   // a call's two launches follow each other, so that calls of several threads on one stream may share a workspace
   static std::mutex mutex;
   const std::lock_guard<std::mutex> lock(mutex);
-  if (row_tiles(p.Lq * p.G) == 1) return d == 128 ? launch_t<128, 1>(p, s) : launch_t<64, 1>(p, s);
-  return d == 128 ? launch_t<128, 2>(p, s) : launch_t<64, 2>(p, s);
+  auto launch = [&](auto special) {
+    constexpr bool kSpecial = decltype(special)::value;
+    if (row_tiles(p.Lq * p.G) == 1) return d == 128 ? launch_t<128, 1, kSpecial>(p, s) : launch_t<64, 1, kSpecial>(p, s);
+    return d == 128 ? launch_t<128, 2, kSpecial>(p, s) : launch_t<64, 2, kSpecial>(p, s);
+  };
+  return p.cap > 0.f || p.slopes ? launch(std::true_type()) : launch(std::false_type());
 }
 
 }  // namespace mf
