@@ -39,7 +39,7 @@
 // on the instructions of 12 warps are the bound: 144 us over 16384 keys with 9 to 16
 // rows, as much again for every further 16.  So they are with heads of 64, whose keys
 // have half the bytes but the same softmax (68 us over 16384 keys, 4.4 TB/s), and
-// with capped scores (122 us).
+// with capped scores (121 us).
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -138,7 +138,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 // tanh: by its series below 0.3, above by the exponential, 1 - 2 / (1 + e^2a); off
 // by 2^-20 of it.  (With tanhf 32 requests of 16384 keys with capped scores took 158
-// us, with this 138, and 122 since a tile's are taken together; two by two in packed
+// us, with this 138, and 121 since a tile's are taken together; two by two in packed
 // arithmetic 2 more.)
 __device__ __forceinline__ float tanh_of(float x) {
   const float a = fabsf(x), q = x * x;
@@ -401,6 +401,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
   bool have = next_part();
   if (have) load_q(parts[0].r, parts[0].u);  // (before the first tiles: what is asked for first comes first)
 
+  // The tile that is the n-th of a part.  Under a bias by distance scores rise towards
+  // the newest key: from there back the reference stays where the first tile puts it.
+  // (32 requests of 16384 keys with slopes 114 us, from the oldest on 126; 9 to 16 rows
+  // that are capped too 185 and 218.)
+  auto nth = [](const Part& x, int n) { return SPECIAL ? x.i0 + x.i1 - 1 - n : n; };
+
   int fill = 0;            // the ring's next slot
   unsigned bad = 0;        // of the ring's blocks: those on no page, NB bits to a slot
   long long offs = 0;      // of the lane's block of 32: its bytes' place, or -1
@@ -412,11 +418,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
       if (at_block == 32) {
         at_block = 0;
         const Part& x = parts[(pushed - 1) & (C::kQueue - 1)];
-        const int ii = i + lane / NB, b = lane % NB;
-        const int tile = ii < x.ta ? ii : x.tb + ii - x.ta;
+        const int at = i + lane / NB, b = lane % NB;
+        const int ii = nth(x, at), tile = ii < x.ta ? ii : x.tb + ii - x.ta;
         const int key = (tile * NB + b) * kFp4Block;
         offs = -1;
-        if (ii < i1 && key < x.len) {
+        if (at < i1 && key < x.len) {
           const int page = key / p.ps;
           const int id = p.table[x.r * p.ld_table + page];
           int rg;
@@ -557,7 +563,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
       const uint8_t* st = smem + warp * C::kRing + slot * C::kStage;
       const unsigned gone = bad >> (slot * NB) & ((1u << NB) - 1u);
       if (++slot == S) slot = 0;
-      const int key0 = (ci < ta ? ci : ci + skip) * TK;
+      const int ii = nth(d, ci), key0 = (ii < ta ? ii : ii + skip) * TK;
+      const bool whole = key0 + TK - 1 <= len - p.Lq && gone == 0 && (len - 1 - key0 < p.window || key0 + TK <= p.n_sink);
 
       // S = K q^T: rows are keys, columns the unit's rows
       float x[NB][NT][4];
@@ -617,7 +624,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
       }
 
       // scores in base 2: x times its factor
-      const bool whole = key0 + TK - 1 <= len - p.Lq && gone == 0 && (len - 1 - key0 < p.window || key0 + TK <= p.n_sink);
       float by[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -629,9 +635,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[b][nt][e] = p.cap * kLog2e * tanh_of(x[b][nt][e] * coef[nt][e & 1]);
+            for (int e = 0; e < 4; ++e) x[b][nt][e] = tanh_of(x[b][nt][e] * coef[nt][e & 1]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) by[nt][0] = by[nt][1] = 1.f;
+        for (int nt = 0; nt < NT; ++nt) by[nt][0] = by[nt][1] = p.cap * kLog2e;
       }
       if (SPECIAL && p.slopes) {
 #pragma unroll
@@ -640,12 +646,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_kernel(const Pa
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const float slope = k ? two.z : two.x;
-            const float near = static_cast<float>(key0 + g - __float_as_int(k ? two.w : two.y));  // less what the row is away, in keys
+            const float bias = slope * static_cast<float>(key0 + g - __float_as_int(k ? two.w : two.y));
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
               for (int e = k; e < 4; e += 2)
-                x[b][nt][e] = fmaf(slope, near + static_cast<float>(16 * b + (e & 2) * 4), x[b][nt][e] * by[nt][k]);
+                x[b][nt][e] = fmaf(x[b][nt][e], by[nt][k], fmaf(slope, static_cast<float>(16 * b + (e & 2) * 4), bias));
             by[nt][k] = 1.f;
           }
         }

@@ -828,3 +828,19 @@ def test_append_of_more_heads_than_32_at_once(dev, layout, rot):
     cache.append(k, v, seq, at, table, rope=mapflow.RotaryPlan(rot, layout=layout), norm=True)
     y, _ = _rotated(k, None, True, at, True, layout, rot)
     _check_held(pages, ps, d, *_slots(seq, at, table, ps), y, v, gk, gv)
+
+
+@pytest.mark.parametrize("d,lq", [(128, 1), (64, 3), (128, 3)])
+def test_biases_that_rise_either_way(dev, d, lq):
+    """Slopes of both signs: the heaviest key is the newest or the oldest, and the reference moves along."""
+    lens = [1500, 64, 333]
+    g, pages, table, lens_t, gk, gv, keys = _world(dev, 36 + d + lq, 3, 2, d, 32, lens)
+    cache = mapflow.PagedCache.fp4(pages, 32, d, k_scale=gk, v_scale=gv)
+    q = _rnd(g, dev, 3, lq, 8, d, std=1.5)
+    slopes = torch.tensor([0.5, -0.5, 3.0, -3.0, 0.01, -0.01, 0.0, 40.0], device=dev)
+    lse = torch.empty(3, lq, 8, dtype=torch.float32, device=dev)
+    for cap in (None, 30.0, 1e5):
+        o = cache.attend(q, table, lens_t, softcap=cap, slopes=slopes, lse=lse)
+        _check_attend(dev, q, lens, keys, o, lse, 0, 0, d ** -0.5, cap, slopes)
+    o = cache.attend(q, table, lens_t, window=100, sinks=40, slopes=slopes, lse=lse)
+    _check_attend(dev, q, lens, keys, o, lse, 100, 40, d ** -0.5, None, slopes)
