@@ -40,6 +40,7 @@
 // rows, as much again for every further 16.  So they are with heads of 64, whose keys
 // have half the bytes but the same softmax (68 us over 16384 keys, 4.4 TB/s), and
 // with capped scores (121 us).
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -63,11 +64,16 @@ constexpr float kLift = 7.f;         // weights are held times 2^7
 constexpr float kNoRef = 1e30f;      // kLift less the reference of a row that has seen no key
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// D dimensions, NT times 8 rows to a unit of work.
+// D dimensions, NT times 8 rows to a unit of work.  Measured with 32 requests of
+// 16384 keys (and 200 of up to 2000): heads of 128 with one to 8 rows take 105 us (56)
+// with 12 warps and tiles of 64 keys, 105 (59) with 16 and 32 (12 and 32 reach 5.5 TB/s
+// from key to key, not 6.4); heads of 64 69 us with 16 and 64, 72 with 12 and 128, 74
+// with 24 and 32.  More rows leave registers and a ring for 12 warps; tiles of 64 do not
+// fit it twice with heads of 128.
 template <int D, int NT>
 struct Cfg {
-  static constexpr int W = NT == 1 ? 16 : 12;                // warps
-  static constexpr int NB = D == 128 ? 2 : 4;            // 16-key blocks of a tile
+  static constexpr int W = NT == 1 && D == 64 ? 16 : 12;   // warps
+  static constexpr int NB = NT > 1 && D == 128 ? 2 : 4;  // 16-key blocks of a tile
   static constexpr int TK = NB * 16;
   static constexpr int kPiece = fp4_piece(D);
   static constexpr int kStage = NB * kPiece;
@@ -1068,7 +1074,7 @@ int row_tiles(int rows) { return rows <= 8 ? 1 : 2; }
 void paged_shape(int Lq, int G, int sms, int* grid, int* parts, int* rows) {
   const int nt = row_tiles(Lq * G);
   *grid = sms;
-  *parts = sms * (2 + (nt == 1 ? Cfg<128, 1>::W : Cfg<128, 2>::W));
+  *parts = sms * (2 + (nt == 1 ? std::max(Cfg<128, 1>::W, Cfg<64, 1>::W) : std::max(Cfg<128, 2>::W, Cfg<64, 2>::W)));
   *rows = Lq * G < 8 * nt ? Lq * G : 8 * nt;
 }
 
