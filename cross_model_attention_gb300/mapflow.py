@@ -882,7 +882,9 @@ class PagedCache:
         self._struct = CacheStruct(fmt, _int("page_size", page_size), _int("H", H), _int("d", d), n_pages,
                                    k.data_ptr(), _ptr(v), ld_k, ld_v, _ptr(ks), _ptr(vs))
         self._c = ctypes.addressof(self._struct)
-        self._scale = d ** -0.5
+        self._scale, self._ld = d ** -0.5, H * d
+        import torch
+        self._bf16, self._i32, self._f32 = torch.bfloat16, torch.int32, torch.float32
         self._ws_of: Dict[Tuple[int, int], int] = {}  # workspace bytes by Lq and H_q
 
     @classmethod
@@ -923,8 +925,7 @@ class PagedCache:
     def _table(self, table, rows=None) -> Tuple[int, int, int]:
         """Checks a table; returns the numbers between two of its rows, its rows and
         its columns."""
-        import torch
-        if table.dtype is torch.int32 and table.get_device() == self._gpu and table.dim() == 2:
+        if table.dtype is self._i32 and table.get_device() == self._gpu and table.dim() == 2:
             n, m = table.shape
             if rows is None or n == rows:
                 if table.is_contiguous():
@@ -934,33 +935,38 @@ class PagedCache:
         raise MapFlowError(MF_ERR_ARG, f"table must be an int32 tensor [{'n_seqs' if rows is None else rows}, max_pages] "
                                        f"on cuda:{self._gpu} with a row's numbers next to each other")
 
+    # (The calls below are made for every layer of a decoding step: a tensor is looked
+    # at in place, by _vector and _rows only to say what is wrong or odd.)
     def append(self, k, v, seq, at, table, rope: Optional["RotaryPlan"] = None, positions=None, k_weight=None,
                eps: float = 1e-6, norm: Optional[bool] = None, stream=None) -> None:
         """Puts k and v (bf16 [T, H, d]) of T tokens in their places, the keys
         normed (when a weight is given or norm is True) and rotated by `rope` at
         `positions` (int32 [T]; None: `at`) on the way (see mf_cache_append)."""
-        raw = None if stream is not None else _raw_current(self._gpu)
-        if raw is not None:
-            return self._append(raw, k, v, seq, at, table, rope, positions, k_weight, eps, norm)
-        guard, raw = _on(self.device, stream)
-        with guard:
-            return self._append(raw, k, v, seq, at, table, rope, positions, k_weight, eps, norm)
-
-    def _append(self, raw, k, v, seq, at, table, rope, positions, k_weight, eps, norm):
-        import torch
-        dt, gpu, i32 = torch.bfloat16, self._gpu, torch.int32
+        gpu = self._gpu
+        raw = None if stream is not None else _raw_current(gpu)
+        if raw is None:
+            guard, _ = _on(self.device, stream)
+            with guard:
+                return self.append(k, v, seq, at, table, rope, positions, k_weight, eps, norm)
+        dt, i32 = self._bf16, self._i32
         T = k.shape[0]
-        shape = (T, self.H, self.d)
-        ld_k = _rows("k", k, shape, dt, gpu)
-        ld_v = _rows("v", v, shape, dt, gpu)
-        one = (T,)
-        _vector("seq", seq, one, i32, gpu)
-        _vector("at", at, one, i32, gpu)
+        shape, one = (T, self.H, self.d), (T,)
+        ld_k = ld_v = self._ld
+        if k.dtype is not dt or k.shape != shape or k.get_device() != gpu or not k.is_contiguous():
+            ld_k = _rows("k", k, shape, dt, gpu)
+        if v.dtype is not dt or v.shape != shape or v.get_device() != gpu or not v.is_contiguous():
+            ld_v = _rows("v", v, shape, dt, gpu)
+        if seq.dtype is not i32 or seq.shape != one or seq.get_device() != gpu or not seq.is_contiguous():
+            _vector("seq", seq, one, i32, gpu)
+        if at.dtype is not i32 or at.shape != one or at.get_device() != gpu or not at.is_contiguous():
+            _vector("at", at, one, i32, gpu)
         ld_t, n_seqs, max_pages = self._table(table)
         p_pos = p_w = turns = rot = layout = 0
         gain = 1.0
         if positions is not None:
-            _vector("positions", positions, (T,), i32, gpu)
+            if positions.dtype is not i32 or positions.shape != one or positions.get_device() != gpu or \
+                    not positions.is_contiguous():
+                _vector("positions", positions, one, i32, gpu)
             p_pos = positions.data_ptr()
         if rope is not None:
             if rope._gpu != gpu:
@@ -984,28 +990,31 @@ class PagedCache:
     def read(self, seq, at, table, k=None, v=None, stream=None):
         """(k, v): bf16 [T, H, d] of T tokens, new tensors unless given; rows of
         tokens that are left out keep what was there (see mf_cache_read)."""
-        raw = None if stream is not None else _raw_current(self._gpu)
-        if raw is not None:
-            return self._read(raw, seq, at, table, k, v)
-        guard, raw = _on(self.device, stream)
-        with guard:
-            return self._read(raw, seq, at, table, k, v)
-
-    def _read(self, raw, seq, at, table, k, v):
-        import torch
         gpu = self._gpu
+        raw = None if stream is not None else _raw_current(gpu)
+        if raw is None:
+            guard, _ = _on(self.device, stream)
+            with guard:
+                return self.read(seq, at, table, k, v)
+        dt, i32 = self._bf16, self._i32
         T = seq.shape[0]
-        _vector("seq", seq, (T,), torch.int32, gpu)
-        _vector("at", at, (T,), torch.int32, gpu)
+        shape, one = (T, self.H, self.d), (T,)
+        if seq.dtype is not i32 or seq.shape != one or seq.get_device() != gpu or not seq.is_contiguous():
+            _vector("seq", seq, one, i32, gpu)
+        if at.dtype is not i32 or at.shape != one or at.get_device() != gpu or not at.is_contiguous():
+            _vector("at", at, one, i32, gpu)
         ld_t, n_seqs, max_pages = self._table(table)
-        shape, ld = (T, self.H, self.d), []
-        for name, t in (("k", k), ("v", v)):
-            ld.append(self.H * self.d if t is None else _rows(name, t, shape, torch.bfloat16, gpu))
+        ld_k = ld_v = self._ld
+        if k is not None and (k.dtype is not dt or k.shape != shape or k.get_device() != gpu or not k.is_contiguous()):
+            ld_k = _rows("k", k, shape, dt, gpu)
+        if v is not None and (v.dtype is not dt or v.shape != shape or v.get_device() != gpu or not v.is_contiguous()):
+            ld_v = _rows("v", v, shape, dt, gpu)
         if k is None or v is None:
-            new = torch.zeros((1 + (k is v), *shape), dtype=torch.bfloat16, device=self.device)
+            import torch
+            new = torch.zeros((1 + (k is v), *shape), dtype=dt, device=self.device)
             k, v = new[0] if k is None else k, new[-1] if v is None else v
-        rc = self._read_call(_read_args(self._c, seq.data_ptr(), at.data_ptr(), table.data_ptr(), ld_t, k.data_ptr(), ld[0],
-                                        v.data_ptr(), ld[1], raw, T, n_seqs, max_pages, 0))
+        rc = self._read_call(_read_args(self._c, seq.data_ptr(), at.data_ptr(), table.data_ptr(), ld_t, k.data_ptr(), ld_k,
+                                        v.data_ptr(), ld_v, raw, T, n_seqs, max_pages, 0))
         if rc:
             _check(rc)
         return k, v
@@ -1017,21 +1026,23 @@ class PagedCache:
         request, the new tokens' among them) -> o [n, Lq, H_q, d].  softcap: scores
         are capped by a tanh; slopes: fp32 [H_q], a bias by distance; lse: fp32 [n,
         Lq, H_q] to fill, or None (see mf_attn_paged)."""
-        raw = None if stream is not None else _raw_current(self._gpu)
-        if raw is not None:
-            return self._attend(raw, q, table, lens, window, sinks, softcap, slopes, scale, o, lse)
-        guard, raw = _on(self.device, stream)
-        with guard:
-            return self._attend(raw, q, table, lens, window, sinks, softcap, slopes, scale, o, lse)
-
-    def _attend(self, raw, q, table, lens, window, sinks, softcap, slopes, scale, o, lse):
-        import torch
-        dt, gpu = torch.bfloat16, self._gpu
+        gpu = self._gpu
+        raw = None if stream is not None else _raw_current(gpu)
+        if raw is None:
+            guard, _ = _on(self.device, stream)
+            with guard:
+                return self.attend(q, table, lens, window, sinks, softcap, slopes, scale, o, lse)
+        dt, i32, f32 = self._bf16, self._i32, self._f32
         if q.dim() != 4:
             raise MapFlowError(MF_ERR_ARG, "q must be [n, Lq, H_q, d]")
-        shape = n, Lq, H_q, _ = (*q.shape[:3], self.d)
-        ld_q = _rows("q", q, shape, dt, gpu)
-        _vector("lens", lens, (n,), torch.int32, gpu)
+        n, Lq, H_q, d = shape = q.shape
+        if d != self.d:
+            raise MapFlowError(MF_ERR_ARG, f"q has heads of {d}, the cache of {self.d}")
+        ld_q = ld_o = H_q * d
+        if q.dtype is not dt or q.get_device() != gpu or not q.is_contiguous():
+            ld_q = _rows("q", q, shape, dt, gpu)
+        if lens.dtype is not i32 or lens.shape != (n,) or lens.get_device() != gpu or not lens.is_contiguous():
+            _vector("lens", lens, (n,), i32, gpu)
         ld_t, _, max_pages = self._table(table, n)
         window, sinks = 0 if window is None else _span("window", window, 1), _span("sinks", sinks, 0)
         if softcap is None:
@@ -1039,15 +1050,16 @@ class PagedCache:
         elif not softcap > 0:
             raise MapFlowError(MF_ERR_ARG, f"softcap = {softcap} must be positive (None: none)")
         if o is None:
-            o, ld_o = _empty(q, shape), H_q * self.d
-        else:
+            o = _empty(q, shape)
+        elif o.dtype is not dt or o.shape != shape or o.get_device() != gpu or not o.is_contiguous():
             ld_o = _rows("o", o, shape, dt, gpu)
         p_lse = p_slopes = 0
         if lse is not None:
-            _vector("lse", lse, shape[:3], torch.float32, gpu)
+            if lse.dtype is not f32 or lse.shape != shape[:3] or lse.get_device() != gpu or not lse.is_contiguous():
+                _vector("lse", lse, shape[:3], f32, gpu)
             p_lse = lse.data_ptr()
         if slopes is not None:
-            _vector("slopes", slopes, (H_q,), torch.float32, gpu)
+            _vector("slopes", slopes, (H_q,), f32, gpu)
             p_slopes = slopes.data_ptr()
         need = self._ws_of.get((Lq, H_q))
         if need is None:
@@ -1059,6 +1071,7 @@ class PagedCache:
         # overlap and have their own.
         ws = _default_ws.get(gpu) if raw == 0 else None
         if ws is None or ws.shape[0] < need:
+            import torch
             ws = torch.empty(need, dtype=torch.uint8, device=self.device)
             if raw == 0:
                 _default_ws[gpu] = ws
