@@ -32,14 +32,14 @@
 // of a pair that warps of a CTA share are joined in shared memory, those that
 // CTAs share through the workspace, by a second kernel; both in a fixed order.
 //
-// Measured in back-to-back graph replays, 32 requests, 32q/8kv heads of 128: 36 us
-// over 4096 keys each, 106.5 over 16384, 200 over 32768: 6.4 TB/s (95 % of the
-// copy rate) from key to key, and 13 us besides, for the lengths and the table (4),
-// the first tiles (4), joining in the CTA (2) and the second kernel (3).  From 9 rows
-// on the instructions of 12 warps are the bound: 144 us over 16384 keys with 9 to 16
+// Measured in back-to-back graph replays, 32 requests, 32q/8kv heads of 128: 35 us
+// over 4096 keys each, 106 over 16384, 200 over 32768: 6.4 TB/s (95 % of the copy
+// rate) from key to key, and 12 us besides, for the lengths and the table (4), the
+// first tiles (3), joining in the CTA (2) and the second kernel (3).  From 9 rows on
+// the instructions of 12 warps are the bound: 142 us over 16384 keys with 9 to 16
 // rows, as much again for every further 16.  So they are with heads of 64, whose keys
-// have half the bytes but the same softmax (68 us over 16384 keys, 4.4 TB/s), and
-// with capped scores (121 us).
+// have half the bytes but the same softmax (69 us over 16384 keys, 4.4 TB/s), with
+// capped scores (124 us) and a bias by distance (113).
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -144,7 +144,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 // tanh: by its series below 0.3, above by the exponential, 1 - 2 / (1 + e^2a); off
 // by 2^-20 of it.  (With tanhf 32 requests of 16384 keys with capped scores took 158
-// us, with this 138, and 121 since a tile's are taken together; two by two in packed
+// us, with this 138, and 121 where a tile's are taken together; two by two in packed
 // arithmetic 2 more.)
 __device__ __forceinline__ float tanh_of(float x) {
   const float a = fabsf(x), q = x * x;
