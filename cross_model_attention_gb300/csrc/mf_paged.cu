@@ -1065,8 +1065,8 @@ cudaError_t launch_t(PagedParams p, cudaStream_t s) {
 
 // Rows to a unit: 8 where there are no more, else 16 and as many units to a head as
 // it takes.  (Units of 32 rows, whose products alone fill 255 registers of 8 warps: 64
-// rows over 32 requests of 16384 keys 488 us, not 548; of 4096 152, not 159; over 8
-// requests of 4000 keys on average 65, not 60.)
+// rows over 32 requests of 16384 keys 488 us, not 531; but of 4096 152, not 150, and over
+// 8 requests of 4000 keys on average 65, not 53.)
 namespace {
 int row_tiles(int rows) { return rows <= 8 ? 1 : 2; }
 }  // namespace
