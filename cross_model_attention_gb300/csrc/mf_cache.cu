@@ -18,7 +18,8 @@
 // 150) are done again in twice that precision, by the warp that finds them, once its
 // rows are done (mf_ff.cuh: 2^-43, which leaves one value in 10^11 undecided).  What
 // is exact in fp32 (values, keys that are neither normed nor rotated) often lies on
-// a step itself: its quotient is corrected by its residue, which finds those exactly.
+// a step itself: its quotient is corrected by its residue, which finds those exactly,
+// and what only rounds to a step goes back to its side.
 //
 // Bound: HBM for bf16 rows (4099 tokens of 40 heads of 128 put in their places in
 // 30 us, 5.6 TB/s, 82 % of the copy rate) and reading (32000 tokens of 8 heads 29 us,
@@ -120,10 +121,19 @@ __device__ __forceinline__ uint32_t scale_about(float top, float off, float inv_
   near |= (two & 0xffu) != (two >> 8);
   return top < INFINITY ? two >> 8 : kNanScale;
 }
-// Where it is exact: the quotient corrected by its residue (see below).
-__device__ __forceinline__ uint32_t scale_exactly(float top, float g6, float inv_g6) {
-  const float q = top * inv_g6;
-  const uint32_t s = f32x2_e4m3(q < 1e4f ? fmaf(fmaf(-q, g6, top), inv_g6, q) : 448.f, 0.f) & 0xffu;
+// Where it is exact: of the two scales within 2^-21 of the quotient, if they are not
+// the same, that on the side of their middle where top / (6 g) lies; a tie to the
+// even one.
+__device__ __forceinline__ uint32_t scale_exactly(float top, float g) {
+  const float g6 = mul_rn(6.f, g), q = top * rcp(g6);
+  const uint32_t two = f32x2_e4m3(q * (1.f - 4.76837158203125e-07f), q * (1.f + 4.76837158203125e-07f));
+  const uint32_t a = two & 0xffu, b = two >> 8;
+  uint32_t s = a;
+  if (a != b) {
+    const float border = 0.5f * (e4m3_f32(a) + e4m3_f32(b));
+    const float d = add_rn(fmaf(-border, g6, top), -border * fmaf(6.f, g, -g6));
+    s = d > 0.f || (d == 0.f && (a & 1)) ? b : a;
+  }
   return top < INFINITY ? s : kNanScale;
 }
 // y / (s g): a product with the reciprocal, corrected by its residue, so that a
@@ -132,20 +142,38 @@ __device__ __forceinline__ float quotient(float y, const Scale& s) {
   const float t = y * s.r;
   return fmaf(fmaf(-t, s.lo, fmaf(-t, s.sg, y)), s.r, t);
 }
-// Codes of 8 values, each exact in fp32.
+// Codes of 8 values, each exact in fp32.  A quotient rounded to fp32 is on the right
+// side of a border, unless it is the border (its last 21 bits are zero) and was not
+// before: then it goes back to the side that its residue says (one value in 10^6; where
+// the quotient is the border, the even code is the right one).
 __device__ __forceinline__ uint32_t codes_exactly(const float* y, const Scale& s) {
   float t[8];
+  bool odd = false;
+  auto on_border = [](float c) { return (__float_as_uint(c) & 0x1fffffu) == 0; };
   if (s.byte == 0x7e) {  // the largest scale: quotients may be of any size
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = fabsf(y[i] * s.r) < 8.f ? quotient(y[i], s) : y[i] * s.r;
+    for (int i = 0; i < 8; ++i) {
+      t[i] = fabsf(y[i] * s.r) < 8.f ? quotient(y[i], s) : y[i] * s.r;
+      odd |= on_border(t[i]);
+    }
   } else {
     const float2 r = make_float2(s.r, s.r), sg = make_float2(-s.sg, -s.sg), lo = make_float2(-s.lo, -s.lo);
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
       const float2 v = make_float2(y[i], y[i + 1]), q = fmul2(v, r);
       const float2 c = ffma2(ffma2(q, lo, ffma2(q, sg, v)), r, q);
+      const float2 rest = ffma2(c, lo, ffma2(c, sg, v));
       t[i] = c.x;
       t[i + 1] = c.y;
+      odd |= (on_border(c.x) && rest.x != 0.f) || (on_border(c.y) && rest.y != 0.f);
+    }
+  }
+  if (odd) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float c = t[i], rest = fmaf(-c, s.lo, fmaf(-c, s.sg, y[i]));
+      if (on_border(c) && rest != 0.f && c != 0.f && fabsf(c) < 8.f)
+        t[i] = __int_as_float(__float_as_int(c) + ((rest > 0.f) == (c > 0.f) ? 1 : -1));
     }
   }
   return f32x8_e2m1(t);
@@ -507,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
     }
     {
       uint32_t w0, w1, b0, b1;
-      const float g6 = 6.f * gk, inv = rcp(g6);
+      const float inv = rcp(6.f * gk);
       if (loose) {
         // (|a| + |b| is at most 2 max(|y_a|, |y_b|) of the rotated pair, both of
         // which are in these blocks)
@@ -523,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
         }
         w1 = codes_about(y + 8, r * r1, off * r1, near);
       } else {  // (one block)
-        b0 = b1 = scale_exactly(t0, g6, inv);
+        b0 = b1 = scale_exactly(t0, gk);
         const Scale s0 = scale_of(b0, gk);
         w0 = codes_exactly(y, s0);
         w1 = codes_exactly(y + 8, s0);
@@ -551,8 +579,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
     float tv = 0.f;
 #pragma unroll
     for (int e = 0; e < 16; e += 2) tv = most(tv, y[e], y[e + 1]);
-    const float g6 = 6.f * gv;
-    const Scale sv = scale_of(scale_exactly(tv, g6, rcp(g6)), gv);
+    const Scale sv = scale_of(scale_exactly(tv, gv), gv);
     const uint32_t d0 = __shfl_sync(kFull, codes_exactly(y, sv), vsrc_lane);
     const uint32_t d1 = __shfl_sync(kFull, codes_exactly(y + 8, sv), vsrc_lane);
     const uint32_t ds = __shfl_sync(kFull, sv.byte, vsrc_lane);

@@ -844,3 +844,43 @@ def test_biases_that_rise_either_way(dev, d, lq):
         _check_attend(dev, q, lens, keys, o, lse, 0, 0, d ** -0.5, cap, slopes)
     o = cache.attend(q, table, lens_t, window=100, sinks=40, slopes=slopes, lse=lse)
     _check_attend(dev, q, lens, keys, o, lse, 100, 40, d ** -0.5, None, slopes)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_quotients_beside_a_border(dev, d):
+    """Head scales that put a block's scale, or a value's code, within fp32's rounding of the
+    border between two: the exact quotient decides (a tie only where it lies on it)."""
+    H, T, ps = 256, 48, 16
+    rng = torch.Generator().manual_seed(40 + d)
+    draw = lambda *shape: torch.rand(*shape, generator=rng, dtype=torch.float64)  # noqa: E731
+    x = (draw(T, H, d) * 2 - 1) * 0.5
+    g = torch.empty(H, dtype=torch.float64)
+    codes = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], dtype=torch.float64)
+    for h in range(H):
+        top = float((0.5 + draw(1) * 8).to(BF).double())
+        if h % 2 == 0:    # top / (6 g) beside the middle of two scales
+            m = float(torch.ldexp(17.0 + 2 * torch.floor(draw(1) * 8), torch.floor(draw(1) * 9) - 7))
+            g[h] = (torch.tensor(top / (6 * m), dtype=torch.float64)).float().double()
+            x[:, h] *= top / 8
+            x[:, h, ::16] = top
+        else:             # a value over s g beside the middle of two codes
+            s = float(torch.ldexp(8.0 + torch.floor(draw(1) * 8), torch.floor(draw(1) * 9) - 6))
+            c = codes[int(draw(1) * 7)].item()
+            g[h] = torch.tensor(top / (s * c), dtype=torch.float64).float().double()
+            x[:, h] *= 4 * s * g[h]
+            x[:, h, ::16] = 6 * s * g[h]
+            x[:, h, 5::16] = top
+            x[:, h, 9::16] = -top
+    x, gs = x.to(BF).to(dev), g.float().to(dev)
+    pages = _pages(dev, T // ps, H, ps, d)
+    cache = mapflow.PagedCache.fp4(pages, ps, d, k_scale=gs, v_scale=gs)
+    seq, at = _tokens([T], dev)
+    table = torch.arange(T // ps, dtype=torch.int32, device=dev)[None]
+    cache.append(x, x, seq, at, table)
+    page, o = _slots(seq, at, table, ps)
+    _check_held(pages, ps, d, page, o, x.double(), x, gs, gs)
+    # rotated and normed dimensions beside such ones, in the same rows
+    plan = mapflow.RotaryPlan(32)
+    cache.append(x, x, seq, at, table, rope=plan)
+    y, _ = _rotated(x, None, False, at, plan, "half", 32)
+    _check_held(pages, ps, d, page, o, y, x, gs, gs)
