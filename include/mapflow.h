@@ -646,9 +646,9 @@ MF_API int mf_attn_status(mf_attn_t h, void* stream);
  *     a value is held as the e2m1 number (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
  *     negatives) nearest to x / (s g), ties to even, at most 6,
  *   and stands for that number times s g.  Which number that is goes by the exact
- *   value of x (two fp32 numbers, good to 2^-43, decide where one cannot).  A block
- *   with a value that is not finite is held as NaN.  16 tokens of a head are 18 d
- *   bytes,
+ *   value of x (two fp32 numbers, good to 2^-43, decide where one cannot), rotated by
+ *   the angles that `turns` gives.  A block with a value that is not finite is held as
+ *   NaN.  16 tokens of a head are 18 d bytes,
  *     keys' codes    [16 tokens][d/2]             (even dimension in the low bits)
  *     values' codes  [2][d/16][8 tokens][8]
  *     keys' scales   [16 tokens][d/16]   values' scales [d/16][16 tokens]   (e4m3)
