@@ -332,8 +332,8 @@ __device__ __forceinline__ Sector get16(const __nv_bfloat16* from, bool even) {
 }
 
 // ------------------------------------------------------------------ append --
-// (Four CTAs to an SM: 16384 tokens of 8 heads 31.3 us; three 33.8, five, which
-// spill, 34.9.)
+// (Four CTAs to an SM: 16384 tokens of 8 heads 32.0 us; three 35.6, five, which
+// spill, 37.3.)
 template <int D, int LAYOUT, bool FP4>
 __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p) {
   constexpr int LPR = D / 16;            // lanes to a row
@@ -710,8 +710,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const CacheParams p) {
 
 // A token's heads in shares: all of them to one group of lanes where that
 // leaves every SM about `rounds` rounds, else spread.  (Appending, whose groups
-// begin with sines and cosines, two: 16384 tokens of 8 heads 31.3 us, with eight
-// 33.2; 4099 of 40 heads in bf16 30.0, with one 34.3 and with four 32.0.  Reading
+// begin with sines and cosines, two: 16384 tokens of 8 heads 32.0 us, with eight
+// 34.3; 4099 of 40 heads in bf16 30.0, with one 34.3 and with four 32.0.  Reading
 // eight: the same 16384 16.4 us, with two 17.0.)
 template <typename F>
 cudaError_t spread(CacheParams p, long long T, int D, int rounds, F&& go) {

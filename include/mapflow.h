@@ -684,8 +684,8 @@ typedef struct {
  * both.  Shares no memory between cache and inputs.  max_pages * page_size is at
  * most 2^26 (MF_ERR_UNSUPPORTED).  T = 0 is a no-op.
  *
- * mf_cache_read — T tokens' keys and values as bf16 rows (each rounded once: a
- * code times its scale times the head's), e.g. for mf_attn_packed over a chunk and
+ * mf_cache_read — T tokens' keys and values as bf16 rows (a code times
+ * its scale times the head's in fp32, rounded), e.g. for mf_attn_packed over a chunk and
  * its cached prefix.  Rows of tokens that are left out are not written.
  * Errors of both: MF_ERR_ARG, MF_ERR_UNSUPPORTED, MF_ERR_CUDA.
  */
