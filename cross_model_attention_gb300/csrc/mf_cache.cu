@@ -440,7 +440,9 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
   }
   // Whether the lane's values are not exact in fp32, and how far they may be off,
   // of |a| + |b| (kAny and kPairs: where only some are, the rest is taken to be so too).
-  const bool loose = p.norm || (LAYOUT == kHalf ? turned : c0 * 8 < p.rot);
+  // At position 0 they are: a prompt's first token would have most of its blocks done
+  // again by one warp, 12 us after the others of 16384.
+  const bool loose = p.norm || ((LAYOUT == kHalf ? turned : c0 * 8 < p.rot) && (pos != 0 || p.gain != 1.f));
   const float err = (p.norm ? 20.f : 16.f) * 5.9604644775390625e-08f * fmaxf(1.f, p.gain);  // 2^-24
 
   // where the rows go
@@ -563,11 +565,17 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
           r1 = scale_of(b1, gk).r;
         }
         w1 = codes_about(y + 8, r * r1, off * r1, near);
-      } else {  // (one block)
-        b0 = b1 = scale_exactly(t0, gk);
+      } else {
+        b0 = scale_exactly(t0, gk);
         const Scale s0 = scale_of(b0, gk);
         w0 = codes_exactly(y, s0);
-        w1 = codes_exactly(y + 8, s0);
+        b1 = b0;
+        Scale s1 = s0;
+        if (LAYOUT == kHalf && turned) {
+          b1 = scale_exactly(t1, gk);
+          s1 = scale_of(b1, gk);
+        }
+        w1 = codes_exactly(y + 8, s1);
       }
       if (live) {
         uint8_t* dst = kdst + i * hstride;

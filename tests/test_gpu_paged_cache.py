@@ -884,3 +884,25 @@ def test_quotients_beside_a_border(dev, d):
     cache.append(x, x, seq, at, table, rope=plan)
     y, _ = _rotated(x, None, False, at, plan, "half", 32)
     _check_held(pages, ps, d, page, o, y, x, gs, gs)
+
+
+@pytest.mark.parametrize("layout,rot", [("half", 128), ("half", 64), ("interleaved", 128), ("half", 20), ("interleaved", 6)])
+def test_position_zero_turns_nothing(dev, layout, rot):
+    g = _gen(dev, 50 + rot)
+    T, H, d, ps = 333, 3, 128, 16
+    k = (torch.randint(-24, 25, (T, H, d), generator=g, device=dev) / 4).to(BF)
+    v = _rnd(g, dev, T, H, d)
+    seq, at = _tokens([T], dev)
+    table = torch.arange((T + ps - 1) // ps, dtype=torch.int32, device=dev)[None]
+    page, o = _slots(seq, at, table, ps)
+    zero = torch.zeros(T, dtype=torch.int32, device=dev)
+    some = torch.where(at % 3 == 0, zero, at)
+    for gs in (None, torch.tensor([0.5, 1.1, 3.0], device=dev)):
+        for pos in (zero, some):
+            pages = _pages(dev, table.shape[1], H, ps, d)
+            cache = mapflow.PagedCache.fp4(pages, ps, d, k_scale=gs, v_scale=gs)
+            cache.append(k, v, seq, at, table, rope=mapflow.RotaryPlan(rot, layout=layout), positions=pos)
+            y, _ = _rotated(k, None, False, pos, True, layout, rot)
+            _check_held(pages, ps, d, page, o, y, v, gs, gs)
+            if pos is zero:
+                assert torch.equal(y, k.double())
