@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
     sn *= p.gain;
   };
 #pragma unroll
-  for (int e = 0; e < 16; ++e) own[e] = 1.f, other[e] = 0.f;
+  for (int e = 0; e < 16; ++e) own[e] = 1.f, other[e] = FP4 ? 0.f : -0.f;  // (kAny: 0 times -0 leaves a row's -0 too)
   if (weight) {
     unpack8(*reinterpret_cast<const uint4*>(weight + c0 * 8), own);
     unpack8(*reinterpret_cast<const uint4*>(weight + c1 * 8), own + 8);
@@ -514,7 +514,9 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
       for (int e = 0; e < 16; e += 2) {
         const float2 x = make_float2(a[e], a[e + 1]);
         const float2 z = LAYOUT == kHalf ? make_float2(a[e ^ 8], a[(e ^ 8) + 1]) : make_float2(x.y, x.x);
-        const float2 v = ffma2(z, make_float2(other[e], other[e + 1]), fmul2(x, make_float2(own[e], own[e + 1])));
+        float2 v = fmul2(x, make_float2(own[e], own[e + 1]));
+        // (rows of bf16: 0 times what is not finite is not 0.  A 4-bit block of it is NaN as a whole)
+        if (FP4 || (LAYOUT == kHalf ? turned : c0 * 8 + e < p.rot)) v = ffma2(z, make_float2(other[e], other[e + 1]), v);
         y[e] = v.x;
         y[e + 1] = v.y;
       }

@@ -1,0 +1,60 @@
+"""Appending to a paged cache at the ends of its inputs' ranges: what is not
+finite, gains below zero, small eps, head scales of any size."""
+import math
+
+import pytest
+import torch
+
+from cross_model_attention_gb300 import mapflow
+from tests import layer_ref
+from tests import paged_ref as ref
+from tests.test_gpu_paged_cache import BF, _check_attend, _check_held, _gen, _pages, _rnd, _slots, _tokens, _world
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    assert torch.cuda.is_available(), "a GPU is needed"
+    return torch.device("cuda", torch.cuda.current_device())
+
+
+def _rows(dev, k, at, ps=16, **kw):
+    """k [T, H, d] as a bf16 cache holds them, at the places `at` of one sequence."""
+    T, H, d = k.shape
+    n = (T + ps - 1) // ps
+    kp, vp = (torch.full((n, ps, H, d), 5.0, dtype=BF, device=dev) for _ in range(2))
+    cache = mapflow.PagedCache.bf16(kp, vp)
+    table = torch.arange(n, dtype=torch.int32, device=dev)[None]
+    cache.append(k, k.clone(), torch.zeros_like(at), at, table, **kw)
+    return kp.view(-1, H, d)[:T]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("layout,rot", [(None, 0), ("half", 32), ("half", 20), ("interleaved", 32), ("interleaved", 6)])
+@pytest.mark.parametrize("norm", [False, True])
+def test_bf16_dimensions_that_are_not_turned(dev, d, layout, rot, norm):
+    g, T, H = _gen(dev, 60 + d + rot), 19, 3
+    k = _rnd(g, dev, T, H, d)
+    k[1, 0, 40] = math.inf       # dimensions past every rotated part, at either end of a pair of
+    k[2, 1, 41] = -math.inf      # neighbours, of chunks of 8 and of halves
+    k[3, 2, 48] = math.nan
+    k[4, 0, 63] = math.inf
+    k[5, 1, d - 1] = math.inf
+    k[6, :, rot:] = -0.0
+    _, at = _tokens([T], dev)
+    w = (1 + 0.1 * torch.randn(d, generator=g, device=dev)).to(BF) if norm else None
+    plan = mapflow.RotaryPlan(rot, layout=layout) if layout else None
+    got = _rows(dev, k, at, rope=plan, norm=norm, k_weight=w)[..., rot:]
+    if not norm:
+        want = k[..., rot:]
+        assert torch.equal(got.isnan(), want.isnan())
+        bits = lambda x: x.nan_to_num(7.0, math.inf, -math.inf).contiguous().view(torch.int16)  # noqa: E731
+        assert torch.equal(bits(got), bits(want))
+        return
+    # a row's infinity leaves 0 beside itself, its NaN nothing
+    y = k.double() * (k.double().square().mean(-1, keepdim=True) + 1e-6).rsqrt() * w.double()
+    want = y[..., rot:]
+    assert torch.equal(got.isnan(), want.isnan())
+    assert ((got.double() - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -17))[~want.isnan()].all()
+    assert torch.equal(got[6].signbit(), torch.ones_like(got[6], dtype=torch.bool))
