@@ -381,7 +381,12 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
   // other half) times `other`: cosines and sines with the weights in them.
   const long long pos = p.rot ? p.positions[tok] : 0;
   const __nv_bfloat16* weight = static_cast<const __nv_bfloat16*>(p.weight);
-  auto weight_of = [&](int d) { return weight ? __bfloat162float(weight[d]) : 1.f; };
+  // (normed rows of bf16: weights times 2^-40, the norm's factor times 2^40, so that no
+  // product with a weight passes fp32's range before a factor of 0 makes the row 0.
+  // The factor first, as in the rotary layer, costs kAny 2 of 54 us.)
+  constexpr float kDown = FP4 ? 1.f : 9.094947017729282e-13f, kUp = FP4 ? 1.f : 1099511627776.f;
+  const float down = p.norm ? kDown : 1.f;
+  auto weight_of = [&](int d) { return weight ? __bfloat162float(weight[d]) * down : down; };
   float own[16], other[16], heaviest = 0.f;
   auto turn_of = [&](int f, float& sn, float& cs) {
     const unsigned long long turn = static_cast<unsigned long long>(pos) * p.freq[f];
@@ -390,10 +395,12 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
     sn *= p.gain;
   };
 #pragma unroll
-  for (int e = 0; e < 16; ++e) own[e] = 1.f, other[e] = FP4 ? 0.f : -0.f;  // (kAny: 0 times -0 leaves a row's -0 too)
+  for (int e = 0; e < 16; ++e) own[e] = down, other[e] = FP4 ? 0.f : -0.f;  // (kAny: 0 times -0 leaves a row's -0 too)
   if (weight) {
     unpack8(*reinterpret_cast<const uint4*>(weight + c0 * 8), own);
     unpack8(*reinterpret_cast<const uint4*>(weight + c1 * 8), own + 8);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) own[e] *= down;
   }
 #pragma unroll
   for (int e = 0; e < 16; ++e) heaviest = fmaxf(heaviest, fabsf(own[e]));
@@ -496,6 +503,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
       for (int off = LPR / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(kFull, ss, off);
       near = !(ss < 1e36f);  // (bf16 squares pass fp32's range)
       asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(ss, 1.f / D, p.eps)));
+      r *= kUp;
     }
     float sum = 0.f;  // kAny: a bound of |a| + |b|
     if (LAYOUT == kAny) {

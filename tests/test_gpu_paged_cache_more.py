@@ -58,3 +58,19 @@ def test_bf16_dimensions_that_are_not_turned(dev, d, layout, rot, norm):
     assert torch.equal(got.isnan(), want.isnan())
     assert ((got.double() - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -17))[~want.isnan()].all()
     assert torch.equal(got[6].signbit(), torch.ones_like(got[6], dtype=torch.bool))
+
+
+@pytest.mark.parametrize("layout,rot", [(None, 0), ("half", 128), ("half", 20), ("interleaved", 128)])
+def test_bf16_rows_whose_squares_pass_the_range(dev, layout, rot):
+    """Squares past fp32's range make a row 0, as in the rotary layer, whatever the weights."""
+    g, T, H, d = _gen(dev, 61), 9, 2, 128
+    k = _rnd(g, dev, T, H, d)
+    k[2:6] = torch.where(k[2:6] > 0, 3e38, -3e38).to(BF)
+    w = torch.full((d,), 4.0, dtype=BF, device=dev)
+    _, at = _tokens([T], dev)
+    plan = mapflow.RotaryPlan(rot, layout=layout) if layout else None
+    got = _rows(dev, k, at, rope=plan, norm=True, k_weight=w)
+    assert (got[2:6] == 0).all() and torch.isfinite(got).all() and (got[:2] != 0).any()
+    if plan is not None:
+        _, want = plan.apply(k.clone(), k, at, norm=True, q_weight=w, k_weight=w)
+        assert (want[2:6] == 0).all()
