@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
   // At position 0 they are: a prompt's first token would have most of its blocks done
   // again by one warp, 12 us after the others of 16384.
   const bool loose = p.norm || ((LAYOUT == kHalf ? turned : c0 * 8 < p.rot) && (pos != 0 || p.gain != 1.f));
-  const float err = (p.norm ? 20.f : 16.f) * 5.9604644775390625e-08f * fmaxf(1.f, p.gain);  // 2^-24
+  const float err = (p.norm ? 20.f : 16.f) * 5.9604644775390625e-08f * fmaxf(1.f, fabsf(p.gain));  // 2^-24
 
   // where the rows go
   uint8_t *kdst = nullptr, *ksdst = nullptr, *vdst = nullptr, *vsdst = nullptr;

@@ -74,3 +74,19 @@ def test_bf16_rows_whose_squares_pass_the_range(dev, layout, rot):
     if plan is not None:
         _, want = plan.apply(k.clone(), k, at, norm=True, q_weight=w, k_weight=w)
         assert (want[2:6] == 0).all()
+
+
+@pytest.mark.parametrize("gain", [-1000.0, -1.5, -0.25, 64.0])
+@pytest.mark.parametrize("layout,rot", [("half", 120), ("half", 128), ("interleaved", 128)])
+def test_gains_of_either_sign(dev, gain, layout, rot):
+    g, T, H, d, ps = _gen(dev, 62), 16384, 8, 128, 64
+    k, v = _rnd(g, dev, T, H, d, std=0.05), _rnd(g, dev, T, H, d)
+    seq, at = _tokens([T], dev)
+    table = torch.arange(T // ps, dtype=torch.int32, device=dev)[None]
+    pages = _pages(dev, T // ps, H, ps, d)
+    plan = mapflow.RotaryPlan(rot, layout=layout)
+    plan.gain = gain
+    mapflow.PagedCache.fp4(pages, ps, d).append(k, v, seq, at, table, rope=plan)
+    f, _ = layer_ref.rope_frequencies(rot)
+    y, _ = layer_ref.rope(k, None, False, 0.0, at, f, gain, rot, layout)
+    _check_held(pages, ps, d, *_slots(seq, at, table, ps), y, v, None, None)
