@@ -260,9 +260,13 @@ __device__ __forceinline__ void exact_blocks(const CacheParams& p, const __nv_bf
   if (turned) ff_sincos(static_cast<uint64_t>(pos) * p.freq[p.layout == 1 ? d >> 1 : first ? d : other], &sn, &cn);
   top = __reduce_max_sync(kFull, top);
   // rows of huge values are brought into range (what the norm gives is in it), with
-  // what they are compared with
+  // what they are compared with; to be normed, rows of tiny ones under a tiny eps too
   const int ex = static_cast<int>(top >> 23) - 127;
-  const float down = ex > 30 ? __int_as_float((127 - min(ex, 127) + 30) << 23) : 1.f;
+  float down = ex > 30 ? __int_as_float((127 - min(ex, 127) + 30) << 23) : 1.f;
+  if (p.norm) {
+    const int e = max(ex, (static_cast<int>(__float_as_uint(p.eps) >> 23) - 127) / 2);
+    if (e < -30) down = __int_as_float((127 - e) << 23);
+  }
   if (!p.norm) g *= down;
   ff r = {1.f, 0.f};
   if (p.norm) {
@@ -501,8 +505,9 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
       float ss = (s0.x + s0.y) + (s1.x + s1.y);
 #pragma unroll
       for (int off = LPR / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(kFull, ss, off);
-      near = !(ss < 1e36f);  // (bf16 squares pass fp32's range)
-      asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(ss, 1.f / D, p.eps)));
+      const float m = fmaf(ss, 1.f / D, p.eps);
+      near = !(ss < 1e36f && m > 1e-30f);  // (bf16 squares pass fp32's range at either end)
+      asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(m));  // (m may be a subnormal number)
       r *= kUp;
     }
     float sum = 0.f;  // kAny: a bound of |a| + |b|

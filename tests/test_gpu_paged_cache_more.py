@@ -90,3 +90,30 @@ def test_gains_of_either_sign(dev, gain, layout, rot):
     f, _ = layer_ref.rope_frequencies(rot)
     y, _ = layer_ref.rope(k, None, False, 0.0, at, f, gain, rot, layout)
     _check_held(pages, ps, d, *_slots(seq, at, table, ps), y, v, None, None)
+
+
+@pytest.mark.parametrize("eps", [1e-40, 1e-36, 1e-25])
+@pytest.mark.parametrize("layout,rot", [(None, 0), ("half", 128), ("half", 20), ("interleaved", 64)])
+def test_small_eps(dev, eps, layout, rot):
+    """Rows of zeros stay zeros and rows of tiny values are normed, down to an eps below fp32's normal numbers."""
+    g, T, H, d, ps = _gen(dev, 63), 64, 3, 128, 16
+    k, v = _rnd(g, dev, T, H, d), _rnd(g, dev, T, H, d)
+    eps = float(torch.tensor(eps, dtype=torch.float32))
+    k[5:9] = 0
+    k[9:30] = (k[9:30].float() * 3 * eps ** 0.5).to(BF)     # squares about eps
+    k[30:40] = (k[30:40].float() * 0.01 * eps ** 0.5).to(BF)
+    seq, at = _tokens([T], dev)
+    plan = mapflow.RotaryPlan(rot, layout=layout) if layout else None
+    if plan is None:
+        y = k.double() * (k.double().square().mean(-1, keepdim=True) + eps).rsqrt()
+    else:
+        f, gain = layer_ref.rope_frequencies(rot)
+        y, _ = layer_ref.rope(k, None, True, eps, at, f, gain, rot, layout)
+    table = torch.arange(T // ps, dtype=torch.int32, device=dev)[None]
+    pages = _pages(dev, T // ps, H, ps, d)
+    mapflow.PagedCache.fp4(pages, ps, d).append(k, v, seq, at, table, rope=plan, norm=True, eps=eps)
+    _check_held(pages, ps, d, *_slots(seq, at, table, ps), y, v, None, None)
+    got = _rows(dev, k, at, rope=plan, norm=True, eps=eps)
+    assert (got[5:9] == 0).all() and torch.isfinite(got).all()
+    # (a square is off by 2^-150 at most, which is 2^-17 of 1e-40)
+    assert ((got.double() - y).abs() <= y.abs() * 2.0 ** -8 + 2.0 ** -15 * y.abs().amax(-1, keepdim=True)).all()
