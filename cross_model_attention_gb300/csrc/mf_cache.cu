@@ -100,6 +100,13 @@ __device__ __forceinline__ float most(float m, float a, float b) {
   return r;
 }
 
+// A head's scale, NaN where it is out of its range (NaN makes every block's scale NaN):
+// there a block's, or its reciprocal, would leave fp32's normal numbers.
+__device__ __forceinline__ float head_scale(const float* g, int h) {
+  constexpr uint32_t kLeast = 0x1f800000u, kMost = 0x5f800000u;  // 2^-64, 2^64
+  const uint32_t x = __float_as_uint(g[h]);
+  return x - kLeast <= kMost - kLeast ? __uint_as_float(x) : NAN;
+}
 struct Scale {
   uint32_t byte;
   float sg, lo, r;  // s g in two parts and the reciprocal of it, 0 where s is 0
@@ -259,11 +266,14 @@ __device__ __forceinline__ void exact_blocks(const CacheParams& p, const __nv_bf
   ff cn = {1.f, 0.f}, sn = {0.f, 0.f};
   if (turned) ff_sincos(static_cast<uint64_t>(pos) * p.freq[p.layout == 1 ? d >> 1 : first ? d : other], &sn, &cn);
   top = __reduce_max_sync(kFull, top);
-  // rows of huge values are brought into range (what the norm gives is in it), with
-  // what they are compared with; to be normed, rows of tiny ones under a tiny eps too
+  // rows of huge values are brought into range, with what they are compared with (a
+  // little, for sums of two: a small head scale has to stay a normal number); to be
+  // normed, further (what the norm gives is in range), and rows of tiny ones under a
+  // tiny eps too
   const int ex = static_cast<int>(top >> 23) - 127;
-  float down = ex > 30 ? __int_as_float((127 - min(ex, 127) + 30) << 23) : 1.f;
+  float down = ex > 100 ? 0.00390625f : 1.f;
   if (p.norm) {
+    down = ex > 30 ? __int_as_float((127 - min(ex, 127) + 30) << 23) : 1.f;
     const int e = max(ex, (static_cast<int>(__float_as_uint(p.eps) >> 23) - 127) / 2);
     if (e < -30) down = __int_as_float((127 - e) << 23);
   }
@@ -478,8 +488,8 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
     vout = static_cast<__nv_bfloat16*>(p.v) + row * p.ld_v + at;
   }
 
-  float gk_next = FP4 && here && p.k_scale ? p.k_scale[h_begin] : 1.f;
-  float gv_next = FP4 && here && p.v_scale ? p.v_scale[h_begin] : 1.f;
+  float gk_next = FP4 && here && p.k_scale ? head_scale(p.k_scale, h_begin) : 1.f;
+  float gv_next = FP4 && here && p.v_scale ? head_scale(p.v_scale, h_begin) : 1.f;
   unsigned again = 0;  // of 32 heads: those with blocks to be done more exactly
 #pragma unroll 1
   for (int ib = 0; ib < p.heads_per_unit; ib += kAhead)
@@ -560,8 +570,8 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
     }
     const float gk = gk_next, gv = gv_next;
     if (i + 1 < n) {
-      if (p.k_scale) gk_next = p.k_scale[h_begin + i + 1];
-      if (p.v_scale) gv_next = p.v_scale[h_begin + i + 1];
+      if (p.k_scale) gk_next = head_scale(p.k_scale, h_begin + i + 1);
+      if (p.v_scale) gv_next = head_scale(p.v_scale, h_begin + i + 1);
     }
     {
       uint32_t w0, w1, b0, b1;
@@ -636,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
             return reinterpret_cast<decltype(x)>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(x), from));
           };
           const int hj = __shfl_sync(kFull, h_begin, from) + j;
-          exact_blocks<D>(p, of(ksrc) + j * D, __shfl_sync(kFull, pos, from), p.k_scale ? p.k_scale[hj] : 1.f,
+          exact_blocks<D>(p, of(ksrc) + j * D, __shfl_sync(kFull, pos, from), p.k_scale ? head_scale(p.k_scale, hj) : 1.f,
                           two ? fl >> 1 : fl, two ? (fl + hc) >> 1 : fl, of(kdst) + j * hstride, of(ksdst) + j * hstride);
         }
       }

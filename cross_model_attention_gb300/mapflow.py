@@ -891,7 +891,8 @@ class PagedCache:
     def fp4(cls, pages, page_size: int, d: int, k_scale=None, v_scale=None) -> "PagedCache":
         """pages: uint8 [n_pages, H, page_size / 16 * 18 * d] on a GPU, contiguous
         (any contents until a token is appended); k_scale and v_scale: fp32 [H],
-        positive, a scale for each head's keys and values, or None (1)."""
+        2^-64 to 2^64, a scale for each head's keys and values (under any other an
+        append holds NaN), or None (1)."""
         import torch
         page_size, d = _int("page_size", page_size), _int("d", d)
         if d not in (64, 128) or page_size < 16 or page_size % 16:

@@ -665,8 +665,9 @@ typedef struct {
   void* k;               /* keys, or the 4-bit pages; 16-byte aligned            */
   void* v;               /* values; NULL for MF_CACHE_FP4                        */
   int64_t ld_k, ld_v;    /* MF_CACHE_BF16: values between tokens (16-byte multiples) */
-  const float* k_scale;  /* DEVICE fp32 [H], positive normal numbers, the heads' g;
-                            NULL: 1 (MF_CACHE_BF16: NULL)                        */
+  const float* k_scale;  /* DEVICE fp32 [H], the heads' g, 2^-64 to 2^64 (an append
+                            under any other holds NaN); NULL: 1 (MF_CACHE_BF16:
+                            NULL)                                                */
   const float* v_scale;
 } mf_cache_t;
 
@@ -715,7 +716,8 @@ MF_API int mf_cache_read(const mf_cache_t* cache, int T, const int32_t* seq, con
  *                the device, so that a captured graph follows it (and the table)
  *                from replay to replay
  *   slopes       DEVICE fp32 [H_q] or NULL
- *   softcap      0: none; scale and scale / softcap lie in (1e-30, 1e30)
+ *   softcap      0: none; scale and scale / softcap lie in (1e-30, 1e30), and so do
+ *                they times a head's k_scale
  *   window       >= 1, or 0: no window          n_sink   >= 0
  *   n            at most 2^20; n * (max_pages * page_size / 32 + 2) below 2^31, and
  *                that times H and a 16th of the rows of a head, Lq * H_q / H, rounded

@@ -117,3 +117,81 @@ def test_small_eps(dev, eps, layout, rot):
     assert (got[5:9] == 0).all() and torch.isfinite(got).all()
     # (a square is off by 2^-150 at most, which is 2^-17 of 1e-40)
     assert ((got.double() - y).abs() <= y.abs() * 2.0 ** -8 + 2.0 ** -15 * y.abs().amax(-1, keepdim=True)).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("layout,rot", [(None, 0), ("half", 64), ("half", 20), ("interleaved", 32)])
+def test_head_scales_at_the_ends_of_their_range(dev, d, layout, rot):
+    g, T, ps = _gen(dev, 64 + d), 80, 16
+    lo, hi = 2.0 ** -64, 2.0 ** 64
+    gk = torch.tensor([lo, 1.37 * lo, hi, hi / 1.37, 1.0, lo, hi], device=dev)
+    size = torch.tensor([lo, lo, hi, hi, 1.0, 1e37, 1e-37], dtype=torch.float64, device=dev)  # of a head's values
+    H = len(gk)
+    k, v = ((torch.randn(T, H, d, generator=g, device=dev, dtype=torch.float64) * size[:, None]).to(BF) for _ in range(2))
+    # scales of a block from 2^-9 to 448, zeros among them
+    mult = 2.0 ** torch.randint(-9, 9, (T, 1, d // 16, 1), generator=g, device=dev).float()
+    few = torch.arange(H, device=dev)[:, None] < 5
+    k, v = (torch.where(few, (x.float().unflatten(-1, (-1, 16)) * mult).flatten(-2).to(BF), x) for x in (k, v))
+    k[7], v[8] = 0, 0
+    seq, at = _tokens([T], dev)
+    table = torch.arange(T // ps, dtype=torch.int32, device=dev)[None]
+    plan = mapflow.RotaryPlan(rot, layout=layout) if layout else None
+    y = k.double()
+    if plan is not None:
+        f, gain = layer_ref.rope_frequencies(rot)
+        y, _ = layer_ref.rope(k, None, False, 0.0, at, f, gain, rot, layout)
+    pages = _pages(dev, T // ps, H, ps, d)
+    cache = mapflow.PagedCache.fp4(pages, ps, d, k_scale=gk, v_scale=gk)
+    cache.append(k, v, seq, at, table, rope=plan)
+    page, o = _slots(seq, at, table, ps)
+    kc, ks, vc, vs = (x[page, o].long() for x in ref.unpack(pages, ps, d))
+    for code, scale, x, gs in ((kc, ks, y, gk), (vc, vs, v.double(), gk)):
+        want_c, want_s = ref.hold(x, gs)
+        assert torch.equal(scale, want_s)
+        assert ((code == want_c) | ((code & 7 == 0) & (want_c & 7 == 0))).all()
+    vo = cache.read(seq, at, table)[1]
+    want = ref.stands_for(vc, vs, gk)
+    assert torch.allclose(vo.double(), want, rtol=2.0 ** -8 + 2.0 ** -23, atol=0)
+
+
+def test_head_scales_out_of_their_range_hold_nan(dev):
+    g, T, d, ps = _gen(dev, 65), 33, 128, 16
+    bad = [0.0, -1.0, 2.0 ** -64 * 0.999, 1e-37, 1e-42, 2.0 ** 64 * 1.001, 1e38, math.inf, -math.inf, math.nan]
+    gk = torch.tensor([1.0] + bad + [2.0 ** 64], device=dev)
+    H = len(gk)
+    k, v = _rnd(g, dev, T, H, d), _rnd(g, dev, T, H, d)
+    k[3], v[4] = 0, 0
+    k[5], v[6] = 1e30, 1e30
+    seq, at = _tokens([T], dev)
+    table = torch.arange(3, dtype=torch.int32, device=dev)[None]
+    for plan, norm in ((None, False), (mapflow.RotaryPlan(d), True), (mapflow.RotaryPlan(20), False),
+                       (mapflow.RotaryPlan(32, layout="interleaved"), True)):
+        pages = _pages(dev, 3, H, ps, d, byte=0)
+        cache = mapflow.PagedCache.fp4(pages, ps, d, k_scale=gk, v_scale=gk)
+        cache.append(k, v, seq, at, table, rope=plan, norm=norm)
+        page, o = _slots(seq, at, table, ps)
+        _, ks, _, vs = (x[page, o].long() for x in ref.unpack(pages, ps, d))
+        for s in (ks, vs):
+            assert (s[:, 1:-1] == 0x7f).all() and (s[:, 0] != 0x7f).all() and (s[:, -1] != 0x7f).all()
+        for x in cache.read(seq, at, table):
+            assert x[:, 1:-1].isnan().all() and torch.isfinite(x[:, 0]).all() and torch.isfinite(x[:, -1]).all()
+
+
+@pytest.mark.parametrize("d,lq", [(128, 1), (64, 3)])
+@pytest.mark.parametrize("e", [-64, 64])
+def test_attention_under_head_scales_at_the_ends(dev, d, lq, e):
+    lens = [700, 33, 5000]
+    g, pages, table, lens_t, gk, gv, keys = _world(dev, 66 + d, 3, 2, d, 32, lens, scales=False)
+    one = torch.ones(2, device=dev)
+    cache = mapflow.PagedCache.fp4(pages, 32, d, k_scale=one * 2.0 ** e, v_scale=one * 2.0 ** -e)
+    q = _rnd(g, dev, 3, lq, 8, d, std=1.5)
+    lse = torch.empty(3, lq, 8, dtype=torch.float32, device=dev)
+    scale = d ** -0.5 * 2.0 ** -e
+    o = cache.attend(q, table, lens_t, scale=scale, lse=lse)
+    plain = mapflow.PagedCache.fp4(pages, 32, d).attend(q, table, lens_t)
+    assert torch.equal(o.double(), plain.double() * 2.0 ** -e)
+
+    def far(r):
+        k, v = keys(r)
+        return k * 2.0 ** e, v
+    _check_attend(dev, q, lens, far, (o.double() * 2.0 ** e), lse, 0, 0, scale, None, None)
