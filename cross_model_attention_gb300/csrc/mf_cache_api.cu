@@ -82,13 +82,30 @@ bool rows_apart(const void* a, int64_t lda, int64_t wa, int64_t na, const void* 
   const int64_t in = ((off % ld) + ld) % ld;  // b's rows' start in a's
   return in >= wa * 2 && in + wb * 2 <= ld;
 }
+int shared(const char* a, const char* b) { return fail(MF_ERR_ARG, "%s shares memory with %s", a, b); }
+// What a call reads besides rows of heads, NULL where there is none.
+struct Read {
+  const char* name;
+  const void* p;
+  int64_t bytes;
+};
+template <int N>
+int check_apart(const char* name, Span out, const Read (&in)[N]) {
+  for (const Read& r : in) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(r.p);
+    if (r.p && !apart(out, {a, a + r.bytes})) return shared(name, r.name);
+  }
+  return MF_OK;
+}
+Span pages_span(const mf_cache_t* c) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(c->k);
+  return {a, a + (uintptr_t)(c->n_pages * c->page_size / kFp4Block) * c->H * fp4_piece(c->d)};
+}
+int64_t table_bytes(int64_t ld, int rows, int max_pages) { return (int64_t)(((uint64_t)(rows - 1) * (uint64_t)ld + max_pages) * 4); }
 // Whether a tensor of T rows shares no memory with the cache.
 bool clear_of(const mf_cache_t* c, const void* p, int64_t ld, int T) {
   const int64_t w = (int64_t)c->H * c->d, rows = c->n_pages * c->page_size;
-  if (c->format == MF_CACHE_FP4) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(c->k);
-    return apart({a, a + (uintptr_t)(rows / kFp4Block) * c->H * fp4_piece(c->d)}, rows_span(p, ld, w, T));
-  }
+  if (c->format == MF_CACHE_FP4) return apart(pages_span(c), rows_span(p, ld, w, T));
   return rows_apart(c->k, c->ld_k, w, rows, p, ld, w, T) && rows_apart(c->v, c->ld_v, w, rows, p, ld, w, T);
 }
 
@@ -168,6 +185,17 @@ int mf_cache_append(const mf_cache_t* cache, const void* k, int64_t ld_k_in, con
       !rows_apart(cache->k, cache->ld_k, (int64_t)cache->H * d, cache->n_pages * cache->page_size, cache->v, cache->ld_v,
                   (int64_t)cache->H * d, cache->n_pages * cache->page_size))
     return fail(MF_ERR_ARG, "the cache's k and v share memory");
+  const Read in[] = {{"seq", seq, T * 4ll}, {"at", at, T * 4ll}, {"table", table, table_bytes(ld_table, n_seqs, max_pages)},
+                     {"positions", positions, T * 4ll}, {"turns", rot_dim ? turns : nullptr, rot_dim * 4ll},
+                     {"k_weight", k_weight, d * 2ll}, {"k_scale", cache->k_scale, cache->H * 4ll},
+                     {"v_scale", cache->v_scale, cache->H * 4ll}};
+  if (cache->format == MF_CACHE_FP4) {
+    if ((rc = check_apart("the cache", pages_span(cache), in)) != MF_OK) return rc;
+  } else {
+    const int64_t w = (int64_t)cache->H * d, rows = cache->n_pages * cache->page_size;
+    if ((rc = check_apart("the cache's k", rows_span(cache->k, cache->ld_k, w, rows), in)) != MF_OK) return rc;
+    if ((rc = check_apart("the cache's v", rows_span(cache->v, cache->ld_v, w, rows), in)) != MF_OK) return rc;
+  }
   CacheParams p{};
   fill(&p, cache, seq, at, table, ld_table, n_seqs, max_pages);
   p.k_in = k;
@@ -202,6 +230,10 @@ int mf_cache_read(const mf_cache_t* cache, int T, const int32_t* seq, const int3
     return fail(MF_ERR_ARG, "k_out or v_out shares memory with the cache");
   const int64_t w = (int64_t)cache->H * cache->d;
   if (!rows_apart(k_out, ld_k_out, w, T, v_out, ld_v_out, w, T)) return fail(MF_ERR_ARG, "k_out and v_out share memory");
+  const Read in[] = {{"seq", seq, T * 4ll}, {"at", at, T * 4ll}, {"table", table, table_bytes(ld_table, n_seqs, max_pages)},
+                     {"k_scale", cache->k_scale, cache->H * 4ll}, {"v_scale", cache->v_scale, cache->H * 4ll}};
+  if ((rc = check_apart("k_out", rows_span(k_out, ld_k_out, w, T), in)) != MF_OK) return rc;
+  if ((rc = check_apart("v_out", rows_span(v_out, ld_v_out, w, T), in)) != MF_OK) return rc;
   CacheParams p{};
   fill(&p, cache, seq, at, table, ld_table, n_seqs, max_pages);
   p.k_out = k_out;
@@ -251,12 +283,28 @@ int mf_attn_paged(const mf_cache_t* cache, int n, int Lq, int H_q, const void* q
   if ((rc = check_rows("q", q, ld_q, H_q, d)) != MF_OK) return rc;
   if ((rc = check_rows("o", o, ld_o, H_q, d)) != MF_OK) return rc;
   const int64_t w = (int64_t)H_q * d, rows = (int64_t)n * Lq;
-  if (!rows_apart(q, ld_q, w, rows, o, ld_o, w, rows)) return fail(MF_ERR_ARG, "o shares memory with q");
+  if (!rows_apart(q, ld_q, w, rows, o, ld_o, w, rows)) return shared("o", "q");
   if ((rc = check_aligned("workspace", workspace, 256)) != MF_OK) return rc;
   PagedLayout l;
   if ((rc = paged_layout(Lq, H_q, H, d, &l)) != MF_OK) return rc;
   if (workspace_bytes < (int64_t)l.bytes)
     return fail(MF_ERR_ARG, "workspace of %lld bytes, %lld are needed", (long long)workspace_bytes, (long long)l.bytes);
+  const Span pages = pages_span(cache), qs = rows_span(q, ld_q, w, rows), os = rows_span(o, ld_o, w, rows);
+  const Read in[] = {{"the cache", cache->k, (int64_t)(pages.b - pages.a)}, {"lens", lens, n * 4ll},
+                     {"table", table, table_bytes(ld_table, n, max_pages)}, {"slopes", slopes, H_q * 4ll},
+                     {"k_scale", cache->k_scale, H * 4ll}, {"v_scale", cache->v_scale, H * 4ll}};
+  if ((rc = check_apart("o", os, in)) != MF_OK) return rc;
+  const uintptr_t ls = reinterpret_cast<uintptr_t>(lse), wsp = reinterpret_cast<uintptr_t>(workspace);
+  const Span lse_s = {ls, lse ? ls + rows * H_q * 4 : ls}, ws_s = {wsp, wsp + l.bytes};
+  if ((rc = check_apart("workspace", ws_s, in)) != MF_OK) return rc;
+  if (!apart(ws_s, qs)) return shared("workspace", "q");
+  if (!apart(ws_s, os)) return shared("workspace", "o");
+  if (lse) {
+    if ((rc = check_apart("lse", lse_s, in)) != MF_OK) return rc;
+    if (!apart(lse_s, qs)) return shared("lse", "q");
+    if (!apart(lse_s, os)) return shared("lse", "o");
+    if (!apart(lse_s, ws_s)) return shared("lse", "workspace");
+  }
   PagedParams p{};
   p.pages = static_cast<const uint8_t*>(cache->k);
   p.k_scale = cache->k_scale;

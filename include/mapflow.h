@@ -682,12 +682,13 @@ typedef struct {
  *   turns, rot_dim, layout, gain   as for mf_qk_norm_rope; rot_dim 0: no rotary
  *   k_weight, norm, eps            as for mf_qk_norm_rope
  * Two tokens of one call at one place leave either's values there, or parts of
- * both.  Shares no memory between cache and inputs.  max_pages * page_size is at
- * most 2^26 (MF_ERR_UNSUPPORTED).  T = 0 is a no-op.
+ * both.  The cache shares no memory with what is read (MF_ERR_ARG).  max_pages *
+ * page_size is at most 2^26 (MF_ERR_UNSUPPORTED).  T = 0 is a no-op.
  *
  * mf_cache_read — T tokens' keys and values as bf16 rows (a code times
  * its scale times the head's in fp32, rounded), e.g. for mf_attn_packed over a chunk and
- * its cached prefix.  Rows of tokens that are left out are not written.
+ * its cached prefix.  Rows of tokens that are left out are not written.  k_out and
+ * v_out share no memory with what is read, nor with each other (MF_ERR_ARG).
  * Errors of both: MF_ERR_ARG, MF_ERR_UNSUPPORTED, MF_ERR_CUDA.
  */
 MF_API int mf_cache_append(const mf_cache_t* cache, const void* k, int64_t ld_k_in, const void* v, int64_t ld_v_in,
@@ -708,8 +709,9 @@ MF_API int mf_cache_read(const mf_cache_t* cache, int T, const int32_t* seq, con
  *     slopes: less slopes[head] * (i - j)
  * and o = softmax(s) v, lse the log of the softmax's denominator.  A row that sees
  * no key gets o = 0 and lse = -inf.
- *   q, o         bf16 [n * Lq][H_q][d], Lq * H_q / H <= 128, H_q <= 1024; o shares no
- *                memory with an input
+ *   q, o         bf16 [n * Lq][H_q][d], Lq * H_q / H <= 128, H_q <= 1024; o, lse and
+ *                the workspace share no memory with what is read, nor with each
+ *                other (MF_ERR_ARG)
  *   table        int32 [n][max_pages], ld_table apart; numbers past a request's
  *                keys, or before its window, are not used
  *   lens         DEVICE int32 [n], held to [0, max_pages * page_size <= 2^26]; read on
