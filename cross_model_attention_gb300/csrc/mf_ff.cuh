@@ -1,18 +1,20 @@
 // mf_ff.cuh — arithmetic in two fp32 numbers (a high part and what it lacks),
-// good to about 2^-44, with sine and cosine of a turn.
+// good to 2^-43.6 (sine and cosine of a turn; sums and products to 2^-45).
 //
 // GB300 has a sixty-fourth of its fp32 rate in fp64: a row of 128 normed, rotated
 // and rounded dimensions took a warp 28 us in it, in this 5, and two blocks of 16
 // dimensions 1.3.  The sums and products are the error-free ones of Dekker (1971)
 // and Knuth, with an fma for a product's rest.
+//
+// A host compiler takes it too, for the tests that compare it with wider numbers.
 #pragma once
 #include <cmath>
 #include <cstdint>
 
-#ifndef __CUDACC__
-#define __host__
-#define __device__
-#define __forceinline__ inline
+#ifdef __CUDACC__
+#define MF_FF __device__ __forceinline__
+#else
+#define MF_FF inline
 #endif
 
 namespace mf {
@@ -22,41 +24,43 @@ struct ff {
 };
 
 // (never contracted into an fma: the rest of a sum is what its rounding lost)
-__host__ __device__ __forceinline__ float mul_rn(float a, float b) {
-#ifdef __CUDA_ARCH__
+MF_FF float mul_rn(float a, float b) {
+#ifdef __CUDACC__
   return __fmul_rn(a, b);
 #else
-  return a * b;
+  const volatile float r = a * b;
+  return r;
 #endif
 }
-__host__ __device__ __forceinline__ float add_rn(float a, float b) {
-#ifdef __CUDA_ARCH__
+MF_FF float add_rn(float a, float b) {
+#ifdef __CUDACC__
   return __fadd_rn(a, b);
 #else
-  return a + b;
+  const volatile float r = a + b;
+  return r;
 #endif
 }
-__host__ __device__ __forceinline__ ff ff_fast_sum(float a, float b) {  // |a| >= |b|
+MF_FF ff ff_fast_sum(float a, float b) {  // |a| >= |b|
   const float s = add_rn(a, b);
   return {s, add_rn(b, -add_rn(s, -a))};
 }
-__host__ __device__ __forceinline__ ff ff_sum(float a, float b) {
+MF_FF ff ff_sum(float a, float b) {
   const float s = add_rn(a, b), bb = add_rn(s, -a);
   return {s, add_rn(add_rn(a, -add_rn(s, -bb)), add_rn(b, -bb))};
 }
-__host__ __device__ __forceinline__ ff ff_add(ff a, ff b) {
+MF_FF ff ff_add(ff a, ff b) {
   const ff s = ff_sum(a.h, b.h);
   return ff_fast_sum(s.h, add_rn(s.l, add_rn(a.l, b.l)));
 }
-__host__ __device__ __forceinline__ ff ff_mul(ff a, ff b) {
+MF_FF ff ff_mul(ff a, ff b) {
   const float p = mul_rn(a.h, b.h);
   return ff_fast_sum(p, fmaf(a.l, b.h, fmaf(a.h, b.l, fmaf(a.h, b.h, -p))));
 }
-__host__ __device__ __forceinline__ ff ff_mul(ff a, float b) {
+MF_FF ff ff_mul(ff a, float b) {
   const float p = mul_rn(a.h, b);
   return ff_fast_sum(p, fmaf(a.l, b, fmaf(a.h, b, -p)));
 }
-__host__ __device__ __forceinline__ ff ff_neg(ff a) { return {-a.h, -a.l}; }
+MF_FF ff ff_neg(ff a) { return {-a.h, -a.l}; }
 
 // cosine and sine of j / 64 of a turn, each in two parts
 #ifdef __CUDACC__
@@ -77,7 +81,7 @@ const float kFfTurn[9][4] = {
 // Cosine and sine of `turn` 2^-64ths of a turn: the nearest quarter turn, then
 // the nearest 64th, whose values are added to those of the rest (at most 0.05
 // radians), of which three terms of the series suffice.
-__host__ __device__ __forceinline__ void ff_sincos(uint64_t turn, ff* sn, ff* cn) {
+MF_FF void ff_sincos(uint64_t turn, ff* sn, ff* cn) {
   const unsigned quarter = static_cast<unsigned>((turn + (1ull << 61)) >> 62) & 3u;
   const int64_t r = static_cast<int64_t>(turn - (static_cast<uint64_t>(quarter) << 62));
   const uint64_t a = r < 0 ? 0ull - static_cast<uint64_t>(r) : static_cast<uint64_t>(r);
@@ -103,3 +107,4 @@ __host__ __device__ __forceinline__ void ff_sincos(uint64_t turn, ff* sn, ff* cn
 }
 
 }  // namespace mf
+#undef MF_FF
