@@ -199,8 +199,9 @@ __device__ __forceinline__ uint32_t codes_exactly(const float* y, const Scale& s
   return f32x8_e2m1(t);
 }
 // Codes of 8 values times r that are off by at most e (which counts the product's
-// own rounding); near: whether one of them has another code as likely (a zero's
-// sign says nothing).
+// own rounding); near: whether one of them has another code as likely.  (A zero's sign
+// says nothing.  Any other's is certain unless e itself passes the first border, as
+// beside values 2^19 times as large.)
 __device__ __forceinline__ uint32_t codes_about(const float* y, float r, float e, bool& near) {
   float lo[8], hi[8];
 #pragma unroll
@@ -211,7 +212,7 @@ __device__ __forceinline__ uint32_t codes_about(const float* y, float r, float e
     hi[i] = b.x, hi[i + 1] = b.y;
   }
   const uint32_t a = f32x8_e2m1(lo), b = f32x8_e2m1(hi);
-  near |= ((a ^ b) & 0x77777777u) != 0;
+  near |= ((a ^ b) & 0x77777777u) != 0 || e > 0.25f;
   return b;
 }
 

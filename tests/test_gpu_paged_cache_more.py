@@ -195,3 +195,26 @@ def test_attention_under_head_scales_at_the_ends(dev, d, lq, e):
         k, v = keys(r)
         return k * 2.0 ** e, v
     _check_attend(dev, q, lens, far, (o.double() * 2.0 ** e), lse, 0, 0, scale, None, None)
+
+
+@pytest.mark.parametrize("size,gain,still", [(2.0 ** 45, 1.0, False), (2.0 ** 60, -0.3, False), (1.0, 1.5, True)])
+@pytest.mark.parametrize("layout,rot", [("half", 128), ("half", 20), ("interleaved", 128), ("half", 64)])
+def test_signs_of_values_that_are_small_beside_others(dev, layout, rot, size, gain, still):
+    """A value within the error of its block's largest, or of its pair's other block's, but past a
+    code of its own block: its sign counts."""
+    g, T, H, d, ps = _gen(dev, 67), 4096, 8, 128, 16
+    k, v = _rnd(g, dev, T, H, d, std=size), _rnd(g, dev, T, H, d)
+    seq, at = _tokens([T], dev)
+    pos = at
+    if still:  # (nothing is turned, the products with the gain round: blocks of very different sizes side by side)
+        pos = torch.zeros_like(at)
+        wide = 2.0 ** torch.randint(0, 23, (T, 1, d // 16, 1), generator=g, device=dev).float()
+        k = (k.float().unflatten(-1, (-1, 16)) * wide).flatten(-2).to(BF)
+    table = torch.arange(T // ps, dtype=torch.int32, device=dev)[None]
+    pages = _pages(dev, T // ps, H, ps, d)
+    plan = mapflow.RotaryPlan(rot, layout=layout)
+    plan.gain = gain
+    mapflow.PagedCache.fp4(pages, ps, d).append(k, v, seq, at, table, rope=plan, positions=pos)
+    f, _ = layer_ref.rope_frequencies(rot)
+    y, _ = layer_ref.rope(k, None, False, 0.0, pos, f, float(torch.tensor(gain)), rot, layout)
+    _check_held(pages, ps, d, *_slots(seq, at, table, ps), y, v, None, None)
