@@ -23,8 +23,9 @@
 //
 // Bound: HBM for bf16 rows (4099 tokens of 40 heads of 128 put in their places in
 // 30 us, 5.6 TB/s, 82 % of the copy rate) and reading (32000 tokens of 8 heads 29 us,
-// 5.8 TB/s); instructions for 4 bits (16384 tokens of 8 heads 32 us, 2.7 TB/s; 27
-// where no block has to be done again).
+// 5.8 TB/s).  For 4 bits (16384 tokens of 8 heads 33 us, 2.6 TB/s) instructions and
+// their latency, 57 % of the issue slots used by 16 warps an SM, and the ends of warps
+// that do blocks again (26 us where none is).
 //
 // Lanes as in the rotary kernel: d / 16 lanes to a head's row, each with two chunks
 // of 8 dimensions that hold both halves of its pairs, sines and cosines kept over a
@@ -154,7 +155,7 @@ __device__ __forceinline__ float quotient(float y, const Scale& s) {
 // before: then it goes back to the side that its residue says (one value in 10^6; where
 // the quotient is the border, the even code is the right one).  Residues are looked at
 // where a lane has a quotient on a border at all: without head scales that is often (16384
-// tokens of 8 heads 36.6 us, with all residues 35.6), with them hardly ever (32.0, 35.1).
+// tokens of 8 heads 37.3 us, with all residues 36.0), with them hardly ever (33.2, 36.1).
 __device__ __forceinline__ uint32_t codes_exactly(const float* y, const Scale& s) {
   float t[8];
   bool odd = false;
@@ -347,8 +348,9 @@ __device__ __forceinline__ Sector get16(const __nv_bfloat16* from, bool even) {
 }
 
 // ------------------------------------------------------------------ append --
-// (Four CTAs to an SM: 16384 tokens of 8 heads 32.0 us; three 35.6, five, which
-// spill, 37.3.)
+// (Four CTAs to an SM: 16384 tokens of 8 heads 33.2 us; three 36.9, five, which
+// spill, 38.1.  At four kAny spills as well, most for rows of bf16:
+// 4099 tokens of 40 heads 49 us, the others 30.)
 template <int D, int LAYOUT, bool FP4>
 __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p) {
   constexpr int LPR = D / 16;            // lanes to a row
@@ -463,7 +465,10 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheParams p
   // Whether the lane's values are not exact in fp32, and how far they may be off,
   // of |a| + |b| (kAny and kPairs: where only some are, the rest is taken to be so too).
   // At position 0 they are: a prompt's first token would have most of its blocks done
-  // again by one warp, 12 us after the others of 16384.
+  // again by one warp, 12 us after the others of 16384.  (So it is with keys that are
+  // neither normed nor scaled where they are hardly turned, for as many tokens as there
+  // are: 64 tokens at position 1 take 6.8 us, at 0 4.0 and at 100 4.5; 16384 at once
+  // 65, 37 and 35, and at position 1 of angles stretched by 64 114.)
   const bool loose = p.norm || ((LAYOUT == kHalf ? turned : c0 * 8 < p.rot) && (pos != 0 || p.gain != 1.f));
   const float err = (p.norm ? 20.f : 16.f) * 5.9604644775390625e-08f * fmaxf(1.f, fabsf(p.gain));  // 2^-24
 
@@ -744,9 +749,9 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const CacheParams p) {
 
 // A token's heads in shares: all of them to one group of lanes where that
 // leaves every SM about `rounds` rounds, else spread.  (Appending, whose groups
-// begin with sines and cosines, two: 16384 tokens of 8 heads 32.0 us, with eight
-// 34.3; 4099 of 40 heads in bf16 30.0, with one 34.3 and with four 32.0.  Reading
-// eight: the same 16384 16.4 us, with two 17.0.)
+// begin with sines and cosines, two: 16384 tokens of 8 heads 33.2 us, with eight
+// 35.6; 4099 of 40 heads in bf16 29.9, with one 34.1 and with four 31.5.  Reading
+// eight: the same 16384 15.8 us, with two 16.4.)
 template <typename F>
 cudaError_t spread(CacheParams p, long long T, int D, int rounds, F&& go) {
   const int groups = kThreads / (D / 16);

@@ -112,8 +112,9 @@ cudaError_t once_per_device(std::atomic<unsigned long long>& done, F&& set) {
   return e;
 }
 
-// Launches a kernel that may be set up while the one before it still runs: its
-// first instruction that touches memory comes after griddepcontrol.wait.
+// Launches a kernel that may be set up while the one before it still runs: it loads
+// and stores nothing before griddepcontrol.wait.  (Prefetches into L2 may come before:
+// they bring no value, and L2 has what is still being written.)
 template <typename P>
 cudaError_t launch_early(void (*kernel)(P), dim3 grid, int threads, size_t smem, cudaStream_t s, const P& p) {
   cudaLaunchConfig_t cfg{};
@@ -332,9 +333,9 @@ struct PagedParams {
   unsigned inv_G;              // rr * inv_G >> 16 = rr / G for rr < 128
   float scale, cap;            // cap 0: none
   // workspace: a CTA's two partial results and a warp's one
-  float* part_o;               // [2 grid + warps][rows][d]
-  float2* part_ml;             // [2 grid + warps][rows]
-  int4* cuts;                  // [2 grid]
+  float* part_o;               // [grid * (2 + warps)][rows][d]
+  float2* part_ml;             // [grid * (2 + warps)][rows]
+  int4* cuts;                  // [grid]
   int rows;                    // of a partial result
   float inv_grid;              // set by the launcher: 1 / CTAs, rounded up
 };

@@ -864,8 +864,9 @@ _default_ws: Dict[int, "object"] = {}  # PagedCache.attend's workspace of each G
 class PagedCache:
     """A paged cache of one layer's keys and values over tensors of the caller
     (see mf_cache_t in mapflow.h): PagedCache.fp4 for pages of 4 bits,
-    PagedCache.bf16 for bf16 rows.  Calls leave nothing behind but what they
-    write to these tensors; no gradient is recorded.
+    PagedCache.bf16 for bf16 rows.  Calls leave no state behind but what they
+    write to these tensors (attend keeps the workspace of each GPU's default
+    stream, up to 18 MB, for its next call); no gradient is recorded.
 
     Tokens are named by `seq` and `at`, int32 [T] on the device: a token's row of
     `table` (int32 [n_seqs, max_pages], page numbers) and its place in that

@@ -635,7 +635,7 @@ MF_API int mf_attn_status(mf_attn_t h, void* stream);
  * kept between calls.  A number of the table is read only for tokens that a call
  * names; a token with seq outside [0, n_seqs), `at` outside [0, max_pages *
  * page_size) or a page outside [0, n_pages) is left out (unused places of a
- * batch: seq = -1), and nothing is read or written for it.
+ * batch: seq = -1): no key or value of it, nor a page, is read or written.
  *
  * MF_CACHE_BF16: rows of heads, keys and values apart: token i of page p is row
  *   p * page_size + i.  With page_size = capacity and table[r] = {r} these are
